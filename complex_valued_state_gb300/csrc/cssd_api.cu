@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/cssd.h"
+#include "api_checks.h"
 #include "cssd_internal.h"
 
 namespace {
@@ -15,7 +16,9 @@ namespace {
 bool supported_n(int64_t n) { return n == 16 || n == 32 || n == 64 || n == 128; }
 bool supported_p(int64_t p) { return p == 16 || p == 32 || p == 64; }
 bool supported_chunk(int c) { return c == 64 || c == 128; }
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using cssd::aligned;
+using cssd::check_all_device;
+using cssd::stream_device;
 
 constexpr int64_t kMaxGridYZ = 65535;
 constexpr int64_t kMaxInt = 2147483647;
@@ -30,35 +33,6 @@ int check_dims(const cssd_dims* d, bool need_seq) {
     if (need_seq && d->seqlen > kMaxInt) return CSSD_ERR_DIMS;
     // the chunk kernels index (batch, head, 64-token tile) in 32 bits
     if (need_seq && (d->seqlen + 63) / 64 > kMaxInt / (d->batch * d->nheads)) return CSSD_ERR_DIMS;
-    return CSSD_OK;
-}
-
-// Device of the stream (or the current device for the default stream).
-int stream_device(cudaStream_t s, int* dev) {
-    if (s == nullptr) return cudaGetDevice(dev) == cudaSuccess ? CSSD_OK : CSSD_ERR_CUDA;
-    return cssd::stream_device_of(s, dev) == cudaSuccess ? CSSD_OK : CSSD_ERR_CUDA;
-}
-
-// The pointer must be device (or managed) memory usable on `dev`.
-int check_device_ptr(const void* p, int dev) {
-    cudaPointerAttributes at;
-    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-        cudaGetLastError();  // clear the sticky-free error this query may set
-        return CSSD_ERR_DEVICE;
-    }
-    if (at.type == cudaMemoryTypeManaged) return CSSD_OK;
-    if (at.type != cudaMemoryTypeDevice || at.device != dev) return CSSD_ERR_DEVICE;
-    return CSSD_OK;
-}
-
-template <typename... Ts>
-int check_all_device(int dev, Ts... ptrs) {
-    const void* arr[] = {ptrs...};
-    for (const void* p : arr) {
-        if (!p) continue;
-        const int s = check_device_ptr(p, dev);
-        if (s != CSSD_OK) return s;
-    }
     return CSSD_OK;
 }
 

@@ -165,4 +165,68 @@ cudaError_t launch_born(const BornArgs& a, cudaStream_t stream);
 // Output of a constant input held forever (h is not used).
 cudaError_t launch_step_infinite(const StepArgs& a, cudaStream_t stream);
 
+// The gated delta rule (delta.cu, delta_tc.cu, delta_step.cu).  Element types
+// are CSSD_BF16, CSSD_F16 and CSSD_F32.
+struct DeltaArgs {
+    int64_t Bz, T, H, KH, N, P;
+    int dtype;
+    float scale;
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;
+    const float* beta;
+    const float* h0;    // may be null (zero state)
+    const int* lens;    // may be null (every row has T tokens)
+    void* o;            // forward
+    float* h_final;     // forward; may be null
+    const void* dout;   // backward from here on
+    const float* dh_final;  // may be null (zero)
+    void* gq;
+    void* gk;
+    void* gv;
+    float* gg;
+    float* gbeta;
+    float* gh0;         // may be null
+};
+size_t delta_workspace_bytes(const DeltaArgs& a);
+size_t delta_backward_workspace_bytes(const DeltaArgs& a);
+cudaError_t launch_delta_forward(const DeltaArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_delta_backward(const DeltaArgs& a, void* workspace, cudaStream_t stream);
+
+struct DeltaStepArgs {
+    int64_t Bz, H, KH, N, P, nslots;
+    int dtype;
+    float scale;
+    float* h;
+    const int* slots;  // may be null (row b uses state b)
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;
+    const float* beta;
+    void* o;
+};
+cudaError_t launch_delta_step(const DeltaStepArgs& a, cudaStream_t stream);
+
+// Layer norm (layernorm.cu).
+struct NormArgs {
+    int64_t rows, width;
+    int xtype, wtype;
+    const void* x;
+    const void* weight;  // may be null (ones)
+    const void* bias;    // may be null (none)
+    float eps;
+    void* y;             // forward
+    float* mean;         // written by the forward, read by the backward
+    float* rstd;
+    const void* dy;      // backward from here on
+    void* gx;
+    void* gweight;       // may be null
+    void* gbias;         // may be null
+};
+size_t layernorm_backward_workspace_bytes(int64_t rows, int64_t width);
+cudaError_t launch_layernorm(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_layernorm_backward(const NormArgs& a, void* workspace, cudaStream_t stream);
+
 }  // namespace cssd

@@ -36,6 +36,9 @@ EXPORTS = ("cssd_workspace_bytes", "cssd_precise_workspace_bytes", "cssd_forward
            "cssd_host_forward_device_bytes", "cssd_chunked_forward_host",
            "cssd_backward_workspace_bytes", "cssd_chunked_backward",
            "cssd_chunked_forward_noalloc", "cssd_step", "cssd_step_n", "cssd_step_infinite", "cssd_cayley_scan", "cssd_born_attention",
+           "cssd_delta_workspace_bytes", "cssd_delta_backward_workspace_bytes", "cssd_delta_forward",
+           "cssd_delta_backward", "cssd_delta_step", "cssd_layernorm", "cssd_layernorm_backward_workspace_bytes",
+           "cssd_layernorm_backward",
            "cssd_profile_events", "cssd_device_status",
            "cssd_selftest_handoff_timeout", "cssd_status_string")
 
@@ -45,6 +48,14 @@ NOALLOC_SCRATCH_BYTES = 16 << 20
 
 class Dims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "nheads", "dstate", "headdim")]
+
+
+class DeltaDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "nheads", "kheads", "dstate", "headdim")]
+
+
+# cssd_dtype
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class CssdError(RuntimeError):
@@ -101,6 +112,22 @@ def load(path: str = LIB_PATH):
             lib.cssd_chunked_backward.restype = ctypes.c_int
             lib.cssd_born_attention.argtypes = [dims_p] + [vp] * 4 + [vp]
             lib.cssd_born_attention.restype = ctypes.c_int
+            ddims_p, i64, sz, flt, i32 = ctypes.POINTER(DeltaDims), ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_int
+            for n in ("cssd_delta_workspace_bytes", "cssd_delta_backward_workspace_bytes"):
+                getattr(lib, n).argtypes = [ddims_p, i32]
+                getattr(lib, n).restype = sz
+            lib.cssd_delta_forward.argtypes = [ddims_p, i32] + [vp] * 5 + [flt] + [vp] * 5 + [sz, vp]
+            lib.cssd_delta_forward.restype = i32
+            lib.cssd_delta_backward.argtypes = [ddims_p, i32] + [vp] * 5 + [flt] + [vp] * 11 + [sz, vp]
+            lib.cssd_delta_backward.restype = i32
+            lib.cssd_delta_step.argtypes = [ddims_p, i32, vp, i64] + [vp] * 6 + [flt, vp, vp]
+            lib.cssd_delta_step.restype = i32
+            lib.cssd_layernorm.argtypes = [i64, i64, i32, i32, vp, vp, vp, flt, vp, vp, vp, vp]
+            lib.cssd_layernorm.restype = i32
+            lib.cssd_layernorm_backward_workspace_bytes.argtypes = [i64, i64]
+            lib.cssd_layernorm_backward_workspace_bytes.restype = sz
+            lib.cssd_layernorm_backward.argtypes = [i64, i64, i32, i32] + [vp] * 9 + [sz, vp]
+            lib.cssd_layernorm_backward.restype = i32
             lib.cssd_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), ctypes.c_int, vp]
             lib.cssd_device_status.restype = ctypes.c_int
             lib.cssd_profile_events.argtypes = [vp, vp]
@@ -526,3 +553,220 @@ def born_attention(q, k, v, *, psi=None, stream=None):
     if st != CSSD_OK:
         raise CssdError(st, "cssd_born_attention")
     return psi
+
+
+def _element_type(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _scratch(workspace, nbytes, dev, stream):
+    """The caller's workspace checked, or one from torch's allocator that
+    belongs to the call's stream."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+            return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _delta_inputs(q, k, v, g, beta, lead):
+    """Shapes shared by the sequence and the single token (`lead` leading axes)."""
+    dt = _element_type(q, "q")
+    if q.dim() != lead + 2 or not isinstance(v, torch.Tensor) or v.dim() != lead + 2:
+        raise ValueError(f"q and v must have {lead + 2} axes")
+    dev, f32 = q.device, torch.float32
+    ax, KH, N = tuple(q.shape[:lead]), q.shape[-2], q.shape[-1]
+    H, P = v.shape[-2], v.shape[-1]
+    _check(q, "q", q.dtype, ax + (KH, N), dev)
+    _check(k, "k", q.dtype, ax + (KH, N), dev)
+    _check(v, "v", q.dtype, ax + (H, P), dev)
+    _check(g, "g", f32, ax + (H,), dev)
+    _check(beta, "beta", f32, ax + (H,), dev)
+    return dt, dev, ax, H, KH, N, P
+
+
+def delta_workspace_bytes(batch: int, seqlen: int, nheads: int, kheads: int, dstate: int, headdim: int, dtype) -> int:
+    d = DeltaDims(batch, seqlen, nheads, kheads, dstate, headdim)
+    return int(load().cssd_delta_workspace_bytes(ctypes.byref(d), _DTYPES[dtype]))
+
+
+def delta_backward_workspace_bytes(batch: int, seqlen: int, nheads: int, kheads: int, dstate: int, headdim: int,
+                                   dtype) -> int:
+    d = DeltaDims(batch, seqlen, nheads, kheads, dstate, headdim)
+    return int(load().cssd_delta_backward_workspace_bytes(ctypes.byref(d), _DTYPES[dtype]))
+
+
+def delta_forward(q, k, v, g, beta, *, scale=None, h0=None, lens=None, o=None, h_final=None, want_state: bool = True,
+                  workspace=None, stream=None):
+    """cssd_delta_forward, the gated delta rule over a sequence; returns (o, h_final or None).
+
+    q, k [Bz,T,KH,N]; v [Bz,T,H,P], all bfloat16, float16 or float32 (H a
+    multiple of KH); g (log decay), beta float32 [Bz,T,H]; h0 float32
+    [Bz,H,N,P], the state before the first token (zero when None); lens int32
+    [Bz], the tokens each row has (all when None).  `scale` (default
+    1/sqrt(N)) multiplies the output.  `workspace` is an optional uint8 tensor
+    of at least delta_workspace_bytes(...) bytes.
+    """
+    lib = load()
+    dt, dev, (Bz, T), H, KH, N, P = _delta_inputs(q, k, v, g, beta, 2)
+    if h0 is not None:
+        _check(h0, "h0", torch.float32, (Bz, H, N, P), dev)
+    if lens is not None:
+        _check(lens, "lens", torch.int32, (Bz,), dev)
+    if o is None:
+        o = torch.empty_like(v)
+    _check(o, "o", q.dtype, (Bz, T, H, P), dev)
+    if h_final is None and want_state:
+        h_final = torch.empty((Bz, H, N, P), dtype=torch.float32, device=dev)
+    if h_final is not None:
+        _check(h_final, "h_final", torch.float32, (Bz, H, N, P), dev)
+    d = DeltaDims(Bz, T, H, KH, N, P)
+    ws, nbytes = _scratch(workspace, int(lib.cssd_delta_workspace_bytes(ctypes.byref(d), dt)), dev, stream)
+    st = lib.cssd_delta_forward(ctypes.byref(d), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                ctypes.c_float(N ** -0.5 if scale is None else scale), _ptr(h0), _ptr(lens), _ptr(o),
+                                _ptr(h_final), _ptr(ws), ctypes.c_size_t(nbytes), _stream_handle(stream, dev))
+    if st != CSSD_OK:
+        raise CssdError(st, "cssd_delta_forward")
+    return o, h_final
+
+
+def delta_backward(q, k, v, g, beta, do, *, scale=None, h0=None, dh_final=None, lens=None, grads=None, workspace=None,
+                   stream=None):
+    """cssd_delta_backward; returns a dict gq, gk, gv (the inputs' type), gg,
+    gbeta, gh0 (float32).
+
+    Inputs as delta_forward; `do` [Bz,T,H,P] is the gradient of o, `dh_final`
+    float32 [Bz,H,N,P] that of the last state (zero when None).  `grads` may
+    hold preallocated outputs under the same keys.
+    """
+    lib = load()
+    dt, dev, (Bz, T), H, KH, N, P = _delta_inputs(q, k, v, g, beta, 2)
+    f32 = torch.float32
+    _check(do, "do", q.dtype, (Bz, T, H, P), dev)
+    for t, n in ((h0, "h0"), (dh_final, "dh_final")):
+        if t is not None:
+            _check(t, n, f32, (Bz, H, N, P), dev)
+    if lens is not None:
+        _check(lens, "lens", torch.int32, (Bz,), dev)
+    r = dict(grads or {})
+    shapes = {"gq": (q.shape, q.dtype), "gk": (q.shape, q.dtype), "gv": (v.shape, q.dtype), "gg": (g.shape, f32),
+              "gbeta": (g.shape, f32), "gh0": ((Bz, H, N, P), f32)}
+    for name, (shape, dtype) in shapes.items():
+        if name not in r:
+            r[name] = torch.empty(shape, dtype=dtype, device=dev)
+        _check(r[name], name, dtype, shape, dev)
+    d = DeltaDims(Bz, T, H, KH, N, P)
+    ws, nbytes = _scratch(workspace, int(lib.cssd_delta_backward_workspace_bytes(ctypes.byref(d), dt)), dev, stream)
+    st = lib.cssd_delta_backward(ctypes.byref(d), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                 ctypes.c_float(N ** -0.5 if scale is None else scale), _ptr(h0), _ptr(lens), _ptr(do),
+                                 _ptr(dh_final), _ptr(r["gq"]), _ptr(r["gk"]), _ptr(r["gv"]), _ptr(r["gg"]),
+                                 _ptr(r["gbeta"]), _ptr(r["gh0"]), _ptr(ws), ctypes.c_size_t(nbytes),
+                                 _stream_handle(stream, dev))
+    if st != CSSD_OK:
+        raise CssdError(st, "cssd_delta_backward")
+    return r
+
+
+def delta_step(h, q, k, v, g, beta, *, scale=None, slots=None, o=None, stream=None):
+    """cssd_delta_step, one token of the gated delta rule: h updated in place; returns o.
+
+    h float32 [nslots,H,N,P]; q, k [Bz,KH,N]; v [Bz,H,P]; g, beta float32
+    [Bz,H]; slots int32 [Bz] names the state of each row (row b uses h[b] when
+    None; a slot outside [0, nslots) leaves every state alone and gives o = 0).
+    """
+    lib = load()
+    dt, dev, (Bz,), H, KH, N, P = _delta_inputs(q, k, v, g, beta, 1)
+    if not isinstance(h, torch.Tensor) or h.dim() != 4:
+        raise ValueError("h must be a tensor [nslots, H, N, P]")
+    _check(h, "h", torch.float32, (h.shape[0], H, N, P), dev)
+    if slots is not None:
+        _check(slots, "slots", torch.int32, (Bz,), dev)
+    if o is None:
+        o = torch.empty_like(v)
+    _check(o, "o", q.dtype, (Bz, H, P), dev)
+    d = DeltaDims(Bz, 1, H, KH, N, P)
+    st = lib.cssd_delta_step(ctypes.byref(d), dt, _ptr(h), int(h.shape[0]), _ptr(slots), _ptr(q), _ptr(k), _ptr(v),
+                             _ptr(g), _ptr(beta), ctypes.c_float(N ** -0.5 if scale is None else scale), _ptr(o),
+                             _stream_handle(stream, dev))
+    if st != CSSD_OK:
+        raise CssdError(st, "cssd_delta_step")
+    return o
+
+
+def _norm_inputs(x, weight, bias=None):
+    xt = _element_type(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one axis")
+    D = x.shape[-1]
+    _check(x, "x", x.dtype, x.shape, x.device)
+    wt = xt
+    for t, n in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        wt = _element_type(t, n)
+        if t.dtype not in (x.dtype, torch.float32):
+            raise TypeError(f"{n} must be {x.dtype} or float32, got {t.dtype}")
+        _check(t, n, t.dtype if weight is None else weight.dtype, (D,), x.device)
+    return xt, wt, x.numel() // D if D else 0, D
+
+
+def layernorm(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, stream=None):
+    """cssd_layernorm over the last axis; returns (y, mean, rstd), mean and
+    rstd float32 over x's leading axes.
+
+    x bfloat16, float16 or float32; weight and bias [D] of x's type or float32
+    (both the same), either may be None.
+    """
+    lib = load()
+    xt, wt, rows, D = _norm_inputs(x, weight, bias)
+    if y is None:
+        y = torch.empty_like(x)
+    _check(y, "y", x.dtype, x.shape, x.device)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    st = lib.cssd_layernorm(rows, D, xt, wt, _ptr(x), _ptr(weight), _ptr(bias), ctypes.c_float(eps), _ptr(y),
+                            _ptr(mean), _ptr(rstd), _stream_handle(stream, x.device))
+    if st != CSSD_OK:
+        raise CssdError(st, "cssd_layernorm")
+    return y, mean, rstd
+
+
+def layernorm_backward(dy, x, weight, mean, rstd, *, want_weight: bool = True, want_bias: bool = True, grads=None,
+                       workspace=None, stream=None):
+    """cssd_layernorm_backward; returns a dict gx (x's type) and, when wanted,
+    gweight and gbias (weight's type; x's when weight is None).
+
+    mean and rstd are those layernorm returned for x.
+    """
+    lib = load()
+    xt, wt, rows, D = _norm_inputs(x, weight)
+    dev = x.device
+    _check(dy, "dy", x.dtype, x.shape, dev)
+    _check(mean, "mean", torch.float32, x.shape[:-1], dev)
+    _check(rstd, "rstd", torch.float32, x.shape[:-1], dev)
+    r = dict(grads or {})
+    wdt = x.dtype if weight is None else weight.dtype
+    shapes = {"gx": (tuple(x.shape), x.dtype)}
+    if want_weight:
+        shapes["gweight"] = ((D,), wdt)
+    if want_bias:
+        shapes["gbias"] = ((D,), wdt)
+    for name, (shape, dtype) in shapes.items():
+        if name not in r:
+            r[name] = torch.empty(shape, dtype=dtype, device=dev)
+        _check(r[name], name, dtype, shape, dev)
+    ws, nbytes = _scratch(workspace, int(lib.cssd_layernorm_backward_workspace_bytes(rows, D)), dev, stream)
+    st = lib.cssd_layernorm_backward(rows, D, xt, wt, _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
+                                     _ptr(r["gx"]), _ptr(r.get("gweight")) if want_weight else None,
+                                     _ptr(r.get("gbias")) if want_bias else None, _ptr(ws), ctypes.c_size_t(nbytes),
+                                     _stream_handle(stream, dev))
+    if st != CSSD_OK:
+        raise CssdError(st, "cssd_layernorm_backward")
+    return r

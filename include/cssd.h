@@ -378,6 +378,110 @@ int cssd_chunked_backward(const cssd_dims* dims, const void* x, const float* dt,
 int cssd_born_attention(const cssd_dims* dims, const void* q, const void* k, const void* v, void* psi,
                         cssd_stream_t stream);
 
+/* ---------------------------------------------------------------- gated delta rule
+ * The real-valued recurrence that corrects what its state already answers:
+ * per batch row b and value head h, with S in R^{N x P} (N = dstate rows, P =
+ * headdim columns, laid out like the complex SSD's h),
+ *     S'  = exp(g_t) S_{t-1}
+ *     S_t = S' + k_t (beta_t (v_t - S'^T k_t))^T
+ *     o_t = scale S_t^T q_t
+ * k is used as given (models normalise it).  Tensor types are CSSD_BF16,
+ * CSSD_F16 or CSSD_F32 (q, k, v, o and their gradients, all of one type); g,
+ * beta, the states and the gradients of those are float32 always.  Sums,
+ * states and every intermediate are kept to fp32 accuracy whatever the type:
+ * outputs differ from the recurrence by the rounding of their own type plus
+ * about 1e-6 of their largest value.
+ *
+ * Supported sizes: dstate and headdim multiples of 16 from 16 to 128 (else
+ * CSSD_ERR_UNSUPPORTED); any batch, seqlen >= 1; nheads a multiple of kheads
+ * (value head h reads key head h / (nheads / kheads)); nheads * batch below
+ * 2^29.  Tensors are dense and row-major, q, k, v, o, the states and the
+ * workspace 16-byte aligned, the float32 and int32 vectors 4-byte.
+ * g is a log decay: at most 0 in a model, though any value whose exponentials
+ * stay in range works; -inf forgets everything before the token.
+ * A NaN or infinity in a token's inputs may reach any output of its 64-token
+ * chunk and what follows; what lies at or past a row's length is never read.
+ * Every wait inside the kernels is bounded (see cssd_device_status). */
+typedef enum { CSSD_BF16 = 0, CSSD_F16 = 1, CSSD_F32 = 2 } cssd_dtype;
+
+typedef struct {
+    int64_t batch;   /* Bz */
+    int64_t seqlen;  /* T (ignored by cssd_delta_step) */
+    int64_t nheads;  /* H, value heads */
+    int64_t kheads;  /* KH, key heads */
+    int64_t dstate;  /* N, width of q and k */
+    int64_t headdim; /* P, width of v and o */
+} cssd_delta_dims;
+
+/* Bytes of device workspace of cssd_delta_forward and cssd_delta_backward (0
+ * for invalid sizes).  The backward keeps two states (8 N P bytes) per head
+ * and 64 tokens. */
+size_t cssd_delta_workspace_bytes(const cssd_delta_dims* dims, int dtype);
+size_t cssd_delta_backward_workspace_bytes(const cssd_delta_dims* dims, int dtype);
+
+/* The recurrence over a whole sequence, in chunks of 64 tokens.
+ *   q, k     [batch, seqlen, kheads, dstate]   v, o  [batch, seqlen, nheads, headdim]
+ *   g, beta  float32 [batch, seqlen, nheads]
+ *   h0       float32 [batch, nheads, dstate, headdim], the state before the
+ *            first token; NULL means zero
+ *   lens     int32 [batch], the tokens each row has (clamped to [0, seqlen]);
+ *            NULL: all of them.  o is zero behind a row's last token.
+ *   h_final  float32 like h0, the state after each row's last token (h0 for an
+ *            empty row); may be NULL, and may be the same buffer as h0
+ *   workspace, workspace_bytes as in cssd_chunked_forward.
+ * Returns a cssd_status. */
+int cssd_delta_forward(const cssd_delta_dims* dims, int dtype, const void* q, const void* k, const void* v,
+                       const float* g, const float* beta, float scale, const float* h0, const int32_t* lens, void* o,
+                       float* h_final, void* workspace, size_t workspace_bytes, cssd_stream_t stream);
+
+/* Gradients of a real loss through cssd_delta_forward: given dout = dL/do and
+ * dh_final = dL/dh_final (NULL means zero), writes gq, gk, gv (the tensors'
+ * type), gg, gbeta (float32) and gh0 = dL/dh0 (float32; may be NULL, and may
+ * be the same buffer as dh_final).  The forward's intermediates are made
+ * again inside the call.  Gradients of a shared key head are summed over its
+ * value heads in a fixed order; nothing depends on the order of atomics, so
+ * the same call gives the same bits.  Behind a row's length gradients are
+ * zero.  Other arguments as cssd_delta_forward. */
+int cssd_delta_backward(const cssd_delta_dims* dims, int dtype, const void* q, const void* k, const void* v,
+                        const float* g, const float* beta, float scale, const float* h0, const int32_t* lens,
+                        const void* dout, const float* dh_final, void* gq, void* gk, void* gv, float* gg, float* gbeta,
+                        float* gh0, void* workspace, size_t workspace_bytes, cssd_stream_t stream);
+
+/* One token for every batch row, the states updated in place.
+ *   h      float32 [nslots, nheads, dstate, headdim]
+ *   slots  int32 [batch], the state each row uses; NULL: row b uses state b
+ *          (nslots >= batch then, else CSSD_ERR_DIMS).  A row whose slot is
+ *          outside [0, nslots) touches no state and gets o = 0.  Two rows must
+ *          not name the same slot.
+ *   q, k [batch, kheads, dstate]   v, o [batch, nheads, headdim]
+ *   g, beta float32 [batch, nheads]
+ * Equals one token of cssd_delta_forward up to rounding. */
+int cssd_delta_step(const cssd_delta_dims* dims, int dtype, float* h, int64_t nslots, const int32_t* slots,
+                    const void* q, const void* k, const void* v, const float* g, const float* beta, float scale,
+                    void* o, cssd_stream_t stream);
+
+/* ---------------------------------------------------------------- layer norm
+ *     y = (x - mean(x)) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean(x))^2) + eps)
+ * over rows of `width` elements.  x, y and their gradients have type xtype;
+ * weight, bias and their gradients have type wtype, which is xtype or
+ * CSSD_F32.  weight and bias may be NULL (ones, no bias).  mean and rstd
+ * (float32 [rows]; may be NULL in the forward) are what the backward takes.
+ * Statistics and sums are fp32.  Any rows >= 1 and width >= 1 (up to 2^24);
+ * tensors dense, 16-byte aligned (mean and rstd 4).  y may be x; gx may be dy
+ * or x.  eps >= 0 (else CSSD_ERR_DIMS).
+ * Returns a cssd_status. */
+int cssd_layernorm(int64_t rows, int64_t width, int xtype, int wtype, const void* x, const void* weight,
+                   const void* bias, float eps, void* y, float* mean, float* rstd, cssd_stream_t stream);
+
+/* Gradients: gx like x, gweight and gbias [width] in wtype (either may be
+ * NULL: not computed), summed over the rows in a fixed order.  workspace: at
+ * least cssd_layernorm_backward_workspace_bytes(rows, width) bytes, 16-byte
+ * aligned, or NULL (the library allocates and frees it stream-ordered). */
+size_t cssd_layernorm_backward_workspace_bytes(int64_t rows, int64_t width);
+int cssd_layernorm_backward(int64_t rows, int64_t width, int xtype, int wtype, const void* dy, const void* x,
+                            const void* weight, const float* mean, const float* rstd, void* gx, void* gweight,
+                            void* gbias, void* workspace, size_t workspace_bytes, cssd_stream_t stream);
+
 /* Device status word.  Every wait a kernel of this library makes on other
  * threads or on the tensor cores is bounded; a wait that gives up lets the
  * kernel finish (its results are then invalid) and ORs a bit into a status word
