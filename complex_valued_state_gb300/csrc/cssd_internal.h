@@ -82,6 +82,7 @@ struct StepArgs {
 constexpr unsigned kStatusHandoff = 1u;   // chunk kernel: a state hand-off wait gave up
 constexpr unsigned kStatusChunkMma = 2u;  // chunk kernel: a tensor-core completion wait gave up
 constexpr unsigned kStatusBornMma = 4u;   // Born attention: a tensor-core completion wait gave up
+constexpr unsigned kStatusDelta = 8u;     // gated delta rule: a wait of a tensor-core kernel gave up
 unsigned* status_word();
 
 // Events the forward records around its dominant kernel (null = off); set by
@@ -193,6 +194,12 @@ size_t delta_workspace_bytes(const DeltaArgs& a);
 size_t delta_backward_workspace_bytes(const DeltaArgs& a);
 cudaError_t launch_delta_forward(const DeltaArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_delta_backward(const DeltaArgs& a, void* workspace, cudaStream_t stream);
+
+namespace delta {
+// The tensor-core kernels (delta_tc.cu), 16-bit types.
+size_t tc_workspace_bytes(const DeltaArgs& a);
+cudaError_t launch_forward_tc(const DeltaArgs& a, void* workspace, cudaStream_t stream);
+}  // namespace delta
 
 struct DeltaStepArgs {
     int64_t Bz, H, KH, N, P, nslots;

@@ -657,16 +657,16 @@ cudaError_t backward(const DeltaArgs& a, void* ws, cudaStream_t st) {
 }  // namespace
 }  // namespace delta
 
-size_t delta_workspace_bytes(const DeltaArgs& a) { return sizeof(float) * delta::tx_floats(a); }
+size_t delta_workspace_bytes(const DeltaArgs& a) {
+    return a.dtype == CSSD_F32 ? sizeof(float) * delta::tx_floats(a) : delta::tc_workspace_bytes(a);
+}
 size_t delta_backward_workspace_bytes(const DeltaArgs& a) {
     return sizeof(float) * (delta::tx_floats(a) + 2 * delta::state_floats(a) + 2 * delta::write_floats(a) +
                             2 * delta::part_floats(a));
 }
 
 cudaError_t launch_delta_forward(const DeltaArgs& a, void* ws, cudaStream_t st) {
-    if (a.dtype == CSSD_BF16) return delta::forward<__nv_bfloat16>(a, ws, st);
-    if (a.dtype == CSSD_F16) return delta::forward<__half>(a, ws, st);
-    return delta::forward<float>(a, ws, st);
+    return a.dtype == CSSD_F32 ? delta::forward<float>(a, ws, st) : delta::launch_forward_tc(a, ws, st);
 }
 cudaError_t launch_delta_backward(const DeltaArgs& a, void* ws, cudaStream_t st) {
     if (a.dtype == CSSD_BF16) return delta::backward<__nv_bfloat16>(a, ws, st);

@@ -1,0 +1,129 @@
+// What the tensor-core kernels of the gated delta rule share: operands in
+// IEEE half with a power-of-two scale a row, the chunk image that the prep
+// kernel leaves for the scans, and waits that give up.
+//
+// Precision.  A 16-bit input row times its power of two is exact in half (11
+// bits hold bf16's 8 and half's own 11; what lies 2^-37 below the row's
+// largest value is dropped).  An intermediate is held as two halves, hi (the
+// value cut to 11 bits) and lo (the remainder): 21 bits and a rounding, 2^-22
+// of the row's largest value.  A product of an exact operand with a split one
+// takes two passes, of two split ones three (lo lo is left out, 2^-22), all
+// into one fp32 accumulator, so the states, which are float32 tensors of the
+// interface, keep fp32 accuracy.
+#pragma once
+
+#include "delta_common.cuh"
+#include "tcgen05.cuh"
+
+namespace cssd {
+namespace delta {
+
+constexpr long long kDeltaWait = 4000000000LL;  // ~2 s at 2 GHz
+
+// The power of two that brings `top` (a row's largest absolute value) into
+// [2^13, 2^14), and its inverse.  An infinite or NaN top gives a scale whose
+// products are infinite or NaN again.
+struct RowScale {
+    float up, down;
+};
+__device__ __forceinline__ RowScale row_scale(float top) {
+    int e = (int)((__float_as_uint(top) >> 23) & 255u);
+    e = max(e, 14);
+    return {__uint_as_float((uint32_t)(267 - e) << 23), __uint_as_float((uint32_t)(e - 13) << 23)};
+}
+
+// Two values (already scaled) as half pairs: element 0 in the low half.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    const float h0 = __uint_as_float(__float_as_uint(x0) & 0xFFFFE000u);
+    const float h1 = __uint_as_float(__float_as_uint(x1) & 0xFFFFE000u);
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(h1), "f"(h0));
+    const float l0 = x0 - h0, l1 = x1 - h1;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(l1), "f"(l0));
+}
+__device__ __forceinline__ uint32_t pack2(float x0, float x1) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x1), "f"(x0));
+    return r;
+}
+
+// A pair of 16-bit inputs as floats.
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// Largest absolute value of packed pairs, as packed 16-bit patterns (for both
+// types the order of |x| is that of the bits; NaN is above infinity).
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b) {
+    return __vmaxu2(a & 0x7FFF7FFFu, b & 0x7FFF7FFFu);
+}
+template <typename E>
+__device__ __forceinline__ float top_of(uint32_t m) {
+    const float2 f = unpack2(m, E());
+    return f.x != f.x || f.y != f.y ? __uint_as_float(0x7F800000u) : fmaxf(f.x, f.y);
+}
+
+// D[tmem] (+)= A[tmem] B[smem]^T, half operands, issued by one thread.  Row m
+// of A is lane m; K elements 2c and 2c + 1 are the halves of column c.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// 32 TMEM lanes (this warp's quarter) x 32 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* m) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(m)) : "memory");
+}
+
+// Wait for a phase parity; false once this or another wait of the CTA has
+// given up (after ~2 s), which `gave_up` tells the others.
+__device__ __forceinline__ bool wait_or_give_up(uint64_t* m, uint32_t parity, volatile int* gave_up) {
+    if (tc::mbar_try_wait(m, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (tc::mbar_try_wait(m, parity)) return true;
+        if (*gave_up) return false;
+        if (clock64() - t0 > kDeltaWait) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+}
+
+// The same by a whole warp: true for all its lanes or for none.
+__device__ __forceinline__ bool warp_wait(uint64_t* m, uint32_t parity, volatile int* gave_up) {
+    return __all_sync(0xffffffffu, wait_or_give_up(m, parity, gave_up));
+}
+
+// The image a chunk's prep leaves in the workspace, copied whole into shared
+// memory by the scans: [T; X] as a B operand of 128 rows (T's 64, then X's)
+// by 64, hi then lo, and the chunk's factors.
+struct Image {
+    static constexpr uint32_t SBO = 128, LBO = 16 * 128;  // row groups, column groups of 8
+    static constexpr uint32_t PART = 8 * LBO;              // one part's bytes (16 KB)
+    static constexpr uint32_t F = 2 * PART;                // floats from here
+    static constexpr int DOWN = 0, IN = 128, OUT = 192, BETA = 256, ALL = 320, FLOATS = 324;
+    static constexpr uint32_t BYTES = F + 4 * FLOATS;
+    static constexpr uint32_t STRIDE = (BYTES + 255) / 256 * 256;
+};
+
+}  // namespace delta
+}  // namespace cssd
