@@ -151,8 +151,7 @@ __global__ void __launch_bounds__(NT) delta_prep(const E* __restrict__ q, const 
     float* sq = sk + C * LK;
     float* a = sq + C * LK;
     float* p = a + C * LT;
-    float* t = p + C * LT;
-    float* w = t + C * LT;
+    float* w = p + C * LT;
     const int64_t t0 = (int64_t)b * ge.T + (int64_t)c * C;
     const int64_t ko = (t0 * KH + h / ge.G) * ge.N, ks = (int64_t)KH * ge.N;
     load_rows(sk, LK, k + ko, ks, C, ge.N, n, tid);
@@ -173,7 +172,8 @@ __global__ void __launch_bounds__(NT) delta_prep(const E* __restrict__ q, const 
             p[i * LT + j] = i >= j ? m * qk[x][y] : 0.f;
         }
     __syncthreads();
-    tri_inverse<LT>(a, t, w, tid);
+    tri_inverse_in_place<LT>(a, w, tid);
+    const float* t = a;
     float x[4][4] = {};
     mm_rk<4, 16>(x, p, LT, t, LT, C, ti, 4 * tj);
     float* out = tx + (int64_t)blockIdx.x * 2 * C * C;
@@ -585,7 +585,7 @@ size_t scan_smem(const DeltaArgs& a) { return sizeof(float) * (2 * C * (a.N + 4)
 
 template <typename E>
 cudaError_t prep(const DeltaArgs& a, float* tx, cudaStream_t st) {
-    const size_t sm = sizeof(float) * (2 * C * (a.N + 4) + 3 * C * LT + 32 * 32);
+    const size_t sm = sizeof(float) * (2 * C * (a.N + 4) + 2 * C * LT + 32 * 32);
     cudaError_t e = allow_smem(delta_prep<E>, sm);
     if (e != cudaSuccess) return e;
     delta_prep<E><<<(unsigned)(a.Bz * a.H * chunks(a)), NT, sm, st>>>(

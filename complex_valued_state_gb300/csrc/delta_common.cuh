@@ -32,10 +32,21 @@ __device__ __forceinline__ int row_len(const int* lens, int b, int T) {
     return lens ? min(max(lens[b], 0), T) : T;
 }
 
+// A sum kept as two floats, value and what its rounding left.
+struct Sum2 {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum2 add(Sum2 a, Sum2 b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+__device__ __forceinline__ float exp_of(Sum2 s) { return expf(s.hi) * (1.f + (isfinite(s.hi) ? s.lo : 0.f)); }
+
 // The decays of one chunk, from the running sum G_i of its log decays.  The
-// sum is taken in double and kept as two floats, because exp(G_i - G_j) needs
-// the difference of two sums to an absolute 1e-7 while the sums themselves
-// reach hundreds.
+// sums are kept as two floats, because exp(G_i - G_j) needs the difference of
+// two sums to an absolute 1e-7 while the sums themselves reach hundreds.
 struct Decays {
     float hi[C], lo[C];  // G_i as hi + lo
     float in[C];         // exp(G_i): from the chunk's start through token i
@@ -50,7 +61,7 @@ struct Decays {
 // so that differences of sums stay numbers; NaN passes through.
 __device__ __forceinline__ void chunk_decays(Decays& d, const float* g, const float* beta, int64_t stride, int n,
                                              int lane) {
-    double s[2];
+    Sum2 s[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
@@ -59,31 +70,27 @@ __device__ __forceinline__ void chunk_decays(Decays& d, const float* g, const fl
             gv = g[i * stride];
             bv = beta[i * stride];
         }
-        gv = gv < -1000.f ? -1000.f : gv;
         d.beta[i] = bv;
-        s[e] = (double)gv;
+        s[e] = {gv < -1000.f ? -1000.f : gv, 0.f};
     }
-    s[1] += s[0];
-    double tot = s[1];
+    s[1] = add(s[0], s[1]);
+    Sum2 tot = s[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, tot, o);
-        if (lane >= o) tot += up;
+        const Sum2 up = {__shfl_up_sync(0xffffffffu, tot.hi, o), __shfl_up_sync(0xffffffffu, tot.lo, o)};
+        if (lane >= o) tot = add(up, tot);
     }
-    double before = __shfl_up_sync(0xffffffffu, tot, 1);
-    if (lane == 0) before = 0.0;
-    const double end = __shfl_sync(0xffffffffu, tot, 31);
+    Sum2 before = {__shfl_up_sync(0xffffffffu, tot.hi, 1), __shfl_up_sync(0xffffffffu, tot.lo, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const Sum2 end = {__shfl_sync(0xffffffffu, tot.hi, 31), __shfl_sync(0xffffffffu, tot.lo, 31)};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
-        const double G = before + s[e];
-        const float hi = (float)G, lo = (float)(G - (double)hi);
-        const double r = end - G;
-        const float rh = (float)r, rl = (float)(r - (double)rh);
-        d.hi[i] = hi;
-        d.lo[i] = isfinite(hi) ? lo : 0.f;
-        d.in[i] = expf(hi) * (1.f + d.lo[i]);
-        d.out[i] = expf(rh) * (1.f + (isfinite(rh) ? rl : 0.f));
+        const Sum2 G = add(before, s[e]);
+        d.hi[i] = G.hi;
+        d.lo[i] = G.lo;
+        d.in[i] = exp_of(G);
+        d.out[i] = exp_of(add(end, {-G.hi, -G.lo}));
         if (i == C - 1) d.all = d.in[i];
     }
 }
@@ -93,54 +100,68 @@ __device__ __forceinline__ float decay_between(const Decays& d, int i, int j) {
     return expf((d.hi[i] - d.hi[j]) + (d.lo[i] - d.lo[j]));
 }
 
-// t = (I + a)^-1 for the strictly lower triangular a (64 x 64, row stride
-// LD, fp32, in shared memory), by 256 threads: the four 16 x 16 blocks on the
-// diagonal by forward substitution, one column a thread, then two rounds of
-//   [L11 0; A21 L22]^-1 = [T11 0; -T22 A21 T11 T22].
-// `w` is 32 x 32 floats of scratch.  All threads call it; t is complete after
-// its last barrier.  t's upper triangle is written as zeros.
+// (I + a)^-1 in place of the strictly lower triangular a (64 x 64, row stride
+// LD, fp32, in shared memory, 16-byte aligned rows), by 256 threads: the four
+// 16 x 16 blocks on the diagonal by forward substitution, one column a thread,
+// then two rounds of
+//   [L11 0; A21 L22]^-1 = [T11 0; -T22 A21 T11 T22],
+// four outputs of a row a thread.  `w` is 32 x 32 floats of scratch, 16-byte
+// aligned.  All threads call it; the result is complete after its last
+// barrier.  The upper triangle has to be zeros and stays so.
 template <int LD>
-__device__ void tri_inverse(const float* a, float* t, float* w, int tid) {
-    for (int e = tid; e < C * C; e += 256) {
-        const int i = e / C, j = e % C;
-        if ((j >> 4) > (i >> 4)) t[i * LD + j] = 0.f;
-    }
+__device__ void tri_inverse_in_place(float* a, float* w, int tid) {
     if (tid < 64) {
         const int b = tid >> 4, j = tid & 15;
-        const float* ab = a + (b * 16) * LD + b * 16;
-        float* tb = t + (b * 16) * LD + b * 16;
+        float* ab = a + (b * 16) * LD + b * 16;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float s = i == j ? 1.f : 0.f;
+            float s = i == j ? 1.f : 0.f, s2 = 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) s = fmaf(-ab[i * LD + m], x[m], s);
-            x[i] = i < j ? 0.f : s;
+            for (int m = 0; m < i; m += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(ab + i * LD + m);
+                s = fmaf(-v.x, x[m], s);
+                if (m + 1 < i) s2 = fmaf(-v.y, x[m + 1], s2);
+                if (m + 2 < i) s = fmaf(-v.z, x[m + 2], s);
+                if (m + 3 < i) s2 = fmaf(-v.w, x[m + 3], s2);
+            }
+            x[i] = i < j ? 0.f : s + s2;
         }
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) tb[i * LD + j] = x[i];
+        for (int i = 0; i < 16; ++i) ab[i * LD + j] = x[i];
     }
     __syncthreads();
 #pragma unroll
     for (int half = 16; half <= 32; half *= 2) {
-        const int pairs = C / (2 * half), per = half * half;
-        for (int e = tid; e < pairs * per; e += 256) {  // w = A21 T11
-            const int p = e / per, r = (e % per) / half, c = e % half;
-            const float* a21 = a + (2 * p + 1) * half * LD + 2 * p * half;
-            const float* t11 = t + 2 * p * half * LD + 2 * p * half;
-            float s = 0.f;
+        // 64 / (2 half) pairs of half x half outputs, a quad of a row a thread
+        const int quads = half / 4, p = tid / (half * quads), r = tid / quads % half, c = tid % quads * 4;
+        const bool on = p < C / (2 * half);
+        float* a21 = a + (2 * p + 1) * half * LD + 2 * p * half;
+        const float* t11 = a + 2 * p * half * LD + 2 * p * half;
+        const float* t22 = a + (2 * p + 1) * half * LD + (2 * p + 1) * half;
+        float* wp = w + p * half * half;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on) {  // w = A21 T11
 #pragma unroll 8
-            for (int m = 0; m < half; ++m) s = fmaf(a21[r * LD + m], t11[m * LD + c], s);
-            w[e] = s;
+            for (int m = 0; m < half; ++m) {
+                const float v = a21[r * LD + m];
+                const float4 t = *reinterpret_cast<const float4*>(t11 + m * LD + c);
+                s.x = fmaf(v, t.x, s.x), s.y = fmaf(v, t.y, s.y), s.z = fmaf(v, t.z, s.z), s.w = fmaf(v, t.w, s.w);
+            }
+            *reinterpret_cast<float4*>(wp + r * half + c) = s;
         }
         __syncthreads();
-        for (int e = tid; e < pairs * per; e += 256) {  // T21 = -T22 w
-            const int p = e / per, r = (e % per) / half, c = e % half;
-            const float* t22 = t + (2 * p + 1) * half * LD + (2 * p + 1) * half;
-            float s = 0.f;
-#pragma unroll 8
-            for (int m = 0; m < half; ++m) s = fmaf(-t22[r * LD + m], w[p * per + m * half + c], s);
-            t[((2 * p + 1) * half + r) * LD + 2 * p * half + c] = s;
+        if (on) {  // T21 = -T22 w, over A21 (T22 is lower triangular: a warp stops at its last row)
+            s = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int stop = (tid | 31) / quads % half + 1;
+#pragma unroll 4
+            for (int m = 0; m < stop; ++m) {
+                const float v = -t22[r * LD + m];
+                const float4 t = *reinterpret_cast<const float4*>(wp + m * half + c);
+                s.x = fmaf(v, t.x, s.x), s.y = fmaf(v, t.y, s.y), s.z = fmaf(v, t.z, s.z), s.w = fmaf(v, t.w, s.w);
+            }
+            *reinterpret_cast<float4*>(a21 + r * LD + c) = s;
         }
         __syncthreads();
     }

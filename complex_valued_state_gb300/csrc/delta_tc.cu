@@ -2,7 +2,7 @@
 // tensor cores (the formulas stand at the head of delta.cu; the operand
 // precision at the head of delta_tc.cuh).
 //
-// delta_prep_tc, one CTA per chunk and value head: [K; Q] K^T by one MMA
+// delta_prep_tc, one CTA per chunk and value head: [Q; K] K^T by one MMA
 // chain, T = (I + A)^-1 and X = P T in fp32 on the CUDA cores, both left in
 // the workspace as the very bytes the scan's B operand wants.
 //
@@ -36,64 +36,48 @@ struct Shape {
 };
 
 // --------------------------------------------------------------- operands
-// [K; Q]: rows i (64 of K, 64 of Q) by ND.  Column groups one 16-byte row
-// apart from a multiple of 128, so that the lanes of a row group's column
-// blocks store to different banks.
-template <int ND>
-struct KQ {
-    static constexpr uint32_t SBO = 128, LBO = 16 * 128 + 16, BYTES = (ND / 8) * LBO;
-    static constexpr uint32_t QROWS = 8 * SBO;  // bytes from K's rows to Q's
-};
-// K^T: rows k (ND) by 64 tokens, for the same reason with padded row groups.
-template <int ND>
-struct KT {
-    static constexpr uint32_t SBO = 144, LBO = (ND / 8) * SBO, BYTES = 8 * LBO;
-};
-
-// One 8 x 8 block (8 tokens from `tok`, 8 columns): raw rows, zero where no
-// token or column is.
-template <typename E>
-__device__ __forceinline__ void load_block(uint4 (&raw)[8], const E* src, int64_t stride, int tok, int n, bool cols) {
+// Half a row (ND / 2 columns) scaled and packed; the scale is the row's over
+// the two lanes that hold it.  Stores into the operand's row `r`, returns the
+// inverse scale.
+template <typename E, int ND>
+__device__ __forceinline__ float store_half_row(const uint4 (&raw)[ND / 16], unsigned char* base, int r, int part) {
+    uint32_t m = 0;
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-        raw[r] = (cols && tok + r < n) ? *reinterpret_cast<const uint4*>(src + (tok + r) * stride) : make_uint4(0, 0, 0, 0);
-}
-// The block scaled row by row (the scale is the row's over the CB lanes that
-// hold its blocks) and packed to half; `down` gets the inverse scales.
-template <typename E, int CB>
-__device__ __forceinline__ void scale_block(const uint4 (&raw)[8], uint32_t (&w)[8][4], float (&down)[8]) {
+    for (int g = 0; g < ND / 16; ++g)
+        m = __vmaxu2(m, __vmaxu2(absmax2(raw[g].x, raw[g].y), absmax2(raw[g].z, raw[g].w)));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const RowScale s = row_scale(top_of<E>(m));
+    unsigned char* p = base + (r / 8) * QK<ND>::SBO + (r % 8) * 16 + part * (ND / 16) * QK<ND>::LBO;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        uint32_t m = absmax2(absmax2(raw[r].x, raw[r].y), absmax2(raw[r].z, raw[r].w));
-#pragma unroll
-        for (int o = 1; o < CB; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const RowScale s = row_scale(top_of<E>(m));
-        down[r] = s.down;
-        const uint32_t in[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
+    for (int g = 0; g < ND / 16; ++g) {
+        const uint32_t in[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+        uint32_t w[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const float2 f = unpack2(in[c], E());
-            w[r][c] = pack2(f.x * s.up, f.y * s.up);
+            w[c] = pack2(f.x * s.up, f.y * s.up);
         }
+        *reinterpret_cast<uint4*>(p + g * QK<ND>::LBO) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    return s.down;
 }
-// Rows as they are: row group rg, column block cb.
-__device__ __forceinline__ void store_rows(unsigned char* base, uint32_t lbo, uint32_t sbo, int rg, int cb,
-                                           const uint32_t (&w)[8][4]) {
-    unsigned char* p = base + cb * lbo + rg * sbo;
+// The transposed operand (rows k, 64 tokens) of 64 rows of the operand at
+// `from`, whose first row is `row0`: 8 x 8 blocks through ldmatrix, a warp four at a
+// time, 128 contiguous bytes a block either way.
+template <int ND>
+__device__ __forceinline__ void transpose_operand(unsigned char* to, const unsigned char* from, int row0, int warp,
+                                                  int warps, int lane) {
+    for (int q = warp; q < 2 * (ND / 8); q += warps) {  // column block q / 2, token blocks 4 (q % 2)..
+        const int cb = q / 2, tb = 4 * (q % 2);
+        const uint32_t at = tc::smem_u32(from) + cb * QK<ND>::LBO + (row0 / 8 + tb + lane / 8) * QK<ND>::SBO + (lane % 8) * 16;
+        uint32_t w[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at)
+                     : "memory");
 #pragma unroll
-    for (int r = 0; r < 8; ++r) *reinterpret_cast<uint4*>(p + 16 * r) = make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]);
-}
-// Transposed: columns become rows, the block's 8 tokens one 16-byte row.
-__device__ __forceinline__ void store_transposed(unsigned char* base, uint32_t lbo, uint32_t sbo, int rg, int cb,
-                                                 const uint32_t (&w)[8][4]) {
-    unsigned char* p = base + rg * lbo + cb * sbo;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const uint32_t sel = c & 1 ? 0x7632u : 0x5410u;
-        *reinterpret_cast<uint4*>(p + 16 * c) =
-            make_uint4(__byte_perm(w[0][c / 2], w[1][c / 2], sel), __byte_perm(w[2][c / 2], w[3][c / 2], sel),
-                       __byte_perm(w[4][c / 2], w[5][c / 2], sel), __byte_perm(w[6][c / 2], w[7][c / 2], sel));
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint32_t*>(to + (tb + i) * KT<ND>::LBO + cb * KT<ND>::SBO + (lane / 4) * 16 + (lane % 4) * 4) = w[i];
     }
 }
 
@@ -101,23 +85,71 @@ __device__ __forceinline__ void store_transposed(unsigned char* base, uint32_t l
 constexpr int PT = 256;      // threads
 constexpr int LT = C + 4;    // row stride of the fp32 matrices
 
-template <int ND>
+template <int ND, bool BACK>
 struct PrepSmem {
-    static constexpr uint32_t STAGE = KQ<ND>::BYTES > Image::STRIDE ? KQ<ND>::BYTES : Image::STRIDE;
-    static constexpr uint32_t A = STAGE, P = A + 4 * C * LT, T = P + 4 * C * LT, W = T + 4 * C * LT;
-    static constexpr uint32_t BYTES = W + 4 * 32 * 32;
+    // The operands of K and Q; once they are read, A (then T) and P (then X)
+    // lie over them, and over those the image, when T and X are in registers.
+    // The backward, which reads T and X again for its second image, has the
+    // images behind them.
+    static constexpr uint32_t OPS = BACK ? Operands<ND>::BWD : Operands<ND>::FWD;
+    static constexpr uint32_t A = 0, P = 4 * C * LT, W = 2 * P, IMG = BACK ? W : 0;
+    static constexpr uint32_t mx(uint32_t a, uint32_t b) { return a > b ? a : b; }
+    static constexpr uint32_t BYTES = mx(mx(OPS, W + 4 * 32 * 32), IMG + Image::STRIDE);
 };
 
-template <typename E, int ND>
-__global__ void __launch_bounds__(PT) delta_prep_tc(const E* __restrict__ q, const E* __restrict__ k,
-                                                    const float* __restrict__ g, const float* __restrict__ beta,
-                                                    const int* __restrict__ lens, unsigned char* __restrict__ image,
-                                                    Shape sh, unsigned* status) {
-    using M = PrepSmem<ND>;
-    constexpr int CB = ND / 8;
+// 16 values of a row of the image (columns 16 part..), scaled and split; returns
+// the sum of their absolute values.
+__device__ __forceinline__ float image_row(unsigned char* img, int row, int part, const float (&e)[16], float up) {
+    float sum = 0.f;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float a = e[8 * g + 2 * u], b = e[8 * g + 2 * u + 1];
+            sum += fabsf(a) + fabsf(b);
+            split2(a * up, b * up, h[u], l[u]);
+        }
+        unsigned char* at = img + (2 * part + g) * Image::LBO + (row / 8) * Image::SBO + (row % 8) * 16;
+        *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(at + Image::PART) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+    return sum;
+}
+
+// One warp: the chunk's decay and the larger of its lanes' bounds.
+__device__ __forceinline__ void put_scalars(float* ff, float all, float b1, float b2, int lane) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
+        b2 = fmaxf(b2, __shfl_xor_sync(0xffffffffu, b2, o));
+    }
+    if (lane == 0) {
+        ff[Image::ALL] = all;
+        ff[Image::BND1] = b1;
+        ff[Image::BND2] = b2;
+        ff[Image::FLOATS - 1] = 0.f;
+    }
+}
+
+// BACK: a second image for the backward scan, [T^T; X^T].
+template <typename E, int ND, bool BACK>
+__global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __restrict__ q, const E* __restrict__ k,
+                                                       const float* __restrict__ g, const float* __restrict__ beta,
+                                                       const int* __restrict__ lens, unsigned char* __restrict__ image,
+                                                       unsigned char* __restrict__ image_t,
+                                                       unsigned char* __restrict__ operands, float scale, Shape sh,
+                                                       unsigned* status) {
+    using M = PrepSmem<ND, BACK>;
+    using O = Operands<ND>;
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ Decays d;
-    __shared__ float s_down[2 * C];
+    __shared__ __align__(16) Decays d;
+    __shared__ __align__(16) float s_down[2 * C];  // inverse scales of K's and Q's rows
+    __shared__ float s_sum[4][C], s_norm[C];      // parts of sums over T's rows (columns); beta e^G |k|
+    __shared__ float s_top[4][PT / 32];
+    __shared__ __align__(16) float s_f[4][C];  // exp(G_a - G_j) s_down[j], a the starts of the 16-token blocks
+    __shared__ float s_e[C];                   // exp(G_i - G_a), a the start of i's block
+    __shared__ int s_steep;
     __shared__ __align__(8) uint64_t mb[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
@@ -128,9 +160,14 @@ __global__ void __launch_bounds__(PT) delta_prep_tc(const E* __restrict__ q, con
     if (n <= 0) return;
     const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C;
     const int64_t ko = (t0 * KH + h / sh.G) * sh.N, ks = (int64_t)KH * sh.N;
-    uint4 raw[8];
-    const int which = tid / (8 * CB), rg = tid / CB % 8, cb = tid % CB;
-    if (tid < 16 * CB) load_block(raw, (which ? q : k) + ko + 8 * cb, ks, 8 * rg, n, 8 * cb < sh.N);
+    uint4 raw[ND / 16];  // half a row: of Q's token tid / 2, or of K's
+    const int qrow = tid / 2, half = tid % 2, tok = qrow % C;
+    {
+        const E* src = (qrow < C ? q : k) + ko + tok * ks + half * (ND / 2);
+#pragma unroll
+        for (int g = 0; g < ND / 16; ++g)
+            raw[g] = tok < n && half * (ND / 2) + 8 * g < sh.N ? *reinterpret_cast<const uint4*>(src + 8 * g) : make_uint4(0, 0, 0, 0);
+    }
     if (warp == 7) {
         tc::tmem_alloc(&s_tmem, 64);
         tc::tmem_relinquish();
@@ -140,15 +177,11 @@ __global__ void __launch_bounds__(PT) delta_prep_tc(const E* __restrict__ q, con
         tc::mbar_init(&mb[1], 1);
         tc::mbar_fence_init();
         s_gave_up = 0;
+        s_steep = 0;
     }
-    if (tid < 16 * CB) {
-        uint32_t w[8][4];
-        float down[8];
-        scale_block<E, CB>(raw, w, down);
-        store_rows(smem, KQ<ND>::LBO, KQ<ND>::SBO, 8 * which + rg, cb, w);
-        if (cb == 0)
-#pragma unroll
-            for (int r = 0; r < 8; ++r) s_down[C * which + 8 * rg + r] = down[r];
+    {
+        const float down = store_half_row<E, ND>(raw, smem, qrow, half);
+        if (half == 0) s_down[qrow < C ? C + tok : tok] = down;  // (K's first)
     }
     if (warp == 6) chunk_decays(d, g + t0 * sh.H + h, beta + t0 * sh.H + h, sh.H, n, lane);
     tc::fence_proxy_async();
@@ -157,53 +190,101 @@ __global__ void __launch_bounds__(PT) delta_prep_tc(const E* __restrict__ q, con
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
     if (tid == 0) {
-        const uint64_t desc = tc::make_desc(tc::smem_u32(smem), KQ<ND>::LBO, KQ<ND>::SBO);
+        const uint64_t desc = tc::make_desc(tc::smem_u32(smem), QK<ND>::LBO, QK<ND>::SBO);
 #pragma unroll
         for (int kk = 0; kk < ND / 16; ++kk) {
-            const uint64_t at = desc + (uint64_t)((2 * kk * KQ<ND>::LBO) >> 4);
-            tc::mma_f16(tmem, at, at, tc::idesc_f16(128, C), kk != 0);
+            const uint64_t at = desc + (uint64_t)((2 * kk * QK<ND>::LBO) >> 4);
+            tc::mma_f16(tmem, at, at + (QK<ND>::KROWS >> 4), tc::idesc_f16(128, C), kk != 0);
         }
         tc::commit(&mb[0]);
     }
-    float* sa = reinterpret_cast<float*>(smem + M::A);
+    float* sa = reinterpret_cast<float*>(smem + M::A);  // A, then T in its place
     float* sp = reinterpret_cast<float*>(smem + M::P);
-    float* st = reinterpret_cast<float*>(smem + M::T);
-    float* sw = reinterpret_cast<float*>(smem + M::W);
-    warp_wait(&mb[0], 0, &s_gave_up);
-    tc::fence_after_sync();
-    {  // lane i of tensor memory: row i of K (the first 64), of Q; columns j in halves
-        const int row = 32 * (warp % 4) + lane, i = row % C, j0 = 32 * (warp / 4);
-        uint32_t v[32];
-        tmem_ld32(tmem + ((uint32_t)(32 * (warp % 4)) << 16) + j0, v);
-        tc::tmem_wait_ld();
-        const bool is_a = row < C;
-        float* dst = (is_a ? sa : sp) + i * LT + j0;
-        const float f = s_down[row] * (is_a ? d.beta[i] : 1.f);
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            float x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int col = j0 + j + u;
-                const bool keep = is_a ? i > col : i >= col;
-                x[u] = keep ? __uint_as_float(v[j + u]) * s_down[col] * f * decay_between(d, i, col) : 0.f;
-            }
-            *reinterpret_cast<float4*>(dst + j) = make_float4(x[0], x[1], x[2], x[3]);
+    {  // the tables of decays while the MMA runs
+        const int a = 16 * (tid / C), j = tid % C;
+        // G_a - G_j as a float and what its rounding leaves
+        const float at = d.hi[a] - d.hi[j], back = at - d.hi[a];
+        const float rest = ((d.hi[a] - (at - back)) - (d.hi[j] + back)) + (d.lo[a] - d.lo[j]);
+        s_f[tid / C][j] = j < a + 16 ? expf(at) * (1.f + rest) * s_down[j] : 0.f;
+        if (j / 16 == tid / C) {
+            s_e[j] = expf(-at) * (1.f - rest);
+            if (!(fabsf(at) < 40.f)) s_steep = 1;  // (a NaN or infinite sum too)
         }
     }
+    const bool owner = h % sh.G == 0;  // this CTA leaves the key head's operands, once for its group
+    if (owner) {
+        transpose_operand<ND>(smem + O::KT0, smem, C, warp, PT / 32, lane);
+        if (BACK) transpose_operand<ND>(smem + O::QT0, smem, 0, warp, PT / 32, lane);
+        tc::fence_proxy_async();
+    }
     __syncthreads();
-    tri_inverse<LT>(sa, st, sw, tid);
-    // X = P T, 4 x 4 a thread; then T's and X's rows as half pairs into the image
+    if (tid == 0 && owner) {
+        bulk_s2g(operands + (((int64_t)b * KH + h / sh.G) * sh.nc + c) * O::stride(BACK), tc::smem_u32(smem), M::OPS);
+        bulk_commit();
+    }
+    {  // lane i of tensor memory: row i of Q (the first 64), of K; columns j in halves
+        const int row = 32 * (warp % 4) + lane, i = row % C, j0 = 32 * (warp / 4);
+        const bool is_a = row >= C;
+        float* dst = (is_a ? sa : sp) + i * LT + j0;
+        const bool above = 32 * (warp % 2) < j0;  // every pair of this warp has i < j
+        uint32_t v[32];
+        warp_wait(&mb[0], 0, &s_gave_up);
+        tc::fence_after_sync();
+        tmem_ld32(tmem + ((uint32_t)(32 * (warp % 4)) << 16) + j0, v);
+        tc::tmem_wait_ld();
+        const float f = is_a ? s_down[i] * d.beta[i] : s_down[C + i];
+        const int last = is_a ? i - 1 : i;  // the row's last column that is not zero
+        float x[32];
+        if (is_a && i / 32 == j0 / 32) {  // (K K^T)_ii: beside the diagonal's own scale
+            float diag = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) diag = j0 + j == i ? __uint_as_float(v[j]) : diag;
+            s_norm[i] = sqrtf(diag) * s_down[i] * d.in[i];
+        }
+        if (above) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = 0.f;
+        } else if (!s_steep) {
+            // e^{G_i - G_j} as a product over the start of i's block: exact enough
+            // while a block's decay, which one factor undoes, stays above e^-40
+            const float fe = f * s_e[i];
+            const float4* fj = reinterpret_cast<const float4*>(s_f[i / 16] + j0);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 m = fj[j / 4];
+                x[j] = j0 + j <= last ? __uint_as_float(v[j]) * (m.x * fe) : 0.f;
+                x[j + 1] = j0 + j + 1 <= last ? __uint_as_float(v[j + 1]) * (m.y * fe) : 0.f;
+                x[j + 2] = j0 + j + 2 <= last ? __uint_as_float(v[j + 2]) * (m.z * fe) : 0.f;
+                x[j + 3] = j0 + j + 3 <= last ? __uint_as_float(v[j + 3]) * (m.w * fe) : 0.f;
+            }
+        } else {
+            const float hi = d.hi[i], lo = d.lo[i];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                // (exp's own error is relative to a value that falls as fast as its argument grows)
+                const float m = __expf((hi - d.hi[j0 + j]) + (lo - d.lo[j0 + j]));
+                x[j] = j0 + j <= last ? __uint_as_float(v[j]) * (s_down[j0 + j] * f) * m : 0.f;
+            }
+        }
+        if (tid == 0) bulk_wait_read();  // the operands are copied out: their memory is free
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    }
+    __syncthreads();
+    tri_inverse_in_place<LT>(sa, reinterpret_cast<float*>(smem + M::W), tid);
+    // X = P T (both lower triangular), 4 x 4 a thread: a warp holds 8 rows and
+    // stops at their last column
     const int ti = tid / 16, tj = tid % 16;
     float x[4][4] = {};
-#pragma unroll 4
-    for (int m = 0; m < C; m += 4) {
+#pragma unroll 2
+    for (int m = 0; m < 8 * (warp + 1); m += 4) {
         float4 bv[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) bv[u] = *reinterpret_cast<const float4*>(st + (m + u) * LT + 4 * tj);
+        for (int u = 0; u < 4; ++u) bv[u] = *reinterpret_cast<const float4*>(sa + (m + u) * LT + 4 * tj);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float4 av = *reinterpret_cast<const float4*>(sp + (ti + 16 * r) * LT + m);
+            const float4 av = *reinterpret_cast<const float4*>(sp + (4 * ti + r) * LT + m);
             const float a[4] = {av.x, av.y, av.z, av.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -214,36 +295,95 @@ __global__ void __launch_bounds__(PT) delta_prep_tc(const E* __restrict__ q, con
             }
         }
     }
-    float* ff = reinterpret_cast<float*>(smem + Image::F);
-    auto put = [&](int row, float (&e)[4]) {  // columns 4 tj.. of one row, held by the 16 threads of ti
-        float top = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const RowScale s = row_scale(top);
-        uint2 hi, lo;
-        split2(e[0] * s.up, e[1] * s.up, hi.x, lo.x);
-        split2(e[2] * s.up, e[3] * s.up, hi.y, lo.y);
-        unsigned char* at = smem + (tj / 2) * Image::LBO + (row / 8) * Image::SBO + (row % 8) * 16 + (tj % 2) * 8;
-        *reinterpret_cast<uint2*>(at) = hi;
-        *reinterpret_cast<uint2*>(at + Image::PART) = lo;
-        if (tj == 0) ff[Image::DOWN + row] = s.down;
+    unsigned char* img = smem + M::IMG;
+    float* ff = reinterpret_cast<float*>(img + Image::F);
+    auto write_out = [&](unsigned char* to) {
+        tc::fence_proxy_async();
+        __syncthreads();
+        if (tid == 0) {
+            bulk_s2g(to + (int64_t)blockIdx.x * Image::STRIDE, tc::smem_u32(img), Image::BYTES);
+            bulk_commit();
+            bulk_wait_read();
+        }
     };
+    __syncthreads();  // P is read
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const float4 tv = *reinterpret_cast<const float4*>(st + (ti + 16 * r) * LT + 4 * tj);
-        float e[4] = {tv.x, tv.y, tv.z, tv.w};
-        put(ti + 16 * r, e);
-        put(C + ti + 16 * r, x[r]);
-    }
-    if (tid < C) {
-        ff[Image::IN + tid] = d.in[tid];
-        ff[Image::OUT + tid] = d.out[tid];
-        ff[Image::BETA + tid] = d.beta[tid];
-    }
-    if (tid < Image::FLOATS - Image::ALL) ff[Image::ALL + tid] = tid == 0 ? d.all : 0.f;
+    for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4*>(sp + (4 * ti + r) * LT + 4 * tj) = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
     __syncthreads();
-    uint4* out = reinterpret_cast<uint4*>(image + (int64_t)blockIdx.x * Image::STRIDE);
-    for (int e = tid; e < (int)(Image::BYTES / 16); e += PT) out[e] = reinterpret_cast<const uint4*>(smem)[e];
+    // T and X into the image: a thread has 16 columns of one row.  One scale a
+    // matrix: the scales have 2^16 to spare.
+    const int row = lane + 32 * (warp & 1), part = warp >> 1;
+    float te[16], xe[16], tops[4] = {};  // of beta T, beta X; of T, X
+#pragma unroll
+    for (int u = 0; u < 16; u += 4) {
+        const float4 t4 = *reinterpret_cast<const float4*>(sa + row * LT + 16 * part + u);
+        const float4 x4 = *reinterpret_cast<const float4*>(sp + row * LT + 16 * part + u);
+        const float4 b4 = *reinterpret_cast<const float4*>(d.beta + 16 * part + u);
+        te[u] = t4.x * b4.x, te[u + 1] = t4.y * b4.y, te[u + 2] = t4.z * b4.z, te[u + 3] = t4.w * b4.w;
+        xe[u] = x4.x * b4.x, xe[u + 1] = x4.y * b4.y, xe[u + 2] = x4.z * b4.z, xe[u + 3] = x4.w * b4.w;
+        tops[0] = fmaxf(fmaxf(fmaxf(tops[0], fabsf(te[u])), fmaxf(fabsf(te[u + 1]), fabsf(te[u + 2]))), fabsf(te[u + 3]));
+        tops[1] = fmaxf(fmaxf(fmaxf(tops[1], fabsf(xe[u])), fmaxf(fabsf(xe[u + 1]), fabsf(xe[u + 2]))), fabsf(xe[u + 3]));
+        if (BACK) {
+            tops[2] = fmaxf(fmaxf(fmaxf(tops[2], fabsf(t4.x)), fmaxf(fabsf(t4.y), fabsf(t4.z))), fabsf(t4.w));
+            tops[3] = fmaxf(fmaxf(fmaxf(tops[3], fabsf(x4.x)), fmaxf(fabsf(x4.y), fabsf(x4.z))), fabsf(x4.w));
+        }
+    }
+    constexpr int NTOP = BACK ? 4 : 2;
+#pragma unroll
+    for (int e = 0; e < NTOP; ++e) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) tops[e] = fmaxf(tops[e], __shfl_xor_sync(0xffffffffu, tops[e], o));
+        if (lane == 0) s_top[e][warp] = tops[e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < NTOP; ++e)
+#pragma unroll
+        for (int w = 0; w < PT / 32; ++w) tops[e] = fmaxf(tops[e], s_top[e][w]);
+    RowScale ts = row_scale(tops[0]), xs = row_scale(tops[1]);
+    // (the forward's matrices carry beta: U = T beta (V - e^G K S))
+    s_sum[part][row] = image_row(img, row, part, te, ts.up);
+    image_row(img, C + row, part, xe, xs.up);
+    __syncthreads();
+    // |R| <= |v| + BND1 |S| and |U'| <= BND2 |R|, of a lane's largest values
+    auto bound2 = [&](int i, const float* f) {
+        return ((s_sum[0][i] + s_sum[1][i]) + (s_sum[2][i] + s_sum[3][i])) * f[i] * s_down[i];
+    };
+    if (tid < C) {
+        const float kd = s_down[tid], qd = s_down[C + tid], fi = d.in[tid];
+        ff[Image::KB + tid] = fi * kd;
+        ff[Image::UU + tid] = ts.down;
+        ff[Image::UW + tid] = ts.down * d.out[tid] * kd;
+        ff[Image::OQ + tid] = scale * fi * qd;
+        ff[Image::OX + tid] = scale * xs.down;
+    } else if (warp == 2) {
+        put_scalars(ff, d.all, fmaxf(s_norm[lane], s_norm[lane + 32]) * sqrtf((float)ND),
+                    fmaxf(bound2(lane, d.out), bound2(lane + 32, d.out)), lane);
+    }
+    write_out(image);
+    if constexpr (BACK) {
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            te[u] = sa[(16 * part + u) * LT + row];
+            xe[u] = sp[(16 * part + u) * LT + row];
+        }
+        ts = row_scale(tops[2]), xs = row_scale(tops[3]);
+        s_sum[part][row] = image_row(img, row, part, te, ts.up);
+        image_row(img, C + row, part, xe, xs.up);
+        __syncthreads();
+        if (tid < C) {
+            const float kd = s_down[tid], qd = s_down[C + tid], fi = d.in[tid];
+            ff[Image::WK + tid] = d.out[tid] * kd;
+            ff[Image::ZT + tid] = ts.down;
+            ff[Image::ZX + tid] = scale * xs.down;
+            ff[Image::RZ + tid] = -fi * d.beta[tid] * kd;
+            ff[Image::DQ + tid] = scale * fi * qd;
+        }
+        write_out(image_t);
+    }
+    if (tid == 0) bulk_wait();
     if (tid == 0 && s_gave_up) {
         tc::drain_mmas(&mb[1], kDeltaWait);
         if (status) atomicOr(status, kStatusDelta);
@@ -253,105 +393,162 @@ __global__ void __launch_bounds__(PT) delta_prep_tc(const E* __restrict__ q, con
 }
 
 // --------------------------------------------------------------- scan
-constexpr int CW = 8;                     // compute warps: two per lane quarter
-constexpr int LW = 4;                     // loader warps
-constexpr int ST = 32 * (CW + 1 + LW);    // threads (warp CW issues the MMAs)
+constexpr int PARTS = 4;       // threads that share a lane's row on the chain
+constexpr int CW = 4 * PARTS;  // chain warps
+constexpr int OW = 4;          // output warps, one per lane quarter
+constexpr int ST = 32 * (CW + OW + 4);  // then two warps that load V, the MMA warp and the bulk loader
+constexpr int EP = C / PARTS;  // tokens of a row a chain thread has
+// Registers a thread of the chain, the outputs and the rest: 4 x 88 + 88 + 40
+// = 4 x 80 + 104 + 56 = 6 x 80, what the block starts with.
+template <int ND>
+struct Regs {
+    static constexpr int CHAIN = ND == 128 ? 88 : 80, OUT = ND == 128 ? 88 : 104, REST = ND == 128 ? 40 : 56;
+};
+// The MMA warp is not the scheduler's that lane quarters 0 and 1 keep busy
+// (at headdim 64 the other two have nothing else to do).
+constexpr int WV = CW + OW, WMMA = WV + 2, WLOAD = WV + 3;
+constexpr int VT = 64;         // threads of the two warps that load V
+constexpr int NV = 3;          // chunks of V in shared memory
 
 template <int ND>
 struct ScanSmem {
-    static constexpr uint32_t KQ0 = 0, KT0 = KQ<ND>::BYTES, IMG = KT0 + KT<ND>::BYTES, V0 = IMG + Image::STRIDE;
-    static constexpr uint32_t COEF = V0 + C * 128 * 2;
-    // per-token factors: what v and the state's answer get in R, U and U'
-    // from their products, and o's two parts
-    static constexpr int VB = 0, KB = 64, UU = 128, UW = 192, OQ = 256, OX = 320, ALL = 384, DOWN = 388, FLOATS = 516;
-    static constexpr uint32_t STAGE = (COEF + 4 * FLOATS + 15) / 16 * 16;
-    static constexpr uint32_t BYTES = 2 * STAGE;
+    static constexpr uint32_t OPS = 0, IMG = (Operands<ND>::FWD + 127) / 128 * 128, STAGE = IMG + Image::STRIDE;
+    static constexpr uint32_t V0 = 2 * STAGE, VBYTES = C * 128 * 2, BYTES = V0 + NV * VBYTES;  // V on a ring of its own
 };
 
-// Tensor-memory columns: the A operands, then the accumulators.  The state's
-// update lies over K S and U, which are read before it is issued.
-constexpr uint32_t COL_S = 0, COL_R = 128, COL_W = 192, COL_KS = 256, COL_U = 320, COL_D = 256, COL_QS = 384,
-                   COL_X = 448, TMEM_COLS = 512;
+// Tensor-memory columns: the A operands (R, and U' over it once the product
+// has read R), then the accumulators S [Q; K] and R [T; X].  An MMA of 128 x 64
+// takes as long as one of 128 x 128 (52 cycles against 67 as issued here), so
+// the parts for the output ride along.  The state's update lies over S K,
+// which is read before it is issued, and the 64 columns behind.
+constexpr uint32_t COL_S = 0, COL_R = 128, COL_QS = 192, COL_KS = 256, COL_D = 256, COL_U = 384, COL_X = 448,
+                   TMEM_COLS = 512;
 
-// What the two warps of a lane quarter share: the larger of the two threads'
-// largest values of a row, through shared memory, two slots in turn.
-struct Pair {
-    float (*slots)[2 * 128];
-    uint64_t* bar;  // two arrivals a phase, one a warp
+// What the chain's threads of a row share: the largest of their values,
+// through shared memory, two slots in turn.
+struct RowTop {
+    float (*slots)[PARTS * 128];
+    uint64_t* bar;  // PARTS arrivals a phase, one a warp
     int* gave_up;
-    int half, v, n = 0;
-    __device__ __forceinline__ float larger(float mine) {
+    int part, v, n = 0;
+    __device__ __forceinline__ float of_all(float x) {
         float* at = slots[n & 1];
-        at[half * 128 + v] = mine;
+        at[part * 128 + v] = x;
         __syncwarp();
         if (v % 32 == 0) mbar_arrive(bar);
-        warp_wait(bar, n & 1, gave_up);  // (a wait that gives up leaves a wrong scale; the chunk's next wait gives up too)
+        warp_wait(bar, n & 1, gave_up);  // (a wait that gives up leaves a wrong bound; the chunk's next wait gives up too)
         ++n;
-        return fmaxf(mine, at[(half ^ 1) * 128 + v]);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) x = fmaxf(x, at[p * 128 + v]);
+        return x;
     }
 };
 
-// NE values of a lane's row (its other part is with the thread of the other
-// half) scaled, split and stored as A-operand columns at `taddr` (hi) and
-// `taddr + part` (lo); returns the inverse scale.
-template <int NE>
-__device__ __forceinline__ float store_operand(const float (&x)[NE], uint32_t taddr, uint32_t part, Pair& pair) {
-    float top = 0.f;
+template <int NP>
+__device__ __forceinline__ float top_of_pairs(const f2 (&x)[NP]) {
+    float t[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NE; i += 2) top = fmaxf(top, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
-    const RowScale s = row_scale(pair.larger(top));
-#pragma unroll
-    for (int c = 0; c < NE; c += 32) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) split2(x[c + 2 * i] * s.up, x[c + 2 * i + 1] * s.up, hi[i], lo[i]);
-        tc::tmem_st16(taddr + c / 2, hi);
-        tc::tmem_st16(taddr + part + c / 2, lo);
+    for (int i = 0; i < NP; ++i) {
+        float a, b;
+        un2(x[i], a, b);
+        t[i & 1] = fmaxf(fmaxf(t[i & 1], fabsf(a)), fabsf(b));
     }
-    tc::tmem_wait_st();
-    return s.down;
+    return fmaxf(t[0], t[1]);
 }
 
+// Eight pairs of a lane's row, already scaled, split and stored as A-operand
+// columns at `hi` and `lo`.
+__device__ __forceinline__ void store_split(const f2 (&y)[8], uint32_t hi, uint32_t lo) {
+    const f2 minus = mk2(-1.f, -1.f);
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float a, b, ra, rb;
+        un2(y[i], a, b);
+        a = __uint_as_float(__float_as_uint(a) & 0xFFFFE000u);
+        b = __uint_as_float(__float_as_uint(b) & 0xFFFFE000u);
+        h[i] = pack2(a, b);
+        un2(fma2(mk2(a, b), minus, y[i]), ra, rb);
+        l[i] = pack2(ra, rb);
+    }
+    tmem_st8(hi, h);
+    tmem_st8(lo, l);
+}
+
+// Everything of this warp before the barrier (tensor-memory accesses too) is
+// before what the barrier's waiters do.
+__device__ __forceinline__ void warp_done(uint64_t* m, int lane) {
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(m);
+}
+
+// kk MMAs over the reduced dimension: A's columns 8 apart, B's descriptor
+// `step` bytes.
+template <int KK, uint32_t STEP>
+__device__ __forceinline__ void chain(uint32_t d, uint32_t a, uint64_t bd, uint32_t id, bool first) {
+#pragma unroll
+    for (int i = 0; i < KK; ++i) mma_f16_ts(d, a + 8 * i, bd + (uint64_t)((i * STEP) >> 4), id, !(first && i == 0));
+}
+
+// Scales of the operands made on the chain.  A half has 16 bits of exponent
+// range below the point where hi and lo together lose a bit of the row's
+// largest value, so a row's scale may come from a bound on it that is loose by
+// up to 2^16.  With E the exact largest value of a lane's state column, found
+// while R [T; X] runs, and V's,
+//     |R|  <= max |v| + max_i(e^{G_i} |k_i|) sqrt(N) E
+//     |U'| <= max_i(|T_i|_1 e^{G_end - G_i}) |R|
+//     |S+| <= e^{G_end} E + 64 max |k_i U'_i|    (U' exact, found while K^T U' runs)
+// (E itself stands in for the bound that the state was stored with, in |R|) so
+// no reduction over a row waits on the chain: an exchange between the threads
+// of a row takes 290 cycles, and exact scales would want three a chunk.
+//
 // KEEP = false: outputs.  KEEP = true: the state entering each chunk and the
 // writes U for the gradients, no outputs.
 template <typename E, int ND, bool KEEP>
-__global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ q, const E* __restrict__ k,
-                                                       const E* __restrict__ v, const unsigned char* __restrict__ image,
-                                                       const float* h0, const int* __restrict__ lens, float scale,
+__global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ v, const unsigned char* __restrict__ image,
+                                                       const unsigned char* __restrict__ operands, const float* h0,
+                                                       const int* __restrict__ lens,
                                                        E* __restrict__ o, float* h_final, float* __restrict__ states,
                                                        float* __restrict__ writes, Shape sh, unsigned* status) {
     using M = ScanSmem<ND>;
-    constexpr int CB = ND / 8, NS = ND / 2;  // NS: state elements a compute thread holds
+    constexpr int NS = ND / PARTS;  // state elements a chain thread holds
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(8) uint64_t mb_full[2], mb_img[2], mb_free[2], mb_ks, mb_r, mb_u, mb_w, mb_d, mb_s, mb_pair[4],
-        mb_load, mb_drain;
-    __shared__ float s_top[2][2 * 128];
+    __shared__ __align__(8) uint64_t mb_full[2], mb_free[2], mb_ks, mb_r, mb_u, mb_w, mb_d, mb_s, mb_o, mb_read, mb_row[4],
+        mb_drain;
+    __shared__ __align__(8) uint64_t mb_vfull[NV], mb_vtop[NV], mb_vfree[NV];
+    __shared__ float s_top[2][PARTS * 128], s_sdown[2][128], s_rdown[2][128], s_vtop[NV][128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bh = blockIdx.x, b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
     const int len = row_len(lens, b, sh.T), nck = (len + C - 1) / C;
-    const int live_warps = 2 * ((P + 31) / 32);
-    if (warp == CW) {
+    const int quarters = (P + 31) / 32;
+    if (warp == WMMA) {
         tc::tmem_alloc(&s_tmem, TMEM_COLS);
         tc::tmem_relinquish();
     }
     if (tid == 0) {
         s_gave_up = 0;
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&mb_full[i], LW);
-            tc::mbar_init(&mb_img[i], 1);
-            tc::mbar_init(&mb_free[i], live_warps);
+            tc::mbar_init(&mb_full[i], 1);
+            tc::mbar_init(&mb_free[i], (PARTS + (KEEP ? 0 : 1)) * quarters);
         }
-        for (int i = 0; i < 4; ++i) tc::mbar_init(&mb_pair[i], 2);
-        tc::mbar_init(&mb_load, LW);
+        for (int i = 0; i < 4; ++i) tc::mbar_init(&mb_row[i], PARTS);
+        for (int i = 0; i < NV; ++i) {
+            tc::mbar_init(&mb_vfull[i], VT);
+            tc::mbar_init(&mb_vtop[i], quarters);
+            tc::mbar_init(&mb_vfree[i], (PARTS + 1) * quarters);
+        }
         tc::mbar_init(&mb_ks, 1);
         tc::mbar_init(&mb_u, 1);
         tc::mbar_init(&mb_d, 1);
         tc::mbar_init(&mb_drain, 1);
-        tc::mbar_init(&mb_r, live_warps);
-        tc::mbar_init(&mb_w, live_warps);
-        tc::mbar_init(&mb_s, live_warps);
+        tc::mbar_init(&mb_o, 2);
+        tc::mbar_init(&mb_read, quarters);
+        tc::mbar_init(&mb_r, PARTS * quarters);
+        tc::mbar_init(&mb_w, PARTS * quarters);
+        tc::mbar_init(&mb_s, PARTS * quarters);
         tc::mbar_fence_init();
     }
     tc::fence_before_sync();
@@ -359,225 +556,326 @@ __global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ q, 
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
 
+    if (warp < CW)
+        set_registers<Regs<ND>::CHAIN, 80>();
+    else if (warp < CW + OW)
+        set_registers<Regs<ND>::OUT, 80>();
+    else
+        fewer_registers<Regs<ND>::REST>();
+
     if (warp < CW) {
-        // ------------------------------------------------ compute warps
-        const int quarter = warp % 4, half = warp / 4, vc = 32 * quarter + lane;
+        // ------------------------------------------------ the chain
+        const int quarter = warp % 4, part = warp / 4, vc = 32 * quarter + lane;
         const bool on = vc < P;
         const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16);
-        if (32 * quarter < P) {
+        if (quarter < quarters) {
             const int64_t so = (int64_t)bh * N * P + vc;
-            const int k0 = half * NS;
-            float s[NS];
+            const int k0 = part * NS;
+            f2 s[NS / 2];
 #pragma unroll
-            for (int i = 0; i < NS; ++i) s[i] = (h0 && on && k0 + i < N) ? h0[so + (int64_t)(k0 + i) * P] : 0.f;
-            Pair pair{s_top, &mb_pair[quarter], &s_gave_up, half, vc};
-            float sdown = 1.f;
-            auto done_with = [&](uint64_t* m) {  // this warp's tensor-memory accesses before the barrier are complete
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(m);
-            };
-            auto put_state = [&](int c) {
+            for (int i = 0; i < NS / 2; ++i) {
+                const int kr = k0 + 2 * i;
+                const bool there = h0 && on && kr < N;  // (N is even)
+                s[i] = mk2(there ? h0[so + (int64_t)kr * P] : 0.f, there ? h0[so + (int64_t)(kr + 1) * P] : 0.f);
+            }
+            RowTop row{s_top, &mb_row[quarter], &s_gave_up, part, vc};
+            auto put_state = [&](int c, float bound) {
+                const RowScale sc = row_scale(bound);
+                const f2 up = mk2(sc.up, sc.up);
+#pragma unroll
+                for (int e = 0; e < NS / 2; e += 8) {
+                    f2 y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = mul2(s[e + i], up);
+                    store_split(y, tq + COL_S + k0 / 2 + e, tq + COL_S + ND / 2 + k0 / 2 + e);
+                }
+                tc::tmem_wait_st();
+                if (part == 0) s_sdown[c & 1][vc] = sc.down;
+                warp_done(&mb_s, lane);
                 if (KEEP && on) {
                     float* dst = states + ((int64_t)bh * sh.nc + c) * N * P + vc;
 #pragma unroll
-                    for (int i = 0; i < NS; ++i)
-                        if (k0 + i < N) dst[(int64_t)(k0 + i) * P] = s[i];
+                    for (int i = 0; i < NS / 2; ++i)
+                        if (k0 + 2 * i < N) {
+                            float a, e;
+                            un2(s[i], a, e);
+                            dst[(k0 + 2 * i) * P] = a;
+                            dst[(k0 + 2 * i + 1) * P] = e;
+                        }
                 }
-                sdown = store_operand<NS>(s, tq + COL_S + k0 / 2, ND / 2, pair);
-                done_with(&mb_s);
+                return sc.down;
             };
-            if (nck > 0) put_state(0);
-            for (int c = 0; c < nck; ++c) {
-                const uint32_t ph = c & 1;
-                unsigned char* stage = smem + (c & 1) * M::STAGE;
-                const float* coef = reinterpret_cast<const float*>(stage + M::COEF) + 32 * half;
-                if (!warp_wait(&mb_full[c & 1], (c >> 1) & 1, &s_gave_up)) break;
-                const float all = reinterpret_cast<const float*>(stage + M::COEF)[M::ALL];
-                const E* vt = reinterpret_cast<const E*>(stage + M::V0) + 32 * half * P + (on ? vc : 0);
-                float x[32];
+            uint32_t vraw[EP / 2];  // this thread's tokens of V, packed as they are
+            float vtop = 0.f;       // the lane's largest
+            auto read_v = [&](int c) {
+                const int slot = c % NV;
+                if (!warp_wait(&mb_vtop[slot], c / NV & 1, &s_gave_up)) return false;
+                const uint16_t* vt = reinterpret_cast<const uint16_t*>(smem + M::V0 + slot * M::VBYTES) + EP * part * P + (on ? vc : 0);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = to_f(vt[i * P]) * coef[M::VB + i];
+                for (int i = 0; i < EP / 2; ++i) vraw[i] = vt[2 * i * P] | (uint32_t)vt[(2 * i + 1) * P] << 16;
+                vtop = s_vtop[slot][vc];
+                warp_done(&mb_vfree[slot], lane);
+                return true;
+            };
+            float sdown = 1.f, sbound = 0.f;
+            bool ok = nck > 0 && read_v(0);
+            if (ok) {
+                sbound = row.of_all(top_of_pairs(s));
+                sdown = put_state(0, sbound);
+                ok = warp_wait(&mb_full[0], 0, &s_gave_up);
+            }
+            for (int c = 0; ok && c < nck; ++c) {
+                const uint32_t ph = c & 1;
+                const float* ff = reinterpret_cast<const float*>(smem + (c & 1) * M::STAGE + M::IMG + Image::F);
+                f2 x[EP / 2], f[EP / 2];
+                uint32_t raw[EP];
+                const float rbound = fmaf(ff[Image::BND1], sbound, vtop);
+                const RowScale rs = row_scale(rbound);
+                auto factors = [&](int which, float m) {
+#pragma unroll
+                    for (int i = 0; i < EP / 4; ++i) {
+                        const float4 w = *reinterpret_cast<const float4*>(ff + which + EP * part + 4 * i);
+                        f[2 * i] = mul2(mk2(w.x, w.y), mk2(m, m));
+                        f[2 * i + 1] = mul2(mk2(w.z, w.w), mk2(m, m));
+                    }
+                };
+                factors(Image::KB, -sdown * rs.up);
+#pragma unroll
+                for (int i = 0; i < EP / 2; ++i) {
+                    const float2 w = unpack2(vraw[i], E());
+                    x[i] = mul2(mk2(w.x, w.y), mk2(rs.up, rs.up));
+                }
+                if (part == 0) s_rdown[c & 1][vc] = rs.down;
                 if (!warp_wait(&mb_ks, ph, &s_gave_up)) break;
                 tc::fence_after_sync();
-                uint32_t raw[32];
-                tmem_ld32(tq + COL_KS + 32 * half, raw);
+                tc::tmem_ld16(tq + COL_KS + EP * part, raw);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = fmaf(-coef[M::KB + i] * sdown, __uint_as_float(raw[i]), x[i]);
-                const float rdown = store_operand<32>(x, tq + COL_R + 16 * half, 32, pair);
-                done_with(&mb_r);
+                for (int i = 0; i < EP / 2; ++i) x[i] = fma2(f[i], raw2(raw[2 * i], raw[2 * i + 1]), x[i]);
+                store_split(x, tq + COL_R + EP / 2 * part, tq + COL_R + 32 + EP / 2 * part);
+                tc::tmem_wait_st();
+                warp_done(&mb_r, lane);
+                // while R [T; X] runs: the exact largest value of S, the next chunk's V
+                const RowScale ws = row_scale(ff[Image::BND2] * rbound);
+                const float stop = row.of_all(top_of_pairs(s));
+                if (c + 1 < nck && !read_v(c + 1)) break;
+                factors(Image::UW, rs.down * ws.up);
                 if (!warp_wait(&mb_u, ph, &s_gave_up)) break;
                 tc::fence_after_sync();
-                tmem_ld32(tq + COL_U + 32 * half, raw);
+                tc::tmem_ld16(tq + COL_U + EP * part, raw);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]) * rdown * coef[M::UW + i];
-                const float wdown = store_operand<32>(x, tq + COL_W + 16 * half, 32, pair);
-                done_with(&mb_w);
-                if (KEEP && on) {
-                    float* dst = writes + (((int64_t)bh * sh.nc + c) * C + 32 * half) * P + vc;
+                for (int i = 0; i < EP / 2; ++i) x[i] = mul2(f[i], raw2(raw[2 * i], raw[2 * i + 1]));
+                store_split(x, tq + COL_R + EP / 2 * part, tq + COL_R + 32 + EP / 2 * part);
+                tc::tmem_wait_st();
+                warp_done(&mb_w, lane);
+                // while U' K runs: the bound on the next state (the rows of K are scaled
+                // to below 2^14, U' carries the inverse)
+                const float all = ff[Image::ALL];
+                sbound = fmaf(all, stop, row.of_all(top_of_pairs(x)) * ws.down * (64.f * 16384.f));
+                if constexpr (KEEP) {
+                    if (on) {
+                        float* dst = writes + (((int64_t)bh * sh.nc + c) * C + EP * part) * P + vc;
+                        factors(Image::UU, rs.down);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) dst[(int64_t)i * P] = __uint_as_float(raw[i]) * rdown * coef[M::UU + i];
+                        for (int i = 0; i < EP / 2; ++i) {
+                            float a, e;
+                            un2(mul2(f[i], raw2(raw[2 * i], raw[2 * i + 1])), a, e);
+                            dst[2 * i * P] = a;
+                            dst[(2 * i + 1) * P] = e;
+                        }
+                    }
                 }
                 if (!warp_wait(&mb_d, ph, &s_gave_up)) break;
                 tc::fence_after_sync();
+                {
+                    const f2 m = mk2(ws.down, ws.down), keep = mk2(all, all);
 #pragma unroll
-                for (int e = 0; e < NS; e += 32) {
-                    tmem_ld32(tq + COL_D + k0 + e, raw);
-                    tc::tmem_wait_ld();
+                    for (int e = 0; e < NS; e += 16) {
+                        tc::tmem_ld16(tq + COL_D + k0 + e, raw);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[e + i] = fmaf(all, s[e + i], __uint_as_float(raw[i]) * wdown);
+                        for (int i = 0; i < 8; ++i)
+                            s[e / 2 + i] = fma2(keep, s[e / 2 + i], mul2(raw2(raw[2 * i], raw[2 * i + 1]), m));
+                    }
                 }
-                const float qdown = sdown;
-                if (c + 1 < nck) put_state(c + 1);
-                if constexpr (!KEEP) {
-                    tmem_ld32(tq + COL_QS + 32 * half, raw);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]) * (qdown * coef[M::OQ + i]);
-                    tmem_ld32(tq + COL_X + 32 * half, raw);
-                    tc::tmem_wait_ld();
-                    const int n = min(len - c * C, C) - 32 * half;
-                    E* dst = o + (((int64_t)b * sh.T + (int64_t)c * C + 32 * half) * sh.H + h) * P + vc;
-                    const int64_t os = (int64_t)sh.H * P;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (on && i < n) dst[i * os] = from_f<E>(fmaf(__uint_as_float(raw[i]), rdown * coef[M::OX + i], x[i]));
+                warp_done(&mb_free[c & 1], lane);
+                if (c + 1 < nck) {
+                    sdown = put_state(c + 1, sbound);
+                    if (!warp_wait(&mb_full[(c + 1) & 1], ((c + 1) >> 1) & 1, &s_gave_up)) break;
                 }
-                done_with(&mb_free[c & 1]);
             }
             if (h_final && on)
 #pragma unroll
-                for (int i = 0; i < NS; ++i)
-                    if (k0 + i < N) h_final[so + (int64_t)(k0 + i) * P] = s[i];
-            if (!KEEP && on)
-                for (int t = len + half; t < sh.T; t += 2) o[(((int64_t)b * sh.T + t) * sh.H + h) * P + vc] = from_f<E>(0.f);
+                for (int i = 0; i < NS / 2; ++i)
+                    if (k0 + 2 * i < N) {
+                        float a, e;
+                        un2(s[i], a, e);
+                        h_final[so + (int64_t)(k0 + 2 * i) * P] = a;
+                        h_final[so + (int64_t)(k0 + 2 * i + 1) * P] = e;
+                    }
         }
-    } else if (warp == CW) {
-        // ------------------------------------------------ MMA issue
-        if (lane == 0) {
-            constexpr uint32_t id64 = tc::idesc_f16(128, C), idn = tc::idesc_f16(128, ND);
+    } else if (warp < CW + OW) {
+        // ------------------------------------------------ outputs
+        const int quarter = warp - CW, vc = 32 * quarter + lane;
+        const bool on = vc < P;
+        const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16);
+        // the largest |v| of a lane's column, for the chain
+        auto find_top = [&](int c) {
+            const int slot = c % NV;
+            if (!warp_wait(&mb_vfull[slot], c / NV & 1, &s_gave_up)) return false;
+            const uint16_t* vt = reinterpret_cast<const uint16_t*>(smem + M::V0 + slot * M::VBYTES) + (on ? vc : 0);
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) m = max(m, (uint32_t)(vt[i * P] & 0x7FFF));
+            s_vtop[slot][vc] = top_of<E>(m);
+            warp_done(&mb_vtop[slot], lane);
+            if (lane == 0) mbar_arrive(&mb_vfree[slot]);
+            return true;
+        };
+        if (quarter < quarters && nck > 0 && find_top(0)) {
+            constexpr int OE = ND == 128 ? 8 : 16;  // columns at a time
+            const int64_t os = (int64_t)sh.H * P;
+            E* dst = KEEP ? nullptr : o + ((int64_t)b * sh.T * sh.H + h) * P + vc;
             for (int c = 0; c < nck; ++c) {
-                const uint32_t ph = c & 1;
-                const uint32_t base = tc::smem_u32(smem) + (c & 1) * M::STAGE;
-                const uint64_t dkq = tc::make_desc(base + M::KQ0, KQ<ND>::LBO, KQ<ND>::SBO);
-                const uint64_t dkt = tc::make_desc(base + M::KT0, KT<ND>::LBO, KT<ND>::SBO);
-                const uint64_t dtx = tc::make_desc(base + M::IMG, Image::LBO, Image::SBO);
-                auto chain = [&](uint32_t d, uint32_t a, uint64_t bd, uint32_t step, int kk, uint32_t id, bool first) {
-                    for (int i = 0; i < kk; ++i) mma_f16_ts(d, a + 8 * i, bd + (uint64_t)((i * step) >> 4), id, !(first && i == 0));
-                };
-                if (!wait_or_give_up(&mb_full[c & 1], (c >> 1) & 1, &s_gave_up)) break;
-                if (!wait_or_give_up(&mb_img[c & 1], (c >> 1) & 1, &s_gave_up)) break;
-                if (!wait_or_give_up(&mb_s, ph, &s_gave_up)) break;
+                if (c + 1 < nck && !find_top(c + 1)) break;
+                if constexpr (KEEP) continue;
+                unsigned char* stage = smem + (c & 1) * M::STAGE;
+                if (!warp_wait(&mb_full[c & 1], (c >> 1) & 1, &s_gave_up)) break;
+                if (!warp_wait(&mb_o, c & 1, &s_gave_up)) break;
                 tc::fence_after_sync();
-                for (int p = 0; p < 2; ++p)
-                    chain(tmem + COL_KS, tmem + COL_S + p * (ND / 2), dkq, 2 * KQ<ND>::LBO, ND / 16, id64, p == 0);
-                tc::commit(&mb_ks);
-                if (!KEEP) {
-                    if (c > 0 && !wait_or_give_up(&mb_free[(c - 1) & 1], ((c - 1) >> 1) & 1, &s_gave_up)) break;
-                    tc::fence_after_sync();
-                    for (int p = 0; p < 2; ++p)
-                        chain(tmem + COL_QS, tmem + COL_S + p * (ND / 2), dkq + (KQ<ND>::QROWS >> 4), 2 * KQ<ND>::LBO, ND / 16,
-                              id64, p == 0);
+                const f2 sd = mk2(s_sdown[c & 1][vc], s_sdown[c & 1][vc]), rd = mk2(s_rdown[c & 1][vc], s_rdown[c & 1][vc]);
+                const float4* coef = reinterpret_cast<const float4*>(stage + M::IMG + Image::F);
+                const int n = min(len - c * C, C);
+                uint32_t y[C / 2];  // the lane's 64 outputs, so that the accumulators are free before they are stored
+#pragma unroll
+                for (int e = 0; e < C; e += OE) {
+                    uint32_t a[OE], x[OE];
+                    if constexpr (OE == 16) {
+                        tc::tmem_ld16(tq + COL_QS + e, a);
+                        tc::tmem_ld16(tq + COL_X + e, x);
+                    } else {
+                        tc::tmem_ld8(tq + COL_QS + e, a);
+                        tc::tmem_ld8(tq + COL_X + e, x);
+                    }
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < OE; i += 4) {
+                        const float4 fq = coef[(Image::OQ + e + i) / 4], fx = coef[(Image::OX + e + i) / 4];
+                        const f2 lo = fma2(raw2(a[i], a[i + 1]), mul2(mk2(fq.x, fq.y), sd),
+                                           mul2(raw2(x[i], x[i + 1]), mul2(mk2(fx.x, fx.y), rd)));
+                        const f2 hi = fma2(raw2(a[i + 2], a[i + 3]), mul2(mk2(fq.z, fq.w), sd),
+                                           mul2(raw2(x[i + 2], x[i + 3]), mul2(mk2(fx.z, fx.w), rd)));
+                        y[(e + i) / 2] = pack_as<E>(lo);
+                        y[(e + i) / 2 + 1] = pack_as<E>(hi);
+                    }
                 }
-                if (!wait_or_give_up(&mb_r, ph, &s_gave_up)) break;
-                tc::fence_after_sync();
-                auto from_r = [&](uint32_t d, uint64_t bd) {  // hi hi + lo hi + hi lo
-                    chain(d, tmem + COL_R, bd, 2 * Image::LBO, 4, id64, true);
-                    chain(d, tmem + COL_R + 32, bd, 2 * Image::LBO, 4, id64, false);
-                    chain(d, tmem + COL_R, bd + (Image::PART >> 4), 2 * Image::LBO, 4, id64, false);
-                };
-                from_r(tmem + COL_U, dtx);
-                tc::commit(&mb_u);
-                if (!KEEP) from_r(tmem + COL_X, dtx + ((8 * Image::SBO) >> 4));
-                if (!wait_or_give_up(&mb_w, ph, &s_gave_up)) break;
-                tc::fence_after_sync();
-                chain(tmem + COL_D, tmem + COL_W, dkt, 2 * KT<ND>::LBO, 4, idn, true);
-                chain(tmem + COL_D, tmem + COL_W + 32, dkt, 2 * KT<ND>::LBO, 4, idn, false);
-                tc::commit(&mb_d);
+                warp_done(&mb_read, lane);
+                warp_done(&mb_free[c & 1], lane);
+                if (on) {
+                    uint16_t* to = reinterpret_cast<uint16_t*>(dst);
+                    if (n == C) {
+#pragma unroll
+                        for (int i = 0; i < C / 2; ++i) {
+                            to[2 * i * os] = (uint16_t)y[i];
+                            to[(2 * i + 1) * os] = (uint16_t)(y[i] >> 16);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < C; ++i)
+                            if (i < n) to[i * os] = (uint16_t)(y[i / 2] >> (i & 1) * 16);
+                    }
+                }
+                dst += C * os;
             }
-            if (s_gave_up) tc::drain_mmas(&mb_drain, kDeltaWait);
         }
-    } else {
-        // ------------------------------------------------ loaders
-        const int t = tid - 32 * (CW + 1);
-        constexpr int NB = 2 * 8 * CB / 128;  // 8 x 8 blocks a thread
-        int last[2] = {-1, -1};               // parity of the last copy into each stage
+        if (!KEEP && on)  // behind the row's last token
+            for (int t = len; t < sh.T; ++t) o[(((int64_t)b * sh.T + t) * sh.H + h) * P + vc] = from_f<E>(0.f);
+    } else if (warp == WMMA) {
+        // ------------------------------------------------ MMA issue
+        constexpr uint32_t id64 = tc::idesc_f16(128, C), id128 = tc::idesc_f16(128, 2 * C), idn = tc::idesc_f16(128, ND);
         for (int c = 0; c < nck; ++c) {
-            unsigned char* stage = smem + (c & 1) * M::STAGE;
-            float* coef = reinterpret_cast<float*>(stage + M::COEF);
-            const int n = min(len - c * C, C);
-            const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C;
-            const int64_t ko = (t0 * KH + h / sh.G) * N, ks = (int64_t)KH * N;
-            const unsigned char* img = image + ((int64_t)bh * sh.nc + c) * Image::STRIDE;
-            const float* ff = reinterpret_cast<const float*>(img + Image::F);
-            uint4 raw[NB][8], vr[8];
-#pragma unroll
-            for (int e = 0; e < NB; ++e) {
-                const int id = t + 128 * e, which = id / (8 * CB), rg = id / CB % 8, cb = id % CB;
-                load_block(raw[e], (which ? q : k) + ko + 8 * cb, ks, 8 * rg, n, 8 * cb < N && !(KEEP && which));
+            const uint32_t ph = c & 1;
+            const uint32_t base = tc::smem_u32(smem) + (c & 1) * M::STAGE;
+            const uint64_t dqk = tc::make_desc(base + M::OPS, QK<ND>::LBO, QK<ND>::SBO);
+            const uint64_t dkt = tc::make_desc(base + M::OPS + Operands<ND>::KT0, KT<ND>::LBO, KT<ND>::SBO);
+            const uint64_t dtx = tc::make_desc(base + M::IMG, Image::LBO, Image::SBO);
+            if (!warp_wait(&mb_full[c & 1], (c >> 1) & 1, &s_gave_up)) break;
+            if (!KEEP && c > 0 && !warp_wait(&mb_read, (c - 1) & 1, &s_gave_up)) break;
+            if (!warp_wait(&mb_s, ph, &s_gave_up)) break;
+            tc::fence_after_sync();
+            const uint32_t d1 = tmem + (KEEP ? COL_KS : COL_QS), d2 = tmem + COL_U;
+            const uint64_t b1 = dqk + (KEEP ? QK<ND>::KROWS >> 4 : 0);
+            constexpr uint32_t id = KEEP ? id64 : id128;  // without outputs only K's and T's rows
+            chain<ND / 16, 2 * QK<ND>::LBO>(d1, tmem + COL_S, b1, id, true);  // hi, then lo
+            chain<ND / 16, 2 * QK<ND>::LBO>(d1, tmem + COL_S + ND / 2, b1, id, false);
+            commit_elected(&mb_ks);
+            if (!warp_wait(&mb_r, ph, &s_gave_up)) break;
+            tc::fence_after_sync();
+            chain<4, 2 * Image::LBO>(d2, tmem + COL_R, dtx, id, true);  // hi hi + lo hi + hi lo
+            chain<4, 2 * Image::LBO>(d2, tmem + COL_R + 32, dtx, id, false);
+            chain<4, 2 * Image::LBO>(d2, tmem + COL_R, dtx + (Image::PART >> 4), id, false);
+            commit_elected(&mb_u);
+            if (!KEEP) {
+                commit_elected(&mb_o);
+                if (lane == 0) mbar_arrive(&mb_o);  // (what the chain wrote before mb_r is before this)
             }
-            const int per = P / 8;  // 16-byte pieces of a row of V
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int id = t + 128 * e, i = id / per, p = id % per;
-                vr[e] = (e < P / 16 && i < n) ? *reinterpret_cast<const uint4*>(v + ((t0 + i) * sh.H + h) * P + 8 * p)
-                                              : make_uint4(0, 0, 0, 0);
-            }
-            float fi = 0.f, fo = 0.f, fb = 0.f, fu = 0.f, fx = 0.f;
-            if (t < C) {
-                fi = ff[Image::IN + t], fo = ff[Image::OUT + t], fb = ff[Image::BETA + t];
-                fu = ff[Image::DOWN + t], fx = ff[Image::DOWN + C + t];
-            }
-            const float fa = ff[Image::ALL];
-            if (c >= 2 && !warp_wait(&mb_free[c & 1], ((c >> 1) - 1) & 1, &s_gave_up)) break;
-            if (t == 0) {
-                tc::mbar_arrive_expect_tx(&mb_img[c & 1], Image::F);
-                tc::bulk_g2s(tc::smem_u32(stage + M::IMG), img, Image::F, &mb_img[c & 1]);
-                last[c & 1] = (c >> 1) & 1;
-            }
-#pragma unroll
-            for (int e = 0; e < NB; ++e) {
-                const int id = t + 128 * e, which = id / (8 * CB), rg = id / CB % 8, cb = id % CB;
-                uint32_t w[8][4];
-                float down[8];
-                scale_block<E, CB>(raw[e], w, down);
-                store_rows(stage + M::KQ0, KQ<ND>::LBO, KQ<ND>::SBO, 8 * which + rg, cb, w);
-                if (which == 0) store_transposed(stage + M::KT0, KT<ND>::LBO, KT<ND>::SBO, rg, cb, w);
-                if (cb == 0)
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) coef[M::DOWN + C * which + 8 * rg + r] = down[r];
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < P / 16) reinterpret_cast<uint4*>(stage + M::V0)[t + 128 * e] = vr[e];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&mb_load);
-            if (!warp_wait(&mb_load, c & 1, &s_gave_up)) break;  // the row scales of all four warps
-            if (t < C) {
-                const float kd = coef[M::DOWN + t], qd = coef[M::DOWN + C + t];
-                coef[M::VB + t] = fb;
-                coef[M::KB + t] = fb * fi * kd;
-                coef[M::UU + t] = fu;
-                coef[M::UW + t] = fu * fo * kd;
-                coef[M::OQ + t] = scale * fi * qd;
-                coef[M::OX + t] = scale * fx;
-                if (t == 0) coef[M::ALL] = fa;
-            }
-            tc::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&mb_full[c & 1]);
+            if (!warp_wait(&mb_w, ph, &s_gave_up)) break;
+            tc::fence_after_sync();
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R, dkt, idn, true);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R + 32, dkt, idn, false);
+            commit_elected(&mb_d);
         }
-        if (t == 0 && s_gave_up)  // no copy may land in shared memory that is no longer this CTA's
+        if (s_gave_up) {
+            commit_elected(&mb_drain);
+            tc::mbar_wait_bounded(&mb_drain, 0, kDeltaWait);
+        }
+    } else if (warp == WLOAD) {
+        // ------------------------------------------------ loader
+        int last[2] = {-1, -1};  // parity of the last copies into each stage
+        const unsigned char* img = image + (int64_t)bh * sh.nc * Image::STRIDE;
+        const unsigned char* ops = operands + ((int64_t)b * KH + h / sh.G) * sh.nc * Operands<ND>::stride(KEEP);
+        for (int c = 0; c < nck; ++c) {
+            const uint32_t at = tc::smem_u32(smem) + (c & 1) * M::STAGE;
+            if (c >= 2 && !warp_wait(&mb_free[c & 1], ((c >> 1) - 1) & 1, &s_gave_up)) break;
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&mb_full[c & 1], Image::BYTES + Operands<ND>::FWD);
+                tc::bulk_g2s(at + M::OPS, ops, Operands<ND>::FWD, &mb_full[c & 1]);
+                tc::bulk_g2s(at + M::IMG, img, Image::BYTES, &mb_full[c & 1]);
+                last[c & 1] = (c >> 1) & 1;
+                if (c + 2 < nck) {  // what the next copies into this stage read, into L2
+                    prefetch_l2(ops + 2 * Operands<ND>::stride(KEEP), Operands<ND>::FWD);
+                    prefetch_l2(img + 2 * Image::STRIDE, Image::BYTES);
+                }
+            }
+            ops += Operands<ND>::stride(KEEP);
+            img += Image::STRIDE;
+        }
+        __syncwarp();
+        if (lane == 0 && s_gave_up)  // no copy may land in shared memory that is no longer this CTA's
             for (int i = 0; i < 2; ++i)
-                if (last[i] >= 0) tc::mbar_wait_bounded(&mb_img[i], last[i], kDeltaWait);
+                if (last[i] >= 0) tc::mbar_wait_bounded(&mb_full[i], last[i], kDeltaWait);
+    } else {
+        // ------------------------------------------------ V (rows of P elements; zeros where no token is)
+        const int t = tid - 32 * WV, per = P / 8;
+        for (int c = 0; c < nck; ++c) {
+            const int slot = c % NV, n = min(len - c * C, C);
+            const uint32_t at = tc::smem_u32(smem) + M::V0 + slot * M::VBYTES;
+            const E* src = v + (((int64_t)b * sh.T + (int64_t)c * C) * sh.H + h) * P;
+            if (c >= NV && !warp_wait(&mb_vfree[slot], (c / NV - 1) & 1, &s_gave_up)) break;
+            for (int id = t; id < C * per; id += VT) {
+                const int i = id / per;
+                cp_async16(at + 16 * id, src + (int64_t)min(i, n - 1) * sh.H * P + 8 * (id - i * per), i < n);
+            }
+            cp_async_arrive(&mb_vfull[slot]);
+        }
+        cp_async_wait_all();
     }
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == CW) tc::tmem_dealloc(tmem, TMEM_COLS);
+    if (warp == WMMA) tc::tmem_dealloc(tmem, TMEM_COLS);
     if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusDelta);
 }
 
@@ -600,20 +898,44 @@ cudaError_t allow(uint32_t bytes) {
     return e;
 }
 
+// Workspace: the images of every chunk and value head, (the backward: those
+// for its own scan too), then the operands of every chunk and key head.
+size_t image_bytes(const DeltaArgs& a) { return (size_t)chunk_count(a) * Image::STRIDE; }
+size_t operand_bytes(const DeltaArgs& a, bool back) {
+    const uint32_t one = a.N <= 64 ? Operands<64>::stride(back) : Operands<128>::stride(back);
+    return (size_t)(chunk_count(a) / a.H * a.KH) * one;
+}
+
+template <typename E, int ND, bool BACK>
+cudaError_t prep_tc(const DeltaArgs& a, unsigned char* image, unsigned char* image_t, unsigned char* operands,
+                    cudaStream_t st) {
+    using M = PrepSmem<ND, BACK>;
+    const cudaError_t e = allow<delta_prep_tc<E, ND, BACK>>(M::BYTES);
+    if (e != cudaSuccess) return e;
+    delta_prep_tc<E, ND, BACK><<<(unsigned)chunk_count(a), PT, M::BYTES, st>>>(
+        static_cast<const E*>(a.q), static_cast<const E*>(a.k), a.g, a.beta, a.lens, image, image_t, operands, a.scale,
+        shape(a), status_word());
+    return cudaGetLastError();
+}
+
+template <typename E, int ND, bool KEEP>
+cudaError_t scan_tc(const DeltaArgs& a, const unsigned char* image, const unsigned char* operands, float* states,
+                    float* writes, cudaStream_t st) {
+    using M = ScanSmem<ND>;
+    const cudaError_t e = allow<delta_scan_tc<E, ND, KEEP>>(M::BYTES);
+    if (e != cudaSuccess) return e;
+    delta_scan_tc<E, ND, KEEP><<<(unsigned)(a.Bz * a.H), ST, M::BYTES, st>>>(
+        static_cast<const E*>(a.v), image, operands, a.h0, a.lens, KEEP ? nullptr : static_cast<E*>(a.o),
+        KEEP ? nullptr : a.h_final, states, writes, shape(a), status_word());
+    return cudaGetLastError();
+}
+
 template <typename E, int ND>
 cudaError_t forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     unsigned char* image = static_cast<unsigned char*>(ws);
-    unsigned* status = status_word();
-    cudaError_t e = allow<delta_prep_tc<E, ND>>(PrepSmem<ND>::BYTES);
-    if (e != cudaSuccess) return e;
-    delta_prep_tc<E, ND><<<(unsigned)chunk_count(a), PT, PrepSmem<ND>::BYTES, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), a.g, a.beta, a.lens, image, shape(a), status);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = allow<delta_scan_tc<E, ND, false>>(ScanSmem<ND>::BYTES)) != cudaSuccess) return e;
-    delta_scan_tc<E, ND, false><<<(unsigned)(a.Bz * a.H), ST, ScanSmem<ND>::BYTES, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), image, a.h0, a.lens, a.scale,
-        static_cast<E*>(a.o), a.h_final, nullptr, nullptr, shape(a), status);
-    return cudaGetLastError();
+    unsigned char* operands = image + image_bytes(a);
+    const cudaError_t e = prep_tc<E, ND, false>(a, image, nullptr, operands, st);
+    return e != cudaSuccess ? e : scan_tc<E, ND, false>(a, image, operands, nullptr, nullptr, st);
 }
 
 template <typename E>
@@ -623,7 +945,7 @@ cudaError_t forward_by_width(const DeltaArgs& a, void* ws, cudaStream_t st) {
 
 }  // namespace
 
-size_t tc_workspace_bytes(const DeltaArgs& a) { return (size_t)chunk_count(a) * Image::STRIDE; }
+size_t tc_workspace_bytes(const DeltaArgs& a) { return image_bytes(a) + operand_bytes(a, false); }
 cudaError_t launch_forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     return a.dtype == CSSD_BF16 ? forward_by_width<__nv_bfloat16>(a, ws, st) : forward_by_width<__half>(a, ws, st);
 }

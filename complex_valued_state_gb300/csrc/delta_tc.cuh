@@ -64,15 +64,55 @@ __device__ __forceinline__ float top_of(uint32_t m) {
     return f.x != f.x || f.y != f.y ? __uint_as_float(0x7F800000u) : fmaxf(f.x, f.y);
 }
 
-// D[tmem] (+)= A[tmem] B[smem]^T, half operands, issued by one thread.  Row m
-// of A is lane m; K elements 2c and 2c + 1 are the halves of column c.
+// D[tmem] (+)= A[tmem] B[smem]^T, half operands.  Row m of A is lane m; K
+// elements 2c and 2c + 1 are the halves of column c.  Called by a converged
+// warp, one elected lane issuing, so that the operands stay warp-uniform (58
+// cycles an MMA when a single diverged lane issued them, against 34 the pipe
+// needs at N = 64).
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
         "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
         : "memory");
 }
+// The elected lane's commit (the same lane: election picks one lane of a mask).
+__device__ __forceinline__ void commit_elected(uint64_t* m) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(tc::smem_u32(m))
+        : "memory");
+}
+
+// Two fp32 operations an instruction.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 mk2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void un2(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 raw2(uint32_t a, uint32_t b) { return mk2(__uint_as_float(a), __uint_as_float(b)); }
+
+// Register shares of the warpgroups (multiples of 8; together at most what
+// the block was launched with).
+template <int R>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // 32 TMEM lanes (this warp's quarter) x 32 consecutive 32-bit columns.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -85,6 +125,55 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
+}
+
+// 16 bytes into shared memory, or zeros where there is nothing to read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16u : 0u) : "memory");
+}
+// An arrival (counted in the barrier's expected ones) once this thread's
+// copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* m) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(m)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) from
+// this CTA's shared memory, in the thread's current bulk group.
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+// `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Until shared memory of the thread's bulk groups may be written again / until they are complete.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+template <int R, int FROM>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (R > FROM) more_registers<R>();
+    if constexpr (R < FROM) fewer_registers<R>();
+}
+// A pair rounded to 16-bit values, element 0 in the low half.
+template <typename E>
+__device__ __forceinline__ uint32_t pack_as(f2 v) {
+    float a, b;
+    uint32_t r;
+    un2(v, a, b);
+    if constexpr (sizeof(E) == 2 && !__is_same(E, __half))
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Registers into 32 TMEM lanes x 8 consecutive columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* m) {
@@ -113,16 +202,42 @@ __device__ __forceinline__ bool warp_wait(uint64_t* m, uint32_t parity, volatile
     return __all_sync(0xffffffffu, wait_or_give_up(m, parity, gave_up));
 }
 
-// The image a chunk's prep leaves in the workspace, copied whole into shared
-// memory by the scans: [T; X] as a B operand of 128 rows (T's 64, then X's)
-// by 64, hi then lo, and the chunk's factors.
+// What a chunk's prep leaves in the workspace, copied whole into shared memory
+// by the scans.  Per value head an image: [T; X] (the backward scan: [T^T;
+// X^T]) as a B operand of 128 rows (T's 64, then X's) by 64, hi then lo, and
+// the per-token factors the scan multiplies by.  Per key head the operands of
+// K and Q, below.
 struct Image {
     static constexpr uint32_t SBO = 128, LBO = 16 * 128;  // row groups, column groups of 8
-    static constexpr uint32_t PART = 8 * LBO;              // one part's bytes (16 KB)
+    static constexpr uint32_t PART = 8 * LBO;              // one part's bytes
     static constexpr uint32_t F = 2 * PART;                // floats from here
-    static constexpr int DOWN = 0, IN = 128, OUT = 192, BETA = 256, ALL = 320, FLOATS = 324;
+    // Forward (T and X times beta): of the state's answer in R, of the products
+    // in U and in U', of the two parts of o.
+    static constexpr int KB = 0, UU = 64, UW = 128, OQ = 192, OX = 256;
+    // Backward: of K dS in the first operand, of the two products in Z, of Z
+    // in the second operand, of dO in the third.
+    static constexpr int WK = 0, ZT = 64, ZX = 128, RZ = 192, DQ = 256;
+    // exp(G_end); and what bounds the scan's operands (see delta_scan_tc).
+    static constexpr int ALL = 320, BND1 = 321, BND2 = 322, FLOATS = 324;
     static constexpr uint32_t BYTES = F + 4 * FLOATS;
     static constexpr uint32_t STRIDE = (BYTES + 255) / 256 * 256;
+};
+// [Q; K]: rows i (64 of Q, 64 of K) by ND.
+template <int ND>
+struct QK {
+    static constexpr uint32_t SBO = 128, LBO = 16 * 128, BYTES = (ND / 8) * LBO;
+    static constexpr uint32_t KROWS = 8 * SBO;  // bytes from Q's rows to K's
+};
+// K^T (the backward scan: Q^T behind it): rows k (ND) by 64 tokens.
+template <int ND>
+struct KT {
+    static constexpr uint32_t SBO = 128, LBO = (ND / 8) * SBO, BYTES = 8 * LBO;
+};
+template <int ND>
+struct Operands {
+    static constexpr uint32_t KT0 = QK<ND>::BYTES, QT0 = KT0 + KT<ND>::BYTES;
+    static constexpr uint32_t FWD = QT0, BWD = QT0 + KT<ND>::BYTES;  // bytes of each direction
+    static constexpr uint32_t stride(bool back) { return ((back ? BWD : FWD) + 255) / 256 * 256; }
 };
 
 }  // namespace delta
