@@ -199,6 +199,12 @@ namespace delta {
 // The tensor-core kernels (delta_tc.cu), 16-bit types.
 size_t tc_workspace_bytes(const DeltaArgs& a);
 cudaError_t launch_forward_tc(const DeltaArgs& a, void* workspace, cudaStream_t stream);
+// The backward's two scans: per chunk the state entering it, the gradient of
+// the state leaving it (fp32 [N][P] each), its writes U and Z (fp32 [64][P]);
+// gh0 is written.  `workspace` holds tc_back_bytes.
+size_t tc_back_bytes(const DeltaArgs& a);
+cudaError_t launch_back_scans_tc(const DeltaArgs& a, void* workspace, float* states, float* after, float* writes,
+                                 float* zs, cudaStream_t stream);
 }  // namespace delta
 
 struct DeltaStepArgs {

@@ -279,13 +279,13 @@ __global__ void __launch_bounds__(NT) delta_scan(const E* __restrict__ q, const 
 
 // --------------------------------------------------------------- backward scan
 // The same walk from the last chunk: the gradient of the state leaving each
-// chunk is kept in `after`, Z in `zs`, and dV is written.
+// chunk is kept in `after`, Z in `zs`.
 template <typename E>
 __global__ void __launch_bounds__(NT) delta_back_scan(const E* __restrict__ q, const E* __restrict__ k,
                                                       const E* __restrict__ dout, const float* __restrict__ g,
                                                       const float* __restrict__ beta, const float* __restrict__ tx,
                                                       const float* dh, const int* __restrict__ lens, float scale,
-                                                      E* __restrict__ gv, float* gh0, float* __restrict__ after,
+                                                      float* gh0, float* __restrict__ after,
                                                       float* __restrict__ zs, Geo ge) {
     extern __shared__ __align__(16) float sm[];
     __shared__ Decays d;
@@ -344,7 +344,6 @@ __global__ void __launch_bounds__(NT) delta_back_scan(const E* __restrict__ q, c
                 r[i * LS + c0 + y] *= d.in[i];
                 if (p0 + c0 + y >= P) continue;
                 zs[ci * C * P + (int64_t)i * P + p0 + c0 + y] = z[x][y];
-                if (i < n) gv[((t0 + i) * ge.H + h) * P + p0 + c0 + y] = from_f<E>(gvv);
             }
         }
         __syncthreads();
@@ -366,12 +365,9 @@ __global__ void __launch_bounds__(NT) delta_back_scan(const E* __restrict__ q, c
     if (gh0)
         for (int e = tid; e < N * PW; e += NT)
             if (p0 + e % PW < P) gh0[so + (int64_t)(e / PW) * P + p0 + e % PW] = s[(e / PW) * LS + e % PW];
-    for (int64_t e = tid; e < (int64_t)(ge.T - len) * PW; e += NT)
-        if (p0 + (int)(e % PW) < P)
-            gv[(((int64_t)b * ge.T + len + e / PW) * ge.H + h) * P + p0 + e % PW] = from_f<E>(0.f);
 }
 
-// --------------------------------------------------------------- dQ, dK, dg, dbeta
+// --------------------------------------------------------------- dQ, dK, dV, dg, dbeta
 // One CTA per chunk and value head.  gq and gk are the key heads' gradients
 // when every value head has its own key head, else this value head's part in
 // fp32, summed over the group by delta_sum_heads in a fixed order.
@@ -382,7 +378,8 @@ __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const 
                                                  const int* __restrict__ lens, float scale,
                                                  const float* __restrict__ states, const float* __restrict__ after,
                                                  const float* __restrict__ writes, const float* __restrict__ zs,
-                                                 O* __restrict__ gq, O* __restrict__ gk, float* __restrict__ gg,
+                                                 O* __restrict__ gq, O* __restrict__ gk, E* __restrict__ gv,
+                                                 float* __restrict__ gg,
                                                  float* __restrict__ gbeta, Geo ge) {
     extern __shared__ __align__(16) float sm[];
     __shared__ Decays d;
@@ -400,6 +397,7 @@ __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const 
             gq[go + (from + e / N) * gs + e % N] = from_f<O>(0.f);
             gk[go + (from + e / N) * gs + e % N] = from_f<O>(0.f);
         }
+        for (int e = tid; e < (here - from) * P; e += NT) gv[vo + (from + e / P) * vs + e % P] = from_f<E>(0.f);
         for (int i = from + tid; i < here; i += NT) gg[(t0 + i) * ge.H + h] = gbeta[(t0 + i) * ge.H + h] = 0.f;
     }
     if (n <= 0) return;
@@ -419,6 +417,7 @@ __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const 
     load_rows(sq, LK, q + ko, ks, C, N, n, tid);
     if (tid < 32) chunk_decays(d, g + t0 * ge.H + h, beta + t0 * ge.H + h, ge.H, n, tid);
     __syncthreads();
+    for (int e = tid; e < n * P; e += NT) gv[vo + (e / P) * vs + e % P] = from_f<E>(d.beta[e / P] * sz[(e / P) * LP + e % P]);
     {
         const int i = tid / 4, l = tid % 4;  // z.v
         float zv = 0.f;
@@ -621,30 +620,17 @@ cudaError_t grad(const DeltaArgs& a, const float* states, const float* after, co
     delta_grad<E, O><<<(unsigned)(a.Bz * a.H * chunks(a)), NT, sm, st>>>(
         static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), a.g, a.beta,
         static_cast<const E*>(a.dout), a.lens, a.scale, states, after, writes, zs, static_cast<O*>(gq),
-        static_cast<O*>(gk), a.gg, a.gbeta, geo(a));
+        static_cast<O*>(gk), static_cast<E*>(a.gv), a.gg, a.gbeta, geo(a));
     return cudaGetLastError();
 }
 
+// The gradient kernel, and the sum over the value heads of a shared key head.
 template <typename E>
-cudaError_t backward(const DeltaArgs& a, void* ws, cudaStream_t st) {
-    float* tx = static_cast<float*>(ws);
-    float* states = tx + tx_floats(a);
-    float* after = states + state_floats(a);
-    float* writes = after + state_floats(a);
-    float* zs = writes + write_floats(a);
-    float* pq = zs + write_floats(a);
-    float* pk = pq + part_floats(a);
-    cudaError_t e = prep<E>(a, tx, st);
-    if (e == cudaSuccess) e = scan<E>(a, tx, nullptr, nullptr, states, writes, st);
-    if (e != cudaSuccess) return e;
-    const size_t sm = scan_smem(a);
-    if ((e = allow_smem(delta_back_scan<E>, sm)) != cudaSuccess) return e;
-    delta_back_scan<E><<<(unsigned)((a.P + PW - 1) / PW * a.Bz * a.H), NT, sm, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.dout), a.g, a.beta, tx, a.dh_final,
-        a.lens, a.scale, static_cast<E*>(a.gv), a.gh0, after, zs, geo(a));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+cudaError_t grads(const DeltaArgs& a, const float* states, const float* after, const float* writes, const float* zs,
+                  float* pq, float* pk, cudaStream_t st) {
     if (a.H == a.KH) return grad<E, E>(a, states, after, writes, zs, a.gq, a.gk, st);
-    if ((e = grad<E, float>(a, states, after, writes, zs, pq, pk, st)) != cudaSuccess) return e;
+    const cudaError_t e = grad<E, float>(a, states, after, writes, zs, pq, pk, st);
+    if (e != cudaSuccess) return e;
     const int64_t n4 = a.Bz * a.T * a.KH * (a.N / 4);
     const unsigned grid = (unsigned)((n4 + 255) / 256 < 65535 ? (n4 + 255) / 256 : 65535);
     delta_sum_heads<E><<<grid, 256, 0, st>>>(reinterpret_cast<const float4*>(pq), static_cast<E*>(a.gq), n4,
@@ -654,6 +640,32 @@ cudaError_t backward(const DeltaArgs& a, void* ws, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <typename E>
+cudaError_t backward(const DeltaArgs& a, void* ws, cudaStream_t st) {
+    float* states = static_cast<float*>(ws);
+    float* after = states + state_floats(a);
+    float* writes = after + state_floats(a);
+    float* zs = writes + write_floats(a);
+    float* pq = zs + write_floats(a);
+    float* pk = pq + part_floats(a);
+    float* tx = pk + part_floats(a);
+    if constexpr (sizeof(E) == 2) {
+        const cudaError_t e = launch_back_scans_tc(a, tx, states, after, writes, zs, st);
+        return e != cudaSuccess ? e : grads<E>(a, states, after, writes, zs, pq, pk, st);
+    } else {
+        cudaError_t e = prep<E>(a, tx, st);
+        if (e == cudaSuccess) e = scan<E>(a, tx, nullptr, nullptr, states, writes, st);
+        if (e != cudaSuccess) return e;
+        const size_t sm = scan_smem(a);
+        if ((e = allow_smem(delta_back_scan<E>, sm)) != cudaSuccess) return e;
+        delta_back_scan<E><<<(unsigned)((a.P + PW - 1) / PW * a.Bz * a.H), NT, sm, st>>>(
+            static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.dout), a.g, a.beta, tx,
+            a.dh_final, a.lens, a.scale, a.gh0, after, zs, geo(a));
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        return grads<E>(a, states, after, writes, zs, pq, pk, st);
+    }
+}
+
 }  // namespace
 }  // namespace delta
 
@@ -661,8 +673,8 @@ size_t delta_workspace_bytes(const DeltaArgs& a) {
     return a.dtype == CSSD_F32 ? sizeof(float) * delta::tx_floats(a) : delta::tc_workspace_bytes(a);
 }
 size_t delta_backward_workspace_bytes(const DeltaArgs& a) {
-    return sizeof(float) * (delta::tx_floats(a) + 2 * delta::state_floats(a) + 2 * delta::write_floats(a) +
-                            2 * delta::part_floats(a));
+    return sizeof(float) * (2 * delta::state_floats(a) + 2 * delta::write_floats(a) + 2 * delta::part_floats(a)) +
+           (a.dtype == CSSD_F32 ? sizeof(float) * delta::tx_floats(a) : delta::tc_back_bytes(a));
 }
 
 cudaError_t launch_delta_forward(const DeltaArgs& a, void* ws, cudaStream_t st) {

@@ -118,17 +118,18 @@ __device__ __forceinline__ float image_row(unsigned char* img, int row, int part
 }
 
 // One warp: the chunk's decay and the larger of its lanes' bounds.
-__device__ __forceinline__ void put_scalars(float* ff, float all, float b1, float b2, int lane) {
+__device__ __forceinline__ void put_scalars(float* ff, float all, float b1, float b2, float b3, int lane) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
         b2 = fmaxf(b2, __shfl_xor_sync(0xffffffffu, b2, o));
+        b3 = fmaxf(b3, __shfl_xor_sync(0xffffffffu, b3, o));
     }
     if (lane == 0) {
         ff[Image::ALL] = all;
         ff[Image::BND1] = b1;
         ff[Image::BND2] = b2;
-        ff[Image::FLOATS - 1] = 0.f;
+        ff[Image::BND3] = b3;
     }
 }
 
@@ -145,7 +146,8 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(16) Decays d;
     __shared__ __align__(16) float s_down[2 * C];  // inverse scales of K's and Q's rows
-    __shared__ float s_sum[4][C], s_norm[C];      // parts of sums over T's rows (columns); beta e^G |k|
+    __shared__ float s_sum[4][C], s_sumx[4][C];   // parts of sums over T's and X's rows (columns)
+    __shared__ float s_norm[C];                   // |k|
     __shared__ float s_top[4][PT / 32];
     __shared__ __align__(16) float s_f[4][C];  // exp(G_a - G_j) s_down[j], a the starts of the 16-token blocks
     __shared__ float s_e[C];                   // exp(G_i - G_a), a the start of i's block
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
     }
     __syncthreads();
     if (tid == 0 && owner) {
-        bulk_s2g(operands + (((int64_t)b * KH + h / sh.G) * sh.nc + c) * O::stride(BACK), tc::smem_u32(smem), M::OPS);
+        bulk_s2g(operands + (((int64_t)b * KH + h / sh.G) * sh.nc + c) * M::OPS, tc::smem_u32(smem), M::OPS);
         bulk_commit();
     }
     {  // lane i of tensor memory: row i of Q (the first 64), of K; columns j in halves
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
             float diag = 0.f;
 #pragma unroll
             for (int j = 0; j < 32; ++j) diag = j0 + j == i ? __uint_as_float(v[j]) : diag;
-            s_norm[i] = sqrtf(diag) * s_down[i] * d.in[i];
+            s_norm[i] = sqrtf(diag) * s_down[i];
         }
         if (above) {
 #pragma unroll
@@ -358,8 +360,8 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
         ff[Image::OQ + tid] = scale * fi * qd;
         ff[Image::OX + tid] = scale * xs.down;
     } else if (warp == 2) {
-        put_scalars(ff, d.all, fmaxf(s_norm[lane], s_norm[lane + 32]) * sqrtf((float)ND),
-                    fmaxf(bound2(lane, d.out), bound2(lane + 32, d.out)), lane);
+        put_scalars(ff, d.all, fmaxf(s_norm[lane] * d.in[lane], s_norm[lane + 32] * d.in[lane + 32]) * sqrtf((float)ND),
+                    fmaxf(bound2(lane, d.out), bound2(lane + 32, d.out)), 0.f, lane);
     }
     write_out(image);
     if constexpr (BACK) {
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
         }
         ts = row_scale(tops[2]), xs = row_scale(tops[3]);
         s_sum[part][row] = image_row(img, row, part, te, ts.up);
-        image_row(img, C + row, part, xe, xs.up);
+        s_sumx[part][row] = image_row(img, C + row, part, xe, xs.up);
         __syncthreads();
         if (tid < C) {
             const float kd = s_down[tid], qd = s_down[C + tid], fi = d.in[tid];
@@ -380,6 +382,18 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
             ff[Image::ZX + tid] = scale * xs.down;
             ff[Image::RZ + tid] = -fi * d.beta[tid] * kd;
             ff[Image::DQ + tid] = scale * fi * qd;
+        } else if (warp == 2) {
+            // |W| <= BND1 |dS|, the second operand <= BND2 |W| + BND3 |dO|, of a lane's largest values
+            float b1 = 0.f, b2 = 0.f, b3 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = lane + 32 * e;
+                const float f = d.in[i] * fabsf(d.beta[i]) * s_down[i];
+                b1 = fmaxf(b1, s_norm[i] * d.out[i]);
+                b2 = fmaxf(b2, f * ((s_sum[0][i] + s_sum[1][i]) + (s_sum[2][i] + s_sum[3][i])));
+                b3 = fmaxf(b3, f * fabsf(scale) * ((s_sumx[0][i] + s_sumx[1][i]) + (s_sumx[2][i] + s_sumx[3][i])));
+            }
+            put_scalars(ff, d.all, b1 * sqrtf((float)ND), b2, b3, lane);
         }
         write_out(image_t);
     }
@@ -834,21 +848,22 @@ __global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ v, 
         // ------------------------------------------------ loader
         int last[2] = {-1, -1};  // parity of the last copies into each stage
         const unsigned char* img = image + (int64_t)bh * sh.nc * Image::STRIDE;
-        const unsigned char* ops = operands + ((int64_t)b * KH + h / sh.G) * sh.nc * Operands<ND>::stride(KEEP);
+        const unsigned char* ops = operands + ((int64_t)b * KH + h / sh.G) * sh.nc * (KEEP ? Operands<ND>::BWD : Operands<ND>::FWD);
         for (int c = 0; c < nck; ++c) {
             const uint32_t at = tc::smem_u32(smem) + (c & 1) * M::STAGE;
             if (c >= 2 && !warp_wait(&mb_free[c & 1], ((c >> 1) - 1) & 1, &s_gave_up)) break;
             if (lane == 0) {
-                tc::mbar_arrive_expect_tx(&mb_full[c & 1], Image::BYTES + Operands<ND>::FWD);
-                tc::bulk_g2s(at + M::OPS, ops, Operands<ND>::FWD, &mb_full[c & 1]);
+                constexpr uint32_t from = KEEP ? QK<ND>::KROWS : 0, bytes = Operands<ND>::FWD - from;
+                tc::mbar_arrive_expect_tx(&mb_full[c & 1], Image::BYTES + bytes);
+                tc::bulk_g2s(at + M::OPS + from, ops + from, bytes, &mb_full[c & 1]);
                 tc::bulk_g2s(at + M::IMG, img, Image::BYTES, &mb_full[c & 1]);
                 last[c & 1] = (c >> 1) & 1;
                 if (c + 2 < nck) {  // what the next copies into this stage read, into L2
-                    prefetch_l2(ops + 2 * Operands<ND>::stride(KEEP), Operands<ND>::FWD);
+                    prefetch_l2(ops + 2 * (KEEP ? Operands<ND>::BWD : Operands<ND>::FWD) + from, bytes);
                     prefetch_l2(img + 2 * Image::STRIDE, Image::BYTES);
                 }
             }
-            ops += Operands<ND>::stride(KEEP);
+            ops += (KEEP ? Operands<ND>::BWD : Operands<ND>::FWD);
             img += Image::STRIDE;
         }
         __syncwarp();
@@ -863,6 +878,389 @@ __global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ v, 
             const uint32_t at = tc::smem_u32(smem) + M::V0 + slot * M::VBYTES;
             const E* src = v + (((int64_t)b * sh.T + (int64_t)c * C) * sh.H + h) * P;
             if (c >= NV && !warp_wait(&mb_vfree[slot], (c / NV - 1) & 1, &s_gave_up)) break;
+            for (int id = t; id < C * per; id += VT) {
+                const int i = id / per;
+                cp_async16(at + 16 * id, src + (int64_t)min(i, n - 1) * sh.H * P + 8 * (id - i * per), i < n);
+            }
+            cp_async_arrive(&mb_vfull[slot]);
+        }
+        cp_async_wait_all();
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == WMMA) tc::tmem_dealloc(tmem, TMEM_COLS);
+    if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusDelta);
+}
+
+// --------------------------------------------------------------- backward scan
+// The same walk from the last chunk, with dS in the state's place:
+//     W^T  = (e^{G_end - G} K dS)^T           A = dS^T, B = K
+//     Z^T  = W^T T + scale dO^T X             A = W^T, B = T^T;  A = dO^T, B = X^T
+//     dS^T = e^{G_end} dS^T - (e^G beta Z)^T K + scale (e^G dO)^T Q
+// The products of dO (exact in half with its row's scale in the first, split
+// in the second) do not wait for the chain; four warps make their operands.
+// The gradient of the state leaving each chunk is kept in `after`, Z in `zs`.
+template <int ND>
+struct BackSmem {
+    static constexpr uint32_t K0 = 0, KT0 = QK<ND>::KROWS, QT0 = KT0 + KT<ND>::BYTES, OPS = QT0 + KT<ND>::BYTES;
+    static constexpr uint32_t IMG = OPS, STAGE = IMG + Image::STRIDE;
+    static constexpr uint32_t V0 = 2 * STAGE, VBYTES = C * 128 * 2, BYTES = V0 + NV * VBYTES;  // dO on a ring of its own
+};
+// Tensor-memory columns.  The state's update lies over K dS and T W, dO's part
+// of it over dO X and dO's first operand: all read before it is issued.
+namespace back {
+constexpr uint32_t COL_S = 0, COL_R = 128, COL_DQ = 192, COL_KS = 256, COL_Z1 = 320, COL_D = 256, COL_Z2 = 384,
+                   COL_DX = 448, COL_E = 384;
+}
+
+template <typename E, int ND>
+__global__ void __launch_bounds__(ST, 1) delta_back_scan_tc(const E* __restrict__ dout,
+                                                            const unsigned char* __restrict__ image,
+                                                            const unsigned char* __restrict__ operands, const float* dh,
+                                                            const int* __restrict__ lens, float* gh0,
+                                                            float* __restrict__ after, float* __restrict__ zs, Shape sh,
+                                                            unsigned* status) {
+    using M = BackSmem<ND>;
+    using namespace back;
+    constexpr uint32_t COL_S = back::COL_S, COL_R = back::COL_R, COL_KS = back::COL_KS, COL_D = back::COL_D;
+    constexpr int NS = ND / PARTS;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(8) uint64_t mb_full[2], mb_free[2], mb_ks, mb_r, mb_z, mb_w, mb_d, mb_s, mb_dx, mb_dq, mb_row[4],
+        mb_drain;
+    __shared__ __align__(8) uint64_t mb_vfull[NV], mb_vfree[NV];
+    __shared__ float s_top[2][PARTS * 128], s_dxdown[128], s_dqdown[128], s_dxtop[128], s_dqtop[128];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_gave_up;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int bh = blockIdx.x, b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
+    const int len = row_len(lens, b, sh.T), nck = (len + C - 1) / C;
+    const int quarters = (P + 31) / 32;
+    if (warp == WMMA) {
+        tc::tmem_alloc(&s_tmem, TMEM_COLS);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        s_gave_up = 0;
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&mb_full[i], 1);
+            tc::mbar_init(&mb_free[i], (PARTS + 1) * quarters);
+        }
+        for (int i = 0; i < 4; ++i) tc::mbar_init(&mb_row[i], PARTS);
+        for (int i = 0; i < NV; ++i) {
+            tc::mbar_init(&mb_vfull[i], VT);
+            tc::mbar_init(&mb_vfree[i], quarters);
+        }
+        tc::mbar_init(&mb_ks, 1);
+        tc::mbar_init(&mb_z, 2);
+        tc::mbar_init(&mb_d, 2);
+        tc::mbar_init(&mb_drain, 1);
+        tc::mbar_init(&mb_dx, quarters);
+        tc::mbar_init(&mb_dq, quarters);
+        tc::mbar_init(&mb_r, PARTS * quarters);
+        tc::mbar_init(&mb_w, PARTS * quarters);
+        tc::mbar_init(&mb_s, PARTS * quarters);
+        tc::mbar_fence_init();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+
+    if (warp < CW)
+        set_registers<Regs<ND>::CHAIN, 80>();
+    else if (warp < CW + OW)
+        set_registers<Regs<ND>::OUT, 80>();
+    else
+        fewer_registers<Regs<ND>::REST>();
+
+    if (warp < CW) {
+        // ------------------------------------------------ the chain
+        const int quarter = warp % 4, part = warp / 4, vc = 32 * quarter + lane;
+        const bool on = vc < P;
+        const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16);
+        if (quarter < quarters) {
+            const int64_t so = (int64_t)bh * N * P + vc;
+            const int k0 = part * NS;
+            f2 s[NS / 2];
+#pragma unroll
+            for (int i = 0; i < NS / 2; ++i) {
+                const int kr = k0 + 2 * i;
+                const bool there = dh && on && kr < N;  // (N is even)
+                s[i] = mk2(there ? dh[so + (int64_t)kr * P] : 0.f, there ? dh[so + (int64_t)(kr + 1) * P] : 0.f);
+            }
+            RowTop row{s_top, &mb_row[quarter], &s_gave_up, part, vc};
+            auto put_state = [&](int c, float bound) {
+                const RowScale sc = row_scale(bound);
+                const f2 up = mk2(sc.up, sc.up);
+#pragma unroll
+                for (int e = 0; e < NS / 2; e += 8) {
+                    f2 y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = mul2(s[e + i], up);
+                    store_split(y, tq + COL_S + k0 / 2 + e, tq + COL_S + ND / 2 + k0 / 2 + e);
+                }
+                tc::tmem_wait_st();
+                warp_done(&mb_s, lane);
+                if (on) {
+                    float* dst = after + ((int64_t)bh * sh.nc + c) * N * P + vc;
+#pragma unroll
+                    for (int i = 0; i < NS / 2; ++i)
+                        if (k0 + 2 * i < N) {
+                            float a, e;
+                            un2(s[i], a, e);
+                            dst[(k0 + 2 * i) * P] = a;
+                            dst[(k0 + 2 * i + 1) * P] = e;
+                        }
+                }
+                return sc.down;
+            };
+            float sdown = 1.f, sbound = 0.f;
+            bool ok = nck > 0;
+            if (ok) {
+                sbound = row.of_all(top_of_pairs(s));
+                sdown = put_state(nck - 1, sbound);
+                ok = warp_wait(&mb_full[0], 0, &s_gave_up);
+            }
+            for (int j = 0; ok && j < nck; ++j) {
+                const int c = nck - 1 - j;
+                const uint32_t ph = j & 1;
+                const float* ff = reinterpret_cast<const float*>(smem + (j & 1) * M::STAGE + M::IMG + Image::F);
+                f2 x[EP / 2], f[EP / 2];
+                uint32_t raw[EP];
+                auto factors = [&](int which, float m) {
+#pragma unroll
+                    for (int i = 0; i < EP / 4; ++i) {
+                        const float4 w = *reinterpret_cast<const float4*>(ff + which + EP * part + 4 * i);
+                        f[2 * i] = mul2(mk2(w.x, w.y), mk2(m, m));
+                        f[2 * i + 1] = mul2(mk2(w.z, w.w), mk2(m, m));
+                    }
+                };
+                const float wbound = ff[Image::BND1] * sbound;
+                const RowScale ws = row_scale(wbound);
+                factors(Image::WK, sdown * ws.up);
+                if (!warp_wait(&mb_ks, ph, &s_gave_up)) break;
+                tc::fence_after_sync();
+                tc::tmem_ld16(tq + COL_KS + EP * part, raw);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < EP / 2; ++i) x[i] = mul2(f[i], raw2(raw[2 * i], raw[2 * i + 1]));
+                store_split(x, tq + COL_R + EP / 2 * part, tq + COL_R + 32 + EP / 2 * part);
+                tc::tmem_wait_st();
+                warp_done(&mb_r, lane);
+                // while W T runs: the exact largest value of dS
+                const float stop = row.of_all(top_of_pairs(s));
+                factors(Image::ZT, ws.down);
+                if (!warp_wait(&mb_z, ph, &s_gave_up)) break;
+                tc::fence_after_sync();
+                tc::tmem_ld16(tq + COL_Z1 + EP * part, raw);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < EP / 2; ++i) x[i] = mul2(f[i], raw2(raw[2 * i], raw[2 * i + 1]));
+                tc::tmem_ld16(tq + COL_Z2 + EP * part, raw);
+                factors(Image::ZX, s_dxdown[vc]);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < EP / 2; ++i) x[i] = fma2(f[i], raw2(raw[2 * i], raw[2 * i + 1]), x[i]);
+                f2 z[EP / 2];
+#pragma unroll
+                for (int i = 0; i < EP / 2; ++i) z[i] = x[i];
+                const RowScale rs = row_scale(fmaf(ff[Image::BND2], wbound, ff[Image::BND3] * s_dxtop[vc]));
+                factors(Image::RZ, rs.up);
+#pragma unroll
+                for (int i = 0; i < EP / 2; ++i) x[i] = mul2(f[i], x[i]);
+                store_split(x, tq + COL_R + EP / 2 * part, tq + COL_R + 32 + EP / 2 * part);
+                tc::tmem_wait_st();
+                warp_done(&mb_w, lane);
+                if (on) {
+                    float* dst = zs + (((int64_t)bh * sh.nc + c) * C + EP * part) * P + vc;
+#pragma unroll
+                    for (int i = 0; i < EP / 2; ++i) {
+                        float a, e;
+                        un2(z[i], a, e);
+                        dst[2 * i * P] = a;
+                        dst[(2 * i + 1) * P] = e;
+                    }
+                }
+                // while the update runs: the bound on the next dS (the rows of K and Q
+                // are scaled to below 2^14, the operands carry the inverses)
+                const float all = ff[Image::ALL];
+                const float rtop = row.of_all(top_of_pairs(x)) * rs.down;
+                if (!warp_wait(&mb_d, ph, &s_gave_up)) break;
+                tc::fence_after_sync();
+                sbound = fmaf(all, stop, (rtop + s_dqtop[vc]) * (64.f * 16384.f));
+                {
+                    const float qdown = s_dqdown[vc];
+                    const f2 m = mk2(rs.down, rs.down), mq = mk2(qdown, qdown), keep = mk2(all, all);
+#pragma unroll
+                    for (int e = 0; e < NS; e += 16) {
+                        tc::tmem_ld16(tq + COL_D + k0 + e, raw);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            s[e / 2 + i] = fma2(keep, s[e / 2 + i], mul2(raw2(raw[2 * i], raw[2 * i + 1]), m));
+                        tc::tmem_ld16(tq + COL_E + k0 + e, raw);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            s[e / 2 + i] = fma2(raw2(raw[2 * i], raw[2 * i + 1]), mq, s[e / 2 + i]);
+                    }
+                }
+                warp_done(&mb_free[j & 1], lane);
+                if (j + 1 < nck) {
+                    sdown = put_state(c - 1, sbound);
+                    if (!warp_wait(&mb_full[(j + 1) & 1], ((j + 1) >> 1) & 1, &s_gave_up)) break;
+                }
+            }
+            if (gh0 && on)
+#pragma unroll
+                for (int i = 0; i < NS / 2; ++i)
+                    if (k0 + 2 * i < N) {
+                        float a, e;
+                        un2(s[i], a, e);
+                        gh0[so + (int64_t)(k0 + 2 * i) * P] = a;
+                        gh0[so + (int64_t)(k0 + 2 * i + 1) * P] = e;
+                    }
+        }
+    } else if (warp < CW + OW) {
+        // ------------------------------------------------ dO's operands
+        const int quarter = warp - CW, vc = 32 * quarter + lane;
+        const bool on = vc < P;
+        const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16);
+        if (quarter < quarters) {
+            for (int j = 0; j < nck; ++j) {
+                const int slot = j % NV;
+                if (!warp_wait(&mb_vfull[slot], j / NV & 1, &s_gave_up)) break;
+                const uint16_t* dt = reinterpret_cast<const uint16_t*>(smem + M::V0 + slot * M::VBYTES) + (on ? vc : 0);
+                uint32_t raw[C / 2];
+#pragma unroll
+                for (int i = 0; i < C / 2; ++i) raw[i] = dt[2 * i * P] | (uint32_t)dt[(2 * i + 1) * P] << 16;
+                if (!on)
+#pragma unroll
+                    for (int i = 0; i < C / 2; ++i) raw[i] = 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&mb_vfree[slot]);
+                if (!warp_wait(&mb_full[j & 1], (j >> 1) & 1, &s_gave_up)) break;
+                const float* ff = reinterpret_cast<const float*>(smem + (j & 1) * M::STAGE + M::IMG + Image::F);
+                uint32_t m = 0;
+                float qt = 0.f;
+#pragma unroll
+                for (int i = 0; i < C / 2; ++i) {
+                    m = __vmaxu2(m, raw[i] & 0x7FFF7FFFu);
+                    const float2 w = unpack2(raw[i], E()), f = *reinterpret_cast<const float2*>(ff + Image::DQ + 2 * i);
+                    qt = fmaxf(fmaxf(qt, fabsf(w.x * f.x)), fabsf(w.y * f.y));
+                }
+                const float top = top_of<E>(m);
+                const RowScale xs = row_scale(top), qs = row_scale(qt);
+                // the columns are free once the chain has stored the state (it has read what lay there)
+                if (!warp_wait(&mb_s, j & 1, &s_gave_up)) break;
+                tc::fence_after_sync();
+                s_dxdown[vc] = xs.down;
+                s_dxtop[vc] = top;
+                s_dqdown[vc] = qs.down;
+                s_dqtop[vc] = qt;
+#pragma unroll
+                for (int e = 0; e < C / 2; e += 8) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 y = unpack2(raw[e + i], E());
+                        w[i] = pack2(y.x * xs.up, y.y * xs.up);
+                    }
+                    tmem_st8(tq + COL_DX + e, w);
+                }
+                tc::tmem_wait_st();
+                warp_done(&mb_dx, lane);
+#pragma unroll
+                for (int e = 0; e < C / 2; e += 8) {
+                    f2 y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 w = unpack2(raw[e + i], E()), f = *reinterpret_cast<const float2*>(ff + Image::DQ + 2 * (e + i));
+                        y[i] = mul2(mk2(w.x * f.x, w.y * f.y), mk2(qs.up, qs.up));
+                    }
+                    store_split(y, tq + COL_DQ + e, tq + COL_DQ + 32 + e);
+                }
+                tc::tmem_wait_st();
+                warp_done(&mb_dq, lane);
+                if (lane == 0) mbar_arrive(&mb_free[j & 1]);
+            }
+        }
+    } else if (warp == WMMA) {
+        // ------------------------------------------------ MMA issue
+        constexpr uint32_t id64 = tc::idesc_f16(128, C), idn = tc::idesc_f16(128, ND);
+        for (int j = 0; j < nck; ++j) {
+            const uint32_t ph = j & 1;
+            const uint32_t base = tc::smem_u32(smem) + (j & 1) * M::STAGE;
+            const uint64_t dk = tc::make_desc(base + M::K0, QK<ND>::LBO, QK<ND>::SBO);
+            const uint64_t dkt = tc::make_desc(base + M::KT0, KT<ND>::LBO, KT<ND>::SBO);
+            const uint64_t dqt = tc::make_desc(base + M::QT0, KT<ND>::LBO, KT<ND>::SBO);
+            const uint64_t dtt = tc::make_desc(base + M::IMG, Image::LBO, Image::SBO);
+            const uint64_t dxt = dtt + ((8 * Image::SBO) >> 4);
+            if (!warp_wait(&mb_full[j & 1], (j >> 1) & 1, &s_gave_up)) break;
+            if (!warp_wait(&mb_s, ph, &s_gave_up)) break;
+            tc::fence_after_sync();
+            chain<ND / 16, 2 * QK<ND>::LBO>(tmem + COL_KS, tmem + COL_S, dk, id64, true);  // hi, then lo
+            chain<ND / 16, 2 * QK<ND>::LBO>(tmem + COL_KS, tmem + COL_S + ND / 2, dk, id64, false);
+            commit_elected(&mb_ks);
+            if (!warp_wait(&mb_dx, ph, &s_gave_up)) break;
+            tc::fence_after_sync();
+            chain<4, 2 * Image::LBO>(tmem + COL_Z2, tmem + COL_DX, dxt, id64, true);
+            chain<4, 2 * Image::LBO>(tmem + COL_Z2, tmem + COL_DX, dxt + (Image::PART >> 4), id64, false);
+            if (!warp_wait(&mb_r, ph, &s_gave_up)) break;
+            tc::fence_after_sync();
+            chain<4, 2 * Image::LBO>(tmem + COL_Z1, tmem + COL_R, dtt, id64, true);  // hi hi + lo hi + hi lo
+            chain<4, 2 * Image::LBO>(tmem + COL_Z1, tmem + COL_R + 32, dtt, id64, false);
+            chain<4, 2 * Image::LBO>(tmem + COL_Z1, tmem + COL_R, dtt + (Image::PART >> 4), id64, false);
+            commit_elected(&mb_z);
+            if (lane == 0) mbar_arrive(&mb_z);  // (dO's scales, written before mb_dx, are before this)
+            if (!warp_wait(&mb_w, ph, &s_gave_up)) break;
+            if (!warp_wait(&mb_dq, ph, &s_gave_up)) break;
+            tc::fence_after_sync();
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R, dkt, idn, true);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R + 32, dkt, idn, false);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_E, tmem + COL_DQ, dqt, idn, true);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_E, tmem + COL_DQ + 32, dqt, idn, false);
+            commit_elected(&mb_d);
+            if (lane == 0) mbar_arrive(&mb_d);
+        }
+        if (s_gave_up) {
+            commit_elected(&mb_drain);
+            tc::mbar_wait_bounded(&mb_drain, 0, kDeltaWait);
+        }
+    } else if (warp == WLOAD) {
+        // ------------------------------------------------ loader
+        int last[2] = {-1, -1};  // parity of the last copies into each stage
+        const unsigned char* img = image + (int64_t)bh * sh.nc * Image::STRIDE;
+        const unsigned char* ops = operands + ((int64_t)b * KH + h / sh.G) * sh.nc * Operands<ND>::BWD + QK<ND>::KROWS;
+        for (int j = 0; j < nck; ++j) {
+            const int c = nck - 1 - j;
+            const uint32_t at = tc::smem_u32(smem) + (j & 1) * M::STAGE;
+            if (j >= 2 && !warp_wait(&mb_free[j & 1], ((j >> 1) - 1) & 1, &s_gave_up)) break;
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&mb_full[j & 1], Image::BYTES + M::OPS);
+                tc::bulk_g2s(at + M::K0, ops + (int64_t)c * Operands<ND>::BWD, M::OPS, &mb_full[j & 1]);
+                tc::bulk_g2s(at + M::IMG, img + (int64_t)c * Image::STRIDE, Image::BYTES, &mb_full[j & 1]);
+                last[j & 1] = (j >> 1) & 1;
+                if (c >= 2) {  // what the next copies into this stage read, into L2
+                    prefetch_l2(ops + (int64_t)(c - 2) * Operands<ND>::BWD, M::OPS);
+                    prefetch_l2(img + (int64_t)(c - 2) * Image::STRIDE, Image::BYTES);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0 && s_gave_up)  // no copy may land in shared memory that is no longer this CTA's
+            for (int i = 0; i < 2; ++i)
+                if (last[i] >= 0) tc::mbar_wait_bounded(&mb_full[i], last[i], kDeltaWait);
+    } else {
+        // ------------------------------------------------ dO (rows of P elements; zeros where no token is)
+        const int t = tid - 32 * WV, per = P / 8;
+        for (int j = 0; j < nck; ++j) {
+            const int c = nck - 1 - j, slot = j % NV, n = min(len - c * C, C);
+            const uint32_t at = tc::smem_u32(smem) + M::V0 + slot * M::VBYTES;
+            const E* src = dout + (((int64_t)b * sh.T + (int64_t)c * C) * sh.H + h) * P;
+            if (j >= NV && !warp_wait(&mb_vfree[slot], (j / NV - 1) & 1, &s_gave_up)) break;
             for (int id = t; id < C * per; id += VT) {
                 const int i = id / per;
                 cp_async16(at + 16 * id, src + (int64_t)min(i, n - 1) * sh.H * P + 8 * (id - i * per), i < n);
@@ -902,7 +1300,7 @@ cudaError_t allow(uint32_t bytes) {
 // for its own scan too), then the operands of every chunk and key head.
 size_t image_bytes(const DeltaArgs& a) { return (size_t)chunk_count(a) * Image::STRIDE; }
 size_t operand_bytes(const DeltaArgs& a, bool back) {
-    const uint32_t one = a.N <= 64 ? Operands<64>::stride(back) : Operands<128>::stride(back);
+    const uint32_t one = a.N <= 64 ? (back ? Operands<64>::BWD : Operands<64>::FWD) : back ? Operands<128>::BWD : Operands<128>::FWD;
     return (size_t)(chunk_count(a) / a.H * a.KH) * one;
 }
 
@@ -938,6 +1336,28 @@ cudaError_t forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     return e != cudaSuccess ? e : scan_tc<E, ND, false>(a, image, operands, nullptr, nullptr, st);
 }
 
+template <typename E, int ND>
+cudaError_t back_scans_tc(const DeltaArgs& a, void* ws, float* states, float* after, float* writes, float* zs,
+                          cudaStream_t st) {
+    unsigned char* image = static_cast<unsigned char*>(ws);
+    unsigned char* image_t = image + image_bytes(a);
+    unsigned char* operands = image_t + image_bytes(a);
+    cudaError_t e = prep_tc<E, ND, true>(a, image, image_t, operands, st);
+    if (e != cudaSuccess) return e;
+    if ((e = scan_tc<E, ND, true>(a, image, operands, states, writes, st)) != cudaSuccess) return e;
+    using M = BackSmem<ND>;
+    if ((e = allow<delta_back_scan_tc<E, ND>>(M::BYTES)) != cudaSuccess) return e;
+    delta_back_scan_tc<E, ND><<<(unsigned)(a.Bz * a.H), ST, M::BYTES, st>>>(
+        static_cast<const E*>(a.dout), image_t, operands, a.dh_final, a.lens, a.gh0, after, zs, shape(a), status_word());
+    return cudaGetLastError();
+}
+template <typename E>
+cudaError_t back_scans_by_width(const DeltaArgs& a, void* ws, float* states, float* after, float* writes, float* zs,
+                                cudaStream_t st) {
+    return a.N <= 64 ? back_scans_tc<E, 64>(a, ws, states, after, writes, zs, st)
+                     : back_scans_tc<E, 128>(a, ws, states, after, writes, zs, st);
+}
+
 template <typename E>
 cudaError_t forward_by_width(const DeltaArgs& a, void* ws, cudaStream_t st) {
     return a.N <= 64 ? forward_tc<E, 64>(a, ws, st) : forward_tc<E, 128>(a, ws, st);
@@ -948,6 +1368,13 @@ cudaError_t forward_by_width(const DeltaArgs& a, void* ws, cudaStream_t st) {
 size_t tc_workspace_bytes(const DeltaArgs& a) { return image_bytes(a) + operand_bytes(a, false); }
 cudaError_t launch_forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     return a.dtype == CSSD_BF16 ? forward_by_width<__nv_bfloat16>(a, ws, st) : forward_by_width<__half>(a, ws, st);
+}
+
+size_t tc_back_bytes(const DeltaArgs& a) { return 2 * image_bytes(a) + operand_bytes(a, true); }
+cudaError_t launch_back_scans_tc(const DeltaArgs& a, void* ws, float* states, float* after, float* writes, float* zs,
+                                 cudaStream_t st) {
+    return a.dtype == CSSD_BF16 ? back_scans_by_width<__nv_bfloat16>(a, ws, states, after, writes, zs, st)
+                                : back_scans_by_width<__half>(a, ws, states, after, writes, zs, st);
 }
 
 }  // namespace delta

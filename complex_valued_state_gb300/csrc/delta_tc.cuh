@@ -214,21 +214,21 @@ struct Image {
     // Forward (T and X times beta): of the state's answer in R, of the products
     // in U and in U', of the two parts of o.
     static constexpr int KB = 0, UU = 64, UW = 128, OQ = 192, OX = 256;
-    // Backward: of K dS in the first operand, of the two products in Z, of Z
+    // Backward: of K dS in the first operand W, of the two products in Z, of Z
     // in the second operand, of dO in the third.
     static constexpr int WK = 0, ZT = 64, ZX = 128, RZ = 192, DQ = 256;
     // exp(G_end); and what bounds the scan's operands (see delta_scan_tc).
-    static constexpr int ALL = 320, BND1 = 321, BND2 = 322, FLOATS = 324;
+    static constexpr int ALL = 320, BND1 = 321, BND2 = 322, BND3 = 323, FLOATS = 324;
     static constexpr uint32_t BYTES = F + 4 * FLOATS;
     static constexpr uint32_t STRIDE = (BYTES + 255) / 256 * 256;
 };
-// [Q; K]: rows i (64 of Q, 64 of K) by ND.
+// [Q; K]: rows i (64 of Q, then 64 of K) by ND; a row group's columns are
+// contiguous, so each of the two is.
 template <int ND>
 struct QK {
-    static constexpr uint32_t SBO = 128, LBO = 16 * 128, BYTES = (ND / 8) * LBO;
-    static constexpr uint32_t KROWS = 8 * SBO;  // bytes from Q's rows to K's
+    static constexpr uint32_t LBO = 128, SBO = (ND / 8) * LBO, KROWS = 8 * SBO, BYTES = 2 * KROWS;
 };
-// K^T (the backward scan: Q^T behind it): rows k (ND) by 64 tokens.
+// K^T, then (the backward) Q^T: rows k (ND) by 64 tokens.
 template <int ND>
 struct KT {
     static constexpr uint32_t SBO = 128, LBO = (ND / 8) * SBO, BYTES = 8 * LBO;
@@ -236,8 +236,7 @@ struct KT {
 template <int ND>
 struct Operands {
     static constexpr uint32_t KT0 = QK<ND>::BYTES, QT0 = KT0 + KT<ND>::BYTES;
-    static constexpr uint32_t FWD = QT0, BWD = QT0 + KT<ND>::BYTES;  // bytes of each direction
-    static constexpr uint32_t stride(bool back) { return ((back ? BWD : FWD) + 255) / 256 * 256; }
+    static constexpr uint32_t FWD = QT0, BWD = QT0 + KT<ND>::BYTES;  // bytes the two directions leave
 };
 
 }  // namespace delta
