@@ -205,6 +205,11 @@ cudaError_t launch_forward_tc(const DeltaArgs& a, void* workspace, cudaStream_t 
 size_t tc_back_bytes(const DeltaArgs& a);
 cudaError_t launch_back_scans_tc(const DeltaArgs& a, void* workspace, float* states, float* after, float* writes,
                                  float* zs, cudaStream_t stream);
+// The gradients from those (the same workspace): gv, gg and gbeta, and gq and
+// gk, or fp32 parts of them per value head [Bz][T][H][N] where key heads are
+// shared.
+cudaError_t launch_grad_tc(const DeltaArgs& a, void* workspace, const float* states, const float* after,
+                           const float* writes, const float* zs, void* gq, void* gk, cudaStream_t stream);
 }  // namespace delta
 
 struct DeltaStepArgs {

@@ -550,10 +550,14 @@ __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const 
     }
 }
 
-// [rows, KH, G, N] fp32 -> [rows, KH, N], summed over G in order.
+// [rows, KH, G, N] fp32 -> [rows, KH, N], summed over G in order; of two
+// arrays, by blockIdx.y.
 template <typename E>
-__global__ void __launch_bounds__(256) delta_sum_heads(const float4* __restrict__ part, E* __restrict__ out, int64_t n4,
-                                                       int G, int N4) {
+__global__ void __launch_bounds__(256) delta_sum_heads(const float4* __restrict__ part0, const float4* __restrict__ part1,
+                                                       E* __restrict__ out0, E* __restrict__ out1, int64_t n4, int G,
+                                                       int N4) {
+    const float4* part = blockIdx.y ? part1 : part0;
+    E* out = blockIdx.y ? out1 : out0;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n4; e += (int64_t)gridDim.x * 256) {
         const float4* p = part + (e / N4) * G * N4 + e % N4;
         float4 s = p[0];
@@ -624,46 +628,44 @@ cudaError_t grad(const DeltaArgs& a, const float* states, const float* after, co
     return cudaGetLastError();
 }
 
-// The gradient kernel, and the sum over the value heads of a shared key head.
-template <typename E>
-cudaError_t grads(const DeltaArgs& a, const float* states, const float* after, const float* writes, const float* zs,
-                  float* pq, float* pk, cudaStream_t st) {
-    if (a.H == a.KH) return grad<E, E>(a, states, after, writes, zs, a.gq, a.gk, st);
-    const cudaError_t e = grad<E, float>(a, states, after, writes, zs, pq, pk, st);
-    if (e != cudaSuccess) return e;
-    const int64_t n4 = a.Bz * a.T * a.KH * (a.N / 4);
-    const unsigned grid = (unsigned)((n4 + 255) / 256 < 65535 ? (n4 + 255) / 256 : 65535);
-    delta_sum_heads<E><<<grid, 256, 0, st>>>(reinterpret_cast<const float4*>(pq), static_cast<E*>(a.gq), n4,
-                                             (int)(a.H / a.KH), (int)(a.N / 4));
-    delta_sum_heads<E><<<grid, 256, 0, st>>>(reinterpret_cast<const float4*>(pk), static_cast<E*>(a.gk), n4,
-                                             (int)(a.H / a.KH), (int)(a.N / 4));
-    return cudaGetLastError();
-}
-
 template <typename E>
 cudaError_t backward(const DeltaArgs& a, void* ws, cudaStream_t st) {
+    constexpr bool TC = sizeof(E) == 2;  // 16-bit types: the tensor-core kernels
     float* states = static_cast<float*>(ws);
     float* after = states + state_floats(a);
     float* writes = after + state_floats(a);
     float* zs = writes + write_floats(a);
     float* pq = zs + write_floats(a);
     float* pk = pq + part_floats(a);
-    float* tx = pk + part_floats(a);
-    if constexpr (sizeof(E) == 2) {
-        const cudaError_t e = launch_back_scans_tc(a, tx, states, after, writes, zs, st);
-        return e != cudaSuccess ? e : grads<E>(a, states, after, writes, zs, pq, pk, st);
+    float* rest = pk + part_floats(a);  // T and X; the tensor-core kernels' own
+    cudaError_t e;
+    if constexpr (TC) {
+        e = launch_back_scans_tc(a, rest, states, after, writes, zs, st);
     } else {
-        cudaError_t e = prep<E>(a, tx, st);
-        if (e == cudaSuccess) e = scan<E>(a, tx, nullptr, nullptr, states, writes, st);
-        if (e != cudaSuccess) return e;
+        e = prep<E>(a, rest, st);
+        if (e == cudaSuccess) e = scan<E>(a, rest, nullptr, nullptr, states, writes, st);
         const size_t sm = scan_smem(a);
-        if ((e = allow_smem(delta_back_scan<E>, sm)) != cudaSuccess) return e;
+        if (e == cudaSuccess) e = allow_smem(delta_back_scan<E>, sm);
+        if (e != cudaSuccess) return e;
         delta_back_scan<E><<<(unsigned)((a.P + PW - 1) / PW * a.Bz * a.H), NT, sm, st>>>(
-            static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.dout), a.g, a.beta, tx,
+            static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.dout), a.g, a.beta, rest,
             a.dh_final, a.lens, a.scale, a.gh0, after, zs, geo(a));
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        return grads<E>(a, states, after, writes, zs, pq, pk, st);
+        e = cudaGetLastError();
     }
+    if (e != cudaSuccess) return e;
+    // key heads that are shared: a part per value head, summed in order
+    const bool shared = a.H != a.KH;
+    if constexpr (TC)
+        e = launch_grad_tc(a, rest, states, after, writes, zs, shared ? pq : a.gq, shared ? pk : a.gk, st);
+    else
+        e = grad<E, float>(a, states, after, writes, zs, shared ? pq : a.gq, shared ? pk : a.gk, st);
+    if (e != cudaSuccess || !shared) return e;
+    const int64_t n4 = a.Bz * a.T * a.KH * (a.N / 4);
+    const unsigned grid = (unsigned)((n4 + 255) / 256 < 65535 ? (n4 + 255) / 256 : 65535);
+    delta_sum_heads<E><<<dim3(grid, 2), 256, 0, st>>>(reinterpret_cast<const float4*>(pq), reinterpret_cast<const float4*>(pk),
+                                                      static_cast<E*>(a.gq), static_cast<E*>(a.gk), n4,
+                                                      (int)(a.H / a.KH), (int)(a.N / 4));
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -149,9 +149,7 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
     __shared__ float s_sum[4][C], s_sumx[4][C];   // parts of sums over T's and X's rows (columns)
     __shared__ float s_norm[C];                   // |k|
     __shared__ float s_top[4][PT / 32];
-    __shared__ __align__(16) float s_f[4][C];  // exp(G_a - G_j) s_down[j], a the starts of the 16-token blocks
-    __shared__ float s_e[C];                   // exp(G_i - G_a), a the start of i's block
-    __shared__ int s_steep;
+    __shared__ __align__(16) DecayTables tab;
     __shared__ __align__(8) uint64_t mb[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
@@ -179,7 +177,7 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
         tc::mbar_init(&mb[1], 1);
         tc::mbar_fence_init();
         s_gave_up = 0;
-        s_steep = 0;
+        tab.steep = 0;
     }
     {
         const float down = store_half_row<E, ND>(raw, smem, qrow, half);
@@ -202,17 +200,7 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
     }
     float* sa = reinterpret_cast<float*>(smem + M::A);  // A, then T in its place
     float* sp = reinterpret_cast<float*>(smem + M::P);
-    {  // the tables of decays while the MMA runs
-        const int a = 16 * (tid / C), j = tid % C;
-        // G_a - G_j as a float and what its rounding leaves
-        const float at = d.hi[a] - d.hi[j], back = at - d.hi[a];
-        const float rest = ((d.hi[a] - (at - back)) - (d.hi[j] + back)) + (d.lo[a] - d.lo[j]);
-        s_f[tid / C][j] = j < a + 16 ? expf(at) * (1.f + rest) * s_down[j] : 0.f;
-        if (j / 16 == tid / C) {
-            s_e[j] = expf(-at) * (1.f - rest);
-            if (!(fabsf(at) < 40.f)) s_steep = 1;  // (a NaN or infinite sum too)
-        }
-    }
+    decay_tables(tab, d, s_down, tid);  // while the MMA runs
     const bool owner = h % sh.G == 0;  // this CTA leaves the key head's operands, once for its group
     if (owner) {
         transpose_operand<ND>(smem + O::KT0, smem, C, warp, PT / 32, lane);
@@ -246,11 +234,9 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
         if (above) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = 0.f;
-        } else if (!s_steep) {
-            // e^{G_i - G_j} as a product over the start of i's block: exact enough
-            // while a block's decay, which one factor undoes, stays above e^-40
-            const float fe = f * s_e[i];
-            const float4* fj = reinterpret_cast<const float4*>(s_f[i / 16] + j0);
+        } else if (!tab.steep) {
+            const float fe = f * tab.e[i];
+            const float4* fj = reinterpret_cast<const float4*>(tab.f[i / 16] + j0);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
                 const float4 m = fj[j / 4];
@@ -260,13 +246,9 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
                 x[j + 3] = j0 + j + 3 <= last ? __uint_as_float(v[j + 3]) * (m.w * fe) : 0.f;
             }
         } else {
-            const float hi = d.hi[i], lo = d.lo[i];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                // (exp's own error is relative to a value that falls as fast as its argument grows)
-                const float m = __expf((hi - d.hi[j0 + j]) + (lo - d.lo[j0 + j]));
-                x[j] = j0 + j <= last ? __uint_as_float(v[j]) * (s_down[j0 + j] * f) * m : 0.f;
-            }
+            for (int j = 0; j < 32; ++j)
+                x[j] = j0 + j <= last ? __uint_as_float(v[j]) * (s_down[j0 + j] * f) * steep_decay(d, i, j0 + j) : 0.f;
         }
         if (tid == 0) bulk_wait_read();  // the operands are copied out: their memory is free
         __syncthreads();
@@ -382,6 +364,8 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
             ff[Image::ZX + tid] = scale * xs.down;
             ff[Image::RZ + tid] = -fi * d.beta[tid] * kd;
             ff[Image::DQ + tid] = scale * fi * qd;
+            ff[Image::KD + tid] = kd;
+            ff[Image::QD + tid] = qd;
         } else if (warp == 2) {
             // |W| <= BND1 |dS|, the second operand <= BND2 |W| + BND3 |dO|, of a lane's largest values
             float b1 = 0.f, b2 = 0.f, b3 = 0.f;
@@ -1277,6 +1261,486 @@ __global__ void __launch_bounds__(ST, 1) delta_back_scan_tc(const E* __restrict_
     if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusDelta);
 }
 
+// --------------------------------------------------------------- dQ, dK, dV, dg, dbeta
+// One CTA per chunk and value head (the formulas stand at the head of
+// delta.cu), the products on the tensor cores with tokens i in the lanes: row
+// i of what becomes dQ in lane i, of dK in lane 64 + i, so that
+//     [dO; Z] U^T, [Q; K] K^T          64 columns each
+//     [dO; Z] S^T, [Z; U] dS^T         N columns each (the first rows of the
+//                                      second are not used)
+//     [Pm 0; W + W^T  Pm^T] [K; Q]     N columns
+// take five MMA chains of 128 rows.  S, dS, Z and U are fp32 and are split on
+// the way into shared memory, a row a scale; dO is exact with its scale, Pm
+// and W are split with one scale a chunk (into tensor memory, over the first
+// two products).  Bound by the loads: 4 N P bytes of S and of dS a chunk and
+// head, twice 256 P of Z and U.
+template <int ND, int PD>
+struct GradSmem {
+    static constexpr int NT = ND == 128 ? 512 : 256;  // 32 columns of dQ, dK a thread
+    static constexpr uint32_t LBO = 128, SBO = (PD / 8) * LBO, ROWS = 8 * SBO;  // 64 rows
+    static constexpr uint32_t HI = 0, LO = 3 * ROWS, ST = 6 * ROWS, STP = (ND / 8) * SBO;  // [dO; Z; U], their rests; S
+    // The operands of K and Q; at the widest, where not everything fits, K^T and
+    // Q^T come late, over dO (read by then) and its rest.
+    static constexpr bool LATE = ND == 128 && PD == 128;
+    static constexpr uint32_t OPS = ST + 2 * STP, FIRST = LATE ? QK<ND>::BYTES : Operands<ND>::BWD, BYTES = OPS + FIRST;
+    static constexpr uint32_t KT0 = LATE ? HI : OPS + Operands<ND>::KT0, QT0 = LATE ? LO : OPS + Operands<ND>::QT0;
+    static_assert(!LATE || KT<ND>::BYTES <= ROWS, "K^T over dO");
+    static constexpr uint32_t MAT = OPS;  // Pm below the diagonal and W^T above, over Q and K when those are read
+    static_assert(4 * C * C <= 2 * QK<ND>::KROWS, "Pm over Q and K");
+};
+
+// 8 rows a warp (row lane % 8), a lane's column groups lane / 8, + 4, ..: the
+// rows of an fp32 matrix with `width` columns, zeros past them.
+template <int NG>
+__device__ __forceinline__ void load_groups(float (&x)[NG][8], const float* row, int lane, int width, bool there) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int c = 8 * (lane / 8 + 4 * g);
+        const bool in = there && c < width;
+        const float4 a = in ? __ldcs(reinterpret_cast<const float4*>(row + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 b = in ? __ldcs(reinterpret_cast<const float4*>(row + c + 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[g][0] = a.x, x[g][1] = a.y, x[g][2] = a.z, x[g][3] = a.w;
+        x[g][4] = b.x, x[g][5] = b.y, x[g][6] = b.z, x[g][7] = b.w;
+    }
+}
+// The largest of a row over its four lanes.
+__device__ __forceinline__ float over_row(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+// The groups scaled by their row's power of two, split and stored; returns
+// the inverse scale.
+template <int NG>
+__device__ __forceinline__ float store_groups(const float (&x)[NG][8], unsigned char* hi, unsigned char* lo, int lane) {
+    float top = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(x[g][u]));
+    const RowScale s = row_scale(over_row(top));
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) split2(x[g][2 * u] * s.up, x[g][2 * u + 1] * s.up, h[u], l[u]);
+        const uint32_t at = (lane / 8 + 4 * g) * 128 + (lane % 8) * 16;
+        *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+    return s.down;
+}
+
+template <typename E, typename O, int ND, int PD>
+__global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ? 1 : 2)
+    delta_grad_tc(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ dout,
+                  const float* __restrict__ g, const float* __restrict__ beta, const int* __restrict__ lens, float scale,
+                  const unsigned char* __restrict__ image_t, const unsigned char* __restrict__ operands,
+                  const float* __restrict__ states, const float* __restrict__ after, const float* __restrict__ writes,
+                  const float* __restrict__ zs, O* __restrict__ gq, O* __restrict__ gk, E* __restrict__ gv,
+                  float* __restrict__ gg, float* __restrict__ gbeta, Shape sh, unsigned* status) {
+    using M = GradSmem<ND, PD>;
+    constexpr int NT = M::NT, NW = NT / 32, NPART = NT / 128, CJ = C / NPART, NG = PD / 32;
+    constexpr uint32_t COL_DU = 0, COL_KK = 64, COL_S = 128, COL_D = 128 + ND, COLS = ND == 128 ? 512 : 256;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(16) Decays d;
+    __shared__ __align__(16) DecayTables tab;
+    __shared__ __align__(16) float s_kd[C], s_qd[C], s_u[C], s_rows[2 * C], s_st[ND], s_ds[ND];
+    __shared__ float s_zv[C], s_gb[NPART][C], s_qgq[NPART][C], s_kz[NPART][C], s_top[NW], s_kus[NW], s_kqd[4];
+    __shared__ double s_dot[NW];
+    __shared__ __align__(8) uint64_t mb_ops, mb_late, mb_1, mb_2, mb_3, mb_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_gave_up;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c = blockIdx.x % sh.nc, bh = blockIdx.x / sh.nc;
+    const int b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
+    const int len = row_len(lens, b, sh.T), n = min(len - c * C, C), here = min(sh.T - c * C, C);
+    const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C, ci = (int64_t)bh * sh.nc + c;
+    const int64_t ko = (t0 * KH + h / sh.G) * N, ks = (int64_t)KH * N, vo = (t0 * sh.H + h) * P, vs = (int64_t)sh.H * P;
+    const int64_t go = (t0 * sh.H + h) * N, gs = (int64_t)sh.H * N;  // of gq and gk: the same as ko when G = 1
+    if (n < here) {  // tokens that are not there
+        const int from = max(n, 0);
+        for (int e = tid; e < (here - from) * N; e += NT) {
+            gq[go + (from + e / N) * gs + e % N] = from_f<O>(0.f);
+            gk[go + (from + e / N) * gs + e % N] = from_f<O>(0.f);
+        }
+        for (int e = tid; e < (here - from) * P; e += NT) gv[vo + (from + e / P) * vs + e % P] = from_f<E>(0.f);
+        for (int i = from + tid; i < here; i += NT) gg[(t0 + i) * sh.H + h] = gbeta[(t0 + i) * sh.H + h] = 0.f;
+    }
+    if (n <= 0) return;
+    const unsigned char* ops = operands + (((int64_t)b * KH + h / sh.G) * sh.nc + c) * Operands<ND>::BWD;
+    if (warp == 0) {
+        tc::tmem_alloc(&s_tmem, COLS);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        s_gave_up = 0;
+        tab.steep = 0;
+        tc::mbar_init(&mb_ops, 1);
+        tc::mbar_init(&mb_1, 1);
+        tc::mbar_init(&mb_2, 1);
+        tc::mbar_init(&mb_3, 2);
+        tc::mbar_init(&mb_late, 1);
+        tc::mbar_init(&mb_drain, 1);
+        tc::mbar_fence_init();
+        tc::mbar_arrive_expect_tx(&mb_ops, M::FIRST);
+        tc::bulk_g2s(tc::smem_u32(smem + M::OPS), ops, M::FIRST, &mb_ops);
+    }
+    if (warp == NW - 1) chunk_decays(d, g + t0 * sh.H + h, beta + t0 * sh.H + h, sh.H, n, lane);
+    const float* fb = reinterpret_cast<const float*>(image_t + ci * Image::STRIDE + Image::F);
+    if (tid < C) {
+        s_kd[tid] = fb[Image::KD + tid];
+        s_qd[tid] = fb[Image::QD + tid];
+    }
+    // Z (with dV and z.v), U, dO: 8 rows a warp
+    for (int w = warp; w < 24; w += NW) {
+        const int what = w / 8, rg = w % 8, i = 8 * rg + lane % 8;
+        unsigned char* hi = smem + M::HI + (what == 0 ? 1 : what == 1 ? 2 : 0) * M::ROWS + rg * M::SBO;
+        if (what < 2) {
+            float x[NG][8];
+            load_groups<NG>(x, (what ? writes : zs) + (ci * C + i) * P, lane, P, true);
+            const float down = store_groups<NG>(x, hi, hi + 3 * M::ROWS, lane);
+            if (lane < 8) (what ? s_u[i] : s_rows[C + i]) = down;
+            if (what == 0) {
+                const float bt = i < n ? beta[(t0 + i) * sh.H + h] : 0.f;
+                float zv = 0.f;
+#pragma unroll
+                for (int e = 0; e < NG; ++e) {
+                    const int col = 8 * (lane / 8 + 4 * e);
+                    if (i < n && col < P) {
+                        const uint4 raw = *reinterpret_cast<const uint4*>(v + vo + i * vs + col);
+                        const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                        uint32_t out[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const float2 y = unpack2(in[u], E());
+                            zv = fmaf(y.x, x[e][2 * u], fmaf(y.y, x[e][2 * u + 1], zv));
+                            out[u] = pack_as<E>(mk2(bt * x[e][2 * u], bt * x[e][2 * u + 1]));
+                        }
+                        *reinterpret_cast<uint4*>(gv + vo + i * vs + col) = make_uint4(out[0], out[1], out[2], out[3]);
+                    }
+                }
+                zv += __shfl_xor_sync(0xffffffffu, zv, 8);
+                zv += __shfl_xor_sync(0xffffffffu, zv, 16);
+                if (lane < 8) s_zv[i] = zv;
+            }
+        } else {
+            uint4 raw[NG];
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < NG; ++e) {
+                const int col = 8 * (lane / 8 + 4 * e);
+                raw[e] = i < n && col < P ? *reinterpret_cast<const uint4*>(dout + vo + i * vs + col) : make_uint4(0, 0, 0, 0);
+                m = __vmaxu2(m, __vmaxu2(absmax2(raw[e].x, raw[e].y), absmax2(raw[e].z, raw[e].w)));
+            }
+            const RowScale sc = row_scale(over_row(top_of<E>(m)));
+#pragma unroll
+            for (int e = 0; e < NG; ++e) {
+                const uint32_t in[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
+                uint32_t out[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float2 y = unpack2(in[u], E());
+                    out[u] = pack2(y.x * sc.up, y.y * sc.up);
+                }
+                const uint32_t at = (lane / 8 + 4 * e) * 128 + (lane % 8) * 16;
+                *reinterpret_cast<uint4*>(hi + at) = make_uint4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<uint4*>(hi + 3 * M::ROWS + at) = make_uint4(0, 0, 0, 0);
+            }
+            if (lane < 8) s_rows[i] = sc.down;
+        }
+    }
+    // S into its operand; dS into registers for the same place later, and <S, dS>
+    float ds[NG][8];
+    const int srow = 8 * warp + lane % 8;
+    {
+        static_assert(NW * 8 == ND, "a warp has 8 rows of the state");
+        float x[NG][8];
+        load_groups<NG>(x, states + (ci * N + srow) * P, lane, P, srow < N);
+        const float down = store_groups<NG>(x, smem + M::ST + warp * M::SBO, smem + M::ST + M::STP + warp * M::SBO, lane);
+        if (lane < 8) s_st[srow] = down;
+        load_groups<NG>(ds, after + (ci * N + srow) * P, lane, P, srow < N);
+        float part = 0.f;
+#pragma unroll
+        for (int e = 0; e < NG; ++e)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) part = fmaf(x[e][u], ds[e][u], part);
+        double dot = (double)part;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) s_dot[warp] = dot;
+    }
+    tc::fence_proxy_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem, base = tc::smem_u32(smem);
+    constexpr uint32_t id64 = tc::idesc_f16(128, C), idn = tc::idesc_f16(128, ND);
+    // a (128 rows, hi and their rests) times b: hi hi + lo hi + hi lo
+    auto split_product = [&](uint32_t dcol, uint32_t a, uint32_t bb, uint32_t brest, uint32_t id) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const uint64_t da = tc::make_desc(base + a + (p == 1 ? 3 * M::ROWS : 0), M::LBO, M::SBO);
+            const uint64_t db = tc::make_desc(base + bb + (p == 2 ? brest : 0), M::LBO, M::SBO);
+#pragma unroll
+            for (int kk = 0; kk < PD / 16; ++kk)
+                tc::mma_f16(tmem + dcol, da + 16 * kk, db + 16 * kk, id, p || kk);
+        }
+    };
+    if (tid == 0) {
+        wait_or_give_up(&mb_ops, 0, &s_gave_up);
+        split_product(COL_DU, M::HI, M::HI + 2 * M::ROWS, 3 * M::ROWS, id64);
+        const uint64_t dqk = tc::make_desc(base + M::OPS, QK<ND>::LBO, QK<ND>::SBO);
+#pragma unroll
+        for (int kk = 0; kk < ND / 16; ++kk)
+            tc::mma_f16(tmem + COL_KK, dqk + 16 * kk, dqk + (QK<ND>::KROWS >> 4) + 16 * kk, id64, kk != 0);
+        tc::commit(&mb_1);
+        split_product(COL_S, M::HI, M::ST, M::STP, idn);
+        tc::commit(&mb_2);
+    }
+    __syncwarp();
+    if (tid < 256) decay_tables(tab, d, nullptr, tid);
+    if (warp == NW - 1) {  // the largest of K's and Q's inverse scales
+        float m = fmaxf(fmaxf(s_kd[lane], s_kd[lane + 32]), fmaxf(s_qd[lane], s_qd[lane + 32]));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) s_kqd[0] = m;
+    }
+    __syncthreads();
+
+    // ---- Pm and W
+    const int quarter = warp % 4, part = warp / 4, row = 32 * quarter + lane, i = row % C, j0 = CJ * part;
+    const bool is_k = row >= C;
+    const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16);
+    float* mat = reinterpret_cast<float*>(smem + M::MAT);
+    auto at = [](int r, int cc) { return r * C + (cc ^ (r & 31)); };  // rows and columns without bank conflicts
+    float pw[CJ];  // this thread's columns of Pm's row i, or of W's
+    {
+        uint32_t du[CJ], kk[CJ];
+        warp_wait(&mb_1, 0, &s_gave_up);
+        tc::fence_after_sync();
+        if constexpr (CJ == 32) {
+            tmem_ld32(tq + COL_DU + j0, du);
+            if (is_k) tmem_ld32(tq + COL_KK + j0, kk);
+        } else {
+            tc::tmem_ld16(tq + COL_DU + j0, du);
+            if (is_k) tc::tmem_ld16(tq + COL_KK + j0, kk);
+        }
+        tc::tmem_wait_ld();
+        const float ri = s_rows[row] * (is_k ? 1.f : scale), ei = tab.e[i], kdi = s_kd[i];
+        float top = 0.f, gb = 0.f;
+#pragma unroll
+        for (int e = 0; e < CJ; ++e) {
+            const int j = j0 + e;
+            const float m = tab.steep ? steep_decay(d, i, j) : ei * tab.f[i / 16][j];
+            const bool keep = is_k ? i > j : i >= j;
+            float x = keep ? __uint_as_float(du[e]) * (ri * s_u[j]) * m : 0.f;
+            if (is_k) {
+                gb = keep ? fmaf(x, __uint_as_float(kk[e]) * (kdi * s_kd[j]), gb) : gb;
+                x *= -d.beta[i];
+            }
+            pw[e] = x;
+            top = fmaxf(top, fabsf(x));
+        }
+        if (is_k) s_gb[part][i] = gb;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) s_top[warp] = top;
+    }
+    tc::fence_before_sync();
+    __syncthreads();  // (Q and K of the operands are read: mb_1)
+    tc::fence_after_sync();
+#pragma unroll
+    for (int e = 0; e < CJ; ++e) {
+        const int j = j0 + e;
+        if (is_k) {
+            if (i > j) mat[at(j, i)] = pw[e];
+        } else if (i >= j) {
+            mat[at(i, j)] = pw[e];
+        }
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, s_top[w]);
+    const RowScale ps = row_scale(top * s_kqd[0]);
+    __syncthreads();
+    // the A operand of the last product: [Pm 0; W + W^T  Pm^T], times the inverse scales of K and Q
+#pragma unroll
+    for (int e = 0; e < CJ; e += 16) {
+        f2 a[8], z[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            float x[2], y[2];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int j = j0 + e + 2 * u + w;
+                x[w] = pw[e + 2 * u + w];
+                y[w] = 0.f;
+                if (is_k) {
+                    if (j > i) x[w] = mat[at(i, j)];
+                    if (j >= i) y[w] = mat[at(j, i)] * (s_qd[j] * ps.up);
+                }
+                x[w] *= s_kd[j] * ps.up;
+            }
+            a[u] = mk2(x[0], x[1]);
+            z[u] = mk2(y[0], y[1]);
+        }
+        store_split(a, tq + (j0 + e) / 2, tq + 32 + (j0 + e) / 2);
+        store_split(z, tq + 64 + (j0 + e) / 2, tq + 96 + (j0 + e) / 2);
+    }
+    tc::tmem_wait_st();
+
+    // ---- the products with S; dS in its place
+    constexpr int NC = ND / NPART;  // 32
+    const int n0 = NC * part;
+    float first[NC];  // of dQ: its part from S; of dK: -beta e^G Z S^T
+    float kz = 0.f, kus = 0.f, qgq = 0.f;
+    uint4 own[NC / 8];  // q's row for dQ, k's for dK
+    {
+        const E* src = (is_k ? k : q) + ko + i * ks + n0;
+#pragma unroll
+        for (int e = 0; e < NC / 8; ++e)
+            own[e] = i < n && n0 + 8 * e < N ? *reinterpret_cast<const uint4*>(src + 8 * e) : make_uint4(0, 0, 0, 0);
+        uint32_t r[NC];
+        warp_wait(&mb_2, 0, &s_gave_up);
+        tc::fence_after_sync();
+        tmem_ld32(tq + COL_S + n0, r);
+        tc::tmem_wait_ld();
+        const float f = s_rows[row] * (is_k ? 1.f : scale * d.in[i]), bg = -d.beta[i] * d.in[i];
+#pragma unroll
+        for (int e = 0; e < NC; ++e) {
+            const float x = __uint_as_float(r[e]) * (f * s_st[n0 + e]);
+            if (is_k) {
+                const uint32_t w = reinterpret_cast<const uint32_t*>(&own[e / 8])[e % 8 / 2];
+                const float2 y = unpack2(w, E());
+                kz = fmaf(e & 1 ? y.y : y.x, x, kz);
+            }
+            first[e] = is_k ? bg * x : x;
+        }
+        const float down = store_groups<NG>(ds, smem + M::ST + warp * M::SBO, smem + M::ST + M::STP + warp * M::SBO, lane);
+        if (lane < 8) s_ds[srow] = down;
+    }
+    tc::fence_proxy_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) {
+        if (lane == 0) {
+            if (M::LATE) {
+                tc::mbar_arrive_expect_tx(&mb_late, 2 * KT<ND>::BYTES);
+                tc::bulk_g2s(base + M::KT0, ops + Operands<ND>::KT0, KT<ND>::BYTES, &mb_late);
+                tc::bulk_g2s(base + M::QT0, ops + Operands<ND>::QT0, KT<ND>::BYTES, &mb_late);
+            }
+            split_product(COL_D, M::HI + M::ROWS, M::ST, M::STP, idn);
+            tc::commit(&mb_3);
+        }
+        __syncwarp();
+        if (M::LATE) warp_wait(&mb_late, 0, &s_gave_up);
+        const uint64_t dkt = tc::make_desc(base + M::KT0, KT<ND>::LBO, KT<ND>::SBO);
+        const uint64_t dqt = tc::make_desc(base + M::QT0, KT<ND>::LBO, KT<ND>::SBO);
+        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem, dkt, idn, true);
+        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem + 32, dkt, idn, false);
+        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem + 64, dqt, idn, false);
+        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem + 96, dqt, idn, false);
+        commit_elected(&mb_3);
+    }
+    warp_wait(&mb_3, 0, &s_gave_up);
+    tc::fence_after_sync();
+    {
+        uint32_t r[NC];
+        tmem_ld32(tq + COL_S + n0, r);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < NC; ++e) first[e] = fmaf(__uint_as_float(r[e]), ps.down, first[e]);
+        if (is_k) {
+            tmem_ld32(tq + COL_D + n0, r);
+            tc::tmem_wait_ld();
+        }
+        const float f = s_u[i] * d.out[i];
+#pragma unroll
+        for (int e = 0; e < NC; ++e) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(&own[e / 8])[e % 8 / 2];
+            const float2 y = unpack2(w, E());
+            const float o = e & 1 ? y.y : y.x;
+            if (is_k) {
+                const float us = __uint_as_float(r[e]) * (f * s_ds[n0 + e]);
+                kus = fmaf(o, us, kus);
+                first[e] += us;
+            } else {
+                qgq = fmaf(o, first[e], qgq);
+            }
+        }
+        O* dst = (is_k ? gk : gq) + go + i * gs + n0;
+        if (i < n) {
+#pragma unroll
+            for (int e = 0; e < NC; e += 8) {
+                if (n0 + e >= N) break;
+                if constexpr (sizeof(O) == 2) {
+                    *reinterpret_cast<uint4*>(dst + e) =
+                        make_uint4(pack_as<E>(mk2(first[e], first[e + 1])), pack_as<E>(mk2(first[e + 2], first[e + 3])),
+                                   pack_as<E>(mk2(first[e + 4], first[e + 5])), pack_as<E>(mk2(first[e + 6], first[e + 7])));
+                } else {
+                    *reinterpret_cast<float4*>(dst + e) = make_float4(first[e], first[e + 1], first[e + 2], first[e + 3]);
+                    *reinterpret_cast<float4*>(dst + e + 4) = make_float4(first[e + 4], first[e + 5], first[e + 6], first[e + 7]);
+                }
+            }
+        }
+        if (is_k) {
+            s_kz[part][i] = kz;
+        } else {
+            s_qgq[part][i] = qgq;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) kus += __shfl_xor_sync(0xffffffffu, kus, o);
+        if (lane == 0) s_kus[warp] = kus;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) {
+        double all = 0.0, us = 0.0;
+        for (int w = 0; w < NW; ++w) {
+            all += s_dot[w];
+            us += (double)s_kus[w];
+        }
+        // <S+, dS+> = e^{G_end} <S, dS+> + sum_i e^{G_end - G_i} u_i.(dS+^T k_i)
+        all = all * (double)d.all + us;
+        double r[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            double qg = 0.0;
+            float kzs = 0.f, gb = 0.f;
+            for (int p = 0; p < NPART; ++p) {
+                qg += (double)s_qgq[p][t];
+                kzs += s_kz[p][t];
+                gb += s_gb[p][t];
+            }
+            r[e] = qg - (double)d.beta[t] * (double)s_zv[t];
+            if (t < n) gbeta[(t0 + t) * sh.H + h] = s_zv[t] - d.in[t] * kzs - gb;
+        }
+        r[0] += r[1];
+        double tot = r[0];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double up = __shfl_down_sync(0xffffffffu, tot, o);
+            if (lane + o < 32) tot += up;
+        }
+        const double behind = tot - r[0];
+        if (2 * lane < n) gg[(t0 + 2 * lane) * sh.H + h] = (float)(behind + r[0] + all);
+        if (2 * lane + 1 < n) gg[(t0 + 2 * lane + 1) * sh.H + h] = (float)(behind + r[1] + all);
+        if (s_gave_up) {
+            if (lane == 0) {
+                tc::drain_mmas(&mb_drain, kDeltaWait);
+                tc::mbar_wait_bounded(&mb_ops, 0, kDeltaWait);
+                if (M::LATE) tc::mbar_wait_bounded(&mb_late, 0, kDeltaWait);
+                if (status) atomicOr(status, kStatusDelta);
+            }
+            __syncwarp();
+        }
+        tc::tmem_dealloc(tmem, COLS);
+    }
+}
+
 Shape shape(const DeltaArgs& a) {
     return Shape{(int)a.T, (int)a.H, (int)(a.H / a.KH), (int)a.N, (int)a.P, (int)((a.T + C - 1) / C)};
 }
@@ -1351,6 +1815,30 @@ cudaError_t back_scans_tc(const DeltaArgs& a, void* ws, float* states, float* af
         static_cast<const E*>(a.dout), image_t, operands, a.dh_final, a.lens, a.gh0, after, zs, shape(a), status_word());
     return cudaGetLastError();
 }
+template <typename E, typename O, int ND, int PD>
+cudaError_t grad_tc(const DeltaArgs& a, const unsigned char* image_t, const unsigned char* operands, const float* states,
+                    const float* after, const float* writes, const float* zs, void* gq, void* gk, cudaStream_t st) {
+    using M = GradSmem<ND, PD>;
+    const cudaError_t e = allow<delta_grad_tc<E, O, ND, PD>>(M::BYTES);
+    if (e != cudaSuccess) return e;
+    delta_grad_tc<E, O, ND, PD><<<(unsigned)chunk_count(a), M::NT, M::BYTES, st>>>(
+        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), static_cast<const E*>(a.dout),
+        a.g, a.beta, a.lens, a.scale, image_t, operands, states, after, writes, zs, static_cast<O*>(gq),
+        static_cast<O*>(gk), static_cast<E*>(a.gv), a.gg, a.gbeta, shape(a), status_word());
+    return cudaGetLastError();
+}
+template <typename E, typename O>
+cudaError_t grad_by_width(const DeltaArgs& a, void* ws, const float* states, const float* after, const float* writes,
+                          const float* zs, void* gq, void* gk, cudaStream_t st) {
+    const unsigned char* image_t = static_cast<const unsigned char*>(ws) + image_bytes(a);
+    const unsigned char* operands = image_t + image_bytes(a);
+    if (a.N <= 64)
+        return a.P <= 64 ? grad_tc<E, O, 64, 64>(a, image_t, operands, states, after, writes, zs, gq, gk, st)
+                         : grad_tc<E, O, 64, 128>(a, image_t, operands, states, after, writes, zs, gq, gk, st);
+    return a.P <= 64 ? grad_tc<E, O, 128, 64>(a, image_t, operands, states, after, writes, zs, gq, gk, st)
+                     : grad_tc<E, O, 128, 128>(a, image_t, operands, states, after, writes, zs, gq, gk, st);
+}
+
 template <typename E>
 cudaError_t back_scans_by_width(const DeltaArgs& a, void* ws, float* states, float* after, float* writes, float* zs,
                                 cudaStream_t st) {
@@ -1370,6 +1858,15 @@ cudaError_t launch_forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     return a.dtype == CSSD_BF16 ? forward_by_width<__nv_bfloat16>(a, ws, st) : forward_by_width<__half>(a, ws, st);
 }
 
+cudaError_t launch_grad_tc(const DeltaArgs& a, void* ws, const float* states, const float* after, const float* writes,
+                           const float* zs, void* gq, void* gk, cudaStream_t st) {
+    const bool shared = a.H != a.KH;
+    if (a.dtype == CSSD_BF16)
+        return shared ? grad_by_width<__nv_bfloat16, float>(a, ws, states, after, writes, zs, gq, gk, st)
+                      : grad_by_width<__nv_bfloat16, __nv_bfloat16>(a, ws, states, after, writes, zs, gq, gk, st);
+    return shared ? grad_by_width<__half, float>(a, ws, states, after, writes, zs, gq, gk, st)
+                  : grad_by_width<__half, __half>(a, ws, states, after, writes, zs, gq, gk, st);
+}
 size_t tc_back_bytes(const DeltaArgs& a) { return 2 * image_bytes(a) + operand_bytes(a, true); }
 cudaError_t launch_back_scans_tc(const DeltaArgs& a, void* ws, float* states, float* after, float* writes, float* zs,
                                  cudaStream_t st) {

@@ -202,6 +202,32 @@ __device__ __forceinline__ bool warp_wait(uint64_t* m, uint32_t parity, volatile
     return __all_sync(0xffffffffu, wait_or_give_up(m, parity, gave_up));
 }
 
+// e^{G_i - G_j} for i >= j as e[i] f[i / 16][j], a product over the start of
+// i's block of 16 tokens (so that a table of 256 exponentials serves a chunk):
+// exact to fp32 rounding while a block's decay, which f undoes, stays above
+// e^-40; `steep` is set where it does not.  `down` (may be null) multiplies f.
+// 256 threads.
+struct DecayTables {
+    float f[4][C], e[C];
+    int steep;  // zeroed by the caller, a barrier before
+};
+__device__ __forceinline__ void decay_tables(DecayTables& t, const Decays& d, const float* down, int tid) {
+    const int a = 16 * (tid / C), j = tid % C;
+    // G_a - G_j as a float and what its rounding leaves
+    const float at = d.hi[a] - d.hi[j], back = at - d.hi[a];
+    const float rest = ((d.hi[a] - (at - back)) - (d.hi[j] + back)) + (d.lo[a] - d.lo[j]);
+    t.f[tid / C][j] = j < a + 16 ? expf(at) * (1.f + rest) * (down ? down[j] : 1.f) : 0.f;
+    if (j / 16 == tid / C) {
+        t.e[j] = expf(-at) * (1.f - rest);
+        if (!(fabsf(at) < 40.f)) t.steep = 1;  // (a NaN or infinite sum too)
+    }
+}
+// The same directly (exp's own error is relative to a value that falls as
+// fast as its argument grows).
+__device__ __forceinline__ float steep_decay(const Decays& d, int i, int j) {
+    return __expf((d.hi[i] - d.hi[j]) + (d.lo[i] - d.lo[j]));
+}
+
 // What a chunk's prep leaves in the workspace, copied whole into shared memory
 // by the scans.  Per value head an image: [T; X] (the backward scan: [T^T;
 // X^T]) as a B operand of 128 rows (T's 64, then X's) by 64, hi then lo, and
@@ -218,7 +244,9 @@ struct Image {
     // in the second operand, of dO in the third.
     static constexpr int WK = 0, ZT = 64, ZX = 128, RZ = 192, DQ = 256;
     // exp(G_end); and what bounds the scan's operands (see delta_scan_tc).
-    static constexpr int ALL = 320, BND1 = 321, BND2 = 322, BND3 = 323, FLOATS = 324;
+    static constexpr int ALL = 320, BND1 = 321, BND2 = 322, BND3 = 323;
+    // Backward: the inverse scales of K's and Q's rows.
+    static constexpr int KD = 324, QD = 388, FLOATS = 452;
     static constexpr uint32_t BYTES = F + 4 * FLOATS;
     static constexpr uint32_t STRIDE = (BYTES + 255) / 256 * 256;
 };
