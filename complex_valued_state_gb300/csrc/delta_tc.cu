@@ -461,13 +461,12 @@ __device__ __forceinline__ void store_split(const f2 (&y)[8], uint32_t hi, uint3
     uint32_t h[8], l[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float a, b, ra, rb;
+        float a, b;
         un2(y[i], a, b);
-        a = __uint_as_float(__float_as_uint(a) & 0xFFFFE000u);
-        b = __uint_as_float(__float_as_uint(b) & 0xFFFFE000u);
         h[i] = pack2(a, b);
-        un2(fma2(mk2(a, b), minus, y[i]), ra, rb);
-        l[i] = pack2(ra, rb);
+        const float2 f = halves(h[i]);
+        un2(fma2(mk2(f.x, f.y), minus, y[i]), a, b);
+        l[i] = pack2(a, b);
     }
     tmem_st8(hi, h);
     tmem_st8(lo, l);
@@ -1345,7 +1344,7 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
     __shared__ __align__(16) Decays d;
     __shared__ __align__(16) DecayTables tab;
     __shared__ __align__(16) float s_kd[C], s_qd[C], s_u[C], s_rows[2 * C], s_st[ND], s_ds[ND];
-    __shared__ float s_zv[C], s_gb[NPART][C], s_qgq[NPART][C], s_kz[NPART][C], s_top[NW], s_kus[NW], s_kqd[4];
+    __shared__ float s_zv[C], s_gb[NPART][C], s_qgq[NPART][C], s_kz[NPART][C], s_top[NW], s_kus[NW], s_kqd;
     __shared__ double s_dot[NW];
     __shared__ __align__(8) uint64_t mb_ops, mb_late, mb_1, mb_2, mb_3, mb_drain;
     __shared__ uint32_t s_tmem;
@@ -1385,89 +1384,84 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
         tc::mbar_arrive_expect_tx(&mb_ops, M::FIRST);
         tc::bulk_g2s(tc::smem_u32(smem + M::OPS), ops, M::FIRST, &mb_ops);
     }
+    // Z (with dV and z.v), U, dO: 8 rows a warp, all loads before the first use
+    const int rg = warp % 8, ti = 8 * rg + lane % 8, srow = 8 * warp + lane % 8;
+    const bool has_z = NW == 8 || warp < 8, has_u = NW == 8 || warp >= 8;  // dO goes with Z
+    float zx[NG][8], ux[NG][8], sx[NG][8];
+    uint4 dr[NG], vr[NG];
+    float bt = 0.f;
+    if (has_z) {
+        load_groups<NG>(zx, zs + (ci * C + ti) * P, lane, P, true);
+        const int64_t row = vo + ti * vs;
+#pragma unroll
+        for (int e = 0; e < NG; ++e) {
+            const int col = 8 * (lane / 8 + 4 * e);
+            const bool in = ti < n && col < P;
+            dr[e] = in ? *reinterpret_cast<const uint4*>(dout + row + col) : make_uint4(0, 0, 0, 0);
+            vr[e] = in ? *reinterpret_cast<const uint4*>(v + row + col) : make_uint4(0, 0, 0, 0);
+        }
+        if (ti < n) bt = beta[(t0 + ti) * sh.H + h];
+    }
+    if (has_u) load_groups<NG>(ux, writes + (ci * C + ti) * P, lane, P, true);
+    load_groups<NG>(sx, states + (ci * N + srow) * P, lane, P, srow < N);
     if (warp == NW - 1) chunk_decays(d, g + t0 * sh.H + h, beta + t0 * sh.H + h, sh.H, n, lane);
-    const float* fb = reinterpret_cast<const float*>(image_t + ci * Image::STRIDE + Image::F);
     if (tid < C) {
+        const float* fb = reinterpret_cast<const float*>(image_t + ci * Image::STRIDE + Image::F);
         s_kd[tid] = fb[Image::KD + tid];
         s_qd[tid] = fb[Image::QD + tid];
     }
-    // Z (with dV and z.v), U, dO: 8 rows a warp
-    for (int w = warp; w < 24; w += NW) {
-        const int what = w / 8, rg = w % 8, i = 8 * rg + lane % 8;
-        unsigned char* hi = smem + M::HI + (what == 0 ? 1 : what == 1 ? 2 : 0) * M::ROWS + rg * M::SBO;
-        if (what < 2) {
-            float x[NG][8];
-            load_groups<NG>(x, (what ? writes : zs) + (ci * C + i) * P, lane, P, true);
-            const float down = store_groups<NG>(x, hi, hi + 3 * M::ROWS, lane);
-            if (lane < 8) (what ? s_u[i] : s_rows[C + i]) = down;
-            if (what == 0) {
-                const float bt = i < n ? beta[(t0 + i) * sh.H + h] : 0.f;
-                float zv = 0.f;
+    unsigned char* hi = smem + M::HI + rg * M::SBO;
+    if (has_z) {
+        const float down = store_groups<NG>(zx, hi + M::ROWS, hi + 4 * M::ROWS, lane);
+        if (lane < 8) s_rows[C + ti] = down;
+        float zv = 0.f;
+        uint32_t m = 0;
 #pragma unroll
-                for (int e = 0; e < NG; ++e) {
-                    const int col = 8 * (lane / 8 + 4 * e);
-                    if (i < n && col < P) {
-                        const uint4 raw = *reinterpret_cast<const uint4*>(v + vo + i * vs + col);
-                        const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                        uint32_t out[4];
+        for (int e = 0; e < NG; ++e) {
+            const uint32_t in[4] = {vr[e].x, vr[e].y, vr[e].z, vr[e].w};
+            uint32_t out[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float2 y = unpack2(in[u], E());
-                            zv = fmaf(y.x, x[e][2 * u], fmaf(y.y, x[e][2 * u + 1], zv));
-                            out[u] = pack_as<E>(mk2(bt * x[e][2 * u], bt * x[e][2 * u + 1]));
-                        }
-                        *reinterpret_cast<uint4*>(gv + vo + i * vs + col) = make_uint4(out[0], out[1], out[2], out[3]);
-                    }
-                }
-                zv += __shfl_xor_sync(0xffffffffu, zv, 8);
-                zv += __shfl_xor_sync(0xffffffffu, zv, 16);
-                if (lane < 8) s_zv[i] = zv;
+            for (int u = 0; u < 4; ++u) {
+                const float2 y = unpack2(in[u], E());
+                zv = fmaf(y.x, zx[e][2 * u], fmaf(y.y, zx[e][2 * u + 1], zv));
+                out[u] = pack_as<E>(mk2(bt * zx[e][2 * u], bt * zx[e][2 * u + 1]));
             }
-        } else {
-            uint4 raw[NG];
-            uint32_t m = 0;
-#pragma unroll
-            for (int e = 0; e < NG; ++e) {
-                const int col = 8 * (lane / 8 + 4 * e);
-                raw[e] = i < n && col < P ? *reinterpret_cast<const uint4*>(dout + vo + i * vs + col) : make_uint4(0, 0, 0, 0);
-                m = __vmaxu2(m, __vmaxu2(absmax2(raw[e].x, raw[e].y), absmax2(raw[e].z, raw[e].w)));
-            }
-            const RowScale sc = row_scale(over_row(top_of<E>(m)));
-#pragma unroll
-            for (int e = 0; e < NG; ++e) {
-                const uint32_t in[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
-                uint32_t out[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float2 y = unpack2(in[u], E());
-                    out[u] = pack2(y.x * sc.up, y.y * sc.up);
-                }
-                const uint32_t at = (lane / 8 + 4 * e) * 128 + (lane % 8) * 16;
-                *reinterpret_cast<uint4*>(hi + at) = make_uint4(out[0], out[1], out[2], out[3]);
-                *reinterpret_cast<uint4*>(hi + 3 * M::ROWS + at) = make_uint4(0, 0, 0, 0);
-            }
-            if (lane < 8) s_rows[i] = sc.down;
+            const int col = 8 * (lane / 8 + 4 * e);
+            if (ti < n && col < P) *reinterpret_cast<uint4*>(gv + vo + ti * vs + col) = make_uint4(out[0], out[1], out[2], out[3]);
+            m = __vmaxu2(m, __vmaxu2(absmax2(dr[e].x, dr[e].y), absmax2(dr[e].z, dr[e].w)));
         }
+        zv += __shfl_xor_sync(0xffffffffu, zv, 8);
+        zv += __shfl_xor_sync(0xffffffffu, zv, 16);
+        const RowScale sc = row_scale(over_row(top_of<E>(m)));
+        if (lane < 8) {
+            s_zv[ti] = zv;
+            s_rows[ti] = sc.down;
+        }
+#pragma unroll
+        for (int e = 0; e < NG; ++e) {
+            const uint32_t in[4] = {dr[e].x, dr[e].y, dr[e].z, dr[e].w};
+            uint32_t out[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float2 y = unpack2(in[u], E());
+                out[u] = pack2(y.x * sc.up, y.y * sc.up);
+            }
+            const uint32_t at = (lane / 8 + 4 * e) * 128 + (lane % 8) * 16;
+            *reinterpret_cast<uint4*>(hi + at) = make_uint4(out[0], out[1], out[2], out[3]);
+            *reinterpret_cast<uint4*>(hi + 3 * M::ROWS + at) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (has_u) {
+        const float down = store_groups<NG>(ux, hi + 2 * M::ROWS, hi + 5 * M::ROWS, lane);
+        if (lane < 8) s_u[ti] = down;
     }
     // S into its operand; dS into registers for the same place later, and <S, dS>
     float ds[NG][8];
-    const int srow = 8 * warp + lane % 8;
     {
         static_assert(NW * 8 == ND, "a warp has 8 rows of the state");
-        float x[NG][8];
-        load_groups<NG>(x, states + (ci * N + srow) * P, lane, P, srow < N);
-        const float down = store_groups<NG>(x, smem + M::ST + warp * M::SBO, smem + M::ST + M::STP + warp * M::SBO, lane);
-        if (lane < 8) s_st[srow] = down;
         load_groups<NG>(ds, after + (ci * N + srow) * P, lane, P, srow < N);
-        float part = 0.f;
-#pragma unroll
-        for (int e = 0; e < NG; ++e)
-#pragma unroll
-            for (int u = 0; u < 8; ++u) part = fmaf(x[e][u], ds[e][u], part);
-        double dot = (double)part;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) s_dot[warp] = dot;
+        const float down = store_groups<NG>(sx, smem + M::ST + warp * M::SBO, smem + M::ST + M::STP + warp * M::SBO, lane);
+        if (lane < 8) s_st[srow] = down;
     }
     tc::fence_proxy_async();
     tc::fence_before_sync();
@@ -1498,94 +1492,134 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
         tc::commit(&mb_2);
     }
     __syncwarp();
-    if (tid < 256) decay_tables(tab, d, nullptr, tid);
+    if (tid < 256) decay_tables(tab, d, s_u, tid);  // (with U's scales, which go with them)
+    {
+        float part = 0.f;
+#pragma unroll
+        for (int e = 0; e < NG; ++e)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) part = fmaf(sx[e][u], ds[e][u], part);
+        double dot = (double)part;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) s_dot[warp] = dot;
+    }
     if (warp == NW - 1) {  // the largest of K's and Q's inverse scales
         float m = fmaxf(fmaxf(s_kd[lane], s_kd[lane + 32]), fmaxf(s_qd[lane], s_qd[lane + 32]));
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) s_kqd[0] = m;
+        if (lane == 0) s_kqd = m;
     }
     __syncthreads();
 
-    // ---- Pm and W
+    // ---- Pm and W: row i of Pm in the lanes of dQ, of W in those of dK
     const int quarter = warp % 4, part = warp / 4, row = 32 * quarter + lane, i = row % C, j0 = CJ * part;
-    const bool is_k = row >= C;
+    const bool is_k = quarter >= 2;
     const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16);
     float* mat = reinterpret_cast<float*>(smem + M::MAT);
     auto at = [](int r, int cc) { return r * C + (cc ^ (r & 31)); };  // rows and columns without bank conflicts
-    float pw[CJ];  // this thread's columns of Pm's row i, or of W's
+    const bool above = 32 * (quarter % 2) + 31 < j0;                  // every pair of this warp has i < j
+    warp_wait(&mb_1, 0, &s_gave_up);
+    tc::fence_after_sync();
     {
-        uint32_t du[CJ], kk[CJ];
-        warp_wait(&mb_1, 0, &s_gave_up);
-        tc::fence_after_sync();
-        if constexpr (CJ == 32) {
-            tmem_ld32(tq + COL_DU + j0, du);
-            if (is_k) tmem_ld32(tq + COL_KK + j0, kk);
-        } else {
-            tc::tmem_ld16(tq + COL_DU + j0, du);
-            if (is_k) tc::tmem_ld16(tq + COL_KK + j0, kk);
-        }
-        tc::tmem_wait_ld();
-        const float ri = s_rows[row] * (is_k ? 1.f : scale), ei = tab.e[i], kdi = s_kd[i];
         float top = 0.f, gb = 0.f;
+        if (!above) {
+            const float ri = s_rows[row] * (is_k ? 1.f : scale), re = ri * tab.e[i], nb = -d.beta[i];
+            const int last = is_k ? i - 1 : i;
+            const bool steep = tab.steep;
+#pragma unroll 1
+            for (int e = 0; e < CJ; e += 8) {
+                const int j = j0 + e;
+                uint32_t du[8], kk[8];
+                tc::tmem_ld8(tq + COL_DU + j, du);
+                if (is_k) tc::tmem_ld8(tq + COL_KK + j, kk);
+                tc::tmem_wait_ld();
+                float x[8];
+                if (!steep) {
 #pragma unroll
-        for (int e = 0; e < CJ; ++e) {
-            const int j = j0 + e;
-            const float m = tab.steep ? steep_decay(d, i, j) : ei * tab.f[i / 16][j];
-            const bool keep = is_k ? i > j : i >= j;
-            float x = keep ? __uint_as_float(du[e]) * (ri * s_u[j]) * m : 0.f;
-            if (is_k) {
-                gb = keep ? fmaf(x, __uint_as_float(kk[e]) * (kdi * s_kd[j]), gb) : gb;
-                x *= -d.beta[i];
+                    for (int u = 0; u < 8; u += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(tab.f[i / 16] + j + u);
+                        x[u] = __uint_as_float(du[u]) * (re * f.x), x[u + 1] = __uint_as_float(du[u + 1]) * (re * f.y);
+                        x[u + 2] = __uint_as_float(du[u + 2]) * (re * f.z), x[u + 3] = __uint_as_float(du[u + 3]) * (re * f.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) x[u] = __uint_as_float(du[u]) * (ri * s_u[j + u]) * steep_decay(d, i, j + u);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) x[u] = j + u <= last ? x[u] : 0.f;
+                if (is_k) {
+#pragma unroll
+                    for (int u = 0; u < 8; u += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(s_kd + j + u);
+                        // (by select: nothing above the diagonal may reach the sum)
+                        gb = fmaf(x[u], j + u <= last ? __uint_as_float(kk[u]) * f.x : 0.f, gb);
+                        gb = fmaf(x[u + 1], j + u + 1 <= last ? __uint_as_float(kk[u + 1]) * f.y : 0.f, gb);
+                        gb = fmaf(x[u + 2], j + u + 2 <= last ? __uint_as_float(kk[u + 2]) * f.z : 0.f, gb);
+                        gb = fmaf(x[u + 3], j + u + 3 <= last ? __uint_as_float(kk[u + 3]) * f.w : 0.f, gb);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        x[u] *= nb;
+                        if (j + u <= last) mat[at(j + u, i)] = x[u];
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (j + u <= last) mat[at(i, j + u)] = x[u];
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(x[u]));
             }
-            pw[e] = x;
-            top = fmaxf(top, fabsf(x));
         }
-        if (is_k) s_gb[part][i] = gb;
+        if (is_k) s_gb[part][i] = gb * s_kd[i];
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (lane == 0) s_top[warp] = top;
     }
     tc::fence_before_sync();
-    __syncthreads();  // (Q and K of the operands are read: mb_1)
+    __syncthreads();
     tc::fence_after_sync();
-#pragma unroll
-    for (int e = 0; e < CJ; ++e) {
-        const int j = j0 + e;
-        if (is_k) {
-            if (i > j) mat[at(j, i)] = pw[e];
-        } else if (i >= j) {
-            mat[at(i, j)] = pw[e];
-        }
-    }
     float top = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) top = fmaxf(top, s_top[w]);
-    const RowScale ps = row_scale(top * s_kqd[0]);
-    __syncthreads();
+    const RowScale ps = row_scale(top * s_kqd);
     // the A operand of the last product: [Pm 0; W + W^T  Pm^T], times the inverse scales of K and Q
-#pragma unroll
+#pragma unroll 1
     for (int e = 0; e < CJ; e += 16) {
-        f2 a[8], z[8];
+        const int j = j0 + e;
+        f2 a[8];
+        const f2 up = mk2(ps.up, ps.up);
+        if (is_k) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            float x[2], y[2];
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int j = j0 + e + 2 * u + w;
-                x[w] = pw[e + 2 * u + w];
-                y[w] = 0.f;
-                if (is_k) {
-                    if (j > i) x[w] = mat[at(i, j)];
-                    if (j >= i) y[w] = mat[at(j, i)] * (s_qd[j] * ps.up);
-                }
-                x[w] *= s_kd[j] * ps.up;
+            for (int u = 0; u < 8; ++u) {  // W below the diagonal lies at (column, row), above it at (row, column)
+                const int c0 = j + 2 * u, c1 = c0 + 1;
+                const float x0 = c0 == i ? 0.f : mat[c0 < i ? at(c0, i) : at(i, c0)];
+                const float x1 = c1 == i ? 0.f : mat[c1 < i ? at(c1, i) : at(i, c1)];
+                a[u] = mul2(mul2(mk2(x0, x1), *reinterpret_cast<const f2*>(s_kd + c0)), up);
             }
-            a[u] = mk2(x[0], x[1]);
-            z[u] = mk2(y[0], y[1]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int c0 = j + 2 * u, c1 = c0 + 1;
+                const float x0 = c0 <= i ? mat[at(i, c0)] : 0.f, x1 = c1 <= i ? mat[at(i, c1)] : 0.f;
+                a[u] = mul2(mul2(mk2(x0, x1), *reinterpret_cast<const f2*>(s_kd + c0)), up);
+            }
         }
-        store_split(a, tq + (j0 + e) / 2, tq + 32 + (j0 + e) / 2);
-        store_split(z, tq + 64 + (j0 + e) / 2, tq + 96 + (j0 + e) / 2);
+        store_split(a, tq + j / 2, tq + 32 + j / 2);
+        if (is_k) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int c0 = j + 2 * u, c1 = c0 + 1;
+                const float x0 = c0 >= i ? mat[at(c0, i)] : 0.f, x1 = c1 >= i ? mat[at(c1, i)] : 0.f;
+                a[u] = mul2(mul2(mk2(x0, x1), *reinterpret_cast<const f2*>(s_qd + c0)), up);
+            }
+            store_split(a, tq + 64 + j / 2, tq + 96 + j / 2);
+        } else {
+            const uint32_t zero[8] = {};
+            tmem_st8(tq + 64 + j / 2, zero);
+            tmem_st8(tq + 96 + j / 2, zero);
+        }
     }
     tc::tmem_wait_st();
 
@@ -1605,16 +1639,21 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
         tc::fence_after_sync();
         tmem_ld32(tq + COL_S + n0, r);
         tc::tmem_wait_ld();
-        const float f = s_rows[row] * (is_k ? 1.f : scale * d.in[i]), bg = -d.beta[i] * d.in[i];
+        const float f = s_rows[row] * (is_k ? 1.f : scale * d.in[i]), bg = is_k ? -d.beta[i] * d.in[i] : 1.f;
 #pragma unroll
-        for (int e = 0; e < NC; ++e) {
-            const float x = __uint_as_float(r[e]) * (f * s_st[n0 + e]);
-            if (is_k) {
-                const uint32_t w = reinterpret_cast<const uint32_t*>(&own[e / 8])[e % 8 / 2];
-                const float2 y = unpack2(w, E());
-                kz = fmaf(e & 1 ? y.y : y.x, x, kz);
+        for (int e = 0; e < NC; e += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(s_st + n0 + e);
+            first[e] = __uint_as_float(r[e]) * (f * w.x), first[e + 1] = __uint_as_float(r[e + 1]) * (f * w.y);
+            first[e + 2] = __uint_as_float(r[e + 2]) * (f * w.z), first[e + 3] = __uint_as_float(r[e + 3]) * (f * w.w);
+        }
+        if (is_k) {
+#pragma unroll
+            for (int e = 0; e < NC; e += 2) {
+                const float2 y = unpack2(reinterpret_cast<const uint32_t*>(&own[e / 8])[e % 8 / 2], E());
+                kz = fmaf(y.x, first[e], fmaf(y.y, first[e + 1], kz));
+                first[e] *= bg;
+                first[e + 1] *= bg;
             }
-            first[e] = is_k ? bg * x : x;
         }
         const float down = store_groups<NG>(ds, smem + M::ST + warp * M::SBO, smem + M::ST + M::STP + warp * M::SBO, lane);
         if (lane < 8) s_ds[srow] = down;
@@ -1655,18 +1694,26 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
             tmem_ld32(tq + COL_D + n0, r);
             tc::tmem_wait_ld();
         }
-        const float f = s_u[i] * d.out[i];
+        if (is_k) {
+            const float f = s_u[i] * d.out[i];
 #pragma unroll
-        for (int e = 0; e < NC; ++e) {
-            const uint32_t w = reinterpret_cast<const uint32_t*>(&own[e / 8])[e % 8 / 2];
-            const float2 y = unpack2(w, E());
-            const float o = e & 1 ? y.y : y.x;
-            if (is_k) {
-                const float us = __uint_as_float(r[e]) * (f * s_ds[n0 + e]);
-                kus = fmaf(o, us, kus);
-                first[e] += us;
-            } else {
-                qgq = fmaf(o, first[e], qgq);
+            for (int e = 0; e < NC; e += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(s_ds + n0 + e);
+                const float us[4] = {__uint_as_float(r[e]) * (f * w.x), __uint_as_float(r[e + 1]) * (f * w.y),
+                                     __uint_as_float(r[e + 2]) * (f * w.z), __uint_as_float(r[e + 3]) * (f * w.w)};
+#pragma unroll
+                for (int u = 0; u < 4; u += 2) {
+                    const float2 y = unpack2(reinterpret_cast<const uint32_t*>(&own[e / 8])[(e + u) % 8 / 2], E());
+                    kus = fmaf(y.x, us[u], fmaf(y.y, us[u + 1], kus));
+                    first[e + u] += us[u];
+                    first[e + u + 1] += us[u + 1];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < NC; e += 2) {
+                const float2 y = unpack2(reinterpret_cast<const uint32_t*>(&own[e / 8])[e % 8 / 2], E());
+                qgq = fmaf(y.x, first[e], fmaf(y.y, first[e + 1], qgq));
             }
         }
         O* dst = (is_k ? gk : gq) + go + i * gs + n0;

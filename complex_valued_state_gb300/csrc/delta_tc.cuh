@@ -5,11 +5,11 @@
 // Precision.  A 16-bit input row times its power of two is exact in half (11
 // bits hold bf16's 8 and half's own 11; what lies 2^-37 below the row's
 // largest value is dropped).  An intermediate is held as two halves, hi (the
-// value cut to 11 bits) and lo (the remainder): 21 bits and a rounding, 2^-22
-// of the row's largest value.  A product of an exact operand with a split one
-// takes two passes, of two split ones three (lo lo is left out, 2^-22), all
-// into one fp32 accumulator, so the states, which are float32 tensors of the
-// interface, keep fp32 accuracy.
+// value rounded to 11 bits) and lo (the remainder, at most 2^-12 of it, rounded
+// to 11 bits): 2^-24 of the row's largest value.  A product of an exact operand
+// with a split one takes two passes, of two split ones three (lo lo is left
+// out, 2^-24), all into one fp32 accumulator, so the states, which are float32
+// tensors of the interface, keep fp32 accuracy.
 #pragma once
 
 #include "delta_common.cuh"
@@ -32,18 +32,17 @@ __device__ __forceinline__ RowScale row_scale(float top) {
     return {__uint_as_float((uint32_t)(267 - e) << 23), __uint_as_float((uint32_t)(e - 13) << 23)};
 }
 
-// Two values (already scaled) as half pairs: element 0 in the low half.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-    const float h0 = __uint_as_float(__float_as_uint(x0) & 0xFFFFE000u);
-    const float h1 = __uint_as_float(__float_as_uint(x1) & 0xFFFFE000u);
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(h1), "f"(h0));
-    const float l0 = x0 - h0, l1 = x1 - h1;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(l1), "f"(l0));
-}
 __device__ __forceinline__ uint32_t pack2(float x0, float x1) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x1), "f"(x0));
     return r;
+}
+__device__ __forceinline__ float2 halves(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+// Two values (already scaled) as half pairs: element 0 in the low half.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    hi = pack2(x0, x1);
+    const float2 h = halves(hi);
+    lo = pack2(x0 - h.x, x1 - h.y);
 }
 
 // A pair of 16-bit inputs as floats.

@@ -10,6 +10,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -555,23 +556,53 @@ def born_attention(q, k, v, *, psi=None, stream=None):
     return psi
 
 
+
+# The functions below are called once a token or a layer, so what they do on
+# the host counts: one comparison chain a tensor, plain integers as pointers,
+# and the size structures kept (by their values).
+def _expect(t, name, dtype, shape, index):
+    """t is a dense tensor of this dtype and shape on CUDA device `index`; otherwise what is wrong is raised."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index \
+            and t.is_contiguous():
+        return
+    _check(t, name, dtype, shape, torch.device("cuda", index) if index >= 0 else torch.device("cpu"))
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _delta_dims(*sizes):
+    return ctypes.byref(DeltaDims(*sizes))
+
+
+def _stream_of(stream, index):
+    if index < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
 def _element_type(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _DTYPES:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    return _DTYPES[t.dtype]
+    return dt
 
 
-def _scratch(workspace, nbytes, dev, stream):
+def _scratch(workspace, nbytes, like, stream):
     """The caller's workspace checked, or one from torch's allocator that
     belongs to the call's stream."""
     if workspace is None:
         if nbytes == 0:
             return None, 0
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
-            return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
-    if workspace.device != dev or not workspace.is_contiguous():
+        if stream is None:
+            return torch.empty(nbytes, dtype=torch.uint8, device=like.device), nbytes
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=like.device), nbytes
+    if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return workspace, workspace.numel() * workspace.element_size()
 
@@ -579,28 +610,28 @@ def _scratch(workspace, nbytes, dev, stream):
 def _delta_inputs(q, k, v, g, beta, lead):
     """Shapes shared by the sequence and the single token (`lead` leading axes)."""
     dt = _element_type(q, "q")
-    if q.dim() != lead + 2 or not isinstance(v, torch.Tensor) or v.dim() != lead + 2:
+    qs = q.shape
+    if len(qs) != lead + 2 or not isinstance(v, torch.Tensor) or v.dim() != lead + 2:
         raise ValueError(f"q and v must have {lead + 2} axes")
-    dev, f32 = q.device, torch.float32
-    ax, KH, N = tuple(q.shape[:lead]), q.shape[-2], q.shape[-1]
-    H, P = v.shape[-2], v.shape[-1]
-    _check(q, "q", q.dtype, ax + (KH, N), dev)
-    _check(k, "k", q.dtype, ax + (KH, N), dev)
-    _check(v, "v", q.dtype, ax + (H, P), dev)
-    _check(g, "g", f32, ax + (H,), dev)
-    _check(beta, "beta", f32, ax + (H,), dev)
-    return dt, dev, ax, H, KH, N, P
+    index, dtype, ax = q.get_device(), q.dtype, qs[:lead]
+    H, P = v.shape[-2:]
+    _expect(q, "q", dtype, qs, index)
+    _expect(k, "k", dtype, qs, index)
+    _expect(v, "v", dtype, ax + (H, P), index)
+    _expect(g, "g", torch.float32, ax + (H,), index)
+    _expect(beta, "beta", torch.float32, ax + (H,), index)
+    return dt, index, ax, H, qs[-2], qs[-1], P
 
 
 def delta_workspace_bytes(batch: int, seqlen: int, nheads: int, kheads: int, dstate: int, headdim: int, dtype) -> int:
-    d = DeltaDims(batch, seqlen, nheads, kheads, dstate, headdim)
-    return int(load().cssd_delta_workspace_bytes(ctypes.byref(d), _DTYPES[dtype]))
+    return int(load().cssd_delta_workspace_bytes(_delta_dims(batch, seqlen, nheads, kheads, dstate, headdim),
+                                                 _DTYPES[dtype]))
 
 
 def delta_backward_workspace_bytes(batch: int, seqlen: int, nheads: int, kheads: int, dstate: int, headdim: int,
                                    dtype) -> int:
-    d = DeltaDims(batch, seqlen, nheads, kheads, dstate, headdim)
-    return int(load().cssd_delta_backward_workspace_bytes(ctypes.byref(d), _DTYPES[dtype]))
+    return int(load().cssd_delta_backward_workspace_bytes(_delta_dims(batch, seqlen, nheads, kheads, dstate, headdim),
+                                                          _DTYPES[dtype]))
 
 
 def delta_forward(q, k, v, g, beta, *, scale=None, h0=None, lens=None, o=None, h_final=None, want_state: bool = True,
@@ -614,26 +645,29 @@ def delta_forward(q, k, v, g, beta, *, scale=None, h0=None, lens=None, o=None, h
     1/sqrt(N)) multiplies the output.  `workspace` is an optional uint8 tensor
     of at least delta_workspace_bytes(...) bytes.
     """
-    lib = load()
-    dt, dev, (Bz, T), H, KH, N, P = _delta_inputs(q, k, v, g, beta, 2)
+    lib = _lib or load()
+    dt, index, (Bz, T), H, KH, N, P = _delta_inputs(q, k, v, g, beta, 2)
+    state = (Bz, H, N, P)
     if h0 is not None:
-        _check(h0, "h0", torch.float32, (Bz, H, N, P), dev)
+        _expect(h0, "h0", torch.float32, state, index)
     if lens is not None:
-        _check(lens, "lens", torch.int32, (Bz,), dev)
+        _expect(lens, "lens", torch.int32, (Bz,), index)
     if o is None:
         o = torch.empty_like(v)
-    _check(o, "o", q.dtype, (Bz, T, H, P), dev)
-    if h_final is None and want_state:
-        h_final = torch.empty((Bz, H, N, P), dtype=torch.float32, device=dev)
+    else:
+        _expect(o, "o", q.dtype, v.shape, index)
     if h_final is not None:
-        _check(h_final, "h_final", torch.float32, (Bz, H, N, P), dev)
-    d = DeltaDims(Bz, T, H, KH, N, P)
-    ws, nbytes = _scratch(workspace, int(lib.cssd_delta_workspace_bytes(ctypes.byref(d), dt)), dev, stream)
-    st = lib.cssd_delta_forward(ctypes.byref(d), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                ctypes.c_float(N ** -0.5 if scale is None else scale), _ptr(h0), _ptr(lens), _ptr(o),
-                                _ptr(h_final), _ptr(ws), ctypes.c_size_t(nbytes), _stream_handle(stream, dev))
-    if st != CSSD_OK:
-        raise CssdError(st, "cssd_delta_forward")
+        _expect(h_final, "h_final", torch.float32, state, index)
+    elif want_state:
+        h_final = torch.empty(state, dtype=torch.float32, device=q.device)
+    st = _stream_of(stream, index)
+    d = _delta_dims(Bz, T, H, KH, N, P)
+    ws, nbytes = _scratch(workspace, lib.cssd_delta_workspace_bytes(d, dt) if workspace is None else 0, q, stream)
+    r = lib.cssd_delta_forward(d, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                               N ** -0.5 if scale is None else scale, _opt(h0), _opt(lens), o.data_ptr(),
+                               _opt(h_final), _opt(ws), nbytes, st)
+    if r != CSSD_OK:
+        raise CssdError(r, "cssd_delta_forward")
     return o, h_final
 
 
@@ -646,31 +680,35 @@ def delta_backward(q, k, v, g, beta, do, *, scale=None, h0=None, dh_final=None, 
     float32 [Bz,H,N,P] that of the last state (zero when None).  `grads` may
     hold preallocated outputs under the same keys.
     """
-    lib = load()
-    dt, dev, (Bz, T), H, KH, N, P = _delta_inputs(q, k, v, g, beta, 2)
-    f32 = torch.float32
-    _check(do, "do", q.dtype, (Bz, T, H, P), dev)
-    for t, n in ((h0, "h0"), (dh_final, "dh_final")):
-        if t is not None:
-            _check(t, n, f32, (Bz, H, N, P), dev)
+    lib = _lib or load()
+    dt, index, (Bz, T), H, KH, N, P = _delta_inputs(q, k, v, g, beta, 2)
+    f32, state = torch.float32, (Bz, H, N, P)
+    _expect(do, "do", q.dtype, v.shape, index)
+    if h0 is not None:
+        _expect(h0, "h0", f32, state, index)
+    if dh_final is not None:
+        _expect(dh_final, "dh_final", f32, state, index)
     if lens is not None:
-        _check(lens, "lens", torch.int32, (Bz,), dev)
-    r = dict(grads or {})
-    shapes = {"gq": (q.shape, q.dtype), "gk": (q.shape, q.dtype), "gv": (v.shape, q.dtype), "gg": (g.shape, f32),
-              "gbeta": (g.shape, f32), "gh0": ((Bz, H, N, P), f32)}
-    for name, (shape, dtype) in shapes.items():
-        if name not in r:
-            r[name] = torch.empty(shape, dtype=dtype, device=dev)
-        _check(r[name], name, dtype, shape, dev)
-    d = DeltaDims(Bz, T, H, KH, N, P)
-    ws, nbytes = _scratch(workspace, int(lib.cssd_delta_backward_workspace_bytes(ctypes.byref(d), dt)), dev, stream)
-    st = lib.cssd_delta_backward(ctypes.byref(d), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                 ctypes.c_float(N ** -0.5 if scale is None else scale), _ptr(h0), _ptr(lens), _ptr(do),
-                                 _ptr(dh_final), _ptr(r["gq"]), _ptr(r["gk"]), _ptr(r["gv"]), _ptr(r["gg"]),
-                                 _ptr(r["gbeta"]), _ptr(r["gh0"]), _ptr(ws), ctypes.c_size_t(nbytes),
-                                 _stream_handle(stream, dev))
-    if st != CSSD_OK:
-        raise CssdError(st, "cssd_delta_backward")
+        _expect(lens, "lens", torch.int32, (Bz,), index)
+    r = dict(grads) if grads else {}
+    for name, like in (("gq", q), ("gk", q), ("gv", v), ("gg", g), ("gbeta", g)):
+        if name in r:
+            _expect(r[name], name, like.dtype, like.shape, index)
+        else:
+            r[name] = torch.empty_like(like)
+    if "gh0" in r:
+        _expect(r["gh0"], "gh0", f32, state, index)
+    else:
+        r["gh0"] = torch.empty(state, dtype=f32, device=q.device)
+    st = _stream_of(stream, index)
+    d = _delta_dims(Bz, T, H, KH, N, P)
+    ws, nbytes = _scratch(workspace, lib.cssd_delta_backward_workspace_bytes(d, dt) if workspace is None else 0, q, stream)
+    status = lib.cssd_delta_backward(d, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                     N ** -0.5 if scale is None else scale, _opt(h0), _opt(lens), do.data_ptr(),
+                                     _opt(dh_final), r["gq"].data_ptr(), r["gk"].data_ptr(), r["gv"].data_ptr(),
+                                     r["gg"].data_ptr(), r["gbeta"].data_ptr(), r["gh0"].data_ptr(), _opt(ws), nbytes, st)
+    if status != CSSD_OK:
+        raise CssdError(status, "cssd_delta_backward")
     return r
 
 
@@ -681,22 +719,23 @@ def delta_step(h, q, k, v, g, beta, *, scale=None, slots=None, o=None, stream=No
     [Bz,H]; slots int32 [Bz] names the state of each row (row b uses h[b] when
     None; a slot outside [0, nslots) leaves every state alone and gives o = 0).
     """
-    lib = load()
-    dt, dev, (Bz,), H, KH, N, P = _delta_inputs(q, k, v, g, beta, 1)
+    lib = _lib or load()
+    dt, index, (Bz,), H, KH, N, P = _delta_inputs(q, k, v, g, beta, 1)
     if not isinstance(h, torch.Tensor) or h.dim() != 4:
         raise ValueError("h must be a tensor [nslots, H, N, P]")
-    _check(h, "h", torch.float32, (h.shape[0], H, N, P), dev)
+    nslots = h.shape[0]
+    _expect(h, "h", torch.float32, (nslots, H, N, P), index)
     if slots is not None:
-        _check(slots, "slots", torch.int32, (Bz,), dev)
+        _expect(slots, "slots", torch.int32, (Bz,), index)
     if o is None:
         o = torch.empty_like(v)
-    _check(o, "o", q.dtype, (Bz, H, P), dev)
-    d = DeltaDims(Bz, 1, H, KH, N, P)
-    st = lib.cssd_delta_step(ctypes.byref(d), dt, _ptr(h), int(h.shape[0]), _ptr(slots), _ptr(q), _ptr(k), _ptr(v),
-                             _ptr(g), _ptr(beta), ctypes.c_float(N ** -0.5 if scale is None else scale), _ptr(o),
-                             _stream_handle(stream, dev))
-    if st != CSSD_OK:
-        raise CssdError(st, "cssd_delta_step")
+    else:
+        _expect(o, "o", q.dtype, v.shape, index)
+    r = lib.cssd_delta_step(_delta_dims(Bz, 1, H, KH, N, P), dt, h.data_ptr(), nslots, _opt(slots), q.data_ptr(),
+                            k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                            N ** -0.5 if scale is None else scale, o.data_ptr(), _stream_of(stream, index))
+    if r != CSSD_OK:
+        raise CssdError(r, "cssd_delta_step")
     return o
 
 
@@ -704,17 +743,20 @@ def _norm_inputs(x, weight, bias=None):
     xt = _element_type(x, "x")
     if x.dim() < 1:
         raise ValueError("x must have at least one axis")
-    D = x.shape[-1]
-    _check(x, "x", x.dtype, x.shape, x.device)
+    index, D = x.get_device(), x.shape[-1]
+    _expect(x, "x", x.dtype, x.shape, index)
     wt = xt
+    wdtype = x.dtype
+    first = True
     for t, n in ((weight, "weight"), (bias, "bias")):
         if t is None:
             continue
-        wt = _element_type(t, n)
-        if t.dtype not in (x.dtype, torch.float32):
-            raise TypeError(f"{n} must be {x.dtype} or float32, got {t.dtype}")
-        _check(t, n, t.dtype if weight is None else weight.dtype, (D,), x.device)
-    return xt, wt, x.numel() // D if D else 0, D
+        if first:
+            wt, wdtype, first = _element_type(t, n), t.dtype, False
+            if wdtype is not x.dtype and wdtype is not torch.float32:
+                raise TypeError(f"{n} must be {x.dtype} or float32, got {t.dtype}")
+        _expect(t, n, wdtype, (D,), index)
+    return xt, wt, x.numel() // D if D else 0, D, index
 
 
 def layernorm(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, stream=None):
@@ -724,17 +766,18 @@ def layernorm(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, stream=No
     x bfloat16, float16 or float32; weight and bias [D] of x's type or float32
     (both the same), either may be None.
     """
-    lib = load()
-    xt, wt, rows, D = _norm_inputs(x, weight, bias)
+    lib = _lib or load()
+    xt, wt, rows, D, index = _norm_inputs(x, weight, bias)
     if y is None:
         y = torch.empty_like(x)
-    _check(y, "y", x.dtype, x.shape, x.device)
+    else:
+        _expect(y, "y", x.dtype, x.shape, index)
     mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     rstd = torch.empty_like(mean)
-    st = lib.cssd_layernorm(rows, D, xt, wt, _ptr(x), _ptr(weight), _ptr(bias), ctypes.c_float(eps), _ptr(y),
-                            _ptr(mean), _ptr(rstd), _stream_handle(stream, x.device))
-    if st != CSSD_OK:
-        raise CssdError(st, "cssd_layernorm")
+    r = lib.cssd_layernorm(rows, D, xt, wt, x.data_ptr(), _opt(weight), _opt(bias), eps, y.data_ptr(), mean.data_ptr(),
+                           rstd.data_ptr(), _stream_of(stream, index))
+    if r != CSSD_OK:
+        raise CssdError(r, "cssd_layernorm")
     return y, mean, rstd
 
 
@@ -745,28 +788,30 @@ def layernorm_backward(dy, x, weight, mean, rstd, *, want_weight: bool = True, w
 
     mean and rstd are those layernorm returned for x.
     """
-    lib = load()
-    xt, wt, rows, D = _norm_inputs(x, weight)
-    dev = x.device
-    _check(dy, "dy", x.dtype, x.shape, dev)
-    _check(mean, "mean", torch.float32, x.shape[:-1], dev)
-    _check(rstd, "rstd", torch.float32, x.shape[:-1], dev)
-    r = dict(grads or {})
-    wdt = x.dtype if weight is None else weight.dtype
-    shapes = {"gx": (tuple(x.shape), x.dtype)}
-    if want_weight:
-        shapes["gweight"] = ((D,), wdt)
-    if want_bias:
-        shapes["gbias"] = ((D,), wdt)
-    for name, (shape, dtype) in shapes.items():
-        if name not in r:
-            r[name] = torch.empty(shape, dtype=dtype, device=dev)
-        _check(r[name], name, dtype, shape, dev)
-    ws, nbytes = _scratch(workspace, int(lib.cssd_layernorm_backward_workspace_bytes(rows, D)), dev, stream)
-    st = lib.cssd_layernorm_backward(rows, D, xt, wt, _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
-                                     _ptr(r["gx"]), _ptr(r.get("gweight")) if want_weight else None,
-                                     _ptr(r.get("gbias")) if want_bias else None, _ptr(ws), ctypes.c_size_t(nbytes),
-                                     _stream_handle(stream, dev))
-    if st != CSSD_OK:
-        raise CssdError(st, "cssd_layernorm_backward")
+    lib = _lib or load()
+    xt, wt, rows, D, index = _norm_inputs(x, weight)
+    _expect(dy, "dy", x.dtype, x.shape, index)
+    _expect(mean, "mean", torch.float32, x.shape[:-1], index)
+    _expect(rstd, "rstd", torch.float32, x.shape[:-1], index)
+    r = dict(grads) if grads else {}
+    if "gx" in r:
+        _expect(r["gx"], "gx", x.dtype, x.shape, index)
+    else:
+        r["gx"] = torch.empty_like(x)
+    wdtype = x.dtype if weight is None else weight.dtype
+    for name, wanted in (("gweight", want_weight), ("gbias", want_bias)):
+        if not wanted:
+            continue
+        if name in r:
+            _expect(r[name], name, wdtype, (D,), index)
+        else:
+            r[name] = torch.empty(D, dtype=wdtype, device=x.device)
+    st = _stream_of(stream, index)
+    ws, nbytes = _scratch(workspace, lib.cssd_layernorm_backward_workspace_bytes(rows, D) if workspace is None else 0, x,
+                          stream)
+    status = lib.cssd_layernorm_backward(rows, D, xt, wt, dy.data_ptr(), x.data_ptr(), _opt(weight), mean.data_ptr(),
+                                         rstd.data_ptr(), r["gx"].data_ptr(), _opt(r.get("gweight")) if want_weight else None,
+                                         _opt(r.get("gbias")) if want_bias else None, _opt(ws), nbytes, st)
+    if status != CSSD_OK:
+        raise CssdError(status, "cssd_layernorm_backward")
     return r
