@@ -396,6 +396,7 @@ constexpr int CW = 4 * PARTS;  // chain warps
 constexpr int OW = 4;          // output warps, one per lane quarter
 constexpr int ST = 32 * (CW + OW + 4);  // then two warps that load V, the MMA warp and the bulk loader
 constexpr int EP = C / PARTS;  // tokens of a row a chain thread has
+constexpr int EXACT = 4;       // chunks between exact bounds on the state (see the scales below)
 // Registers a thread of the chain, the outputs and the rest: 4 x 88 + 88 + 40
 // = 4 x 80 + 104 + 56 = 6 x 80, what the block starts with.
 template <int ND>
@@ -480,24 +481,25 @@ __device__ __forceinline__ void warp_done(uint64_t* m, int lane) {
     if (lane == 0) mbar_arrive(m);
 }
 
-// kk MMAs over the reduced dimension: A's columns 8 apart, B's descriptor
-// `step` bytes.
+// KK MMAs over the reduced dimension: A's columns 8 apart, B's descriptor STEP
+// bytes (its address field, in the low word, does not carry out).
 template <int KK, uint32_t STEP>
 __device__ __forceinline__ void chain(uint32_t d, uint32_t a, uint64_t bd, uint32_t id, bool first) {
+    const uint32_t lo = (uint32_t)bd, hi = (uint32_t)(bd >> 32);
 #pragma unroll
-    for (int i = 0; i < KK; ++i) mma_f16_ts(d, a + 8 * i, bd + (uint64_t)((i * STEP) >> 4), id, !(first && i == 0));
+    for (int i = 0; i < KK; ++i) mma_f16_ts(d, a + 8 * i, lo + ((i * STEP) >> 4), hi, id, !(first && i == 0));
 }
 
 // Scales of the operands made on the chain.  A half has 16 bits of exponent
 // range below the point where hi and lo together lose a bit of the row's
 // largest value, so a row's scale may come from a bound on it that is loose by
-// up to 2^16.  With E the exact largest value of a lane's state column, found
-// while R [T; X] runs, and V's,
+// up to 2^16.  With E the largest value of a lane's state column, exact every
+// fourth chunk (found while R [T; X] runs) and else the bound it was stored
+// with, and V's,
 //     |R|  <= max |v| + max_i(e^{G_i} |k_i|) sqrt(N) E
 //     |U'| <= max_i(|T_i|_1 e^{G_end - G_i}) |R|
 //     |S+| <= e^{G_end} E + 64 max |k_i U'_i|    (U' exact, found while K^T U' runs)
-// (E itself stands in for the bound that the state was stored with, in |R|) so
-// no reduction over a row waits on the chain: an exchange between the threads
+// so no reduction over a row waits on the chain: an exchange between the threads
 // of a row takes 290 cycles, and exact scales would want three a chunk.
 //
 // KEEP = false: outputs.  KEEP = true: the state entering each chunk and the
@@ -654,7 +656,7 @@ __global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ v, 
                 warp_done(&mb_r, lane);
                 // while R [T; X] runs: the exact largest value of S, the next chunk's V
                 const RowScale ws = row_scale(ff[Image::BND2] * rbound);
-                const float stop = row.of_all(top_of_pairs(s));
+                const float stop = c % EXACT == EXACT - 1 ? row.of_all(top_of_pairs(s)) : sbound;
                 if (c + 1 < nck && !read_v(c + 1)) break;
                 factors(Image::UW, rs.down * ws.up);
                 if (!warp_wait(&mb_u, ph, &s_gave_up)) break;
@@ -687,14 +689,12 @@ __global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ v, 
                 tc::fence_after_sync();
                 {
                     const f2 m = mk2(ws.down, ws.down), keep = mk2(all, all);
+                    uint32_t dr[NS];
 #pragma unroll
-                    for (int e = 0; e < NS; e += 16) {
-                        tc::tmem_ld16(tq + COL_D + k0 + e, raw);
-                        tc::tmem_wait_ld();
+                    for (int e = 0; e < NS; e += 16) tc::tmem_ld16(tq + COL_D + k0 + e, *reinterpret_cast<uint32_t(*)[16]>(dr + e));
+                    tc::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            s[e / 2 + i] = fma2(keep, s[e / 2 + i], mul2(raw2(raw[2 * i], raw[2 * i + 1]), m));
-                    }
+                    for (int i = 0; i < NS / 2; ++i) s[i] = fma2(keep, s[i], mul2(raw2(dr[2 * i], dr[2 * i + 1]), m));
                 }
                 warp_done(&mb_free[c & 1], lane);
                 if (c + 1 < nck) {
@@ -730,12 +730,12 @@ __global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ v, 
             if (lane == 0) mbar_arrive(&mb_vfree[slot]);
             return true;
         };
-        if (quarter < quarters && nck > 0 && find_top(0)) {
+        if (quarter < quarters && nck > 0 && find_top(0) && (nck == 1 || find_top(1))) {
             constexpr int OE = ND == 128 ? 8 : 16;  // columns at a time
             const int64_t os = (int64_t)sh.H * P;
             E* dst = KEEP ? nullptr : o + ((int64_t)b * sh.T * sh.H + h) * P + vc;
             for (int c = 0; c < nck; ++c) {
-                if (c + 1 < nck && !find_top(c + 1)) break;
+                if (c + 2 < nck && !find_top(c + 2)) break;  // (two ahead: the chain reads it a chunk early)
                 if constexpr (KEEP) continue;
                 unsigned char* stage = smem + (c & 1) * M::STAGE;
                 if (!warp_wait(&mb_full[c & 1], (c >> 1) & 1, &s_gave_up)) break;
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(ST, 1) delta_back_scan_tc(const E* __restrict_
                 tc::tmem_wait_st();
                 warp_done(&mb_r, lane);
                 // while W T runs: the exact largest value of dS
-                const float stop = row.of_all(top_of_pairs(s));
+                const float stop = j % EXACT == EXACT - 1 ? row.of_all(top_of_pairs(s)) : sbound;
                 factors(Image::ZT, ws.down);
                 if (!warp_wait(&mb_z, ph, &s_gave_up)) break;
                 tc::fence_after_sync();

@@ -13,6 +13,7 @@
 #pragma once
 
 #include "delta_common.cuh"
+#include "pairs.cuh"
 #include "tcgen05.cuh"
 
 namespace cssd {
@@ -68,13 +69,14 @@ __device__ __forceinline__ float top_of(uint32_t m) {
 // warp, one elected lane issuing, so that the operands stay warp-uniform (58
 // cycles an MMA when a single diverged lane issued them, against 34 the pipe
 // needs at N = 64).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t.reg .b64 b;\n\t"
         "elect.sync r|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
         : "memory");
 }
 // The elected lane's commit (the same lane: election picks one lane of a mask).
@@ -86,24 +88,6 @@ __device__ __forceinline__ void commit_elected(uint64_t* m) {
         : "memory");
 }
 
-// Two fp32 operations an instruction.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 mk2(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void un2(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 __device__ __forceinline__ f2 raw2(uint32_t a, uint32_t b) { return mk2(__uint_as_float(a), __uint_as_float(b)); }
 
 // Register shares of the warpgroups (multiples of 8; together at most what

@@ -17,6 +17,8 @@
 
 #include "cssd_internal.h"
 #include "delta_common.cuh"
+#include "pairs.cuh"
+#include "tcgen05.cuh"
 
 namespace cssd {
 namespace {
@@ -172,9 +174,173 @@ __global__ void __launch_bounds__(256) norm_stream(const E* x, const WT* __restr
 }
 
 // --------------------------------------------------------------- backward
-// A CTA's threads own the row's vectors (IT each) and walk R rows at a time,
-// so that 2 R IT loads a thread are in flight before a barrier; the sums of dw
-// and db stay in registers until the end.
+// One row's share of the sums (a: dy w, so sum a and sum a xh) and of the
+// column sums, for a vector of the row, two elements an instruction.
+// `r2` holds rstd twice, `mr2` -mean rstd.
+template <typename E>
+__device__ __forceinline__ void back_sums(const uint4& xr, const uint4& dr, f2 r2, f2 mr2, const f2* wv, f2& s1, f2& s2,
+                                          f2 (&gw)[Vec<E>::W / 2], f2 (&gb)[Vec<E>::W / 2]) {
+    float xf[Vec<E>::W], df[Vec<E>::W];
+    unpack<E>(xr, xf);
+    unpack<E>(dr, df);
+#pragma unroll
+    for (int u = 0; u < Vec<E>::W / 2; ++u) {
+        const f2 d = mk2(df[2 * u], df[2 * u + 1]);
+        const f2 xh = fma2(mk2(xf[2 * u], xf[2 * u + 1]), r2, mr2), a = mul2(d, wv[u]);
+        s1 = add2(s1, a);
+        s2 = fma2(a, xh, s2);
+        gw[u] = fma2(d, xh, gw[u]);
+        gb[u] = add2(gb[u], d);
+    }
+}
+// dx of the vector: `t1` and `t2` hold -rstd times the row's two means.
+template <typename E>
+__device__ __forceinline__ uint4 back_dx(const uint4& xr, const uint4& dr, f2 r2, f2 mr2, const f2* wv, f2 t1, f2 t2) {
+    float xf[Vec<E>::W], df[Vec<E>::W];
+    unpack<E>(xr, xf);
+    unpack<E>(dr, df);
+#pragma unroll
+    for (int u = 0; u < Vec<E>::W / 2; ++u) {
+        const f2 xh = fma2(mk2(xf[2 * u], xf[2 * u + 1]), r2, mr2);
+        const f2 a = mul2(mul2(mk2(df[2 * u], df[2 * u + 1]), wv[u]), r2);
+        un2(fma2(xh, t2, add2(a, t1)), xf[2 * u], xf[2 * u + 1]);
+    }
+    return pack<E>(xf);
+}
+
+// G warps a row, IT vectors a thread, rows of x and dy by bulk copies into a
+// ring in shared memory, kStages - 1 rows ahead: registers hold the column sums
+// alone, and the copies in flight (8 / G groups of warps times the ring) are
+// what keeps the memory busy.  The warps add up their column sums at the end.
+constexpr int kRowWarps = 8;
+constexpr int kStages = 4;
+constexpr long long kNormWait = 4000000000LL;  // ~2 s at 2 GHz
+
+template <int G>
+__device__ __forceinline__ void group_barrier(int group) {
+    if constexpr (G == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * G) : "memory");
+}
+
+template <typename E, typename WT, int IT, int G>
+__global__ void __launch_bounds__(32 * kRowWarps, 2)
+    norm_back_ring(const E* dy, const E* x, const WT* __restrict__ w, const float* __restrict__ mean,
+                   const float* __restrict__ rstd, E* gx, float* __restrict__ part, int64_t rows, int width, bool want_w,
+                   bool want_b, unsigned* status) {
+    constexpr int W = Vec<E>::W, NG = kRowWarps / G, TG = 32 * G;
+    extern __shared__ __align__(128) unsigned char ring[];  // [group][stage][x, dy][width], then the weights
+    __shared__ __align__(8) uint64_t full[NG][kStages];
+    __shared__ float red[2][kRowWarps][2];
+    __shared__ int s_gave_up;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, group = warp / G, gt = tid % TG, nv = width / W;
+    const uint32_t bytes = (uint32_t)width * sizeof(E);
+    unsigned char* mine = ring + (size_t)group * kStages * 2 * bytes;
+    float* sw = reinterpret_cast<float*>(ring + (size_t)NG * kStages * 2 * bytes);
+    for (int c = tid; c < width; c += 32 * kRowWarps) sw[c] = w ? to_f(w[c]) : 1.f;
+    if (tid == 0) {
+        s_gave_up = 0;
+        for (int i = 0; i < NG; ++i)
+            for (int j = 0; j < kStages; ++j) tc::mbar_init(&full[i][j], 1);
+        tc::mbar_fence_init();
+    }
+    __syncthreads();
+    f2 gw[IT][W / 2], gb[IT][W / 2];
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int u = 0; u < W / 2; ++u) gw[i][u] = gb[i][u] = 0;
+    const float inv = 1.f / (float)width;
+    const int64_t step = (int64_t)gridDim.x * NG, row0 = (int64_t)blockIdx.x * NG + group;
+    auto fetch = [&](int64_t k) {  // the group's k-th row
+        const int64_t row = row0 + k * step;
+        if (row >= rows) return;
+        const int st = (int)(k % kStages);
+        const uint32_t at = tc::smem_u32(mine) + st * 2 * bytes;
+        tc::mbar_arrive_expect_tx(&full[group][st], 2 * bytes);
+        tc::bulk_g2s(at, x + row * width, bytes, &full[group][st]);
+        tc::bulk_g2s(at + bytes, dy + row * width, bytes, &full[group][st]);
+    };
+    if (gt == 0)
+        for (int k = 0; k < kStages - 1; ++k) fetch(k);
+    int64_t k = 0;
+    for (int64_t row = row0; row < rows; row += step, ++k) {
+        const int st = (int)(k % kStages);
+        const float m = mean[row], rs = rstd[row];
+        // (a wait that gives up: the row's results are wrong and the status word says so)
+        if (!tc::mbar_wait_bounded(&full[group][st], (uint32_t)(k / kStages & 1), kNormWait)) s_gave_up = 1;
+        const uint4* xr = reinterpret_cast<const uint4*>(mine + st * 2 * bytes);
+        const uint4* dr = reinterpret_cast<const uint4*>(mine + st * 2 * bytes + bytes);
+        const f2 r2 = mk2(rs, rs), mr2 = mk2(-m * rs, -m * rs);
+        f2 p1 = 0, p2 = 0;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = gt + TG * i;
+            if (c < nv) back_sums<E>(xr[c], dr[c], r2, mr2, reinterpret_cast<const f2*>(sw + c * W), p1, p2, gw[i], gb[i]);
+        }
+        float s1 = sum2(p1), s2 = sum2(p2);
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        if constexpr (G > 1) {
+            float(*r)[2] = red[k & 1];
+            if (lane == 0) r[warp][0] = s1, r[warp][1] = s2;
+            group_barrier<G>(group);
+            s1 = s2 = 0.f;
+#pragma unroll
+            for (int e = 0; e < G; ++e) s1 += r[group * G + e][0], s2 += r[group * G + e][1];
+        } else {
+            __syncwarp();
+        }
+        // every thread of the group is past the row before: its stage is free
+        if (gt == 0) fetch(k + kStages - 1);
+        const float t1 = -rs * s1 * inv, t2 = -rs * s2 * inv;
+        uint4* gp = reinterpret_cast<uint4*>(gx + row * width);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = gt + TG * i;
+            if (c < nv)
+                __stcs(gp + c, back_dx<E>(xr[c], dr[c], r2, mr2, reinterpret_cast<const f2*>(sw + c * W), mk2(t1, t1), mk2(t2, t2)));
+        }
+    }
+    if (gt == 0 && s_gave_up)  // no copy may land in shared memory that is no longer this CTA's
+        for (int64_t e = k > kStages ? k - kStages : 0; e < k; ++e)
+            tc::mbar_wait_bounded(&full[group][e % kStages], (uint32_t)(e / kStages & 1), kNormWait);
+    // the groups' column sums, one after another (the copies have all been waited for)
+    __syncthreads();
+    float* sum = reinterpret_cast<float*>(ring);
+    float* pw = part + (int64_t)blockIdx.x * 2 * width;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        for (int e = 0; e < NG; ++e) {
+            if (group == e)
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+#pragma unroll
+                    for (int u = 0; u < W; u += 2) {
+                        float v[2];
+                        un2(which ? gb[i][u / 2] : gw[i][u / 2], v[0], v[1]);
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            float* at = sum + ((u + z) * IT + i) * TG + gt;  // (threads side by side)
+                            *at = (e ? *at : 0.f) + v[z];
+                        }
+                    }
+            __syncthreads();
+        }
+        if (which ? want_b : want_w)
+            for (int c = tid; c < width; c += 32 * kRowWarps) {
+                const int v = c / W, u = c % W;
+                pw[which * width + c] = sum[(u * IT + v / TG) * TG + v % TG];
+            }
+        __syncthreads();
+    }
+    if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusNorm);
+}
+
+// Wide rows: a CTA's threads own the row's vectors (IT each) and walk R rows
+// at a time, so that 2 R IT loads a thread are in flight before a barrier; the
+// sums of dw and db stay in registers until the end.
 template <typename E, typename WT, int IT, int R, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_back_rows(const E* dy, const E* x,
                                                        const WT* __restrict__ w, const float* __restrict__ mean,
@@ -184,13 +350,16 @@ __global__ void __launch_bounds__(MAXT) norm_back_rows(const E* dy, const E* x,
     constexpr int W = Vec<E>::W;
     __shared__ float red[2][MAXT / 32][2 * R];
     const int tid = threadIdx.x, nt = blockDim.x, nw = nt / 32, nv = width / W;
-    float gw[IT][W], gb[IT][W], wv[IT][W];
+    f2 gw[IT][W / 2], gb[IT][W / 2], wv[IT][W / 2];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int c = tid + nt * i;
+        float f[W];
 #pragma unroll
-        for (int u = 0; u < W; ++u) gw[i][u] = gb[i][u] = 0.f, wv[i][u] = 0.f;
-        if (c < nv) load_w<WT, W>(w, (int64_t)c * W, 1.f, wv[i]);
+        for (int u = 0; u < W; ++u) f[u] = 0.f;
+        if (c < nv) load_w<WT, W>(w, (int64_t)c * W, 1.f, f);
+#pragma unroll
+        for (int u = 0; u < W / 2; ++u) gw[i][u] = gb[i][u] = 0, wv[i][u] = mk2(f[2 * u], f[2 * u + 1]);
     }
     const float inv = 1.f / (float)width;
     int flip = 0;
@@ -213,21 +382,13 @@ __global__ void __launch_bounds__(MAXT) norm_back_rows(const E* dy, const E* x,
         float s[2 * R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            s[2 * r] = s[2 * r + 1] = 0.f;
+            f2 p1 = 0, p2 = 0;
+            const f2 r2 = mk2(rs[r], rs[r]), mr2 = mk2(-m[r] * rs[r], -m[r] * rs[r]);
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                float xf[W], df[W];
-                unpack<E>(xr[r][i], xf);
-                unpack<E>(dr[r][i], df);
-#pragma unroll
-                for (int u = 0; u < W; ++u) {
-                    const float xh = (xf[u] - m[r]) * rs[r], a = df[u] * wv[i][u];
-                    s[2 * r] += a;
-                    s[2 * r + 1] = fmaf(a, xh, s[2 * r + 1]);
-                    gw[i][u] = fmaf(df[u], xh, gw[i][u]);
-                    gb[i][u] += df[u];
-                }
-            }
+            for (int i = 0; i < IT; ++i)
+                if (tid + nt * i < nv) back_sums<E>(xr[r][i], dr[r][i], r2, mr2, wv[i], p1, p2, gw[i], gb[i]);
+            s[2 * r] = sum2(p1);
+            s[2 * r + 1] = sum2(p2);
         }
 #pragma unroll
         for (int e = 0; e < 2 * R; ++e) {
@@ -244,19 +405,14 @@ __global__ void __launch_bounds__(MAXT) norm_back_rows(const E* dy, const E* x,
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (r0 + r >= rows) break;
+            const f2 r2 = mk2(rs[r], rs[r]), mr2 = mk2(-m[r] * rs[r], -m[r] * rs[r]);
+            const float t1 = -rs[r] * s[2 * r], t2 = -rs[r] * s[2 * r + 1];
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int c = tid + nt * i;
-                if (c >= nv) continue;
-                float xf[W], df[W];
-                unpack<E>(xr[r][i], xf);
-                unpack<E>(dr[r][i], df);
-#pragma unroll
-                for (int u = 0; u < W; ++u) {
-                    const float xh = (xf[u] - m[r]) * rs[r];
-                    xf[u] = rs[r] * (df[u] * wv[i][u] - s[2 * r] - xh * s[2 * r + 1]);
-                }
-                __stcs(reinterpret_cast<uint4*>(gx + (r0 + r) * width) + c, pack<E>(xf));
+                if (c < nv)
+                    __stcs(reinterpret_cast<uint4*>(gx + (r0 + r) * width) + c,
+                           back_dx<E>(xr[r][i], dr[r][i], r2, mr2, wv[i], mk2(t1, t1), mk2(t2, t2)));
             }
         }
     }
@@ -266,9 +422,12 @@ __global__ void __launch_bounds__(MAXT) norm_back_rows(const E* dy, const E* x,
         const int c = tid + nt * i;
         if (c >= nv) continue;
 #pragma unroll
-        for (int u = 0; u < W; ++u) {
-            if (want_w) pw[c * W + u] = gw[i][u];
-            if (want_b) pw[width + c * W + u] = gb[i][u];
+        for (int u = 0; u < W; u += 2) {
+            float v0, v1;
+            un2(gw[i][u / 2], v0, v1);
+            if (want_w) pw[c * W + u] = v0, pw[c * W + u + 1] = v1;
+            un2(gb[i][u / 2], v0, v1);
+            if (want_b) pw[width + c * W + u] = v0, pw[width + c * W + u + 1] = v1;
         }
     }
 }
@@ -325,30 +484,28 @@ __global__ void __launch_bounds__(256) norm_back_cols(const E* dy, const E* x,
     }
 }
 
-// part [n][2][width] -> gweight, gbias: 32 columns x 8 lanes over n, in a
+// part [n][2][width] -> gweight, gbias: 32 columns x 32 lanes over n, in a
 // fixed order.
 template <typename WT>
-__global__ void __launch_bounds__(256) norm_back_join(const float* __restrict__ part, int n, int64_t width,
-                                                      WT* __restrict__ gw, WT* __restrict__ gb) {
-    __shared__ float red[8][33];
+__global__ void __launch_bounds__(1024) norm_back_join(const float* __restrict__ part, int n, int64_t width,
+                                                       WT* __restrict__ gw, WT* __restrict__ gb) {
+    __shared__ float red[32][33];
     WT* out = blockIdx.y ? gb : gw;
     if (!out) return;
     const int lx = threadIdx.x % 32, ly = threadIdx.x / 32;
     const int64_t c = (int64_t)blockIdx.x * 32 + lx;
     float s = 0.f;
     if (c < width)
-#pragma unroll 4
-        for (int i = ly; i < n; i += 8) s += part[((int64_t)i * 2 + blockIdx.y) * width + c];
+#pragma unroll 8
+        for (int i = ly; i < n; i += 32) s += part[((int64_t)i * 2 + blockIdx.y) * width + c];
     red[ly][lx] = s;
     __syncthreads();
-    if (ly == 0 && c < width) {
-        s = 0.f;
-        for (int i = 0; i < 8; ++i) s += red[i][lx];
-        out[c] = from_f<WT>(s);
-    }
+    s = warp_sum(red[lx][ly]);  // column ly, over the lanes
+    const int64_t oc = (int64_t)blockIdx.x * 32 + ly;
+    if (lx == 0 && oc < width) out[oc] = from_f<WT>(s);
 }
 
-constexpr int kBackGrid = 304;  // row CTAs of the backward: two an SM (152 SMs)
+constexpr int kBackGrid = 304;  // CTAs of the backward: two an SM (152 SMs)
 
 template <typename E>
 bool vectors_fit(int64_t width, int64_t most) {
@@ -380,9 +537,9 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+// Partial column sums the backward's kernels may leave (each has a row at least).
 int back_groups(int64_t rows) {
-    const int64_t want = (rows + 3) / 4;
-    return (int)(want < kBackGrid ? want : kBackGrid);
+    return (int)(rows < kBackGrid ? rows : kBackGrid);
 }
 
 template <typename E, typename WT>
@@ -392,21 +549,53 @@ cudaError_t norm_bwd(const NormArgs& a, void* ws, cudaStream_t st) {
     const WT* w = static_cast<const WT*>(a.weight);
     E* gx = static_cast<E*>(a.gx);
     float2* sums = static_cast<float2*>(ws);
-    const int n = back_groups(a.rows);
+    int n = back_groups(a.rows);
     float* part = reinterpret_cast<float*>(sums + a.rows);
     const bool ww = a.gweight, wb = a.gbias;
     if (vectors_fit<E>(a.width, 2048)) {
         const int nv = (int)(a.width / Vec<E>::W);
-        auto go = [&](auto* kernel, int it) {
+        auto go = [&](auto* kernel, int it, int at_once) {
+            const int64_t want = (a.rows + at_once - 1) / at_once;
+            n = (int)(want < kBackGrid ? want : kBackGrid);
             const int nt = ((nv + it - 1) / it + 31) / 32 * 32;
             kernel<<<n, nt, 0, st>>>(dy, x, w, a.mean, a.rstd, gx, part, a.rows, (int)a.width, ww, wb);
         };
-        if (nv <= 256)
-            go(norm_back_rows<E, WT, 1, 4, 256>, 1);
+        // the ring's size: two tensors' rows a stage; the column sums go over it at the end
+        auto with_ring = [&](auto g, auto it) {
+            constexpr int G = decltype(g)::value, IT = decltype(it)::value, NG = kRowWarps / G;
+            const size_t bytes = (size_t)NG * kStages * 2 * a.width * sizeof(E) + (size_t)a.width * 4;
+            const size_t sums = sizeof(float) * 32 * G * IT * Vec<E>::W;
+            const size_t smem = bytes > sums ? bytes : sums;
+            const int64_t want = (a.rows + NG - 1) / NG;
+            n = (int)(want < kBackGrid ? want : kBackGrid);
+            auto* kernel = norm_back_ring<E, WT, IT, G>;
+            const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e == cudaSuccess)
+                kernel<<<n, 32 * kRowWarps, smem, st>>>(dy, x, w, a.mean, a.rstd, gx, part, a.rows, (int)a.width, ww, wb,
+                                                        status_word());
+            return e;
+        };
+        auto by_vectors = [&](auto g) {
+            const int it = (nv + 32 * decltype(g)::value - 1) / (32 * decltype(g)::value);
+            if (it <= 1) return with_ring(g, std::integral_constant<int, 1>());
+            if (it <= 2) return with_ring(g, std::integral_constant<int, 2>());
+            return with_ring(g, std::integral_constant<int, 3>());
+        };
+        cudaError_t e = cudaSuccess;
+        if (nv <= 96)
+            e = by_vectors(std::integral_constant<int, 1>());
+        else if (nv <= 192)
+            e = by_vectors(std::integral_constant<int, 2>());
+        else if (nv <= 384)
+            e = by_vectors(std::integral_constant<int, 4>());
+        else if (nv <= 768)
+            e = by_vectors(std::integral_constant<int, 8>());
         else if (nv <= 1024)
-            go(norm_back_rows<E, WT, 2, 2, 512>, 2);
+            go(norm_back_rows<E, WT, 2, 2, 512>, 2, 2);
         else
-            go(norm_back_rows<E, WT, 2, 1, 1024>, 2);
+            go(norm_back_rows<E, WT, 2, 1, 1024>, 2, 1);
+        if (e != cudaSuccess) return e;
     } else {
         norm_back_sums<E, WT><<<(unsigned)(a.rows < 8192 ? a.rows : 8192), 256, 0, st>>>(dy, x, w, a.mean, a.rstd, sums,
                                                                                         a.rows, a.width);
@@ -415,7 +604,7 @@ cudaError_t norm_bwd(const NormArgs& a, void* ws, cudaStream_t st) {
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!ww && !wb)) return e;
-    norm_back_join<WT><<<dim3((unsigned)((a.width + 31) / 32), 2), 256, 0, st>>>(
+    norm_back_join<WT><<<dim3((unsigned)((a.width + 31) / 32), 2), 1024, 0, st>>>(
         part, n, a.width, static_cast<WT*>(a.gweight), static_cast<WT*>(a.gbias));
     return cudaGetLastError();
 }
