@@ -88,13 +88,11 @@ constexpr int LT = C + 4;    // row stride of the fp32 matrices
 template <int ND, bool BACK>
 struct PrepSmem {
     // The operands of K and Q; once they are read, A (then T) and P (then X)
-    // lie over them, and over those the image, when T and X are in registers.
-    // The backward, which reads T and X again for its second image, has the
-    // images behind them.
+    // lie over them, and over those the images, when T and X are in registers.
     static constexpr uint32_t OPS = BACK ? Operands<ND>::BWD : Operands<ND>::FWD;
-    static constexpr uint32_t A = 0, P = 4 * C * LT, W = 2 * P, IMG = BACK ? W : 0;
+    static constexpr uint32_t A = 0, P = 4 * C * LT, W = 2 * P;
     static constexpr uint32_t mx(uint32_t a, uint32_t b) { return a > b ? a : b; }
-    static constexpr uint32_t BYTES = mx(mx(OPS, W + 4 * 32 * 32), IMG + Image::STRIDE);
+    static constexpr uint32_t BYTES = mx(mx(OPS, W + 4 * 32 * 32), Image::STRIDE);
 };
 
 // 16 values of a row of the image (columns 16 part..), scaled and split; returns
@@ -135,7 +133,7 @@ __device__ __forceinline__ void put_scalars(float* ff, float all, float b1, floa
 
 // BACK: a second image for the backward scan, [T^T; X^T].
 template <typename E, int ND, bool BACK>
-__global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __restrict__ q, const E* __restrict__ k,
+__global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __restrict__ q, const E* __restrict__ k,
                                                        const float* __restrict__ g, const float* __restrict__ beta,
                                                        const int* __restrict__ lens, unsigned char* __restrict__ image,
                                                        unsigned char* __restrict__ image_t,
@@ -279,7 +277,7 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
             }
         }
     }
-    unsigned char* img = smem + M::IMG;
+    unsigned char* img = smem;
     float* ff = reinterpret_cast<float*>(img + Image::F);
     auto write_out = [&](unsigned char* to) {
         tc::fence_proxy_async();
@@ -313,11 +311,18 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
             tops[3] = fmaxf(fmaxf(fmaxf(tops[3], fabsf(x4.x)), fmaxf(fabsf(x4.y), fabsf(x4.z))), fabsf(x4.w));
         }
     }
+    float tt[BACK ? 16 : 1], xt[BACK ? 16 : 1];  // of the transposes, for the second image
+    if constexpr (BACK)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            tt[u] = sa[(16 * part + u) * LT + row];
+            xt[u] = sp[(16 * part + u) * LT + row];
+        }
     constexpr int NTOP = BACK ? 4 : 2;
 #pragma unroll
     for (int e = 0; e < NTOP; ++e) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) tops[e] = fmaxf(tops[e], __shfl_xor_sync(0xffffffffu, tops[e], o));
+        // (non-negative: the order of the bits; a NaN is the largest)
+        tops[e] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tops[e])));
         if (lane == 0) s_top[e][warp] = tops[e];
     }
     __syncthreads();
@@ -347,15 +352,10 @@ __global__ void __launch_bounds__(PT, BACK ? 2 : 4) delta_prep_tc(const E* __res
     }
     write_out(image);
     if constexpr (BACK) {
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            te[u] = sa[(16 * part + u) * LT + row];
-            xe[u] = sp[(16 * part + u) * LT + row];
-        }
+        __syncthreads();  // (the first is copied out)
         ts = row_scale(tops[2]), xs = row_scale(tops[3]);
-        s_sum[part][row] = image_row(img, row, part, te, ts.up);
-        s_sumx[part][row] = image_row(img, C + row, part, xe, xs.up);
+        s_sum[part][row] = image_row(img, row, part, tt, ts.up);
+        s_sumx[part][row] = image_row(img, C + row, part, xt, xs.up);
         __syncthreads();
         if (tid < C) {
             const float kd = s_down[tid], qd = s_down[C + tid], fi = d.in[tid];
@@ -502,25 +502,55 @@ __device__ __forceinline__ void chain(uint32_t d, uint32_t a, uint64_t bd, uint3
 // so no reduction over a row waits on the chain: an exchange between the threads
 // of a row takes 290 cycles, and exact scales would want three a chunk.
 //
+// What a scan's warps share beside its buffers (behind them in dynamic shared
+// memory).
+struct ScanShared {
+    uint64_t full[2], free[2], ks, r, u, w, d, s, o, read, row[4], drain, vfull[NV], vtop[NV], vfree[NV];
+    float top[2][PARTS * 128], sdown[2][128], rdown[2][128], vmax[NV][128];
+    uint32_t tmem;
+    int gave_up;
+};
+
+template <typename E>
+struct ScanArgs {
+    const E* v;
+    const unsigned char* image;
+    const unsigned char* operands;
+    const float* h0;
+    E* o;
+    float* h_final;
+    float* states;
+    float* writes;
+};
+
 // KEEP = false: outputs.  KEEP = true: the state entering each chunk and the
 // writes U for the gradients, no outputs.
 template <typename E, int ND, bool KEEP>
-__global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ v, const unsigned char* __restrict__ image,
-                                                       const unsigned char* __restrict__ operands, const float* h0,
-                                                       const int* __restrict__ lens,
-                                                       E* __restrict__ o, float* h_final, float* __restrict__ states,
-                                                       float* __restrict__ writes, Shape sh, unsigned* status) {
+__device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const int* __restrict__ lens, const Shape& sh,
+                                          unsigned* status, unsigned char* smem) {
+    const E* __restrict__ v = g.v;
+    const unsigned char* __restrict__ image = g.image;
+    const unsigned char* __restrict__ operands = g.operands;
+    const float* h0 = g.h0;
+    E* __restrict__ o = g.o;
+    float* h_final = g.h_final;
+    float* __restrict__ states = g.states;
+    float* __restrict__ writes = g.writes;
     using M = ScanSmem<ND>;
     constexpr int NS = ND / PARTS;  // state elements a chain thread holds
-    extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(8) uint64_t mb_full[2], mb_free[2], mb_ks, mb_r, mb_u, mb_w, mb_d, mb_s, mb_o, mb_read, mb_row[4],
-        mb_drain;
-    __shared__ __align__(8) uint64_t mb_vfull[NV], mb_vtop[NV], mb_vfree[NV];
-    __shared__ float s_top[2][PARTS * 128], s_sdown[2][128], s_rdown[2][128], s_vtop[NV][128];
-    __shared__ uint32_t s_tmem;
-    __shared__ int s_gave_up;
+    ScanShared& z = *reinterpret_cast<ScanShared*>(smem + M::BYTES);
+    auto &mb_full = z.full, &mb_free = z.free;
+    auto &mb_ks = z.ks, &mb_r = z.r, &mb_u = z.u, &mb_w = z.w, &mb_d = z.d, &mb_s = z.s, &mb_o = z.o, &mb_read = z.read;
+    auto& mb_row = z.row;
+    auto& mb_drain = z.drain;
+    auto &mb_vfull = z.vfull, &mb_vtop = z.vtop, &mb_vfree = z.vfree;
+    auto& s_top = z.top;
+    auto &s_sdown = z.sdown, &s_rdown = z.rdown;
+    auto& s_vtop = z.vmax;
+    auto& s_tmem = z.tmem;
+    auto& s_gave_up = z.gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int bh = blockIdx.x, b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
+    const int b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
     const int len = row_len(lens, b, sh.T), nck = (len + C - 1) / C;
     const int quarters = (P + 31) / 32;
     if (warp == WMMA) {
@@ -877,6 +907,13 @@ __global__ void __launch_bounds__(ST, 1) delta_scan_tc(const E* __restrict__ v, 
     if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusDelta);
 }
 
+template <typename E, int ND>
+__global__ void __launch_bounds__(ST, 1) delta_scan_tc(ScanArgs<E> g, const int* __restrict__ lens, Shape sh,
+                                                       unsigned* status) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    scan_body<E, ND, false>(g, blockIdx.x, lens, sh, status, smem);
+}
+
 // --------------------------------------------------------------- backward scan
 // The same walk from the last chunk, with dS in the state's place:
 //     W^T  = (e^{G_end - G} K dS)^T           A = dS^T, B = K
@@ -898,26 +935,50 @@ constexpr uint32_t COL_S = 0, COL_R = 128, COL_DQ = 192, COL_KS = 256, COL_Z1 = 
                    COL_DX = 448, COL_E = 384;
 }
 
+struct BackShared {
+    uint64_t full[2], free[2], ks, r, z, w, d, s, dx, dq, row[4], drain, vfull[NV], vfree[NV];
+    float top[2][PARTS * 128], dxdown[128], dqdown[128], dxtop[128], dqtop[128];
+    uint32_t tmem;
+    int gave_up;
+};
+
+template <typename E>
+struct BackArgs {
+    const E* dout;
+    const unsigned char* image;
+    const unsigned char* operands;
+    const float* dh;
+    float* gh0;
+    float* after;
+    float* zs;
+};
+
 template <typename E, int ND>
-__global__ void __launch_bounds__(ST, 1) delta_back_scan_tc(const E* __restrict__ dout,
-                                                            const unsigned char* __restrict__ image,
-                                                            const unsigned char* __restrict__ operands, const float* dh,
-                                                            const int* __restrict__ lens, float* gh0,
-                                                            float* __restrict__ after, float* __restrict__ zs, Shape sh,
-                                                            unsigned* status) {
+__device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, const int* __restrict__ lens, const Shape& sh,
+                                               unsigned* status, unsigned char* smem) {
+    const E* __restrict__ dout = g.dout;
+    const unsigned char* __restrict__ image = g.image;
+    const unsigned char* __restrict__ operands = g.operands;
+    const float* dh = g.dh;
+    float* gh0 = g.gh0;
+    float* __restrict__ after = g.after;
+    float* __restrict__ zs = g.zs;
     using M = BackSmem<ND>;
     using namespace back;
     constexpr uint32_t COL_S = back::COL_S, COL_R = back::COL_R, COL_KS = back::COL_KS, COL_D = back::COL_D;
     constexpr int NS = ND / PARTS;
-    extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(8) uint64_t mb_full[2], mb_free[2], mb_ks, mb_r, mb_z, mb_w, mb_d, mb_s, mb_dx, mb_dq, mb_row[4],
-        mb_drain;
-    __shared__ __align__(8) uint64_t mb_vfull[NV], mb_vfree[NV];
-    __shared__ float s_top[2][PARTS * 128], s_dxdown[128], s_dqdown[128], s_dxtop[128], s_dqtop[128];
-    __shared__ uint32_t s_tmem;
-    __shared__ int s_gave_up;
+    BackShared& y = *reinterpret_cast<BackShared*>(smem + M::BYTES);
+    auto &mb_full = y.full, &mb_free = y.free;
+    auto &mb_ks = y.ks, &mb_r = y.r, &mb_z = y.z, &mb_w = y.w, &mb_d = y.d, &mb_s = y.s, &mb_dx = y.dx, &mb_dq = y.dq;
+    auto& mb_row = y.row;
+    auto& mb_drain = y.drain;
+    auto &mb_vfull = y.vfull, &mb_vfree = y.vfree;
+    auto& s_top = y.top;
+    auto &s_dxdown = y.dxdown, &s_dqdown = y.dqdown, &s_dxtop = y.dxtop, &s_dqtop = y.dqtop;
+    auto& s_tmem = y.tmem;
+    auto& s_gave_up = y.gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int bh = blockIdx.x, b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
+    const int b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
     const int len = row_len(lens, b, sh.T), nck = (len + C - 1) / C;
     const int quarters = (P + 31) / 32;
     if (warp == WMMA) {
@@ -1258,6 +1319,19 @@ __global__ void __launch_bounds__(ST, 1) delta_back_scan_tc(const E* __restrict_
     tc::fence_after_sync();
     if (warp == WMMA) tc::tmem_dealloc(tmem, TMEM_COLS);
     if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusDelta);
+}
+
+// Both of the gradients' scans, which do not need one another: a CTA of each
+// per value head in one launch, so that up to 76 heads run both at once.
+template <typename E, int ND>
+__global__ void __launch_bounds__(ST, 1) delta_both_scans_tc(BackArgs<E> back, ScanArgs<E> fwd, const int* __restrict__ lens,
+                                                             Shape sh, unsigned* status) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const int heads = gridDim.x / 2;
+    if ((int)blockIdx.x < heads)
+        back_scan_body<E, ND>(back, blockIdx.x, lens, sh, status, smem);
+    else
+        scan_body<E, ND, true>(fwd, blockIdx.x - heads, lens, sh, status, smem);
 }
 
 // --------------------------------------------------------------- dQ, dK, dV, dg, dbeta
@@ -1827,24 +1901,17 @@ cudaError_t prep_tc(const DeltaArgs& a, unsigned char* image, unsigned char* ima
     return cudaGetLastError();
 }
 
-template <typename E, int ND, bool KEEP>
-cudaError_t scan_tc(const DeltaArgs& a, const unsigned char* image, const unsigned char* operands, float* states,
-                    float* writes, cudaStream_t st) {
-    using M = ScanSmem<ND>;
-    const cudaError_t e = allow<delta_scan_tc<E, ND, KEEP>>(M::BYTES);
-    if (e != cudaSuccess) return e;
-    delta_scan_tc<E, ND, KEEP><<<(unsigned)(a.Bz * a.H), ST, M::BYTES, st>>>(
-        static_cast<const E*>(a.v), image, operands, a.h0, a.lens, KEEP ? nullptr : static_cast<E*>(a.o),
-        KEEP ? nullptr : a.h_final, states, writes, shape(a), status_word());
-    return cudaGetLastError();
-}
-
 template <typename E, int ND>
 cudaError_t forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     unsigned char* image = static_cast<unsigned char*>(ws);
     unsigned char* operands = image + image_bytes(a);
-    const cudaError_t e = prep_tc<E, ND, false>(a, image, nullptr, operands, st);
-    return e != cudaSuccess ? e : scan_tc<E, ND, false>(a, image, operands, nullptr, nullptr, st);
+    cudaError_t e = prep_tc<E, ND, false>(a, image, nullptr, operands, st);
+    if (e != cudaSuccess) return e;
+    constexpr uint32_t smem = ScanSmem<ND>::BYTES + sizeof(ScanShared);
+    if ((e = allow<delta_scan_tc<E, ND>>(smem)) != cudaSuccess) return e;
+    const ScanArgs<E> g{static_cast<const E*>(a.v), image, operands, a.h0, static_cast<E*>(a.o), a.h_final, nullptr, nullptr};
+    delta_scan_tc<E, ND><<<(unsigned)(a.Bz * a.H), ST, smem, st>>>(g, a.lens, shape(a), status_word());
+    return cudaGetLastError();
 }
 
 template <typename E, int ND>
@@ -1855,11 +1922,12 @@ cudaError_t back_scans_tc(const DeltaArgs& a, void* ws, float* states, float* af
     unsigned char* operands = image_t + image_bytes(a);
     cudaError_t e = prep_tc<E, ND, true>(a, image, image_t, operands, st);
     if (e != cudaSuccess) return e;
-    if ((e = scan_tc<E, ND, true>(a, image, operands, states, writes, st)) != cudaSuccess) return e;
-    using M = BackSmem<ND>;
-    if ((e = allow<delta_back_scan_tc<E, ND>>(M::BYTES)) != cudaSuccess) return e;
-    delta_back_scan_tc<E, ND><<<(unsigned)(a.Bz * a.H), ST, M::BYTES, st>>>(
-        static_cast<const E*>(a.dout), image_t, operands, a.dh_final, a.lens, a.gh0, after, zs, shape(a), status_word());
+    constexpr uint32_t f = ScanSmem<ND>::BYTES + sizeof(ScanShared), r = BackSmem<ND>::BYTES + sizeof(BackShared);
+    constexpr uint32_t smem = f > r ? f : r;
+    if ((e = allow<delta_both_scans_tc<E, ND>>(smem)) != cudaSuccess) return e;
+    const ScanArgs<E> fwd{static_cast<const E*>(a.v), image, operands, a.h0, nullptr, nullptr, states, writes};
+    const BackArgs<E> back{static_cast<const E*>(a.dout), image_t, operands, a.dh_final, a.gh0, after, zs};
+    delta_both_scans_tc<E, ND><<<(unsigned)(2 * a.Bz * a.H), ST, smem, st>>>(back, fwd, a.lens, shape(a), status_word());
     return cudaGetLastError();
 }
 template <typename E, typename O, int ND, int PD>
