@@ -33,6 +33,7 @@ namespace {
 
 struct Shape {
     int T, H, G, N, P, nc;  // G: value heads per key head
+    int c0, c1;             // the chunks of this launch
 };
 
 // --------------------------------------------------------------- operands
@@ -152,11 +153,17 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int c = blockIdx.x % sh.nc, bh = blockIdx.x / sh.nc;
+    const int c = sh.c0 + blockIdx.x % (sh.c1 - sh.c0), bh = blockIdx.x / (sh.c1 - sh.c0);
     const int b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G;
     const int n = min(row_len(lens, b, sh.T) - c * C, C);
-    if (n <= 0) return;
-    const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C;
+    // A launch that overlaps the scan before it (see forward_tc) ends no sooner
+    // than that scan, so that what follows in the stream comes after both.
+    const bool last_block = blockIdx.x == gridDim.x - 1;
+    if (n <= 0) {
+        if (last_block) wait_for_previous();
+        return;
+    }
+    const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C, ci = (int64_t)bh * sh.nc + c;
     const int64_t ko = (t0 * KH + h / sh.G) * sh.N, ks = (int64_t)KH * sh.N;
     uint4 raw[ND / 16];  // half a row: of Q's token tid / 2, or of K's
     const int qrow = tid / 2, half = tid % 2, tok = qrow % C;
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
         tc::fence_proxy_async();
         __syncthreads();
         if (tid == 0) {
-            bulk_s2g(to + (int64_t)blockIdx.x * Image::STRIDE, tc::smem_u32(img), Image::BYTES);
+            bulk_s2g(to + ci * Image::STRIDE, tc::smem_u32(img), Image::BYTES);
             bulk_commit();
             bulk_wait_read();
         }
@@ -388,6 +395,7 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
     }
     __syncthreads();
     if (warp == 7) tc::tmem_dealloc(tmem, 64);
+    if (last_block) wait_for_previous();
 }
 
 // --------------------------------------------------------------- scan
@@ -551,7 +559,9 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
     auto& s_gave_up = z.gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
-    const int len = row_len(lens, b, sh.T), nck = (len + C - 1) / C;
+    // chunks count from this launch's first, of the sequence's `tok` and on
+    const int tok = sh.c0 * C, len = max(row_len(lens, b, sh.T) - tok, 0);
+    const int nck = min((len + C - 1) / C, sh.c1 - sh.c0);
     const int quarters = (P + 31) / 32;
     if (warp == WMMA) {
         tc::tmem_alloc(&s_tmem, TMEM_COLS);
@@ -622,7 +632,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                 if (part == 0) s_sdown[c & 1][vc] = sc.down;
                 warp_done(&mb_s, lane);
                 if (KEEP && on) {
-                    float* dst = states + ((int64_t)bh * sh.nc + c) * N * P + vc;
+                    float* dst = states + ((int64_t)bh * sh.nc + sh.c0 + c) * N * P + vc;
 #pragma unroll
                     for (int i = 0; i < NS / 2; ++i)
                         if (k0 + 2 * i < N) {
@@ -704,7 +714,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                 sbound = fmaf(all, stop, row.of_all(top_of_pairs(x)) * ws.down * (64.f * 16384.f));
                 if constexpr (KEEP) {
                     if (on) {
-                        float* dst = writes + (((int64_t)bh * sh.nc + c) * C + EP * part) * P + vc;
+                        float* dst = writes + (((int64_t)bh * sh.nc + sh.c0 + c) * C + EP * part) * P + vc;
                         factors(Image::UU, rs.down);
 #pragma unroll
                         for (int i = 0; i < EP / 2; ++i) {
@@ -763,7 +773,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
         if (quarter < quarters && nck > 0 && find_top(0) && (nck == 1 || find_top(1))) {
             constexpr int OE = ND == 128 ? 8 : 16;  // columns at a time
             const int64_t os = (int64_t)sh.H * P;
-            E* dst = KEEP ? nullptr : o + ((int64_t)b * sh.T * sh.H + h) * P + vc;
+            E* dst = KEEP ? nullptr : o + (((int64_t)b * sh.T + tok) * sh.H + h) * P + vc;
             for (int c = 0; c < nck; ++c) {
                 if (c + 2 < nck && !find_top(c + 2)) break;  // (two ahead: the chain reads it a chunk early)
                 if constexpr (KEEP) continue;
@@ -816,8 +826,8 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                 dst += C * os;
             }
         }
-        if (!KEEP && on)  // behind the row's last token
-            for (int t = len; t < sh.T; ++t) o[(((int64_t)b * sh.T + t) * sh.H + h) * P + vc] = from_f<E>(0.f);
+        if (!KEEP && on && sh.c1 == sh.nc)  // behind the row's last token
+            for (int t = row_len(lens, b, sh.T); t < sh.T; ++t) o[(((int64_t)b * sh.T + t) * sh.H + h) * P + vc] = from_f<E>(0.f);
     } else if (warp == WMMA) {
         // ------------------------------------------------ MMA issue
         constexpr uint32_t id64 = tc::idesc_f16(128, C), id128 = tc::idesc_f16(128, 2 * C), idn = tc::idesc_f16(128, ND);
@@ -860,8 +870,9 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
     } else if (warp == WLOAD) {
         // ------------------------------------------------ loader
         int last[2] = {-1, -1};  // parity of the last copies into each stage
-        const unsigned char* img = image + (int64_t)bh * sh.nc * Image::STRIDE;
-        const unsigned char* ops = operands + ((int64_t)b * KH + h / sh.G) * sh.nc * (KEEP ? Operands<ND>::BWD : Operands<ND>::FWD);
+        const unsigned char* img = image + ((int64_t)bh * sh.nc + sh.c0) * Image::STRIDE;
+        const unsigned char* ops =
+            operands + (((int64_t)b * KH + h / sh.G) * sh.nc + sh.c0) * (KEEP ? Operands<ND>::BWD : Operands<ND>::FWD);
         for (int c = 0; c < nck; ++c) {
             const uint32_t at = tc::smem_u32(smem) + (c & 1) * M::STAGE;
             if (c >= 2 && !warp_wait(&mb_free[c & 1], ((c >> 1) - 1) & 1, &s_gave_up)) break;
@@ -889,7 +900,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
         for (int c = 0; c < nck; ++c) {
             const int slot = c % NV, n = min(len - c * C, C);
             const uint32_t at = tc::smem_u32(smem) + M::V0 + slot * M::VBYTES;
-            const E* src = v + (((int64_t)b * sh.T + (int64_t)c * C) * sh.H + h) * P;
+            const E* src = v + (((int64_t)b * sh.T + tok + (int64_t)c * C) * sh.H + h) * P;
             if (c >= NV && !warp_wait(&mb_vfree[slot], (c / NV - 1) & 1, &s_gave_up)) break;
             for (int id = t; id < C * per; id += VT) {
                 const int i = id / per;
@@ -911,6 +922,7 @@ template <typename E, int ND>
 __global__ void __launch_bounds__(ST, 1) delta_scan_tc(ScanArgs<E> g, const int* __restrict__ lens, Shape sh,
                                                        unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
+    let_next_start();  // (the next chunks' prep, on the SMs that the heads leave)
     scan_body<E, ND, false>(g, blockIdx.x, lens, sh, status, smem);
 }
 
@@ -1863,7 +1875,8 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
 }
 
 Shape shape(const DeltaArgs& a) {
-    return Shape{(int)a.T, (int)a.H, (int)(a.H / a.KH), (int)a.N, (int)a.P, (int)((a.T + C - 1) / C)};
+    const int nc = (int)((a.T + C - 1) / C);
+    return Shape{(int)a.T, (int)a.H, (int)(a.H / a.KH), (int)a.N, (int)a.P, nc, 0, nc};
 }
 int64_t chunk_count(const DeltaArgs& a) { return a.Bz * a.H * ((a.T + C - 1) / C); }
 
@@ -1889,29 +1902,58 @@ size_t operand_bytes(const DeltaArgs& a, bool back) {
     return (size_t)(chunk_count(a) / a.H * a.KH) * one;
 }
 
+// The prep of the shape's chunks; with `overlap` it may start while the kernel
+// before it in the stream still runs.
 template <typename E, int ND, bool BACK>
-cudaError_t prep_tc(const DeltaArgs& a, unsigned char* image, unsigned char* image_t, unsigned char* operands,
-                    cudaStream_t st) {
+cudaError_t prep_tc(const DeltaArgs& a, const Shape& sh, unsigned char* image, unsigned char* image_t,
+                    unsigned char* operands, bool overlap, cudaStream_t st) {
     using M = PrepSmem<ND, BACK>;
     const cudaError_t e = allow<delta_prep_tc<E, ND, BACK>>(M::BYTES);
     if (e != cudaSuccess) return e;
-    delta_prep_tc<E, ND, BACK><<<(unsigned)chunk_count(a), PT, M::BYTES, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), a.g, a.beta, a.lens, image, image_t, operands, a.scale,
-        shape(a), status_word());
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.Bz * a.H * (sh.c1 - sh.c0)));
+    cfg.blockDim = dim3(PT);
+    cfg.dynamicSmemBytes = M::BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, delta_prep_tc<E, ND, BACK>, static_cast<const E*>(a.q), static_cast<const E*>(a.k), a.g,
+                              a.beta, a.lens, image, image_t, operands, a.scale, sh, status_word());
+}
+
+// Parts of a sequence that are prepared and scanned in turn, the next part's
+// prep beside the scan: the scan has one CTA per head, so with fewer heads than
+// SMs the prep (a CTA per chunk and head) takes the others.  One part costs two
+// more launches and the state's way through memory (about 8 us), so a part has
+// at least 16 chunks (60 to 100 us of scan).
+int parts_of(const DeltaArgs& a) {
+    const int64_t nc = (a.T + C - 1) / C;
+    if (a.Bz * a.H > 120) return 1;
+    return (int)(nc < 32 ? 1 : nc / 16 < 8 ? nc / 16 : 8);
 }
 
 template <typename E, int ND>
 cudaError_t forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     unsigned char* image = static_cast<unsigned char*>(ws);
     unsigned char* operands = image + image_bytes(a);
-    cudaError_t e = prep_tc<E, ND, false>(a, image, nullptr, operands, st);
-    if (e != cudaSuccess) return e;
+    float* between = reinterpret_cast<float*>(operands + operand_bytes(a, false));  // the state from part to part
     constexpr uint32_t smem = ScanSmem<ND>::BYTES + sizeof(ScanShared);
-    if ((e = allow<delta_scan_tc<E, ND>>(smem)) != cudaSuccess) return e;
-    const ScanArgs<E> g{static_cast<const E*>(a.v), image, operands, a.h0, static_cast<E*>(a.o), a.h_final, nullptr, nullptr};
-    delta_scan_tc<E, ND><<<(unsigned)(a.Bz * a.H), ST, smem, st>>>(g, a.lens, shape(a), status_word());
-    return cudaGetLastError();
+    cudaError_t e = allow<delta_scan_tc<E, ND>>(smem);
+    const int parts = parts_of(a);
+    Shape sh = shape(a);
+    for (int p = 0; p < parts && e == cudaSuccess; ++p) {
+        sh.c0 = (int)((int64_t)sh.nc * p / parts);
+        sh.c1 = (int)((int64_t)sh.nc * (p + 1) / parts);
+        if ((e = prep_tc<E, ND, false>(a, sh, image, nullptr, operands, p > 0, st)) != cudaSuccess) break;
+        const ScanArgs<E> g{static_cast<const E*>(a.v), image, operands, p ? between : a.h0, static_cast<E*>(a.o),
+                            p + 1 < parts ? between : a.h_final, nullptr, nullptr};
+        delta_scan_tc<E, ND><<<(unsigned)(a.Bz * a.H), ST, smem, st>>>(g, a.lens, sh, status_word());
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 template <typename E, int ND>
@@ -1920,7 +1962,7 @@ cudaError_t back_scans_tc(const DeltaArgs& a, void* ws, float* states, float* af
     unsigned char* image = static_cast<unsigned char*>(ws);
     unsigned char* image_t = image + image_bytes(a);
     unsigned char* operands = image_t + image_bytes(a);
-    cudaError_t e = prep_tc<E, ND, true>(a, image, image_t, operands, st);
+    cudaError_t e = prep_tc<E, ND, true>(a, shape(a), image, image_t, operands, false, st);
     if (e != cudaSuccess) return e;
     constexpr uint32_t f = ScanSmem<ND>::BYTES + sizeof(ScanShared), r = BackSmem<ND>::BYTES + sizeof(BackShared);
     constexpr uint32_t smem = f > r ? f : r;
@@ -1968,7 +2010,9 @@ cudaError_t forward_by_width(const DeltaArgs& a, void* ws, cudaStream_t st) {
 
 }  // namespace
 
-size_t tc_workspace_bytes(const DeltaArgs& a) { return image_bytes(a) + operand_bytes(a, false); }
+size_t tc_workspace_bytes(const DeltaArgs& a) {
+    return image_bytes(a) + operand_bytes(a, false) + (parts_of(a) > 1 ? sizeof(float) * a.Bz * a.H * a.N * a.P : 0);
+}
 cudaError_t launch_forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     return a.dtype == CSSD_BF16 ? forward_by_width<__nv_bfloat16>(a, ws, st) : forward_by_width<__half>(a, ws, st);
 }
