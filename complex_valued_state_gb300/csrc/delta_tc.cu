@@ -24,6 +24,7 @@
 // X R run beside the chain).
 
 #include <atomic>
+#include <type_traits>
 
 #include "delta_tc.cuh"
 
@@ -1367,11 +1368,16 @@ struct GradSmem {
     // The operands of K and Q; at the widest, where not everything fits, K^T and
     // Q^T come late, over dO (read by then) and its rest.
     static constexpr bool LATE = ND == 128 && PD == 128;
-    static constexpr uint32_t OPS = ST + 2 * STP, FIRST = LATE ? QK<ND>::BYTES : Operands<ND>::BWD, BYTES = OPS + FIRST;
-    static constexpr uint32_t KT0 = LATE ? HI : OPS + Operands<ND>::KT0, QT0 = LATE ? LO : OPS + Operands<ND>::QT0;
+    static constexpr uint32_t OPS = ST + 2 * STP;
+    // Pm below the diagonal and W^T above, fp32, over Q and K when those are
+    // read: 65 columns a row, so that neither a row's nor a column's readers
+    // meet in a bank.
+    static constexpr int LM = C + 1;
+    static constexpr uint32_t MAT = OPS, MAT_BYTES = (4 * C * LM + 127) / 128 * 128;
+    static constexpr uint32_t QK_BYTES = QK<ND>::BYTES > MAT_BYTES ? QK<ND>::BYTES : MAT_BYTES;
+    static constexpr uint32_t KT0 = LATE ? HI : OPS + QK_BYTES, QT0 = LATE ? LO : KT0 + KT<ND>::BYTES;
+    static constexpr uint32_t BYTES = OPS + QK_BYTES + (LATE ? 0 : 2 * KT<ND>::BYTES);
     static_assert(!LATE || KT<ND>::BYTES <= ROWS, "K^T over dO");
-    static constexpr uint32_t MAT = OPS;  // Pm below the diagonal and W^T above, over Q and K when those are read
-    static_assert(4 * C * C <= 2 * QK<ND>::KROWS, "Pm over Q and K");
 };
 
 // 8 rows a warp (row lane % 8), a lane's column groups lane / 8, + 4, ..: the
@@ -1467,8 +1473,9 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
         tc::mbar_init(&mb_late, 1);
         tc::mbar_init(&mb_drain, 1);
         tc::mbar_fence_init();
-        tc::mbar_arrive_expect_tx(&mb_ops, M::FIRST);
-        tc::bulk_g2s(tc::smem_u32(smem + M::OPS), ops, M::FIRST, &mb_ops);
+        tc::mbar_arrive_expect_tx(&mb_ops, M::LATE ? QK<ND>::BYTES : Operands<ND>::BWD);
+        tc::bulk_g2s(tc::smem_u32(smem + M::OPS), ops, QK<ND>::BYTES, &mb_ops);
+        if (!M::LATE) tc::bulk_g2s(tc::smem_u32(smem + M::KT0), ops + Operands<ND>::KT0, 2 * KT<ND>::BYTES, &mb_ops);
     }
     // Z (with dV and z.v), U, dO: 8 rows a warp, all loads before the first use
     const int rg = warp % 8, ti = 8 * rg + lane % 8, srow = 8 * warp + lane % 8;
@@ -1603,7 +1610,8 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
     const bool is_k = quarter >= 2;
     const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16);
     float* mat = reinterpret_cast<float*>(smem + M::MAT);
-    auto at = [](int r, int cc) { return r * C + (cc ^ (r & 31)); };  // rows and columns without bank conflicts
+    float* mrow = mat + i * M::LM;  // row i
+    float* mcol = mat + i;          // column i
     const bool above = 32 * (quarter % 2) + 31 < j0;                  // every pair of this warp has i < j
     warp_wait(&mb_1, 0, &s_gave_up);
     tc::fence_after_sync();
@@ -1613,9 +1621,9 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
             const float ri = s_rows[row] * (is_k ? 1.f : scale), re = ri * tab.e[i], nb = -d.beta[i];
             const int last = is_k ? i - 1 : i;
             const bool steep = tab.steep;
-#pragma unroll 1
-            for (int e = 0; e < CJ; e += 8) {
-                const int j = j0 + e;
+            // eight columns; MASK where some of the warp's rows end among them
+            auto columns = [&](int j, auto mask) {
+                constexpr bool MASK = decltype(mask)::value;
                 uint32_t du[8], kk[8];
                 tc::tmem_ld8(tq + COL_DU + j, du);
                 if (is_k) tc::tmem_ld8(tq + COL_KK + j, kk);
@@ -1632,32 +1640,43 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
 #pragma unroll
                     for (int u = 0; u < 8; ++u) x[u] = __uint_as_float(du[u]) * (ri * s_u[j + u]) * steep_decay(d, i, j + u);
                 }
+                if (MASK)
 #pragma unroll
-                for (int u = 0; u < 8; ++u) x[u] = j + u <= last ? x[u] : 0.f;
+                    for (int u = 0; u < 8; ++u) x[u] = j + u <= last ? x[u] : 0.f;
                 if (is_k) {
 #pragma unroll
                     for (int u = 0; u < 8; u += 4) {
                         const float4 f = *reinterpret_cast<const float4*>(s_kd + j + u);
-                        // (by select: nothing above the diagonal may reach the sum)
-                        gb = fmaf(x[u], j + u <= last ? __uint_as_float(kk[u]) * f.x : 0.f, gb);
-                        gb = fmaf(x[u + 1], j + u + 1 <= last ? __uint_as_float(kk[u + 1]) * f.y : 0.f, gb);
-                        gb = fmaf(x[u + 2], j + u + 2 <= last ? __uint_as_float(kk[u + 2]) * f.z : 0.f, gb);
-                        gb = fmaf(x[u + 3], j + u + 3 <= last ? __uint_as_float(kk[u + 3]) * f.w : 0.f, gb);
+                        const float fu[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const float y = __uint_as_float(kk[u + w]) * fu[w];
+                            // (by select: nothing above the diagonal may reach the sum)
+                            gb = fmaf(x[u + w], !MASK || j + u + w <= last ? y : 0.f, gb);
+                        }
                     }
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                         x[u] *= nb;
-                        if (j + u <= last) mat[at(j + u, i)] = x[u];
+                        if (!MASK || j + u <= last) mcol[(j + u) * M::LM] = x[u];
                     }
                 } else {
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        if (j + u <= last) mat[at(i, j + u)] = x[u];
+                        if (!MASK || j + u <= last) mrow[j + u] = x[u];
                 }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(x[u]));
+            };
+#pragma unroll 1
+            for (int j = j0; j < j0 + CJ; j += 8) {
+                if (j + 8 <= 32 * (quarter % 2))
+                    columns(j, std::false_type());
+                else
+                    columns(j, std::true_type());
             }
         }
+        // sum_j W_ij k_i.k_j = -beta_i times what dbeta wants
         if (is_k) s_gb[part][i] = gb * s_kd[i];
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -1676,29 +1695,36 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
         const int j = j0 + e;
         f2 a[8];
         const f2 up = mk2(ps.up, ps.up);
+        const float *row0 = mrow + j, *col0 = mcol + j * M::LM;
         if (is_k) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {  // W below the diagonal lies at (column, row), above it at (row, column)
-                const int c0 = j + 2 * u, c1 = c0 + 1;
-                const float x0 = c0 == i ? 0.f : mat[c0 < i ? at(c0, i) : at(i, c0)];
-                const float x1 = c1 == i ? 0.f : mat[c1 < i ? at(c1, i) : at(i, c1)];
-                a[u] = mul2(mul2(mk2(x0, x1), *reinterpret_cast<const f2*>(s_kd + c0)), up);
+                float x[2];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int cc = 2 * u + w;
+                    x[w] = *(j + cc < i ? col0 + cc * M::LM : row0 + cc);
+                    if (j + cc == i) x[w] = 0.f;
+                }
+                a[u] = mul2(mul2(mk2(x[0], x[1]), *reinterpret_cast<const f2*>(s_kd + j + 2 * u)), up);
             }
         } else {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const int c0 = j + 2 * u, c1 = c0 + 1;
-                const float x0 = c0 <= i ? mat[at(i, c0)] : 0.f, x1 = c1 <= i ? mat[at(i, c1)] : 0.f;
-                a[u] = mul2(mul2(mk2(x0, x1), *reinterpret_cast<const f2*>(s_kd + c0)), up);
+                float x[2];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) x[w] = j + 2 * u + w <= i ? row0[2 * u + w] : 0.f;
+                a[u] = mul2(mul2(mk2(x[0], x[1]), *reinterpret_cast<const f2*>(s_kd + j + 2 * u)), up);
             }
         }
         store_split(a, tq + j / 2, tq + 32 + j / 2);
         if (is_k) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const int c0 = j + 2 * u, c1 = c0 + 1;
-                const float x0 = c0 >= i ? mat[at(c0, i)] : 0.f, x1 = c1 >= i ? mat[at(c1, i)] : 0.f;
-                a[u] = mul2(mul2(mk2(x0, x1), *reinterpret_cast<const f2*>(s_qd + c0)), up);
+                float x[2];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) x[w] = j + 2 * u + w >= i ? col0[(2 * u + w) * M::LM] : 0.f;
+                a[u] = mul2(mul2(mk2(x[0], x[1]), *reinterpret_cast<const f2*>(s_qd + j + 2 * u)), up);
             }
             store_split(a, tq + 64 + j / 2, tq + 96 + j / 2);
         } else {
