@@ -172,6 +172,8 @@ def _stream_handle(stream, device):
 STATUS_HANDOFF_TIMEOUT = 1
 STATUS_CHUNK_MMA_TIMEOUT = 2
 STATUS_BORN_MMA_TIMEOUT = 4
+STATUS_DELTA_TIMEOUT = 8
+STATUS_NORM_TIMEOUT = 16
 
 
 def device_status(clear: bool = False, device=None, stream=None) -> int:
@@ -757,6 +759,10 @@ def _norm_inputs(x, weight, bias=None):
                 raise TypeError(f"{n} must be {x.dtype} or float32, got {t.dtype}")
         _expect(t, n, wdtype, (D,), index)
     return xt, wt, x.numel() // D if D else 0, D, index
+
+
+def layernorm_backward_workspace_bytes(rows: int, width: int) -> int:
+    return int(load().cssd_layernorm_backward_workspace_bytes(rows, width))
 
 
 def layernorm(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, stream=None):

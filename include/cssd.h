@@ -489,6 +489,9 @@ int cssd_layernorm_backward(int64_t rows, int64_t width, int xtype, int wtype, c
  *   1  the chunked forward: a state hand-off from the previous chunk timed out
  *   2  the chunked forward: a tensor-core completion wait timed out
  *   4  Born attention: a tensor-core completion wait timed out
+ *   8  the gated delta rule (16-bit forward or gradients): a wait for a copy,
+ *      a tensor-core completion or another group of threads timed out
+ *  16  the layer norm's gradients: a wait for a copy timed out
  * The chunked forward's bits also cover cssd_chunked_backward, the precise
  * and host-streamed forwards, which run the same kernel.  This call reads the
  * word of the stream's device (which must be the current device) after the

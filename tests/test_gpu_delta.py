@@ -375,3 +375,62 @@ def test_long_sequence(cs):
     """2000 tokens of slow decays, 16-bit, sampled against the recurrence."""
     d, opt, _ = make(17, 1, 2000, 3, 1, 128, 128, dtype="bf16", state=True, rate=0.02)
     check_forward(cs, d, opt)
+
+
+@pytest.mark.parametrize("shape", [(6, 2085, 2, 1, 64, 64), (6, 2048, 1, 1, 128, 128), (6, 3300, 2, 2, 48, 80)])
+def test_long_ragged_rows(cs, shape):
+    """Few heads of many chunks: rows that end in the first chunks, at and just
+    past the middle, and at the last token; the state is written over h0."""
+    T = shape[1]
+    lens = [0, 1, 700, 1024, 1025, T]
+    d, opt, _ = make(18, *shape, dtype="bf16", state=True, ragged=lens, rate=0.05)
+    for b, n in enumerate(lens):
+        for t in d.values():
+            t[b, n:] = float("nan")
+    n, m = np64({k: torch.nan_to_num(v) for k, v in d.items()}), np64(opt)
+    want_o, want_h, _ = ref.delta_forward(*(n[k] for k in ("q", "k", "v", "g", "beta")), 0.25, m["h0"], m["lens"])
+    g, o_ = on(d), on(opt)
+    o, h = cs.delta_forward(**g, h0=o_["h0"], lens=o_["lens"], h_final=o_["h0"], scale=0.25)
+    assert h is o_["h0"]
+    close(o, want_o, "o")
+    close(h, want_h, "h_final")
+    for b, ln in enumerate(lens):
+        assert (o[b, ln:] == 0).all()
+    assert torch.equal(h[0].cpu(), opt["h0"][0])
+    alone, none = cs.delta_forward(**g, **on(opt), scale=0.25, want_state=False)
+    assert none is None and torch.equal(alone, o)
+
+
+def test_long_sequence_stream_and_graph(cs):
+    """The same over several launches: another stream, back to back calls on
+    one workspace, a captured graph replayed twice on other contents."""
+    shape = (1, 4200, 3, 3, 64, 64)
+    d, opt, _ = make(19, *shape, dtype="fp16", state=True, rate=0.05)
+    d2, opt2, _ = make(20, *shape, dtype="fp16", state=True, rate=0.05)
+    ws = torch.empty(cs.delta_workspace_bytes(*shape, torch.float16), dtype=torch.uint8, device="cuda")
+    g, o_, g2, o2 = on(d), on(opt), on(d2), on(opt2)
+    check_forward(cs, d, opt)
+    want, want2 = cs.delta_forward(**g, **o_), cs.delta_forward(**g2, **o2)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [cs.delta_forward(**a, **b, workspace=ws, stream=s) for a, b in ((g, o_), (g2, o2)) * 3]
+    s.synchronize()
+    for i, (o, h) in enumerate(got):
+        w = (want, want2)[i % 2]
+        assert torch.equal(o, w[0]) and torch.equal(h, w[1]), i
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, h = cs.delta_forward(**g, **o_)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(h, want[1])
+    for a, b in ((g, g2), (o_, o2)):
+        for n in a:
+            if a[n] is not None:
+                a[n].copy_(b[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want2[0]) and torch.equal(h, want2[1])
+    assert cs.device_status() == 0

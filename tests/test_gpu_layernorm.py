@@ -102,6 +102,26 @@ def test_row_counts(cs, rows):
         close(g["gbias"], gb, "gbias", top=np.max(np.sum(np.abs(f64(dy)), 0)), inner=steps)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,width", [(1, 4096), (2, 6144), (3, 8192), (7, 12296), (5, 16001)])
+def test_few_wide_rows(cs, rows, width, dtype):
+    """Fewer rows than groups that sum them; rows of other widths between a
+    thread's registers, a ring's stages and the streamed sums."""
+    x, w, b, dy = make(rows + width, rows, width, dtype, "fp32")
+    y, mean, rstd = cs.layernorm(x.cuda(), dev(w), dev(b))
+    want, m, r = ref.layernorm(f64(x), f64(w), f64(b), 1e-5)
+    close(y, want, "y", inner=4 * INNER)
+    ws = torch.empty(cs.layernorm_backward_workspace_bytes(rows, width), dtype=torch.uint8, device="cuda")
+    g = cs.layernorm_backward(dy.cuda(), x.cuda(), dev(w), mean, rstd, workspace=ws)
+    gx, gw, gb = ref.layernorm_backward(f64(dy), f64(x), f64(w), 1e-5)
+    xh = (f64(x) - m[:, None]) * r[:, None]
+    steps = (rows / 304 + 64) * 2.0 ** -24
+    close(g["gx"], gx, "gx", inner=8 * INNER)
+    close(g["gweight"], gw, "gweight", top=np.max(np.sum(np.abs(f64(dy) * xh), 0)), inner=steps + 4 * INNER)
+    close(g["gbias"], gb, "gbias", top=np.max(np.sum(np.abs(f64(dy)), 0)), inner=steps)
+    assert cs.device_status() == 0
+
+
 @pytest.mark.parametrize("width", [96, 101])
 def test_without_affine_and_partial_gradients(cs, width):
     x, _, _, dy = make(3, 20, width, "fp16", "fp16", affine=False)
