@@ -919,12 +919,46 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
     if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusDelta);
 }
 
+// Chains on SMs.  A CTA's tensor memory fills its SM, so n chains (a head's
+// scan, each a walk that cannot be split) on fewer SMs would run in whole waves:
+// 192 on 152 take twice as long as 152.  Cut into `pieces` of equal length and
+// run in `rounds` launches, chain i sits out rounds - pieces of them, those
+// after its own, so that a round has n pieces / rounds CTAs; the state goes from
+// piece to piece through `between`.  192 chains: 3 pieces in 4 rounds, forward
+// 8 x 2048 x 24 64/64 in 362 us against 394 in one launch; 160: 317 against 347;
+// gradients 4 x 2048 x 24 (192 chains) 544 against 554.  A round costs 10 to 18
+// us more than its chunks, so 6 x 1024 x 16 128/128 gradients lose 1.4 %.
+struct Rounds {
+    int n, pieces, rounds, now;
+    float* between;
+    // The chain of CTA `cta` this round (or n and above: none) and its piece.
+    __device__ __forceinline__ int chain(int cta, int& piece) const {
+        const int s = cta % pieces, c = (now - s + rounds) % rounds, wrapped = c + pieces - rounds;
+        piece = now < c ? now : now - c + max(wrapped, 0);
+        return cta / pieces * rounds + c;
+    }
+};
+
+// Sets the first and last chunk and where the state comes from and goes to.
+template <typename E>
+__device__ __forceinline__ void take_piece(ScanArgs<E>& g, Shape& sh, const Rounds& turn, int piece) {
+    const int n = sh.c1 - sh.c0, from = sh.c0;
+    if (piece > 0) g.h0 = turn.between;
+    if (piece + 1 < turn.pieces) g.h_final = turn.between;
+    sh.c0 = from + n * piece / turn.pieces;
+    sh.c1 = from + n * (piece + 1) / turn.pieces;
+}
+
 template <typename E, int ND>
-__global__ void __launch_bounds__(ST, 1) delta_scan_tc(ScanArgs<E> g, const int* __restrict__ lens, Shape sh,
+__global__ void __launch_bounds__(ST, 1) delta_scan_tc(ScanArgs<E> g, const int* __restrict__ lens, Shape sh, Rounds turn,
                                                        unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
     let_next_start();  // (the next chunks' prep, on the SMs that the heads leave)
-    scan_body<E, ND, false>(g, blockIdx.x, lens, sh, status, smem);
+    int piece = 0;
+    const int bh = turn.chain(blockIdx.x, piece);
+    if (bh >= turn.n) return;
+    take_piece(g, sh, turn, piece);
+    scan_body<E, ND, false>(g, bh, lens, sh, status, smem);
 }
 
 // --------------------------------------------------------------- backward scan
@@ -992,7 +1026,8 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
     auto& s_gave_up = y.gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
-    const int len = row_len(lens, b, sh.T), nck = (len + C - 1) / C;
+    const int len = row_len(lens, b, sh.T);
+    const int end = min((len + C - 1) / C, sh.c1), nck = max(end - sh.c0, 0);  // the row's chunks of this launch
     const int quarters = (P + 31) / 32;
     if (warp == WMMA) {
         tc::tmem_alloc(&s_tmem, TMEM_COLS);
@@ -1077,11 +1112,11 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
             bool ok = nck > 0;
             if (ok) {
                 sbound = row.of_all(top_of_pairs(s));
-                sdown = put_state(nck - 1, sbound);
+                sdown = put_state(end - 1, sbound);
                 ok = warp_wait(&mb_full[0], 0, &s_gave_up);
             }
             for (int j = 0; ok && j < nck; ++j) {
-                const int c = nck - 1 - j;
+                const int c = end - 1 - j;
                 const uint32_t ph = j & 1;
                 const float* ff = reinterpret_cast<const float*>(smem + (j & 1) * M::STAGE + M::IMG + Image::F);
                 f2 x[EP / 2], f[EP / 2];
@@ -1292,7 +1327,7 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
         const unsigned char* img = image + (int64_t)bh * sh.nc * Image::STRIDE;
         const unsigned char* ops = operands + ((int64_t)b * KH + h / sh.G) * sh.nc * Operands<ND>::BWD + QK<ND>::KROWS;
         for (int j = 0; j < nck; ++j) {
-            const int c = nck - 1 - j;
+            const int c = end - 1 - j;
             const uint32_t at = tc::smem_u32(smem) + (j & 1) * M::STAGE;
             if (j >= 2 && !warp_wait(&mb_free[j & 1], ((j >> 1) - 1) & 1, &s_gave_up)) break;
             if (lane == 0) {
@@ -1300,7 +1335,7 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
                 tc::bulk_g2s(at + M::K0, ops + (int64_t)c * Operands<ND>::BWD, M::OPS, &mb_full[j & 1]);
                 tc::bulk_g2s(at + M::IMG, img + (int64_t)c * Image::STRIDE, Image::BYTES, &mb_full[j & 1]);
                 last[j & 1] = (j >> 1) & 1;
-                if (c >= 2) {  // what the next copies into this stage read, into L2
+                if (c - 2 >= sh.c0) {  // what the next copies into this stage read, into L2
                     prefetch_l2(ops + (int64_t)(c - 2) * Operands<ND>::BWD, M::OPS);
                     prefetch_l2(img + (int64_t)(c - 2) * Image::STRIDE, Image::BYTES);
                 }
@@ -1314,7 +1349,7 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
         // ------------------------------------------------ dO (rows of P elements; zeros where no token is)
         const int t = tid - 32 * WV, per = P / 8;
         for (int j = 0; j < nck; ++j) {
-            const int c = nck - 1 - j, slot = j % NV, n = min(len - c * C, C);
+            const int c = end - 1 - j, slot = j % NV, n = min(len - c * C, C);
             const uint32_t at = tc::smem_u32(smem) + M::V0 + slot * M::VBYTES;
             const E* src = dout + (((int64_t)b * sh.T + (int64_t)c * C) * sh.H + h) * P;
             if (j >= NV && !warp_wait(&mb_vfree[slot], (j / NV - 1) & 1, &s_gave_up)) break;
@@ -1334,17 +1369,28 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
     if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusDelta);
 }
 
-// Both of the gradients' scans, which do not need one another: a CTA of each
-// per value head in one launch, so that up to 76 heads run both at once.
+// Both of the gradients' scans, which do not need one another, in one launch a
+// round: chains 0 .. n / 2 - 1 run the backward scan, the others the forward.
 template <typename E, int ND>
 __global__ void __launch_bounds__(ST, 1) delta_both_scans_tc(BackArgs<E> back, ScanArgs<E> fwd, const int* __restrict__ lens,
-                                                             Shape sh, unsigned* status) {
+                                                             Shape sh, Rounds turn, unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
-    const int heads = gridDim.x / 2;
-    if ((int)blockIdx.x < heads)
-        back_scan_body<E, ND>(back, blockIdx.x, lens, sh, status, smem);
-    else
-        scan_body<E, ND, true>(fwd, blockIdx.x - heads, lens, sh, status, smem);
+    const int heads = turn.n / 2;
+    int piece = 0;
+    const int i = turn.chain(blockIdx.x, piece);
+    if (i >= turn.n) return;
+    if (i < heads) {
+        const int nc = sh.nc;
+        if (piece > 0) back.dh = turn.between;
+        if (piece + 1 < turn.pieces) back.gh0 = turn.between;
+        sh.c0 = nc - nc * (piece + 1) / turn.pieces;
+        sh.c1 = nc - nc * piece / turn.pieces;
+        back_scan_body<E, ND>(back, i, lens, sh, status, smem);
+    } else {
+        turn.between += (int64_t)heads * sh.N * sh.P;
+        take_piece(fwd, sh, turn, piece);
+        scan_body<E, ND, true>(fwd, i - heads, lens, sh, status, smem);
+    }
 }
 
 // --------------------------------------------------------------- dQ, dK, dV, dg, dbeta
@@ -1950,6 +1996,30 @@ cudaError_t prep_tc(const DeltaArgs& a, const Shape& sh, unsigned char* image, u
                               a.beta, a.lens, image, image_t, operands, a.scale, sh, status_word());
 }
 
+// The SMs of the current device.
+cudaError_t sm_count(int* n) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+}
+
+// The cut of n chains of nc chunks that takes the fewest chunks' time, a round
+// counted as ROUND chunks more (its launch, and the state's way out and in).
+Rounds cut(int64_t n, int nc, int sms, float* between) {
+    constexpr int ROUND = 3;
+    Rounds best{(int)n, 1, 1, 0, between};  // one launch: waves of whole chains
+    double least = (double)((n + sms - 1) / sms) * nc + ROUND;
+    for (int pieces = 2; n > sms && pieces <= 8 && pieces <= nc; ++pieces) {
+        int rounds = (int)((n * pieces + sms - 1) / sms);
+        while (pieces * ((n + rounds - 1) / rounds) > sms) ++rounds;
+        const double t = rounds * ((double)((nc + pieces - 1) / pieces) + ROUND);
+        if (t < least) least = t, best.pieces = pieces, best.rounds = rounds;
+    }
+    return best;
+}
+unsigned ctas(const Rounds& r) { return (unsigned)(r.pieces * ((r.n + r.rounds - 1) / r.rounds)); }
+size_t state_bytes(const DeltaArgs& a) { return sizeof(float) * a.Bz * a.H * a.N * a.P; }
+
 // Parts of a sequence that are prepared and scanned in turn, the next part's
 // prep beside the scan: the scan has one CTA per head, so with fewer heads than
 // SMs the prep (a CTA per chunk and head) takes the others.  One part costs two
@@ -1968,6 +2038,8 @@ cudaError_t forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     float* between = reinterpret_cast<float*>(operands + operand_bytes(a, false));  // the state from part to part
     constexpr uint32_t smem = ScanSmem<ND>::BYTES + sizeof(ScanShared);
     cudaError_t e = allow<delta_scan_tc<E, ND>>(smem);
+    int sms = 0;
+    if (e == cudaSuccess) e = sm_count(&sms);
     const int parts = parts_of(a);
     Shape sh = shape(a);
     for (int p = 0; p < parts && e == cudaSuccess; ++p) {
@@ -1976,8 +2048,11 @@ cudaError_t forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
         if ((e = prep_tc<E, ND, false>(a, sh, image, nullptr, operands, p > 0, st)) != cudaSuccess) break;
         const ScanArgs<E> g{static_cast<const E*>(a.v), image, operands, p ? between : a.h0, static_cast<E*>(a.o),
                             p + 1 < parts ? between : a.h_final, nullptr, nullptr};
-        delta_scan_tc<E, ND><<<(unsigned)(a.Bz * a.H), ST, smem, st>>>(g, a.lens, sh, status_word());
-        e = cudaGetLastError();
+        Rounds turn = cut(a.Bz * a.H, sh.c1 - sh.c0, sms, between);
+        for (; turn.now < turn.rounds && e == cudaSuccess; ++turn.now) {
+            delta_scan_tc<E, ND><<<ctas(turn), ST, smem, st>>>(g, a.lens, sh, turn, status_word());
+            e = cudaGetLastError();
+        }
     }
     return e;
 }
@@ -1995,8 +2070,15 @@ cudaError_t back_scans_tc(const DeltaArgs& a, void* ws, float* states, float* af
     if ((e = allow<delta_both_scans_tc<E, ND>>(smem)) != cudaSuccess) return e;
     const ScanArgs<E> fwd{static_cast<const E*>(a.v), image, operands, a.h0, nullptr, nullptr, states, writes};
     const BackArgs<E> back{static_cast<const E*>(a.dout), image_t, operands, a.dh_final, a.gh0, after, zs};
-    delta_both_scans_tc<E, ND><<<(unsigned)(2 * a.Bz * a.H), ST, smem, st>>>(back, fwd, a.lens, shape(a), status_word());
-    return cudaGetLastError();
+    int sms = 0;
+    if ((e = sm_count(&sms)) != cudaSuccess) return e;
+    const Shape sh = shape(a);
+    Rounds turn = cut(2 * a.Bz * a.H, sh.nc, sms, reinterpret_cast<float*>(operands + operand_bytes(a, true)));
+    for (; turn.now < turn.rounds && e == cudaSuccess; ++turn.now) {
+        delta_both_scans_tc<E, ND><<<ctas(turn), ST, smem, st>>>(back, fwd, a.lens, sh, turn, status_word());
+        e = cudaGetLastError();
+    }
+    return e;
 }
 template <typename E, typename O, int ND, int PD>
 cudaError_t grad_tc(const DeltaArgs& a, const unsigned char* image_t, const unsigned char* operands, const float* states,
@@ -2037,7 +2119,7 @@ cudaError_t forward_by_width(const DeltaArgs& a, void* ws, cudaStream_t st) {
 }  // namespace
 
 size_t tc_workspace_bytes(const DeltaArgs& a) {
-    return image_bytes(a) + operand_bytes(a, false) + (parts_of(a) > 1 ? sizeof(float) * a.Bz * a.H * a.N * a.P : 0);
+    return image_bytes(a) + operand_bytes(a, false) + state_bytes(a);
 }
 cudaError_t launch_forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     return a.dtype == CSSD_BF16 ? forward_by_width<__nv_bfloat16>(a, ws, st) : forward_by_width<__half>(a, ws, st);
@@ -2052,7 +2134,7 @@ cudaError_t launch_grad_tc(const DeltaArgs& a, void* ws, const float* states, co
     return shared ? grad_by_width<__half, float>(a, ws, states, after, writes, zs, gq, gk, st)
                   : grad_by_width<__half, __half>(a, ws, states, after, writes, zs, gq, gk, st);
 }
-size_t tc_back_bytes(const DeltaArgs& a) { return 2 * image_bytes(a) + operand_bytes(a, true); }
+size_t tc_back_bytes(const DeltaArgs& a) { return 2 * image_bytes(a) + operand_bytes(a, true) + 2 * state_bytes(a); }
 cudaError_t launch_back_scans_tc(const DeltaArgs& a, void* ws, float* states, float* after, float* writes, float* zs,
                                  cudaStream_t st) {
     return a.dtype == CSSD_BF16 ? back_scans_by_width<__nv_bfloat16>(a, ws, states, after, writes, zs, st)

@@ -434,3 +434,19 @@ def test_long_sequence_stream_and_graph(cs):
     torch.cuda.synchronize()
     assert torch.equal(o, want2[0]) and torch.equal(h, want2[1])
     assert cs.device_status() == 0
+
+
+@pytest.mark.parametrize("shape", [(10, 700, 17, 17, 64, 64), (3, 650, 90, 90, 32, 32), (2, 333, 100, 50, 128, 128)])
+def test_more_heads_than_sms(cs, shape):
+    """More chains than SMs, whose scans are cut into pieces: rows that end in
+    each piece, with a state and gradients of it, twice the same bits."""
+    B, T = shape[:2]
+    lens = [0, 1, T // 3, T // 2 + 1, T - 1, T, 64, 65, 128, 300][-B:]
+    d, opt, back = make(21, *shape, dtype="bf16", state=True, ragged=lens, rate=0.2)
+    check_forward(cs, d, opt)
+    check_backward(cs, d, opt, back)
+    runs = [cs.delta_forward(**on(d), **on(opt)) + tuple(cs.delta_backward(**on(d), **on(back), **on(opt)).values())
+            for _ in range(2)]
+    for x, y in zip(*runs):
+        assert torch.equal(x, y)
+    assert cs.device_status() == 0
