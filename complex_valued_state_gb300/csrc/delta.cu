@@ -9,11 +9,14 @@
 //     R  = beta (V - e^G K S)                       64 x P
 //     U  = T R,   O = scale (e^G Q S + X R)
 //     S+ = e^{G_end} S + K^T (e^{G_end - G} U)
-// so that T and X are made for all chunks at once and only three products a
-// chunk wait for the state.  The gradients run the same chain backwards:
-//     Z  = T^T (e^{G_end - G} K dS+) + scale X^T dO        (of R)
+// and with W = T beta e^G K and Q' = e^G Q - X beta e^G K what a chunk asks of
+// the state that enters it is two products, one behind the other:
+//     [U; O] = [T; scale X] beta V + [-W; scale Q'] S
+//     S+ = e^{G_end} S + K^T (e^{G_end - G} U)
+// The gradients run the same chain backwards:
+//     Z  = T^T (e^{G_end - G} K) dS+ + scale X^T dO        (of R)
 //     dV = beta Z
-//     dS = e^{G_end} dS+ + scale (e^G Q)^T dO - (e^G K)^T (beta Z)
+//     dS = e^{G_end} dS+ - (beta e^G K)^T Z + scale (e^G Q)^T dO
 // and, per chunk, with everything above at hand,
 //     dQ = scale e^G dO S^T + Pm K,             Pm = scale M o (dO U^T)
 //     dK = Pm^T Q + (W + W^T) K - beta e^G Z S^T + e^{G_end - G} U dS+^T,
@@ -23,12 +26,13 @@
 // (each e^{G_i} multiplies exactly what q_i reads and what v_i is compared
 // with, so dL/dG_i is the difference of those two inner products).
 //
-// These kernels serve fp32 tensors (and hold the sums, the states and every
-// intermediate of the 16-bit ones too where those take them): the products
-// are plain fp32 multiply-adds from shared memory, 4 x 4 outputs a thread.
+// These kernels serve fp32 tensors, with plain fp32 multiply-adds from shared
+// memory.  What does not wait for the state is made for all chunks at once by
+// delta_prep; delta_scan and delta_both_scans walk the chunks.
 
 #include "cssd_internal.h"
 #include "delta_common.cuh"
+#include "pairs.cuh"
 
 namespace cssd {
 namespace delta {
@@ -36,8 +40,7 @@ namespace {
 
 constexpr int NT = 256;       // threads of every kernel here
 constexpr int LT = C + 4;     // row stride of a 64 x 64 matrix in shared memory
-constexpr int PW = 32;        // state columns a scan CTA owns
-constexpr int LS = PW + 4;    // their row stride
+constexpr int PW = 16;        // state columns a scan CTA owns
 
 struct Geo {
     int T, H, G, N, P, nc;  // G: value heads per key head
@@ -60,16 +63,6 @@ __device__ void load_rows(float* dst, int ld, const T* src, int64_t stride, int 
 #pragma unroll
             for (int u = 0; u < E; ++u) dst[r * ld + c + u] = 0.f;
         }
-    }
-}
-
-// rows x PW columns from column p0 of an array with `width` columns (zeros
-// past it and past row n).
-template <typename T>
-__device__ void load_slice(float* dst, const T* src, int64_t stride, int rows, int p0, int width, int n, int tid) {
-    for (int e = tid; e < rows * PW; e += NT) {
-        const int r = e / PW, c = e % PW;
-        dst[r * LS + c] = (r < n && p0 + c < width) ? to_f(src[r * stride + p0 + c]) : 0.f;
     }
 }
 
@@ -98,22 +91,55 @@ __device__ __forceinline__ void mm_rk(float (&acc)[RA][4], const float* A, int l
     }
 }
 
-// acc[a][c] += sum_i A[i lda + r0 + a] B[i ldb + c0 + c].
-template <int RA>
-__device__ __forceinline__ void mm_kr(float (&acc)[RA][4], const float* A, int lda, const float* B, int ldb, int K,
-                                      int r0, int c0) {
+// acc[a][c] += sum_i A[i lda + r0 + a] f[i] B[i ldb + c0 + c], i from i0 to C - 1.
+__device__ __forceinline__ void mm_kr(float (&acc)[4][4], const float* A, int lda, const float* f, const float* B, int ldb,
+                                      int i0, int r0, int c0) {
 #pragma unroll 4
-    for (int i = 0; i < K; ++i) {
-        const float4 b = ld4(B + i * ldb + c0);
+    for (int i = i0; i < C; ++i) {
+        const float4 b = ld4(B + i * ldb + c0), v = ld4(A + i * lda + r0);
+        const float x[4] = {v.x * f[i], v.y * f[i], v.z * f[i], v.w * f[i]};
 #pragma unroll
-        for (int a = 0; a < RA; ++a) {
-            const float v = A[i * lda + r0 + a];
-            acc[a][0] = fmaf(v, b.x, acc[a][0]);
-            acc[a][1] = fmaf(v, b.y, acc[a][1]);
-            acc[a][2] = fmaf(v, b.z, acc[a][2]);
-            acc[a][3] = fmaf(v, b.w, acc[a][3]);
+        for (int a = 0; a < 4; ++a) {
+            acc[a][0] = fmaf(x[a], b.x, acc[a][0]);
+            acc[a][1] = fmaf(x[a], b.y, acc[a][1]);
+            acc[a][2] = fmaf(x[a], b.z, acc[a][2]);
+            acc[a][3] = fmaf(x[a], b.w, acc[a][3]);
         }
     }
+}
+
+// t += T B and, with BOTH, x += X B for the rows r0 .. r0 + 3 of the lower
+// triangular T and X (row stride LT), row j of B times f[j].
+template <bool BOTH>
+__device__ __forceinline__ void mm_lower(float (&t)[4][4], float (&x)[4][4], const float* T, const float* X, const float* f,
+                                         const float* B, int ldb, int r0, int c0) {
+    for (int k = 0; k <= r0; k += 4) {
+        float4 b[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            b[u] = ld4(B + (k + u) * ldb + c0);
+            const float m = f[k + u];
+            b[u].x *= m, b[u].y *= m, b[u].z *= m, b[u].w *= m;
+        }
+#pragma unroll
+        for (int h = 0; h < (BOTH ? 2 : 1); ++h)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const float4 v = ld4((h ? X : T) + (r0 + a) * LT + k);
+                const float w[4] = {v.x, v.y, v.z, v.w};
+                float(&acc)[4] = h ? x[a] : t[a];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    acc[0] = fmaf(w[u], b[u].x, acc[0]);
+                    acc[1] = fmaf(w[u], b[u].y, acc[1]);
+                    acc[2] = fmaf(w[u], b[u].z, acc[2]);
+                    acc[3] = fmaf(w[u], b[u].w, acc[3]);
+                }
+            }
+    }
+}
+__device__ __forceinline__ void st4(float* p, const float (&v)[4], float m) {
+    *reinterpret_cast<float4*>(p) = make_float4(m * v[0], m * v[1], m * v[2], m * v[3]);
 }
 
 // acc[a][c] += sum_k A[(r0 + RS a) lda + k] B[(c0 + CS c) ldb + k], K a multiple of 4.
@@ -134,237 +160,348 @@ __device__ __forceinline__ void mm_rr(float (&acc)[RA][4], const float* A, int l
     }
 }
 
-// --------------------------------------------------------------- T and X
-// One CTA per chunk and value head: tx[chunk] = T then X, 64 x 64 each.
-template <typename E>
-__global__ void __launch_bounds__(NT) delta_prep(const E* __restrict__ q, const E* __restrict__ k,
+// --------------------------------------------------------------- what does not wait for the state
+// Floats of one chunk and value head as the scans read them: the 64 rows that
+// multiply the state (128 with those of the output) and the 64 rows that update
+// it, all of stride N + 4, then e^{G_end}.
+__host__ __device__ constexpr int image_floats(int rows, int N) { return (rows + C) * (N + 4) + 4; }
+
+struct Made {
+    float *fwd, *uo;        // forward image (128 rows; 64 for the gradients), [T; scale X] beta V (T's alone for the gradients)
+    float *back, *z, *add;  // backward image, scale X^T dO [64, P], scale (e^G Q)^T dO [N, P]
+};
+
+// One CTA per chunk and value head.  Bound by shared memory: 4 x 4 outputs a
+// thread read 8 float4 for 64 multiply-adds.
+template <bool BACK>
+__global__ void __launch_bounds__(NT) delta_prep(const float* __restrict__ q, const float* __restrict__ k,
+                                                 const float* __restrict__ v, const float* __restrict__ dout,
                                                  const float* __restrict__ g, const float* __restrict__ beta,
-                                                 const int* __restrict__ lens, float* __restrict__ tx, Geo ge) {
+                                                 const int* __restrict__ lens, float scale, Made made, Geo ge) {
     extern __shared__ __align__(16) float sm[];
     __shared__ Decays d;
+    __shared__ float s_bin[C], s_one[C];
     const int tid = threadIdx.x, c = blockIdx.x % ge.nc, bh = blockIdx.x / ge.nc;
-    const int b = bh / ge.H, h = bh % ge.H, KH = ge.H / ge.G;
+    const int b = bh / ge.H, h = bh % ge.H, KH = ge.H / ge.G, N = ge.N, P = ge.P;
     const int n = min(row_len(lens, b, ge.T) - c * C, C);
     if (n <= 0) return;
-    const int LK = ge.N + 4;
+    const int LK = N + 4, LP = P + 4;
     float* sk = sm;
     float* sq = sk + C * LK;
-    float* a = sq + C * LK;
-    float* p = a + C * LT;
-    float* w = p + C * LT;
-    const int64_t t0 = (int64_t)b * ge.T + (int64_t)c * C;
-    const int64_t ko = (t0 * KH + h / ge.G) * ge.N, ks = (int64_t)KH * ge.N;
-    load_rows(sk, LK, k + ko, ks, C, ge.N, n, tid);
-    load_rows(sq, LK, q + ko, ks, C, ge.N, n, tid);
+    float* sv = sq + C * LK;  // V, then dO
+    float* t = sv + C * LP;
+    float* x = t + C * LT;
+    float* w = x + C * LT;
+    const int64_t t0 = (int64_t)b * ge.T + (int64_t)c * C, ci = blockIdx.x;
+    const int64_t ko = (t0 * KH + h / ge.G) * N, ks = (int64_t)KH * N, vo = (t0 * ge.H + h) * P, vs = (int64_t)ge.H * P;
+    load_rows(sk, LK, k + ko, ks, C, N, n, tid);
+    load_rows(sq, LK, q + ko, ks, C, N, n, tid);
+    load_rows(sv, LP, v + vo, vs, C, P, n, tid);
     if (tid < 32) chunk_decays(d, g + t0 * ge.H + h, beta + t0 * ge.H + h, ge.H, n, tid);
     __syncthreads();
-    const int ti = tid / 16, tj = tid % 16;
-    float kk[4][4] = {}, qk[4][4] = {};
-    mm_rr<4, 16, 16>(kk, sk, LK, sk, LK, ge.N, ti, tj);
-    mm_rr<4, 16, 16>(qk, sq, LK, sk, LK, ge.N, ti, tj);
+    if (tid < C) s_bin[tid] = d.beta[tid] * d.in[tid], s_one[tid] = 1.f;
+    {
+        const int ti = tid / 16, tj = tid % 16;
+        float kk[4][4] = {}, qk[4][4] = {};
+        mm_rr<4, 16, 16>(kk, sk, LK, sk, LK, N, ti, tj);
+        mm_rr<4, 16, 16>(qk, sq, LK, sk, LK, N, ti, tj);
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+        for (int a = 0; a < 4; ++a)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int i = ti + 16 * x, j = tj + 16 * y;
-            const float m = i >= j ? decay_between(d, i, j) : 0.f;
-            a[i * LT + j] = i > j ? d.beta[i] * (m * kk[x][y]) : 0.f;
-            p[i * LT + j] = i >= j ? m * qk[x][y] : 0.f;
-        }
+            for (int y = 0; y < 4; ++y) {
+                const int i = ti + 16 * a, j = tj + 16 * y;
+                const float m = i >= j ? decay_between(d, i, j) : 0.f;
+                t[i * LT + j] = i > j ? d.beta[i] * (m * kk[a][y]) : 0.f;
+                x[i * LT + j] = i >= j ? m * qk[a][y] : 0.f;
+            }
+    }
     __syncthreads();
-    tri_inverse_in_place<LT>(a, w, tid);
-    const float* t = a;
-    float x[4][4] = {};
-    mm_rk<4, 16>(x, p, LT, t, LT, C, ti, 4 * tj);
-    float* out = tx + (int64_t)blockIdx.x * 2 * C * C;
+    tri_inverse_in_place<LT>(t, w, tid);
+    const int r0 = 4 * (tid / 16), c0 = 4 * (tid % 16);
+    {
+        float acc[4][4] = {}, none[4][4];
+        mm_lower<false>(acc, none, x, nullptr, s_one, t, LT, r0, c0);
+        __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int i = ti + 16 * r;
-        *reinterpret_cast<float4*>(out + i * C + 4 * tj) = ld4(t + i * LT + 4 * tj);
-        *reinterpret_cast<float4*>(out + C * C + i * C + 4 * tj) = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
+        for (int a = 0; a < 4; ++a) st4(x + (r0 + a) * LT + c0, acc[a], 1.f);
+    }
+    __syncthreads();
+    float* img = made.fwd + ci * image_floats(BACK ? C : 2 * C, N);
+    float* rows = img + (BACK ? C : 2 * C) * LK;  // the rows that update the state
+    float* bimg = BACK ? made.back + ci * image_floats(C, N) : nullptr;
+    for (int col = c0; col < N; col += 64) {
+        float tk[4][4] = {}, xk[4][4] = {};
+        mm_lower<!BACK>(tk, xk, t, x, s_bin, sk, LK, r0, col);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const int i = r0 + a;
+            const float4 kr = ld4(sk + i * LK + col);
+            st4(img + i * LK + col, tk[a], -1.f);
+            const float ku[4] = {kr.x, kr.y, kr.z, kr.w};
+            st4(rows + i * LK + col, ku, d.out[i]);
+            if constexpr (BACK) {
+                st4(bimg + (C + i) * LK + col, ku, -s_bin[i]);
+            } else {
+                const float4 qr = ld4(sq + i * LK + col);
+                const float in = d.in[i];
+                const float y[4] = {fmaf(in, qr.x, -xk[a][0]), fmaf(in, qr.y, -xk[a][1]), fmaf(in, qr.z, -xk[a][2]),
+                                    fmaf(in, qr.w, -xk[a][3])};
+                st4(img + (C + i) * LK + col, y, scale);
+            }
+        }
+        if constexpr (BACK) {
+            float wk[4][4] = {};
+            mm_kr(wk, t, LT, d.out, sk, LK, r0, r0, col);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) st4(bimg + (r0 + a) * LK + col, wk[a], 1.f);
+        }
+    }
+    if (tid < 4) {
+        rows[C * LK + tid] = d.all;
+        if (BACK) bimg[2 * C * LK + tid] = d.all;
+    }
+    float* uo = made.uo + ci * (BACK ? C : 2 * C) * P;
+    for (int col = c0; col < P; col += 64) {
+        float tv[4][4] = {}, xv[4][4] = {};
+        mm_lower<!BACK>(tv, xv, t, x, d.beta, sv, LP, r0, col);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            st4(uo + (r0 + a) * P + col, tv[a], 1.f);
+            if (!BACK) st4(uo + (C + r0 + a) * P + col, xv[a], scale);
+        }
+    }
+    if constexpr (BACK) {
+        __syncthreads();
+        load_rows(sv, LP, dout + vo, vs, C, P, n, tid);
+        __syncthreads();
+        float* z = made.z + ci * C * P;
+        float* add = made.add + ci * N * P;
+        for (int col = c0; col < P; col += 64) {
+            float xd[4][4] = {};
+            mm_kr(xd, x, LT, s_one, sv, LP, r0, r0, col);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) st4(z + (r0 + a) * P + col, xd[a], scale);
+            for (int r = r0; r < N; r += 64) {
+                float qd[4][4] = {};
+                mm_kr(qd, sq, LK, d.in, sv, LP, 0, r, col);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) st4(add + (r + a) * P + col, qd[a], scale);
+            }
+        }
     }
 }
 
-// --------------------------------------------------------------- forward scan
+// --------------------------------------------------------------- the scans
 // One CTA per value head and slice of PW state columns (they never mix),
-// walking the chunks.  With `states`, the state entering each chunk and the
-// writes U are kept for the gradients and no output is made.
-template <typename E>
-__global__ void __launch_bounds__(NT) delta_scan(const E* __restrict__ q, const E* __restrict__ k,
-                                                 const E* __restrict__ v, const float* __restrict__ g,
-                                                 const float* __restrict__ beta, const float* __restrict__ tx,
-                                                 const float* h0, const int* __restrict__ lens, float scale,
-                                                 E* __restrict__ o, float* h_final, float* __restrict__ states,
-                                                 float* __restrict__ writes, Geo ge) {
-    extern __shared__ __align__(16) float sm[];
-    __shared__ Decays d;
-    const int np = (ge.P + PW - 1) / PW;
-    const int tid = threadIdx.x, p0 = (int)(blockIdx.x % np) * PW, bh = (int)(blockIdx.x / np);
-    const int b = bh / ge.H, h = bh % ge.H, KH = ge.H / ge.G, N = ge.N, P = ge.P;
-    const int len = row_len(lens, b, ge.T), LK = N + 4;
-    float* kq = sm;                  // K rows then Q rows
-    float* stx = kq + 2 * C * LK;    // T rows then X rows
-    float* s = stx + 2 * C * LT;
-    float* r = s + N * LS;
-    float* u = r + C * LS;
-    const int rg = tid / 8, c0 = 4 * (tid % 8);
-    const int64_t so = (int64_t)bh * N * P;
-    if (h0) {
-        load_slice(s, h0 + so, P, N, p0, P, N, tid);
-    } else {
-        for (int e = tid; e < N * LS; e += NT) s[e] = 0.f;
-    }
-    for (int c = 0; c * C < len; ++c) {
-        const int n = min(len - c * C, C);
-        const int64_t t0 = (int64_t)b * ge.T + (int64_t)c * C;
-        const int64_t ko = (t0 * KH + h / ge.G) * N, ks = (int64_t)KH * N;
-        const int64_t ci = (int64_t)bh * ge.nc + c;
-        __syncthreads();
-        load_rows(kq, LK, k + ko, ks, C, N, n, tid);
-        if (o) load_rows(kq + C * LK, LK, q + ko, ks, C, N, n, tid);
-        load_rows(stx, LT, tx + ci * 2 * C * C, C, 2 * C, C, 2 * C, tid);
-        load_slice(r, v + (t0 * ge.H + h) * P, (int64_t)ge.H * P, C, p0, P, n, tid);
-        if (tid < 32) chunk_decays(d, g + t0 * ge.H + h, beta + t0 * ge.H + h, ge.H, n, tid);
-        __syncthreads();
-        if (states)
-            for (int e = tid; e < N * PW; e += NT)
-                if (p0 + e % PW < P) states[ci * N * P + (int64_t)(e / PW) * P + p0 + e % PW] = s[(e / PW) * LS + e % PW];
-        float ks_[4][4] = {};
-        mm_rk<4, 32>(ks_, kq, LK, s, LS, N, rg, c0);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int i = rg + 32 * x;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) r[i * LS + c0 + y] = d.beta[i] * (r[i * LS + c0 + y] - d.in[i] * ks_[x][y]);
-        }
-        __syncthreads();
-        float ur[4][4] = {};
-        mm_rk<4, 32>(ur, stx, LT, r, LS, C, rg, c0);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int i = rg + 32 * x;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                u[i * LS + c0 + y] = d.out[i] * ur[x][y];
-                if (p0 + c0 + y >= P) continue;
-                if (writes) writes[ci * C * P + (int64_t)i * P + p0 + c0 + y] = ur[x][y];
-                if (o && i < n)
-                    o[((t0 + i) * ge.H + h) * P + p0 + c0 + y] =
-                        from_f<E>(scale * (d.in[i] * ks_[x + 2][y] + ur[x + 2][y]));
-            }
-        }
-        __syncthreads();
-        if (4 * rg < N) {
-            float ns[4][4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) ns[x][y] = d.all * s[(4 * rg + x) * LS + c0 + y];
-            mm_kr<4>(ns, kq, LK, u, LS, C, 4 * rg, c0);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) s[(4 * rg + x) * LS + c0 + y] = ns[x][y];
-        }
-    }
-    __syncthreads();
-    if (h_final)
-        for (int e = tid; e < N * PW; e += NT)
-            if (p0 + e % PW < P) h_final[so + (int64_t)(e / PW) * P + p0 + e % PW] = s[(e / PW) * LS + e % PW];
-    if (o)
-        for (int64_t e = tid; e < (int64_t)(ge.T - len) * PW; e += NT)
-            if (p0 + (int)(e % PW) < P)
-                o[(((int64_t)b * ge.T + len + e / PW) * ge.H + h) * P + p0 + e % PW] = from_f<E>(0.f);
+// walking the chunks with the next chunk's image on its way (cp.async).  Shared
+// memory hands a warp 128 bytes a cycle, the same word to all lanes or not, so
+// what bounds both products is the bytes a thread reads for a multiply-add:
+// tiles of 4 rows x 4 columns (2 bytes; a row x 8 columns, 4.5, took twice as
+// long), the sum split over neighbouring lanes so that every thread has a tile
+// and joined by shuffles, which leave each lane its rows of the tile.
+struct ScanIo {
+    const float *img, *init, *add;  // as made; add: forward null
+    const float* s0;                // the state before the first chunk, or null
+    float* s_end;                   // after the last, or null
+    float* kept;                    // the state entering each chunk (backward: leaving), or null
+    float* made;                    // the first 64 rows of the first product, U or Z, or null
+    float* o;                       // outputs (ROWS = 128)
+};
+
+constexpr int LU = PW + 8;  // row stride of U
+__host__ __device__ constexpr int state_stride(int rows, int N) { return (N + 31) / 32 * 32 + 4 * (NT / rows); }
+
+template <int ROWS>
+constexpr uint32_t scan_smem(int N) {
+    return sizeof(float) * (2 * image_floats(ROWS, N) + PW * state_stride(ROWS, N) + C * LU);
 }
 
-// --------------------------------------------------------------- backward scan
-// The same walk from the last chunk: the gradient of the state leaving each
-// chunk is kept in `after`, Z in `zs`.
-template <typename E>
-__global__ void __launch_bounds__(NT) delta_back_scan(const E* __restrict__ q, const E* __restrict__ k,
-                                                      const E* __restrict__ dout, const float* __restrict__ g,
-                                                      const float* __restrict__ beta, const float* __restrict__ tx,
-                                                      const float* dh, const int* __restrict__ lens, float scale,
-                                                      float* gh0, float* __restrict__ after,
-                                                      float* __restrict__ zs, Geo ge) {
-    extern __shared__ __align__(16) float sm[];
-    __shared__ Decays d;
-    const int np = (ge.P + PW - 1) / PW;
-    const int tid = threadIdx.x, p0 = (int)(blockIdx.x % np) * PW, bh = (int)(blockIdx.x / np);
-    const int b = bh / ge.H, h = bh % ge.H, KH = ge.H / ge.G, N = ge.N, P = ge.P;
-    const int len = row_len(lens, b, ge.T), LK = N + 4;
-    float* kq = sm;
-    float* stx = kq + 2 * C * LK;
-    float* s = stx + 2 * C * LT;  // dS
-    float* r = s + N * LS;        // scale dO, then scale e^G dO
-    float* u = r + C * LS;        // e^{G_end - G} K dS, then -e^G beta Z
-    const int rg = tid / 8, c0 = 4 * (tid % 8);
-    const int64_t so = (int64_t)bh * N * P;
-    if (dh) {
-        load_slice(s, dh + so, P, N, p0, P, N, tid);
+// Sums y over the SPLIT neighbouring lanes that hold parts of it; lane l of
+// them gets rows l 4 / SPLIT and on, in y's first.
+template <int SPLIT>
+__device__ __forceinline__ void join(float (&y)[4][4], int l) {
+    if (SPLIT == 4) {
+        const bool high = l & 2;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float other = __shfl_xor_sync(0xffffffffu, high ? y[a][i] : y[a + 2][i], 2);
+                y[a][i] = (high ? y[a + 2][i] : y[a][i]) + other;
+            }
+        const bool odd = l & 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? y[0][i] : y[1][i], 1);
+            y[0][i] = (odd ? y[1][i] : y[0][i]) + other;
+        }
     } else {
-        for (int e = tid; e < N * LS; e += NT) s[e] = 0.f;
+        const bool odd = l & 1;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? y[a][i] : y[a + 2][i], 1);
+                y[a][i] = (odd ? y[a + 2][i] : y[a][i]) + other;
+            }
     }
-    for (int c = (len + C - 1) / C - 1; c >= 0; --c) {
-        const int n = min(len - c * C, C);
-        const int64_t t0 = (int64_t)b * ge.T + (int64_t)c * C;
-        const int64_t ko = (t0 * KH + h / ge.G) * N, ks = (int64_t)KH * N;
+}
+
+template <int ROWS, int ND, bool BACK>
+__device__ __forceinline__ void scan_body(const ScanIo& io, int bh, int p0, const int* __restrict__ lens, const Geo& ge,
+                                          float* sm) {
+    // Lanes that share a tile of the first product (ROWS x PW) and of the second
+    // (ND x PW), and the rows each is left with.
+    constexpr int S1 = NT / ROWS, S2 = NT / ND, R1 = 4 / S1, R2 = 4 / S2;
+    const int tid = threadIdx.x, b = bh / ge.H, h = bh % ge.H, N = ge.N, P = ge.P, LA = N + 4;
+    const int LS = state_stride(ROWS, N);
+    const int len = row_len(lens, b, ge.T), nck = (len + C - 1) / C;
+    const int image = image_floats(ROWS, N);
+    float* st = sm + 2 * image;  // the state: column 4 x + i of the slice in row 4 i + x
+    float* su = st + PW * LS;    // U or Z, [64][LU]
+    const int l1 = tid % S1, x1 = tid / S1 % 4, tile1 = tid / (4 * S1) * 4, row = tile1 + R1 * l1;
+    const int l2 = tid % S2, x2 = tid / S2 % 4, tile2 = tid / (4 * S2) * 4, nr = tile2 + R2 * l2;
+    const bool there = tile2 < N;  // (all of a warp, or none: N is a multiple of 16)
+    const int64_t so = ((int64_t)bh * N + nr) * P + p0 + 4 * x2;  // this thread's state
+    auto load = [&](int c, int buf) {
+        const float* src = io.img + ((int64_t)bh * ge.nc + c) * image;
+        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(sm + buf * image);
+        for (int e = tid; e < image / 4; e += NT)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * e), "l"(src + 4 * e) : "memory");
+    };
+    float4 init[R1], add[R2];
+    auto load_init = [&](int c) {
+        const float* src = io.init + (((int64_t)bh * ge.nc + c) * ROWS + row) * P + p0 + 4 * x1;
+#pragma unroll
+        for (int a = 0; a < R1; ++a) init[a] = ld4(src + a * P);
+        if (BACK && there) {
+            const float* more = io.add + (((int64_t)bh * ge.nc + c) * N + nr) * P + p0 + 4 * x2;
+#pragma unroll
+            for (int a = 0; a < R2; ++a) add[a] = ld4(more + a * P);
+        }
+    };
+    float s[R2][4];
+#pragma unroll
+    for (int a = 0; a < R2; ++a) {
+        const float4 v = io.s0 && there ? ld4(io.s0 + so + a * P) : make_float4(0.f, 0.f, 0.f, 0.f);
+        s[a][0] = v.x, s[a][1] = v.y, s[a][2] = v.z, s[a][3] = v.w;
+    }
+    auto put_state = [&] {
+#pragma unroll
+        for (int a = 0; a < R2; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st[(4 * i + x2) * LS + nr + a] = s[a][i];
+    };
+    auto chunk = [&](int it) { return BACK ? nck - 1 - it : it; };
+    if (there) put_state();
+    if (nck > 0) {
+        load(chunk(0), 0);
+        load_init(chunk(0));
+    }
+    for (int it = 0; it < nck; ++it) {
+        const int c = chunk(it);
         const int64_t ci = (int64_t)bh * ge.nc + c;
+        const float* img = sm + (it & 1) * image;
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
-        load_rows(kq, LK, k + ko, ks, C, N, n, tid);
-        load_rows(kq + C * LK, LK, q + ko, ks, C, N, n, tid);
-        load_rows(stx, LT, tx + ci * 2 * C * C, C, 2 * C, C, 2 * C, tid);
-        load_slice(r, dout + (t0 * ge.H + h) * P, (int64_t)ge.H * P, C, p0, P, n, tid);
-        if (tid < 32) chunk_decays(d, g + t0 * ge.H + h, beta + t0 * ge.H + h, ge.H, n, tid);
-        __syncthreads();
-        for (int e = tid; e < N * PW; e += NT)
-            if (p0 + e % PW < P) after[ci * N * P + (int64_t)(e / PW) * P + p0 + e % PW] = s[(e / PW) * LS + e % PW];
-        float w[2][4] = {};
-        mm_rk<2, 32>(w, kq, LK, s, LS, N, rg, c0);
+        if (it + 1 < nck) load(chunk(it + 1), (it + 1) & 1);
+        {
+            f2 acc[4][4] = {};  // sums over even and odd k
+#pragma unroll 2
+            for (int e = 4 * l1; e < N; e += 4 * S1) {
+                ulonglong2 x[4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+                for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(st + (4 * i + x1) * LS + e);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int i = rg + 32 * x;
-                u[i * LS + c0 + y] = d.out[i] * w[x][y];
-                r[i * LS + c0 + y] *= scale;
+                for (int a = 0; a < 4; ++a) {
+                    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(img + (tile1 + a) * LA + e);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[a][i] = fma2(w.y, x[i].y, fma2(w.x, x[i].x, acc[a][i]));
+                }
             }
-        __syncthreads();
-        float z[2][4] = {};
-        mm_kr<2>(z, stx, LT, u, LS, C, 2 * rg, c0);
-        mm_kr<2>(z, stx + C * LT, LT, r, LS, C, 2 * rg, c0);
-        __syncthreads();
+            float y[4][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int i = 2 * rg + x;
+            for (int a = 0; a < 4; ++a)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float gvv = d.beta[i] * z[x][y];
-                u[i * LS + c0 + y] = -d.in[i] * gvv;
-                r[i * LS + c0 + y] *= d.in[i];
-                if (p0 + c0 + y >= P) continue;
-                zs[ci * C * P + (int64_t)i * P + p0 + c0 + y] = z[x][y];
+                for (int i = 0; i < 4; ++i) y[a][i] = sum2(acc[a][i]);
+            join<S1>(y, l1);
+#pragma unroll
+            for (int a = 0; a < R1; ++a) {
+                const float4 z = make_float4(y[a][0] + init[a].x, y[a][1] + init[a].y, y[a][2] + init[a].z, y[a][3] + init[a].w);
+                const int r = row + a;
+                if (ROWS == C || tile1 < C) {
+                    *reinterpret_cast<float4*>(su + r * LU + 4 * x1) = z;
+                    if (io.made) *reinterpret_cast<float4*>(io.made + (ci * C + r) * P + p0 + 4 * x1) = z;
+                } else if (c * C + r - C < len) {
+                    *reinterpret_cast<float4*>(io.o + (((int64_t)b * ge.T + (int64_t)c * C + r - C) * ge.H + h) * P + p0 + 4 * x1) = z;
+                }
             }
         }
+        float4 more[R2];
+        if (BACK)
+#pragma unroll
+            for (int a = 0; a < R2; ++a) more[a] = add[a];
+        if (it + 1 < nck) load_init(chunk(it + 1));
         __syncthreads();
-        if (4 * rg < N) {
-            float ns[4][4];
+        if (there) {
+            if (io.kept)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+                for (int a = 0; a < R2; ++a)
+                    *reinterpret_cast<float4*>(io.kept + (ci * N + nr + a) * P + p0 + 4 * x2) =
+                        make_float4(s[a][0], s[a][1], s[a][2], s[a][3]);
+            const float* ku = img + ROWS * LA + tile2;
+            f2 d[2][4] = {};  // pairs of rows
+#pragma unroll 4
+            for (int i = l2; i < C; i += S2) {
+                const ulonglong2 kv = *reinterpret_cast<const ulonglong2*>(ku + i * LA);
+                const float4 u = ld4(su + i * LU + 4 * x2);
+                const float w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int y = 0; y < 4; ++y) ns[x][y] = d.all * s[(4 * rg + x) * LS + c0 + y];
-            mm_kr<4>(ns, kq, LK, u, LS, C, 4 * rg, c0);
-            mm_kr<4>(ns, kq + C * LK, LK, r, LS, C, 4 * rg, c0);
+                for (int y = 0; y < 4; ++y) {
+                    const f2 u2 = mk2(w[y], w[y]);
+                    d[0][y] = fma2(kv.x, u2, d[0][y]);
+                    d[1][y] = fma2(kv.y, u2, d[1][y]);
+                }
+            }
+            float y[4][4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int i = 0; i < 4; ++i) un2(d[0][i], y[0][i], y[1][i]), un2(d[1][i], y[2][i], y[3][i]);
+            join<S2>(y, l2);
+            const float all = img[(ROWS + C) * LA];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) s[(4 * rg + x) * LS + c0 + y] = ns[x][y];
+            for (int a = 0; a < R2; ++a) {
+                if (BACK) y[a][0] += more[a].x, y[a][1] += more[a].y, y[a][2] += more[a].z, y[a][3] += more[a].w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[a][i] = fmaf(all, s[a][i], y[a][i]);
+            }
+            put_state();
         }
     }
-    __syncthreads();
-    if (gh0)
-        for (int e = tid; e < N * PW; e += NT)
-            if (p0 + e % PW < P) gh0[so + (int64_t)(e / PW) * P + p0 + e % PW] = s[(e / PW) * LS + e % PW];
+    if (io.s_end && there)
+#pragma unroll
+        for (int a = 0; a < R2; ++a)
+            *reinterpret_cast<float4*>(io.s_end + so + a * P) = make_float4(s[a][0], s[a][1], s[a][2], s[a][3]);
+    if (ROWS > C)  // behind the row's last token
+        for (int64_t e = tid; e < (int64_t)(ge.T - len) * PW; e += NT)
+            io.o[(((int64_t)b * ge.T + len + e / PW) * ge.H + h) * P + p0 + e % PW] = 0.f;
+}
+
+template <int ND>
+__global__ void __launch_bounds__(NT) delta_scan(ScanIo io, const int* __restrict__ lens, Geo ge) {
+    extern __shared__ __align__(16) float sm[];
+    const int np = ge.P / PW;
+    scan_body<2 * C, ND, false>(io, blockIdx.x / np, (int)(blockIdx.x % np) * PW, lens, ge, sm);
+}
+
+// Both of the gradients' scans, which do not need one another.
+template <int ND>
+__global__ void __launch_bounds__(NT) delta_both_scans(ScanIo back, ScanIo fwd, const int* __restrict__ lens, Geo ge) {
+    extern __shared__ __align__(16) float sm[];
+    const int np = ge.P / PW, half = gridDim.x / 2, i = blockIdx.x % half;
+    if ((int)blockIdx.x < half)
+        scan_body<C, ND, true>(back, i / np, i % np * PW, lens, ge, sm);
+    else
+        scan_body<C, ND, false>(fwd, i / np, i % np * PW, lens, ge, sm);
 }
 
 // --------------------------------------------------------------- dQ, dK, dV, dg, dbeta
@@ -571,7 +708,6 @@ __global__ void __launch_bounds__(256) delta_sum_heads(const float4* __restrict_
 }
 
 int64_t chunks(const DeltaArgs& a) { return (a.T + C - 1) / C; }
-size_t tx_floats(const DeltaArgs& a) { return (size_t)(a.Bz * a.H * chunks(a)) * 2 * C * C; }
 size_t state_floats(const DeltaArgs& a) { return (size_t)(a.Bz * a.H * chunks(a)) * a.N * a.P; }
 size_t write_floats(const DeltaArgs& a) { return (size_t)(a.Bz * a.H * chunks(a)) * C * a.P; }
 size_t part_floats(const DeltaArgs& a) { return a.H == a.KH ? 0 : (size_t)(a.Bz * a.T * a.H) * a.N; }
@@ -584,35 +720,66 @@ cudaError_t allow_smem(F* f, size_t bytes) {
 Geo geo(const DeltaArgs& a) {
     return Geo{(int)a.T, (int)a.H, (int)(a.H / a.KH), (int)a.N, (int)a.P, (int)chunks(a)};
 }
-size_t scan_smem(const DeltaArgs& a) { return sizeof(float) * (2 * C * (a.N + 4) + 2 * C * LT + a.N * LS + 2 * C * LS); }
+// What delta_prep makes, laid out in the workspace.
+Made made_in(const DeltaArgs& a, float* ws, bool back) {
+    const int64_t n = a.Bz * a.H * chunks(a);
+    Made m{};
+    m.fwd = ws;
+    m.uo = m.fwd + n * image_floats(back ? C : 2 * C, (int)a.N);
+    m.back = m.uo + n * (back ? C : 2 * C) * a.P;
+    m.z = m.back + (back ? n * image_floats(C, (int)a.N) : 0);
+    m.add = m.z + (back ? n * C * a.P : 0);
+    return m;
+}
+size_t made_floats(const DeltaArgs& a, bool back) {
+    const int64_t n = a.Bz * a.H * chunks(a);
+    const int64_t one = image_floats(back ? C : 2 * C, (int)a.N) + (back ? C : 2 * C) * a.P;
+    return (size_t)(n * (one + (back ? image_floats(C, (int)a.N) + (C + a.N) * a.P : 0)));
+}
 
-template <typename E>
-cudaError_t prep(const DeltaArgs& a, float* tx, cudaStream_t st) {
-    const size_t sm = sizeof(float) * (2 * C * (a.N + 4) + 2 * C * LT + 32 * 32);
-    cudaError_t e = allow_smem(delta_prep<E>, sm);
+template <bool BACK>
+cudaError_t prep(const DeltaArgs& a, const Made& m, cudaStream_t st) {
+    const size_t sm = sizeof(float) * (2 * C * (a.N + 4) + C * (a.P + 4) + 2 * C * LT + 32 * 32);
+    const cudaError_t e = allow_smem(delta_prep<BACK>, sm);
     if (e != cudaSuccess) return e;
-    delta_prep<E><<<(unsigned)(a.Bz * a.H * chunks(a)), NT, sm, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), a.g, a.beta, a.lens, tx, geo(a));
+    delta_prep<BACK><<<(unsigned)(a.Bz * a.H * chunks(a)), NT, sm, st>>>(
+        static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v),
+        static_cast<const float*>(a.dout), a.g, a.beta, a.lens, a.scale, m, geo(a));
     return cudaGetLastError();
 }
 
-template <typename E>
-cudaError_t scan(const DeltaArgs& a, const float* tx, void* o, float* h_final, float* states, float* writes,
-                 cudaStream_t st) {
-    const size_t sm = scan_smem(a);
-    cudaError_t e = allow_smem(delta_scan<E>, sm);
+template <int ND>
+cudaError_t scan(const DeltaArgs& a, const ScanIo& io, cudaStream_t st) {
+    const uint32_t sm = scan_smem<2 * C>((int)a.N);
+    const cudaError_t e = allow_smem(delta_scan<ND>, sm);
     if (e != cudaSuccess) return e;
-    delta_scan<E><<<(unsigned)((a.P + PW - 1) / PW * a.Bz * a.H), NT, sm, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), a.g, a.beta, tx, a.h0, a.lens,
-        a.scale, static_cast<E*>(o), h_final, states, writes, geo(a));
+    delta_scan<ND><<<(unsigned)(a.Bz * a.H * (a.P / PW)), NT, sm, st>>>(io, a.lens, geo(a));
+    return cudaGetLastError();
+}
+template <int ND>
+cudaError_t both(const DeltaArgs& a, const ScanIo& back, const ScanIo& fwd, cudaStream_t st) {
+    const uint32_t sm = scan_smem<C>((int)a.N);
+    const cudaError_t e = allow_smem(delta_both_scans<ND>, sm);
+    if (e != cudaSuccess) return e;
+    delta_both_scans<ND><<<(unsigned)(2 * a.Bz * a.H * (a.P / PW)), NT, sm, st>>>(back, fwd, a.lens, geo(a));
     return cudaGetLastError();
 }
 
-template <typename E>
 cudaError_t forward(const DeltaArgs& a, void* ws, cudaStream_t st) {
-    float* tx = static_cast<float*>(ws);
-    cudaError_t e = prep<E>(a, tx, st);
-    return e != cudaSuccess ? e : scan<E>(a, tx, a.o, a.h_final, nullptr, nullptr, st);
+    const Made m = made_in(a, static_cast<float*>(ws), false);
+    const cudaError_t e = prep<false>(a, m, st);
+    if (e != cudaSuccess) return e;
+    const ScanIo io{m.fwd, m.uo, nullptr, a.h0, a.h_final, nullptr, nullptr, static_cast<float*>(a.o)};
+    return a.N <= 64 ? scan<64>(a, io, st) : scan<128>(a, io, st);
+}
+cudaError_t both_scans(const DeltaArgs& a, float* ws, float* states, float* after, float* writes, float* zs,
+                       cudaStream_t st) {
+    const Made m = made_in(a, ws, true);
+    const cudaError_t e = prep<true>(a, m, st);
+    if (e != cudaSuccess) return e;
+    const ScanIo fwd{m.fwd, m.uo, nullptr, a.h0, nullptr, states, writes, nullptr};
+    const ScanIo back{m.back, m.z, m.add, a.dh_final, a.gh0, after, zs, nullptr};
+    return a.N <= 64 ? both<64>(a, back, fwd, st) : both<128>(a, back, fwd, st);
 }
 
 template <typename E, typename O>
@@ -637,20 +804,12 @@ cudaError_t backward(const DeltaArgs& a, void* ws, cudaStream_t st) {
     float* zs = writes + write_floats(a);
     float* pq = zs + write_floats(a);
     float* pk = pq + part_floats(a);
-    float* rest = pk + part_floats(a);  // T and X; the tensor-core kernels' own
+    float* rest = pk + part_floats(a);  // what prep makes; the tensor-core kernels' own
     cudaError_t e;
     if constexpr (TC) {
         e = launch_back_scans_tc(a, rest, states, after, writes, zs, st);
     } else {
-        e = prep<E>(a, rest, st);
-        if (e == cudaSuccess) e = scan<E>(a, rest, nullptr, nullptr, states, writes, st);
-        const size_t sm = scan_smem(a);
-        if (e == cudaSuccess) e = allow_smem(delta_back_scan<E>, sm);
-        if (e != cudaSuccess) return e;
-        delta_back_scan<E><<<(unsigned)((a.P + PW - 1) / PW * a.Bz * a.H), NT, sm, st>>>(
-            static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.dout), a.g, a.beta, rest,
-            a.dh_final, a.lens, a.scale, a.gh0, after, zs, geo(a));
-        e = cudaGetLastError();
+        e = both_scans(a, rest, states, after, writes, zs, st);
     }
     if (e != cudaSuccess) return e;
     // key heads that are shared: a part per value head, summed in order
@@ -672,15 +831,15 @@ cudaError_t backward(const DeltaArgs& a, void* ws, cudaStream_t st) {
 }  // namespace delta
 
 size_t delta_workspace_bytes(const DeltaArgs& a) {
-    return a.dtype == CSSD_F32 ? sizeof(float) * delta::tx_floats(a) : delta::tc_workspace_bytes(a);
+    return a.dtype == CSSD_F32 ? sizeof(float) * delta::made_floats(a, false) : delta::tc_workspace_bytes(a);
 }
 size_t delta_backward_workspace_bytes(const DeltaArgs& a) {
     return sizeof(float) * (2 * delta::state_floats(a) + 2 * delta::write_floats(a) + 2 * delta::part_floats(a)) +
-           (a.dtype == CSSD_F32 ? sizeof(float) * delta::tx_floats(a) : delta::tc_back_bytes(a));
+           (a.dtype == CSSD_F32 ? sizeof(float) * delta::made_floats(a, true) : delta::tc_back_bytes(a));
 }
 
 cudaError_t launch_delta_forward(const DeltaArgs& a, void* ws, cudaStream_t st) {
-    return a.dtype == CSSD_F32 ? delta::forward<float>(a, ws, st) : delta::launch_forward_tc(a, ws, st);
+    return a.dtype == CSSD_F32 ? delta::forward(a, ws, st) : delta::launch_forward_tc(a, ws, st);
 }
 cudaError_t launch_delta_backward(const DeltaArgs& a, void* ws, cudaStream_t st) {
     if (a.dtype == CSSD_BF16) return delta::backward<__nv_bfloat16>(a, ws, st);
