@@ -40,7 +40,6 @@ namespace {
 
 constexpr int NT = 256;       // threads of every kernel here
 constexpr int LT = C + 4;     // row stride of a 64 x 64 matrix in shared memory
-constexpr int PW = 16;        // state columns a scan CTA owns
 
 struct Geo {
     int T, H, G, N, P, nc;  // G: value heads per key head
@@ -68,24 +67,25 @@ __device__ void load_rows(float* dst, int ld, const T* src, int64_t stride, int 
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// acc[a][c] += sum_k A[(r0 + RS a) lda + k] B[k ldb + c0 + c], K a multiple of 4.
-template <int RA, int RS>
-__device__ __forceinline__ void mm_rk(float (&acc)[RA][4], const float* A, int lda, const float* B, int ldb, int K,
-                                      int r0, int c0) {
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+
+// A0 B^T and A1 B^T, rows r0 + 16 a and columns c0 + 16 c, without the 16 x 16
+// blocks above the diagonal.
+__device__ __forceinline__ void mm_lower_rr(float (&acc0)[4][4], float (&acc1)[4][4], const float* A0, const float* A1,
+                                            int lda, const float* B, int ldb, int K, int r0, int c0) {
     for (int k = 0; k < K; k += 4) {
         float4 b[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) b[u] = ld4(B + (k + u) * ldb + c0);
+        for (int c = 0; c < 4; ++c) b[c] = ld4(B + (c0 + 16 * c) * ldb + k);
 #pragma unroll
-        for (int a = 0; a < RA; ++a) {
-            const float4 v = ld4(A + (r0 + RS * a) * lda + k);
-            const float w[4] = {v.x, v.y, v.z, v.w};
+        for (int a = 0; a < 4; ++a) {
+            const float4 u = ld4(A0 + (r0 + 16 * a) * lda + k), w = ld4(A1 + (r0 + 16 * a) * lda + k);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                acc[a][0] = fmaf(w[u], b[u].x, acc[a][0]);
-                acc[a][1] = fmaf(w[u], b[u].y, acc[a][1]);
-                acc[a][2] = fmaf(w[u], b[u].z, acc[a][2]);
-                acc[a][3] = fmaf(w[u], b[u].w, acc[a][3]);
+            for (int c = 0; c <= a; ++c) {
+                acc0[a][c] = dot4(u, b[c], acc0[a][c]);
+                acc1[a][c] = dot4(w, b[c], acc1[a][c]);
             }
         }
     }
@@ -154,8 +154,7 @@ __device__ __forceinline__ void mm_rr(float (&acc)[RA][4], const float* A, int l
         for (int a = 0; a < RA; ++a) {
             const float4 v = ld4(A + (r0 + RS * a) * lda + k);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                acc[a][c] = fmaf(v.x, b[c].x, fmaf(v.y, b[c].y, fmaf(v.z, b[c].z, fmaf(v.w, b[c].w, acc[a][c]))));
+            for (int c = 0; c < 4; ++c) acc[a][c] = dot4(v, b[c], acc[a][c]);
         }
     }
 }
@@ -203,8 +202,7 @@ __global__ void __launch_bounds__(NT) delta_prep(const float* __restrict__ q, co
     {
         const int ti = tid / 16, tj = tid % 16;
         float kk[4][4] = {}, qk[4][4] = {};
-        mm_rr<4, 16, 16>(kk, sk, LK, sk, LK, N, ti, tj);
-        mm_rr<4, 16, 16>(qk, sq, LK, sk, LK, N, ti, tj);
+        mm_lower_rr(kk, qk, sk, sq, LK, sk, LK, N, ti, tj);
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -308,12 +306,15 @@ struct ScanIo {
     float* o;                       // outputs (ROWS = 128)
 };
 
-constexpr int LU = PW + 8;  // row stride of U
-__host__ __device__ constexpr int state_stride(int rows, int N) { return (N + 31) / 32 * 32 + 4 * (NT / rows); }
+// Up to this many CTAs of 16 columns, half of the SMs, a CTA takes 8 with half
+// the threads: 1 x 1000 x 12, 64/64 (48 CTAs) in 61 us against 69.
+constexpr int NARROW = 76;
+constexpr int scan_threads(int PW) { return 16 * PW; }
+__host__ __device__ constexpr int state_stride(int rows, int N) { return (N + 31) / 32 * 32 + 4 * (256 / rows); }
 
-template <int ROWS>
+template <int ROWS, int PW>
 constexpr uint32_t scan_smem(int N) {
-    return sizeof(float) * (2 * image_floats(ROWS, N) + PW * state_stride(ROWS, N) + C * LU);
+    return sizeof(float) * (2 * image_floats(ROWS, N) + PW * state_stride(ROWS, N) + C * (PW + 8));
 }
 
 // Sums y over the SPLIT neighbouring lanes that hold parts of it; lane l of
@@ -347,20 +348,21 @@ __device__ __forceinline__ void join(float (&y)[4][4], int l) {
     }
 }
 
-template <int ROWS, int ND, bool BACK>
+template <int ROWS, int ND, int PW, bool BACK>
 __device__ __forceinline__ void scan_body(const ScanIo& io, int bh, int p0, const int* __restrict__ lens, const Geo& ge,
                                           float* sm) {
     // Lanes that share a tile of the first product (ROWS x PW) and of the second
     // (ND x PW), and the rows each is left with.
-    constexpr int S1 = NT / ROWS, S2 = NT / ND, R1 = 4 / S1, R2 = 4 / S2;
+    constexpr int S1 = 256 / ROWS, S2 = 256 / ND, R1 = 4 / S1, R2 = 4 / S2;
+    constexpr int NT = scan_threads(PW), X = PW / 4, LU = PW + 8;  // tiles across, row stride of U
     const int tid = threadIdx.x, b = bh / ge.H, h = bh % ge.H, N = ge.N, P = ge.P, LA = N + 4;
     const int LS = state_stride(ROWS, N);
     const int len = row_len(lens, b, ge.T), nck = (len + C - 1) / C;
     const int image = image_floats(ROWS, N);
-    float* st = sm + 2 * image;  // the state: column 4 x + i of the slice in row 4 i + x
+    float* st = sm + 2 * image;  // the state: column 4 x + i of the slice in row X i + x
     float* su = st + PW * LS;    // U or Z, [64][LU]
-    const int l1 = tid % S1, x1 = tid / S1 % 4, tile1 = tid / (4 * S1) * 4, row = tile1 + R1 * l1;
-    const int l2 = tid % S2, x2 = tid / S2 % 4, tile2 = tid / (4 * S2) * 4, nr = tile2 + R2 * l2;
+    const int l1 = tid % S1, x1 = tid / S1 % X, tile1 = tid / (X * S1) * 4, row = tile1 + R1 * l1;
+    const int l2 = tid % S2, x2 = tid / S2 % X, tile2 = tid / (X * S2) * 4, nr = tile2 + R2 * l2;
     const bool there = tile2 < N;  // (all of a warp, or none: N is a multiple of 16)
     const int64_t so = ((int64_t)bh * N + nr) * P + p0 + 4 * x2;  // this thread's state
     auto load = [&](int c, int buf) {
@@ -390,7 +392,7 @@ __device__ __forceinline__ void scan_body(const ScanIo& io, int bh, int p0, cons
 #pragma unroll
         for (int a = 0; a < R2; ++a)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st[(4 * i + x2) * LS + nr + a] = s[a][i];
+            for (int i = 0; i < 4; ++i) st[(X * i + x2) * LS + nr + a] = s[a][i];
     };
     auto chunk = [&](int it) { return BACK ? nck - 1 - it : it; };
     if (there) put_state();
@@ -411,7 +413,7 @@ __device__ __forceinline__ void scan_body(const ScanIo& io, int bh, int p0, cons
             for (int e = 4 * l1; e < N; e += 4 * S1) {
                 ulonglong2 x[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(st + (4 * i + x1) * LS + e);
+                for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(st + (X * i + x1) * LS + e);
 #pragma unroll
                 for (int a = 0; a < 4; ++a) {
                     const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(img + (tile1 + a) * LA + e);
@@ -486,22 +488,23 @@ __device__ __forceinline__ void scan_body(const ScanIo& io, int bh, int p0, cons
             io.o[(((int64_t)b * ge.T + len + e / PW) * ge.H + h) * P + p0 + e % PW] = 0.f;
 }
 
-template <int ND>
-__global__ void __launch_bounds__(NT) delta_scan(ScanIo io, const int* __restrict__ lens, Geo ge) {
+template <int ND, int PW>
+__global__ void __launch_bounds__(scan_threads(PW)) delta_scan(ScanIo io, const int* __restrict__ lens, Geo ge) {
     extern __shared__ __align__(16) float sm[];
     const int np = ge.P / PW;
-    scan_body<2 * C, ND, false>(io, blockIdx.x / np, (int)(blockIdx.x % np) * PW, lens, ge, sm);
+    scan_body<2 * C, ND, PW, false>(io, blockIdx.x / np, (int)(blockIdx.x % np) * PW, lens, ge, sm);
 }
 
 // Both of the gradients' scans, which do not need one another.
 template <int ND>
-__global__ void __launch_bounds__(NT) delta_both_scans(ScanIo back, ScanIo fwd, const int* __restrict__ lens, Geo ge) {
+__global__ void __launch_bounds__(scan_threads(16)) delta_both_scans(ScanIo back, ScanIo fwd, const int* __restrict__ lens, Geo ge) {
     extern __shared__ __align__(16) float sm[];
+    constexpr int PW = 16;
     const int np = ge.P / PW, half = gridDim.x / 2, i = blockIdx.x % half;
     if ((int)blockIdx.x < half)
-        scan_body<C, ND, true>(back, i / np, i % np * PW, lens, ge, sm);
+        scan_body<C, ND, PW, true>(back, i / np, i % np * PW, lens, ge, sm);
     else
-        scan_body<C, ND, false>(fwd, i / np, i % np * PW, lens, ge, sm);
+        scan_body<C, ND, PW, false>(fwd, i / np, i % np * PW, lens, ge, sm);
 }
 
 // --------------------------------------------------------------- dQ, dK, dV, dg, dbeta
@@ -544,9 +547,8 @@ __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const 
     float* su = sz + C * LP;
     float* sk = su + C * LP;
     float* sq = sk + C * LK;
-    float* pm = sq + C * LK;
-    float* wm = pm + C * LT;
-    float* sb = wm + C * LT;  // 32 rows of S, then of dS+
+    float* pw = sq + C * LK;  // Pm and, above the diagonal, W^T
+    float* sb = pw + C * LT;  // 32 rows of S, then of dS+
     load_rows(so, LP, dout + vo, vs, C, P, n, tid);
     load_rows(sz, LP, zs + ci * C * P, P, C, P, C, tid);
     load_rows(su, LP, writes + ci * C * P, P, C, P, C, tid);
@@ -567,8 +569,7 @@ __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const 
     {
         const int ti = tid / 16, tj = tid % 16;
         float du[4][4] = {}, zu[4][4] = {}, kk[4][4] = {};
-        mm_rr<4, 16, 16>(du, so, LP, su, LP, P, ti, tj);
-        mm_rr<4, 16, 16>(zu, sz, LP, su, LP, P, ti, tj);
+        mm_lower_rr(du, zu, so, sz, LP, su, LP, P, ti, tj);
         mm_rr<4, 16, 16>(kk, sk, LK, sk, LK, N, ti, tj);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -578,13 +579,11 @@ __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const 
             for (int y = 0; y < 4; ++y) {
                 const int j = tj + 16 * y;
                 const float m = i >= j ? decay_between(d, i, j) : 0.f;
-                pm[i * LT + j] = i >= j ? scale * (m * du[x][y]) : 0.f;
+                if (i >= j) pw[i * LT + j] = scale * (m * du[x][y]);
                 if (i > j) {
                     const float z = m * zu[x][y];
                     gb = fmaf(z, kk[x][y], gb);
-                    wm[i * LT + j] = wm[j * LT + i] = -d.beta[i] * z;
-                } else if (i == j) {
-                    wm[i * LT + i] = 0.f;
+                    pw[j * LT + i] = -d.beta[i] * z;
                 }
             }
 #pragma unroll
@@ -601,8 +600,20 @@ __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const 
         load_rows(sb, LP, states + ci * N * P + (int64_t)nb * P, P, 32, P, rows, tid);
         __syncthreads();
         float aq[2][4] = {}, az[2][4] = {}, au[2][4] = {};
-        mm_rr<2, 32, 8>(aq, so, LP, sb, LP, P, rg, cg);
-        mm_rr<2, 32, 8>(az, sz, LP, sb, LP, P, rg, cg);
+        for (int e = 0; e < P; e += 4) {
+            float4 x[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) x[y] = ld4(sb + (cg + 8 * y) * LP + e);
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const float4 u = ld4(so + (rg + 32 * a) * LP + e), w = ld4(sz + (rg + 32 * a) * LP + e);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    aq[a][y] = dot4(u, x[y], aq[a][y]);
+                    az[a][y] = dot4(w, x[y], az[a][y]);
+                }
+            }
+        }
         __syncthreads();
         float part = 0.f;
         for (int e = tid; e < rows * P; e += NT) {
@@ -614,35 +625,69 @@ __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const 
         dot += (double)part;
         __syncthreads();
         mm_rr<2, 32, 8>(au, su, LP, sb, LP, P, rg, cg);
+        float qv[2][4], kv[2][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int i = rg + 32 * x;
-            float qv[4], kv[4];
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                qv[y] = scale * d.in[i] * aq[x][y];
-                kv[y] = d.out[i] * au[x][y] - d.beta[i] * d.in[i] * az[x][y];
+                const int i = rg + 32 * x;
+                qv[x][y] = scale * d.in[i] * aq[x][y];
+                kv[x][y] = d.out[i] * au[x][y] - d.beta[i] * d.in[i] * az[x][y];
             }
-            // (columns past N read the padding or the next row of sk; they are not kept)
-            for (int j = 0; j < C; ++j) {
-                const float p1 = pm[i * LT + j], p2 = pm[j * LT + i], p3 = wm[i * LT + j];
+        // rows j by fours: before a warp's four rows i only Pm_ij and W_ij, behind
+        // them only Pm_ji and W_ji (columns past N read a padding or another row
+        // that is there; they are not kept)
+        for (int j = 0; j < C; j += 4) {
+            float kr[4][4], qr[4][4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const int col = min(nb + cg + 8 * y, N - 1);
-                    qv[y] = fmaf(p1, sk[j * LK + col], qv[y]);
-                    kv[y] = fmaf(p2, sq[j * LK + col], fmaf(p3, sk[j * LK + col], kv[y]));
+                    kr[u][y] = sk[(j + u) * LK + col], qr[u][y] = sq[(j + u) * LK + col];
+                }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int i = rg + 32 * x, first = rg / 4 * 4 + 32 * x;
+                const float4 r = ld4(pw + i * LT + j);
+                const float a[4] = {r.x, r.y, r.z, r.w};  // (i, j), and (j, i):
+                const float t[4] = {pw[j * LT + i], pw[(j + 1) * LT + i], pw[(j + 2) * LT + i], pw[(j + 3) * LT + i]};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (j < first) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            qv[x][y] = fmaf(a[u], kr[u][y], qv[x][y]);
+                            kv[x][y] = fmaf(t[u], kr[u][y], kv[x][y]);
+                        }
+                    } else if (j > first) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) kv[x][y] = fmaf(t[u], qr[u][y], fmaf(a[u], kr[u][y], kv[x][y]));
+                    } else {
+                        const int k = j + u;
+                        const float p1 = k <= i ? a[u] : 0.f, p2 = k >= i ? t[u] : 0.f, p3 = k < i ? t[u] : k > i ? a[u] : 0.f;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            qv[x][y] = fmaf(p1, kr[u][y], qv[x][y]);
+                            kv[x][y] = fmaf(p2, qr[u][y], fmaf(p3, kr[u][y], kv[x][y]));
+                        }
+                    }
                 }
             }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int i = rg + 32 * x;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const int col = nb + cg + 8 * y;
                 if (col >= N) continue;
-                qgq[x] = fmaf(sq[i * LK + col], qv[y], qgq[x]);
+                qgq[x] = fmaf(sq[i * LK + col], qv[x][y], qgq[x]);
                 kz[x] = fmaf(sk[i * LK + col], az[x][y], kz[x]);
                 kus = fmaf(d.out[i] * sk[i * LK + col], au[x][y], kus);
                 if (i < n) {
-                    gq[go + i * gs + col] = from_f<O>(qv[y]);
-                    gk[go + i * gs + col] = from_f<O>(kv[y]);
+                    gq[go + i * gs + col] = from_f<O>(qv[x][y]);
+                    gk[go + i * gs + col] = from_f<O>(kv[x][y]);
                 }
             }
         }
@@ -748,20 +793,24 @@ cudaError_t prep(const DeltaArgs& a, const Made& m, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int ND>
+template <int ND, int PW>
 cudaError_t scan(const DeltaArgs& a, const ScanIo& io, cudaStream_t st) {
-    const uint32_t sm = scan_smem<2 * C>((int)a.N);
-    const cudaError_t e = allow_smem(delta_scan<ND>, sm);
+    const uint32_t sm = scan_smem<2 * C, PW>((int)a.N);
+    const cudaError_t e = allow_smem(delta_scan<ND, PW>, sm);
     if (e != cudaSuccess) return e;
-    delta_scan<ND><<<(unsigned)(a.Bz * a.H * (a.P / PW)), NT, sm, st>>>(io, a.lens, geo(a));
+    delta_scan<ND, PW><<<(unsigned)(a.Bz * a.H * (a.P / PW)), scan_threads(PW), sm, st>>>(io, a.lens, geo(a));
     return cudaGetLastError();
 }
 template <int ND>
+cudaError_t scan_by_heads(const DeltaArgs& a, const ScanIo& io, cudaStream_t st) {
+    return a.Bz * a.H * (a.P / 16) <= NARROW ? scan<ND, 8>(a, io, st) : scan<ND, 16>(a, io, st);
+}
+template <int ND>
 cudaError_t both(const DeltaArgs& a, const ScanIo& back, const ScanIo& fwd, cudaStream_t st) {
-    const uint32_t sm = scan_smem<C>((int)a.N);
+    const uint32_t sm = scan_smem<C, 16>((int)a.N);
     const cudaError_t e = allow_smem(delta_both_scans<ND>, sm);
     if (e != cudaSuccess) return e;
-    delta_both_scans<ND><<<(unsigned)(2 * a.Bz * a.H * (a.P / PW)), NT, sm, st>>>(back, fwd, a.lens, geo(a));
+    delta_both_scans<ND><<<(unsigned)(2 * a.Bz * a.H * (a.P / 16)), scan_threads(16), sm, st>>>(back, fwd, a.lens, geo(a));
     return cudaGetLastError();
 }
 
@@ -770,7 +819,7 @@ cudaError_t forward(const DeltaArgs& a, void* ws, cudaStream_t st) {
     const cudaError_t e = prep<false>(a, m, st);
     if (e != cudaSuccess) return e;
     const ScanIo io{m.fwd, m.uo, nullptr, a.h0, a.h_final, nullptr, nullptr, static_cast<float*>(a.o)};
-    return a.N <= 64 ? scan<64>(a, io, st) : scan<128>(a, io, st);
+    return a.N <= 64 ? scan_by_heads<64>(a, io, st) : scan_by_heads<128>(a, io, st);
 }
 cudaError_t both_scans(const DeltaArgs& a, float* ws, float* states, float* after, float* writes, float* zs,
                        cudaStream_t st) {
@@ -785,7 +834,7 @@ cudaError_t both_scans(const DeltaArgs& a, float* ws, float* states, float* afte
 template <typename E, typename O>
 cudaError_t grad(const DeltaArgs& a, const float* states, const float* after, const float* writes, const float* zs,
                  void* gq, void* gk, cudaStream_t st) {
-    const size_t sm = sizeof(float) * (3 * C * (a.P + 4) + 2 * C * (a.N + 4) + 2 * C * LT + 32 * (a.P + 4));
+    const size_t sm = sizeof(float) * (3 * C * (a.P + 4) + 2 * C * (a.N + 4) + C * LT + 32 * (a.P + 4));
     cudaError_t e = allow_smem(delta_grad<E, O>, sm);
     if (e != cudaSuccess) return e;
     delta_grad<E, O><<<(unsigned)(a.Bz * a.H * chunks(a)), NT, sm, st>>>(

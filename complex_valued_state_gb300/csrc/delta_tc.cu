@@ -532,17 +532,39 @@ struct ScanArgs {
     float* writes;
 };
 
+// Chains on SMs.  A CTA's tensor memory fills its SM, so n chains (a head's
+// scan, each a walk that cannot be split) on fewer SMs would run in whole waves:
+// 192 on 152 take twice as long as 152.  Cut into `pieces` of equal length and
+// run in `rounds` launches, chain i sits out rounds - pieces of them, those
+// after its own, so that a round has n pieces / rounds CTAs; the state goes from
+// piece to piece through `between`.  192 chains: 3 pieces in 4 rounds, forward
+// 8 x 2048 x 24 64/64 in 362 us against 394 in one launch; 160: 317 against 347;
+// gradients 4 x 2048 x 24 (192 chains) 544 against 554.  A round costs 10 to 18
+// us more than its chunks, so 6 x 1024 x 16 128/128 gradients lose 1.4 %.
+struct Rounds {
+    int n, pieces, rounds, now;
+    float* between;
+    // The chain of CTA `cta` this round (or n and above: none) and its piece.
+    __device__ __forceinline__ int chain(int cta, int& piece) const {
+        const int s = cta % pieces, c = (now - s + rounds) % rounds, wrapped = c + pieces - rounds;
+        piece = now < c ? now : now - c + max(wrapped, 0);
+        return cta / pieces * rounds + c;
+    }
+    // Chunks before piece i of nc.
+    __device__ __forceinline__ int before(int i, int nc) const { return nc * i / pieces; }
+};
+
 // KEEP = false: outputs.  KEEP = true: the state entering each chunk and the
 // writes U for the gradients, no outputs.
 template <typename E, int ND, bool KEEP>
 __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const int* __restrict__ lens, const Shape& sh,
-                                          unsigned* status, unsigned char* smem) {
+                                          const Rounds& turn, int piece, float* between, unsigned* status,
+                                          unsigned char* smem) {
     const E* __restrict__ v = g.v;
     const unsigned char* __restrict__ image = g.image;
     const unsigned char* __restrict__ operands = g.operands;
-    const float* h0 = g.h0;
+    const float* h0 = piece > 0 ? between : g.h0;
     E* __restrict__ o = g.o;
-    float* h_final = g.h_final;
     float* __restrict__ states = g.states;
     float* __restrict__ writes = g.writes;
     using M = ScanSmem<ND>;
@@ -560,9 +582,10 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
     auto& s_gave_up = z.gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
-    // chunks count from this launch's first, of the sequence's `tok` and on
-    const int tok = sh.c0 * C, len = max(row_len(lens, b, sh.T) - tok, 0);
-    const int nck = min((len + C - 1) / C, sh.c1 - sh.c0);
+    // chunks count from this piece's first, of the sequence's `tok` and on
+    const int c0 = sh.c0 + turn.before(piece, sh.c1 - sh.c0), c1 = sh.c0 + turn.before(piece + 1, sh.c1 - sh.c0);
+    const int tok = c0 * C, len = max(row_len(lens, b, sh.T) - tok, 0);
+    const int nck = min((len + C - 1) / C, c1 - c0);
     const int quarters = (P + 31) / 32;
     if (warp == WMMA) {
         tc::tmem_alloc(&s_tmem, TMEM_COLS);
@@ -633,7 +656,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                 if (part == 0) s_sdown[c & 1][vc] = sc.down;
                 warp_done(&mb_s, lane);
                 if (KEEP && on) {
-                    float* dst = states + ((int64_t)bh * sh.nc + sh.c0 + c) * N * P + vc;
+                    float* dst = states + ((int64_t)bh * sh.nc + c0 + c) * N * P + vc;
 #pragma unroll
                     for (int i = 0; i < NS / 2; ++i)
                         if (k0 + 2 * i < N) {
@@ -715,7 +738,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                 sbound = fmaf(all, stop, row.of_all(top_of_pairs(x)) * ws.down * (64.f * 16384.f));
                 if constexpr (KEEP) {
                     if (on) {
-                        float* dst = writes + (((int64_t)bh * sh.nc + sh.c0 + c) * C + EP * part) * P + vc;
+                        float* dst = writes + (((int64_t)bh * sh.nc + c0 + c) * C + EP * part) * P + vc;
                         factors(Image::UU, rs.down);
 #pragma unroll
                         for (int i = 0; i < EP / 2; ++i) {
@@ -743,6 +766,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                     if (!warp_wait(&mb_full[(c + 1) & 1], ((c + 1) >> 1) & 1, &s_gave_up)) break;
                 }
             }
+            float* h_final = piece + 1 < turn.pieces ? between : g.h_final;
             if (h_final && on)
 #pragma unroll
                 for (int i = 0; i < NS / 2; ++i)
@@ -827,7 +851,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                 dst += C * os;
             }
         }
-        if (!KEEP && on && sh.c1 == sh.nc)  // behind the row's last token
+        if (!KEEP && on && sh.c0 + turn.before(piece + 1, sh.c1 - sh.c0) == sh.nc)  // behind the row's last token
             for (int t = row_len(lens, b, sh.T); t < sh.T; ++t) o[(((int64_t)b * sh.T + t) * sh.H + h) * P + vc] = from_f<E>(0.f);
     } else if (warp == WMMA) {
         // ------------------------------------------------ MMA issue
@@ -871,9 +895,9 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
     } else if (warp == WLOAD) {
         // ------------------------------------------------ loader
         int last[2] = {-1, -1};  // parity of the last copies into each stage
-        const unsigned char* img = image + ((int64_t)bh * sh.nc + sh.c0) * Image::STRIDE;
+        const unsigned char* img = image + ((int64_t)bh * sh.nc + c0) * Image::STRIDE;
         const unsigned char* ops =
-            operands + (((int64_t)b * KH + h / sh.G) * sh.nc + sh.c0) * (KEEP ? Operands<ND>::BWD : Operands<ND>::FWD);
+            operands + (((int64_t)b * KH + h / sh.G) * sh.nc + c0) * (KEEP ? Operands<ND>::BWD : Operands<ND>::FWD);
         for (int c = 0; c < nck; ++c) {
             const uint32_t at = tc::smem_u32(smem) + (c & 1) * M::STAGE;
             if (c >= 2 && !warp_wait(&mb_free[c & 1], ((c >> 1) - 1) & 1, &s_gave_up)) break;
@@ -919,36 +943,6 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
     if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusDelta);
 }
 
-// Chains on SMs.  A CTA's tensor memory fills its SM, so n chains (a head's
-// scan, each a walk that cannot be split) on fewer SMs would run in whole waves:
-// 192 on 152 take twice as long as 152.  Cut into `pieces` of equal length and
-// run in `rounds` launches, chain i sits out rounds - pieces of them, those
-// after its own, so that a round has n pieces / rounds CTAs; the state goes from
-// piece to piece through `between`.  192 chains: 3 pieces in 4 rounds, forward
-// 8 x 2048 x 24 64/64 in 362 us against 394 in one launch; 160: 317 against 347;
-// gradients 4 x 2048 x 24 (192 chains) 544 against 554.  A round costs 10 to 18
-// us more than its chunks, so 6 x 1024 x 16 128/128 gradients lose 1.4 %.
-struct Rounds {
-    int n, pieces, rounds, now;
-    float* between;
-    // The chain of CTA `cta` this round (or n and above: none) and its piece.
-    __device__ __forceinline__ int chain(int cta, int& piece) const {
-        const int s = cta % pieces, c = (now - s + rounds) % rounds, wrapped = c + pieces - rounds;
-        piece = now < c ? now : now - c + max(wrapped, 0);
-        return cta / pieces * rounds + c;
-    }
-};
-
-// Sets the first and last chunk and where the state comes from and goes to.
-template <typename E>
-__device__ __forceinline__ void take_piece(ScanArgs<E>& g, Shape& sh, const Rounds& turn, int piece) {
-    const int n = sh.c1 - sh.c0, from = sh.c0;
-    if (piece > 0) g.h0 = turn.between;
-    if (piece + 1 < turn.pieces) g.h_final = turn.between;
-    sh.c0 = from + n * piece / turn.pieces;
-    sh.c1 = from + n * (piece + 1) / turn.pieces;
-}
-
 template <typename E, int ND>
 __global__ void __launch_bounds__(ST, 1) delta_scan_tc(ScanArgs<E> g, const int* __restrict__ lens, Shape sh, Rounds turn,
                                                        unsigned* status) {
@@ -956,9 +950,7 @@ __global__ void __launch_bounds__(ST, 1) delta_scan_tc(ScanArgs<E> g, const int*
     let_next_start();  // (the next chunks' prep, on the SMs that the heads leave)
     int piece = 0;
     const int bh = turn.chain(blockIdx.x, piece);
-    if (bh >= turn.n) return;
-    take_piece(g, sh, turn, piece);
-    scan_body<E, ND, false>(g, bh, lens, sh, status, smem);
+    if (bh < turn.n) scan_body<E, ND, false>(g, bh, lens, sh, turn, piece, turn.between, status, smem);
 }
 
 // --------------------------------------------------------------- backward scan
@@ -1002,12 +994,11 @@ struct BackArgs {
 
 template <typename E, int ND>
 __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, const int* __restrict__ lens, const Shape& sh,
-                                               unsigned* status, unsigned char* smem) {
+                                               const Rounds& turn, int piece, unsigned* status, unsigned char* smem) {
     const E* __restrict__ dout = g.dout;
     const unsigned char* __restrict__ image = g.image;
     const unsigned char* __restrict__ operands = g.operands;
-    const float* dh = g.dh;
-    float* gh0 = g.gh0;
+    const float* dh = piece > 0 ? turn.between : g.dh;
     float* __restrict__ after = g.after;
     float* __restrict__ zs = g.zs;
     using M = BackSmem<ND>;
@@ -1027,7 +1018,8 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G, N = sh.N, P = sh.P;
     const int len = row_len(lens, b, sh.T);
-    const int end = min((len + C - 1) / C, sh.c1), nck = max(end - sh.c0, 0);  // the row's chunks of this launch
+    const int first = sh.nc - turn.before(piece + 1, sh.nc);  // the row's chunks of this piece: [first, end)
+    const int end = min((len + C - 1) / C, sh.nc - turn.before(piece, sh.nc)), nck = max(end - first, 0);
     const int quarters = (P + 31) / 32;
     if (warp == WMMA) {
         tc::tmem_alloc(&s_tmem, TMEM_COLS);
@@ -1205,6 +1197,7 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
                     if (!warp_wait(&mb_full[(j + 1) & 1], ((j + 1) >> 1) & 1, &s_gave_up)) break;
                 }
             }
+            float* gh0 = piece + 1 < turn.pieces ? turn.between : g.gh0;
             if (gh0 && on)
 #pragma unroll
                 for (int i = 0; i < NS / 2; ++i)
@@ -1335,7 +1328,7 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
                 tc::bulk_g2s(at + M::K0, ops + (int64_t)c * Operands<ND>::BWD, M::OPS, &mb_full[j & 1]);
                 tc::bulk_g2s(at + M::IMG, img + (int64_t)c * Image::STRIDE, Image::BYTES, &mb_full[j & 1]);
                 last[j & 1] = (j >> 1) & 1;
-                if (c - 2 >= sh.c0) {  // what the next copies into this stage read, into L2
+                if (c - 2 >= first) {  // what the next copies into this stage read, into L2
                     prefetch_l2(ops + (int64_t)(c - 2) * Operands<ND>::BWD, M::OPS);
                     prefetch_l2(img + (int64_t)(c - 2) * Image::STRIDE, Image::BYTES);
                 }
@@ -1378,19 +1371,11 @@ __global__ void __launch_bounds__(ST, 1) delta_both_scans_tc(BackArgs<E> back, S
     const int heads = turn.n / 2;
     int piece = 0;
     const int i = turn.chain(blockIdx.x, piece);
-    if (i >= turn.n) return;
-    if (i < heads) {
-        const int nc = sh.nc;
-        if (piece > 0) back.dh = turn.between;
-        if (piece + 1 < turn.pieces) back.gh0 = turn.between;
-        sh.c0 = nc - nc * (piece + 1) / turn.pieces;
-        sh.c1 = nc - nc * piece / turn.pieces;
-        back_scan_body<E, ND>(back, i, lens, sh, status, smem);
-    } else {
-        turn.between += (int64_t)heads * sh.N * sh.P;
-        take_piece(fwd, sh, turn, piece);
-        scan_body<E, ND, true>(fwd, i - heads, lens, sh, status, smem);
-    }
+    if (i < heads)
+        back_scan_body<E, ND>(back, i, lens, sh, turn, piece, status, smem);
+    else if (i < turn.n)
+        scan_body<E, ND, true>(fwd, i - heads, lens, sh, turn, piece, turn.between + (int64_t)heads * sh.N * sh.P, status,
+                               smem);
 }
 
 // --------------------------------------------------------------- dQ, dK, dV, dg, dbeta
