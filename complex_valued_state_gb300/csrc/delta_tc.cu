@@ -943,14 +943,20 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
     if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusDelta);
 }
 
-template <typename E, int ND>
+// CUT: in pieces (else the whole chain of head blockIdx.x: what a piece needs
+// costs the scan registers, 1065 us against 1040 at 1 x 16384 x 32, 128/64).
+template <typename E, int ND, bool CUT>
 __global__ void __launch_bounds__(ST, 1) delta_scan_tc(ScanArgs<E> g, const int* __restrict__ lens, Shape sh, Rounds turn,
                                                        unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
     let_next_start();  // (the next chunks' prep, on the SMs that the heads leave)
-    int piece = 0;
-    const int bh = turn.chain(blockIdx.x, piece);
-    if (bh < turn.n) scan_body<E, ND, false>(g, bh, lens, sh, turn, piece, turn.between, status, smem);
+    if constexpr (CUT) {
+        int piece = 0;
+        const int bh = turn.chain(blockIdx.x, piece);
+        if (bh < turn.n) scan_body<E, ND, false>(g, bh, lens, sh, turn, piece, turn.between, status, smem);
+    } else {
+        scan_body<E, ND, false>(g, blockIdx.x, lens, sh, Rounds{0, 1, 1, 0, nullptr}, 0, nullptr, status, smem);
+    }
 }
 
 // --------------------------------------------------------------- backward scan
@@ -2022,7 +2028,8 @@ cudaError_t forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
     unsigned char* operands = image + image_bytes(a);
     float* between = reinterpret_cast<float*>(operands + operand_bytes(a, false));  // the state from part to part
     constexpr uint32_t smem = ScanSmem<ND>::BYTES + sizeof(ScanShared);
-    cudaError_t e = allow<delta_scan_tc<E, ND>>(smem);
+    cudaError_t e = allow<delta_scan_tc<E, ND, false>>(smem);
+    if (e == cudaSuccess) e = allow<delta_scan_tc<E, ND, true>>(smem);
     int sms = 0;
     if (e == cudaSuccess) e = sm_count(&sms);
     const int parts = parts_of(a);
@@ -2035,7 +2042,10 @@ cudaError_t forward_tc(const DeltaArgs& a, void* ws, cudaStream_t st) {
                             p + 1 < parts ? between : a.h_final, nullptr, nullptr};
         Rounds turn = cut(a.Bz * a.H, sh.c1 - sh.c0, sms, between);
         for (; turn.now < turn.rounds && e == cudaSuccess; ++turn.now) {
-            delta_scan_tc<E, ND><<<ctas(turn), ST, smem, st>>>(g, a.lens, sh, turn, status_word());
+            if (turn.rounds > 1)
+                delta_scan_tc<E, ND, true><<<ctas(turn), ST, smem, st>>>(g, a.lens, sh, turn, status_word());
+            else
+                delta_scan_tc<E, ND, false><<<ctas(turn), ST, smem, st>>>(g, a.lens, sh, turn, status_word());
             e = cudaGetLastError();
         }
     }
