@@ -317,37 +317,6 @@ constexpr uint32_t scan_smem(int N) {
     return sizeof(float) * (2 * image_floats(ROWS, N) + PW * state_stride(ROWS, N) + C * (PW + 8));
 }
 
-// Sums y over the SPLIT neighbouring lanes that hold parts of it; lane l of
-// them gets rows l 4 / SPLIT and on, in y's first.
-template <int SPLIT>
-__device__ __forceinline__ void join(float (&y)[4][4], int l) {
-    if (SPLIT == 4) {
-        const bool high = l & 2;
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float other = __shfl_xor_sync(0xffffffffu, high ? y[a][i] : y[a + 2][i], 2);
-                y[a][i] = (high ? y[a + 2][i] : y[a][i]) + other;
-            }
-        const bool odd = l & 1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? y[0][i] : y[1][i], 1);
-            y[0][i] = (odd ? y[1][i] : y[0][i]) + other;
-        }
-    } else {
-        const bool odd = l & 1;
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float other = __shfl_xor_sync(0xffffffffu, odd ? y[a][i] : y[a + 2][i], 1);
-                y[a][i] = (odd ? y[a + 2][i] : y[a][i]) + other;
-            }
-    }
-}
-
 template <int ROWS, int ND, int PW, bool BACK>
 __device__ __forceinline__ void scan_body(const ScanIo& io, int bh, int p0, const int* __restrict__ lens, const Geo& ge,
                                           float* sm) {
@@ -784,7 +753,7 @@ size_t made_floats(const DeltaArgs& a, bool back) {
 
 template <bool BACK>
 cudaError_t prep(const DeltaArgs& a, const Made& m, cudaStream_t st) {
-    const size_t sm = sizeof(float) * (2 * C * (a.N + 4) + C * (a.P + 4) + 2 * C * LT + 32 * 32);
+    const size_t sm = sizeof(float) * (2 * C * (a.N + 4) + C * (a.P + 4) + 2 * C * LT + kInverseScratch);
     const cudaError_t e = allow_smem(delta_prep<BACK>, sm);
     if (e != cudaSuccess) return e;
     delta_prep<BACK><<<(unsigned)(a.Bz * a.H * chunks(a)), NT, sm, st>>>(

@@ -100,14 +100,59 @@ __device__ __forceinline__ float decay_between(const Decays& d, int i, int j) {
     return expf((d.hi[i] - d.hi[j]) + (d.lo[i] - d.lo[j]));
 }
 
+// Sums y over the SPLIT neighbouring lanes that hold parts of it; lane l of
+// them gets rows l R / SPLIT and on of the R, in y's first.
+template <int SPLIT, int R>
+__device__ __forceinline__ void join(float (&y)[R][4], int l) {
+    if (SPLIT == 4) {
+        const bool high = l & 2;
+#pragma unroll
+        for (int a = 0; a < R / 2; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float other = __shfl_xor_sync(0xffffffffu, high ? y[a][i] : y[a + R / 2][i], 2);
+                y[a][i] = (high ? y[a + R / 2][i] : y[a][i]) + other;
+            }
+    }
+    constexpr int H = SPLIT == 4 ? R / 4 : R / 2;
+    const bool odd = l & 1;
+#pragma unroll
+    for (int a = 0; a < H; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? y[a][i] : y[a + H][i], 1);
+            y[a][i] = (odd ? y[a + H][i] : y[a][i]) + other;
+        }
+}
+
+// y += rows r0 .. r0 + 3 of A times columns c0 .. c0 + 3 of B, k from `from` on
+// in steps of four below `to`: a quarter of the product.
+__device__ __forceinline__ void quarter_product(float (&y)[4][4], const float* A, int lda, const float* B, int ldb, int r0,
+                                                int c0, int from, int to) {
+#pragma unroll 2
+    for (int m = from; m < to; m += 4) {
+        const float4 t = *reinterpret_cast<const float4*>(B + m * ldb + c0);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const float v = A[(r0 + a) * lda + m];
+            y[a][0] = fmaf(v, t.x, y[a][0]);
+            y[a][1] = fmaf(v, t.y, y[a][1]);
+            y[a][2] = fmaf(v, t.z, y[a][2]);
+            y[a][3] = fmaf(v, t.w, y[a][3]);
+        }
+    }
+}
+
 // (I + a)^-1 in place of the strictly lower triangular a (64 x 64, row stride
 // LD, fp32, in shared memory, 16-byte aligned rows), by 256 threads: the four
 // 16 x 16 blocks on the diagonal by forward substitution, one column a thread,
 // then two rounds of
-//   [L11 0; A21 L22]^-1 = [T11 0; -T22 A21 T11 T22],
-// four outputs of a row a thread.  `w` is 32 x 32 floats of scratch, 16-byte
-// aligned.  All threads call it; the result is complete after its last
-// barrier.  The upper triangle has to be zeros and stays so.
+//     [L11 0; A21 L22]^-1 = [T11 0; -T22 A21 T11 T22],
+// 4 x 4 outputs to four neighbouring lanes that share the sum: 2 bytes of
+// shared memory a multiply-add, which is what bounds it.  `w` is kInverseScratch
+// floats, 16-byte aligned.  All threads call it; the result is complete after
+// its last barrier.  The upper triangle has to be zeros and stays so.
+constexpr int kInverseScratch = 32 * 36;
 template <int LD>
 __device__ void tri_inverse_in_place(float* a, float* w, int tid) {
     if (tid < 64) {
@@ -134,34 +179,29 @@ __device__ void tri_inverse_in_place(float* a, float* w, int tid) {
     __syncthreads();
 #pragma unroll
     for (int half = 16; half <= 32; half *= 2) {
-        // 64 / (2 half) pairs of half x half outputs, a quad of a row a thread
-        const int quads = half / 4, p = tid / (half * quads), r = tid / quads % half, c = tid % quads * 4;
-        const bool on = p < C / (2 * half);
+        // a warp: two rows of four tiles, so that the lanes' words of A and rows of
+        // B meet no bank twice
+        const int l = tid & 3, t = tid >> 2, LW = half + 4;
+        const int c0 = 4 * ((t >> 1 & 3) + (half == 32 ? t >> 1 & 4 : 0));
+        const int r0 = 4 * ((t & 1) + (half == 32 ? t >> 3 & 6 : t >> 2 & 2));
+        const int p = half == 32 ? 0 : t >> 4;
+        const bool on = p < C / (2 * half);  // (whole warps)
         float* a21 = a + (2 * p + 1) * half * LD + 2 * p * half;
         const float* t11 = a + 2 * p * half * LD + 2 * p * half;
         const float* t22 = a + (2 * p + 1) * half * LD + (2 * p + 1) * half;
-        float* wp = w + p * half * half;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        float* wp = w + p * half * LW;
         if (on) {  // w = A21 T11
-#pragma unroll 8
-            for (int m = 0; m < half; ++m) {
-                const float v = a21[r * LD + m];
-                const float4 t = *reinterpret_cast<const float4*>(t11 + m * LD + c);
-                s.x = fmaf(v, t.x, s.x), s.y = fmaf(v, t.y, s.y), s.z = fmaf(v, t.z, s.z), s.w = fmaf(v, t.w, s.w);
-            }
-            *reinterpret_cast<float4*>(wp + r * half + c) = s;
+            float y[4][4] = {};
+            quarter_product(y, a21, LD, t11, LD, r0, c0, c0 + l, half);
+            join<4>(y, l);
+            *reinterpret_cast<float4*>(wp + (r0 + l) * LW + c0) = make_float4(y[0][0], y[0][1], y[0][2], y[0][3]);
         }
         __syncthreads();
-        if (on) {  // T21 = -T22 w, over A21 (T22 is lower triangular: a warp stops at its last row)
-            s = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int stop = (tid | 31) / quads % half + 1;
-#pragma unroll 4
-            for (int m = 0; m < stop; ++m) {
-                const float v = -t22[r * LD + m];
-                const float4 t = *reinterpret_cast<const float4*>(wp + m * half + c);
-                s.x = fmaf(v, t.x, s.x), s.y = fmaf(v, t.y, s.y), s.z = fmaf(v, t.z, s.z), s.w = fmaf(v, t.w, s.w);
-            }
-            *reinterpret_cast<float4*>(a21 + r * LD + c) = s;
+        if (on) {  // T21 = -T22 w, over A21
+            float y[4][4] = {};
+            quarter_product(y, t22, LD, wp, LW, r0, c0, l, r0 + 4);
+            join<4>(y, l);
+            *reinterpret_cast<float4*>(a21 + (r0 + l) * LD + c0) = make_float4(-y[0][0], -y[0][1], -y[0][2], -y[0][3]);
         }
         __syncthreads();
     }

@@ -94,7 +94,7 @@ struct PrepSmem {
     static constexpr uint32_t OPS = BACK ? Operands<ND>::BWD : Operands<ND>::FWD;
     static constexpr uint32_t A = 0, P = 4 * C * LT, W = 2 * P;
     static constexpr uint32_t mx(uint32_t a, uint32_t b) { return a > b ? a : b; }
-    static constexpr uint32_t BYTES = mx(mx(OPS, W + 4 * 32 * 32), Image::STRIDE);
+    static constexpr uint32_t BYTES = mx(mx(OPS, W + 4 * kInverseScratch), Image::STRIDE);
 };
 
 // 16 values of a row of the image (columns 16 part..), scaled and split; returns
@@ -263,18 +263,19 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
     }
     __syncthreads();
     tri_inverse_in_place<LT>(sa, reinterpret_cast<float*>(smem + M::W), tid);
-    // X = P T (both lower triangular), 4 x 4 a thread: a warp holds 8 rows and
-    // stops at their last column
-    const int ti = tid / 16, tj = tid % 16;
-    float x[4][4] = {};
-#pragma unroll 2
-    for (int m = 0; m < 8 * (warp + 1); m += 4) {
+    // X = P T (both lower triangular), 8 x 4 to two neighbouring lanes that share
+    // the sum (1.5 bytes of shared memory a multiply-add; 4 x 4, 2): a warp holds
+    // 8 rows and stops at their last column
+    const int l = tid & 1, tj = tid / 2 % 16;
+    float x[8][4] = {};
+#pragma unroll 1
+    for (int m = 4 * l; m < 8 * (warp + 1); m += 8) {
         float4 bv[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) bv[u] = *reinterpret_cast<const float4*>(sa + (m + u) * LT + 4 * tj);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float4 av = *reinterpret_cast<const float4*>(sp + (4 * ti + r) * LT + m);
+        for (int r = 0; r < 8; ++r) {
+            const float4 av = *reinterpret_cast<const float4*>(sp + (8 * warp + r) * LT + m);
             const float a[4] = {av.x, av.y, av.z, av.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -285,6 +286,7 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
             }
         }
     }
+    join<2>(x, l);
     unsigned char* img = smem;
     float* ff = reinterpret_cast<float*>(img + Image::F);
     auto write_out = [&](unsigned char* to) {
@@ -299,21 +301,24 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
     __syncthreads();  // P is read
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<float4*>(sp + (4 * ti + r) * LT + 4 * tj) = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
+        *reinterpret_cast<float4*>(sp + (8 * warp + 4 * l + r) * LT + 4 * tj) = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
     __syncthreads();
     // T and X into the image: a thread has 16 columns of one row.  One scale a
     // matrix: the scales have 2^16 to spare.
     const int row = lane + 32 * (warp & 1), part = warp >> 1;
-    float te[16], xe[16], tops[4] = {};  // of beta T, beta X; of T, X
+    // (The gradients' forward scan makes no outputs: its image has no X.)
+    float te[16], xe[BACK ? 1 : 16], tops[4] = {};  // of beta T, beta X; of T, X
 #pragma unroll
     for (int u = 0; u < 16; u += 4) {
         const float4 t4 = *reinterpret_cast<const float4*>(sa + row * LT + 16 * part + u);
         const float4 x4 = *reinterpret_cast<const float4*>(sp + row * LT + 16 * part + u);
         const float4 b4 = *reinterpret_cast<const float4*>(d.beta + 16 * part + u);
         te[u] = t4.x * b4.x, te[u + 1] = t4.y * b4.y, te[u + 2] = t4.z * b4.z, te[u + 3] = t4.w * b4.w;
-        xe[u] = x4.x * b4.x, xe[u + 1] = x4.y * b4.y, xe[u + 2] = x4.z * b4.z, xe[u + 3] = x4.w * b4.w;
+        if constexpr (!BACK) {
+            xe[u] = x4.x * b4.x, xe[u + 1] = x4.y * b4.y, xe[u + 2] = x4.z * b4.z, xe[u + 3] = x4.w * b4.w;
+            tops[1] = fmaxf(fmaxf(fmaxf(tops[1], fabsf(xe[u])), fmaxf(fabsf(xe[u + 1]), fabsf(xe[u + 2]))), fabsf(xe[u + 3]));
+        }
         tops[0] = fmaxf(fmaxf(fmaxf(tops[0], fabsf(te[u])), fmaxf(fabsf(te[u + 1]), fabsf(te[u + 2]))), fabsf(te[u + 3]));
-        tops[1] = fmaxf(fmaxf(fmaxf(tops[1], fabsf(xe[u])), fmaxf(fabsf(xe[u + 1]), fabsf(xe[u + 2]))), fabsf(xe[u + 3]));
         if (BACK) {
             tops[2] = fmaxf(fmaxf(fmaxf(tops[2], fabsf(t4.x)), fmaxf(fabsf(t4.y), fabsf(t4.z))), fabsf(t4.w));
             tops[3] = fmaxf(fmaxf(fmaxf(tops[3], fabsf(x4.x)), fmaxf(fabsf(x4.y), fabsf(x4.z))), fabsf(x4.w));
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
     RowScale ts = row_scale(tops[0]), xs = row_scale(tops[1]);
     // (the forward's matrices carry beta: U = T beta (V - e^G K S))
     s_sum[part][row] = image_row(img, row, part, te, ts.up);
-    image_row(img, C + row, part, xe, xs.up);
+    if constexpr (!BACK) image_row(img, C + row, part, xe, xs.up);
     __syncthreads();
     // |R| <= |v| + BND1 |S| and |U'| <= BND2 |R|, of a lane's largest values
     auto bound2 = [&](int i, const float* f) {
@@ -352,8 +357,10 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
         ff[Image::KB + tid] = fi * kd;
         ff[Image::UU + tid] = ts.down;
         ff[Image::UW + tid] = ts.down * d.out[tid] * kd;
-        ff[Image::OQ + tid] = scale * fi * qd;
-        ff[Image::OX + tid] = scale * xs.down;
+        if (!BACK) {
+            ff[Image::OQ + tid] = scale * fi * qd;
+            ff[Image::OX + tid] = scale * xs.down;
+        }
     } else if (warp == 2) {
         put_scalars(ff, d.all, fmaxf(s_norm[lane] * d.in[lane], s_norm[lane + 32] * d.in[lane + 32]) * sqrtf((float)ND),
                     fmaxf(bound2(lane, d.out), bound2(lane + 32, d.out)), 0.f, lane);
