@@ -9,6 +9,8 @@
 // batch has several CTAs a head to spread over the SMs and a single sequence
 // still gets N P / 4096 of them a head.  Eight lanes hold a row's 32 columns
 // as float4 (128 contiguous bytes), 16 row groups of them N / 16 rows each.
+// Measured: 256 x 32 heads, 128/64: 81 us, 6.7 TB/s; 77 rows of a pool, 32
+// heads, 128/128: 50 us, 6.4 TB/s; one row of 12 heads, 64/64: 2.2 us.
 
 #include "cssd_internal.h"
 #include "delta_common.cuh"

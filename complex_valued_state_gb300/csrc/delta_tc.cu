@@ -3,25 +3,31 @@
 // precision at the head of delta_tc.cuh).
 //
 // delta_prep_tc, one CTA per chunk and value head: [Q; K] K^T by one MMA
-// chain, T = (I + A)^-1 and X = P T in fp32 on the CUDA cores, both left in
-// the workspace as the very bytes the scan's B operand wants.
+// chain, T = (I + A)^-1 and X = P T in fp32 on the CUDA cores, all left in the
+// workspace as the very bytes the scan's B operands want.
 //
 // delta_scan_tc, one CTA per value head, walks the chunks.  Everything is laid
 // out transposed, one state column v per tensor-memory lane:
 //     [v, i] = S^T K^T, S^T Q^T   A = S^T from tensor memory, B = K, Q
-//     R^T = beta (V - e^G K S)^T  by the thread(s) of lane v
-//     U^T, (X R)^T                A = R^T from tensor memory, B = T, X
+//     R^T = (V - e^G K S)^T       by the four threads of lane v
+//     U^T, (X R)^T                A = R^T from tensor memory, B = T, X (times beta)
 //     S^T += U'^T K               A = U'^T from tensor memory, B = K^T
-// so that each product's result lands in the lane whose thread makes the next
-// A operand from it: rows never leave their lane, a row's scale needs no
-// exchange beyond the two threads that share it, and no operand made on the
+// so that each product's result lands in the lane whose threads make the next
+// A operand from it: rows never leave their lane, and no operand made on the
 // way goes through shared memory.  Shared memory holds the B operands alone,
-// two chunks deep, written by four loader warps (8 x 8 blocks: rows for K and
-// Q, transposed in registers for K^T) and, for [T; X], by one bulk copy.
+// two chunks deep, by bulk copies of what the prep left, and V or dO on a ring
+// of its own.
 //
 // What bounds the scan: the chain of a chunk, three MMA groups with the
 // threads' work between them (the state is the only thing that waits; Q S and
-// X R run beside the chain).
+// X R run beside the chain).  A chunk takes 2.9 us at 64/64 (4 x 2048 x 24: two
+// scans of 16 chunks, 48 us each on 96 SMs) and 3.8 us at 128/64; the tensor
+// pipe is 15 % busy.
+//
+// Whole calls, bf16: forward 4 x 2048 x 24, 64/64 187 us (prep 92 us, half of it
+// beside the scan); 1 x 16384 x 32, 128/64 1050 us; gradients 4 x 2048 x 24,
+// 64/64 530 us (prep 112, scans 206, delta_grad_tc 209), 4 x 1501 x 16 on 8 key
+// heads, 128/128 354 us (45, 111, 178 and 20 for the sum over shared heads).
 
 #include <atomic>
 #include <type_traits>
@@ -84,6 +90,9 @@ __device__ __forceinline__ void transpose_operand(unsigned char* to, const unsig
 }
 
 // --------------------------------------------------------------- prep
+// Bound by instruction issue (59 % busy) and the barriers between its stages
+// (the loads, the MMA, the inverse, X, the image): 35 ns a chunk and head at 64/64
+// forward, 37 for the gradients, whose second image stands for the outputs' X.
 constexpr int PT = 256;      // threads
 constexpr int LT = C + 4;    // row stride of the fp32 matrices
 
@@ -1402,8 +1411,10 @@ __global__ void __launch_bounds__(ST, 1) delta_both_scans_tc(BackArgs<E> back, S
 // take five MMA chains of 128 rows.  S, dS, Z and U are fp32 and are split on
 // the way into shared memory, a row a scale; dO is exact with its scale, Pm
 // and W are split with one scale a chunk (into tensor memory, over the first
-// two products).  Bound by the loads: 4 N P bytes of S and of dS a chunk and
-// head, twice 256 P of Z and U.
+// two products).  4 x 2048 x 24, 64/64: 209 us for 406 MB read, 2 TB/s; bound by
+// the latency of a CTA's stages (20 us from its loads to its last store, issue 27 %
+// busy) at the two CTAs an SM that 128 registers a thread leave.  512 threads a
+// CTA took 246 us against 228 then, an L2 prefetch of the next CTAs' data 236.
 template <int ND, int PD>
 struct GradSmem {
     static constexpr int NT = ND == 128 ? 512 : 256;  // 32 columns of dQ, dK a thread
@@ -2022,10 +2033,12 @@ size_t state_bytes(const DeltaArgs& a) { return sizeof(float) * a.Bz * a.H * a.N
 // prep beside the scan: the scan has one CTA per head, so with fewer heads than
 // SMs the prep (a CTA per chunk and head) takes the others.  One part costs two
 // more launches and the state's way through memory (about 8 us), so a part has
-// at least 16 chunks (60 to 100 us of scan).
+// at least 16 chunks (60 to 100 us of scan).  In parts against whole, 2048
+// tokens, 64/64: 24 heads 120 against 128 us, 48 134 and 150, 96 194 and 196,
+// 120 222 and 220, 144 259 and 253; 16384 tokens of 32 heads, 128/64: 1043 and 1265.
 int parts_of(const DeltaArgs& a) {
     const int64_t nc = (a.T + C - 1) / C;
-    if (a.Bz * a.H > 120) return 1;
+    if (a.Bz * a.H > 100) return 1;
     return (int)(nc < 32 ? 1 : nc / 16 < 8 ? nc / 16 : 8);
 }
 
