@@ -32,6 +32,11 @@ __device__ __forceinline__ int row_len(const int* lens, int b, int T) {
     return lens ? min(max(lens[b], 0), T) : T;
 }
 
+// Programmatic dependent launch: let the kernel behind this one in the stream
+// (if it was launched so) start; wait until the kernel before it has ended.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // A sum kept as two floats, value and what its rounding left.
 struct Sum2 {
     float hi, lo;

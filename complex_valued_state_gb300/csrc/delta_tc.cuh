@@ -163,11 +163,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* m) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(m)) : "memory");
 }
 
-// Programmatic dependent launch: let the kernel behind this one in the stream
-// (if it was launched so) start; wait until the kernel before it has ended.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Wait for a phase parity; false once this or another wait of the CTA has
 // given up (after ~2 s), which `gave_up` tells the others.
 __device__ __forceinline__ bool wait_or_give_up(uint64_t* m, uint32_t parity, volatile int* gave_up) {

@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, group = warp / G, gt = tid % TG, nv = width / W;
     const uint32_t bytes = (uint32_t)width * sizeof(E);
+    delta::let_next_start();
     unsigned char* mine = ring + (size_t)group * kStages * 2 * bytes;
     float* sw = reinterpret_cast<float*>(ring + (size_t)NG * kStages * 2 * bytes);
     for (int c = tid; c < width; c += 32 * kRowWarps) sw[c] = w ? to_f(w[c]) : 1.f;
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(256) norm_back_cols(const E* dy, const E* x,
 // part [n][2][width] -> gweight, gbias: 32 columns x 32 lanes over n, in a
 // fixed order.
 template <typename WT>
-__global__ void __launch_bounds__(1024) norm_back_join(const float* __restrict__ part, int n, int64_t width,
+__global__ void __launch_bounds__(1024) norm_back_join(const float* part, int n, int64_t width,
                                                        WT* __restrict__ gw, WT* __restrict__ gb) {
     __shared__ float red[32][33];
     WT* out = blockIdx.y ? gb : gw;
@@ -501,6 +502,7 @@ __global__ void __launch_bounds__(1024) norm_back_join(const float* __restrict__
     const int lx = threadIdx.x % 32, ly = threadIdx.x / 32;
     const int64_t c = (int64_t)blockIdx.x * 32 + lx;
     float s = 0.f;
+    delta::wait_for_previous();  // (nothing of `part` is read before)
     if (c < width)
 #pragma unroll 8
         for (int i = ly; i < n; i += 32) s += part[((int64_t)i * 2 + blockIdx.y) * width + c];
@@ -610,9 +612,18 @@ cudaError_t norm_bwd(const NormArgs& a, void* ws, cudaStream_t st) {
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!ww && !wb)) return e;
-    norm_back_join<WT><<<dim3((unsigned)((a.width + 31) / 32), 2), 1024, 0, st>>>(
-        part, n, a.width, static_cast<WT*>(a.gweight), static_cast<WT*>(a.gbias));
-    return cudaGetLastError();
+    // launched while the kernel before it runs, so that its CTAs are there when that ends
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.width + 31) / 32), 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_back_join<WT>, static_cast<const float*>(part), n, a.width,
+                              static_cast<WT*>(a.gweight), static_cast<WT*>(a.gbias));
 }
 
 // Calls f with null pointers of the tensor and the weight type.
