@@ -731,11 +731,6 @@ size_t state_floats(const DeltaArgs& a) { return (size_t)(a.Bz * a.H * chunks(a)
 size_t write_floats(const DeltaArgs& a) { return (size_t)(a.Bz * a.H * chunks(a)) * C * a.P; }
 size_t part_floats(const DeltaArgs& a) { return a.H == a.KH ? 0 : (size_t)(a.Bz * a.T * a.H) * a.N; }
 
-template <typename F>
-cudaError_t allow_smem(F* f, size_t bytes) {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(f), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 Geo geo(const DeltaArgs& a) {
     return Geo{(int)a.T, (int)a.H, (int)(a.H / a.KH), (int)a.N, (int)a.P, (int)chunks(a)};
 }
@@ -758,8 +753,11 @@ size_t made_floats(const DeltaArgs& a, bool back) {
 
 template <bool BACK>
 cudaError_t prep(const DeltaArgs& a, const Made& m, cudaStream_t st) {
-    const size_t sm = sizeof(float) * (2 * C * (a.N + 4) + C * (a.P + 4) + 2 * C * LT + kInverseScratch);
-    const cudaError_t e = allow_smem(delta_prep<BACK>, sm);
+    auto bytes = [](int64_t N, int64_t P) {
+        return (uint32_t)(sizeof(float) * (2 * C * (N + 4) + C * (P + 4) + 2 * C * LT + kInverseScratch));
+    };
+    const uint32_t sm = bytes(a.N, a.P);
+    const cudaError_t e = allow<delta_prep<BACK>>(bytes(128, 128));
     if (e != cudaSuccess) return e;
     delta_prep<BACK><<<(unsigned)(a.Bz * a.H * chunks(a)), NT, sm, st>>>(
         static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v),
@@ -770,7 +768,7 @@ cudaError_t prep(const DeltaArgs& a, const Made& m, cudaStream_t st) {
 template <int ND, int PW>
 cudaError_t scan(const DeltaArgs& a, const ScanIo& io, cudaStream_t st) {
     const uint32_t sm = scan_smem<2 * C, PW>((int)a.N);
-    const cudaError_t e = allow_smem(delta_scan<ND, PW>, sm);
+    const cudaError_t e = allow<delta_scan<ND, PW>>(scan_smem<2 * C, PW>(ND));
     if (e != cudaSuccess) return e;
     delta_scan<ND, PW><<<(unsigned)(a.Bz * a.H * (a.P / PW)), scan_threads(PW), sm, st>>>(io, a.lens, geo(a));
     return cudaGetLastError();
@@ -782,7 +780,7 @@ cudaError_t scan_by_heads(const DeltaArgs& a, const ScanIo& io, cudaStream_t st)
 template <int ND>
 cudaError_t both(const DeltaArgs& a, const ScanIo& back, const ScanIo& fwd, cudaStream_t st) {
     const uint32_t sm = scan_smem<C, 16>((int)a.N);
-    const cudaError_t e = allow_smem(delta_both_scans<ND>, sm);
+    const cudaError_t e = allow<delta_both_scans<ND>>(scan_smem<C, 16>(ND));
     if (e != cudaSuccess) return e;
     delta_both_scans<ND><<<(unsigned)(2 * a.Bz * a.H * (a.P / 16)), scan_threads(16), sm, st>>>(back, fwd, a.lens, geo(a));
     return cudaGetLastError();
@@ -808,8 +806,11 @@ cudaError_t both_scans(const DeltaArgs& a, float* ws, float* states, float* afte
 template <typename E, typename O>
 cudaError_t grad(const DeltaArgs& a, const float* states, const float* after, const float* writes, const float* zs,
                  void* gq, void* gk, cudaStream_t st) {
-    const size_t sm = sizeof(float) * (3 * C * (a.P + 4) + 2 * C * (a.N + 4) + C * LT + 32 * (a.P + 4));
-    cudaError_t e = allow_smem(delta_grad<E, O>, sm);
+    auto bytes = [](int64_t N, int64_t P) {
+        return (uint32_t)(sizeof(float) * (3 * C * (P + 4) + 2 * C * (N + 4) + C * LT + 32 * (P + 4)));
+    };
+    const uint32_t sm = bytes(a.N, a.P);
+    cudaError_t e = allow<delta_grad<E, O>>(bytes(128, 128));
     if (e != cudaSuccess) return e;
     delta_grad<E, O><<<(unsigned)(a.Bz * a.H * chunks(a)), NT, sm, st>>>(
         static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), a.g, a.beta,

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "cssd_internal.h"
 
 namespace cssd {
@@ -36,6 +38,21 @@ __device__ __forceinline__ int row_len(const int* lens, int b, int T) {
 // (if it was launched so) start; wait until the kernel before it has ended.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Dynamic shared memory of kernel F, allowed once per device (`bytes` is the
+// most that any launch of F asks for).
+template <auto* F>
+inline cudaError_t allow(uint32_t bytes) {
+    static std::atomic<uint64_t> done[2] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool track = dev >= 0 && dev < 128;
+    if (track && (done[dev / 64].load(std::memory_order_acquire) >> (dev % 64) & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(F), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && track) done[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_release);
+    return e;
+}
 
 // A sum kept as two floats, value and what its rounding left.
 struct Sum2 {

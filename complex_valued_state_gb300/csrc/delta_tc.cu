@@ -29,7 +29,6 @@
 // 64/64 530 us (prep 112, scans 206, delta_grad_tc 209), 4 x 1501 x 16 on 8 key
 // heads, 128/128 354 us (45, 111, 178 and 20 for the sum over shared heads).
 
-#include <atomic>
 #include <type_traits>
 
 #include "delta_tc.cuh"
@@ -1960,20 +1959,6 @@ Shape shape(const DeltaArgs& a) {
     return Shape{(int)a.T, (int)a.H, (int)(a.H / a.KH), (int)a.N, (int)a.P, nc, 0, nc};
 }
 int64_t chunk_count(const DeltaArgs& a) { return a.Bz * a.H * ((a.T + C - 1) / C); }
-
-// Dynamic shared memory of kernel F, allowed once per device.
-template <auto* F>
-cudaError_t allow(uint32_t bytes) {
-    static std::atomic<uint64_t> done[2] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const bool track = dev >= 0 && dev < 128;
-    if (track && (done[dev / 64].load(std::memory_order_acquire) >> (dev % 64) & 1)) return cudaSuccess;
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(F), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && track) done[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_release);
-    return e;
-}
 
 // Workspace: the images of every chunk and value head, (the backward: those
 // for its own scan too), then the operands of every chunk and key head.

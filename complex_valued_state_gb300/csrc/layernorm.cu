@@ -12,8 +12,8 @@
 // the rows of its CTA, and the CTAs' sums are added up by a second kernel.
 //
 // Measured, bf16: 8192 x 1536 forward 10.3 us (4.9 TB/s of tensors that L2
-// partly holds), gradients 23 us (3.2 TB/s: the CTAs' 304 partial sums and the
-// kernel that joins them take 5 us of it); gradients of 65536 x 2048 168 us
+// partly holds), gradients 22 us (3.4 TB/s: the CTAs' 304 partial sums and the
+// kernel that joins them take 4 us of it); gradients of 65536 x 2048 168 us
 // (4.8 TB/s).
 
 #include <type_traits>
@@ -576,11 +576,10 @@ cudaError_t norm_bwd(const NormArgs& a, void* ws, cudaStream_t st) {
             const size_t smem = bytes > sums ? bytes : sums;
             const int64_t want = (a.rows + NG - 1) / NG;
             n = (int)(want < kBackGrid ? want : kBackGrid);
-            auto* kernel = norm_back_ring<E, WT, IT, G>;
-            const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            constexpr uint32_t most = 32 * G * IT * Vec<E>::W * (NG * kStages * 2 * sizeof(E) + 4);  // of the widest row
+            const cudaError_t e = delta::allow<norm_back_ring<E, WT, IT, G>>(most);
             if (e == cudaSuccess)
-                kernel<<<n, 32 * kRowWarps, smem, st>>>(dy, x, w, a.mean, a.rstd, gx, part, a.rows, (int)a.width, ww, wb,
+                norm_back_ring<E, WT, IT, G><<<n, 32 * kRowWarps, smem, st>>>(dy, x, w, a.mean, a.rstd, gx, part, a.rows, (int)a.width, ww, wb,
                                                         status_word());
             return e;
         };
