@@ -884,14 +884,14 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
             const uint32_t d1 = tmem + (KEEP ? COL_KS : COL_QS), d2 = tmem + COL_U;
             const uint64_t b1 = dqk + (KEEP ? QK<ND>::KROWS >> 4 : 0);
             constexpr uint32_t id = KEEP ? id64 : id128;  // without outputs only K's and T's rows
-            chain<ND / 16, 2 * QK<ND>::LBO>(d1, tmem + COL_S, b1, id, true);  // hi, then lo
-            chain<ND / 16, 2 * QK<ND>::LBO>(d1, tmem + COL_S + ND / 2, b1, id, false);
+            chain<ND / 16, 2 * QK<ND>::LBO>(d1, tmem + COL_S + ND / 2, b1, id, true);  // lo, then hi
+            chain<ND / 16, 2 * QK<ND>::LBO>(d1, tmem + COL_S, b1, id, false);
             commit_elected(&mb_ks);
             if (!warp_wait(&mb_r, ph, &s_gave_up)) break;
             tc::fence_after_sync();
-            chain<4, 2 * Image::LBO>(d2, tmem + COL_R, dtx, id, true);  // hi hi + lo hi + hi lo
-            chain<4, 2 * Image::LBO>(d2, tmem + COL_R + 32, dtx, id, false);
+            chain<4, 2 * Image::LBO>(d2, tmem + COL_R + 32, dtx, id, true);  // lo hi + hi lo + hi hi
             chain<4, 2 * Image::LBO>(d2, tmem + COL_R, dtx + (Image::PART >> 4), id, false);
+            chain<4, 2 * Image::LBO>(d2, tmem + COL_R, dtx, id, false);
             commit_elected(&mb_u);
             if (!KEEP) {
                 commit_elected(&mb_o);
@@ -899,8 +899,8 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
             }
             if (!warp_wait(&mb_w, ph, &s_gave_up)) break;
             tc::fence_after_sync();
-            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R, dkt, idn, true);
-            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R + 32, dkt, idn, false);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R + 32, dkt, idn, true);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R, dkt, idn, false);
             commit_elected(&mb_d);
         }
         if (s_gave_up) {
@@ -1307,27 +1307,27 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
             if (!warp_wait(&mb_full[j & 1], (j >> 1) & 1, &s_gave_up)) break;
             if (!warp_wait(&mb_s, ph, &s_gave_up)) break;
             tc::fence_after_sync();
-            chain<ND / 16, 2 * QK<ND>::LBO>(tmem + COL_KS, tmem + COL_S, dk, id64, true);  // hi, then lo
-            chain<ND / 16, 2 * QK<ND>::LBO>(tmem + COL_KS, tmem + COL_S + ND / 2, dk, id64, false);
+            chain<ND / 16, 2 * QK<ND>::LBO>(tmem + COL_KS, tmem + COL_S + ND / 2, dk, id64, true);  // lo, then hi
+            chain<ND / 16, 2 * QK<ND>::LBO>(tmem + COL_KS, tmem + COL_S, dk, id64, false);
             commit_elected(&mb_ks);
             if (!warp_wait(&mb_dx, ph, &s_gave_up)) break;
             tc::fence_after_sync();
-            chain<4, 2 * Image::LBO>(tmem + COL_Z2, tmem + COL_DX, dxt, id64, true);
-            chain<4, 2 * Image::LBO>(tmem + COL_Z2, tmem + COL_DX, dxt + (Image::PART >> 4), id64, false);
+            chain<4, 2 * Image::LBO>(tmem + COL_Z2, tmem + COL_DX, dxt + (Image::PART >> 4), id64, true);
+            chain<4, 2 * Image::LBO>(tmem + COL_Z2, tmem + COL_DX, dxt, id64, false);
             if (!warp_wait(&mb_r, ph, &s_gave_up)) break;
             tc::fence_after_sync();
-            chain<4, 2 * Image::LBO>(tmem + COL_Z1, tmem + COL_R, dtt, id64, true);  // hi hi + lo hi + hi lo
-            chain<4, 2 * Image::LBO>(tmem + COL_Z1, tmem + COL_R + 32, dtt, id64, false);
+            chain<4, 2 * Image::LBO>(tmem + COL_Z1, tmem + COL_R + 32, dtt, id64, true);  // lo hi + hi lo + hi hi
             chain<4, 2 * Image::LBO>(tmem + COL_Z1, tmem + COL_R, dtt + (Image::PART >> 4), id64, false);
+            chain<4, 2 * Image::LBO>(tmem + COL_Z1, tmem + COL_R, dtt, id64, false);
             commit_elected(&mb_z);
             if (lane == 0) mbar_arrive(&mb_z);  // (dO's scales, written before mb_dx, are before this)
             if (!warp_wait(&mb_w, ph, &s_gave_up)) break;
             if (!warp_wait(&mb_dq, ph, &s_gave_up)) break;
             tc::fence_after_sync();
-            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R, dkt, idn, true);
-            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R + 32, dkt, idn, false);
-            chain<4, 2 * KT<ND>::LBO>(tmem + COL_E, tmem + COL_DQ, dqt, idn, true);
-            chain<4, 2 * KT<ND>::LBO>(tmem + COL_E, tmem + COL_DQ + 32, dqt, idn, false);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R + 32, dkt, idn, true);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_D, tmem + COL_R, dkt, idn, false);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_E, tmem + COL_DQ + 32, dqt, idn, true);
+            chain<4, 2 * KT<ND>::LBO>(tmem + COL_E, tmem + COL_DQ, dqt, idn, false);
             commit_elected(&mb_d);
             if (lane == 0) mbar_arrive(&mb_d);
         }
@@ -1616,12 +1616,12 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem, base = tc::smem_u32(smem);
     constexpr uint32_t id64 = tc::idesc_f16(128, C), idn = tc::idesc_f16(128, ND);
-    // a (128 rows, hi and their rests) times b: hi hi + lo hi + hi lo
+    // a (128 rows, hi and their rests) times b: lo hi + hi lo + hi hi
     auto split_product = [&](uint32_t dcol, uint32_t a, uint32_t bb, uint32_t brest, uint32_t id) {
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
-            const uint64_t da = tc::make_desc(base + a + (p == 1 ? 3 * M::ROWS : 0), M::LBO, M::SBO);
-            const uint64_t db = tc::make_desc(base + bb + (p == 2 ? brest : 0), M::LBO, M::SBO);
+            const uint64_t da = tc::make_desc(base + a + (p == 0 ? 3 * M::ROWS : 0), M::LBO, M::SBO);
+            const uint64_t db = tc::make_desc(base + bb + (p == 1 ? brest : 0), M::LBO, M::SBO);
 #pragma unroll
             for (int kk = 0; kk < PD / 16; ++kk)
                 tc::mma_f16(tmem + dcol, da + 16 * kk, db + 16 * kk, id, p || kk);
@@ -1842,10 +1842,10 @@ __global__ void __launch_bounds__(GradSmem<ND, PD>::NT, ND == 128 || PD == 128 ?
         if (M::LATE) warp_wait(&mb_late, 0, &s_gave_up);
         const uint64_t dkt = tc::make_desc(base + M::KT0, KT<ND>::LBO, KT<ND>::SBO);
         const uint64_t dqt = tc::make_desc(base + M::QT0, KT<ND>::LBO, KT<ND>::SBO);
-        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem, dkt, idn, true);
-        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem + 32, dkt, idn, false);
-        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem + 64, dqt, idn, false);
+        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem + 32, dkt, idn, true);
         chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem + 96, dqt, idn, false);
+        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem, dkt, idn, false);
+        chain<4, 2 * KT<ND>::LBO>(tmem + COL_S, tmem + 64, dqt, idn, false);
         commit_elected(&mb_3);
     }
     warp_wait(&mb_3, 0, &s_gave_up);

@@ -8,8 +8,10 @@
 // value rounded to 11 bits) and lo (the remainder, at most 2^-12 of it, rounded
 // to 11 bits): 2^-24 of the row's largest value.  A product of an exact operand
 // with a split one takes two passes, of two split ones three (lo lo is left
-// out, 2^-24), all into one fp32 accumulator, so the states, which are float32
-// tensors of the interface, keep fp32 accuracy.
+// out, 2^-24), all into one fp32 accumulator, the low parts first: the
+// accumulator drops what lies below its last bit at every step, and so only the
+// last pass does at the full value.  The states, which are float32 tensors of
+// the interface, keep fp32 accuracy.
 #pragma once
 
 #include "delta_common.cuh"
