@@ -25,7 +25,7 @@
 // pipe is 15 % busy.
 //
 // Whole calls, bf16: forward 4 x 2048 x 24, 64/64 187 us (prep 92 us, half of it
-// beside the scan); 1 x 16384 x 32, 128/64 1050 us; gradients 4 x 2048 x 24,
+// beside the scan); 1 x 16384 x 32, 128/64 1072 us; gradients 4 x 2048 x 24,
 // 64/64 530 us (prep 112, scans 206, delta_grad_tc 209), 4 x 1501 x 16 on 8 key
 // heads, 128/128 354 us (45, 111, 178 and 20 for the sum over shared heads).
 
