@@ -334,7 +334,11 @@ __device__ __forceinline__ void scan_body(const ScanIo& io, int bh, int p0, cons
     float* su = st + PW * LS;    // U or Z, [64][LU]
     const int l1 = tid % S1, x1 = tid / S1 % X, tile1 = tid / (X * S1) * 4, row = tile1 + R1 * l1;
     const int l2 = tid % S2, x2 = tid / S2 % X, tile2 = tid / (X * S2) * 4, nr = tile2 + R2 * l2;
-    const bool there = tile2 < N;  // (all of a warp, or none: N is a multiple of 16)
+    // Whether this thread's rows of the state are there, the same for the S2 lanes of
+    // a tile, and whether any of its warp's are: a warp has 16 rows, or 32 (ND = 128
+    // in slices of 8 columns), and N, a multiple of 16, may end inside those.  What
+    // shuffles goes by the warp.
+    const bool there = tile2 < N, warp_there = (tid & ~31) / (X * S2) * 4 < N;
     const int64_t so = ((int64_t)bh * N + nr) * P + p0 + 4 * x2;  // this thread's state
     auto load = [&](int c, int buf) {
         const float* src = io.img + ((int64_t)bh * ge.nc + c) * image;
@@ -416,13 +420,8 @@ __device__ __forceinline__ void scan_body(const ScanIo& io, int bh, int p0, cons
             for (int a = 0; a < R2; ++a) more[a] = add[a];
         if (it + 1 < nck) load_init(chunk(it + 1));
         __syncthreads();
-        if (there) {
-            if (io.kept)
-#pragma unroll
-                for (int a = 0; a < R2; ++a)
-                    *reinterpret_cast<float4*>(io.kept + (ci * N + nr + a) * P + p0 + 4 * x2) =
-                        make_float4(s[a][0], s[a][1], s[a][2], s[a][3]);
-            const float* ku = img + ROWS * LA + tile2;
+        if (warp_there) {
+            const float* ku = img + ROWS * LA + min(tile2, N - 4);  // (lanes without rows: any that are there)
             f2 d[2][4] = {};  // pairs of rows
 #pragma unroll 4
             for (int i = l2; i < C; i += S2) {
@@ -440,14 +439,21 @@ __device__ __forceinline__ void scan_body(const ScanIo& io, int bh, int p0, cons
 #pragma unroll
             for (int i = 0; i < 4; ++i) un2(d[0][i], y[0][i], y[1][i]), un2(d[1][i], y[2][i], y[3][i]);
             join<S2>(y, l2);
-            const float all = img[(ROWS + C) * LA];
+            if (there) {
+                if (io.kept)
 #pragma unroll
-            for (int a = 0; a < R2; ++a) {
-                if (BACK) y[a][0] += more[a].x, y[a][1] += more[a].y, y[a][2] += more[a].z, y[a][3] += more[a].w;
+                    for (int a = 0; a < R2; ++a)
+                        *reinterpret_cast<float4*>(io.kept + (ci * N + nr + a) * P + p0 + 4 * x2) =
+                            make_float4(s[a][0], s[a][1], s[a][2], s[a][3]);
+                const float all = img[(ROWS + C) * LA];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[a][i] = fmaf(all, s[a][i], y[a][i]);
+                for (int a = 0; a < R2; ++a) {
+                    if (BACK) y[a][0] += more[a].x, y[a][1] += more[a].y, y[a][2] += more[a].z, y[a][3] += more[a].w;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[a][i] = fmaf(all, s[a][i], y[a][i]);
+                }
+                put_state();
             }
-            put_state();
         }
     }
     if (io.s_end && there)

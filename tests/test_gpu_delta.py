@@ -113,6 +113,22 @@ def test_backward(cs, shape, dtype):
     check_backward(cs, d, opt, back)
 
 
+# State widths that end inside a warp's 32 rows, on both sides of the head count
+# at which the fp32 scan takes narrower slices (batch x heads x headdim / 16 = 76).
+UNEVEN = [(1, 200, 2, 1, 80, 64), (2, 130, 3, 3, 112, 48), (1, 64, 1, 1, 112, 128), (2, 150, 10, 5, 80, 64),
+          (1, 129, 20, 20, 112, 80)]
+
+
+@pytest.mark.parametrize("dtype", ["fp32"])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("shape", UNEVEN)
+def test_uneven_state_widths(cs, shape, ragged, dtype):
+    lens = [shape[1] - 70, 65][:shape[0]] if ragged else None
+    d, opt, back = make(sum(shape) + 3, *shape, dtype=dtype, state=True, ragged=lens)
+    check_forward(cs, d, opt)
+    check_backward(cs, d, opt, back)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("NP", [(64, 64), (128, 128), (48, 80)])
 def test_ragged_rows(cs, NP, dtype):
