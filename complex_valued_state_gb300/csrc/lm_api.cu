@@ -30,8 +30,10 @@ int check_delta_dims(const cssd_delta_dims* d, int dtype, bool need_seq) {
     if (!supported_type(dtype) || !supported_width(d->dstate) || !supported_width(d->headdim)) return CSSD_ERR_UNSUPPORTED;
     if (d->nheads % d->kheads) return CSSD_ERR_DIMS;
     // the kernels index (batch, head, state slice) and (batch, head, chunk) in
-    // 32 bits and take up to four slices of a state
-    if (d->batch > kMaxInt || d->nheads > kMaxInt || !product_fits(d->batch, d->nheads, kMaxInt / 4)) return CSSD_ERR_DIMS;
+    // 32 bits: a step takes up to four slices of a state, a sequence in fp32 one of
+    // 16 columns each and its gradients that for two scans in one launch
+    const int64_t slices = need_seq && d->headdim / 8 > 4 ? d->headdim / 8 : 4;
+    if (d->batch > kMaxInt || d->nheads > kMaxInt || !product_fits(d->batch, d->nheads, kMaxInt / slices)) return CSSD_ERR_DIMS;
     if (need_seq) {
         if (d->seqlen > kMaxInt - 64) return CSSD_ERR_DIMS;
         if (!product_fits(d->batch * d->nheads, (d->seqlen + 63) / 64, kMaxInt)) return CSSD_ERR_DIMS;

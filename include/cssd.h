@@ -395,7 +395,7 @@ int cssd_born_attention(const cssd_dims* dims, const void* q, const void* k, con
  * Supported sizes: dstate and headdim multiples of 16 from 16 to 128 (else
  * CSSD_ERR_UNSUPPORTED); any batch, seqlen >= 1; nheads a multiple of kheads
  * (value head h reads key head h / (nheads / kheads)); nheads * batch below
- * 2^29.  Tensors are dense and row-major, q, k, v, o, the states and the
+ * 2^29, of a sequence whose headdim is above 32 below 2^34 / headdim.  Tensors are dense and row-major, q, k, v, o, the states and the
  * workspace 16-byte aligned, the float32 and int32 vectors 4-byte.
  * g is a log decay: at most 0 in a model, though any value whose exponentials
  * stay in range works; -inf forgets everything before the token.

@@ -124,6 +124,22 @@ def test_forward_refusals(lib):
     assert lib.cssd_delta_workspace_bytes(dims(*OK), 7) == 0
 
 
+def test_sizes_past_the_grid(lib):
+    """A sequence in fp32 takes a block per head and 16 columns, the gradients two:
+    sizes whose count of blocks would not fit 31 bits are refused."""
+    heads = (1 << 31) // 16
+    for dtype in (0, 2):
+        for n, P in ((heads, 128), (1 << 28, 64), (1 << 29, 16), (1 << 29, 32)):
+            for b, h in ((n, 1), (1, n), (1 << 10, n >> 10)):
+                d = (b, 1, h, 1, 16, P)
+                assert lib.cssd_delta_workspace_bytes(dims(*d), dtype) == 0, d
+                assert lib.cssd_delta_backward_workspace_bytes(dims(*d), dtype) == 0, d
+                assert forward(lib, d, dtype) == -2, d
+        for n, P in ((heads - 1, 128), ((1 << 28) - 1, 64), ((1 << 29) - 1, 32), ((1 << 29) - 1, 16)):
+            assert lib.cssd_delta_workspace_bytes(dims(1, 1, n, 1, 16, P), dtype) > 0, (n, P)
+            assert lib.cssd_delta_backward_workspace_bytes(dims(n, 1, 1, 1, 16, P), dtype) > 0, (n, P)
+
+
 def test_backward_refusals(lib):
     need = lib.cssd_delta_backward_workspace_bytes(dims(*OK), 2)
     assert need >= 2 * 4 * 2 * 4 * 2 * 64 * 64  # two fp32 states a head and chunk
