@@ -5,6 +5,12 @@ checks dtype / shape / contiguity, and passes raw pointers and sizes to the C
 ABI declared in ``include/cssd.h``.  All arithmetic runs in the library's
 kernels.  If ``libcssd.so`` is missing the first call raises: there is no CPU
 fallback.
+
+With ``stream=`` a call runs on that stream in place of the current one.  What
+it returns then belongs to that stream's memory pool and is recorded on the
+current stream, which has to wait for the other before it reads it.  Tensors
+that the caller passes are the caller's: ready on that stream, and kept (or
+recorded on it) until its work is done.
 """
 
 from __future__ import annotations
@@ -168,6 +174,22 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory of a result.  With a stream of the caller's it is from that stream's
+    pool: memory of the current stream's may still be in use there, and would go
+    back there, were the result dropped, while the call's kernels write it."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))  # whose reads come before the memory's next use
+    return t
+
+
+def _empty_like(t, stream):
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
+
+
 # Bits of the device status word (cssd_device_status).
 STATUS_HANDOFF_TIMEOUT = 1
 STATUS_CHUNK_MMA_TIMEOUT = 2
@@ -259,10 +281,10 @@ def chunked_forward(x, dt, A, B, C, D, *, chunk: int = 64, y=None, h_final=None,
     _check(C, "C", c64, (Bz, T, H, N), dev)
     _check(D, "D", f32, (H,), dev)
     if y is None:
-        y = torch.empty((Bz, T, H, P), dtype=c64, device=dev)
+        y = _empty((Bz, T, H, P), c64, dev, stream)
     _check(y, "y", c64, (Bz, T, H, P), dev)
     if h_final is None and want_state:
-        h_final = torch.empty((Bz, H, N, P), dtype=c64, device=dev)
+        h_final = _empty((Bz, H, N, P), c64, dev, stream)
     if h_final is not None:
         _check(h_final, "h_final", c64, (Bz, H, N, P), dev)
     ws_bytes = 0
@@ -388,7 +410,7 @@ def chunked_backward(x, dt, A, B, C, D, dy, *, chunk: int = 64, grads=None, work
               "gC": ((Bz, T, H, N), c64), "gD": ((H,), f32)}
     for k, (shp, dtp) in shapes.items():
         if k not in g:
-            g[k] = torch.empty(shp, dtype=dtp, device=dev)
+            g[k] = _empty(shp, dtp, dev, stream)
         _check(g[k], k, dtp, shp, dev)
     ws_bytes = 0
     if workspace is not None:
@@ -425,10 +447,10 @@ def chunked_forward_noalloc(x, dt, A, B, C, D, *, chunk: int = 64, y=None, h_fin
     _check(C, "C", c64, (Bz, T, H, N), dev)
     _check(D, "D", f32, (H,), dev)
     if y is None:
-        y = torch.empty((Bz, T, H, P), dtype=c64, device=dev)
+        y = _empty((Bz, T, H, P), c64, dev, stream)
     _check(y, "y", c64, (Bz, T, H, P), dev)
     if h_final is None and want_state:
-        h_final = torch.empty((Bz, H, N, P), dtype=c64, device=dev)
+        h_final = _empty((Bz, H, N, P), c64, dev, stream)
     if h_final is not None:
         _check(h_final, "h_final", c64, (Bz, H, N, P), dev)
     d = Dims(Bz, T, H, N, P)
@@ -439,7 +461,7 @@ def chunked_forward_noalloc(x, dt, A, B, C, D, *, chunk: int = 64, y=None, h_fin
     return y, h_final
 
 
-def _check_step_inputs(dev, Bz, H, N, P, x, dt, A, B, C, D, y):
+def _check_step_inputs(dev, Bz, H, N, P, x, dt, A, B, C, D, y, stream):
     c64, f32 = torch.complex64, torch.float32
     _check(x, "x", c64, (Bz, H, P), dev)
     _check(dt, "dt", f32, (Bz, H), dev)
@@ -448,7 +470,7 @@ def _check_step_inputs(dev, Bz, H, N, P, x, dt, A, B, C, D, y):
     _check(C, "C", c64, (Bz, H, N), dev)
     _check(D, "D", f32, (H,), dev)
     if y is None:
-        y = torch.empty((Bz, H, P), dtype=c64, device=dev)
+        y = _empty((Bz, H, P), c64, dev, stream)
     _check(y, "y", c64, (Bz, H, P), dev)
     return y
 
@@ -463,7 +485,7 @@ def step(h, x, dt, A, B, C, D, *, y=None, stream=None):
     dev = h.device
     Bz, H, N, P = h.shape
     _check(h, "h", torch.complex64, (Bz, H, N, P), dev)
-    y = _check_step_inputs(dev, Bz, H, N, P, x, dt, A, B, C, D, y)
+    y = _check_step_inputs(dev, Bz, H, N, P, x, dt, A, B, C, D, y, stream)
     d = Dims(Bz, 1, H, N, P)
     st = lib.cssd_step(ctypes.byref(d), _ptr(h), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(y),
                        _stream_handle(stream, dev))
@@ -479,7 +501,7 @@ def step_n(h, x, dt, A, B, C, D, nsteps, *, y=None, stream=None):
     dev = h.device
     Bz, H, N, P = h.shape
     _check(h, "h", torch.complex64, (Bz, H, N, P), dev)
-    y = _check_step_inputs(dev, Bz, H, N, P, x, dt, A, B, C, D, y)
+    y = _check_step_inputs(dev, Bz, H, N, P, x, dt, A, B, C, D, y, stream)
     d = Dims(Bz, 1, H, N, P)
     st = lib.cssd_step_n(ctypes.byref(d), _ptr(h), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                          ctypes.c_int64(int(nsteps)), _ptr(y), _stream_handle(stream, dev))
@@ -495,7 +517,7 @@ def step_infinite(x, dt, A, B, C, D, *, y=None, stream=None):
     dev = x.device
     Bz, H, P = x.shape
     N = B.shape[-1]
-    y = _check_step_inputs(dev, Bz, H, N, P, x, dt, A, B, C, D, y)
+    y = _check_step_inputs(dev, Bz, H, N, P, x, dt, A, B, C, D, y, stream)
     d = Dims(Bz, 1, H, N, P)
     st = lib.cssd_step_infinite(ctypes.byref(d), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(y),
                                 _stream_handle(stream, dev))
@@ -522,10 +544,10 @@ def cayley_scan(phi, u, b, C, *, psi0=None, chunk=64, log_clamp=-30.0, y=None, p
     if psi0 is not None:
         _check(psi0, "psi0", c64, (Bz, H, N), dev)
     if y is None:
-        y = torch.empty((Bz, T, H, N), dtype=c64, device=dev)
+        y = _empty((Bz, T, H, N), c64, dev, stream)
     _check(y, "y", c64, (Bz, T, H, N), dev)
     if psi_final is None:
-        psi_final = torch.empty((Bz, H, N), dtype=c64, device=dev)
+        psi_final = _empty((Bz, H, N), c64, dev, stream)
     _check(psi_final, "psi_final", c64, (Bz, H, N), dev)
     d = Dims(Bz, T, H, N, 0)
     st = lib.cssd_cayley_scan(ctypes.byref(d), _ptr(phi), _ptr(u), _ptr(b), _ptr(C), _ptr(psi0), _ptr(y),
@@ -549,7 +571,7 @@ def born_attention(q, k, v, *, psi=None, stream=None):
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _check(t, n, c64, (Bz, T, H, D), dev)
     if psi is None:
-        psi = torch.empty((Bz, T, H, D), dtype=c64, device=dev)
+        psi = _empty((Bz, T, H, D), c64, dev, stream)
     _check(psi, "psi", c64, (Bz, T, H, D), dev)
     d = Dims(Bz, T, H, D, 0)
     st = lib.cssd_born_attention(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(psi), _stream_handle(stream, dev))
@@ -655,13 +677,13 @@ def delta_forward(q, k, v, g, beta, *, scale=None, h0=None, lens=None, o=None, h
     if lens is not None:
         _expect(lens, "lens", torch.int32, (Bz,), index)
     if o is None:
-        o = torch.empty_like(v)
+        o = _empty_like(v, stream)
     else:
         _expect(o, "o", q.dtype, v.shape, index)
     if h_final is not None:
         _expect(h_final, "h_final", torch.float32, state, index)
     elif want_state:
-        h_final = torch.empty(state, dtype=torch.float32, device=q.device)
+        h_final = _empty(state, torch.float32, q.device, stream)
     st = _stream_of(stream, index)
     d = _delta_dims(Bz, T, H, KH, N, P)
     ws, nbytes = _scratch(workspace, lib.cssd_delta_workspace_bytes(d, dt) if workspace is None else 0, q, stream)
@@ -697,11 +719,11 @@ def delta_backward(q, k, v, g, beta, do, *, scale=None, h0=None, dh_final=None, 
         if name in r:
             _expect(r[name], name, like.dtype, like.shape, index)
         else:
-            r[name] = torch.empty_like(like)
+            r[name] = _empty_like(like, stream)
     if "gh0" in r:
         _expect(r["gh0"], "gh0", f32, state, index)
     else:
-        r["gh0"] = torch.empty(state, dtype=f32, device=q.device)
+        r["gh0"] = _empty(state, f32, q.device, stream)
     st = _stream_of(stream, index)
     d = _delta_dims(Bz, T, H, KH, N, P)
     ws, nbytes = _scratch(workspace, lib.cssd_delta_backward_workspace_bytes(d, dt) if workspace is None else 0, q, stream)
@@ -730,7 +752,7 @@ def delta_step(h, q, k, v, g, beta, *, scale=None, slots=None, o=None, stream=No
     if slots is not None:
         _expect(slots, "slots", torch.int32, (Bz,), index)
     if o is None:
-        o = torch.empty_like(v)
+        o = _empty_like(v, stream)
     else:
         _expect(o, "o", q.dtype, v.shape, index)
     r = lib.cssd_delta_step(_delta_dims(Bz, 1, H, KH, N, P), dt, h.data_ptr(), nslots, _opt(slots), q.data_ptr(),
@@ -775,11 +797,11 @@ def layernorm(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, stream=No
     lib = _lib or load()
     xt, wt, rows, D, index = _norm_inputs(x, weight, bias)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty_like(x, stream)
     else:
         _expect(y, "y", x.dtype, x.shape, index)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
+    mean = _empty(x.shape[:-1], torch.float32, x.device, stream)
+    rstd = _empty_like(mean, stream)
     r = lib.cssd_layernorm(rows, D, xt, wt, x.data_ptr(), _opt(weight), _opt(bias), eps, y.data_ptr(), mean.data_ptr(),
                            rstd.data_ptr(), _stream_of(stream, index))
     if r != CSSD_OK:
@@ -803,7 +825,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, *, want_weight: bool = True, w
     if "gx" in r:
         _expect(r["gx"], "gx", x.dtype, x.shape, index)
     else:
-        r["gx"] = torch.empty_like(x)
+        r["gx"] = _empty_like(x, stream)
     wdtype = x.dtype if weight is None else weight.dtype
     for name, wanted in (("gweight", want_weight), ("gbias", want_bias)):
         if not wanted:
@@ -811,7 +833,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, *, want_weight: bool = True, w
         if name in r:
             _expect(r[name], name, wdtype, (D,), index)
         else:
-            r[name] = torch.empty(D, dtype=wdtype, device=x.device)
+            r[name] = _empty((D,), wdtype, x.device, stream)
     st = _stream_of(stream, index)
     ws, nbytes = _scratch(workspace, lib.cssd_layernorm_backward_workspace_bytes(rows, D) if workspace is None else 0, x,
                           stream)
