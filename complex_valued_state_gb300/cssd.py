@@ -809,15 +809,22 @@ def layernorm(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, stream=No
     return y, mean, rstd
 
 
-def layernorm_backward(dy, x, weight, mean, rstd, *, want_weight: bool = True, want_bias: bool = True, grads=None,
-                       workspace=None, stream=None):
+def layernorm_backward(dy, x, weight, mean, rstd, *, want_weight: bool = True, want_bias: bool = True, wdtype=None,
+                       grads=None, workspace=None, stream=None):
     """cssd_layernorm_backward; returns a dict gx (x's type) and, when wanted,
-    gweight and gbias (weight's type; x's when weight is None).
+    gweight and gbias, of type `wdtype`: weight's or, without a weight, the
+    bias's, x's type (the default then) or float32.
 
     mean and rstd are those layernorm returned for x.
     """
     lib = _lib or load()
-    xt, wt, rows, D, index = _norm_inputs(x, weight)
+    xt, _, rows, D, index = _norm_inputs(x, weight)
+    allowed = (x.dtype, torch.float32) if weight is None else (weight.dtype,)
+    if wdtype is None:
+        wdtype = allowed[0]
+    elif wdtype not in allowed:
+        raise TypeError(f"wdtype must be {' or '.join(map(str, allowed))}, got {wdtype}")
+    wt = _DTYPES[wdtype]
     _expect(dy, "dy", x.dtype, x.shape, index)
     _expect(mean, "mean", torch.float32, x.shape[:-1], index)
     _expect(rstd, "rstd", torch.float32, x.shape[:-1], index)
@@ -826,7 +833,6 @@ def layernorm_backward(dy, x, weight, mean, rstd, *, want_weight: bool = True, w
         _expect(r["gx"], "gx", x.dtype, x.shape, index)
     else:
         r["gx"] = _empty_like(x, stream)
-    wdtype = x.dtype if weight is None else weight.dtype
     for name, wanted in (("gweight", want_weight), ("gbias", want_bias)):
         if not wanted:
             continue

@@ -248,3 +248,22 @@ def test_binding_rejects_wrong_tensors():
         cssd.layernorm(x.t())
     with pytest.raises(ValueError):
         cssd.layernorm_backward(x, x, None, torch.zeros(3), torch.zeros(4))
+
+
+def test_binding_types_of_norm_gradients():
+    """Without a weight `wdtype` names the bias's type: its gradient is taken in
+    that type (past the checks, tensors off the GPU are refused)."""
+    x, stat = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(4)
+    f32, half = torch.zeros(8), torch.zeros(8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        cssd.layernorm_backward(x, x, None, stat, stat, want_weight=False, wdtype=torch.float32, grads={"gbias": f32})
+    with pytest.raises(ValueError, match="CUDA device"):
+        cssd.layernorm_backward(x, x, f32, stat, stat, wdtype=torch.float32, grads={"gweight": f32, "gbias": f32})
+    with pytest.raises(TypeError, match="gbias"):
+        cssd.layernorm_backward(x, x, None, stat, stat, wdtype=torch.float32, grads={"gbias": half})
+    with pytest.raises(TypeError, match="gbias"):
+        cssd.layernorm_backward(x, x, None, stat, stat, grads={"gbias": f32})
+    with pytest.raises(TypeError, match="wdtype"):
+        cssd.layernorm_backward(x, x, None, stat, stat, wdtype=torch.float16)
+    with pytest.raises(TypeError, match="wdtype"):
+        cssd.layernorm_backward(x, x, f32, stat, stat, wdtype=torch.bfloat16)

@@ -210,3 +210,18 @@ def test_offsets_past_32_bits(cs, width):
     gx, gw, gb = ref.layernorm_backward(f64(last), f64(last), None, 1e-5)
     close(g["gx"][-8:], gx, "gx", top=np.max(rs), inner=8 * INNER)
     close(g["gbias"], gb, "gbias", top=np.max(np.sum(np.abs(f64(last)), 0)))
+
+
+@pytest.mark.parametrize("width", [96, 101, 8200])
+def test_float_bias_without_weight(cs, width):
+    """A float32 bias of a bfloat16 x: its gradient keeps float32's digits (the
+    sums of 300 rows in bfloat16 would be off by up to 2^-9 of themselves)."""
+    x, _, _, dy = make(8, 300, width, "bf16", "fp32", affine=False)
+    b = torch.linspace(-1, 1, width)
+    y, mean, rstd = cs.layernorm(x.cuda(), None, b.cuda())
+    want, m, r = ref.layernorm(f64(x), None, f64(b), 1e-5)
+    close(y, want, "y", inner=4 * INNER)
+    g = cs.layernorm_backward(dy.cuda(), x.cuda(), None, mean, rstd, want_weight=False, wdtype=torch.float32)
+    assert g["gbias"].dtype is torch.float32
+    _, _, gb = ref.layernorm_backward(f64(dy), f64(x), None, 1e-5)
+    close(g["gbias"], gb, "gbias", top=np.max(np.sum(np.abs(f64(dy)), 0)), inner=(300 / 304 + 64) * 2.0 ** -24)
