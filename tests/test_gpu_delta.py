@@ -119,7 +119,7 @@ UNEVEN = [(1, 200, 2, 1, 80, 64), (2, 130, 3, 3, 112, 48), (1, 64, 1, 1, 112, 12
           (1, 129, 20, 20, 112, 80)]
 
 
-@pytest.mark.parametrize("dtype", ["fp32"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("ragged", [False, True])
 @pytest.mark.parametrize("shape", UNEVEN)
 def test_uneven_state_widths(cs, shape, ragged, dtype):
