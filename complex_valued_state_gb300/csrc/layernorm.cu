@@ -179,9 +179,10 @@ __global__ void __launch_bounds__(256) norm_stream(const E* x, const WT* __restr
 // --------------------------------------------------------------- backward
 // One row's share of the sums (a: dy w, so sum a and sum a xh) and of the
 // column sums, for a vector of the row, two elements an instruction.
-// `r2` holds rstd twice, `mr2` -mean rstd.
+// `r2` holds rstd twice, `m2` -mean: the mean is taken off before rstd is
+// multiplied on, since x rstd - mean rstd would be off by 2^-24 of mean rstd.
 template <typename E>
-__device__ __forceinline__ void back_sums(const uint4& xr, const uint4& dr, f2 r2, f2 mr2, const f2* wv, f2& s1, f2& s2,
+__device__ __forceinline__ void back_sums(const uint4& xr, const uint4& dr, f2 r2, f2 m2, const f2* wv, f2& s1, f2& s2,
                                           f2 (&gw)[Vec<E>::W / 2], f2 (&gb)[Vec<E>::W / 2]) {
     float xf[Vec<E>::W], df[Vec<E>::W];
     unpack<E>(xr, xf);
@@ -189,7 +190,7 @@ __device__ __forceinline__ void back_sums(const uint4& xr, const uint4& dr, f2 r
 #pragma unroll
     for (int u = 0; u < Vec<E>::W / 2; ++u) {
         const f2 d = mk2(df[2 * u], df[2 * u + 1]);
-        const f2 xh = fma2(mk2(xf[2 * u], xf[2 * u + 1]), r2, mr2), a = mul2(d, wv[u]);
+        const f2 xh = mul2(add2(mk2(xf[2 * u], xf[2 * u + 1]), m2), r2), a = mul2(d, wv[u]);
         s1 = add2(s1, a);
         s2 = fma2(a, xh, s2);
         gw[u] = fma2(d, xh, gw[u]);
@@ -198,15 +199,15 @@ __device__ __forceinline__ void back_sums(const uint4& xr, const uint4& dr, f2 r
 }
 // dx of the vector: `t1` and `t2` hold -rstd times the row's two means.
 template <typename E>
-__device__ __forceinline__ uint4 back_dx(const uint4& xr, const uint4& dr, f2 r2, f2 mr2, const f2* wv, f2 t1, f2 t2) {
+__device__ __forceinline__ uint4 back_dx(const uint4& xr, const uint4& dr, f2 r2, f2 m2, const f2* wv, f2 t1, f2 t2) {
     float xf[Vec<E>::W], df[Vec<E>::W];
     unpack<E>(xr, xf);
     unpack<E>(dr, df);
 #pragma unroll
     for (int u = 0; u < Vec<E>::W / 2; ++u) {
-        const f2 xh = fma2(mk2(xf[2 * u], xf[2 * u + 1]), r2, mr2);
-        const f2 a = mul2(mul2(mk2(df[2 * u], df[2 * u + 1]), wv[u]), r2);
-        un2(fma2(xh, t2, add2(a, t1)), xf[2 * u], xf[2 * u + 1]);
+        const f2 xh = mul2(add2(mk2(xf[2 * u], xf[2 * u + 1]), m2), r2);
+        const f2 a = mul2(mk2(df[2 * u], df[2 * u + 1]), wv[u]);
+        un2(fma2(xh, t2, fma2(a, r2, t1)), xf[2 * u], xf[2 * u + 1]);
     }
     return pack<E>(xf);
 }
@@ -278,12 +279,12 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
         if (!tc::mbar_wait_bounded(&full[group][st], (uint32_t)(k / kStages & 1), kNormWait)) s_gave_up = 1;
         const uint4* xr = reinterpret_cast<const uint4*>(mine + st * 2 * bytes);
         const uint4* dr = reinterpret_cast<const uint4*>(mine + st * 2 * bytes + bytes);
-        const f2 r2 = mk2(rs, rs), mr2 = mk2(-m * rs, -m * rs);
+        const f2 r2 = mk2(rs, rs), m2 = mk2(-m, -m);
         f2 p1 = 0, p2 = 0;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = gt + TG * i;
-            if (c < nv) back_sums<E>(xr[c], dr[c], r2, mr2, reinterpret_cast<const f2*>(sw + c * W), p1, p2, gw[i], gb[i]);
+            if (c < nv) back_sums<E>(xr[c], dr[c], r2, m2, reinterpret_cast<const f2*>(sw + c * W), p1, p2, gw[i], gb[i]);
         }
         float s1 = sum2(p1), s2 = sum2(p2);
         s1 = warp_sum(s1);
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
         for (int i = 0; i < IT; ++i) {
             const int c = gt + TG * i;
             if (c < nv)
-                __stcs(gp + c, back_dx<E>(xr[c], dr[c], r2, mr2, reinterpret_cast<const f2*>(sw + c * W), mk2(t1, t1), mk2(t2, t2)));
+                __stcs(gp + c, back_dx<E>(xr[c], dr[c], r2, m2, reinterpret_cast<const f2*>(sw + c * W), mk2(t1, t1), mk2(t2, t2)));
         }
     }
     if (gt == 0 && s_gave_up)  // no copy may land in shared memory that is no longer this CTA's
@@ -390,10 +391,10 @@ __global__ void __launch_bounds__(MAXT) norm_back_rows(const E* dy, const E* x,
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             f2 p1 = 0, p2 = 0;
-            const f2 r2 = mk2(rs[r], rs[r]), mr2 = mk2(-m[r] * rs[r], -m[r] * rs[r]);
+            const f2 r2 = mk2(rs[r], rs[r]), m2 = mk2(-m[r], -m[r]);
 #pragma unroll
             for (int i = 0; i < IT; ++i)
-                if (tid + nt * i < nv) back_sums<E>(xr[r][i], dr[r][i], r2, mr2, wv[i], p1, p2, gw[i], gb[i]);
+                if (tid + nt * i < nv) back_sums<E>(xr[r][i], dr[r][i], r2, m2, wv[i], p1, p2, gw[i], gb[i]);
             s[2 * r] = sum2(p1);
             s[2 * r + 1] = sum2(p2);
         }
@@ -412,14 +413,14 @@ __global__ void __launch_bounds__(MAXT) norm_back_rows(const E* dy, const E* x,
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (r0 + r >= rows) break;
-            const f2 r2 = mk2(rs[r], rs[r]), mr2 = mk2(-m[r] * rs[r], -m[r] * rs[r]);
+            const f2 r2 = mk2(rs[r], rs[r]), m2 = mk2(-m[r], -m[r]);
             const float t1 = -rs[r] * s[2 * r], t2 = -rs[r] * s[2 * r + 1];
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int c = tid + nt * i;
                 if (c < nv)
                     __stcs(reinterpret_cast<uint4*>(gx + (r0 + r) * width) + c,
-                           back_dx<E>(xr[r][i], dr[r][i], r2, mr2, wv[i], mk2(t1, t1), mk2(t2, t2)));
+                           back_dx<E>(xr[r][i], dr[r][i], r2, m2, wv[i], mk2(t1, t1), mk2(t2, t2)));
             }
         }
     }

@@ -225,3 +225,23 @@ def test_float_bias_without_weight(cs, width):
     assert g["gbias"].dtype is torch.float32
     _, _, gb = ref.layernorm_backward(f64(dy), f64(x), None, 1e-5)
     close(g["gbias"], gb, "gbias", top=np.max(np.sum(np.abs(f64(dy)), 0)), inner=(300 / 304 + 64) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype,width", [("fp32", 512), ("fp32", 1028), ("fp32", 4096), ("fp32", 513), ("fp16", 512)])
+def test_gradients_of_rows_far_from_zero(cs, dtype, width):
+    """Rows 10000 deviations from zero (100 in fp16): with the mean as it is given,
+    x - mean is off by 2^-24 of itself, so x^ and each term of the weight gradient
+    by 3 x 2^-24, whatever the offset."""
+    r = np.random.default_rng(9)
+    x = torch.from_numpy(((100.0 if dtype == "fp16" else 1e4) + r.standard_normal((9, width))).astype(np.float32)).to(TYPES[dtype])
+    dy = torch.from_numpy(r.standard_normal((9, width)).astype(np.float32)).to(TYPES[dtype])
+    w = torch.from_numpy((1 + 0.3 * r.standard_normal(width)).astype(np.float32))
+    _, mean, rstd = cs.layernorm(x.cuda(), w.cuda())
+    g = cs.layernorm_backward(dy.cuda(), x.cuda(), w.cuda(), mean, rstd)
+    rs = f64(rstd.cpu())[:, None]
+    xh = (f64(x) - f64(mean.cpu())[:, None]) * rs
+    a = f64(dy) * f64(w)
+    gx = rs * (a - a.mean(1, keepdims=True) - xh * (a * xh).mean(1, keepdims=True))
+    close(g["gx"], gx, "gx")
+    terms = np.max(np.sum(np.abs(f64(dy) * xh), 0))
+    close(g["gweight"], (f64(dy) * xh).sum(0), "gweight", top=terms, inner=(9 / 304 + 64 + 3) * 2.0 ** -24)
