@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
             ff[Image::OX + tid] = scale * xs.down;
         }
     } else if (warp == 2) {
-        put_scalars(ff, d.all, fmaxf(s_norm[lane] * d.in[lane], s_norm[lane + 32] * d.in[lane + 32]) * sqrtf((float)ND),
+        put_scalars(ff, d.all, fmaxf(s_norm[lane] * d.in[lane], s_norm[lane + 32] * d.in[lane + 32]) * sqrtf((float)sh.N),
                     fmaxf(bound2(lane, d.out), bound2(lane + 32, d.out)), 0.f, lane);
     }
     write_out(image);
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
                 b2 = fmaxf(b2, f * ((s_sum[0][i] + s_sum[1][i]) + (s_sum[2][i] + s_sum[3][i])));
                 b3 = fmaxf(b3, f * fabsf(scale) * ((s_sumx[0][i] + s_sumx[1][i]) + (s_sumx[2][i] + s_sumx[3][i])));
             }
-            put_scalars(ff, d.all, b1 * sqrtf((float)ND), b2, b3, lane);
+            put_scalars(ff, d.all, b1 * sqrtf((float)sh.N), b2, b3, lane);
         }
         write_out(image_t);
     }
@@ -420,7 +420,6 @@ constexpr int CW = 4 * PARTS;  // chain warps
 constexpr int OW = 4;          // output warps, one per lane quarter
 constexpr int ST = 32 * (CW + OW + 4);  // then two warps that load V, the MMA warp and the bulk loader
 constexpr int EP = C / PARTS;  // tokens of a row a chain thread has
-constexpr int EXACT = 4;       // chunks between exact bounds on the state (see the scales below)
 // Registers a thread of the chain, the outputs and the rest: 4 x 88 + 88 + 40
 // = 4 x 80 + 104 + 56 = 6 x 80, what the block starts with.
 template <int ND>
@@ -447,23 +446,28 @@ struct ScanSmem {
 constexpr uint32_t COL_S = 0, COL_R = 128, COL_QS = 192, COL_KS = 256, COL_D = 256, COL_U = 384, COL_X = 448,
                    TMEM_COLS = 512;
 
-// What the chain's threads of a row share: the largest of their values,
-// through shared memory, two slots in turn.
-struct RowTop {
-    float (*slots)[PARTS * 128];
+// What the chain's threads of a row share: the largest of their first values
+// and the sum of their second ones, through shared memory, two slots in turn.
+// (The sum in one order, so that all of them get the same bits.)
+struct RowShare {
+    float2 (*slots)[PARTS * 128];
     uint64_t* bar;  // PARTS arrivals a phase, one a warp
     int* gave_up;
     int part, v, n = 0;
-    __device__ __forceinline__ float of_all(float x) {
-        float* at = slots[n & 1];
-        at[part * 128 + v] = x;
+    __device__ __forceinline__ float2 of_all(float top, float part_of_sum) {
+        float2* at = slots[n & 1];
+        at[part * 128 + v] = make_float2(top, part_of_sum);
         __syncwarp();
         if (v % 32 == 0) mbar_arrive(bar);
         warp_wait(bar, n & 1, gave_up);  // (a wait that gives up leaves a wrong bound; the chunk's next wait gives up too)
         ++n;
+        float2 y = at[v];
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) x = fmaxf(x, at[p * 128 + v]);
-        return x;
+        for (int p = 1; p < PARTS; ++p) {
+            const float2 x = at[p * 128 + v];
+            y = make_float2(fmaxf(y.x, x.x), y.y + x.y);
+        }
+        return y;
     }
 };
 
@@ -478,7 +482,6 @@ __device__ __forceinline__ float top_of_pairs(const f2 (&x)[NP]) {
     }
     return fmaxf(t[0], t[1]);
 }
-
 // Eight pairs of a lane's row, already scaled, split and stored as A-operand
 // columns at `hi` and `lo`.
 __device__ __forceinline__ void store_split(const f2 (&y)[8], uint32_t hi, uint32_t lo) {
@@ -517,20 +520,29 @@ __device__ __forceinline__ void chain(uint32_t d, uint32_t a, uint64_t bd, uint3
 // Scales of the operands made on the chain.  A half has 16 bits of exponent
 // range below the point where hi and lo together lose a bit of the row's
 // largest value, so a row's scale may come from a bound on it that is loose by
-// up to 2^16.  With E the largest value of a lane's state column, exact every
-// fourth chunk (found while R [T; X] runs) and else the bound it was stored
-// with, and V's,
+// up to 2^16.  With E the bound on a lane's state column, max and sum over it and
+// over the chunk's tokens,
 //     |R|  <= max |v| + max_i(e^{G_i} |k_i|) sqrt(N) E
 //     |U'| <= max_i(|T_i|_1 e^{G_end - G_i}) |R|
-//     |S+| <= e^{G_end} E + 64 max |k_i U'_i|    (U' exact, found while K^T U' runs)
-// so no reduction over a row waits on the chain: an exchange between the threads
-// of a row takes 290 cycles, and exact scales would want three a chunk.
+//     |S+| <= E+ = e^{G_end} max |S| + max |k| sum_i |U'_i|
+// (the sum as 16 times the largest of each of the lane's four threads), so no
+// reduction over a row waits on the chain: an exchange between the threads of a
+// row takes 290 cycles, and exact scales would want three a chunk.  The one
+// exchange, of max |S| and the largest |U'|, runs beside U'^T K.  E so knows of all
+// writes but the last chunk's.  Replayed on the host with random values (16 to 128
+// keys, beta up to 2) U' is bounded to 2^9 .. 2^16 of its largest value.  After a
+// single value 10^4 times the others, while a state of 16 keys forgets it (beta 1
+// to 1.9), the last state is off by 2e-6 to 6e-6 of its largest value, fp32
+// arithmetic by 3e-6 to 4e-6; with max |S| found every fourth chunk only and 64
+// times the largest |U'| as the sum it was 7e-5 to 3e-4.  The exact maximum costs
+// 1.4 % at 4 x 2048 x 24, 64/64 and nothing at dstate 128.
 //
 // What a scan's warps share beside its buffers (behind them in dynamic shared
 // memory).
 struct ScanShared {
     uint64_t full[2], free[2], ks, r, u, w, d, s, o, read, row[4], drain, vfull[NV], vtop[NV], vfree[NV];
-    float top[2][PARTS * 128], sdown[2][128], rdown[2][128], vmax[NV][128];
+    float2 sizes[2][PARTS * 128];
+    float sdown[2][128], rdown[2][128], vmax[NV][128];
     uint32_t tmem;
     int gave_up;
 };
@@ -590,7 +602,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
     auto& mb_row = z.row;
     auto& mb_drain = z.drain;
     auto &mb_vfull = z.vfull, &mb_vtop = z.vtop, &mb_vfree = z.vfree;
-    auto& s_top = z.top;
+    auto& s_sizes = z.sizes;
     auto &s_sdown = z.sdown, &s_rdown = z.rdown;
     auto& s_vtop = z.vmax;
     auto& s_tmem = z.tmem;
@@ -656,7 +668,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                 const bool there = h0 && on && kr < N;  // (N is even)
                 s[i] = mk2(there ? h0[so + (int64_t)kr * P] : 0.f, there ? h0[so + (int64_t)(kr + 1) * P] : 0.f);
             }
-            RowTop row{s_top, &mb_row[quarter], &s_gave_up, part, vc};
+            RowShare row{s_sizes, &mb_row[quarter], &s_gave_up, part, vc};
             auto put_state = [&](int c, float bound) {
                 const RowScale sc = row_scale(bound);
                 const f2 up = mk2(sc.up, sc.up);
@@ -698,7 +710,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
             float sdown = 1.f, sbound = 0.f;
             bool ok = nck > 0 && read_v(0);
             if (ok) {
-                sbound = row.of_all(top_of_pairs(s));
+                sbound = row.of_all(top_of_pairs(s), 0.f).x;
                 sdown = put_state(0, sbound);
                 ok = warp_wait(&mb_full[0], 0, &s_gave_up);
             }
@@ -735,7 +747,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                 warp_done(&mb_r, lane);
                 // while R [T; X] runs: the exact largest value of S, the next chunk's V
                 const RowScale ws = row_scale(ff[Image::BND2] * rbound);
-                const float stop = c % EXACT == EXACT - 1 ? row.of_all(top_of_pairs(s)) : sbound;
+                const float top = top_of_pairs(s);
                 if (c + 1 < nck && !read_v(c + 1)) break;
                 factors(Image::UW, rs.down * ws.up);
                 if (!warp_wait(&mb_u, ph, &s_gave_up)) break;
@@ -748,9 +760,10 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
                 tc::tmem_wait_st();
                 warp_done(&mb_w, lane);
                 // while U' K runs: the bound on the next state (the rows of K are scaled
-                // to below 2^14, U' carries the inverse)
+                // to below 2^14, U' carries the inverse; a thread has EP of U')
                 const float all = ff[Image::ALL];
-                sbound = fmaf(all, stop, row.of_all(top_of_pairs(x)) * ws.down * (64.f * 16384.f));
+                const float2 sizes = row.of_all(top, top_of_pairs(x));
+                sbound = fmaf(all, sizes.x, sizes.y * ws.down * (EP * 16384.f));
                 if constexpr (KEEP) {
                     if (on) {
                         float* dst = writes + (((int64_t)bh * sh.nc + c0 + c) * C + EP * part) * P + vc;
@@ -997,7 +1010,8 @@ constexpr uint32_t COL_S = 0, COL_R = 128, COL_DQ = 192, COL_KS = 256, COL_Z1 = 
 
 struct BackShared {
     uint64_t full[2], free[2], ks, r, z, w, d, s, dx, dq, row[4], drain, vfull[NV], vfree[NV];
-    float top[2][PARTS * 128], dxdown[128], dqdown[128], dxtop[128], dqtop[128];
+    float2 sizes[2][PARTS * 128];
+    float dxdown[128], dqdown[128], dxtop[128], dqsum[128];
     uint32_t tmem;
     int gave_up;
 };
@@ -1032,8 +1046,8 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
     auto& mb_row = y.row;
     auto& mb_drain = y.drain;
     auto &mb_vfull = y.vfull, &mb_vfree = y.vfree;
-    auto& s_top = y.top;
-    auto &s_dxdown = y.dxdown, &s_dqdown = y.dqdown, &s_dxtop = y.dxtop, &s_dqtop = y.dqtop;
+    auto& s_sizes = y.sizes;
+    auto &s_dxdown = y.dxdown, &s_dqdown = y.dqdown, &s_dxtop = y.dxtop, &s_dqsum = y.dqsum;
     auto& s_tmem = y.tmem;
     auto& s_gave_up = y.gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1095,7 +1109,7 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
                 const bool there = dh && on && kr < N;  // (N is even)
                 s[i] = mk2(there ? dh[so + (int64_t)kr * P] : 0.f, there ? dh[so + (int64_t)(kr + 1) * P] : 0.f);
             }
-            RowTop row{s_top, &mb_row[quarter], &s_gave_up, part, vc};
+            RowShare row{s_sizes, &mb_row[quarter], &s_gave_up, part, vc};
             auto put_state = [&](int c, float bound) {
                 const RowScale sc = row_scale(bound);
                 const f2 up = mk2(sc.up, sc.up);
@@ -1124,7 +1138,7 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
             float sdown = 1.f, sbound = 0.f;
             bool ok = nck > 0;
             if (ok) {
-                sbound = row.of_all(top_of_pairs(s));
+                sbound = row.of_all(top_of_pairs(s), 0.f).x;
                 sdown = put_state(end - 1, sbound);
                 ok = warp_wait(&mb_full[0], 0, &s_gave_up);
             }
@@ -1155,7 +1169,7 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
                 tc::tmem_wait_st();
                 warp_done(&mb_r, lane);
                 // while W T runs: the exact largest value of dS
-                const float stop = j % EXACT == EXACT - 1 ? row.of_all(top_of_pairs(s)) : sbound;
+                const float top = top_of_pairs(s);
                 factors(Image::ZT, ws.down);
                 if (!warp_wait(&mb_z, ph, &s_gave_up)) break;
                 tc::fence_after_sync();
@@ -1191,10 +1205,10 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
                 // while the update runs: the bound on the next dS (the rows of K and Q
                 // are scaled to below 2^14, the operands carry the inverses)
                 const float all = ff[Image::ALL];
-                const float rtop = row.of_all(top_of_pairs(x)) * rs.down;
+                const float2 sizes = row.of_all(top, top_of_pairs(x));
                 if (!warp_wait(&mb_d, ph, &s_gave_up)) break;
                 tc::fence_after_sync();
-                sbound = fmaf(all, stop, (rtop + s_dqtop[vc]) * (64.f * 16384.f));
+                sbound = fmaf(all, sizes.x, (sizes.y * (EP * rs.down) + s_dqsum[vc]) * 16384.f);
                 {
                     const float qdown = s_dqdown[vc];
                     const f2 m = mk2(rs.down, rs.down), mq = mk2(qdown, qdown), keep = mk2(all, all);
@@ -1250,12 +1264,14 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
                 if (!warp_wait(&mb_full[j & 1], (j >> 1) & 1, &s_gave_up)) break;
                 const float* ff = reinterpret_cast<const float*>(smem + (j & 1) * M::STAGE + M::IMG + Image::F);
                 uint32_t m = 0;
-                float qt = 0.f;
+                float qt = 0.f, qsum = 0.f;
 #pragma unroll
                 for (int i = 0; i < C / 2; ++i) {
                     m = __vmaxu2(m, raw[i] & 0x7FFF7FFFu);
                     const float2 w = unpack2(raw[i], E()), f = *reinterpret_cast<const float2*>(ff + Image::DQ + 2 * i);
-                    qt = fmaxf(fmaxf(qt, fabsf(w.x * f.x)), fabsf(w.y * f.y));
+                    const float a = fabsf(w.x * f.x), b = fabsf(w.y * f.y);
+                    qt = fmaxf(fmaxf(qt, a), b);
+                    qsum += a + b;
                 }
                 const float top = top_of<E>(m);
                 const RowScale xs = row_scale(top), qs = row_scale(qt);
@@ -1265,7 +1281,7 @@ __device__ __forceinline__ void back_scan_body(const BackArgs<E>& g, int bh, con
                 s_dxdown[vc] = xs.down;
                 s_dxtop[vc] = top;
                 s_dqdown[vc] = qs.down;
-                s_dqtop[vc] = qt;
+                s_dqsum[vc] = qsum;
 #pragma unroll
                 for (int e = 0; e < C / 2; e += 8) {
                     uint32_t w[8];

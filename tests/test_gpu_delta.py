@@ -466,3 +466,88 @@ def test_more_heads_than_sms(cs, shape):
     for x, y in zip(*runs):
         assert torch.equal(x, y)
     assert cs.device_status() == 0
+
+
+def unit(x):
+    return x / np.linalg.norm(x, axis=-1, keepdims=True)
+
+
+def repeats(d):
+    """The largest sum of sizes in a row of (I + A)^-1 over the chunks: how often
+    an error of R counts in U (key heads not shared, no decay)."""
+    n = np64(d)
+    most = 1.0
+    for b in range(n["k"].shape[0]):
+        for h in range(n["k"].shape[2]):
+            for c in range(0, n["k"].shape[1], 64):
+                k, beta = n["k"][b, c:c + 64, h], n["beta"][b, c:c + 64, h]
+                t = np.linalg.inv(np.eye(len(k)) + np.tril(beta[:, None] * (k @ k.T), -1))
+                most = max(most, np.abs(t).sum(1).max())
+    return most
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("beta,alike", [((1.0, 1.9), 0.0), ((2.0, 2.0), 0.0), ((0.9, 1.0), 0.9), ((1.0, 1.9), 0.9)])
+@pytest.mark.parametrize("NP", [(64, 64), (16, 32), (128, 128)])
+def test_strong_writes(cs, NP, beta, alike, dtype):
+    """Writes that overshoot (beta above 1) and keys that are much alike, without
+    decay: the triangular system sums terms larger than its solution, so the bar
+    counts them."""
+    N, P = NP
+    d, opt, back = make(22, 1, 330, 2, 2, N, P, state=True)
+    r = np.random.default_rng(23)
+    k = unit((1 - alike) * r.standard_normal(d["k"].shape) + 3 * alike * r.standard_normal((1, 1, 2, N)))
+    d["k"] = torch.from_numpy(k).float()
+    for n in ("q", "k", "v"):
+        d[n] = d[n].to(TYPES[dtype])
+    back["do"] = back["do"].to(TYPES[dtype])
+    d["g"].zero_()
+    d["beta"] = torch.from_numpy(r.uniform(*beta, d["beta"].shape)).float()
+    inner = INNER * repeats(d)
+    o, h = cs.delta_forward(**on(d), **on(opt), scale=0.25)
+    g = cs.delta_backward(**on(d), **on(back), **on(opt), scale=0.25)
+    n, m, b = np64(d), np64(opt), np64(back)
+    args = [n[x] for x in ("q", "k", "v", "g", "beta")]
+    want_o, want_h, _ = ref.delta_forward(*args, 0.25, m["h0"])
+    w = ref.delta_backward(*args, 0.25, b["do"], m["h0"], b["dh_final"])
+    close(o, want_o, "o", inner=inner)
+    close(h, want_h, "h_final", inner=inner)
+    for name in ("gq", "gk", "gv", "gbeta", "gh0"):
+        close(g[name], w[name], name, inner=inner)
+    close(g["gg"], w["gg"], "gg", scale=w["gg_terms"], inner=inner)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("where", ["v", "do"])
+@pytest.mark.parametrize("size", [1e3, 1e4])
+@pytest.mark.parametrize("beta,known", [((0.0, 1.0), False), ((1.0, 1.9), False), ((0.9, 1.0), True)])
+@pytest.mark.parametrize("NP", [(16, 32), (64, 64), (128, 128)])
+def test_one_large_token(cs, NP, beta, known, size, where, dtype):
+    """One value, or one output's gradient, thousands of times the others, which
+    the state has forgotten by the end (few keys, no decay): the float32 results
+    against what the fp32 kernels make of the same 16-bit inputs.  An operand of
+    the 16-bit kernels is held to 2^-24 of its row's largest value while its scale
+    is at most 2^16 off, to 2^-22 at 2^18, 4 times an fp32 rounding, and a
+    product has two such operands at most: 8 times the fp32 kernels' error, and
+    the 1e-6 that every result may be off by."""
+    N, P = NP
+    T, H = 512, 2
+    r = np.random.default_rng(24)
+    k, q, v, do = unit(r.standard_normal((1, T, H, N))), unit(r.standard_normal((1, T, H, N))), \
+        r.standard_normal((1, T, H, P)), r.standard_normal((1, T, H, P))
+    if known:  # the state comes to answer every value
+        v = np.einsum("bthn,hnp->bthp", k, r.standard_normal((H, N, P)))
+    (v if where == "v" else do)[:, 266] *= size
+    q, k, v, do = (torch.from_numpy(x).float().to(TYPES[dtype]) for x in (q, k, v, do))
+    g, b = torch.zeros(1, T, H), torch.from_numpy(r.uniform(*beta, (1, T, H))).float()
+    n = [x.double().numpy() for x in (q, k, v, g, b)]
+    want = {"h": ref.delta_forward(*n, 1.0)[1], **ref.delta_backward(*n, 1.0, do.double().numpy())}
+    got, plain = [], []
+    for to, into in ((lambda x: x.cuda(), got), (lambda x: x.float().cuda(), plain)):
+        a = [to(q), to(k), to(v), g.cuda(), b.cuda()]
+        back = cs.delta_backward(*a, to(do), scale=1.0)
+        into += [cs.delta_forward(*a, scale=1.0)[1], back["gh0"], back["gbeta"]]
+    for x, y, name in zip(got, plain, ("h", "gh0", "gbeta")):
+        top = np.abs(want[name]).max()
+        err, fp32 = (np.abs(t.cpu().double().numpy() - want[name]).max() / top for t in (x, y))
+        assert err <= 8 * fp32 + 1e-6, f"{name}: {err:.2g} of its largest value, the fp32 kernels {fp32:.2g}"
