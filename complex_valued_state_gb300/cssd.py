@@ -187,7 +187,7 @@ def _empty(shape, dtype, device, stream):
 
 
 def _empty_like(t, stream):
-    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
+    return _empty(t.shape, t.dtype, t.device, stream)
 
 
 # Bits of the device status word (cssd_device_status).
@@ -583,7 +583,8 @@ def born_attention(q, k, v, *, psi=None, stream=None):
 
 # The functions below are called once a token or a layer, so what they do on
 # the host counts: one comparison chain a tensor, plain integers as pointers,
-# and the size structures kept (by their values).
+# the size structures kept (by their values), and results of calls on the
+# current stream straight from torch.
 def _expect(t, name, dtype, shape, index):
     """t is a dense tensor of this dtype and shape on CUDA device `index`; otherwise what is wrong is raised."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index \
@@ -677,13 +678,14 @@ def delta_forward(q, k, v, g, beta, *, scale=None, h0=None, lens=None, o=None, h
     if lens is not None:
         _expect(lens, "lens", torch.int32, (Bz,), index)
     if o is None:
-        o = _empty_like(v, stream)
+        o = torch.empty_like(v) if stream is None else _empty_like(v, stream)
     else:
         _expect(o, "o", q.dtype, v.shape, index)
     if h_final is not None:
         _expect(h_final, "h_final", torch.float32, state, index)
     elif want_state:
-        h_final = _empty(state, torch.float32, q.device, stream)
+        h_final = (torch.empty(state, dtype=torch.float32, device=q.device) if stream is None
+                   else _empty(state, torch.float32, q.device, stream))
     st = _stream_of(stream, index)
     d = _delta_dims(Bz, T, H, KH, N, P)
     ws, nbytes = _scratch(workspace, lib.cssd_delta_workspace_bytes(d, dt) if workspace is None else 0, q, stream)
@@ -719,7 +721,7 @@ def delta_backward(q, k, v, g, beta, do, *, scale=None, h0=None, dh_final=None, 
         if name in r:
             _expect(r[name], name, like.dtype, like.shape, index)
         else:
-            r[name] = _empty_like(like, stream)
+            r[name] = torch.empty_like(like) if stream is None else _empty_like(like, stream)
     if "gh0" in r:
         _expect(r["gh0"], "gh0", f32, state, index)
     else:
@@ -752,7 +754,7 @@ def delta_step(h, q, k, v, g, beta, *, scale=None, slots=None, o=None, stream=No
     if slots is not None:
         _expect(slots, "slots", torch.int32, (Bz,), index)
     if o is None:
-        o = _empty_like(v, stream)
+        o = torch.empty_like(v) if stream is None else _empty_like(v, stream)
     else:
         _expect(o, "o", q.dtype, v.shape, index)
     r = lib.cssd_delta_step(_delta_dims(Bz, 1, H, KH, N, P), dt, h.data_ptr(), nslots, _opt(slots), q.data_ptr(),
@@ -797,11 +799,12 @@ def layernorm(x, weight=None, bias=None, *, eps: float = 1e-5, y=None, stream=No
     lib = _lib or load()
     xt, wt, rows, D, index = _norm_inputs(x, weight, bias)
     if y is None:
-        y = _empty_like(x, stream)
+        y = torch.empty_like(x) if stream is None else _empty_like(x, stream)
     else:
         _expect(y, "y", x.dtype, x.shape, index)
-    mean = _empty(x.shape[:-1], torch.float32, x.device, stream)
-    rstd = _empty_like(mean, stream)
+    mean = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if stream is None
+            else _empty(x.shape[:-1], torch.float32, x.device, stream))
+    rstd = torch.empty_like(mean) if stream is None else _empty_like(mean, stream)
     r = lib.cssd_layernorm(rows, D, xt, wt, x.data_ptr(), _opt(weight), _opt(bias), eps, y.data_ptr(), mean.data_ptr(),
                            rstd.data_ptr(), _stream_of(stream, index))
     if r != CSSD_OK:
@@ -832,7 +835,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, *, want_weight: bool = True, w
     if "gx" in r:
         _expect(r["gx"], "gx", x.dtype, x.shape, index)
     else:
-        r["gx"] = _empty_like(x, stream)
+        r["gx"] = torch.empty_like(x) if stream is None else _empty_like(x, stream)
     for name, wanted in (("gweight", want_weight), ("gbias", want_bias)):
         if not wanted:
             continue
