@@ -173,7 +173,7 @@ struct Made {
 // One CTA per chunk and value head.  Bound by shared memory, 4 x 4 outputs a
 // thread reading 8 float4 for 64 multiply-adds (12 for 128 where two products
 // share a factor), and by having 1.3 CTAs an SM at the sizes measured: 27 us for
-// 1 x 1000 x 12, 64/64; 35 us for the gradients' 2 x 515 x 12.
+// 1 x 1000 x 12, 64/64; 33 us for the gradients' 2 x 515 x 12.
 template <bool BACK>
 __global__ void __launch_bounds__(NT) delta_prep(const float* __restrict__ q, const float* __restrict__ k,
                                                  const float* __restrict__ v, const float* __restrict__ dout,
@@ -309,7 +309,9 @@ struct ScanIo {
 };
 
 // Up to this many CTAs of 16 columns, half of the SMs, a CTA takes 8 with half
-// the threads: 1 x 1000 x 12, 64/64 (48 CTAs) in 61 us against 69.
+// the threads.  1000 tokens from a cold L2, 64/64: 48 CTAs 71 us against 79, 76 72
+// against 79, 96 108 against 106, 152 116 against 110; 128/128: 48 93 against 119,
+// 96 179 against 152.
 constexpr int NARROW = 76;
 constexpr int scan_threads(int PW) { return 16 * PW; }
 __host__ __device__ constexpr int state_stride(int rows, int N) { return (N + 31) / 32 * 32 + 4 * (256 / rows); }
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(scan_threads(PW)) delta_scan(ScanIo io, const 
 }
 
 // Both of the gradients' scans, which do not need one another (2 x 515 x 12,
-// 64/64: 36 us; one behind the other, with three products a chunk, they took 199).
+// 64/64: 37 us; one behind the other, with three products a chunk, they took 199).
 template <int ND>
 __global__ void __launch_bounds__(scan_threads(16)) delta_both_scans(ScanIo back, ScanIo fwd, const int* __restrict__ lens, Geo ge) {
     extern __shared__ __align__(16) float sm[];
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(scan_threads(16)) delta_both_scans(ScanIo back
 // when every value head has its own key head, else this value head's part in
 // fp32, summed over the group by delta_sum_heads in a fixed order.  Bound by
 // shared memory (2.3 bytes a multiply-add) at two CTAs an SM: 2 x 515 x 12, 64/64
-// 59 us; with a matrix each for Pm and W, one CTA an SM, 84.
+// 61 us; with a matrix each for Pm and W, one CTA an SM, 84.
 template <typename E, typename O>
 __global__ void __launch_bounds__(NT) delta_grad(const E* __restrict__ q, const E* __restrict__ k,
                                                  const E* __restrict__ v, const float* __restrict__ g,

@@ -20,14 +20,14 @@
 //
 // What bounds the scan: the chain of a chunk, three MMA groups with the
 // threads' work between them (the state is the only thing that waits; Q S and
-// X R run beside the chain).  A chunk takes 2.9 us at 64/64 (4 x 2048 x 24: two
-// scans of 16 chunks, 48 us each on 96 SMs) and 3.8 us at 128/64; the tensor
-// pipe is 15 % busy.
+// X R run beside the chain).  A chunk takes 2.6 us at 64/64, 3.5 at 128/64 and 3.9
+// at 128/128 (what a row of 4 heads takes more for each); the tensor pipe is 15 %
+// busy.
 //
-// Whole calls, bf16: forward 4 x 2048 x 24, 64/64 187 us (prep 92 us, half of it
-// beside the scan); 1 x 16384 x 32, 128/64 1072 us; gradients 4 x 2048 x 24,
-// 64/64 530 us (prep 112, scans 206, delta_grad_tc 209), 4 x 1501 x 16 on 8 key
-// heads, 128/128 354 us (45, 111, 178 and 20 for the sum over shared heads).
+// Whole calls, bf16: forward 4 x 2048 x 24, 64/64 189 us (prep 107 us alone, half
+// of it beside the scan); 1 x 16384 x 32, 128/64 1058 us; gradients 4 x 2048 x 24,
+// 64/64 535 us (prep 115, scans 209, delta_grad_tc 211), 4 x 1501 x 16 on 8 key
+// heads, 128/128 356 us (45, 114, 176 and 21 for the sum over shared heads).
 
 #include <type_traits>
 
@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(PT, BACK ? 3 : 4) delta_prep_tc(const E* __res
     // T and X into the image: a thread has 16 columns of one row.  One scale a
     // matrix: the scales have 2^16 to spare.
     const int row = lane + 32 * (warp & 1), part = warp >> 1;
-    // (The gradients' forward scan makes no outputs: its image has no X.)
+    // (The gradients' forward scan makes no outputs: X's part of its image is copied
+    // as it lies here and not read.)
     float te[16], xe[BACK ? 1 : 16], tops[4] = {};  // of beta T, beta X; of T, X
 #pragma unroll
     for (int u = 0; u < 16; u += 4) {
@@ -421,7 +422,9 @@ constexpr int OW = 4;          // output warps, one per lane quarter
 constexpr int ST = 32 * (CW + OW + 4);  // then two warps that load V, the MMA warp and the bulk loader
 constexpr int EP = C / PARTS;  // tokens of a row a chain thread has
 // Registers a thread of the chain, the outputs and the rest: 4 x 88 + 88 + 40
-// = 4 x 80 + 104 + 56 = 6 x 80, what the block starts with.
+// = 4 x 80 + 104 + 56 = 6 x 80, what the block starts with.  The compiler has 80 for
+// all and spills: 36 bytes of loads at dstate 64 (52 in pieces, both scans 56), 200
+// at 128 (236, 508).
 template <int ND>
 struct Regs {
     static constexpr int CHAIN = ND == 128 ? 88 : 80, OUT = ND == 128 ? 88 : 104, REST = ND == 128 ? 40 : 56;
@@ -524,7 +527,7 @@ __device__ __forceinline__ void chain(uint32_t d, uint32_t a, uint64_t bd, uint3
 // over the chunk's tokens,
 //     |R|  <= max |v| + max_i(e^{G_i} |k_i|) sqrt(N) E
 //     |U'| <= max_i(|T_i|_1 e^{G_end - G_i}) |R|
-//     |S+| <= E+ = e^{G_end} max |S| + max |k| sum_i |U'_i|
+//     |S+| <= e^{G_end} max |S| + max |k| sum_i |U'_i|, the next E
 // (the sum as 16 times the largest of each of the lane's four threads), so no
 // reduction over a row waits on the chain: an exchange between the threads of a
 // row takes 290 cycles, and exact scales would want three a chunk.  The one
@@ -565,9 +568,9 @@ struct ScanArgs {
 // run in `rounds` launches, chain i sits out rounds - pieces of them, those
 // after its own, so that a round has n pieces / rounds CTAs; the state goes from
 // piece to piece through `between`.  192 chains: 3 pieces in 4 rounds, forward
-// 8 x 2048 x 24 64/64 in 362 us against 394 in one launch; 160: 317 against 347;
-// gradients 4 x 2048 x 24 (192 chains) 544 against 554.  A round costs 10 to 18
-// us more than its chunks, so 6 x 1024 x 16 128/128 gradients lose 1.4 %.
+// 8 x 2048 x 24 64/64 in 357 us against 382 in one launch; 160: 315 against 347;
+// gradients 4 x 2048 x 24 (192 chains) 536 against 550, 6 x 1024 x 16, 128/128 567
+// against 574 (from a cold L2).  A round costs 10 to 18 us more than its chunks.
 struct Rounds {
     int n, pieces, rounds, now;
     float* between;
@@ -972,7 +975,7 @@ __device__ __forceinline__ void scan_body(const ScanArgs<E>& g, int bh, const in
 }
 
 // CUT: in pieces (else the whole chain of head blockIdx.x: what a piece needs
-// costs the scan registers, 1065 us against 1040 at 1 x 16384 x 32, 128/64).
+// costs the scan registers, 1086 us against 1065 at 1 x 16384 x 32, 128/64).
 template <typename E, int ND, bool CUT>
 __global__ void __launch_bounds__(ST, 1) delta_scan_tc(ScanArgs<E> g, const int* __restrict__ lens, Shape sh, Rounds turn,
                                                        unsigned* status) {
@@ -1426,7 +1429,7 @@ __global__ void __launch_bounds__(ST, 1) delta_both_scans_tc(BackArgs<E> back, S
 // take five MMA chains of 128 rows.  S, dS, Z and U are fp32 and are split on
 // the way into shared memory, a row a scale; dO is exact with its scale, Pm
 // and W are split with one scale a chunk (into tensor memory, over the first
-// two products).  4 x 2048 x 24, 64/64: 209 us for 406 MB read, 2 TB/s; bound by
+// two products).  4 x 2048 x 24, 64/64: 211 us for 406 MB read, 2 TB/s; bound by
 // the latency of a CTA's stages (20 us from its loads to its last store, issue 27 %
 // busy) at the two CTAs an SM that 128 registers a thread leave.  512 threads a
 // CTA took 246 us against 228 then, an L2 prefetch of the next CTAs' data 236.
@@ -2034,9 +2037,10 @@ size_t state_bytes(const DeltaArgs& a) { return sizeof(float) * a.Bz * a.H * a.N
 // prep beside the scan: the scan has one CTA per head, so with fewer heads than
 // SMs the prep (a CTA per chunk and head) takes the others.  One part costs two
 // more launches and the state's way through memory (about 8 us), so a part has
-// at least 16 chunks (60 to 100 us of scan).  In parts against whole, 2048
-// tokens, 64/64: 24 heads 120 against 128 us, 48 134 and 150, 96 194 and 196,
-// 120 222 and 220, 144 259 and 253; 16384 tokens of 32 heads, 128/64: 1043 and 1265.
+// at least 16 chunks (40 to 60 us of scan).  In parts against whole, from a cold L2,
+// 2048 tokens, 64/64: 24 heads 121 against 128 us, 48 134 and 151, 96 196 and 198
+// (128/128: 272 and 280), 120 226 and 222 (318 and 316), 144 262 and 255; 16384
+// tokens of 32 heads, 128/64: 1065 and 1281.
 int parts_of(const DeltaArgs& a) {
     const int64_t nc = (a.T + C - 1) / C;
     if (a.Bz * a.H > 100) return 1;

@@ -13,8 +13,10 @@
 //
 // Measured, bf16: 8192 x 1536 forward 10.3 us (4.9 TB/s of tensors that L2
 // partly holds), gradients 22 us (3.4 TB/s: the CTAs' 304 partial sums and the
-// kernel that joins them take 4 us of it); gradients of 65536 x 2048 168 us
-// (4.8 TB/s).
+// kernel that joins them take 4 us of it); gradients of 65536 x 2048 165 us
+// (4.9 TB/s).  From a cold L2 8192 x 1536 takes 20 and 30 us, and the streaming
+// kernels, which read 2 bytes a lane and in the gradients everything twice, 30 and
+// 50 us for 8192 x 1001.
 
 #include <type_traits>
 
@@ -345,10 +347,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
     if (tid == 0 && s_gave_up && status) atomicOr(status, kStatusNorm);
 }
 
-// Rows of more than 768 vectors, whose ring would leave one CTA an SM: a CTA's
-// threads own the row's vectors (IT each) and walk R rows
-// at a time, so that 2 R IT loads a thread are in flight before a barrier; the
-// sums of dw and db stay in registers until the end.
+// Rows of more than 768 vectors, three a thread of the ring's 256.  (The ring of
+// 16-bit rows leaves one CTA an SM above about 5770 columns already: 8192 rows of
+// 5760 take 69 us from a cold L2, of 6144 99.)  A CTA's threads own the row's
+// vectors (IT each) and walk R rows at a time, so that 2 R IT loads a thread are
+// in flight before a barrier; the sums of dw and db stay in registers until the
+// end.  8192 x 8192 bf16 takes 143 us from a cold L2 (1024 threads, 64 registers: the
+// 16-bit forms spill 156 to 308 bytes a thread).
 template <typename E, typename WT, int IT, int R, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_back_rows(const E* dy, const E* x,
                                                        const WT* __restrict__ w, const float* __restrict__ mean,

@@ -390,7 +390,8 @@ int cssd_born_attention(const cssd_dims* dims, const void* q, const void* k, con
  * beta, the states and the gradients of those are float32 always.  Sums,
  * states and every intermediate are kept to fp32 accuracy whatever the type:
  * outputs differ from the recurrence by the rounding of their own type plus
- * about 1e-6 of their largest value.
+ * about 1e-6 of their largest value; 1e-5 where keys are much alike and beta
+ * near 2, or after a value 1e4 times the others that a small state forgets.
  *
  * Supported sizes: dstate and headdim multiples of 16 from 16 to 128 (else
  * CSSD_ERR_UNSUPPORTED); any batch, seqlen >= 1; nheads a multiple of kheads
@@ -414,8 +415,10 @@ typedef struct {
 } cssd_delta_dims;
 
 /* Bytes of device workspace of cssd_delta_forward and cssd_delta_backward (0
- * for invalid sizes).  The backward keeps two states (8 N P bytes) per head
- * and 64 tokens. */
+ * for invalid sizes).  The backward keeps, per value head and 64 tokens, two
+ * states (8 N P bytes) and two matrices of the tokens (512 P), and for the
+ * 16-bit types 69632 bytes, with 32768 (dstate above 64: 65536) per key head: 0.5
+ * GB for 4 x 2048 tokens of 24 heads, 64/64. */
 size_t cssd_delta_workspace_bytes(const cssd_delta_dims* dims, int dtype);
 size_t cssd_delta_backward_workspace_bytes(const cssd_delta_dims* dims, int dtype);
 
