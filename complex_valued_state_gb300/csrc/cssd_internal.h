@@ -248,4 +248,103 @@ size_t layernorm_backward_workspace_bytes(int64_t rows, int64_t width);
 cudaError_t launch_layernorm(const NormArgs& a, cudaStream_t stream);
 cudaError_t launch_layernorm_backward(const NormArgs& a, void* workspace, cudaStream_t stream);
 
+// Linear attention with a decay for each head (linattn_*.cu).
+struct LinattnArgs {
+    int64_t Bz, T, H, KH, N, P;
+    int dtype;
+    float scale;
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;
+    bool g_tokens;      // g is [Bz][T][H], else [H]
+    const float* h0;    // may be null (zero state)
+    const int* lens;    // may be null (every row has T tokens)
+    void* o;            // forward
+    float* h_final;     // forward; may be null
+    const void* dout;   // backward from here on
+    const float* dh_final;  // may be null (zero)
+    void* gq;
+    void* gk;
+    void* gv;
+    float* gg;          // may be null
+    float* gh0;         // may be null
+};
+size_t linattn_workspace_bytes(const LinattnArgs& a);
+size_t linattn_backward_workspace_bytes(const LinattnArgs& a);
+cudaError_t launch_linattn_forward(const LinattnArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_linattn_backward(const LinattnArgs& a, void* workspace, cudaStream_t stream);
+namespace linattn {  // by element type, one source file each (linattn_kernels.cuh)
+cudaError_t forward_bf16(const LinattnArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t forward_f16(const LinattnArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t forward_f32(const LinattnArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t backward_bf16(const LinattnArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t backward_f16(const LinattnArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t backward_f32(const LinattnArgs& a, void* workspace, cudaStream_t stream);
+}  // namespace linattn
+
+struct LinattnStepArgs {
+    int64_t Bz, H, KH, N, P, nslots;
+    int dtype;
+    float scale;
+    float* h;
+    const int* slots;  // may be null (row b uses state b)
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;
+    bool g_tokens;     // g is [Bz][H], else [H]
+    void* o;
+};
+cudaError_t launch_linattn_step(const LinattnStepArgs& a, cudaStream_t stream);
+
+// The norms before and after a block (blocknorm.cu).  `layer`: the mean is taken off.
+struct AddNormArgs {
+    int64_t rows, width;
+    int xtype, rtype, wtype;
+    bool layer;
+    float alpha, eps;
+    const void* x;        // backward: may be null without gscale
+    const void* residual; // forward
+    const void* scale;    // may be null (ones)
+    const void* weight;   // may be null (ones)
+    const void* bias;     // may be null (none)
+    void* s;              // written by the forward, read by the backward
+    void* y;              // forward
+    float* mean;          // written by the forward (layer; may be null there), read by the backward
+    float* rstd;
+    const void* dy;       // backward from here on
+    const void* ds;       // may be null (zero)
+    void* gx;
+    void* gresidual;
+    void* gscale;         // may be null, as gweight and gbias
+    void* gweight;
+    void* gbias;
+};
+size_t add_norm_backward_workspace_bytes(int64_t rows, int64_t width);
+cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t stream);
+cudaError_t launch_add_norm_backward(const AddNormArgs& a, void* workspace, cudaStream_t stream);
+
+struct GatedNormArgs {
+    int64_t rows, width, group;
+    int xtype, wtype;
+    bool layer, gate_first;
+    float eps;
+    const void* x;
+    const void* z;
+    const void* weight;  // may be null (ones)
+    const void* bias;    // may be null (none)
+    void* y;             // forward
+    float* mean;         // [rows][width / group], as in AddNormArgs
+    float* rstd;
+    const void* dy;      // backward from here on
+    void* gx;
+    void* gz;
+    void* gweight;       // may be null
+    void* gbias;         // may be null
+};
+size_t gated_norm_backward_workspace_bytes(int64_t rows, int64_t width, int64_t group);
+cudaError_t launch_gated_norm(const GatedNormArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_norm_backward(const GatedNormArgs& a, void* workspace, cudaStream_t stream);
+
 }  // namespace cssd

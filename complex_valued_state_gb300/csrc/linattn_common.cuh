@@ -1,0 +1,227 @@
+// Helpers of the linear-attention chunk kernels: values as bfloat16 planes, the
+// warp-level matrix products over tiles in shared memory, and the decays of one
+// chunk.
+#pragma once
+
+#include "delta_common.cuh"
+
+namespace cssd {
+namespace linattn {
+
+using delta::add;
+using delta::exp_of;
+using delta::from_f;
+using delta::row_len;
+using delta::Sum2;
+using delta::to_f;
+
+// --------------------------------------------------------------- planes
+// A value is held as a sum of bfloat16 planes, each the rounding of what the
+// planes before it left: a bfloat16 is one plane, a half (11 significant bits)
+// exactly two, a float (24 bits) exactly three.  bfloat16 has the exponents of
+// float, so no plane needs a scale.  What the kernels make on the way (decayed
+// keys, scores, states) is split the same way, and a product of two values takes
+// the plane pairs (i, j) with i + j below a number of planes.
+template <typename E>
+struct Type;
+template <>
+struct Type<__nv_bfloat16> {
+    static constexpr int NP = 1;
+};
+template <>
+struct Type<__half> {
+    static constexpr int NP = 2;
+};
+template <>
+struct Type<float> {
+    static constexpr int NP = 3;
+};
+
+__device__ __forceinline__ uint32_t pack_bf(float x, float y) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// x and y as NPL planes, two values a word.
+template <int NPL>
+__device__ __forceinline__ void split(float x, float y, uint32_t (&p)[NPL]) {
+    p[0] = pack_bf(x, y);
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) {
+        x -= lo_f(p[i - 1]);
+        y -= hi_f(p[i - 1]);
+        p[i] = pack_bf(x, y);
+    }
+}
+
+// --------------------------------------------------------------- tiles
+// Rows of W columns, 2 bytes each, with 16 bytes between: eight rows then start
+// in different banks, which is what ldmatrix wants.
+constexpr int pitch(int w) { return 2 * w + 16; }
+
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+// A lane's address in a 16 x 16 block whose first element is (r0, c0): `FLIP` puts
+// the second 8 rows into the third and fourth matrix (else into the second and
+// fourth).
+//   A [m][k]  ldsm    <false>      A stored [k][m]  ldsm_t  <true>
+//   B [n][k]  ldsm    <true>       B stored [k][n]  ldsm_t  <false>
+// (of B the registers 0, 1 are the first eight columns n, 2 and 3 the others)
+template <bool FLIP>
+__device__ __forceinline__ uint32_t lane_at(uint32_t base, int pitch_, int r0, int c0, int lane) {
+    const int r = r0 + (lane & 7) + (FLIP ? (lane >> 4) * 8 : (lane >> 3 & 1) * 8);
+    const int c = c0 + (FLIP ? (lane >> 3 & 1) * 8 : (lane >> 4) * 8);
+    return base + r * pitch_ + 2 * c;
+}
+// c += A B for 16 x 8 outputs and 16 of the sum.
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
+    const int bytes = there ? 16 : 0;  // (nothing is read where it is not; the rest is zero)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// `rows` tokens of `width` columns (a multiple of 16; rows from n on are zeros)
+// into the planes at `dst`, `plane` bytes apart, W columns a row.  bfloat16
+// comes by cp.async (the caller commits and waits), the others through registers.
+template <typename E, int W>
+__device__ __forceinline__ void load_tile(unsigned char* dst, int plane, const E* src, int64_t stride, int rows, int n,
+                                          int width, int tid, int threads) {
+    constexpr int NP = Type<E>::NP, V = 16 / sizeof(E);
+    const int per = width / V;
+    if constexpr (NP == 1) {
+        const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+        if (width == W) {  // (a power of two: no division)
+            for (int i = tid; i < rows * (W / V); i += threads) {
+                const int r = i / (W / V), c = i % (W / V);
+                cp16(base + r * pitch(W) + 16 * c, src + (r < n ? r * stride + c * V : 0), r < n);
+            }
+        } else {
+            for (int i = tid; i < rows * per; i += threads) {
+                const int r = i / per, c = i - r * per;
+                cp16(base + r * pitch(W) + 16 * c, src + (r < n ? r * stride + c * V : 0), r < n);
+            }
+        }
+    } else {
+        for (int i = tid; i < rows * per; i += threads) {
+            const int r = i / per, c = i - r * per;
+            alignas(16) E e[V];
+            *reinterpret_cast<uint4*>(e) =
+                r < n ? *reinterpret_cast<const uint4*>(src + r * stride + c * V) : make_uint4(0, 0, 0, 0);
+            uint32_t w[NP][V / 2];
+#pragma unroll
+            for (int u = 0; u < V / 2; ++u) {
+                uint32_t p[NP];
+                split<NP>(to_f(e[2 * u]), to_f(e[2 * u + 1]), p);
+#pragma unroll
+                for (int z = 0; z < NP; ++z) w[z][u] = p[z];
+            }
+#pragma unroll
+            for (int z = 0; z < NP; ++z) {
+                unsigned char* at = dst + z * plane + r * pitch(W) + c * V * 2;
+                if constexpr (V == 8)
+                    *reinterpret_cast<uint4*>(at) = make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]);
+                else
+                    *reinterpret_cast<uint2*>(at) = make_uint2(w[z][0], w[z][1]);
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------- decays
+// G_i is the running sum of the log decays of a chunk.  The decay between two
+// tokens j < i of different blocks of 16 is taken as three factors,
+//     exp(G_i - G_j) = e_i X[block of j][block of i] f_j
+// (from the block's start through i; between the blocks; from j to its block's
+// end), none of which can overflow where the product does not, for g <= 0; in a
+// block it is exp of the difference.  Sums are kept as two floats: the
+// differences have to be right to an absolute 1e-7 while the sums reach hundreds.
+template <int C>
+struct alignas(16) Decays {
+    static constexpr int NB = C / 16;
+    float hi[C], lo[C];  // G_i
+    float in[C];         // exp(G_i)
+    float out[C];        // exp(G_end - G_i)
+    float e[C], f[C];
+    float x[NB][NB];
+    float all;           // exp(G_end)
+};
+
+// One warp.  Tokens at or past n count as g = 0.  g is of the chunk's first token, `stride` elements
+// between tokens (0: one decay for all).  A log decay of -inf counts as -1000, whose exponential is
+// 0 too, so that differences stay numbers.  `FULL` fills the tables of pairs too.
+template <int C, bool FULL>
+__device__ __forceinline__ void chunk_decays(Decays<C>& d, const float* g, int64_t stride, int n, int lane) {
+    constexpr int K = C / 32;
+    Sum2 s[K];
+#pragma unroll
+    for (int e = 0; e < K; ++e) {
+        const int i = K * lane + e;
+        const float gv = i < n ? g[i * stride] : 0.f;
+        s[e] = {gv < -1000.f ? -1000.f : gv, 0.f};
+        if (e) s[e] = add(s[e - 1], s[e]);
+    }
+    Sum2 tot = s[K - 1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum2 up = {__shfl_up_sync(0xffffffffu, tot.hi, o), __shfl_up_sync(0xffffffffu, tot.lo, o)};
+        if (lane >= o) tot = add(up, tot);
+    }
+    Sum2 before = {__shfl_up_sync(0xffffffffu, tot.hi, 1), __shfl_up_sync(0xffffffffu, tot.lo, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const Sum2 end = {__shfl_sync(0xffffffffu, tot.hi, 31), __shfl_sync(0xffffffffu, tot.lo, 31)};
+#pragma unroll
+    for (int e = 0; e < K; ++e) {
+        const int i = K * lane + e;
+        const Sum2 G = add(before, s[e]);
+        d.hi[i] = G.hi;
+        d.lo[i] = G.lo;
+        d.in[i] = exp_of(G);
+        d.out[i] = exp_of(add(end, {-G.hi, -G.lo}));
+        if (i == C - 1) d.all = d.in[i];
+    }
+    if constexpr (FULL) {
+        __syncwarp();
+        auto G = [&](int i) { return i < 0 ? Sum2{0.f, 0.f} : Sum2{d.hi[i], d.lo[i]}; };
+        auto between = [&](int i, int j) {
+            const Sum2 a = G(i), b = G(j);
+            return exp_of(add(a, {-b.hi, -b.lo}));
+        };
+#pragma unroll
+        for (int e = 0; e < K; ++e) {
+            const int i = K * lane + e;
+            d.e[i] = between(i, i / 16 * 16 - 1);
+            d.f[i] = between(i / 16 * 16 + 15, i);
+        }
+        for (int i = lane; i < C / 16 * (C / 16); i += 32) {
+            const int a = i / (C / 16), b = i % (C / 16);
+            d.x[a][b] = a < b ? between(16 * b - 1, 16 * a + 15) : 0.f;
+        }
+    }
+}
+
+}  // namespace linattn
+}  // namespace cssd

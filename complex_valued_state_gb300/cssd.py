@@ -46,6 +46,10 @@ EXPORTS = ("cssd_workspace_bytes", "cssd_precise_workspace_bytes", "cssd_forward
            "cssd_delta_workspace_bytes", "cssd_delta_backward_workspace_bytes", "cssd_delta_forward",
            "cssd_delta_backward", "cssd_delta_step", "cssd_layernorm", "cssd_layernorm_backward_workspace_bytes",
            "cssd_layernorm_backward",
+           "cssd_linattn_workspace_bytes", "cssd_linattn_backward_workspace_bytes", "cssd_linattn_forward",
+           "cssd_linattn_backward", "cssd_linattn_step", "cssd_add_norm", "cssd_add_norm_backward_workspace_bytes",
+           "cssd_add_norm_backward", "cssd_gated_norm", "cssd_gated_norm_backward_workspace_bytes",
+           "cssd_gated_norm_backward",
            "cssd_profile_events", "cssd_device_status",
            "cssd_selftest_handoff_timeout", "cssd_status_string")
 
@@ -135,6 +139,27 @@ def load(path: str = LIB_PATH):
             lib.cssd_layernorm_backward_workspace_bytes.restype = sz
             lib.cssd_layernorm_backward.argtypes = [i64, i64, i32, i32] + [vp] * 9 + [sz, vp]
             lib.cssd_layernorm_backward.restype = i32
+            for n in ("cssd_linattn_workspace_bytes", "cssd_linattn_backward_workspace_bytes"):
+                getattr(lib, n).argtypes = [ddims_p, i32]
+                getattr(lib, n).restype = sz
+            lib.cssd_linattn_forward.argtypes = [ddims_p, i32] + [vp] * 4 + [i32, flt] + [vp] * 5 + [sz, vp]
+            lib.cssd_linattn_forward.restype = i32
+            lib.cssd_linattn_backward.argtypes = [ddims_p, i32] + [vp] * 4 + [i32, flt] + [vp] * 10 + [sz, vp]
+            lib.cssd_linattn_backward.restype = i32
+            lib.cssd_linattn_step.argtypes = [ddims_p, i32, vp, i64] + [vp] * 5 + [i32, flt, vp, vp]
+            lib.cssd_linattn_step.restype = i32
+            lib.cssd_add_norm.argtypes = [i64, i64] + [i32] * 4 + [vp] * 3 + [flt, vp, vp, flt] + [vp] * 5
+            lib.cssd_add_norm.restype = i32
+            lib.cssd_add_norm_backward_workspace_bytes.argtypes = [i64, i64]
+            lib.cssd_add_norm_backward_workspace_bytes.restype = sz
+            lib.cssd_add_norm_backward.argtypes = [i64, i64] + [i32] * 4 + [vp] * 5 + [flt] + [vp] * 9 + [sz, vp]
+            lib.cssd_add_norm_backward.restype = i32
+            lib.cssd_gated_norm.argtypes = [i64, i64, i64] + [i32] * 4 + [vp] * 4 + [flt] + [vp] * 4
+            lib.cssd_gated_norm.restype = i32
+            lib.cssd_gated_norm_backward_workspace_bytes.argtypes = [i64, i64, i64]
+            lib.cssd_gated_norm_backward_workspace_bytes.restype = sz
+            lib.cssd_gated_norm_backward.argtypes = [i64, i64, i64] + [i32] * 4 + [vp] * 12 + [sz, vp]
+            lib.cssd_gated_norm_backward.restype = i32
             lib.cssd_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), ctypes.c_int, vp]
             lib.cssd_device_status.restype = ctypes.c_int
             lib.cssd_profile_events.argtypes = [vp, vp]
@@ -851,4 +876,352 @@ def layernorm_backward(dy, x, weight, mean, rstd, *, want_weight: bool = True, w
                                          _opt(r.get("gbias")) if want_bias else None, _opt(ws), nbytes, st)
     if status != CSSD_OK:
         raise CssdError(status, "cssd_layernorm_backward")
+    return r
+
+
+def _linattn_inputs(q, k, v, g, lead):
+    """As _delta_inputs; g is [.., H] or, one decay a head, [H]."""
+    dt = _element_type(q, "q")
+    qs = q.shape
+    if len(qs) != lead + 2 or not isinstance(v, torch.Tensor) or v.dim() != lead + 2:
+        raise ValueError(f"q and v must have {lead + 2} axes")
+    index, dtype, ax = q.get_device(), q.dtype, qs[:lead]
+    H, P = v.shape[-2:]
+    _expect(q, "q", dtype, qs, index)
+    _expect(k, "k", dtype, qs, index)
+    _expect(v, "v", dtype, ax + (H, P), index)
+    tokens = not isinstance(g, torch.Tensor) or g.dim() != 1
+    _expect(g, "g", torch.float32, ax + (H,) if tokens else (H,), index)
+    return dt, index, ax, H, qs[-2], qs[-1], P, int(tokens)
+
+
+def linattn_workspace_bytes(batch: int, seqlen: int, nheads: int, kheads: int, dstate: int, headdim: int, dtype) -> int:
+    return int(load().cssd_linattn_workspace_bytes(_delta_dims(batch, seqlen, nheads, kheads, dstate, headdim),
+                                                   _DTYPES[dtype]))
+
+
+def linattn_backward_workspace_bytes(batch: int, seqlen: int, nheads: int, kheads: int, dstate: int, headdim: int,
+                                     dtype) -> int:
+    return int(load().cssd_linattn_backward_workspace_bytes(_delta_dims(batch, seqlen, nheads, kheads, dstate, headdim),
+                                                            _DTYPES[dtype]))
+
+
+def linattn_forward(q, k, v, g, *, scale=None, h0=None, lens=None, o=None, h_final=None, want_state: bool = True,
+                    workspace=None, stream=None):
+    """cssd_linattn_forward, linear attention with a decay for each head over a sequence; returns (o, h_final or None).
+
+    q, k [Bz,T,KH,N]; v [Bz,T,H,P], all bfloat16, float16 or float32 (H a
+    multiple of KH); g (log decay) float32 [Bz,T,H], or [H] for one decay a
+    head; h0 float32 [Bz,H,N,P], the state before the first token (zero when
+    None); lens int32 [Bz], the tokens each row has (all when None).  `scale`
+    (default 1/sqrt(N)) multiplies the output.  `workspace` is an optional
+    uint8 tensor of at least linattn_workspace_bytes(...) bytes.
+    """
+    lib = _lib or load()
+    dt, index, (Bz, T), H, KH, N, P, tokens = _linattn_inputs(q, k, v, g, 2)
+    state = (Bz, H, N, P)
+    if h0 is not None:
+        _expect(h0, "h0", torch.float32, state, index)
+    if lens is not None:
+        _expect(lens, "lens", torch.int32, (Bz,), index)
+    if o is None:
+        o = torch.empty_like(v) if stream is None else _empty_like(v, stream)
+    else:
+        _expect(o, "o", q.dtype, v.shape, index)
+    if h_final is not None:
+        _expect(h_final, "h_final", torch.float32, state, index)
+    elif want_state:
+        h_final = (torch.empty(state, dtype=torch.float32, device=q.device) if stream is None
+                   else _empty(state, torch.float32, q.device, stream))
+    st = _stream_of(stream, index)
+    d = _delta_dims(Bz, T, H, KH, N, P)
+    ws, nbytes = _scratch(workspace, lib.cssd_linattn_workspace_bytes(d, dt) if workspace is None else 0, q, stream)
+    r = lib.cssd_linattn_forward(d, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), tokens,
+                                 N ** -0.5 if scale is None else scale, _opt(h0), _opt(lens), o.data_ptr(),
+                                 _opt(h_final), _opt(ws), nbytes, st)
+    if r != CSSD_OK:
+        raise CssdError(r, "cssd_linattn_forward")
+    return o, h_final
+
+
+def linattn_backward(q, k, v, g, do, *, scale=None, h0=None, dh_final=None, lens=None, want_g: bool = True, grads=None,
+                     workspace=None, stream=None):
+    """cssd_linattn_backward; returns a dict gq, gk, gv (the inputs' type), gh0
+    and, when wanted, gg (float32, shaped like g).
+
+    Inputs as linattn_forward; `do` [Bz,T,H,P] is the gradient of o, `dh_final`
+    float32 [Bz,H,N,P] that of the last state (zero when None).  `grads` may
+    hold preallocated outputs under the same keys.
+    """
+    lib = _lib or load()
+    dt, index, (Bz, T), H, KH, N, P, tokens = _linattn_inputs(q, k, v, g, 2)
+    f32, state = torch.float32, (Bz, H, N, P)
+    _expect(do, "do", q.dtype, v.shape, index)
+    if h0 is not None:
+        _expect(h0, "h0", f32, state, index)
+    if dh_final is not None:
+        _expect(dh_final, "dh_final", f32, state, index)
+    if lens is not None:
+        _expect(lens, "lens", torch.int32, (Bz,), index)
+    r = dict(grads) if grads else {}
+    for name, like in (("gq", q), ("gk", q), ("gv", v), ("gg", g)):
+        if name in r:
+            _expect(r[name], name, like.dtype, like.shape, index)
+        elif name != "gg" or want_g:
+            r[name] = torch.empty_like(like) if stream is None else _empty_like(like, stream)
+    if "gh0" in r:
+        _expect(r["gh0"], "gh0", f32, state, index)
+    else:
+        r["gh0"] = _empty(state, f32, q.device, stream)
+    st = _stream_of(stream, index)
+    d = _delta_dims(Bz, T, H, KH, N, P)
+    ws, nbytes = _scratch(workspace, lib.cssd_linattn_backward_workspace_bytes(d, dt) if workspace is None else 0, q,
+                          stream)
+    status = lib.cssd_linattn_backward(d, dt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), tokens,
+                                       N ** -0.5 if scale is None else scale, _opt(h0), _opt(lens), do.data_ptr(),
+                                       _opt(dh_final), r["gq"].data_ptr(), r["gk"].data_ptr(), r["gv"].data_ptr(),
+                                       _opt(r.get("gg")), r["gh0"].data_ptr(), _opt(ws), nbytes, st)
+    if status != CSSD_OK:
+        raise CssdError(status, "cssd_linattn_backward")
+    return r
+
+
+def linattn_step(h, q, k, v, g, *, scale=None, slots=None, o=None, stream=None):
+    """cssd_linattn_step, one token of linear attention with a decay for each
+    head: h updated in place; returns o.
+
+    h float32 [nslots,H,N,P]; q, k [Bz,KH,N]; v [Bz,H,P]; g float32 [Bz,H] or
+    [H]; slots as in delta_step.
+    """
+    lib = _lib or load()
+    dt, index, (Bz,), H, KH, N, P, tokens = _linattn_inputs(q, k, v, g, 1)
+    if not isinstance(h, torch.Tensor) or h.dim() != 4:
+        raise ValueError("h must be a tensor [nslots, H, N, P]")
+    nslots = h.shape[0]
+    _expect(h, "h", torch.float32, (nslots, H, N, P), index)
+    if slots is not None:
+        _expect(slots, "slots", torch.int32, (Bz,), index)
+    if o is None:
+        o = torch.empty_like(v) if stream is None else _empty_like(v, stream)
+    else:
+        _expect(o, "o", q.dtype, v.shape, index)
+    r = lib.cssd_linattn_step(_delta_dims(Bz, 1, H, KH, N, P), dt, h.data_ptr(), nslots, _opt(slots), q.data_ptr(),
+                              k.data_ptr(), v.data_ptr(), g.data_ptr(), tokens, N ** -0.5 if scale is None else scale,
+                              o.data_ptr(), _stream_of(stream, index))
+    if r != CSSD_OK:
+        raise CssdError(r, "cssd_linattn_step")
+    return o
+
+
+# cssd_norm_kind
+_KINDS = {"rms": 0, "layer": 1}
+
+
+def _kind(kind):
+    if kind not in _KINDS:
+        raise ValueError(f"kind must be 'rms' or 'layer', got {kind!r}")
+    return _KINDS[kind]
+
+
+def _block_inputs(x, vectors, wdtype=None):
+    """x, and vectors over its last axis that have one type, x's or float32 (named by `wdtype` where there is none)."""
+    xt = _element_type(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one axis")
+    index, D = x.get_device(), x.shape[-1]
+    _expect(x, "x", x.dtype, x.shape, index)
+    for t, n in vectors:
+        if t is None:
+            continue
+        if wdtype is None:
+            _element_type(t, n)
+            wdtype = t.dtype
+        _expect(t, n, wdtype, (D,), index)
+    if wdtype is None:
+        wdtype = x.dtype
+    if wdtype is not x.dtype and wdtype is not torch.float32:
+        raise TypeError(f"the vectors must be {x.dtype} or float32, got {wdtype}")
+    return xt, _DTYPES[wdtype], wdtype, x.numel() // D if D else 0, D, index
+
+
+def _stream_type(t, name, x, index):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not x.dtype and t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be {x.dtype} or float32, got {t.dtype}")
+    _expect(t, name, t.dtype, x.shape, index)
+    return _DTYPES[t.dtype]
+
+
+def add_norm(x, residual, weight=None, bias=None, *, kind: str = "rms", alpha: float = 1.0, scale=None,
+             eps: float = 1e-5, s=None, y=None, stream=None):
+    """cssd_add_norm: s = residual + alpha (scale * x), y = norm(s) weight +
+    bias over the last axis; returns (y, s, mean, rstd), mean None for "rms".
+
+    x bfloat16, float16 or float32; residual of x's type or float32 (s is the
+    same; it may be residual itself); scale, weight and bias [D] of x's type or
+    float32 (all the same), any may be None.  mean and rstd are float32 over
+    x's leading axes.
+    """
+    lib = _lib or load()
+    k = _kind(kind)
+    xt, wt, _, rows, D, index = _block_inputs(x, ((weight, "weight"), (bias, "bias"), (scale, "scale")))
+    rt = _stream_type(residual, "residual", x, index)
+    if s is None:
+        s = torch.empty_like(residual) if stream is None else _empty_like(residual, stream)
+    else:
+        _expect(s, "s", residual.dtype, x.shape, index)
+    if y is None:
+        y = torch.empty_like(x) if stream is None else _empty_like(x, stream)
+    else:
+        _expect(y, "y", x.dtype, x.shape, index)
+    rstd = _stats(x.shape[:-1], x, stream)
+    mean = _stats(x.shape[:-1], x, stream) if k else None
+    r = lib.cssd_add_norm(rows, D, xt, rt, wt, k, x.data_ptr(), residual.data_ptr(), _opt(scale), alpha, _opt(weight),
+                          _opt(bias), eps, s.data_ptr(), y.data_ptr(), _opt(mean), rstd.data_ptr(),
+                          _stream_of(stream, index))
+    if r != CSSD_OK:
+        raise CssdError(r, "cssd_add_norm")
+    return y, s, mean, rstd
+
+
+def _stats(shape, x, stream):
+    return (torch.empty(shape, dtype=torch.float32, device=x.device) if stream is None
+            else _empty(shape, torch.float32, x.device, stream))
+
+
+def add_norm_backward_workspace_bytes(rows: int, width: int) -> int:
+    return int(load().cssd_add_norm_backward_workspace_bytes(rows, width))
+
+
+def add_norm_backward(dy, ds, x, s, weight, mean, rstd, *, alpha: float = 1.0, scale=None, want_weight: bool = True,
+                      want_bias: bool = True, want_scale=None, wdtype=None, grads=None, workspace=None, stream=None):
+    """cssd_add_norm_backward; returns a dict gx (dy's type), gresidual (s's
+    type) and, when wanted, gweight, gbias and gscale (by default where there
+    is a scale), of the vectors' type (`wdtype`, default dy's, without any).
+
+    s, mean and rstd are those add_norm returned (mean None: the norm was
+    "rms"); ds is the gradient that reaches s otherwise, or None.  x is used
+    for gscale alone and may be None without it.
+    """
+    lib = _lib or load()
+    xt, wt, wdtype, rows, D, index = _block_inputs(dy, ((weight, "weight"), (scale, "scale")), wdtype)
+    f32, lead = torch.float32, dy.shape[:-1]
+    rt = _stream_type(s, "s", dy, index)
+    if ds is not None:
+        _expect(ds, "ds", s.dtype, dy.shape, index)
+    if want_scale is None:
+        want_scale = scale is not None
+    if x is not None:
+        _expect(x, "x", dy.dtype, dy.shape, index)
+    elif want_scale:
+        raise ValueError("gscale needs x")
+    if mean is not None:
+        _expect(mean, "mean", f32, lead, index)
+    _expect(rstd, "rstd", f32, lead, index)
+    r = _block_grads(grads, (("gx", dy), ("gresidual", s)),
+                     (("gweight", want_weight), ("gbias", want_bias), ("gscale", want_scale)), wdtype, D, index, stream)
+    st = _stream_of(stream, index)
+    ws, nbytes = _scratch(workspace, lib.cssd_add_norm_backward_workspace_bytes(rows, D) if workspace is None else 0, dy,
+                          stream)
+    status = lib.cssd_add_norm_backward(rows, D, xt, rt, wt, 0 if mean is None else 1, dy.data_ptr(), _opt(ds), _opt(x),
+                                        s.data_ptr(), _opt(scale), alpha, _opt(weight), _opt(mean), rstd.data_ptr(),
+                                        r["gx"].data_ptr(), r["gresidual"].data_ptr(),
+                                        _opt(r.get("gscale")) if want_scale else None,
+                                        _opt(r.get("gweight")) if want_weight else None,
+                                        _opt(r.get("gbias")) if want_bias else None, _opt(ws), nbytes, st)
+    if status != CSSD_OK:
+        raise CssdError(status, "cssd_add_norm_backward")
+    return r
+
+
+def _block_grads(grads, tensors, vectors, wdtype, D, index, stream):
+    r = dict(grads) if grads else {}
+    for name, like in tensors:
+        if name in r:
+            _expect(r[name], name, like.dtype, like.shape, index)
+        else:
+            r[name] = torch.empty_like(like) if stream is None else _empty_like(like, stream)
+    for name, wanted in vectors:
+        if not wanted:
+            continue
+        if name in r:
+            _expect(r[name], name, wdtype, (D,), index)
+        else:
+            r[name] = _empty((D,), wdtype, tensors[0][1].device, stream)
+    return r
+
+
+def _group(group, D):
+    group = D if group is None else int(group)
+    if group < 1 or D % group:
+        raise ValueError(f"group must divide the last axis ({D}), got {group}")
+    return group
+
+
+def gated_norm(x, z, weight=None, bias=None, *, kind: str = "rms", group=None, gate_first: bool = False,
+               eps: float = 1e-5, y=None, stream=None):
+    """cssd_gated_norm: y = (norm(x) weight + bias) silu(z), or with
+    `gate_first` norm(x silu(z)) weight + bias; returns (y, mean, rstd), mean
+    None for "rms".
+
+    The norm is over groups of `group` columns of the last axis (all of it when
+    None).  x and z bfloat16, float16 or float32; weight and bias [D] of x's
+    type or float32 (both the same), either may be None.  mean and rstd are
+    float32 [..., D / group].
+    """
+    lib = _lib or load()
+    k = _kind(kind)
+    xt, wt, _, rows, D, index = _block_inputs(x, ((weight, "weight"), (bias, "bias")))
+    _expect(z, "z", x.dtype, x.shape, index)
+    group = _group(group, D)
+    if y is None:
+        y = torch.empty_like(x) if stream is None else _empty_like(x, stream)
+    else:
+        _expect(y, "y", x.dtype, x.shape, index)
+    stats = (*x.shape[:-1], D // group)
+    rstd = _stats(stats, x, stream)
+    mean = _stats(stats, x, stream) if k else None
+    r = lib.cssd_gated_norm(rows, D, group, xt, wt, k, int(gate_first), x.data_ptr(), z.data_ptr(), _opt(weight),
+                            _opt(bias), eps, y.data_ptr(), _opt(mean), rstd.data_ptr(), _stream_of(stream, index))
+    if r != CSSD_OK:
+        raise CssdError(r, "cssd_gated_norm")
+    return y, mean, rstd
+
+
+def gated_norm_backward_workspace_bytes(rows: int, width: int, group=None) -> int:
+    return int(load().cssd_gated_norm_backward_workspace_bytes(rows, width, width if group is None else group))
+
+
+def gated_norm_backward(dy, x, z, weight, bias, mean, rstd, *, group=None, gate_first: bool = False,
+                        want_weight: bool = True, want_bias: bool = True, wdtype=None, grads=None, workspace=None,
+                        stream=None):
+    """cssd_gated_norm_backward; returns a dict gx, gz (x's type) and, when
+    wanted, gweight and gbias, of the vectors' type (`wdtype`, default x's,
+    without any).
+
+    mean and rstd are those gated_norm returned (mean None: the norm was
+    "rms"); the other arguments as given to it.
+    """
+    lib = _lib or load()
+    xt, wt, wdtype, rows, D, index = _block_inputs(x, ((weight, "weight"), (bias, "bias")), wdtype)
+    group = _group(group, D)
+    _expect(dy, "dy", x.dtype, x.shape, index)
+    _expect(z, "z", x.dtype, x.shape, index)
+    stats = (*x.shape[:-1], D // group)
+    if mean is not None:
+        _expect(mean, "mean", torch.float32, stats, index)
+    _expect(rstd, "rstd", torch.float32, stats, index)
+    r = _block_grads(grads, (("gx", x), ("gz", z)), (("gweight", want_weight), ("gbias", want_bias)), wdtype, D, index,
+                     stream)
+    st = _stream_of(stream, index)
+    ws, nbytes = _scratch(workspace, lib.cssd_gated_norm_backward_workspace_bytes(rows, D, group) if workspace is None
+                          else 0, x, stream)
+    status = lib.cssd_gated_norm_backward(rows, D, group, xt, wt, 0 if mean is None else 1, int(gate_first),
+                                          dy.data_ptr(), x.data_ptr(), z.data_ptr(), _opt(weight), _opt(bias),
+                                          _opt(mean), rstd.data_ptr(), r["gx"].data_ptr(), r["gz"].data_ptr(),
+                                          _opt(r.get("gweight")) if want_weight else None,
+                                          _opt(r.get("gbias")) if want_bias else None, _opt(ws), nbytes, st)
+    if status != CSSD_OK:
+        raise CssdError(status, "cssd_gated_norm_backward")
     return r

@@ -485,6 +485,121 @@ int cssd_layernorm_backward(int64_t rows, int64_t width, int xtype, int wtype, c
                             const void* weight, const float* mean, const float* rstd, void* gx, void* gweight,
                             void* gbias, void* workspace, size_t workspace_bytes, cssd_stream_t stream);
 
+/* ---------------------------------------------------------------- linear attention
+ * A real state that decays and takes each token's value at its key, per batch
+ * row b and value head h, with S in R^{N x P} (N = dstate rows, P = headdim
+ * columns, laid out like the delta rule's):
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T
+ *     o_t = scale S_t^T q_t
+ * g is a log decay: one a token and head (g_tokens nonzero) or one a head
+ * (g_tokens 0: float32 [nheads]).  Sizes, types, layouts, shared key heads,
+ * alignment and the meaning of `lens` are those of the gated delta rule above;
+ * batch * nheads * (seqlen / 32, rounded up) below 2^31.
+ *
+ * Sums and states are kept to fp32 accuracy whatever the type.  What 16-bit
+ * outputs are made from is held to 16 significant bits (2^-17 relative) before
+ * the output's own rounding; states, the gradients of states and of g are
+ * float32 and differ from the recurrence by about 1e-6 of their largest value.
+ * g is at most 0 in a model, though any value whose exponentials stay in range
+ * works; -inf forgets everything before the token.  A NaN or infinity in a
+ * token's inputs may reach any output of its chunk (up to 128 tokens) and what
+ * follows; what lies at or past a row's length is never read.  No kernel waits
+ * for another thread block, and nothing depends on the order of atomics: the
+ * same call gives the same bits. */
+
+/* Bytes of device workspace of cssd_linattn_forward and cssd_linattn_backward
+ * (0 for invalid sizes): a state (4 N P bytes) per chunk and value head, two
+ * for the gradients, which with shared key heads keep 8 N bytes more per token
+ * and value head.  A chunk is 128 tokens of bfloat16, 64 of float16, 64 or (N
+ * or P above 64) 32 of float32.  25 MB forward and 51 MB backward for 4 x 2048 tokens of 24
+ * heads, 64/64, bfloat16. */
+size_t cssd_linattn_workspace_bytes(const cssd_delta_dims* dims, int dtype);
+size_t cssd_linattn_backward_workspace_bytes(const cssd_delta_dims* dims, int dtype);
+
+/* The recurrence over a whole sequence.
+ *   q, k     [batch, seqlen, kheads, dstate]   v, o  [batch, seqlen, nheads, headdim]
+ *   g        float32 [batch, seqlen, nheads] or [nheads]
+ *   h0, lens, h_final, workspace, workspace_bytes as in cssd_delta_forward.
+ * Returns a cssd_status. */
+int cssd_linattn_forward(const cssd_delta_dims* dims, int dtype, const void* q, const void* k, const void* v,
+                         const float* g, int g_tokens, float scale, const float* h0, const int32_t* lens, void* o,
+                         float* h_final, void* workspace, size_t workspace_bytes, cssd_stream_t stream);
+
+/* Gradients of a real loss through cssd_linattn_forward: given dout = dL/do and
+ * dh_final = dL/dh_final (NULL means zero), writes gq, gk, gv (the tensors'
+ * type), gg (float32 like g; NULL: not computed) and gh0 (float32; may be
+ * NULL, and may be the same buffer as dh_final).  Sums over a shared key
+ * head's value heads, and over the tokens of one decay a head, are taken in a
+ * fixed order.  Behind a row's length gradients are zero. */
+int cssd_linattn_backward(const cssd_delta_dims* dims, int dtype, const void* q, const void* k, const void* v,
+                          const float* g, int g_tokens, float scale, const float* h0, const int32_t* lens,
+                          const void* dout, const float* dh_final, void* gq, void* gk, void* gv, float* gg, float* gh0,
+                          void* workspace, size_t workspace_bytes, cssd_stream_t stream);
+
+/* One token for every batch row, the states updated in place: arguments as
+ * cssd_delta_step without beta; g float32 [batch, nheads] or (g_tokens 0)
+ * [nheads].  Equals one token of cssd_linattn_forward up to rounding. */
+int cssd_linattn_step(const cssd_delta_dims* dims, int dtype, float* h, int64_t nslots, const int32_t* slots,
+                      const void* q, const void* k, const void* v, const float* g, int g_tokens, float scale, void* o,
+                      cssd_stream_t stream);
+
+/* ---------------------------------------------------------------- norms of a block
+ * norm(h) of n elements is, by `kind`,
+ *     CSSD_RMS    h rstd,           rstd = 1 / sqrt(mean(h^2) + eps)
+ *     CSSD_LAYER  (h - mean) rstd,  rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+ * Statistics and sums are fp32.  Vectors of `width` (weight, bias, scale, and
+ * their gradients) have type wtype, which is xtype or CSSD_F32, and each may
+ * be NULL (ones; no bias; gradient not computed).  Tensors are dense, 16-byte
+ * aligned (mean and rstd 4).  rows from 1 to 2^31 - 1, width from 1 to 2^24.
+ * mean (used by CSSD_LAYER alone) and rstd are float32; in the forward calls
+ * either may be NULL. */
+typedef enum { CSSD_RMS = 0, CSSD_LAYER = 1 } cssd_norm_kind;
+
+/* Before a block: the residual stream takes the block before it in, and is
+ * normalised for the next.
+ *     s = residual + alpha (scale * x)       y = norm(s) weight + bias
+ *   x, y       xtype [rows, width]
+ *   residual, s  rtype (xtype or CSSD_F32) [rows, width]; the norm is of s as it
+ *              is stored (rounded to rtype), which is what the gradients read
+ *   mean, rstd [rows]
+ * s may be residual, and y may be x.  eps >= 0 (else CSSD_ERR_DIMS). */
+int cssd_add_norm(int64_t rows, int64_t width, int xtype, int rtype, int wtype, int kind, const void* x,
+                  const void* residual, const void* scale, float alpha, const void* weight, const void* bias, float eps,
+                  void* s, void* y, float* mean, float* rstd, cssd_stream_t stream);
+
+/* Its gradients, given dy = dL/dy and ds = what reaches s otherwise (NULL:
+ * zero): gresidual (rtype), gx (xtype), and gscale, gweight, gbias (wtype),
+ * summed over the rows in a fixed order.  x is read for gscale alone (else it
+ * may be NULL).  gx may be dy or x, and gresidual may be ds or s.  workspace:
+ * at least cssd_add_norm_backward_workspace_bytes(rows, width) bytes, 16-byte
+ * aligned, or NULL (the library allocates and frees it stream-ordered). */
+size_t cssd_add_norm_backward_workspace_bytes(int64_t rows, int64_t width);
+int cssd_add_norm_backward(int64_t rows, int64_t width, int xtype, int rtype, int wtype, int kind, const void* dy,
+                           const void* ds, const void* x, const void* s, const void* scale, float alpha,
+                           const void* weight, const float* mean, const float* rstd, void* gx, void* gresidual,
+                           void* gscale, void* gweight, void* gbias, void* workspace, size_t workspace_bytes,
+                           cssd_stream_t stream);
+
+/* After a mixer: its output normalised over groups of `group` columns (a
+ * divisor of width) and gated by z, silu(z) = z / (1 + exp(-z)),
+ *     gate_first 0   y = (norm(x) weight + bias) silu(z)
+ *     gate_first 1   y = norm(x silu(z)) weight + bias
+ *   x, z, y    xtype [rows, width]
+ *   mean, rstd [rows, width / group]
+ * y may be x or z. */
+int cssd_gated_norm(int64_t rows, int64_t width, int64_t group, int xtype, int wtype, int kind, int gate_first,
+                    const void* x, const void* z, const void* weight, const void* bias, float eps, void* y, float* mean,
+                    float* rstd, cssd_stream_t stream);
+
+/* Its gradients: gx and gz (xtype), gweight and gbias (wtype), summed over the
+ * rows in a fixed order.  gx and gz may be two of dy, x and z.  workspace as
+ * above. */
+size_t cssd_gated_norm_backward_workspace_bytes(int64_t rows, int64_t width, int64_t group);
+int cssd_gated_norm_backward(int64_t rows, int64_t width, int64_t group, int xtype, int wtype, int kind, int gate_first,
+                             const void* dy, const void* x, const void* z, const void* weight, const void* bias,
+                             const float* mean, const float* rstd, void* gx, void* gz, void* gweight, void* gbias,
+                             void* workspace, size_t workspace_bytes, cssd_stream_t stream);
+
 /* Device status word.  Every wait a kernel of this library makes on other
  * threads or on the tensor cores is bounded; a wait that gives up lets the
  * kernel finish (its results are then invalid) and ORs a bit into a status word
