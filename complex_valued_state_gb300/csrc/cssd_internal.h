@@ -298,7 +298,7 @@ struct LinattnStepArgs {
 };
 cudaError_t launch_linattn_step(const LinattnStepArgs& a, cudaStream_t stream);
 
-// The norms before and after a block (blocknorm.cu).  `layer`: the mean is taken off.
+// The norms before and after a block (addnorm_*.cu, gatednorm_*.cu).  `layer`: the mean is taken off.
 struct AddNormArgs {
     int64_t rows, width;
     int xtype, rtype, wtype;
@@ -346,5 +346,20 @@ struct GatedNormArgs {
 size_t gated_norm_backward_workspace_bytes(int64_t rows, int64_t width, int64_t group);
 cudaError_t launch_gated_norm(const GatedNormArgs& a, cudaStream_t stream);
 cudaError_t launch_gated_norm_backward(const GatedNormArgs& a, void* workspace, cudaStream_t stream);
+
+namespace blocknorm {  // by element type, one source file each
+cudaError_t add_bf16(const AddNormArgs& a, cudaStream_t stream);
+cudaError_t add_f16(const AddNormArgs& a, cudaStream_t stream);
+cudaError_t add_f32(const AddNormArgs& a, cudaStream_t stream);
+cudaError_t add_back_bf16(const AddNormArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t add_back_f16(const AddNormArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t add_back_f32(const AddNormArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t gated_bf16(const GatedNormArgs& a, cudaStream_t stream);
+cudaError_t gated_f16(const GatedNormArgs& a, cudaStream_t stream);
+cudaError_t gated_f32(const GatedNormArgs& a, cudaStream_t stream);
+cudaError_t gated_back_bf16(const GatedNormArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t gated_back_f16(const GatedNormArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t gated_back_f32(const GatedNormArgs& a, void* workspace, cudaStream_t stream);
+}  // namespace blocknorm
 
 }  // namespace cssd
