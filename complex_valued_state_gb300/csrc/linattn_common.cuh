@@ -4,6 +4,7 @@
 #pragma once
 
 #include "delta_common.cuh"
+#include "pairs.cuh"
 
 namespace cssd {
 namespace linattn {
@@ -104,33 +105,28 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// `rows` tokens of `width` columns (a multiple of 16; rows from n on are zeros)
-// into the planes at `dst`, `plane` bytes apart, W columns a row.  bfloat16
-// comes by cp.async (the caller commits and waits), the others through registers.
-template <typename E, int W>
-__device__ __forceinline__ void load_tile(unsigned char* dst, int plane, const E* src, int64_t stride, int rows, int n,
-                                          int width, int tid, int threads) {
-    constexpr int NP = Type<E>::NP, V = 16 / sizeof(E);
-    const int per = width / V;
+// ROWS tokens of `width` columns (a multiple of 16, at most W; rows from n on are zeros) into the planes at `dst`,
+// `plane` bytes apart.  bfloat16 comes by cp.async (the caller commits and waits), the others through registers.
+template <typename E, int W, int ROWS, int NT>
+__device__ __forceinline__ void load_tile(unsigned char* dst, int plane, const E* src, int64_t stride, int n, int width, int tid) {
+    constexpr int NP = Type<E>::NP, V = 16 / sizeof(E), PER = W / V, STEP = NT / PER;
+    static_assert(NT % PER == 0 && ROWS % STEP == 0, "whole rows a step");
+    const int r0 = tid / PER, c = tid % PER;
+    if (c * V >= width) return;
+    src += r0 * stride + c * V;
     if constexpr (NP == 1) {
-        const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-        if (width == W) {  // (a power of two: no division)
-            for (int i = tid; i < rows * (W / V); i += threads) {
-                const int r = i / (W / V), c = i % (W / V);
-                cp16(base + r * pitch(W) + 16 * c, src + (r < n ? r * stride + c * V : 0), r < n);
-            }
-        } else {
-            for (int i = tid; i < rows * per; i += threads) {
-                const int r = i / per, c = i - r * per;
-                cp16(base + r * pitch(W) + 16 * c, src + (r < n ? r * stride + c * V : 0), r < n);
-            }
+        uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + r0 * pitch(W) + 16 * c;
+#pragma unroll
+        for (int r = 0; r < ROWS; r += STEP, to += STEP * pitch(W)) {
+            const bool there = r0 + r < n;
+            cp16(to, src + (there ? r * stride : -r0 * stride), there);
         }
     } else {
-        for (int i = tid; i < rows * per; i += threads) {
-            const int r = i / per, c = i - r * per;
+        unsigned char* at = dst + r0 * pitch(W) + c * V * 2;
+#pragma unroll
+        for (int r = 0; r < ROWS; r += STEP, at += STEP * pitch(W)) {
             alignas(16) E e[V];
-            *reinterpret_cast<uint4*>(e) =
-                r < n ? *reinterpret_cast<const uint4*>(src + r * stride + c * V) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(e) = r0 + r < n ? *reinterpret_cast<const uint4*>(src + r * stride) : make_uint4(0, 0, 0, 0);
             uint32_t w[NP][V / 2];
 #pragma unroll
             for (int u = 0; u < V / 2; ++u) {
@@ -141,11 +137,10 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, int plane, const E
             }
 #pragma unroll
             for (int z = 0; z < NP; ++z) {
-                unsigned char* at = dst + z * plane + r * pitch(W) + c * V * 2;
                 if constexpr (V == 8)
-                    *reinterpret_cast<uint4*>(at) = make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]);
+                    *reinterpret_cast<uint4*>(at + z * plane) = make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]);
                 else
-                    *reinterpret_cast<uint2*>(at) = make_uint2(w[z][0], w[z][1]);
+                    *reinterpret_cast<uint2*>(at + z * plane) = make_uint2(w[z][0], w[z][1]);
             }
         }
     }
@@ -164,27 +159,35 @@ struct alignas(16) Decays {
     static constexpr int NB = C / 16;
     float hi[C], lo[C];  // G_i
     float in[C];         // exp(G_i)
-    float out[C];        // exp(G_end - G_i)
     float e[C], f[C];
     float x[NB][NB];
-    float all;           // exp(G_end)
+    float all, unused[3];  // exp(G_end)
+    float out[C];        // exp(G_end - G_i); (last: the outputs do without it)
 };
 
-// One warp.  Tokens at or past n count as g = 0.  g is of the chunk's first token, `stride` elements
-// between tokens (0: one decay for all).  A log decay of -inf counts as -1000, whose exponential is
-// 0 too, so that differences stay numbers.  `FULL` fills the tables of pairs too.
-template <int C, bool FULL>
-__device__ __forceinline__ void chunk_decays(Decays<C>& d, const float* g, int64_t stride, int n, int lane) {
+// The running sums of a chunk's log decays, K = C / 32 consecutive tokens a lane.
+template <int C>
+struct Sums {
+    static constexpr int K = C / 32;
+    Sum2 G[K];
+    Sum2 end;
+};
+// One warp.  Tokens at or past n count as g = 0.  g is of the chunk's first token, `stride` elements between tokens
+// (0: one decay for all).  A log decay of -inf counts as -1000, whose exponential is 0 too, so that differences
+// stay numbers.
+template <int C>
+__device__ __forceinline__ Sums<C> chunk_sums(const float* g, int64_t stride, int n, int lane) {
     constexpr int K = C / 32;
-    Sum2 s[K];
+    Sums<C> s;
+    float gv[K];
+#pragma unroll
+    for (int e = 0; e < K; ++e) gv[e] = K * lane + e < n ? g[(K * lane + e) * stride] : 0.f;
 #pragma unroll
     for (int e = 0; e < K; ++e) {
-        const int i = K * lane + e;
-        const float gv = i < n ? g[i * stride] : 0.f;
-        s[e] = {gv < -1000.f ? -1000.f : gv, 0.f};
-        if (e) s[e] = add(s[e - 1], s[e]);
+        s.G[e] = {gv[e] < -1000.f ? -1000.f : gv[e], 0.f};
+        if (e) s.G[e] = add(s.G[e - 1], s.G[e]);
     }
-    Sum2 tot = s[K - 1];
+    Sum2 tot = s.G[K - 1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const Sum2 up = {__shfl_up_sync(0xffffffffu, tot.hi, o), __shfl_up_sync(0xffffffffu, tot.lo, o)};
@@ -192,35 +195,40 @@ __device__ __forceinline__ void chunk_decays(Decays<C>& d, const float* g, int64
     }
     Sum2 before = {__shfl_up_sync(0xffffffffu, tot.hi, 1), __shfl_up_sync(0xffffffffu, tot.lo, 1)};
     if (lane == 0) before = {0.f, 0.f};
-    const Sum2 end = {__shfl_sync(0xffffffffu, tot.hi, 31), __shfl_sync(0xffffffffu, tot.lo, 31)};
+    s.end = {__shfl_sync(0xffffffffu, tot.hi, 31), __shfl_sync(0xffffffffu, tot.lo, 31)};
+#pragma unroll
+    for (int e = 0; e < K; ++e) s.G[e] = add(before, s.G[e]);
+    return s;
+}
+__device__ __forceinline__ float exp_between(Sum2 a, Sum2 b) { return exp_of(add(a, {-b.hi, -b.lo})); }
+
+// The chunk's tables from its sums, by one warp, into memory of any kind.
+template <int C>
+__device__ __forceinline__ void put_decays(Decays<C>& d, const Sums<C>& s, int lane) {
+    constexpr int K = C / 32, LPB = 16 / K, NB = C / 16;  // lanes per block of 16 tokens
+    const Sum2 tot = s.G[K - 1];
+    auto of_lane = [&](int l) {  // the sum through lane l's last token (l -1: none)
+        const Sum2 v = {__shfl_sync(0xffffffffu, tot.hi, l < 0 ? 0 : l), __shfl_sync(0xffffffffu, tot.lo, l < 0 ? 0 : l)};
+        return l < 0 ? Sum2{0.f, 0.f} : v;
+    };
+    const Sum2 first = of_lane(lane / LPB * LPB - 1), last = of_lane(lane / LPB * LPB + LPB - 1);
 #pragma unroll
     for (int e = 0; e < K; ++e) {
         const int i = K * lane + e;
-        const Sum2 G = add(before, s[e]);
-        d.hi[i] = G.hi;
-        d.lo[i] = G.lo;
-        d.in[i] = exp_of(G);
-        d.out[i] = exp_of(add(end, {-G.hi, -G.lo}));
-        if (i == C - 1) d.all = d.in[i];
+        d.hi[i] = s.G[e].hi;
+        d.lo[i] = s.G[e].lo;
+        d.in[i] = exp_of(s.G[e]);
+        d.out[i] = exp_between(s.end, s.G[e]);
+        d.e[i] = exp_between(s.G[e], first);
+        d.f[i] = exp_between(last, s.G[e]);
     }
-    if constexpr (FULL) {
-        __syncwarp();
-        auto G = [&](int i) { return i < 0 ? Sum2{0.f, 0.f} : Sum2{d.hi[i], d.lo[i]}; };
-        auto between = [&](int i, int j) {
-            const Sum2 a = G(i), b = G(j);
-            return exp_of(add(a, {-b.hi, -b.lo}));
-        };
 #pragma unroll
-        for (int e = 0; e < K; ++e) {
-            const int i = K * lane + e;
-            d.e[i] = between(i, i / 16 * 16 - 1);
-            d.f[i] = between(i / 16 * 16 + 15, i);
-        }
-        for (int i = lane; i < C / 16 * (C / 16); i += 32) {
-            const int a = i / (C / 16), b = i % (C / 16);
-            d.x[a][b] = a < b ? between(16 * b - 1, 16 * a + 15) : 0.f;
-        }
+    for (int i0 = 0; i0 < NB * NB; i0 += 32) {
+        const int i = i0 + lane, a = i / NB % NB, b = i % NB;
+        const Sum2 end = of_lane(a * LPB + LPB - 1), start = of_lane(b * LPB - 1);
+        if (i < NB * NB) (&d.x[0][0])[i] = a < b ? exp_between(start, end) : 0.f;
     }
+    if (lane == 0) d.all = exp_of(s.end);
 }
 
 }  // namespace linattn

@@ -4,26 +4,24 @@
 // M_ij = e^{G_i - G_j} (i >= j),
 //     o_i   = scale (e^{G_i} q_i S + sum_j M_ij (q_i.k_j) v_j)
 //     S+    = e^{G_end} S + sum_j e^{G_end - G_j} k_j v_j^T
-// and, dS+ being the gradient of the state that leaves the chunk,
+// and, dS+ being the gradient of the state that leaves the chunk and
+// W_ij = scale M_ij (q_i.k_j) (do_i.v_j),
 //     dq_i  = scale (e^{G_i} do_i S^T + sum_j M_ij (do_i.v_j) k_j)
 //     dk_j  = e^{G_end - G_j} v_j dS+^T + scale sum_i M_ij (do_i.v_j) q_i
 //     dv_j  = e^{G_end - G_j} k_j dS+   + scale sum_i M_ij (q_i.k_j) do_i
 //     dS    = e^{G_end} dS+ + sum_i scale e^{G_i} q_i do_i^T
-//     dg_t  = e^{G_end} <S, dS+> + sum_{all j} c_j + sum_{u >= t} (q_u.dq_u - k_u.dk_u)
-// with c_j the first term's share of k_j.dk_j.  (dg_t = <e^{g_t} S_{t-1}, dL/dS_t>; what leaves the chunk
-// is <S+, dS+>, the terms before the last sum.)
+//     dg_t  = e^{G_end} <S, dS+> + sum_{j < t} b_j + sum_{u >= t} (a_u + sum_j W_uj - sum_i W_iu)
+// with a_u, b_j the first terms' shares of q_u.dq_u and k_j.dk_j.  (dg_t = <e^{g_t} S_{t-1}, dL/dS_t>, every pair
+// and every state's term that spans t; W is made from the scores in fp32, so that dg does not see the splitting of
+// the operands.)
 //
-// Three kernels:
-//   states   walks the chunks of a row and head (or of a segment of them) and
-//            leaves the state before each chunk; for the gradients the same walk
-//            backwards over (q, do) leaves dS+ of each chunk
-//   segments where a row was cut into segments: the state before each of them
-//   out, grad one CTA a chunk and head, 16 tokens a warp: scores by blocks of 16 x 16,
-//            which pass from the accumulators of one product into the operands of
-//            the next in registers
-// The chunks do not wait for one another, so everything but the states' walk
-// is as parallel as there are chunks.
-
+// Two kernels:
+//   states   walks the chunks of a row and head and leaves the state before each chunk; for the gradients the same
+//            walk backwards over (q, do) leaves dS+ of each chunk.  A row is cut into up to 8 segments, a cluster of
+//            CTAs, which tell one another the segments' own states at the end.
+//   out, grad one CTA a chunk and head, 16 tokens a warp: scores by blocks of 16 x 16, which pass from the
+//            accumulators of one product into the operands of the next in registers
+// The chunks do not wait for one another, so everything but the states' walk is as parallel as there are chunks.
 #pragma once
 
 #include <type_traits>
@@ -37,184 +35,224 @@ namespace {
 
 struct Shape {
     int T, H, G, N, P, nc;   // G: value heads per key head; nc: chunks of T tokens
-    int seg, nseg;           // chunks a segment; segments
+    int seg, nseg;           // chunks a segment; segments (at most kMostSegments)
     int64_t g_row, g_tok;    // elements between batch rows and tokens of g (0: one decay a head)
     int BH;
     float scale;
 };
+constexpr int kMostSegments = 8;  // CTAs of a cluster
 
-// What a launch leaves for the others, in the workspace.
+// What the states' walk leaves for the others, in the workspace.
 struct Scratch {
     float* states;   // [dir][b h][chunk][N][P]: before (dir 0) or after (dir 1) each chunk, without what came before its segment
-    float* segs;     // [dir][b h][segment][N][P]: a segment's own state at its end, then the state before it
+    float* ends;     // [dir][b h][segment][N][P]: a segment's own state at its end
+    float* starts;   // [dir][b h][segment][N][P]: the state before it
     float* seg_all;  // [dir][b h][segment]: its decay
     float* dec;      // [dir][b h][chunk]: decay from the segment's start to the chunk
+    void* decays;    // [b h][chunk] Decays<C>
 };
+
+__host__ __device__ constexpr int imax(int a, int b) { return a > b ? a : b; }
+__host__ __device__ constexpr int imin(int a, int b) { return a < b ? a : b; }
 
 // --------------------------------------------------------------- products
-__host__ __device__ constexpr int imax(int a, int b) { return a > b ? a : b; }
+constexpr int NT = 256;  // threads of out and grad
 
-// The sum over one chunk for 16 rows a warp,
-//     acc = row_state (A S) + sum over blocks (A B^T, decayed) Z
-// A, B and Z are tiles [token][column] of NPL planes, S a matrix [n][p] of SP planes that is filled by
-// `fill` 64 rows at a time.  LOWER: the rows are the later tokens (o, dq), else the earlier ones (dk, dv).
-// STRANS: A's columns are n and the outputs p (o, dv), else A's columns are p and the outputs n.
-template <int NPL, int SP, int QP, int PP, int C, int KW, int OW, bool LOWER, bool STRANS>
-struct Product {
-    static constexpr int SN = STRANS ? KW : OW, SPW = STRANS ? OW : KW;  // S's widths: n, p
-    static constexpr int RB = C / 16;
-
-    template <typename Fill>
-    static __device__ __forceinline__ void state(float (&acc)[OW / 8][4], uint32_t a, uint32_t s, int block, int kw, int ow,
-                                                 int lane, Fill fill) {
-        const int n = STRANS ? kw : ow;  // the state's rows
-#pragma unroll
-        for (int sl = 0; sl < SN / 64; ++sl) {
-            if (64 * sl >= n) break;
-            __syncthreads();
-            fill(sl);
-            __syncthreads();
-            if constexpr (STRANS) {
-#pragma unroll
-                for (int kt = 0; kt < 4; ++kt) {
-                    const int k = 64 * sl + 16 * kt;
-                    if (k >= kw) break;
-                    uint32_t af[NPL][4];
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i)
-                        ldsm(af[i], lane_at<false>(a + i * C * pitch(KW), pitch(KW), 16 * block, k, lane));
-#pragma unroll
-                    for (int nt = 0; nt < OW / 16; ++nt) {
-                        if (16 * nt >= ow) break;
-#pragma unroll
-                        for (int j = SP - 1; j >= 0; --j) {
-                            uint32_t bf[4];
-                            ldsm_t(bf, lane_at<false>(s + j * 64 * pitch(SPW), pitch(SPW), 16 * kt, 16 * nt, lane));
-#pragma unroll
-                            for (int i = NPL - 1; i >= 0; --i)
-                                if (i + j < SP) {
-                                    mma(acc[2 * nt], af[i], bf[0], bf[1]);
-                                    mma(acc[2 * nt + 1], af[i], bf[2], bf[3]);
-                                }
-                        }
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int kt = 0; kt < KW / 16; ++kt) {
-                    if (16 * kt >= kw) break;
-                    uint32_t af[NPL][4];
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i)
-                        ldsm(af[i], lane_at<false>(a + i * C * pitch(KW), pitch(KW), 16 * block, 16 * kt, lane));
-#pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) {
-                        if (64 * sl + 16 * nt >= ow) break;
-#pragma unroll
-                        for (int j = SP - 1; j >= 0; --j) {
-                            uint32_t bf[4];
-                            ldsm(bf, lane_at<true>(s + j * 64 * pitch(SPW), pitch(SPW), 16 * nt, 16 * kt, lane));
-#pragma unroll
-                            for (int i = NPL - 1; i >= 0; --i)
-                                if (i + j < SP) {
-                                    mma(acc[8 * sl + 2 * nt], af[i], bf[0], bf[1]);
-                                    mma(acc[8 * sl + 2 * nt + 1], af[i], bf[2], bf[3]);
-                                }
-                        }
-                    }
-                }
-            }
-        }
-    }
-
-    // `factor`: of every score.  `last`: blocks of tokens that there are.
-    static __device__ __forceinline__ void pairs(float (&acc)[OW / 8][4], uint32_t a, uint32_t b, uint32_t z, int block, int kw,
-                                                 int ow, int last, float factor, const Decays<C>& d, int lane) {
-        const int r0 = 16 * block + lane / 4, c0 = 2 * (lane % 4);
-        uint32_t keep[NPL == 1 ? KW / 16 : 1][4];
-        if constexpr (NPL == 1)
-#pragma unroll
-            for (int kt = 0; kt < KW / 16; ++kt)
-                if (16 * kt < kw) ldsm(keep[kt], lane_at<false>(a, pitch(KW), 16 * block, 16 * kt, lane));
-        float row[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) row[e] = factor * (LOWER ? d.e[r0 + 8 * e] : d.f[r0 + 8 * e]);
-#pragma unroll 1
-        for (int o = LOWER ? 0 : block; o < (LOWER ? block + 1 : last); ++o) {
-            float sc[2][4] = {};
-#pragma unroll
-            for (int kt = 0; kt < KW / 16; ++kt) {
-                if (16 * kt >= kw) break;
-                if constexpr (NPL == 1) {
-                    uint32_t bf[4];
-                    ldsm(bf, lane_at<true>(b, pitch(KW), 16 * o, 16 * kt, lane));
-                    mma(sc[0], keep[kt], bf[0], bf[1]);
-                    mma(sc[1], keep[kt], bf[2], bf[3]);
-                } else {
-                    uint32_t af[NPL][4];
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i)
-                        ldsm(af[i], lane_at<false>(a + i * C * pitch(KW), pitch(KW), 16 * block, 16 * kt, lane));
-#pragma unroll
-                    for (int j = NPL - 1; j >= 0; --j) {
-                        uint32_t bf[4];
-                        ldsm(bf, lane_at<true>(b + j * C * pitch(KW), pitch(KW), 16 * o, 16 * kt, lane));
-#pragma unroll
-                        for (int i = NPL - 1; i >= 0; --i)
-                            if (i + j < QP) {
-                                mma(sc[0], af[i], bf[0], bf[1]);
-                                mma(sc[1], af[i], bf[2], bf[3]);
-                            }
-                    }
-                }
-            }
-            // rows r0, r0 + 8; columns 16 o + c0, + 1, + 8, + 9
-            if (o != block) {
-                const float x = LOWER ? d.x[o][block] : d.x[block][o];
-                const float x0 = row[0] * x, x1 = row[1] * x;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 c = *reinterpret_cast<const float2*>((LOWER ? d.f : d.e) + 16 * o + 8 * h + c0);
-                    sc[h][0] *= x0 * c.x, sc[h][1] *= x0 * c.y;
-                    sc[h][2] *= x1 * c.x, sc[h][3] *= x1 * c.y;
-                }
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = r0 + 8 * (e / 2), c = 16 * o + 8 * h + c0 + e % 2;
-                        const int i = LOWER ? r : c, j = LOWER ? c : r;
-                        const float m = factor * __expf((d.hi[i] - d.hi[j]) + (d.lo[i] - d.lo[j]));
-                        sc[h][e] = i >= j ? sc[h][e] * m : 0.f;
-                    }
-            }
-            uint32_t p[PP][4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint32_t w[PP];
-                split<PP>(sc[u / 2][2 * (u % 2)], sc[u / 2][2 * (u % 2) + 1], w);
-#pragma unroll
-                for (int i = 0; i < PP; ++i) p[i][u] = w[i];
-            }
-#pragma unroll
-            for (int nt = 0; nt < OW / 16; ++nt) {
-                if (16 * nt >= ow) break;
-#pragma unroll
-                for (int j = NPL - 1; j >= 0; --j) {
-                    uint32_t bf[4];
-                    ldsm_t(bf, lane_at<false>(z + j * C * pitch(OW), pitch(OW), 16 * o, 16 * nt, lane));
-#pragma unroll
-                    for (int i = PP - 1; i >= 0; --i)
-                        if (i + j < PP) {
-                            mma(acc[2 * nt], p[i], bf[0], bf[1]);
-                            mma(acc[2 * nt + 1], p[i], bf[2], bf[3]);
-                        }
-                }
-            }
-        }
+// A warp's part of a chunk: 16 rows and, with fewer than eight blocks of rows, a share of the columns.  The two
+// warps of a scheduler (w, w + 4) get blocks from both ends, so that the triangle's work is even over the four.
+template <int C>
+struct Part {
+    static constexpr int RB = C / 16, CS = 8 / RB;  // blocks of rows, shares of the columns
+    int block, share;
+    __device__ __forceinline__ explicit Part(int warp) {
+        if (RB == 8)
+            block = warp < 4 ? warp : 11 - warp, share = 0;
+        else if (RB == 4)
+            block = warp < 4 ? warp : 7 - warp, share = warp / 4;
+        else
+            block = (warp ^ warp / 4) & 1, share = warp / 2;
     }
 };
+
+// acc += A S (or A S^T) of 16 rows and columns col0.. (CW of them): one slice of 64 of the state's rows n, as SP
+// planes at `s`.  A is a tile [token][column] of NPL planes.
+//   TRANS   A's columns are n, the outputs are p:  acc[., p] += sum_n A[., n] S[n][p]
+//   else    A's columns are p, the outputs are n:  acc[., n] += sum_p A[., p] S[n][p], n of this slice
+template <int NPL, int SP, int C, int KW, int OW, int CW, bool TRANS>
+__device__ __forceinline__ void times_state(float (&acc)[CW / 8][4], uint32_t a, uint32_t s, int block, int col0, int sl, int kw,
+                                            int ow, int lane) {
+    constexpr int SPITCH = pitch(TRANS ? OW : KW);
+    constexpr int KT = TRANS ? imin(4, KW / 16) : KW / 16;
+    const int k0 = TRANS ? 64 * sl : 0;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+        if (k0 + 16 * kt >= kw) break;
+        uint32_t af[NPL][4];
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) ldsm(af[i], lane_at<false>(a + i * C * pitch(KW), pitch(KW), 16 * block, k0 + 16 * kt, lane));
+#pragma unroll
+        for (int nt = 0; nt < CW / 16; ++nt) {
+            const int col = col0 + 16 * nt;
+            if (col >= ow) break;
+            if (!TRANS && col / 64 != sl) continue;
+#pragma unroll
+            for (int j = SP - 1; j >= 0; --j) {
+                uint32_t bf[4];
+                if (TRANS)
+                    ldsm_t(bf, lane_at<false>(s + j * 64 * SPITCH, SPITCH, 16 * kt, col, lane));
+                else
+                    ldsm(bf, lane_at<true>(s + j * 64 * SPITCH, SPITCH, col % 64, 16 * kt, lane));
+#pragma unroll
+                for (int i = NPL - 1; i >= 0; --i)
+                    if (i + j < SP) {
+                        mma(acc[2 * nt], af[i], bf[0], bf[1]);
+                        mma(acc[2 * nt + 1], af[i], bf[2], bf[3]);
+                    }
+            }
+        }
+    }
+}
+
+// The operands A of the scores: kept in registers where they are one plane of at most 64 columns.
+template <int NPL, int C, int KW>
+struct Rows {
+    static constexpr bool KEEP = NPL == 1 && KW <= 64;
+    uint32_t f[KEEP ? KW / 16 : 1][4];
+    uint32_t at;
+    __device__ __forceinline__ Rows(uint32_t a, int block, int kw, int lane) : at(lane_at<false>(a, pitch(KW), 16 * block, 0, lane)) {
+        if constexpr (KEEP)
+#pragma unroll
+            for (int kt = 0; kt < KW / 16; ++kt)
+                if (16 * kt < kw) ldsm(f[kt], at + 32 * kt);
+    }
+};
+// sc = A B^T for the warp's 16 rows and the 16 tokens of block `o` of B.
+template <int NPL, int QP, int C, int KW>
+__device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW>& a, uint32_t b, int o, int kw, int lane) {
+    const uint32_t at = lane_at<true>(b, pitch(KW), 16 * o, 0, lane);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[h][e] = 0.f;
+#pragma unroll
+    for (int kt = 0; kt < KW / 16; ++kt) {
+        if (16 * kt >= kw) break;
+        if constexpr (Rows<NPL, C, KW>::KEEP) {
+            uint32_t bf[4];
+            ldsm(bf, at + 32 * kt);
+            mma(sc[0], a.f[kt], bf[0], bf[1]);
+            mma(sc[1], a.f[kt], bf[2], bf[3]);
+        } else {
+            uint32_t af[NPL][4];
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) ldsm(af[i], a.at + i * C * pitch(KW) + 32 * kt);
+#pragma unroll
+            for (int j = NPL - 1; j >= 0; --j) {
+                uint32_t bf[4];
+                ldsm(bf, at + j * C * pitch(KW) + 32 * kt);
+#pragma unroll
+                for (int i = NPL - 1; i >= 0; --i)
+                    if (i + j < QP) {
+                        mma(sc[0], af[i], bf[0], bf[1]);
+                        mma(sc[1], af[i], bf[2], bf[3]);
+                    }
+            }
+        }
+    }
+}
+// The factors scale M of a block's pairs: the warp's rows (the later tokens if LOWER, else the earlier ones) with
+// the tokens of block `o`; 0 where the pair is none.  `row`: scale times the rows' own factors.
+template <int C, bool LOWER>
+__device__ __forceinline__ void pair_factors(float (&m)[2][4], const Decays<C>& d, int block, int o, const float (&row)[2], float scale,
+                                             int lane) {
+    const int c0 = 16 * o + 2 * (lane % 4);
+    if (o != block) {
+        const float x = LOWER ? d.x[o][block] : d.x[block][o];
+        const f2 r0 = mk2(row[0] * x, row[0] * x), r1 = mk2(row[1] * x, row[1] * x);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f2 c = *reinterpret_cast<const f2*>((LOWER ? d.f : d.e) + c0 + 8 * h);
+            un2(mul2(r0, c), m[h][0], m[h][1]);
+            un2(mul2(r1, c), m[h][2], m[h][3]);
+        }
+    } else {
+        const int r0 = 16 * block + lane / 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = r0 + 8 * (e / 2), c = c0 + 8 * h + e % 2, i = LOWER ? r : c, j = LOWER ? c : r;
+                m[h][e] = i >= j ? scale * __expf((d.hi[i] - d.hi[j]) + (d.lo[i] - d.lo[j])) : 0.f;
+            }
+    }
+}
+template <int C, bool LOWER>
+__device__ __forceinline__ void row_factors(float (&row)[2], const Decays<C>& d, int block, float scale, int lane) {
+    const float* t = (LOWER ? d.e : d.f) + 16 * block + lane / 4;
+    row[0] = scale * t[0], row[1] = scale * t[8];
+}
+__device__ __forceinline__ void multiply(float (&sc)[2][4], const float (&m)[2][4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) un2(mul2(mk2(sc[h][e], sc[h][e + 1]), mk2(m[h][e], m[h][e + 1])), sc[h][e], sc[h][e + 1]);
+}
+// acc += P Z for columns col0.. of Z's 16 tokens of block `o`; the scores P, split in PP planes, are the operand as
+// they lie.
+template <int NPL, int PP, int C, int OW, int CW>
+__device__ __forceinline__ void times_tokens(float (&acc)[CW / 8][4], const float (&sc)[2][4], uint32_t z, int col0, int o, int ow, int lane) {
+    uint32_t p[PP][4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        uint32_t w[PP];
+        split<PP>(sc[u / 2][2 * (u % 2)], sc[u / 2][2 * (u % 2) + 1], w);
+#pragma unroll
+        for (int i = 0; i < PP; ++i) p[i][u] = w[i];
+    }
+    const uint32_t at = lane_at<false>(z, pitch(OW), 16 * o, col0, lane);
+#pragma unroll
+    for (int nt = 0; nt < CW / 16; ++nt) {
+        if (col0 + 16 * nt >= ow) break;
+#pragma unroll
+        for (int j = NPL - 1; j >= 0; --j) {
+            uint32_t bf[4];
+            ldsm_t(bf, at + j * C * pitch(OW) + 32 * nt);
+#pragma unroll
+            for (int i = PP - 1; i >= 0; --i)
+                if (i + j < PP) {
+                    mma(acc[2 * nt], p[i], bf[0], bf[1]);
+                    mma(acc[2 * nt + 1], p[i], bf[2], bf[3]);
+                }
+        }
+    }
+}
+// acc = sum over the blocks at or before the warp's of (A B^T, decayed) Z.
+template <int NPL, int QP, int PP, int C, int KW, int OW, int CW>
+__device__ __forceinline__ void earlier_pairs(float (&acc)[CW / 8][4], uint32_t a, uint32_t b, uint32_t z, int block, int col0, int kw, int ow,
+                                              float scale, const Decays<C>& d, int lane) {
+    const Rows<NPL, C, KW> rows(a, block, kw, lane);
+    float row[2];
+    row_factors<C, true>(row, d, block, scale, lane);
+#pragma unroll 1
+    for (int o = 0; o <= block; ++o) {
+        float sc[2][4], m[2][4];
+        scores<NPL, QP, C, KW>(sc, rows, b, o, kw, lane);
+        pair_factors<C, true>(m, d, block, o, row, scale, lane);
+        if (o == block) {  // (a score that is not wanted may be anything)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[h][e] = lane / 4 + 8 * (e / 2) >= 8 * h + 2 * (lane % 4) + e % 2 ? sc[h][e] : 0.f;
+        }
+        multiply(sc, m);
+        times_tokens<NPL, PP, C, OW, CW>(acc, sc, z, col0, o, ow, lane);
+    }
+}
+template <int N>
+__device__ __forceinline__ void scale_rows(float (&acc)[N][4], float f0, float f1) {
+#pragma unroll
+    for (auto& t : acc) t[0] *= f0, t[1] *= f0, t[2] *= f1, t[3] *= f1;
+}
 
 // The state before chunk c (dir 0) or after it (dir 1), as the states' walk left it.
 struct StateAt {
@@ -233,58 +271,67 @@ struct StateAt {
 };
 __device__ __forceinline__ StateAt state_at(const Scratch& w, const Shape& sh, int dir, int64_t bh, int c, int live, bool start) {
     const int64_t np = (int64_t)sh.N * sh.P, row = (int64_t)dir * sh.BH + bh;
-    const int walk = dir ? live - 1 - c : c, s = walk / sh.seg;
+    const int walk = dir ? live - 1 - c : c;
     StateAt r{w.states + (row * sh.nc + c) * np, nullptr, 0.f};
     if (sh.nseg == 1) {
         if (walk == 0 && !start) r.own = nullptr;
         return r;
     }
+    const int s = walk / sh.seg;
     if (walk % sh.seg == 0) r.own = nullptr;
     if (s > 0 || start) {
-        r.seg = w.segs + (row * sh.nseg + s) * np;
+        r.seg = w.starts + (row * sh.nseg + s) * np;
         r.dec = w.dec[row * sh.nc + c];
     }
     return r;
 }
 
-// 64 rows of a state from row 64 sl on, as SP planes.
+// 64 rows of a state from row 64 sl on: fetched into registers, and put as SP planes.
 template <int SP, int PD>
-__device__ __forceinline__ void fill_state(unsigned char* dst, const StateAt& st, int sl, const Shape& sh, int tid, int threads) {
-    const int per = sh.P / 4, rows = min(64, sh.N - 64 * sl);
-    for (int i = tid; i < rows * per; i += threads) {
-        const int r = i / per, c = i - r * per;
-        const float4 v = st.at((int64_t)(64 * sl + r) * sh.P + 4 * c);
-        uint32_t x[SP], y[SP];
-        split<SP>(v.x, v.y, x);
-        split<SP>(v.z, v.w, y);
+struct StateTile {
+    static constexpr int PER = PD / 4, STEP = NT / PER, K = 64 / STEP;
+    float4 v[K];
+    __device__ __forceinline__ void fetch(const StateAt& st, int sl, const Shape& sh, int tid) {
+        const int r = 64 * sl + tid / PER, c = 4 * (tid % PER);
 #pragma unroll
-        for (int z = 0; z < SP; ++z)
-            *reinterpret_cast<uint2*>(dst + z * 64 * pitch(PD) + r * pitch(PD) + 8 * c) = make_uint2(x[z], y[z]);
+        for (int k = 0; k < K; ++k)
+            v[k] = c < sh.P && r + STEP * k < sh.N ? st.at((int64_t)(r + STEP * k) * sh.P + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-}
+    __device__ __forceinline__ void put(unsigned char* dst, int tid) const {
+        unsigned char* at = dst + tid / PER * pitch(PD) + 8 * (tid % PER);
+#pragma unroll
+        for (int k = 0; k < K; ++k, at += STEP * pitch(PD)) {
+            uint32_t x[SP], y[SP];
+            split<SP>(v[k].x, v[k].y, x);
+            split<SP>(v[k].z, v[k].w, y);
+#pragma unroll
+            for (int z = 0; z < SP; ++z) *reinterpret_cast<uint2*>(at + z * 64 * pitch(PD)) = make_uint2(x[z], y[z]);
+        }
+    }
+};
 
 // --------------------------------------------------------------- states
-// A CTA has 64 columns p of a state (its columns never mix), a warp 16 rows n of
-// them in registers, and takes every token's decayed key (three planes) times
-// its value.  One more warp makes the next chunk's decays.
+// A CTA has 64 columns p of a state (its columns never mix), a warp 16 rows n of them in registers, and takes
+// every token's decayed key (three planes) times its value.  Tokens come 64 at a time, bfloat16 ones two stages
+// ahead; the decays of eight chunks are made at once, a warp each.
 template <typename E, int ND, int C>
 struct StatesSmem {
-    static constexpr int NP = Type<E>::NP;
-    static constexpr int X = NP * C * pitch(ND), Y = NP * C * pitch(64);
-    static constexpr int STAGES = NP == 1 ? 2 : 1;  // (bfloat16 comes a chunk ahead)
-    static constexpr int BYTES = STAGES * (X + Y);
-    static constexpr int WARPS = ND / 16;
+    static constexpr int NP = Type<E>::NP, HT = imin(C, 64), STAGES = NP == 1 ? 3 : 2, BATCH = 8;
+    static constexpr int X = NP * HT * pitch(ND), Y = NP * HT * pitch(64);
+    static constexpr int W = STAGES * (X + Y), BYTES = W + 4 * BATCH * (C + 4);
+    static constexpr int THREADS = 2 * ND;
 };
 
 template <typename E, int ND, int C>
-__global__ void __launch_bounds__(32 * (StatesSmem<E, ND, C>::WARPS + 1))
-    states_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ dout,
-                  const float* __restrict__ g, const int* __restrict__ lens, const float* h0, const float* dh_final,
-                  float* h_final, float* gh0, Scratch w, Shape sh) {
+__global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v,
+                                                        const E* __restrict__ dout, const float* __restrict__ g,
+                                                        const int* __restrict__ lens, const float* h0, const float* dh_final,
+                                                        float* h_final, float* gh0, Scratch w, Shape sh) {
     using M = StatesSmem<E, ND, C>;
-    constexpr int NP = M::NP, NT = 32 * (M::WARPS + 1);
+    constexpr int NP = M::NP, THREADS = M::THREADS, HT = M::HT, HALVES = C / HT, STAGES = M::STAGES, BATCH = M::BATCH;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ __align__(16) Decays<C> tab[2];
+    float* weights = reinterpret_cast<float*>(smem + M::W);  // [BATCH][C]
+    float* totals = weights + BATCH * C;                     // [BATCH]
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int slices = (sh.P + 63) / 64, bh = blockIdx.x / slices, s = blockIdx.y, dir = blockIdx.z;
     const int p0 = 64 * (blockIdx.x % slices), cols = min(64, sh.P - p0);
@@ -292,25 +339,25 @@ __global__ void __launch_bounds__(32 * (StatesSmem<E, ND, C>::WARPS + 1))
     const int len = row_len(lens, b, sh.T), live = (len + C - 1) / C;
     const int w0 = s * sh.seg, w1 = min(w0 + sh.seg, live);
     const int64_t np = (int64_t)sh.N * sh.P, row = (int64_t)dir * sh.BH + bh;
-    const bool chain = warp < M::WARPS;
     const int n0 = 16 * warp;
-    const bool mine = chain && n0 < sh.N, first = tid == 0 && p0 == 0;
+    const bool mine = n0 < sh.N, first = tid == 0 && p0 == 0;
     const E* xs = (dir ? q : k) + (int64_t)(h / sh.G) * sh.N;
     const E* ys = (dir ? dout : v) + (int64_t)h * sh.P + p0;
     const int64_t xst = (int64_t)KH * sh.N, yst = (int64_t)sh.H * sh.P;
     const float* gs = g + b * sh.g_row + h;
     auto chunk_of = [&](int i) { return dir ? live - 1 - i : i; };
-    auto fetch = [&](int i) {
-        const int c = chunk_of(i), n = min(len - c * C, C);
-        const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C;
-        unsigned char* at = smem + (M::STAGES == 2 ? (i & 1) * (M::X + M::Y) : 0);
-        load_tile<E, ND>(at, C * pitch(ND), xs + t0 * xst, xst, C, n, sh.N, tid, NT);
-        load_tile<E, 64>(at + M::X, C * pitch(64), ys + t0 * yst, yst, C, n, cols, tid, NT);
+    auto fetch = [&](int t) {  // the t-th stage of this segment
+        const int i = w0 + t / HALVES, at0 = chunk_of(i) * C + t % HALVES * HT;
+        if (i < w1) {
+            const int64_t t0 = (int64_t)b * sh.T + min(at0, len - 1);  // (a half without tokens reads nothing)
+            unsigned char* at = smem + t % STAGES * (M::X + M::Y);
+            load_tile<E, ND, HT, THREADS>(at, HT * pitch(ND), xs + t0 * xst, xst, len - at0, sh.N, tid);
+            load_tile<E, 64, HT, THREADS>(at + M::X, HT * pitch(64), ys + t0 * yst, yst, len - at0, cols, tid);
+        }
+        if (NP == 1) cp_commit();
     };
-    auto decays = [&](int i) {
-        const int c = chunk_of(i);
-        chunk_decays<C, false>(tab[i & 1], gs + (int64_t)c * C * sh.g_tok, sh.g_tok, min(len - c * C, C), lane);
-    };
+#pragma unroll
+    for (int t = 0; t < STAGES - 1; ++t) fetch(t);
     float st[8][4];
     const float* start = dir ? dh_final : h0;
     auto each = [&](auto f) {  // pairs of the warp's part of the state
@@ -331,54 +378,54 @@ __global__ void __launch_bounds__(32 * (StatesSmem<E, ND, C>::WARPS + 1))
             const float2 a = *reinterpret_cast<const float2*>(start + bh * np + i);
             x = a.x, y = a.y;
         });
-    if (w0 < w1) {
-        if constexpr (M::STAGES == 2) {
-            fetch(w0);
-            cp_commit();
-        }
-        if (!chain) decays(w0);
-    }
     float all = 1.f;  // decay since the segment's start
-    for (int i = w0; i < w1; ++i) {
-        if constexpr (M::STAGES == 2) {
-            if (i + 1 < w1) fetch(i + 1);
-            cp_commit();
-            cp_wait<1>();
-        } else {
-            fetch(i);
+    for (int i = w0, t = 0; i < w1; ++i) {
+        if ((i - w0) % BATCH == 0) {
+            if (i > w0) __syncthreads();  // (the weights of the batch before are read)
+            for (int j = warp; j < min(BATCH, w1 - i); j += THREADS / 32) {
+                const int c = chunk_of(i + j);
+                const Sums<C> G = chunk_sums<C>(gs + (int64_t)c * C * sh.g_tok, sh.g_tok, len - c * C, lane);
+#pragma unroll
+                for (int e = 0; e < Sums<C>::K; ++e)
+                    weights[j * C + Sums<C>::K * lane + e] = dir ? sh.scale * exp_of(G.G[e]) : exp_between(G.end, G.G[e]);
+                if (lane == 0) totals[j] = exp_of(G.end);
+                if (dir == 0 && p0 == 0) put_decays(static_cast<Decays<C>*>(w.decays)[(int64_t)bh * sh.nc + c], G, lane);
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        const Decays<C>& d = tab[i & 1];
         const int c = chunk_of(i);
+        const float* wt = weights + (i - w0) % BATCH * C;
+        const float total = totals[(i - w0) % BATCH];
         const bool empty = sh.nseg == 1 ? i == 0 && !start : i == w0;  // (not read by anyone)
         if (mine && !empty) {
             float* to = w.states + (row * sh.nc + c) * np;
             each([&](int64_t at, float x, float y) { *reinterpret_cast<float2*>(to + at) = make_float2(x, y); });
         }
         if (sh.nseg > 1 && first) w.dec[row * sh.nc + c] = all;
-        if (!chain && i + 1 < w1) decays(i + 1);
-        if (mine) {
-            const uint32_t x = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + (M::STAGES == 2 ? (i & 1) * (M::X + M::Y) : 0);
-            const uint32_t y = x + M::X;
-            // the leading plane's products apart from the others': small terms are
-            // not lost under large ones inside the matrix instruction
-            float big[8][4] = {}, rest[8][4] = {};
-            const float* wt = dir ? d.in : d.out;
-            const float f = dir ? sh.scale : 1.f;
-#pragma unroll 2
-            for (int kt = 0; kt < C / 16; ++kt) {
+        // the leading plane's products apart from the others': small terms are not lost
+        // under large ones inside the matrix instruction
+        float big[8][4] = {}, rest[8][4] = {};
+#pragma unroll 1
+        for (int half = 0; half < HALVES; ++half, ++t) {
+            if (NP == 1) cp_wait<STAGES - 2>();
+            __syncthreads();
+            fetch(t + STAGES - 1);
+            if (!mine) continue;
+            const uint32_t x = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + t % STAGES * (M::X + M::Y), y = x + M::X;
+#pragma unroll
+            for (int kt = 0; kt < HT / 16; ++kt) {
                 uint32_t raw[NP][4], a[3][4];
 #pragma unroll
-                for (int z = 0; z < NP; ++z) ldsm_t(raw[z], lane_at<true>(x + z * C * pitch(ND), pitch(ND), 16 * kt, n0, lane));
-                const float2 u0 = *reinterpret_cast<const float2*>(wt + 16 * kt + 2 * (lane % 4));
-                const float2 u1 = *reinterpret_cast<const float2*>(wt + 16 * kt + 8 + 2 * (lane % 4));
+                for (int z = 0; z < NP; ++z) ldsm_t(raw[z], lane_at<true>(x + z * HT * pitch(ND), pitch(ND), 16 * kt, n0, lane));
+                const float2 u0 = *reinterpret_cast<const float2*>(wt + half * HT + 16 * kt + 2 * (lane % 4));
+                const float2 u1 = *reinterpret_cast<const float2*>(wt + half * HT + 16 * kt + 8 + 2 * (lane % 4));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     float e0 = 0.f, e1 = 0.f;
 #pragma unroll
                     for (int z = NP - 1; z >= 0; --z) e0 += lo_f(raw[z][r]), e1 += hi_f(raw[z][r]);
                     uint32_t pl[3];
-                    split<3>(e0 * (f * (r < 2 ? u0.x : u1.x)), e1 * (f * (r < 2 ? u0.y : u1.y)), pl);
+                    split<3>(e0 * (r < 2 ? u0.x : u1.x), e1 * (r < 2 ? u0.y : u1.y), pl);
                     a[0][r] = pl[0], a[1][r] = pl[1], a[2][r] = pl[2];
                 }
 #pragma unroll
@@ -387,7 +434,7 @@ __global__ void __launch_bounds__(32 * (StatesSmem<E, ND, C>::WARPS + 1))
 #pragma unroll
                     for (int j = NP - 1; j >= 0; --j) {
                         uint32_t bf[4];
-                        ldsm_t(bf, lane_at<false>(y + j * C * pitch(64), pitch(64), 16 * kt, 16 * nt, lane));
+                        ldsm_t(bf, lane_at<false>(y + j * HT * pitch(64), pitch(64), 16 * kt, 16 * nt, lane));
 #pragma unroll
                         for (int z = 2; z >= 0; --z)
                             if (z + j < 3) {
@@ -402,197 +449,222 @@ __global__ void __launch_bounds__(32 * (StatesSmem<E, ND, C>::WARPS + 1))
                     }
                 }
             }
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) st[nt][e] = fmaf(d.all, st[nt][e], big[nt][e] + rest[nt][e]);
         }
-        all *= d.all;
-        __syncthreads();
-    }
-    float* to = sh.nseg > 1 ? w.segs + (row * sh.nseg + s) * np : (dir ? gh0 : h_final);
-    if (sh.nseg == 1 && to) to += bh * np;
-    if (mine && to && (sh.nseg == 1 || w0 < w1))
-        each([&](int64_t at, float x, float y) { *reinterpret_cast<float2*>(to + at) = make_float2(x, y); });
-    if (sh.nseg > 1 && first) w.seg_all[row * sh.nseg + s] = all;
-}
-
-// In place of each segment's own state, the state before it; the last goes out.
-template <int C>
-__global__ void __launch_bounds__(128) segments_kernel(const int* __restrict__ lens, const float* h0, const float* dh_final,
-                                                       float* h_final, float* gh0, Scratch w, Shape sh) {
-    const int64_t np = (int64_t)sh.N * sh.P;
-    const int bh = blockIdx.y, dir = blockIdx.z;
-    const int64_t row = (int64_t)dir * sh.BH + bh, i = ((int64_t)blockIdx.x * 128 + threadIdx.x) * 4;
-    if (i >= np) return;
-    const int live = (row_len(lens, bh / sh.H, sh.T) + C - 1) / C, n = (live + sh.seg - 1) / sh.seg;
-    const float* start = dir ? dh_final : h0;
-    float4 r = start ? *reinterpret_cast<const float4*>(start + bh * np + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    float4* at = reinterpret_cast<float4*>(w.segs + row * sh.nseg * np + i);
-    const float* all = w.seg_all + row * sh.nseg;
-#pragma unroll 4
-    for (int s = 0; s < n; ++s, at += np / 4) {
-        const float4 own = *at;
-        *at = r;
-        const float d = all[s];
-        r.x = fmaf(d, r.x, own.x), r.y = fmaf(d, r.y, own.y), r.z = fmaf(d, r.z, own.z), r.w = fmaf(d, r.w, own.w);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st[nt][e] = fmaf(total, st[nt][e], big[nt][e] + rest[nt][e]);
+        all *= total;
     }
     float* last = dir ? gh0 : h_final;
-    if (last) *reinterpret_cast<float4*>(last + bh * np + i) = r;
+    if (sh.nseg == 1) {
+        if (mine && last)
+            each([&](int64_t at, float x, float y) { *reinterpret_cast<float2*>(last + bh * np + at) = make_float2(x, y); });
+        return;
+    }
+    // the segments' own states at their ends, from which each makes the state before it
+    float* ends = w.ends + row * sh.nseg * np;
+    if (mine) each([&](int64_t at, float x, float y) { *reinterpret_cast<float2*>(ends + s * np + at) = make_float2(x, y); });
+    if (tid == 0) w.seg_all[(row * slices + p0 / 64) * sh.nseg + s] = all;
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (!mine) return;
+    const float* alls = w.seg_all + (row * slices + p0 / 64) * sh.nseg;
+    const bool ends_row = s == max((live + sh.seg - 1) / sh.seg - 1, 0);  // the row's last segment
+    float decay[kMostSegments];  // from the end of segment e to this one's start
+    float d = 1.f;
+#pragma unroll
+    for (int e = kMostSegments - 1; e >= 0; --e) {
+        decay[e] = e < s ? d : 0.f;
+        if (e < s) d *= __ldcg(alls + e);
+    }
+    each([&](int64_t at, float& x, float& y) {
+        float2 r = make_float2(0.f, 0.f);
+        if (start) {
+            const float2 a = *reinterpret_cast<const float2*>(start + bh * np + at);
+            r.x = d * a.x, r.y = d * a.y;
+        }
+#pragma unroll
+        for (int e = 0; e < kMostSegments; ++e)
+            if (e < s) {
+                const float2 a = __ldcg(reinterpret_cast<const float2*>(ends + e * np + at));
+                r.x = fmaf(decay[e], a.x, r.x), r.y = fmaf(decay[e], a.y, r.y);
+            }
+        if (s > 0 || start) *reinterpret_cast<float2*>(w.starts + (row * sh.nseg + s) * np + at) = r;
+        if (ends_row && last) *reinterpret_cast<float2*>(last + bh * np + at) = make_float2(fmaf(all, r.x, x), fmaf(all, r.y, y));
+    });
 }
 
 // --------------------------------------------------------------- outputs
-// A warp's 16 rows of `acc`, times `factor`, to tokens row0.. of a tensor with `stride` elements between
-// tokens: n rows have values, those from n to `rows` are zeros.  16-bit types go
-// through `stage` (16 rows of the warp's own) for whole 16-byte stores.
-template <typename E, int OW>
-__device__ __forceinline__ void put_rows(E* out, int64_t stride, const float (&acc)[OW / 8][4], float factor, unsigned char* stage,
+// A warp's 16 rows and CW columns (from col0) of `acc`, times `factor`, to tokens of a tensor with `stride` elements
+// between them: n rows have values, those from n to `rows` are zeros.  16-bit types go through `stage` (the
+// warp's 16 rows, OW columns) for whole 16-byte stores.
+template <typename E, int OW, int CW>
+__device__ __forceinline__ void put_rows(E* out, int64_t stride, const float (&acc)[CW / 8][4], float factor, unsigned char* stage, int col0,
                                          int ow, int n, int rows, int lane) {
     if constexpr (sizeof(E) == 2) {
+        unsigned char* at = stage + lane / 4 * pitch(OW) + 2 * col0 + 4 * (lane % 4);
+        __syncwarp();  // (what was staged here before is read)
 #pragma unroll
-        for (int nt = 0; nt < OW / 8; ++nt)
+        for (int nt = 0; nt < CW / 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 alignas(4) E w[2] = {from_f<E>(factor * acc[nt][2 * e]), from_f<E>(factor * acc[nt][2 * e + 1])};
-                *reinterpret_cast<uint32_t*>(stage + (lane / 4 + 8 * e) * pitch(OW) + 16 * nt + 4 * (lane % 4)) =
-                    *reinterpret_cast<uint32_t*>(w);
+                *reinterpret_cast<uint32_t*>(at + 8 * e * pitch(OW) + 16 * nt) = *reinterpret_cast<uint32_t*>(w);
             }
         __syncwarp();
-        const int per = ow / 8;
-        for (int i = lane; i < 16 * per; i += 32) {
-            const int r = i / per, c = i - r * per;
-            if (r < rows)
-                __stcs(reinterpret_cast<uint4*>(out + r * stride + 8 * c),
-                       r < n ? *reinterpret_cast<const uint4*>(stage + r * pitch(OW) + 16 * c) : make_uint4(0, 0, 0, 0));
+        constexpr int PER = CW / 8, STEP = 32 / PER;
+        const int c = col0 + lane % PER * 8;
+#pragma unroll
+        for (int r0 = 0; r0 < 16; r0 += STEP) {
+            const int r = r0 + lane / PER;
+            if (r < rows && c < ow)
+                __stcs(reinterpret_cast<uint4*>(out + r * stride + c),
+                       r < n ? *reinterpret_cast<const uint4*>(stage + r * pitch(OW) + 2 * c) : make_uint4(0, 0, 0, 0));
         }
-        __syncwarp();
     } else {
 #pragma unroll
-        for (int nt = 0; nt < OW / 8; ++nt) {
-            if (8 * nt >= ow) break;
+        for (int nt = 0; nt < CW / 8; ++nt) {
+            if (col0 + 8 * nt >= ow) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = lane / 4 + 8 * e;
                 if (r < rows)
-                    *reinterpret_cast<float2*>(out + r * stride + 8 * nt + 2 * (lane % 4)) =
+                    *reinterpret_cast<float2*>(out + r * stride + col0 + 8 * nt + 2 * (lane % 4)) =
                         r < n ? make_float2(factor * acc[nt][2 * e], factor * acc[nt][2 * e + 1]) : make_float2(0.f, 0.f);
             }
         }
     }
 }
-
-// The rows of a warp: blocks from both ends meet in one scheduler (warps w, w + 4), so that the
-// triangle's work is even over the four.
-template <int RB>
-__device__ __forceinline__ int block_of(int warp) {
-    return RB == 8 ? (warp < 4 ? warp : 11 - warp) : warp;
+// Zeros over `rows` tokens of a chunk that has none.
+template <typename E>
+__device__ __forceinline__ void clear_rows(E* at, int64_t stride, int width, int rows, int tid) {
+    const int per = width * (int)sizeof(E) / 16;
+    for (int i = tid; i < rows * per; i += NT) reinterpret_cast<uint4*>(at + (i / per) * stride)[i % per] = make_uint4(0, 0, 0, 0);
+}
+// The first `bytes` of a chunk's tables, by cp.async.
+__device__ __forceinline__ void load_decays(unsigned char* dst, const void* src, int bytes, int tid) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    for (int i = tid; i < bytes / 16; i += NT) cp16(to + 16 * i, static_cast<const unsigned char*>(src) + 16 * i, true);
 }
 
 template <typename E, int ND, int PD, int C>
 struct OutSmem {
     static constexpr int NP = Type<E>::NP, SP = NP == 3 ? 3 : 2;
     static constexpr int Q = 0, K = Q + NP * C * pitch(ND), V = K + NP * C * pitch(ND), S = V + NP * C * pitch(PD);
-    static constexpr int BYTES = S + imax(SP * 64 * pitch(PD), sizeof(E) == 2 ? C * pitch(PD) : 0);
+    static constexpr int D = S + imax(SP * 64 * pitch(PD), sizeof(E) == 2 ? C * pitch(PD) : 0);
+    static constexpr int TABLE = sizeof(Decays<C>) - 4 * C, BYTES = D + TABLE;
+    static constexpr int CTAS = BYTES + 1024 <= 228 * 1024 / 3 ? 3 : BYTES + 1024 <= 114 * 1024 ? 2 : 1;
 };
 
 template <typename E, int ND, int PD, int C>
-__global__ void __launch_bounds__(2 * C) out_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v,
-                                                    const float* __restrict__ g, const int* __restrict__ lens, bool start,
-                                                    E* __restrict__ o, Scratch w, Shape sh) {
+__global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
+    out_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const int* __restrict__ lens, bool start,
+               E* __restrict__ o, Scratch w, Shape sh) {
     using M = OutSmem<E, ND, PD, C>;
-    constexpr int NT = 2 * C;
+    constexpr int NP = M::NP, SP = M::SP, CW = PD / Part<C>::CS;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ __align__(16) Decays<C> d;
+    const Decays<C>& d = *reinterpret_cast<const Decays<C>*>(smem + M::D);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int h = blockIdx.x % sh.H, bc = blockIdx.x / sh.H, c = bc % sh.nc, b = bc / sh.nc, KH = sh.H / sh.G;
     const int len = row_len(lens, b, sh.T), live = (len + C - 1) / C, n = min(len - c * C, C), rows = min(sh.T - c * C, C);
     const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C, bh = (int64_t)b * sh.H + h, os = (int64_t)sh.H * sh.P;
     E* orow = o + t0 * os + (int64_t)h * sh.P;
-    if (n <= 0) {
-        const int per = sh.P * (int)sizeof(E) / 16;
-        for (int i = tid; i < rows * per; i += NT)
-            reinterpret_cast<uint4*>(orow + (i / per) * os)[i % per] = make_uint4(0, 0, 0, 0);
-        return;
-    }
+    if (n <= 0) return clear_rows(orow, os, sh.P, rows, tid);
     const int64_t ks = (int64_t)KH * sh.N, ko = t0 * ks + (int64_t)(h / sh.G) * sh.N;
-    load_tile<E, ND>(smem + M::Q, C * pitch(ND), q + ko, ks, C, n, sh.N, tid, NT);
-    load_tile<E, ND>(smem + M::K, C * pitch(ND), k + ko, ks, C, n, sh.N, tid, NT);
-    load_tile<E, PD>(smem + M::V, C * pitch(PD), v + t0 * os + (int64_t)h * sh.P, os, C, n, sh.P, tid, NT);
+    load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, M::TABLE, tid);
+    load_tile<E, ND, C, NT>(smem + M::Q, C * pitch(ND), q + ko, ks, n, sh.N, tid);
+    load_tile<E, ND, C, NT>(smem + M::K, C * pitch(ND), k + ko, ks, n, sh.N, tid);
+    load_tile<E, PD, C, NT>(smem + M::V, C * pitch(PD), v + t0 * os + (int64_t)h * sh.P, os, n, sh.P, tid);
     cp_commit();
-    if (warp == 0) chunk_decays<C, true>(d, g + b * sh.g_row + h + (int64_t)c * C * sh.g_tok, sh.g_tok, n, lane);
     const StateAt st = state_at(w, sh, 0, bh, c, live, start);
+    StateTile<SP, PD> tile;
+    if (st.any()) {
+        tile.fetch(st, 0, sh, tid);
+        tile.put(smem + M::S, tid);
+    }
     cp_wait<0>();
     __syncthreads();
-    using Pr = Product<M::NP, M::SP, M::NP == 3 ? 3 : M::NP, M::SP, C, ND, PD, true, true>;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    const int block = block_of<C / 16>(warp), r0 = 16 * block + lane / 4;
-    float acc[PD / 8][4] = {};
+    const Part<C> part(warp);
+    const int block = part.block, col0 = part.share * CW, r0 = 16 * block + lane / 4;
+    float acc[CW / 8][4] = {};
     if (st.any()) {
-        Pr::state(acc, base + M::Q, base + M::S, block, sh.N, sh.P, lane,
-                  [&](int sl) { fill_state<M::SP, PD>(smem + M::S, st, sl, sh, tid, NT); });
-        const float f0 = d.in[r0], f1 = d.in[r0 + 8];
 #pragma unroll
-        for (int nt = 0; nt < PD / 8; ++nt) acc[nt][0] *= f0, acc[nt][1] *= f0, acc[nt][2] *= f1, acc[nt][3] *= f1;
+        for (int sl = 0; sl < ND / 64; ++sl) {
+            if (64 * sl >= sh.N) break;
+            if (sl) {
+                tile.fetch(st, sl, sh, tid);
+                __syncthreads();
+                tile.put(smem + M::S, tid);
+                __syncthreads();
+            }
+            times_state<NP, SP, C, ND, PD, CW, true>(acc, base + M::Q, base + M::S, block, col0, sl, sh.N, sh.P, lane);
+        }
+        scale_rows(acc, d.in[r0], d.in[r0 + 8]);
     }
     if (16 * block < n)
-        Pr::pairs(acc, base + M::Q, base + M::K, base + M::V, block, sh.N, sh.P, 0, 1.f, d, lane);
-    if (sizeof(E) == 2) __syncthreads();  // (the state's planes are read: the stage lies over them)
-    put_rows<E, PD>(orow + 16 * block * os, os, acc, sh.scale, smem + M::S + 16 * block * pitch(PD), sh.P, n - 16 * block,
-                    rows - 16 * block, lane);
+        earlier_pairs<NP, NP, SP, C, ND, PD, CW>(acc, base + M::Q, base + M::K, base + M::V, block, col0, sh.N, sh.P, 1.f, d, lane);
+    if (sizeof(E) == 2 && st.any()) __syncthreads();  // (the state's planes are read: the stage lies over them)
+    put_rows<E, PD, CW>(orow + 16 * block * os, os, acc, sh.scale, smem + M::S + 16 * block * pitch(PD), col0, sh.P, n - 16 * block,
+                        rows - 16 * block, lane);
 }
 
 // --------------------------------------------------------------- gradients
-// Scores and states are split in three planes for dq and dk, whose sums make dg
-// (a float32 result), in two for dv, which is rounded to 16 bits.
+// The states have three planes for dq and dk, from which dg (a float32 result) takes its terms, and two for dv.
 template <typename E, int ND, int PD, int C>
 struct GradSmem {
-    static constexpr int NP = Type<E>::NP;
+    static constexpr int NP = Type<E>::NP, SP = NP == 3 ? 3 : 2, RB = C / 16;
     static constexpr int X = NP * C * pitch(ND), Y = NP * C * pitch(PD);
     static constexpr int Q = 0, K = X, V = 2 * X, DO = 2 * X + Y, S = 2 * X + 2 * Y;
-    static constexpr int BYTES = S + imax(3 * 64 * pitch(PD), sizeof(E) == 2 ? C * pitch(imax(ND, PD)) : 0);
+    static constexpr int D = S + imax(3 * 64 * pitch(PD), sizeof(E) == 2 ? C * pitch(imax(ND, PD)) : 0);
+    static constexpr int COL = D + sizeof(Decays<C>);      // [RB][C] sums of W over the tokens j of a block
+    static constexpr int ROW = COL + 4 * RB * C;           // [C] sums of W over i
+    static constexpr int AQ = ROW + 4 * C, BK = AQ + 8 / RB * C * 4, BYTES = BK + 8 / RB * C * 4;  // [share][C]
+    static constexpr int CTAS = BYTES + 1280 <= 114 * 1024 ? 2 : 1;
 };
 
-// Sum over a row's columns of the accumulators times a tile's values (rows r0 and r0 + 8), in every lane
-// of the four that share the rows.
-template <int NPL, int C, int W>
-__device__ __forceinline__ float2 dot_rows(const float (&acc)[W / 8][4], const unsigned char* tile, int block, int width, int lane) {
-    float s0 = 0.f, s1 = 0.f;
+// Sum over a row's columns of the accumulators times a tile's values (rows r0 and r0 + 8), in every lane of the
+// four that share the rows.
+template <int NPL, int C, int W, int CW>
+__device__ __forceinline__ float2 dot_rows(const float (&acc)[CW / 8][4], const unsigned char* tile, int block, int col0, int width, int lane) {
+    float s[2] = {};
+    const unsigned char* at = tile + (16 * block + lane / 4) * pitch(W) + 2 * col0 + 4 * (lane % 4);
 #pragma unroll
-    for (int nt = 0; nt < W / 8; ++nt) {
-        if (8 * nt >= width) break;
+    for (int nt = 0; nt < CW / 8; ++nt) {
+        if (col0 + 8 * nt >= width) break;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float x = 0.f, y = 0.f;
 #pragma unroll
             for (int z = NPL - 1; z >= 0; --z) {
-                const uint32_t v = *reinterpret_cast<const uint32_t*>(tile + z * C * pitch(W) + (16 * block + lane / 4 + 8 * e) * pitch(W) +
-                                                                      16 * nt + 4 * (lane % 4));
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(at + z * C * pitch(W) + 8 * e * pitch(W) + 16 * nt);
                 x += lo_f(v), y += hi_f(v);
             }
-            float& s = e ? s1 : s0;
-            s = fmaf(acc[nt][2 * e], x, s);
-            s = fmaf(acc[nt][2 * e + 1], y, s);
+            s[e] = fmaf(acc[nt][2 * e], x, fmaf(acc[nt][2 * e + 1], y, s[e]));
         }
     }
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) {
-        s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+        s[1] += __shfl_xor_sync(0xffffffffu, s[1], o);
     }
-    return make_float2(s0, s1);
+    return make_float2(s[0], s[1]);
 }
 
 template <typename E, int ND, int PD, int C>
-__global__ void __launch_bounds__(2 * C) grad_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v,
-                                                     const E* __restrict__ dout, const float* __restrict__ g,
-                                                     const int* __restrict__ lens, bool start, bool end, E* __restrict__ gq,
-                                                     E* __restrict__ gk, E* __restrict__ gv, float* __restrict__ parts,
-                                                     float* __restrict__ gg, float* __restrict__ gg_part, Scratch w, Shape sh) {
+__global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
+    grad_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ dout,
+                const int* __restrict__ lens, bool start, bool end, E* __restrict__ gq, E* __restrict__ gk, E* __restrict__ gv,
+                float* __restrict__ parts, float* __restrict__ gg, float* __restrict__ gg_part, Scratch w, Shape sh) {
     using M = GradSmem<E, ND, PD, C>;
-    constexpr int NT = 2 * C, NP = M::NP;
+    constexpr int NP = M::NP, SP = M::SP, QP = NP == 1 ? 1 : 3, CN = ND / Part<C>::CS, CP = PD / Part<C>::CS, SHARES = Part<C>::CS;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ __align__(16) Decays<C> d;
-    __shared__ float s_r[C], s_state[C], s_dot[NT / 32];
+    __shared__ float s_dot[NT / 32];
+    const Decays<C>& d = *reinterpret_cast<const Decays<C>*>(smem + M::D);
+    float(*s_col)[C] = reinterpret_cast<float(*)[C]>(smem + M::COL);
+    float* s_row = reinterpret_cast<float*>(smem + M::ROW);
+    float(*s_aq)[C] = reinterpret_cast<float(*)[C]>(smem + M::AQ);
+    float(*s_bk)[C] = reinterpret_cast<float(*)[C]>(smem + M::BK);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int h = blockIdx.x % sh.H, bc = blockIdx.x / sh.H, c = bc % sh.nc, b = bc / sh.nc, KH = sh.H / sh.G;
     const int len = row_len(lens, b, sh.T), live = (len + C - 1) / C, n = min(len - c * C, C), rows = min(sh.T - c * C, C);
@@ -603,127 +675,195 @@ __global__ void __launch_bounds__(2 * C) grad_kernel(const E* __restrict__ q, co
     const int64_t ps = (int64_t)sh.H * sh.N, po = t0 * ps + (int64_t)h * sh.N, pk = (int64_t)(gridDim.x / (sh.nc * sh.H)) * sh.T * ps;
     float* ggp = gg ? gg + t0 * sh.H + h : nullptr;
     if (n <= 0) {
-        auto clear = [&](auto* at, int64_t stride, int width) {
-            const int per = width * (int)sizeof(*at) / 16;
-            for (int i = tid; i < rows * per; i += NT)
-                reinterpret_cast<uint4*>(at + (i / per) * stride)[i % per] = make_uint4(0, 0, 0, 0);
-        };
-        clear(gv + oo, os, sh.P);
+        clear_rows(gv + oo, os, sh.P, rows, tid);
         if (parts) {
-            clear(parts + po, ps, sh.N);
-            clear(parts + pk + po, ps, sh.N);
+            clear_rows(parts + po, ps, sh.N, rows, tid);
+            clear_rows(parts + pk + po, ps, sh.N, rows, tid);
         } else {
-            clear(gq + ko, ks, sh.N);
-            clear(gk + ko, ks, sh.N);
+            clear_rows(gq + ko, ks, sh.N, rows, tid);
+            clear_rows(gk + ko, ks, sh.N, rows, tid);
         }
         if (ggp)
             for (int i = tid; i < rows; i += NT) ggp[(int64_t)i * sh.H] = 0.f;
         if (gg_part && tid == 0) gg_part[blockIdx.x] = 0.f;
         return;
     }
-    load_tile<E, ND>(smem + M::Q, C * pitch(ND), q + ko, ks, C, n, sh.N, tid, NT);
-    load_tile<E, ND>(smem + M::K, C * pitch(ND), k + ko, ks, C, n, sh.N, tid, NT);
-    load_tile<E, PD>(smem + M::V, C * pitch(PD), v + oo, os, C, n, sh.P, tid, NT);
-    load_tile<E, PD>(smem + M::DO, C * pitch(PD), dout + oo, os, C, n, sh.P, tid, NT);
+    load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, sizeof(Decays<C>), tid);
+    load_tile<E, PD, C, NT>(smem + M::DO, C * pitch(PD), dout + oo, os, n, sh.P, tid);
+    load_tile<E, PD, C, NT>(smem + M::V, C * pitch(PD), v + oo, os, n, sh.P, tid);
+    load_tile<E, ND, C, NT>(smem + M::K, C * pitch(ND), k + ko, ks, n, sh.N, tid);
+    load_tile<E, ND, C, NT>(smem + M::Q, C * pitch(ND), q + ko, ks, n, sh.N, tid);
     cp_commit();
-    if (warp == 0) chunk_decays<C, true>(d, g + b * sh.g_row + h + (int64_t)c * C * sh.g_tok, sh.g_tok, n, lane);
     const StateAt sb = state_at(w, sh, 0, bh, c, live, start), sa = state_at(w, sh, 1, bh, c, live, end);
+    StateTile<3, PD> tile;
+    if (sb.any()) {
+        tile.fetch(sb, 0, sh, tid);
+        tile.put(smem + M::S, tid);
+    }
     cp_wait<0>();
     __syncthreads();
-    constexpr int QP = NP == 1 ? 1 : 3, VP = NP == 3 ? 3 : 2;
-    using Pq = Product<NP, 3, QP, 3, C, PD, ND, true, false>;
-    using Pk = Product<NP, 3, QP, 3, C, PD, ND, false, false>;
-    using Pv = Product<NP, VP, QP, VP, C, ND, PD, false, true>;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    const int block = block_of<C / 16>(warp), r0 = 16 * block + lane / 4, last = (n + 15) / 16;
+    const Part<C> part(warp);
+    const int block = part.block, r0 = 16 * block + lane / 4, last = (n + 15) / 16, nq = 16 * block;
+    const int colN = part.share * CN, colP = part.share * CP;
     const bool on = block < last;
     const float scale = sh.scale;
-    auto rows_times = [&](auto& acc, float f0, float f1) {
-#pragma unroll
-        for (auto& t : acc) t[0] *= f0, t[1] *= f0, t[2] *= f1, t[3] *= f1;
-    };
-    float2 rq;
     {
-        float acc[ND / 8][4] = {};
+        float acc[CN / 8][4] = {};
+        float2 a = make_float2(0.f, 0.f);
         if (sb.any()) {
-            Pq::state(acc, base + M::DO, base + M::S, block, sh.P, sh.N, lane,
-                      [&](int sl) { fill_state<3, PD>(smem + M::S, sb, sl, sh, tid, NT); });
-            rows_times(acc, scale * d.in[r0], scale * d.in[r0 + 8]);
+#pragma unroll
+            for (int sl = 0; sl < ND / 64; ++sl) {
+                if (64 * sl >= sh.N) break;
+                if (sl) {
+                    tile.fetch(sb, sl, sh, tid);
+                    __syncthreads();
+                    tile.put(smem + M::S, tid);
+                    __syncthreads();
+                }
+                times_state<NP, 3, C, PD, ND, CN, false>(acc, base + M::DO, base + M::S, block, colN, sl, sh.P, sh.N, lane);
+            }
+            scale_rows(acc, scale * d.in[r0], scale * d.in[r0 + 8]);
+            a = dot_rows<NP, C, ND, CN>(acc, smem + M::Q, block, colN, sh.N, lane);
         }
-        if (on) Pq::pairs(acc, base + M::DO, base + M::V, base + M::K, block, sh.P, sh.N, 0, scale, d, lane);
-        rq = dot_rows<NP, C, ND>(acc, smem + M::Q, block, sh.N, lane);
-        __syncthreads();
+        if (lane % 4 == 0) s_aq[part.share][r0] = a.x, s_aq[part.share][r0 + 8] = a.y;
+        if (on) earlier_pairs<NP, QP, SP, C, PD, ND, CN>(acc, base + M::DO, base + M::V, base + M::K, block, colN, sh.P, sh.N, scale, d, lane);
+        if (sizeof(E) == 2 && sb.any()) __syncthreads();  // (the stage lies over the state's planes)
         if (parts)
-            put_rows<float, ND>(parts + po + 16 * block * ps, ps, acc, 1.f, nullptr, sh.N, n - 16 * block, rows - 16 * block, lane);
+            put_rows<float, ND, CN>(parts + po + nq * ps, ps, acc, 1.f, nullptr, colN, sh.N, n - nq, rows - nq, lane);
         else
-            put_rows<E, ND>(gq + ko + 16 * block * ks, ks, acc, 1.f, smem + M::S + 16 * block * pitch(ND), sh.N, n - 16 * block,
-                            rows - 16 * block, lane);
+            put_rows<E, ND, CN>(gq + ko + nq * ks, ks, acc, 1.f, smem + M::S + nq * pitch(ND), colN, sh.N, n - nq, rows - nq, lane);
     }
     float dot = 0.f;  // <S, dS+>
-    {
-        float acc[ND / 8][4] = {};
-        float2 own = make_float2(0.f, 0.f);
-        if (sa.any()) {
-            const bool both = sb.any();
-            Pk::state(acc, base + M::V, base + M::S, block, sh.P, sh.N, lane, [&](int sl) {
-                fill_state<3, PD>(smem + M::S, sa, sl, sh, tid, NT);
-                if (both) {
-                    const int per = sh.P / 4, top = min(64, sh.N - 64 * sl) * per;
-                    for (int i = tid; i < top; i += NT) {
-                        const int64_t at = (int64_t)64 * sl * sh.P + 4 * i;
-                        const float4 x = sb.at(at), y = sa.at(at);
-                        dot = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot))));
-                    }
-                }
-            });
-            rows_times(acc, d.out[r0], d.out[r0 + 8]);
-            own = dot_rows<NP, C, ND>(acc, smem + M::K, block, sh.N, lane);
-        }
-        if (on) Pk::pairs(acc, base + M::V, base + M::DO, base + M::Q, block, sh.P, sh.N, last, scale, d, lane);
-        const float2 rk = dot_rows<NP, C, ND>(acc, smem + M::K, block, sh.N, lane);
-        if (lane % 4 == 0) {
-            s_r[r0] = rq.x - rk.x, s_r[r0 + 8] = rq.y - rk.y;
-            s_state[r0] = own.x, s_state[r0 + 8] = own.y;
-        }
+    float dk[CN / 8][4] = {}, dv[CP / 8][4] = {};
+    float2 own = make_float2(0.f, 0.f);
+    if (sa.any()) {
+        const bool both = sb.any();
 #pragma unroll
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) s_dot[warp] = dot;
-        __syncthreads();
-        if (parts)
-            put_rows<float, ND>(parts + pk + po + 16 * block * ps, ps, acc, 1.f, nullptr, sh.N, n - 16 * block, rows - 16 * block, lane);
-        else
-            put_rows<E, ND>(gk + ko + 16 * block * ks, ks, acc, 1.f, smem + M::S + 16 * block * pitch(ND), sh.N, n - 16 * block,
-                            rows - 16 * block, lane);
+        for (int sl = 0; sl < ND / 64; ++sl) {
+            if (64 * sl >= sh.N) break;
+            tile.fetch(sa, sl, sh, tid);
+            __syncthreads();
+            tile.put(smem + M::S, tid);
+            if (both) {
+                using ST = StateTile<3, PD>;
+                const int r = 64 * sl + tid / ST::PER, x = 4 * (tid % ST::PER);
+#pragma unroll
+                for (int e = 0; e < ST::K; ++e)
+                    if (x < sh.P && r + ST::STEP * e < sh.N) {
+                        const float4 u = sb.at((int64_t)(r + ST::STEP * e) * sh.P + x), y = tile.v[e];
+                        dot = fmaf(u.x, y.x, fmaf(u.y, y.y, fmaf(u.z, y.z, fmaf(u.w, y.w, dot))));
+                    }
+            }
+            __syncthreads();
+            times_state<NP, 3, C, PD, ND, CN, false>(dk, base + M::V, base + M::S, block, colN, sl, sh.P, sh.N, lane);
+            times_state<NP, SP, C, ND, PD, CP, true>(dv, base + M::K, base + M::S, block, colP, sl, sh.N, sh.P, lane);
+        }
+        scale_rows(dk, d.out[r0], d.out[r0 + 8]);
+        scale_rows(dv, d.out[r0], d.out[r0 + 8]);
+        own = dot_rows<NP, C, ND, CN>(dk, smem + M::K, block, colN, sh.N, lane);
     }
+    if (lane % 4 == 0) s_bk[part.share][r0] = own.x, s_bk[part.share][r0 + 8] = own.y;
+    float wr[2] = {};  // sums of W over the tokens i
+    if (on) {
+        const Rows<NP, C, ND> rk(base + M::K, block, sh.N, lane);
+        const Rows<NP, C, PD> rv(base + M::V, block, sh.P, lane);
+        float row[2];
+        row_factors<C, false>(row, d, block, scale, lane);
+#pragma unroll 1
+        for (int o = block; o < last; ++o) {
+            float sa_[2][4], sb_[2][4], m[2][4];
+            scores<NP, QP, C, ND>(sa_, rk, base + M::Q, o, sh.N, lane);   // k_j . q_i
+            scores<NP, QP, C, PD>(sb_, rv, base + M::DO, o, sh.P, lane);  // v_j . do_i
+            pair_factors<C, false>(m, d, block, o, row, scale, lane);
+            if (o == block) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (8 * x + 2 * (lane % 4) + e % 2 < lane / 4 + 8 * (e / 2)) sa_[x][e] = sb_[x][e] = 0.f;
+            }
+            multiply(sa_, m);
+            float ws[2][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ws[x][e] = sa_[x][e] * sb_[x][e];
+            multiply(sb_, m);
+            wr[0] += (ws[0][0] + ws[0][1]) + (ws[1][0] + ws[1][1]);
+            wr[1] += (ws[0][2] + ws[0][3]) + (ws[1][2] + ws[1][3]);
+            {  // over the 16 tokens j, for the four columns of a lane: halves change hands
+                float c0 = ws[0][0] + ws[0][2], c1 = ws[0][1] + ws[0][3], c2 = ws[1][0] + ws[1][2], c3 = ws[1][1] + ws[1][3];
+                const bool up = lane & 16, odd = lane & 8;
+                const float g0 = __shfl_xor_sync(0xffffffffu, up ? c0 : c2, 16), g1 = __shfl_xor_sync(0xffffffffu, up ? c1 : c3, 16);
+                c0 = (up ? c2 : c0) + g0, c1 = (up ? c3 : c1) + g1;
+                const float g2 = __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 8);
+                c0 = (odd ? c1 : c0) + g2;
+                c0 += __shfl_xor_sync(0xffffffffu, c0, 4);
+                if (!(lane & 4) && part.share == 0) s_col[block][16 * o + (up ? 8 : 0) + 2 * (lane % 4) + (odd ? 1 : 0)] = c0;
+            }
+            times_tokens<NP, SP, C, PD, CP>(dv, sa_, base + M::DO, colP, o, sh.P, lane);
+            times_tokens<NP, SP, C, ND, CN>(dk, sb_, base + M::Q, colN, o, sh.N, lane);
+        }
+    }
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+        wr[0] += __shfl_xor_sync(0xffffffffu, wr[0], o);
+        wr[1] += __shfl_xor_sync(0xffffffffu, wr[1], o);
+    }
+    if (lane % 4 == 0 && part.share == 0) s_row[r0] = wr[0], s_row[r0 + 8] = wr[1];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) s_dot[warp] = dot;
+    __syncthreads();
+    if (parts)
+        put_rows<float, ND, CN>(parts + pk + po + nq * ps, ps, dk, 1.f, nullptr, colN, sh.N, n - nq, rows - nq, lane);
+    else
+        put_rows<E, ND, CN>(gk + ko + nq * ks, ks, dk, 1.f, smem + M::S + nq * pitch(ND), colN, sh.N, n - nq, rows - nq, lane);
+    if (sizeof(E) == 2 && (ND != PD || !parts)) __syncthreads();  // (the stage's rows lie elsewhere now, or are still read)
+    put_rows<E, PD, CP>(gv + oo + nq * os, os, dv, 1.f, smem + M::S + nq * pitch(PD), colP, sh.P, n - nq, rows - nq, lane);
     if (warp == 0 && (ggp || gg_part)) {
         float all = 0.f;
         for (int i = 0; i < NT / 32; ++i) all += s_dot[i];
         all *= d.all;
-        // a lane's tokens, then the lanes after it
         constexpr int PER = C / 32;
-        float r[PER], tail = 0.f, states = 0.f;
+        float r[PER], bk[PER], tail = 0.f, head = 0.f;  // suffix sums of a lane's tokens, and prefix sums before each
 #pragma unroll
         for (int e = PER - 1; e >= 0; --e) {
-            r[e] = s_r[PER * lane + e];
-            tail += r[e];
+            const int i = PER * lane + e;
+            float x = 0.f;
+            if (i < 16 * last) {
+#pragma unroll
+                for (int u = 0; u < SHARES; ++u) x += s_aq[u][i];
+                float y = 0.f;
+                for (int u = 0; u <= i / 16; ++u) y += s_col[u][i];
+                x += y - s_row[i];
+            }
+            tail += x;
             r[e] = tail;
-            states += s_state[PER * lane + e];
         }
-        float after = tail;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            bk[e] = head;
+#pragma unroll
+            for (int u = 0; u < SHARES; ++u) head += s_bk[u][PER * lane + e];
+        }
+        float after = tail, before = head;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float t = __shfl_down_sync(0xffffffffu, after, o);
-            if (lane + o < 32) after += t;
+            const float x = __shfl_down_sync(0xffffffffu, after, o), y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane + o < 32) after += x;
+            if (lane >= o) before += y;
         }
-        after -= tail;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) states += __shfl_xor_sync(0xffffffffu, states, o);
-        const float leaves = all + states;
+        after = __shfl_down_sync(0xffffffffu, after, 1);
+        before = __shfl_up_sync(0xffffffffu, before, 1);
+        if (lane == 31) after = 0.f;
+        if (lane == 0) before = 0.f;
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const int i = PER * lane + e;
-            const float x = i < n ? leaves + (after + r[e]) : 0.f;
+            const float x = i < n ? all + (before + bk[e]) + (after + r[e]) : 0.f;
             sum += x;
             if (ggp && i < rows) ggp[(int64_t)i * sh.H] = x;
         }
@@ -732,18 +872,6 @@ __global__ void __launch_bounds__(2 * C) grad_kernel(const E* __restrict__ q, co
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0) gg_part[blockIdx.x] = sum;
         }
-    }
-    {
-        float acc[PD / 8][4] = {};
-        if (sa.any()) {
-            Pv::state(acc, base + M::K, base + M::S, block, sh.N, sh.P, lane,
-                      [&](int sl) { fill_state<VP, PD>(smem + M::S, sa, sl, sh, tid, NT); });
-            rows_times(acc, d.out[r0], d.out[r0 + 8]);
-        }
-        if (on) Pv::pairs(acc, base + M::K, base + M::Q, base + M::DO, block, sh.N, sh.P, last, scale, d, lane);
-        if (sizeof(E) == 2) __syncthreads();
-        put_rows<E, PD>(gv + oo + 16 * block * os, os, acc, 1.f, smem + M::S + 16 * block * pitch(PD), sh.P, n - 16 * block,
-                        rows - 16 * block, lane);
     }
 }
 
@@ -784,28 +912,32 @@ __global__ void __launch_bounds__(128) join_g_kernel(const float* __restrict__ p
 }
 
 // --------------------------------------------------------------- launches
-// The chunk: what leaves a chunk's tiles of the gradients and 64 rows of a state
-// room in one SM's shared memory.
+// The chunk: what leaves a chunk's tiles of the gradients and 64 rows of a state room in one SM's shared memory.
 template <typename E, int ND, int PD>
 constexpr int chunk_tokens() {
     return Type<E>::NP == 1 ? 128 : Type<E>::NP == 2 ? 64 : imax(ND, PD) == 64 ? 64 : 32;
 }
-int chunk_of(const LinattnArgs& a) {
+inline int chunk_of(const LinattnArgs& a) {
     if (a.dtype == CSSD_BF16) return 128;
     if (a.dtype == CSSD_F16) return 64;
     return a.N <= 64 && a.P <= 64 ? 64 : 32;
 }
+inline size_t decays_bytes(const LinattnArgs& a) {
+    const int C = chunk_of(a);
+    return C == 128 ? sizeof(Decays<128>) : C == 64 ? sizeof(Decays<64>) : sizeof(Decays<32>);
+}
 
 constexpr int kStateCtas = 304;  // CTAs that the states' walk aims at: two an SM
 
-Shape shape_of(const LinattnArgs& a, int dirs) {
+inline Shape shape_of(const LinattnArgs& a, int dirs) {
     Shape sh{};
     const int C = chunk_of(a);
     sh.T = (int)a.T, sh.H = (int)a.H, sh.G = (int)(a.H / a.KH), sh.N = (int)a.N, sh.P = (int)a.P;
     sh.nc = (int)((a.T + C - 1) / C);
     sh.BH = (int)(a.Bz * a.H);
     const int64_t rows = a.Bz * a.H * dirs * ((a.P + 63) / 64);
-    const int64_t want = rows >= kStateCtas ? 1 : (kStateCtas + rows - 1) / rows;
+    int64_t want = rows >= kStateCtas ? 1 : kStateCtas / rows;
+    if (want > kMostSegments) want = kMostSegments;
     sh.seg = (int)((sh.nc + want - 1) / want);
     sh.nseg = (sh.nc + sh.seg - 1) / sh.seg;
     sh.g_row = a.g_tokens ? a.T * a.H : 0;
@@ -814,47 +946,53 @@ Shape shape_of(const LinattnArgs& a, int dirs) {
     return sh;
 }
 
-size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
+inline size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 
-size_t scratch_bytes(const LinattnArgs& a, int dirs) {
+// The workspace's parts; returns what they take together.
+inline size_t scratch_of(const LinattnArgs& a, int dirs, void* ws, Scratch& s) {
     const Shape sh = shape_of(a, dirs);
     const size_t rows = (size_t)dirs * sh.BH, np = (size_t)sh.N * sh.P * 4;
-    size_t n = up(rows * sh.nc * np);
-    if (sh.nseg > 1) n += up(rows * sh.nseg * np) + up(rows * sh.nseg * 4) + up(rows * sh.nc * 4);
-    return n;
-}
-Scratch scratch_of(const LinattnArgs& a, int dirs, void* ws) {
-    const Shape sh = shape_of(a, dirs);
-    const size_t rows = (size_t)dirs * sh.BH, np = (size_t)sh.N * sh.P * 4;
-    unsigned char* p = static_cast<unsigned char*>(ws);
-    Scratch s{};
+    size_t at = 0;
     auto take = [&](size_t n) {
-        float* at = reinterpret_cast<float*>(p);
-        p += up(n);
-        return at;
+        void* p = static_cast<unsigned char*>(ws) + at;
+        at += up(n);
+        return static_cast<float*>(p);
     };
+    s = Scratch{};
     s.states = take(rows * sh.nc * np);
+    s.decays = take((size_t)sh.BH * sh.nc * decays_bytes(a));
     if (sh.nseg > 1) {
-        s.segs = take(rows * sh.nseg * np);
-        s.seg_all = take(rows * sh.nseg * 4);
+        s.ends = take(rows * sh.nseg * np);
+        s.starts = take(rows * sh.nseg * np);
+        s.seg_all = take(rows * ((sh.P + 63) / 64) * sh.nseg * 4);
         s.dec = take(rows * sh.nc * 4);
     }
-    return s;
+    return at;
+}
+inline size_t scratch_bytes(const LinattnArgs& a, int dirs) {
+    Scratch s;
+    return scratch_of(a, dirs, nullptr, s);
 }
 
 template <typename E, int ND, int PD>
 cudaError_t run_states(const LinattnArgs& a, int dirs, const Scratch& w, const Shape& sh, cudaStream_t st) {
     constexpr int C = chunk_tokens<E, ND, PD>();
     using M = StatesSmem<E, ND, C>;
-    auto* kernel = states_kernel<E, ND, C>;
     cudaError_t e = delta::allow<states_kernel<E, ND, C>>(M::BYTES);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(sh.BH * ((sh.P + 63) / 64), sh.nseg, dirs), 32 * (M::WARPS + 1), M::BYTES, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.g,
-        a.lens, a.h0, a.dh_final, a.h_final, a.gh0, w, sh);
-    if (sh.nseg > 1)
-        segments_kernel<C><<<dim3((sh.N * sh.P + 511) / 512, sh.BH, dirs), 128, 0, st>>>(a.lens, a.h0, a.dh_final, a.h_final, a.gh0, w, sh);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sh.BH * ((sh.P + 63) / 64), sh.nseg, dirs);
+    cfg.blockDim = dim3(M::THREADS);
+    cfg.dynamicSmemBytes = M::BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1, attr.val.clusterDim.y = sh.nseg, attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, states_kernel<E, ND, C>, static_cast<const E*>(a.q), static_cast<const E*>(a.k),
+                              static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.g, a.lens, a.h0, a.dh_final, a.h_final, a.gh0, w,
+                              sh);
 }
 
 template <typename E, int ND, int PD>
@@ -862,33 +1000,34 @@ cudaError_t forward(const LinattnArgs& a, void* ws, cudaStream_t st) {
     constexpr int C = chunk_tokens<E, ND, PD>();
     using M = OutSmem<E, ND, PD, C>;
     const Shape sh = shape_of(a, 1);
-    const Scratch w = scratch_of(a, 1, ws);
+    Scratch w;
+    scratch_of(a, 1, ws, w);
     cudaError_t e = run_states<E, ND, PD>(a, 1, w, sh, st);
     if (e == cudaSuccess) e = delta::allow<out_kernel<E, ND, PD, C>>(M::BYTES);
     if (e != cudaSuccess) return e;
-    out_kernel<E, ND, PD, C><<<(unsigned)(sh.BH * sh.nc), 2 * C, M::BYTES, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), a.g, a.lens, a.h0 != nullptr,
-        static_cast<E*>(a.o), w, sh);
+    out_kernel<E, ND, PD, C><<<(unsigned)(sh.BH * sh.nc), NT, M::BYTES, st>>>(static_cast<const E*>(a.q), static_cast<const E*>(a.k),
+                                                                            static_cast<const E*>(a.v), a.lens, a.h0 != nullptr,
+                                                                            static_cast<E*>(a.o), w, sh);
     return cudaGetLastError();
 }
 
-size_t parts_bytes(const LinattnArgs& a) { return a.H == a.KH ? 0 : up((size_t)2 * a.Bz * a.T * a.H * a.N * 4); }
+inline size_t parts_bytes(const LinattnArgs& a) { return a.H == a.KH ? 0 : up((size_t)2 * a.Bz * a.T * a.H * a.N * 4); }
 
 template <typename E, int ND, int PD>
 cudaError_t backward(const LinattnArgs& a, void* ws, cudaStream_t st) {
     constexpr int C = chunk_tokens<E, ND, PD>();
     using M = GradSmem<E, ND, PD, C>;
     const Shape sh = shape_of(a, 2);
-    const Scratch w = scratch_of(a, 2, ws);
-    unsigned char* rest = static_cast<unsigned char*>(ws) + scratch_bytes(a, 2);
+    Scratch w;
+    unsigned char* rest = static_cast<unsigned char*>(ws) + scratch_of(a, 2, ws, w);
     float* parts = parts_bytes(a) ? reinterpret_cast<float*>(rest) : nullptr;
     float* gg_part = a.gg && !a.g_tokens ? reinterpret_cast<float*>(rest + parts_bytes(a)) : nullptr;
     cudaError_t e = run_states<E, ND, PD>(a, 2, w, sh, st);
     if (e == cudaSuccess) e = delta::allow<grad_kernel<E, ND, PD, C>>(M::BYTES);
     if (e != cudaSuccess) return e;
-    grad_kernel<E, ND, PD, C><<<(unsigned)(sh.BH * sh.nc), 2 * C, M::BYTES, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.g,
-        a.lens, a.h0 != nullptr, a.dh_final != nullptr, static_cast<E*>(a.gq), static_cast<E*>(a.gk), static_cast<E*>(a.gv), parts,
+    grad_kernel<E, ND, PD, C><<<(unsigned)(sh.BH * sh.nc), NT, M::BYTES, st>>>(
+        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.lens,
+        a.h0 != nullptr, a.dh_final != nullptr, static_cast<E*>(a.gq), static_cast<E*>(a.gk), static_cast<E*>(a.gv), parts,
         a.g_tokens ? a.gg : nullptr, gg_part, w, sh);
     if (parts) {
         const int64_t vectors = a.Bz * a.T * a.KH * (a.N / 4);
