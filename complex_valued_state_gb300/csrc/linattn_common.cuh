@@ -87,7 +87,13 @@ __device__ __forceinline__ uint32_t lane_at(uint32_t base, int pitch_, int r0, i
     const int c = c0 + (FLIP ? (lane >> 3 & 1) * 8 : (lane >> 4) * 8);
     return base + r * pitch_ + 2 * c;
 }
-// c += A B for 16 x 8 outputs and 16 of the sum.
+// c = A B (the sum's first 16), and c += A B, for 16 x 8 outputs.
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -114,19 +120,18 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, int plane, const E
     const int r0 = tid / PER, c = tid % PER;
     if (c * V >= width) return;
     src += r0 * stride + c * V;
+    const int64_t step = STEP * stride;
     if constexpr (NP == 1) {
         uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + r0 * pitch(W) + 16 * c;
+        n -= r0;
 #pragma unroll
-        for (int r = 0; r < ROWS; r += STEP, to += STEP * pitch(W)) {
-            const bool there = r0 + r < n;
-            cp16(to, src + (there ? r * stride : -r0 * stride), there);
-        }
+        for (int r = 0; r < ROWS; r += STEP, src += step) cp16(to + r * pitch(W), src, r < n);
     } else {
         unsigned char* at = dst + r0 * pitch(W) + c * V * 2;
 #pragma unroll
-        for (int r = 0; r < ROWS; r += STEP, at += STEP * pitch(W)) {
+        for (int r = 0; r < ROWS; r += STEP, at += STEP * pitch(W), src += step) {
             alignas(16) E e[V];
-            *reinterpret_cast<uint4*>(e) = r0 + r < n ? *reinterpret_cast<const uint4*>(src + r * stride) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(e) = r0 + r < n ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
             uint32_t w[NP][V / 2];
 #pragma unroll
             for (int u = 0; u < V / 2; ++u) {
@@ -145,6 +150,21 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, int plane, const E
         }
     }
 }
+
+// Division of n < 2^31 by a number that is the same all over a launch.
+struct Divisor {
+    uint32_t d, m, s;
+    __host__ static Divisor of(uint32_t d) {
+        uint32_t s = 0;
+        while ((1ull << s) < d) ++s;
+        return {d, (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1), s};
+    }
+    __device__ __forceinline__ int div(int n, int& rest) const {
+        const uint32_t q = (__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s;
+        rest = (int)((uint32_t)n - q * d);
+        return (int)q;
+    }
+};
 
 // --------------------------------------------------------------- decays
 // G_i is the running sum of the log decays of a chunk.  The decay between two

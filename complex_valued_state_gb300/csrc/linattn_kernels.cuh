@@ -39,6 +39,7 @@ struct Shape {
     int64_t g_row, g_tok;    // elements between batch rows and tokens of g (0: one decay a head)
     int BH;
     float scale;
+    Divisor by_h, by_nc, by_slices;
 };
 constexpr int kMostSegments = 8;  // CTAs of a cluster
 
@@ -131,17 +132,24 @@ template <int NPL, int QP, int C, int KW>
 __device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW>& a, uint32_t b, int o, int kw, int lane) {
     const uint32_t at = lane_at<true>(b, pitch(KW), 16 * o, 0, lane);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[h][e] = 0.f;
-#pragma unroll
     for (int kt = 0; kt < KW / 16; ++kt) {
         if (16 * kt >= kw) break;
-        if constexpr (Rows<NPL, C, KW>::KEEP) {
-            uint32_t bf[4];
+        if constexpr (NPL == 1) {
+            uint32_t bf[4], af[4];
             ldsm(bf, at + 32 * kt);
-            mma(sc[0], a.f[kt], bf[0], bf[1]);
-            mma(sc[1], a.f[kt], bf[2], bf[3]);
+            if constexpr (Rows<NPL, C, KW>::KEEP) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) af[e] = a.f[kt][e];
+            } else {
+                ldsm(af, a.at + 32 * kt);
+            }
+            if (kt == 0) {
+                mma_first(sc[0], af, bf[0], bf[1]);
+                mma_first(sc[1], af, bf[2], bf[3]);
+            } else {
+                mma(sc[0], af, bf[0], bf[1]);
+                mma(sc[1], af, bf[2], bf[3]);
+            }
         } else {
             uint32_t af[NPL][4];
 #pragma unroll
@@ -153,8 +161,13 @@ __device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW>
 #pragma unroll
                 for (int i = NPL - 1; i >= 0; --i)
                     if (i + j < QP) {
-                        mma(sc[0], af[i], bf[0], bf[1]);
-                        mma(sc[1], af[i], bf[2], bf[3]);
+                        if (kt == 0 && j == NPL - 1 && i == imin(NPL - 1, QP - NPL)) {
+                            mma_first(sc[0], af[i], bf[0], bf[1]);
+                            mma_first(sc[1], af[i], bf[2], bf[3]);
+                        } else {
+                            mma(sc[0], af[i], bf[0], bf[1]);
+                            mma(sc[1], af[i], bf[2], bf[3]);
+                        }
                     }
             }
         }
@@ -260,7 +273,7 @@ struct StateAt {
     const float* seg;   // null: none
     float dec;
     __device__ __forceinline__ bool any() const { return own || seg; }
-    __device__ __forceinline__ float4 at(int64_t i) const {
+    __device__ __forceinline__ float4 at(int i) const {
         float4 v = own ? __ldcs(reinterpret_cast<const float4*>(own + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
         if (seg) {
             const float4 s = *reinterpret_cast<const float4*>(seg + i);
@@ -291,11 +304,11 @@ template <int SP, int PD>
 struct StateTile {
     static constexpr int PER = PD / 4, STEP = NT / PER, K = 64 / STEP;
     float4 v[K];
-    __device__ __forceinline__ void fetch(const StateAt& st, int sl, const Shape& sh, int tid) {
+    __device__ __forceinline__ void fetch(const StateAt& st, int sl, int N, int P, int tid) {
         const int r = 64 * sl + tid / PER, c = 4 * (tid % PER);
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            v[k] = c < sh.P && r + STEP * k < sh.N ? st.at((int64_t)(r + STEP * k) * sh.P + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[k] = c < P && r + STEP * k < N ? st.at((r + STEP * k) * P + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __device__ __forceinline__ void put(unsigned char* dst, int tid) const {
         unsigned char* at = dst + tid / PER * pitch(PD) + 8 * (tid % PER);
@@ -322,7 +335,7 @@ struct StatesSmem {
     static constexpr int THREADS = 2 * ND;
 };
 
-template <typename E, int ND, int C>
+template <typename E, int ND, int C, bool FULL>
 __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v,
                                                         const E* __restrict__ dout, const float* __restrict__ g,
                                                         const int* __restrict__ lens, const float* h0, const float* dh_final,
@@ -333,17 +346,18 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
     float* weights = reinterpret_cast<float*>(smem + M::W);  // [BATCH][C]
     float* totals = weights + BATCH * C;                     // [BATCH]
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int slices = (sh.P + 63) / 64, bh = blockIdx.x / slices, s = blockIdx.y, dir = blockIdx.z;
-    const int p0 = 64 * (blockIdx.x % slices), cols = min(64, sh.P - p0);
-    const int b = bh / sh.H, h = bh % sh.H, KH = sh.H / sh.G;
+    const int N = FULL ? ND : sh.N, P = sh.P, s = blockIdx.y, dir = blockIdx.z;
+    int slice, h;
+    const int bh = sh.by_slices.div(blockIdx.x, slice), b = sh.by_h.div(bh, h), slices = (int)sh.by_slices.d;
+    const int p0 = 64 * slice, cols = FULL ? 64 : min(64, P - p0), KH = sh.H / sh.G;
     const int len = row_len(lens, b, sh.T), live = (len + C - 1) / C;
     const int w0 = s * sh.seg, w1 = min(w0 + sh.seg, live);
-    const int64_t np = (int64_t)sh.N * sh.P, row = (int64_t)dir * sh.BH + bh;
+    const int64_t np = (int64_t)N * P, row = (int64_t)dir * sh.BH + bh;
     const int n0 = 16 * warp;
-    const bool mine = n0 < sh.N, first = tid == 0 && p0 == 0;
-    const E* xs = (dir ? q : k) + (int64_t)(h / sh.G) * sh.N;
-    const E* ys = (dir ? dout : v) + (int64_t)h * sh.P + p0;
-    const int64_t xst = (int64_t)KH * sh.N, yst = (int64_t)sh.H * sh.P;
+    const bool mine = n0 < N, first = tid == 0 && p0 == 0;
+    const E* xs = (dir ? q : k) + (int64_t)(h / sh.G) * N;
+    const E* ys = (dir ? dout : v) + (int64_t)h * P + p0;
+    const int64_t xst = (int64_t)KH * N, yst = (int64_t)sh.H * P;
     const float* gs = g + b * sh.g_row + h;
     auto chunk_of = [&](int i) { return dir ? live - 1 - i : i; };
     auto fetch = [&](int t) {  // the t-th stage of this segment
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
         if (i < w1) {
             const int64_t t0 = (int64_t)b * sh.T + min(at0, len - 1);  // (a half without tokens reads nothing)
             unsigned char* at = smem + t % STAGES * (M::X + M::Y);
-            load_tile<E, ND, HT, THREADS>(at, HT * pitch(ND), xs + t0 * xst, xst, len - at0, sh.N, tid);
+            load_tile<E, ND, HT, THREADS>(at, HT * pitch(ND), xs + t0 * xst, xst, len - at0, N, tid);
             load_tile<E, 64, HT, THREADS>(at + M::X, HT * pitch(64), ys + t0 * yst, yst, len - at0, cols, tid);
         }
         if (NP == 1) cp_commit();
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
                 const int p = 8 * nt + 2 * (lane % 4);
-                if (p < cols) f((int64_t)(n0 + lane / 4 + 4 * e) * sh.P + p0 + p, st[nt][e], st[nt][e + 1]);
+                if (p < cols) f((int64_t)(n0 + lane / 4 + 4 * e) * P + p0 + p, st[nt][e], st[nt][e + 1]);
             }
     };
 #pragma unroll
@@ -421,9 +435,9 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
                 const float2 u1 = *reinterpret_cast<const float2*>(wt + half * HT + 16 * kt + 8 + 2 * (lane % 4));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    float e0 = 0.f, e1 = 0.f;
+                    float e0 = lo_f(raw[NP - 1][r]), e1 = hi_f(raw[NP - 1][r]);
 #pragma unroll
-                    for (int z = NP - 1; z >= 0; --z) e0 += lo_f(raw[z][r]), e1 += hi_f(raw[z][r]);
+                    for (int z = NP - 2; z >= 0; --z) e0 += lo_f(raw[z][r]), e1 += hi_f(raw[z][r]);
                     uint32_t pl[3];
                     split<3>(e0 * (r < 2 ? u0.x : u1.x), e1 * (r < 2 ? u0.y : u1.y), pl);
                     a[0][r] = pl[0], a[1][r] = pl[1], a[2][r] = pl[2];
@@ -465,10 +479,10 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
     // the segments' own states at their ends, from which each makes the state before it
     float* ends = w.ends + row * sh.nseg * np;
     if (mine) each([&](int64_t at, float x, float y) { *reinterpret_cast<float2*>(ends + s * np + at) = make_float2(x, y); });
-    if (tid == 0) w.seg_all[(row * slices + p0 / 64) * sh.nseg + s] = all;
+    if (tid == 0) w.seg_all[(row * slices + slice) * sh.nseg + s] = all;
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (!mine) return;
-    const float* alls = w.seg_all + (row * slices + p0 / 64) * sh.nseg;
+    const float* alls = w.seg_all + (row * slices + slice) * sh.nseg;
     const bool ends_row = s == max((live + sh.seg - 1) / sh.seg - 1, 0);  // the row's last segment
     float decay[kMostSegments];  // from the end of segment e to this one's start
     float d = 1.f;
@@ -556,7 +570,7 @@ struct OutSmem {
     static constexpr int CTAS = BYTES + 1024 <= 228 * 1024 / 3 ? 3 : BYTES + 1024 <= 114 * 1024 ? 2 : 1;
 };
 
-template <typename E, int ND, int PD, int C>
+template <typename E, int ND, int PD, int C, bool FULL>
 __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
     out_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const int* __restrict__ lens, bool start,
                E* __restrict__ o, Scratch w, Shape sh) {
@@ -565,21 +579,23 @@ __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
     extern __shared__ __align__(128) unsigned char smem[];
     const Decays<C>& d = *reinterpret_cast<const Decays<C>*>(smem + M::D);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int h = blockIdx.x % sh.H, bc = blockIdx.x / sh.H, c = bc % sh.nc, b = bc / sh.nc, KH = sh.H / sh.G;
+    const int N = FULL ? ND : sh.N, P = FULL ? PD : sh.P, KH = sh.H / sh.G;
+    int h, c;
+    const int b = sh.by_nc.div(sh.by_h.div(blockIdx.x, h), c);
     const int len = row_len(lens, b, sh.T), live = (len + C - 1) / C, n = min(len - c * C, C), rows = min(sh.T - c * C, C);
-    const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C, bh = (int64_t)b * sh.H + h, os = (int64_t)sh.H * sh.P;
-    E* orow = o + t0 * os + (int64_t)h * sh.P;
-    if (n <= 0) return clear_rows(orow, os, sh.P, rows, tid);
-    const int64_t ks = (int64_t)KH * sh.N, ko = t0 * ks + (int64_t)(h / sh.G) * sh.N;
+    const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C, bh = (int64_t)b * sh.H + h, os = (int64_t)sh.H * P;
+    E* orow = o + t0 * os + (int64_t)h * P;
+    if (n <= 0) return clear_rows(orow, os, P, rows, tid);
+    const int64_t ks = (int64_t)KH * N, ko = t0 * ks + (int64_t)(h / sh.G) * N;
     load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, M::TABLE, tid);
-    load_tile<E, ND, C, NT>(smem + M::Q, C * pitch(ND), q + ko, ks, n, sh.N, tid);
-    load_tile<E, ND, C, NT>(smem + M::K, C * pitch(ND), k + ko, ks, n, sh.N, tid);
-    load_tile<E, PD, C, NT>(smem + M::V, C * pitch(PD), v + t0 * os + (int64_t)h * sh.P, os, n, sh.P, tid);
+    load_tile<E, ND, C, NT>(smem + M::Q, C * pitch(ND), q + ko, ks, n, N, tid);
+    load_tile<E, ND, C, NT>(smem + M::K, C * pitch(ND), k + ko, ks, n, N, tid);
+    load_tile<E, PD, C, NT>(smem + M::V, C * pitch(PD), v + t0 * os + (int64_t)h * P, os, n, P, tid);
     cp_commit();
     const StateAt st = state_at(w, sh, 0, bh, c, live, start);
     StateTile<SP, PD> tile;
     if (st.any()) {
-        tile.fetch(st, 0, sh, tid);
+        tile.fetch(st, 0, N, P, tid);
         tile.put(smem + M::S, tid);
     }
     cp_wait<0>();
@@ -591,21 +607,21 @@ __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
     if (st.any()) {
 #pragma unroll
         for (int sl = 0; sl < ND / 64; ++sl) {
-            if (64 * sl >= sh.N) break;
+            if (64 * sl >= N) break;
             if (sl) {
-                tile.fetch(st, sl, sh, tid);
+                tile.fetch(st, sl, N, P, tid);
                 __syncthreads();
                 tile.put(smem + M::S, tid);
                 __syncthreads();
             }
-            times_state<NP, SP, C, ND, PD, CW, true>(acc, base + M::Q, base + M::S, block, col0, sl, sh.N, sh.P, lane);
+            times_state<NP, SP, C, ND, PD, CW, true>(acc, base + M::Q, base + M::S, block, col0, sl, N, P, lane);
         }
         scale_rows(acc, d.in[r0], d.in[r0 + 8]);
     }
     if (16 * block < n)
-        earlier_pairs<NP, NP, SP, C, ND, PD, CW>(acc, base + M::Q, base + M::K, base + M::V, block, col0, sh.N, sh.P, 1.f, d, lane);
+        earlier_pairs<NP, NP, SP, C, ND, PD, CW>(acc, base + M::Q, base + M::K, base + M::V, block, col0, N, P, 1.f, d, lane);
     if (sizeof(E) == 2 && st.any()) __syncthreads();  // (the state's planes are read: the stage lies over them)
-    put_rows<E, PD, CW>(orow + 16 * block * os, os, acc, sh.scale, smem + M::S + 16 * block * pitch(PD), col0, sh.P, n - 16 * block,
+    put_rows<E, PD, CW>(orow + 16 * block * os, os, acc, sh.scale, smem + M::S + 16 * block * pitch(PD), col0, P, n - 16 * block,
                         rows - 16 * block, lane);
 }
 
@@ -651,7 +667,7 @@ __device__ __forceinline__ float2 dot_rows(const float (&acc)[CW / 8][4], const 
     return make_float2(s[0], s[1]);
 }
 
-template <typename E, int ND, int PD, int C>
+template <typename E, int ND, int PD, int C, bool FULL>
 __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
     grad_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ dout,
                 const int* __restrict__ lens, bool start, bool end, E* __restrict__ gq, E* __restrict__ gk, E* __restrict__ gv,
@@ -666,22 +682,24 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
     float(*s_aq)[C] = reinterpret_cast<float(*)[C]>(smem + M::AQ);
     float(*s_bk)[C] = reinterpret_cast<float(*)[C]>(smem + M::BK);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int h = blockIdx.x % sh.H, bc = blockIdx.x / sh.H, c = bc % sh.nc, b = bc / sh.nc, KH = sh.H / sh.G;
+    const int N = FULL ? ND : sh.N, P = FULL ? PD : sh.P, KH = sh.H / sh.G;
+    int h, c;
+    const int b = sh.by_nc.div(sh.by_h.div(blockIdx.x, h), c);
     const int len = row_len(lens, b, sh.T), live = (len + C - 1) / C, n = min(len - c * C, C), rows = min(sh.T - c * C, C);
     const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C, bh = (int64_t)b * sh.H + h;
-    const int64_t ks = (int64_t)KH * sh.N, ko = t0 * ks + (int64_t)(h / sh.G) * sh.N;
-    const int64_t os = (int64_t)sh.H * sh.P, oo = t0 * os + (int64_t)h * sh.P;
+    const int64_t ks = (int64_t)KH * N, ko = t0 * ks + (int64_t)(h / sh.G) * N;
+    const int64_t os = (int64_t)sh.H * P, oo = t0 * os + (int64_t)h * P;
     // with shared key heads a value head leaves its part in fp32
-    const int64_t ps = (int64_t)sh.H * sh.N, po = t0 * ps + (int64_t)h * sh.N, pk = (int64_t)(gridDim.x / (sh.nc * sh.H)) * sh.T * ps;
+    const int64_t ps = (int64_t)sh.H * N, po = t0 * ps + (int64_t)h * N, pk = (int64_t)(gridDim.x / (sh.nc * sh.H)) * sh.T * ps;
     float* ggp = gg ? gg + t0 * sh.H + h : nullptr;
     if (n <= 0) {
-        clear_rows(gv + oo, os, sh.P, rows, tid);
+        clear_rows(gv + oo, os, P, rows, tid);
         if (parts) {
-            clear_rows(parts + po, ps, sh.N, rows, tid);
-            clear_rows(parts + pk + po, ps, sh.N, rows, tid);
+            clear_rows(parts + po, ps, N, rows, tid);
+            clear_rows(parts + pk + po, ps, N, rows, tid);
         } else {
-            clear_rows(gq + ko, ks, sh.N, rows, tid);
-            clear_rows(gk + ko, ks, sh.N, rows, tid);
+            clear_rows(gq + ko, ks, N, rows, tid);
+            clear_rows(gk + ko, ks, N, rows, tid);
         }
         if (ggp)
             for (int i = tid; i < rows; i += NT) ggp[(int64_t)i * sh.H] = 0.f;
@@ -689,15 +707,15 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
         return;
     }
     load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, sizeof(Decays<C>), tid);
-    load_tile<E, PD, C, NT>(smem + M::DO, C * pitch(PD), dout + oo, os, n, sh.P, tid);
-    load_tile<E, PD, C, NT>(smem + M::V, C * pitch(PD), v + oo, os, n, sh.P, tid);
-    load_tile<E, ND, C, NT>(smem + M::K, C * pitch(ND), k + ko, ks, n, sh.N, tid);
-    load_tile<E, ND, C, NT>(smem + M::Q, C * pitch(ND), q + ko, ks, n, sh.N, tid);
+    load_tile<E, PD, C, NT>(smem + M::DO, C * pitch(PD), dout + oo, os, n, P, tid);
+    load_tile<E, PD, C, NT>(smem + M::V, C * pitch(PD), v + oo, os, n, P, tid);
+    load_tile<E, ND, C, NT>(smem + M::K, C * pitch(ND), k + ko, ks, n, N, tid);
+    load_tile<E, ND, C, NT>(smem + M::Q, C * pitch(ND), q + ko, ks, n, N, tid);
     cp_commit();
     const StateAt sb = state_at(w, sh, 0, bh, c, live, start), sa = state_at(w, sh, 1, bh, c, live, end);
     StateTile<3, PD> tile;
     if (sb.any()) {
-        tile.fetch(sb, 0, sh, tid);
+        tile.fetch(sb, 0, N, P, tid);
         tile.put(smem + M::S, tid);
     }
     cp_wait<0>();
@@ -714,25 +732,25 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
         if (sb.any()) {
 #pragma unroll
             for (int sl = 0; sl < ND / 64; ++sl) {
-                if (64 * sl >= sh.N) break;
+                if (64 * sl >= N) break;
                 if (sl) {
-                    tile.fetch(sb, sl, sh, tid);
+                    tile.fetch(sb, sl, N, P, tid);
                     __syncthreads();
                     tile.put(smem + M::S, tid);
                     __syncthreads();
                 }
-                times_state<NP, 3, C, PD, ND, CN, false>(acc, base + M::DO, base + M::S, block, colN, sl, sh.P, sh.N, lane);
+                times_state<NP, 3, C, PD, ND, CN, false>(acc, base + M::DO, base + M::S, block, colN, sl, P, N, lane);
             }
             scale_rows(acc, scale * d.in[r0], scale * d.in[r0 + 8]);
-            a = dot_rows<NP, C, ND, CN>(acc, smem + M::Q, block, colN, sh.N, lane);
+            a = dot_rows<NP, C, ND, CN>(acc, smem + M::Q, block, colN, N, lane);
         }
         if (lane % 4 == 0) s_aq[part.share][r0] = a.x, s_aq[part.share][r0 + 8] = a.y;
-        if (on) earlier_pairs<NP, QP, SP, C, PD, ND, CN>(acc, base + M::DO, base + M::V, base + M::K, block, colN, sh.P, sh.N, scale, d, lane);
+        if (on) earlier_pairs<NP, QP, SP, C, PD, ND, CN>(acc, base + M::DO, base + M::V, base + M::K, block, colN, P, N, scale, d, lane);
         if (sizeof(E) == 2 && sb.any()) __syncthreads();  // (the stage lies over the state's planes)
         if (parts)
-            put_rows<float, ND, CN>(parts + po + nq * ps, ps, acc, 1.f, nullptr, colN, sh.N, n - nq, rows - nq, lane);
+            put_rows<float, ND, CN>(parts + po + nq * ps, ps, acc, 1.f, nullptr, colN, N, n - nq, rows - nq, lane);
         else
-            put_rows<E, ND, CN>(gq + ko + nq * ks, ks, acc, 1.f, smem + M::S + nq * pitch(ND), colN, sh.N, n - nq, rows - nq, lane);
+            put_rows<E, ND, CN>(gq + ko + nq * ks, ks, acc, 1.f, smem + M::S + nq * pitch(ND), colN, N, n - nq, rows - nq, lane);
     }
     float dot = 0.f;  // <S, dS+>
     float dk[CN / 8][4] = {}, dv[CP / 8][4] = {};
@@ -741,8 +759,8 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
         const bool both = sb.any();
 #pragma unroll
         for (int sl = 0; sl < ND / 64; ++sl) {
-            if (64 * sl >= sh.N) break;
-            tile.fetch(sa, sl, sh, tid);
+            if (64 * sl >= N) break;
+            tile.fetch(sa, sl, N, P, tid);
             __syncthreads();
             tile.put(smem + M::S, tid);
             if (both) {
@@ -750,31 +768,31 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
                 const int r = 64 * sl + tid / ST::PER, x = 4 * (tid % ST::PER);
 #pragma unroll
                 for (int e = 0; e < ST::K; ++e)
-                    if (x < sh.P && r + ST::STEP * e < sh.N) {
-                        const float4 u = sb.at((int64_t)(r + ST::STEP * e) * sh.P + x), y = tile.v[e];
+                    if (x < P && r + ST::STEP * e < N) {
+                        const float4 u = sb.at((r + ST::STEP * e) * P + x), y = tile.v[e];
                         dot = fmaf(u.x, y.x, fmaf(u.y, y.y, fmaf(u.z, y.z, fmaf(u.w, y.w, dot))));
                     }
             }
             __syncthreads();
-            times_state<NP, 3, C, PD, ND, CN, false>(dk, base + M::V, base + M::S, block, colN, sl, sh.P, sh.N, lane);
-            times_state<NP, SP, C, ND, PD, CP, true>(dv, base + M::K, base + M::S, block, colP, sl, sh.N, sh.P, lane);
+            times_state<NP, 3, C, PD, ND, CN, false>(dk, base + M::V, base + M::S, block, colN, sl, P, N, lane);
+            times_state<NP, SP, C, ND, PD, CP, true>(dv, base + M::K, base + M::S, block, colP, sl, N, P, lane);
         }
         scale_rows(dk, d.out[r0], d.out[r0 + 8]);
         scale_rows(dv, d.out[r0], d.out[r0 + 8]);
-        own = dot_rows<NP, C, ND, CN>(dk, smem + M::K, block, colN, sh.N, lane);
+        own = dot_rows<NP, C, ND, CN>(dk, smem + M::K, block, colN, N, lane);
     }
     if (lane % 4 == 0) s_bk[part.share][r0] = own.x, s_bk[part.share][r0 + 8] = own.y;
     float wr[2] = {};  // sums of W over the tokens i
     if (on) {
-        const Rows<NP, C, ND> rk(base + M::K, block, sh.N, lane);
-        const Rows<NP, C, PD> rv(base + M::V, block, sh.P, lane);
+        const Rows<NP, C, ND> rk(base + M::K, block, N, lane);
+        const Rows<NP, C, PD> rv(base + M::V, block, P, lane);
         float row[2];
         row_factors<C, false>(row, d, block, scale, lane);
 #pragma unroll 1
         for (int o = block; o < last; ++o) {
             float sa_[2][4], sb_[2][4], m[2][4];
-            scores<NP, QP, C, ND>(sa_, rk, base + M::Q, o, sh.N, lane);   // k_j . q_i
-            scores<NP, QP, C, PD>(sb_, rv, base + M::DO, o, sh.P, lane);  // v_j . do_i
+            scores<NP, QP, C, ND>(sa_, rk, base + M::Q, o, N, lane);   // k_j . q_i
+            scores<NP, QP, C, PD>(sb_, rv, base + M::DO, o, P, lane);  // v_j . do_i
             pair_factors<C, false>(m, d, block, o, row, scale, lane);
             if (o == block) {
 #pragma unroll
@@ -802,8 +820,8 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
                 c0 += __shfl_xor_sync(0xffffffffu, c0, 4);
                 if (!(lane & 4) && part.share == 0) s_col[block][16 * o + (up ? 8 : 0) + 2 * (lane % 4) + (odd ? 1 : 0)] = c0;
             }
-            times_tokens<NP, SP, C, PD, CP>(dv, sa_, base + M::DO, colP, o, sh.P, lane);
-            times_tokens<NP, SP, C, ND, CN>(dk, sb_, base + M::Q, colN, o, sh.N, lane);
+            times_tokens<NP, SP, C, PD, CP>(dv, sa_, base + M::DO, colP, o, P, lane);
+            times_tokens<NP, SP, C, ND, CN>(dk, sb_, base + M::Q, colN, o, N, lane);
         }
     }
 #pragma unroll
@@ -817,11 +835,11 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
     if (lane == 0) s_dot[warp] = dot;
     __syncthreads();
     if (parts)
-        put_rows<float, ND, CN>(parts + pk + po + nq * ps, ps, dk, 1.f, nullptr, colN, sh.N, n - nq, rows - nq, lane);
+        put_rows<float, ND, CN>(parts + pk + po + nq * ps, ps, dk, 1.f, nullptr, colN, N, n - nq, rows - nq, lane);
     else
-        put_rows<E, ND, CN>(gk + ko + nq * ks, ks, dk, 1.f, smem + M::S + nq * pitch(ND), colN, sh.N, n - nq, rows - nq, lane);
+        put_rows<E, ND, CN>(gk + ko + nq * ks, ks, dk, 1.f, smem + M::S + nq * pitch(ND), colN, N, n - nq, rows - nq, lane);
     if (sizeof(E) == 2 && (ND != PD || !parts)) __syncthreads();  // (the stage's rows lie elsewhere now, or are still read)
-    put_rows<E, PD, CP>(gv + oo + nq * os, os, dv, 1.f, smem + M::S + nq * pitch(PD), colP, sh.P, n - nq, rows - nq, lane);
+    put_rows<E, PD, CP>(gv + oo + nq * os, os, dv, 1.f, smem + M::S + nq * pitch(PD), colP, P, n - nq, rows - nq, lane);
     if (warp == 0 && (ggp || gg_part)) {
         float all = 0.f;
         for (int i = 0; i < NT / 32; ++i) all += s_dot[i];
@@ -943,6 +961,9 @@ inline Shape shape_of(const LinattnArgs& a, int dirs) {
     sh.g_row = a.g_tokens ? a.T * a.H : 0;
     sh.g_tok = a.g_tokens ? a.H : 0;
     sh.scale = a.scale;
+    sh.by_h = Divisor::of((uint32_t)sh.H);
+    sh.by_nc = Divisor::of((uint32_t)sh.nc);
+    sh.by_slices = Divisor::of((uint32_t)((sh.P + 63) / 64));
     return sh;
 }
 
@@ -974,11 +995,11 @@ inline size_t scratch_bytes(const LinattnArgs& a, int dirs) {
     return scratch_of(a, dirs, nullptr, s);
 }
 
-template <typename E, int ND, int PD>
+template <typename E, int ND, int PD, bool FULL>
 cudaError_t run_states(const LinattnArgs& a, int dirs, const Scratch& w, const Shape& sh, cudaStream_t st) {
     constexpr int C = chunk_tokens<E, ND, PD>();
     using M = StatesSmem<E, ND, C>;
-    cudaError_t e = delta::allow<states_kernel<E, ND, C>>(M::BYTES);
+    cudaError_t e = delta::allow<states_kernel<E, ND, C, FULL>>(M::BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sh.BH * ((sh.P + 63) / 64), sh.nseg, dirs);
@@ -990,22 +1011,22 @@ cudaError_t run_states(const LinattnArgs& a, int dirs, const Scratch& w, const S
     attr.val.clusterDim.x = 1, attr.val.clusterDim.y = sh.nseg, attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, states_kernel<E, ND, C>, static_cast<const E*>(a.q), static_cast<const E*>(a.k),
+    return cudaLaunchKernelEx(&cfg, states_kernel<E, ND, C, FULL>, static_cast<const E*>(a.q), static_cast<const E*>(a.k),
                               static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.g, a.lens, a.h0, a.dh_final, a.h_final, a.gh0, w,
                               sh);
 }
 
-template <typename E, int ND, int PD>
+template <typename E, int ND, int PD, bool FULL>
 cudaError_t forward(const LinattnArgs& a, void* ws, cudaStream_t st) {
     constexpr int C = chunk_tokens<E, ND, PD>();
     using M = OutSmem<E, ND, PD, C>;
     const Shape sh = shape_of(a, 1);
     Scratch w;
     scratch_of(a, 1, ws, w);
-    cudaError_t e = run_states<E, ND, PD>(a, 1, w, sh, st);
-    if (e == cudaSuccess) e = delta::allow<out_kernel<E, ND, PD, C>>(M::BYTES);
+    cudaError_t e = run_states<E, ND, PD, FULL>(a, 1, w, sh, st);
+    if (e == cudaSuccess) e = delta::allow<out_kernel<E, ND, PD, C, FULL>>(M::BYTES);
     if (e != cudaSuccess) return e;
-    out_kernel<E, ND, PD, C><<<(unsigned)(sh.BH * sh.nc), NT, M::BYTES, st>>>(static_cast<const E*>(a.q), static_cast<const E*>(a.k),
+    out_kernel<E, ND, PD, C, FULL><<<(unsigned)(sh.BH * sh.nc), NT, M::BYTES, st>>>(static_cast<const E*>(a.q), static_cast<const E*>(a.k),
                                                                             static_cast<const E*>(a.v), a.lens, a.h0 != nullptr,
                                                                             static_cast<E*>(a.o), w, sh);
     return cudaGetLastError();
@@ -1013,7 +1034,7 @@ cudaError_t forward(const LinattnArgs& a, void* ws, cudaStream_t st) {
 
 inline size_t parts_bytes(const LinattnArgs& a) { return a.H == a.KH ? 0 : up((size_t)2 * a.Bz * a.T * a.H * a.N * 4); }
 
-template <typename E, int ND, int PD>
+template <typename E, int ND, int PD, bool FULL>
 cudaError_t backward(const LinattnArgs& a, void* ws, cudaStream_t st) {
     constexpr int C = chunk_tokens<E, ND, PD>();
     using M = GradSmem<E, ND, PD, C>;
@@ -1022,10 +1043,10 @@ cudaError_t backward(const LinattnArgs& a, void* ws, cudaStream_t st) {
     unsigned char* rest = static_cast<unsigned char*>(ws) + scratch_of(a, 2, ws, w);
     float* parts = parts_bytes(a) ? reinterpret_cast<float*>(rest) : nullptr;
     float* gg_part = a.gg && !a.g_tokens ? reinterpret_cast<float*>(rest + parts_bytes(a)) : nullptr;
-    cudaError_t e = run_states<E, ND, PD>(a, 2, w, sh, st);
-    if (e == cudaSuccess) e = delta::allow<grad_kernel<E, ND, PD, C>>(M::BYTES);
+    cudaError_t e = run_states<E, ND, PD, FULL>(a, 2, w, sh, st);
+    if (e == cudaSuccess) e = delta::allow<grad_kernel<E, ND, PD, C, FULL>>(M::BYTES);
     if (e != cudaSuccess) return e;
-    grad_kernel<E, ND, PD, C><<<(unsigned)(sh.BH * sh.nc), NT, M::BYTES, st>>>(
+    grad_kernel<E, ND, PD, C, FULL><<<(unsigned)(sh.BH * sh.nc), NT, M::BYTES, st>>>(
         static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.lens,
         a.h0 != nullptr, a.dh_final != nullptr, static_cast<E*>(a.gq), static_cast<E*>(a.gk), static_cast<E*>(a.gv), parts,
         a.g_tokens ? a.gg : nullptr, gg_part, w, sh);
@@ -1038,21 +1059,29 @@ cudaError_t backward(const LinattnArgs& a, void* ws, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-// Calls f with the widths' tiles (64 or 128 columns).
+// Calls f with the widths' tiles (64 or 128 columns) and whether the widths fill them: the kernels then have no
+// tests of columns (4 x 2048 x 24, 64/64: see the measurements at the head).
 template <typename F>
 cudaError_t by_widths(const LinattnArgs& a, F f) {
     using I64 = std::integral_constant<int, 64>;
     using I128 = std::integral_constant<int, 128>;
-    if (a.N <= 64) return a.P <= 64 ? f(I64(), I64()) : f(I64(), I128());
-    return a.P <= 64 ? f(I128(), I64()) : f(I128(), I128());
+    auto full = [&](auto n, auto p) {
+        return a.N == decltype(n)::value && a.P == decltype(p)::value ? f(n, p, std::true_type()) : f(n, p, std::false_type());
+    };
+    if (a.N <= 64) return a.P <= 64 ? full(I64(), I64()) : full(I64(), I128());
+    return a.P <= 64 ? full(I128(), I64()) : full(I128(), I128());
 }
 template <typename E>
 cudaError_t forward_of(const LinattnArgs& a, void* ws, cudaStream_t st) {
-    return by_widths(a, [&](auto n, auto p) { return forward<E, decltype(n)::value, decltype(p)::value>(a, ws, st); });
+    return by_widths(a, [&](auto n, auto p, auto full) {
+        return forward<E, decltype(n)::value, decltype(p)::value, decltype(full)::value>(a, ws, st);
+    });
 }
 template <typename E>
 cudaError_t backward_of(const LinattnArgs& a, void* ws, cudaStream_t st) {
-    return by_widths(a, [&](auto n, auto p) { return backward<E, decltype(n)::value, decltype(p)::value>(a, ws, st); });
+    return by_widths(a, [&](auto n, auto p, auto full) {
+        return backward<E, decltype(n)::value, decltype(p)::value, decltype(full)::value>(a, ws, st);
+    });
 }
 
 }  // namespace
