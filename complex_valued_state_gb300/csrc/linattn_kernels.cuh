@@ -324,38 +324,40 @@ struct StateTile {
 };
 
 // --------------------------------------------------------------- states
-// A CTA has 64 columns p of a state (its columns never mix), a warp 16 rows n of them in registers, and takes
-// every token's decayed key (three planes) times its value.  Tokens come 64 at a time, bfloat16 ones two stages
-// ahead; the decays of eight chunks are made at once, a warp each.
-template <typename E, int ND, int C>
+// A CTA has 64 x 64 of a state (which never mix with the others), a warp 16 rows n of them in registers, and
+// takes every token's decayed key (three planes) times its value.  Tokens come 64 at a time, bfloat16 ones two
+// stages ahead; the decays of eight chunks are made at once, a warp each.
+template <typename E, int C>
 struct StatesSmem {
     static constexpr int NP = Type<E>::NP, HT = imin(C, 64), STAGES = NP == 1 ? 3 : 2, BATCH = 8;
-    static constexpr int X = NP * HT * pitch(ND), Y = NP * HT * pitch(64);
+    static constexpr int X = NP * HT * pitch(64), Y = X;
     static constexpr int W = STAGES * (X + Y), BYTES = W + 4 * BATCH * (C + 4);
-    static constexpr int THREADS = 2 * ND;
+    static constexpr int THREADS = 128;
 };
 
-template <typename E, int ND, int C, bool FULL>
-__global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v,
+template <typename E, int C, bool FULL>
+__global__ void __launch_bounds__(128) states_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v,
                                                         const E* __restrict__ dout, const float* __restrict__ g,
                                                         const int* __restrict__ lens, const float* h0, const float* dh_final,
                                                         float* h_final, float* gh0, Scratch w, Shape sh) {
-    using M = StatesSmem<E, ND, C>;
+    using M = StatesSmem<E, C>;
     constexpr int NP = M::NP, THREADS = M::THREADS, HT = M::HT, HALVES = C / HT, STAGES = M::STAGES, BATCH = M::BATCH;
     extern __shared__ __align__(128) unsigned char smem[];
     float* weights = reinterpret_cast<float*>(smem + M::W);  // [BATCH][C]
     float* totals = weights + BATCH * C;                     // [BATCH]
+    delta::let_next_start();  // (the kernel behind this one waits for its end before it reads what it leaves)
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int N = FULL ? ND : sh.N, P = sh.P, s = blockIdx.y, dir = blockIdx.z;
+    const int N = sh.N, P = sh.P, s = blockIdx.y, dir = blockIdx.z;
     int slice, h;
     const int bh = sh.by_slices.div(blockIdx.x, slice), b = sh.by_h.div(bh, h), slices = (int)sh.by_slices.d;
-    const int p0 = 64 * slice, cols = FULL ? 64 : min(64, P - p0), KH = sh.H / sh.G;
+    const int across = P > 64 ? 2 : 1, p0 = 64 * (slice % across), m0 = 64 * (slice / across), KH = sh.H / sh.G;
+    const int cols = FULL ? 64 : min(64, P - p0), own = FULL ? 64 : min(64, N - m0);  // of this CTA
     const int len = row_len(lens, b, sh.T), live = (len + C - 1) / C;
     const int w0 = s * sh.seg, w1 = min(w0 + sh.seg, live);
     const int64_t np = (int64_t)N * P, row = (int64_t)dir * sh.BH + bh;
     const int n0 = 16 * warp;
-    const bool mine = n0 < N, first = tid == 0 && p0 == 0;
-    const E* xs = (dir ? q : k) + (int64_t)(h / sh.G) * N;
+    const bool mine = n0 < own, first = tid == 0 && slice == 0;
+    const E* xs = (dir ? q : k) + (int64_t)(h / sh.G) * N + m0;
     const E* ys = (dir ? dout : v) + (int64_t)h * P + p0;
     const int64_t xst = (int64_t)KH * N, yst = (int64_t)sh.H * P;
     const float* gs = g + b * sh.g_row + h;
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
         if (i < w1) {
             const int64_t t0 = (int64_t)b * sh.T + min(at0, len - 1);  // (a half without tokens reads nothing)
             unsigned char* at = smem + t % STAGES * (M::X + M::Y);
-            load_tile<E, ND, HT, THREADS>(at, HT * pitch(ND), xs + t0 * xst, xst, len - at0, N, tid);
+            load_tile<E, 64, HT, THREADS>(at, HT * pitch(64), xs + t0 * xst, xst, len - at0, own, tid);
             load_tile<E, 64, HT, THREADS>(at + M::X, HT * pitch(64), ys + t0 * yst, yst, len - at0, cols, tid);
         }
         if (NP == 1) cp_commit();
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
                 const int p = 8 * nt + 2 * (lane % 4);
-                if (p < cols) f((int64_t)(n0 + lane / 4 + 4 * e) * P + p0 + p, st[nt][e], st[nt][e + 1]);
+                if (p < cols) f((int64_t)(m0 + n0 + lane / 4 + 4 * e) * P + p0 + p, st[nt][e], st[nt][e + 1]);
             }
     };
 #pragma unroll
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
                 for (int e = 0; e < Sums<C>::K; ++e)
                     weights[j * C + Sums<C>::K * lane + e] = dir ? sh.scale * exp_of(G.G[e]) : exp_between(G.end, G.G[e]);
                 if (lane == 0) totals[j] = exp_of(G.end);
-                if (dir == 0 && p0 == 0) put_decays(static_cast<Decays<C>*>(w.decays)[(int64_t)bh * sh.nc + c], G, lane);
+                if (dir == 0 && slice == 0) put_decays(static_cast<Decays<C>*>(w.decays)[(int64_t)bh * sh.nc + c], G, lane);
             }
             __syncthreads();
         }
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
             for (int kt = 0; kt < HT / 16; ++kt) {
                 uint32_t raw[NP][4], a[3][4];
 #pragma unroll
-                for (int z = 0; z < NP; ++z) ldsm_t(raw[z], lane_at<true>(x + z * HT * pitch(ND), pitch(ND), 16 * kt, n0, lane));
+                for (int z = 0; z < NP; ++z) ldsm_t(raw[z], lane_at<true>(x + z * HT * pitch(64), pitch(64), 16 * kt, n0, lane));
                 const float2 u0 = *reinterpret_cast<const float2*>(wt + half * HT + 16 * kt + 2 * (lane % 4));
                 const float2 u1 = *reinterpret_cast<const float2*>(wt + half * HT + 16 * kt + 8 + 2 * (lane % 4));
 #pragma unroll
@@ -480,32 +482,37 @@ __global__ void __launch_bounds__(2 * ND) states_kernel(const E* __restrict__ q,
     float* ends = w.ends + row * sh.nseg * np;
     if (mine) each([&](int64_t at, float x, float y) { *reinterpret_cast<float2*>(ends + s * np + at) = make_float2(x, y); });
     if (tid == 0) w.seg_all[(row * slices + slice) * sh.nseg + s] = all;
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (!mine) return;
-    const float* alls = w.seg_all + (row * slices + slice) * sh.nseg;
-    const bool ends_row = s == max((live + sh.seg - 1) / sh.seg - 1, 0);  // the row's last segment
-    float decay[kMostSegments];  // from the end of segment e to this one's start
-    float d = 1.f;
+    auto cluster_sync = [] { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); };
+    cluster_sync();
+    if (mine) {
+        const float* alls = w.seg_all + (row * slices + slice) * sh.nseg;
+        float decay[kMostSegments];  // from the end of segment e to this one's start
+        float d = 1.f;
 #pragma unroll
-    for (int e = kMostSegments - 1; e >= 0; --e) {
-        decay[e] = e < s ? d : 0.f;
-        if (e < s) d *= __ldcg(alls + e);
-    }
-    each([&](int64_t at, float& x, float& y) {
-        float2 r = make_float2(0.f, 0.f);
-        if (start) {
-            const float2 a = *reinterpret_cast<const float2*>(start + bh * np + at);
-            r.x = d * a.x, r.y = d * a.y;
+        for (int e = kMostSegments - 1; e >= 0; --e) {
+            decay[e] = e < s ? d : 0.f;
+            if (e < s) d *= __ldcg(alls + e);
         }
-#pragma unroll
-        for (int e = 0; e < kMostSegments; ++e)
-            if (e < s) {
-                const float2 a = __ldcg(reinterpret_cast<const float2*>(ends + e * np + at));
-                r.x = fmaf(decay[e], a.x, r.x), r.y = fmaf(decay[e], a.y, r.y);
+        each([&](int64_t at, float& x, float& y) {
+            float2 r = make_float2(0.f, 0.f);
+            if (start) {
+                const float2 a = *reinterpret_cast<const float2*>(start + bh * np + at);
+                r.x = d * a.x, r.y = d * a.y;
             }
-        if (s > 0 || start) *reinterpret_cast<float2*>(w.starts + (row * sh.nseg + s) * np + at) = r;
-        if (ends_row && last) *reinterpret_cast<float2*>(last + bh * np + at) = make_float2(fmaf(all, r.x, x), fmaf(all, r.y, y));
-    });
+#pragma unroll
+            for (int e = 0; e < kMostSegments; ++e)
+                if (e < s) {
+                    const float2 a = __ldcg(reinterpret_cast<const float2*>(ends + e * np + at));
+                    r.x = fmaf(decay[e], a.x, r.x), r.y = fmaf(decay[e], a.y, r.y);
+                }
+            if (s > 0 || start) *reinterpret_cast<float2*>(w.starts + (row * sh.nseg + s) * np + at) = r;
+            x = fmaf(all, r.x, x), y = fmaf(all, r.y, y);
+        });
+    }
+    if (!last) return;
+    if (start) cluster_sync();  // (the last state may lie over the first)
+    if (mine && s == max((live + sh.seg - 1) / sh.seg - 1, 0))  // the row's last segment
+        each([&](int64_t at, float x, float y) { *reinterpret_cast<float2*>(last + bh * np + at) = make_float2(x, y); });
 }
 
 // --------------------------------------------------------------- outputs
@@ -585,12 +592,16 @@ __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
     const int len = row_len(lens, b, sh.T), live = (len + C - 1) / C, n = min(len - c * C, C), rows = min(sh.T - c * C, C);
     const int64_t t0 = (int64_t)b * sh.T + (int64_t)c * C, bh = (int64_t)b * sh.H + h, os = (int64_t)sh.H * P;
     E* orow = o + t0 * os + (int64_t)h * P;
-    if (n <= 0) return clear_rows(orow, os, P, rows, tid);
+    if (n <= 0) {
+        delta::wait_for_previous();  // (no block writes or ends before the kernel before this one has)
+        return clear_rows(orow, os, P, rows, tid);
+    }
     const int64_t ks = (int64_t)KH * N, ko = t0 * ks + (int64_t)(h / sh.G) * N;
-    load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, M::TABLE, tid);
     load_tile<E, ND, C, NT>(smem + M::Q, C * pitch(ND), q + ko, ks, n, N, tid);
     load_tile<E, ND, C, NT>(smem + M::K, C * pitch(ND), k + ko, ks, n, N, tid);
     load_tile<E, PD, C, NT>(smem + M::V, C * pitch(PD), v + t0 * os + (int64_t)h * P, os, n, P, tid);
+    delta::wait_for_previous();  // (from here on: what the states' walk left)
+    load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, M::TABLE, tid);
     cp_commit();
     const StateAt st = state_at(w, sh, 0, bh, c, live, start);
     StateTile<SP, PD> tile;
@@ -693,6 +704,7 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
     const int64_t ps = (int64_t)sh.H * N, po = t0 * ps + (int64_t)h * N, pk = (int64_t)(gridDim.x / (sh.nc * sh.H)) * sh.T * ps;
     float* ggp = gg ? gg + t0 * sh.H + h : nullptr;
     if (n <= 0) {
+        delta::wait_for_previous();  // (no block writes or ends before the kernel before this one has)
         clear_rows(gv + oo, os, P, rows, tid);
         if (parts) {
             clear_rows(parts + po, ps, N, rows, tid);
@@ -706,11 +718,12 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
         if (gg_part && tid == 0) gg_part[blockIdx.x] = 0.f;
         return;
     }
-    load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, sizeof(Decays<C>), tid);
     load_tile<E, PD, C, NT>(smem + M::DO, C * pitch(PD), dout + oo, os, n, P, tid);
     load_tile<E, PD, C, NT>(smem + M::V, C * pitch(PD), v + oo, os, n, P, tid);
     load_tile<E, ND, C, NT>(smem + M::K, C * pitch(ND), k + ko, ks, n, N, tid);
     load_tile<E, ND, C, NT>(smem + M::Q, C * pitch(ND), q + ko, ks, n, N, tid);
+    delta::wait_for_previous();  // (from here on: what the states' walk left)
+    load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, sizeof(Decays<C>), tid);
     cp_commit();
     const StateAt sb = state_at(w, sh, 0, bh, c, live, start), sa = state_at(w, sh, 1, bh, c, live, end);
     StateTile<3, PD> tile;
@@ -945,7 +958,8 @@ inline size_t decays_bytes(const LinattnArgs& a) {
     return C == 128 ? sizeof(Decays<128>) : C == 64 ? sizeof(Decays<64>) : sizeof(Decays<32>);
 }
 
-constexpr int kStateCtas = 304;  // CTAs that the states' walk aims at: two an SM
+constexpr int kStateCtas = 456;  // CTAs that the states' walk aims at: three an SM
+inline int slices_of(const LinattnArgs& a) { return (a.N > 64 ? 2 : 1) * (a.P > 64 ? 2 : 1); }
 
 inline Shape shape_of(const LinattnArgs& a, int dirs) {
     Shape sh{};
@@ -953,7 +967,7 @@ inline Shape shape_of(const LinattnArgs& a, int dirs) {
     sh.T = (int)a.T, sh.H = (int)a.H, sh.G = (int)(a.H / a.KH), sh.N = (int)a.N, sh.P = (int)a.P;
     sh.nc = (int)((a.T + C - 1) / C);
     sh.BH = (int)(a.Bz * a.H);
-    const int64_t rows = a.Bz * a.H * dirs * ((a.P + 63) / 64);
+    const int64_t rows = a.Bz * a.H * dirs * slices_of(a);
     int64_t want = rows >= kStateCtas ? 1 : kStateCtas / rows;
     if (want > kMostSegments) want = kMostSegments;
     sh.seg = (int)((sh.nc + want - 1) / want);
@@ -963,7 +977,7 @@ inline Shape shape_of(const LinattnArgs& a, int dirs) {
     sh.scale = a.scale;
     sh.by_h = Divisor::of((uint32_t)sh.H);
     sh.by_nc = Divisor::of((uint32_t)sh.nc);
-    sh.by_slices = Divisor::of((uint32_t)((sh.P + 63) / 64));
+    sh.by_slices = Divisor::of((uint32_t)slices_of(a));
     return sh;
 }
 
@@ -985,7 +999,7 @@ inline size_t scratch_of(const LinattnArgs& a, int dirs, void* ws, Scratch& s) {
     if (sh.nseg > 1) {
         s.ends = take(rows * sh.nseg * np);
         s.starts = take(rows * sh.nseg * np);
-        s.seg_all = take(rows * ((sh.P + 63) / 64) * sh.nseg * 4);
+        s.seg_all = take(rows * slices_of(a) * sh.nseg * 4);
         s.dec = take(rows * sh.nc * 4);
     }
     return at;
@@ -995,14 +1009,13 @@ inline size_t scratch_bytes(const LinattnArgs& a, int dirs) {
     return scratch_of(a, dirs, nullptr, s);
 }
 
-template <typename E, int ND, int PD, bool FULL>
+template <typename E, int C, bool FULL>
 cudaError_t run_states(const LinattnArgs& a, int dirs, const Scratch& w, const Shape& sh, cudaStream_t st) {
-    constexpr int C = chunk_tokens<E, ND, PD>();
-    using M = StatesSmem<E, ND, C>;
-    cudaError_t e = delta::allow<states_kernel<E, ND, C, FULL>>(M::BYTES);
+    using M = StatesSmem<E, C>;
+    cudaError_t e = delta::allow<states_kernel<E, C, FULL>>(M::BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sh.BH * ((sh.P + 63) / 64), sh.nseg, dirs);
+    cfg.gridDim = dim3(sh.BH * slices_of(a), sh.nseg, dirs);
     cfg.blockDim = dim3(M::THREADS);
     cfg.dynamicSmemBytes = M::BYTES;
     cfg.stream = st;
@@ -1011,9 +1024,25 @@ cudaError_t run_states(const LinattnArgs& a, int dirs, const Scratch& w, const S
     attr.val.clusterDim.x = 1, attr.val.clusterDim.y = sh.nseg, attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, states_kernel<E, ND, C, FULL>, static_cast<const E*>(a.q), static_cast<const E*>(a.k),
+    return cudaLaunchKernelEx(&cfg, states_kernel<E, C, FULL>, static_cast<const E*>(a.q), static_cast<const E*>(a.k),
                               static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.g, a.lens, a.h0, a.dh_final, a.h_final, a.gh0, w,
                               sh);
+}
+
+// Launches a kernel that may start while the one before it in the stream still runs.
+template <typename... A, typename... B>
+cudaError_t launch_behind(void (*kernel)(A...), unsigned grid, int bytes, cudaStream_t st, B... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<A>(args)...);
 }
 
 template <typename E, int ND, int PD, bool FULL>
@@ -1023,13 +1052,11 @@ cudaError_t forward(const LinattnArgs& a, void* ws, cudaStream_t st) {
     const Shape sh = shape_of(a, 1);
     Scratch w;
     scratch_of(a, 1, ws, w);
-    cudaError_t e = run_states<E, ND, PD, FULL>(a, 1, w, sh, st);
+    cudaError_t e = run_states<E, C, FULL>(a, 1, w, sh, st);
     if (e == cudaSuccess) e = delta::allow<out_kernel<E, ND, PD, C, FULL>>(M::BYTES);
     if (e != cudaSuccess) return e;
-    out_kernel<E, ND, PD, C, FULL><<<(unsigned)(sh.BH * sh.nc), NT, M::BYTES, st>>>(static_cast<const E*>(a.q), static_cast<const E*>(a.k),
-                                                                            static_cast<const E*>(a.v), a.lens, a.h0 != nullptr,
-                                                                            static_cast<E*>(a.o), w, sh);
-    return cudaGetLastError();
+    return launch_behind(out_kernel<E, ND, PD, C, FULL>, (unsigned)(sh.BH * sh.nc), M::BYTES, st, static_cast<const E*>(a.q),
+                         static_cast<const E*>(a.k), static_cast<const E*>(a.v), a.lens, a.h0 != nullptr, static_cast<E*>(a.o), w, sh);
 }
 
 inline size_t parts_bytes(const LinattnArgs& a) { return a.H == a.KH ? 0 : up((size_t)2 * a.Bz * a.T * a.H * a.N * 4); }
@@ -1043,13 +1070,14 @@ cudaError_t backward(const LinattnArgs& a, void* ws, cudaStream_t st) {
     unsigned char* rest = static_cast<unsigned char*>(ws) + scratch_of(a, 2, ws, w);
     float* parts = parts_bytes(a) ? reinterpret_cast<float*>(rest) : nullptr;
     float* gg_part = a.gg && !a.g_tokens ? reinterpret_cast<float*>(rest + parts_bytes(a)) : nullptr;
-    cudaError_t e = run_states<E, ND, PD, FULL>(a, 2, w, sh, st);
+    cudaError_t e = run_states<E, C, FULL>(a, 2, w, sh, st);
     if (e == cudaSuccess) e = delta::allow<grad_kernel<E, ND, PD, C, FULL>>(M::BYTES);
     if (e != cudaSuccess) return e;
-    grad_kernel<E, ND, PD, C, FULL><<<(unsigned)(sh.BH * sh.nc), NT, M::BYTES, st>>>(
-        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.lens,
-        a.h0 != nullptr, a.dh_final != nullptr, static_cast<E*>(a.gq), static_cast<E*>(a.gk), static_cast<E*>(a.gv), parts,
-        a.g_tokens ? a.gg : nullptr, gg_part, w, sh);
+    e = launch_behind(grad_kernel<E, ND, PD, C, FULL>, (unsigned)(sh.BH * sh.nc), M::BYTES, st, static_cast<const E*>(a.q),
+                      static_cast<const E*>(a.k), static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.lens, a.h0 != nullptr,
+                      a.dh_final != nullptr, static_cast<E*>(a.gq), static_cast<E*>(a.gk), static_cast<E*>(a.gv), parts,
+                      a.g_tokens ? a.gg : nullptr, gg_part, w, sh);
+    if (e != cudaSuccess) return e;
     if (parts) {
         const int64_t vectors = a.Bz * a.T * a.KH * (a.N / 4);
         join_kernel<E><<<dim3((unsigned)((vectors + 255) / 256), 2), 256, 0, st>>>(parts, static_cast<E*>(a.gq), static_cast<E*>(a.gk),

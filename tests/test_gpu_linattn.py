@@ -408,3 +408,19 @@ def test_errors_are_roundings(cs):
     assert off(h, wh) < 1e-6 and off(r["gh0"], w["gh0"]) < 1e-6 and off(r["gg"], w["gg"]) < 1e-6
     for x, y in ((o, wo), (r["gq"], w["gq"]), (r["gk"], w["gk"]), (r["gv"], w["gv"])):
         assert off(x, y) < 2.0 ** -9
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("NP", [(64, 64), (128, 128), (96, 80)])
+def test_states_in_place(cs, NP, dtype):
+    """The last state over the first one, and gh0 over dh_final, where a row's walk is cut into segments (few
+    heads, many chunks) that all read the first one."""
+    d, opt, back = make(19, 1, 1100, 1, 1, *NP, dtype=dtype, state=True)
+    g, b, h0 = on(d), on(back), opt["h0"].cuda()
+    o, h = cs.linattn_forward(**g, h0=h0)
+    r = cs.linattn_backward(**g, **b, h0=h0)
+    for _ in range(20):
+        state, dh = h0.clone(), b["dh_final"].clone()
+        o2, _ = cs.linattn_forward(**g, h0=state, h_final=state)
+        cs.linattn_backward(**g, do=b["do"], dh_final=dh, h0=h0, grads={"gh0": dh})
+        assert torch.equal(o, o2) and torch.equal(h, state) and torch.equal(r["gh0"], dh)
