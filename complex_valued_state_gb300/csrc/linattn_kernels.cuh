@@ -91,25 +91,31 @@ __device__ __forceinline__ void times_state(float (&acc)[CW / 8][4], uint32_t a,
         uint32_t af[NPL][4];
 #pragma unroll
         for (int i = 0; i < NPL; ++i) ldsm(af[i], lane_at<false>(a + i * C * pitch(KW), pitch(KW), 16 * block, k0 + 16 * kt, lane));
+        // (columns inside: a sum is added to again only after all the others)
 #pragma unroll
-        for (int nt = 0; nt < CW / 16; ++nt) {
-            const int col = col0 + 16 * nt;
-            if (col >= ow) break;
-            if (!TRANS && col / 64 != sl) continue;
+        for (int j = SP - 1; j >= 0; --j) {
+            uint32_t bf[CW / 16][4];
 #pragma unroll
-            for (int j = SP - 1; j >= 0; --j) {
-                uint32_t bf[4];
+            for (int nt = 0; nt < CW / 16; ++nt) {
+                const int col = col0 + 16 * nt;
+                if (col >= ow) break;
+                if (!TRANS && col / 64 != sl) continue;
                 if (TRANS)
-                    ldsm_t(bf, lane_at<false>(s + j * 64 * SPITCH, SPITCH, 16 * kt, col, lane));
+                    ldsm_t(bf[nt], lane_at<false>(s + j * 64 * SPITCH, SPITCH, 16 * kt, col, lane));
                 else
-                    ldsm(bf, lane_at<true>(s + j * 64 * SPITCH, SPITCH, col % 64, 16 * kt, lane));
-#pragma unroll
-                for (int i = NPL - 1; i >= 0; --i)
-                    if (i + j < SP) {
-                        mma(acc[2 * nt], af[i], bf[0], bf[1]);
-                        mma(acc[2 * nt + 1], af[i], bf[2], bf[3]);
-                    }
+                    ldsm(bf[nt], lane_at<true>(s + j * 64 * SPITCH, SPITCH, col % 64, 16 * kt, lane));
             }
+#pragma unroll
+            for (int i = NPL - 1; i >= 0; --i)
+                if (i + j < SP)
+#pragma unroll
+                    for (int nt = 0; nt < CW / 16; ++nt) {
+                        const int col = col0 + 16 * nt;
+                        if (col >= ow) break;
+                        if (!TRANS && col / 64 != sl) continue;
+                        mma(acc[2 * nt], af[i], bf[nt][0], bf[nt][1]);
+                        mma(acc[2 * nt + 1], af[i], bf[nt][2], bf[nt][3]);
+                    }
         }
     }
 }
@@ -175,11 +181,11 @@ __device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW>
 }
 // The factors scale M of a block's pairs: the warp's rows (the later tokens if LOWER, else the earlier ones) with
 // the tokens of block `o`; 0 where the pair is none.  `row`: scale times the rows' own factors.
-template <int C, bool LOWER>
+template <int C, bool LOWER, bool DIAG>
 __device__ __forceinline__ void pair_factors(float (&m)[2][4], const Decays<C>& d, int block, int o, const float (&row)[2], float scale,
                                              int lane) {
     const int c0 = 16 * o + 2 * (lane % 4);
-    if (o != block) {
+    if constexpr (!DIAG) {
         const float x = LOWER ? d.x[o][block] : d.x[block][o];
         const f2 r0 = mk2(row[0] * x, row[0] * x), r1 = mk2(row[1] * x, row[1] * x);
 #pragma unroll
@@ -223,21 +229,25 @@ __device__ __forceinline__ void times_tokens(float (&acc)[CW / 8][4], const floa
         for (int i = 0; i < PP; ++i) p[i][u] = w[i];
     }
     const uint32_t at = lane_at<false>(z, pitch(OW), 16 * o, col0, lane);
+    constexpr int NG = imin(CW / 16, 4);  // 64 columns at a time
 #pragma unroll
-    for (int nt = 0; nt < CW / 16; ++nt) {
-        if (col0 + 16 * nt >= ow) break;
+    for (int n0 = 0; n0 < CW / 16; n0 += NG)
 #pragma unroll
         for (int j = NPL - 1; j >= 0; --j) {
-            uint32_t bf[4];
-            ldsm_t(bf, at + j * C * pitch(OW) + 32 * nt);
+            uint32_t bf[NG][4];
+#pragma unroll
+            for (int nt = 0; nt < NG; ++nt)
+                if (col0 + 16 * (n0 + nt) < ow) ldsm_t(bf[nt], at + j * C * pitch(OW) + 32 * (n0 + nt));
 #pragma unroll
             for (int i = PP - 1; i >= 0; --i)
-                if (i + j < PP) {
-                    mma(acc[2 * nt], p[i], bf[0], bf[1]);
-                    mma(acc[2 * nt + 1], p[i], bf[2], bf[3]);
-                }
+                if (i + j < PP)
+#pragma unroll
+                    for (int nt = 0; nt < NG; ++nt)
+                        if (col0 + 16 * (n0 + nt) < ow) {
+                            mma(acc[2 * (n0 + nt)], p[i], bf[nt][0], bf[nt][1]);
+                            mma(acc[2 * (n0 + nt) + 1], p[i], bf[nt][2], bf[nt][3]);
+                        }
         }
-    }
 }
 // acc = sum over the blocks at or before the warp's of (A B^T, decayed) Z.
 template <int NPL, int QP, int PP, int C, int KW, int OW, int CW>
@@ -246,12 +256,12 @@ __device__ __forceinline__ void earlier_pairs(float (&acc)[CW / 8][4], uint32_t 
     const Rows<NPL, C, KW> rows(a, block, kw, lane);
     float row[2];
     row_factors<C, true>(row, d, block, scale, lane);
-#pragma unroll 1
-    for (int o = 0; o <= block; ++o) {
+    auto with = [&](int o, auto diag) {
+        constexpr bool DIAG = decltype(diag)::value;
         float sc[2][4], m[2][4];
         scores<NPL, QP, C, KW>(sc, rows, b, o, kw, lane);
-        pair_factors<C, true>(m, d, block, o, row, scale, lane);
-        if (o == block) {  // (a score that is not wanted may be anything)
+        pair_factors<C, true, DIAG>(m, d, block, o, row, scale, lane);
+        if constexpr (DIAG) {  // (a score that is not wanted may be anything)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -259,7 +269,10 @@ __device__ __forceinline__ void earlier_pairs(float (&acc)[CW / 8][4], uint32_t 
         }
         multiply(sc, m);
         times_tokens<NPL, PP, C, OW, CW>(acc, sc, z, col0, o, ow, lane);
-    }
+    };
+#pragma unroll 1
+    for (int o = 0; o < block; ++o) with(o, std::false_type());
+    with(block, std::true_type());
 }
 template <int N>
 __device__ __forceinline__ void scale_rows(float (&acc)[N][4], float f0, float f1) {
@@ -445,24 +458,22 @@ __global__ void __launch_bounds__(128) states_kernel(const E* __restrict__ q, co
                     a[0][r] = pl[0], a[1][r] = pl[1], a[2][r] = pl[2];
                 }
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    if (16 * nt >= cols) break;
+                for (int j = NP - 1; j >= 0; --j) {
+                    uint32_t bf[4][4];
 #pragma unroll
-                    for (int j = NP - 1; j >= 0; --j) {
-                        uint32_t bf[4];
-                        ldsm_t(bf, lane_at<false>(y + j * HT * pitch(64), pitch(64), 16 * kt, 16 * nt, lane));
+                    for (int nt = 0; nt < 4; ++nt)
+                        if (16 * nt < cols) ldsm_t(bf[nt], lane_at<false>(y + j * HT * pitch(64), pitch(64), 16 * kt, 16 * nt, lane));
 #pragma unroll
-                        for (int z = 2; z >= 0; --z)
-                            if (z + j < 3) {
-                                if (z + j == 0) {
-                                    mma(big[2 * nt], a[z], bf[0], bf[1]);
-                                    mma(big[2 * nt + 1], a[z], bf[2], bf[3]);
-                                } else {
-                                    mma(rest[2 * nt], a[z], bf[0], bf[1]);
-                                    mma(rest[2 * nt + 1], a[z], bf[2], bf[3]);
+                    for (int z = 2; z >= 0; --z)
+                        if (z + j < 3)
+#pragma unroll
+                            for (int nt = 0; nt < 4; ++nt)
+                                if (16 * nt < cols) {
+                                    float(&c0)[4] = z + j == 0 ? big[2 * nt] : rest[2 * nt];
+                                    float(&c1)[4] = z + j == 0 ? big[2 * nt + 1] : rest[2 * nt + 1];
+                                    mma(c0, a[z], bf[nt][0], bf[nt][1]);
+                                    mma(c1, a[z], bf[nt][2], bf[nt][3]);
                                 }
-                            }
-                    }
                 }
             }
         }
@@ -806,8 +817,10 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
             float sa_[2][4], sb_[2][4], m[2][4];
             scores<NP, QP, C, ND>(sa_, rk, base + M::Q, o, N, lane);   // k_j . q_i
             scores<NP, QP, C, PD>(sb_, rv, base + M::DO, o, P, lane);  // v_j . do_i
-            pair_factors<C, false>(m, d, block, o, row, scale, lane);
-            if (o == block) {
+            if (o != block) {
+                pair_factors<C, false, false>(m, d, block, o, row, scale, lane);
+            } else {
+                pair_factors<C, false, true>(m, d, block, o, row, scale, lane);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
