@@ -4,7 +4,6 @@
 #pragma once
 
 #include "delta_common.cuh"
-#include "pairs.cuh"
 
 namespace cssd {
 namespace linattn {

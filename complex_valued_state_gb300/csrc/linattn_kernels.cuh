@@ -187,12 +187,11 @@ __device__ __forceinline__ void pair_factors(float (&m)[2][4], const Decays<C>& 
     const int c0 = 16 * o + 2 * (lane % 4);
     if constexpr (!DIAG) {
         const float x = LOWER ? d.x[o][block] : d.x[block][o];
-        const f2 r0 = mk2(row[0] * x, row[0] * x), r1 = mk2(row[1] * x, row[1] * x);
+        const float x0 = row[0] * x, x1 = row[1] * x;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const f2 c = *reinterpret_cast<const f2*>((LOWER ? d.f : d.e) + c0 + 8 * h);
-            un2(mul2(r0, c), m[h][0], m[h][1]);
-            un2(mul2(r1, c), m[h][2], m[h][3]);
+            const float2 c = *reinterpret_cast<const float2*>((LOWER ? d.f : d.e) + c0 + 8 * h);
+            m[h][0] = x0 * c.x, m[h][1] = x0 * c.y, m[h][2] = x1 * c.x, m[h][3] = x1 * c.y;
         }
     } else {
         const int r0 = 16 * block + lane / 4;
@@ -214,7 +213,7 @@ __device__ __forceinline__ void multiply(float (&sc)[2][4], const float (&m)[2][
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) un2(mul2(mk2(sc[h][e], sc[h][e + 1]), mk2(m[h][e], m[h][e + 1])), sc[h][e], sc[h][e + 1]);
+        for (int e = 0; e < 4; ++e) sc[h][e] *= m[h][e];
 }
 // acc += P Z for columns col0.. of Z's 16 tokens of block `o`; the scores P, split in PP planes, are the operand as
 // they lie.
