@@ -305,8 +305,8 @@ __device__ __forceinline__ StateAt state_at(const Scratch& w, const Shape& sh, i
     const int s = walk / sh.seg;
     if (walk % sh.seg == 0) r.own = nullptr;
     if (s > 0 || start) {
-        r.seg = w.starts + (row * sh.nseg + s) * np;
         r.dec = w.dec[row * sh.nc + c];
+        if (r.dec != 0.f) r.seg = w.starts + (row * sh.nseg + s) * np;  // (else nothing is left of it; NaN is not 0)
     }
     return r;
 }
@@ -970,7 +970,7 @@ inline size_t decays_bytes(const LinattnArgs& a) {
     return C == 128 ? sizeof(Decays<128>) : C == 64 ? sizeof(Decays<64>) : sizeof(Decays<32>);
 }
 
-constexpr int kStateCtas = 456;  // CTAs that the states' walk aims at: three an SM
+constexpr int kStateCtas = 384;  // CTAs that the states' walk may have (up to three an SM are resident)
 inline int slices_of(const LinattnArgs& a) { return (a.N > 64 ? 2 : 1) * (a.P > 64 ? 2 : 1); }
 
 inline Shape shape_of(const LinattnArgs& a, int dirs) {
