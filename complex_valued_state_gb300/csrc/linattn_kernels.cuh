@@ -496,28 +496,42 @@ __global__ void __launch_bounds__(128) states_kernel(const E* __restrict__ q, co
     cluster_sync();
     if (mine) {
         const float* alls = w.seg_all + (row * slices + slice) * sh.nseg;
-        float decay[kMostSegments];  // from the end of segment e to this one's start
+        float r[8][4] = {};  // the state before this segment: from the nearest one back
+        auto add = [&](const float* from, float d) {  // (all loads before the sums)
+            float2 a[16];
+            int i = 0;
+            each([&](int64_t at, float&, float&) { a[i++] = __ldcg(reinterpret_cast<const float2*>(from + at)); });
+            i = 0;
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2)
+                    if (8 * nt + 2 * (lane % 4) < cols) {
+                        r[nt][e] = fmaf(d, a[i].x, r[nt][e]), r[nt][e + 1] = fmaf(d, a[i].y, r[nt][e + 1]);
+                        ++i;
+                    }
+        };
         float d = 1.f;
-#pragma unroll
-        for (int e = kMostSegments - 1; e >= 0; --e) {
-            decay[e] = e < s ? d : 0.f;
-            if (e < s) d *= __ldcg(alls + e);
+        for (int e = s - 1; e >= 0; --e) {
+            add(ends + e * np, d);
+            d *= __ldcg(alls + e);
         }
-        each([&](int64_t at, float& x, float& y) {
-            float2 r = make_float2(0.f, 0.f);
-            if (start) {
-                const float2 a = *reinterpret_cast<const float2*>(start + bh * np + at);
-                r.x = d * a.x, r.y = d * a.y;
-            }
+        if (start) add(start + bh * np, d);
+        if (s > 0 || start) {
+            float* to = w.starts + (row * sh.nseg + s) * np;
 #pragma unroll
-            for (int e = 0; e < kMostSegments; ++e)
-                if (e < s) {
-                    const float2 a = __ldcg(reinterpret_cast<const float2*>(ends + e * np + at));
-                    r.x = fmaf(decay[e], a.x, r.x), r.y = fmaf(decay[e], a.y, r.y);
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int p = 8 * nt + 2 * (lane % 4);
+                    if (p < cols)
+                        *reinterpret_cast<float2*>(to + (int64_t)(m0 + n0 + lane / 4 + 4 * e) * P + p0 + p) = make_float2(r[nt][e], r[nt][e + 1]);
                 }
-            if (s > 0 || start) *reinterpret_cast<float2*>(w.starts + (row * sh.nseg + s) * np + at) = r;
-            x = fmaf(all, r.x, x), y = fmaf(all, r.y, y);
-        });
+        }
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st[nt][e] = fmaf(all, r[nt][e], st[nt][e]);
     }
     if (!last) return;
     if (start) cluster_sync();  // (the last state may lie over the first)
