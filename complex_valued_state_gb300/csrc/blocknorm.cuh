@@ -73,6 +73,13 @@ __device__ __forceinline__ void load_once(const T* p, float (&f)[W]) {
 #pragma unroll
     for (int i = 0; i < W; ++i) f[i] = to_f(t[i]);
 }
+template <typename E>
+__device__ __forceinline__ void unpack(const uint4& raw, float (&f)[Vec<E>::W]) {
+    alignas(16) E t[Vec<E>::W];
+    *reinterpret_cast<uint4*>(t) = raw;
+#pragma unroll
+    for (int i = 0; i < Vec<E>::W; ++i) f[i] = to_f(t[i]);
+}
 template <typename T, int W>
 __device__ __forceinline__ void store(T* p, const float (&f)[W]) {
     alignas(16) T t[W];
@@ -129,7 +136,7 @@ bool vectors_fit(int64_t width, int64_t most) {
 // a time in a CTA; registers hold the column sums alone, and the copies in flight are what keeps the memory
 // busy.  The warps add up their column sums at the end.
 constexpr int kRowWarps = 8;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr long long kNormWait = 4000000000LL;  // ~2 s at 2 GHz
 
 template <int G>

@@ -8,69 +8,79 @@ namespace cssd {
 namespace {
 
 // --------------------------------------------------------------- gated, forward
-// TPR threads a group of a row, the group in registers as IT vectors a thread; with at most a warp a group, no
-// barrier.
-template <typename E, typename W, int TPR, int IT>
+// TPR threads a group of a row, the group in registers as IT vectors a thread, and UN groups a team one after
+// another in memory, all of whose loads come first; with at most a warp a group, no barrier.
+template <typename E, typename W, int TPR, int IT, int UN>
 __global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) gated_rows(GatedNormArgs a, int groups, unsigned units) {
     constexpr int V = Vec<E>::W, RPC = TPR <= 32 ? 128 / TPR : 1;
     __shared__ float red[32];
     const int tid = threadIdx.x % TPR, width = (int)a.group, nv = width / V;
-    const unsigned u0 = blockIdx.x * RPC + threadIdx.x / TPR;
-    const bool live = u0 < units;  // (with barriers a CTA has one group)
-    const int64_t at = (int64_t)(live ? u0 : 0) * width;
-    const int c0 = (int)(u0 % (unsigned)groups) * width;
-    float f[IT][V], z[IT][V];
+    const unsigned u0 = blockIdx.x * (RPC * UN) + threadIdx.x / TPR;  // (unit n is u0 + n RPC)
+    uint4 xr[UN][IT], zr[UN][IT];  // (as they come: half the registers of their values)
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int c = (tid + TPR * i) * V;
+    for (int n = 0; n < UN; ++n) {
+        const bool live = u0 + n * RPC < units;  // (with barriers a CTA has one group)
+        const int64_t at = (int64_t)(u0 + n * RPC) * width;
 #pragma unroll
-        for (int u = 0; u < V; ++u) f[i][u] = z[i][u] = 0.f;
-        if (live && c < width) {
-            load_once<E, V>(static_cast<const E*>(a.x) + at + c, f[i]);
-            load_once<E, V>(static_cast<const E*>(a.z) + at + c, z[i]);
+        for (int i = 0; i < IT; ++i) {
+            const int c = (tid + TPR * i) * V;
+            const bool in = live && c < width;
+            xr[n][i] = in ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const E*>(a.x) + at + c)) : make_uint4(0, 0, 0, 0);
+            zr[n][i] = in ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const E*>(a.z) + at + c)) : make_uint4(0, 0, 0, 0);
         }
     }
-#pragma unroll
-    for (int i = 0; i < IT; ++i)
-#pragma unroll
-        for (int u = 0; u < V; ++u) {
-            z[i][u] *= sigmoid(z[i][u]);
-            if (a.gate_first) f[i][u] *= z[i][u];
-        }
     const float inv = 1.f / (float)width;
-    float m = 0.f, t = 0.f;
-    if (a.layer) {
+#pragma unroll
+    for (int n = 0; n < UN; ++n) {
+        const unsigned unit = u0 + n * RPC;
+        const bool live = unit < units;
+        const int64_t at = (int64_t)unit * width;
+        const int c0 = (int)(unit % (unsigned)groups) * width;
+        float f[IT][V], z[IT][V];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            unpack<E>(xr[n][i], f[i]);
+            unpack<E>(zr[n][i], z[i]);
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                z[i][u] *= sigmoid(z[i][u]);
+                if (a.gate_first) f[i][u] *= z[i][u];
+            }
+        }
+        float m = 0.f, t = 0.f;
+        if (a.layer) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+#pragma unroll
+                for (int u = 0; u < V; ++u) t += f[i][u];
+            m = lanes_sum<TPR>(t, red, tid) * inv;
+            t = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < IT; ++i)
+            if (tid + TPR * i < nv)
 #pragma unroll
-            for (int u = 0; u < V; ++u) t += f[i][u];
-        m = lanes_sum<TPR>(t, red, tid) * inv;
-        t = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < IT; ++i)
-        if (tid + TPR * i < nv)
-#pragma unroll
-            for (int u = 0; u < V; ++u) t = fmaf(f[i][u] - m, f[i][u] - m, t);
-    const float r = rsqrtf(lanes_sum<TPR>(t, red, tid) * inv + a.eps);
-    if (!live) return;
-    if (tid == 0) {
-        if (a.mean && a.layer) a.mean[u0] = m;
-        if (a.rstd) a.rstd[u0] = r;
-    }
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int c = (tid + TPR * i) * V;
-        if (c >= width) break;
-        float w[V], b[V];
-        load_or<W, V>(static_cast<const W*>(a.weight), c0 + c, 1.f, w);
-        load_or<W, V>(static_cast<const W*>(a.bias), c0 + c, 0.f, b);
-#pragma unroll
-        for (int u = 0; u < V; ++u) {
-            w[u] = fmaf((f[i][u] - m) * r, w[u], b[u]);
-            if (!a.gate_first) w[u] *= z[i][u];
+                for (int u = 0; u < V; ++u) t = fmaf(f[i][u] - m, f[i][u] - m, t);
+        const float r = rsqrtf(lanes_sum<TPR>(t, red, tid) * inv + a.eps);
+        if (!live) continue;
+        if (tid == 0) {
+            if (a.mean && a.layer) a.mean[unit] = m;
+            if (a.rstd) a.rstd[unit] = r;
         }
-        store<E, V>(static_cast<E*>(a.y) + at + c, w);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (tid + TPR * i) * V;
+            if (c >= width) break;
+            float w[V], b[V];
+            load_or<W, V>(static_cast<const W*>(a.weight), c0 + c, 1.f, w);
+            load_or<W, V>(static_cast<const W*>(a.bias), c0 + c, 0.f, b);
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                w[u] = fmaf((f[i][u] - m) * r, w[u], b[u]);
+                if (!a.gate_first) w[u] *= z[i][u];
+            }
+            store<E, V>(static_cast<E*>(a.y) + at + c, w);
+        }
     }
 }
 
@@ -185,7 +195,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) gated_back_ring(GatedNormAr
         }
         if (!tc::mbar_wait_bounded(&full[group][st], (uint32_t)(k / kStages & 1), kNormWait)) s_gave_up = 1;
         const E* in = reinterpret_cast<const E*>(mine + (size_t)st * bytes);
-        float s1[IT], s2[IT];
+        float s1[IT], s2[IT], sg[IT][V];  // (the sigmoids are kept from one pass to the next)
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int v = gt + TG * i;
@@ -198,7 +208,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) gated_back_ring(GatedNormAr
                 load<float, V>(sw + v * V, w);
 #pragma unroll
                 for (int u = 0; u < V; ++u) {
-                    const float gate = z[u] * sigmoid(z[u]);
+                    sg[i][u] = sigmoid(z[u]);
+                    const float gate = z[u] * sg[i][u];
                     const float hh = ((FIRST ? x[u] * gate : x[u]) - m[i]) * r[i], du = FIRST ? d[u] : d[u] * gate, g = du * w[u];
                     s1[i] += g;
                     s2[i] = fmaf(g, hh, s2[i]);
@@ -239,8 +250,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) gated_back_ring(GatedNormAr
                 if (!FIRST) load<float, V>(sb + v * V, b);
 #pragma unroll
                 for (int u = 0; u < V; ++u) {
-                    float gate, slope;
-                    gate_of(z[u], gate, slope);
+                    const float gate = z[u] * sg[i][u], slope = sg[i][u] * fmaf(z[u], 1.f - sg[i][u], 1.f);
                     const float hh = ((FIRST ? x[u] * gate : x[u]) - m[i]) * r[i], du = FIRST ? d[u] : d[u] * gate;
                     const float dh = r[i] * (du * w[u] - t1 - hh * t2);
                     z[u] = (FIRST ? dh * x[u] : d[u] * fmaf(hh, w[u], b[u])) * slope;
@@ -321,8 +331,17 @@ cudaError_t gated_fwd(const GatedNormArgs& a, cudaStream_t st) {
     if (vectors_fit<E>(a.group, 1024))
         return by_vectors<true>(a.group / Vec<E>::W, [&](auto t, auto i) {
             constexpr int TPR = decltype(t)::value, IT = decltype(i)::value, RPC = TPR <= 32 ? 128 / TPR : 1;
-            gated_rows<E, W, TPR, IT><<<(unsigned)((units + RPC - 1) / RPC), TPR * RPC, 0, st>>>(a, (int)(a.width / a.group), (unsigned)units);
-            return cudaGetLastError();
+            constexpr int MANY = TPR > 32 || IT > 2 ? 1 : 2 / IT;
+            auto go = [&](auto un) {
+                constexpr int UN = decltype(un)::value;
+                gated_rows<E, W, TPR, IT, UN><<<(unsigned)((units + RPC * UN - 1) / (RPC * UN)), TPR * RPC, 0, st>>>(
+                    a, (int)(a.width / a.group), (unsigned)units);
+                return cudaGetLastError();
+            };
+            // (few groups: one a team, so that they spread over the SMs)
+            if constexpr (MANY > 1)
+                if (units >= (int64_t)RPC * MANY * 152) return go(std::integral_constant<int, MANY>());
+            return go(std::integral_constant<int, 1>());
         });
     if (a.group <= 1024)
         gated_stream<E, W, 32><<<grid_of((units + 7) / 8, 8192), 256, 0, st>>>(a);
