@@ -10,6 +10,12 @@
 // rounded to its type before the norm sees it, so that the gradients, which read s, are those of what was
 // computed.  Sums over the rows are taken in a fixed order: a thread owns its columns over the rows of its CTA,
 // and a second kernel adds up the CTAs' sums.
+//
+// Measured, 8192 x 1536 bf16 (device time): add with an fp32 residual 25 us (151 MB: 5.9 TB/s), its gradients 41 and 4
+// for the join (227 MB: 5.0 TB/s with it); gated by heads of 64 17 us (76 MB: 4.4 TB/s; issue 76 % busy: the gate's
+// exponential and reciprocal), gradients over whole rows 32 and 4 (126 MB: 3.5 TB/s).  Widths that are no whole
+// 16-byte vectors, and rows too wide for the registers or the ring, take the streaming kernels, which read a row
+// again from the caches for each sum: 47, 93, 102 and 117 us for these cases.
 
 #include <initializer_list>
 #include <type_traits>
@@ -134,7 +140,8 @@ bool vectors_fit(int64_t width, int64_t most) {
 // --------------------------------------------------------------- the gradients' ring
 // Rows come by bulk copies into a ring in shared memory, kStages - 1 rows ahead: G warps a row, so 8 / G rows at
 // a time in a CTA; registers hold the column sums alone, and the copies in flight are what keeps the memory
-// busy.  The warps add up their column sums at the end.
+// busy.  The warps add up their column sums at the end.  Two stages: with three the gated gradients took 35.9 us
+// against 32.1 and the others the same; 16 warps a CTA 50 us, three CTAs an SM 39.
 constexpr int kRowWarps = 8;
 constexpr int kStages = 2;
 constexpr long long kNormWait = 4000000000LL;  // ~2 s at 2 GHz

@@ -22,6 +22,22 @@
 //   out, grad one CTA a chunk and head, 16 tokens a warp: scores by blocks of 16 x 16, which pass from the
 //            accumulators of one product into the operands of the next in registers
 // The chunks do not wait for one another, so everything but the states' walk is as parallel as there are chunks.
+//
+// What a value is rounded to: inputs are exact in their planes; decayed keys, and states for dq and dk, have three
+// (24 bits: float32 results, the last state, dS and dg, come from them); scores, and states for 16-bit results,
+// two (16 bits, 2^-18 of each term at most, far below the result's own rounding).  One plane of the scores
+// would add an error as large as the output's own rounding and made the forward no faster (67.3 us against 67.3).
+//
+// The products are warp-level matrix instructions, whose rate here is 581 TFLOP/s (measured), a third of the
+// tcgen05 ones': with it the 64/64 forward of 4 x 2048 x 24 needs 22 us of tensor time beside 34 us of its
+// memory traffic (the states among it), in exchange for scores that never leave the registers, three CTAs an SM
+// and no barrier inside a chunk's products.  Where both widths are 128 it bounds, with the shared memory's
+// bandwidth (every warp reads all of a state for its 16 rows): see the gradients.
+//
+// Measured, bf16 (device time): forward 4 x 2048 x 24, 64/64 65 us (walk 29, outputs 37: half of it the loads'
+// latency at three CTAs an SM; without any products 41 us); 1 x 16384 x 32, 128/64 294 us (walk 118, 1 GB moved with
+// the states); gradients 4 x 2048 x 24, 64/64 184 us (walk 47, grad_kernel 137); 4 x 1501 x 16 on 8 key heads,
+// 128/128 182 to 212 us by the rows' lengths (walk 51, grad_kernel 145, sum over shared heads 23).
 #pragma once
 
 #include <type_traits>
@@ -592,6 +608,8 @@ __device__ __forceinline__ void load_decays(unsigned char* dst, const void* src,
     for (int i = tid; i < bytes / 16; i += NT) cp16(to + 16 * i, static_cast<const unsigned char*>(src) + 16 * i, true);
 }
 
+// Three CTAs an SM at 64/64 (80 registers, 76 KB): 37 us for 4 x 2048 x 24, tensor pipe 42 % busy, issue 38 %; with
+// two blocks of scores in flight a warp at two CTAs an SM the call took 71.0 us against 68.9.
 template <typename E, int ND, int PD, int C>
 struct OutSmem {
     static constexpr int NP = Type<E>::NP, SP = NP == 3 ? 3 : 2;
@@ -661,6 +679,11 @@ __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
 }
 
 // --------------------------------------------------------------- gradients
+// 4 x 2048 x 24, 64/64: 137 us at two CTAs an SM, tensor pipe 38 % busy, issue 33 % (dk and dv 50 us, the state's
+// products 45, dq 15, loads and stores the rest).  128/128: one CTA an SM (four tiles of 34 KB), 255 registers; the
+// state's products are half of it (80 of 157 us), whose operands' reads from shared memory (2 MB a chunk) and tensor
+// time (27000 cycles a chunk) are equal.  16 warps a CTA, sharing columns, took 225 us against 212 there and 256
+// against 184 at 64/64 (scores twice).
 // The states have three planes for dq and dk, from which dg (a float32 result) takes its terms, and two for dv.
 template <typename E, int ND, int PD, int C>
 struct GradSmem {
@@ -984,7 +1007,10 @@ inline size_t decays_bytes(const LinattnArgs& a) {
     return C == 128 ? sizeof(Decays<128>) : C == 64 ? sizeof(Decays<64>) : sizeof(Decays<32>);
 }
 
-constexpr int kStateCtas = 384;  // CTAs that the states' walk may have (up to three an SM are resident)
+// CTAs that the states' walk may have, by cutting rows into segments: as many as are resident at once where clusters
+// of segments have to fit a group of SMs (1 x 16384 x 32, 128/64: 299 us with 6 segments a row, 331 with 7, 307 with 4;
+// 4 x 2048 x 24, 64/64: 68.9 with 4, 69.6 with 3, 75.0 with 2; its gradients 189 with 2, 193 uncut).
+constexpr int kStateCtas = 384;
 inline int slices_of(const LinattnArgs& a) { return (a.N > 64 ? 2 : 1) * (a.P > 64 ? 2 : 1); }
 
 inline Shape shape_of(const LinattnArgs& a, int dirs) {
@@ -1114,7 +1140,7 @@ cudaError_t backward(const LinattnArgs& a, void* ws, cudaStream_t st) {
 }
 
 // Calls f with the widths' tiles (64 or 128 columns) and whether the widths fill them: the kernels then have no
-// tests of columns (4 x 2048 x 24, 64/64: see the measurements at the head).
+// tests of columns (4 x 2048 x 24, 64/64: forward 75 us against 87, gradients 194 against 244).
 template <typename F>
 cudaError_t by_widths(const LinattnArgs& a, F f) {
     using I64 = std::integral_constant<int, 64>;

