@@ -83,7 +83,8 @@ constexpr unsigned kStatusHandoff = 1u;   // chunk kernel: a state hand-off wait
 constexpr unsigned kStatusChunkMma = 2u;  // chunk kernel: a tensor-core completion wait gave up
 constexpr unsigned kStatusBornMma = 4u;   // Born attention: a tensor-core completion wait gave up
 constexpr unsigned kStatusDelta = 8u;     // gated delta rule: a wait of a tensor-core kernel gave up
-constexpr unsigned kStatusNorm = 16u;     // layer norm's gradients: a wait for a row's copy gave up
+constexpr unsigned kStatusNorm = 16u;     // a norm's gradients: a wait for a row's copy gave up
+constexpr unsigned kStatusLinattn = 32u;  // linear attention: a tensor-core completion wait gave up
 unsigned* status_word();
 
 // Events the forward records around its dominant kernel (null = off); set by

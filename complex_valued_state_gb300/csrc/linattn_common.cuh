@@ -86,6 +86,39 @@ __device__ __forceinline__ uint32_t lane_at(uint32_t base, int pitch_, int r0, i
     const int c = c0 + (FLIP ? (lane >> 3 & 1) * 8 : (lane >> 4) * 8);
     return base + r * pitch_ + 2 * c;
 }
+// The tiles of kernels with products on tcgen05 instead hold eight columns of all their rows after one another, 16 bytes a row: blocks
+// of 8 x 8 are 128 contiguous bytes, which ldmatrix reads without conflicts and the tcgen05 descriptors take as they
+// are, either way round.  16 bytes between the groups of columns let a row be written without conflicts too.  (The
+// kernels without such products are slower on these tiles, whose rows a copy writes to eight places: 75 us against 65 for the
+// forward of 4 x 2048 x 24, 64/64.)
+__host__ __device__ constexpr int group_bytes(int rows) { return 16 * rows + 16; }
+__host__ __device__ constexpr int plane_bytes(int rows, int w) { return w / 8 * group_bytes(rows); }
+// As lane_at, for a tile of ROWS rows.
+template <bool FLIP, int ROWS>
+__device__ __forceinline__ uint32_t core_at(uint32_t base, int r0, int c0, int lane) {
+    const int r = r0 + (lane & 7) + (FLIP ? (lane >> 4) * 8 : (lane >> 3 & 1) * 8);
+    const int cg = c0 / 8 + (FLIP ? (lane >> 3 & 1) : (lane >> 4));
+    return base + cg * group_bytes(ROWS) + 16 * r;
+}
+// Where a block of 16 tokens lies among a tile's rows.  TC (128 rows, products on tcgen05): the blocks b and 7 - b lie
+// side by side, in the 32 lanes of tensor memory that the two warps which have them may read.
+template <bool TC>
+__device__ __forceinline__ int place(int block) {
+    return TC ? (block < 4 ? 2 * block : 15 - 2 * block) : block;
+}
+// A tile of ROWS rows of W columns in either layout (TC: the core one): the bytes of a plane and from 16 columns to
+// the next, and a lane's address in the 16 x 16 block of tokens `block`, columns c0..
+template <bool TC, int ROWS, int W>
+struct Tile {
+    static constexpr int PLANE = TC ? plane_bytes(ROWS, W) : ROWS * pitch(W), STEP = TC ? 2 * group_bytes(ROWS) : 32;
+    template <bool FLIP>
+    static __device__ __forceinline__ uint32_t at(uint32_t base, int block, int c0, int lane) {
+        if constexpr (TC)
+            return core_at<FLIP, ROWS>(base, 16 * place<ROWS == 128>(block), c0, lane);
+        else
+            return lane_at<FLIP>(base, pitch(W), 16 * block, c0, lane);
+    }
+};
 // c = A B (the sum's first 16), and c += A B, for 16 x 8 outputs.
 __device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm(
@@ -148,6 +181,19 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, int plane, const E
             }
         }
     }
+}
+
+// 128 tokens of `width` bfloat16 columns (at most W; rows from n on are zeros) into a core tile, by NT threads.
+template <int W, int NT>
+__device__ __forceinline__ void load_core(unsigned char* dst, const __nv_bfloat16* src, int64_t stride, int n, int width, int tid) {
+    constexpr int PER = W / 8, STEP = NT / PER;
+    const int t0 = tid / PER, col = tid % PER * 8;
+    if (col >= width) return;
+    src += t0 * stride + col;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + col / 8 * group_bytes(128);
+#pragma unroll
+    for (int t = 0; t < 128; t += STEP, src += STEP * stride)
+        cp16(to + 16 * (16 * place<true>((t0 + t) / 16) + (t0 + t) % 16), src, t0 + t < n);
 }
 
 // Division of n < 2^31 by a number that is the same all over a launch.

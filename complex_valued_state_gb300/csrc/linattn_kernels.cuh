@@ -28,22 +28,23 @@
 // two (16 bits, 2^-18 of each term at most, far below the result's own rounding).  One plane of the scores
 // would add an error as large as the output's own rounding and made the forward no faster (67.3 us against 67.3).
 //
-// The products are warp-level matrix instructions, whose rate here is 581 TFLOP/s (measured), a third of the
+// Most products are warp-level matrix instructions, whose rate here is 581 TFLOP/s (measured), a third of the
 // tcgen05 ones': with it the 64/64 forward of 4 x 2048 x 24 needs 22 us of tensor time beside 34 us of its
 // memory traffic (the states among it), in exchange for scores that never leave the registers, three CTAs an SM
-// and no barrier inside a chunk's products.  Where both widths are 128 it bounds, with the shared memory's
-// bandwidth (every warp reads all of a state for its 16 rows): see the gradients.
+// and no barrier inside a chunk's products.  The state's products of the wide gradients are tcgen05 ones: there every
+// warp would read all of a state from shared memory for its 16 rows.
 //
 // Measured, bf16 (device time): forward 4 x 2048 x 24, 64/64 65 us (walk 29, outputs 37: half of it the loads'
 // latency at three CTAs an SM; without any products 41 us); 1 x 16384 x 32, 128/64 294 us (walk 118, 1 GB moved with
 // the states); gradients 4 x 2048 x 24, 64/64 184 us (walk 47, grad_kernel 137); 4 x 1501 x 16 on 8 key heads,
-// 128/128 182 to 212 us by the rows' lengths (walk 51, grad_kernel 145, sum over shared heads 23).
+// 128/128 197 us at 82 % of the tokens (walk 51, grad_kernel 130, sum over shared heads 23).
 #pragma once
 
 #include <type_traits>
 
 #include "cssd_internal.h"
 #include "linattn_common.cuh"
+#include "tcgen05.cuh"
 
 namespace cssd {
 namespace linattn {
@@ -98,7 +99,8 @@ struct Part {
 template <int NPL, int SP, int C, int KW, int OW, int CW, bool TRANS>
 __device__ __forceinline__ void times_state(float (&acc)[CW / 8][4], uint32_t a, uint32_t s, int block, int col0, int sl, int kw,
                                             int ow, int lane) {
-    constexpr int SPITCH = pitch(TRANS ? OW : KW);
+    using TA = Tile<false, C, KW>;
+    using TS = Tile<false, 64, TRANS ? OW : KW>;
     constexpr int KT = TRANS ? imin(4, KW / 16) : KW / 16;
     const int k0 = TRANS ? 64 * sl : 0;
 #pragma unroll
@@ -106,7 +108,7 @@ __device__ __forceinline__ void times_state(float (&acc)[CW / 8][4], uint32_t a,
         if (k0 + 16 * kt >= kw) break;
         uint32_t af[NPL][4];
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) ldsm(af[i], lane_at<false>(a + i * C * pitch(KW), pitch(KW), 16 * block, k0 + 16 * kt, lane));
+        for (int i = 0; i < NPL; ++i) ldsm(af[i], TA::template at<false>(a + i * TA::PLANE, block, k0 + 16 * kt, lane));
         // (columns inside: a sum is added to again only after all the others)
 #pragma unroll
         for (int j = SP - 1; j >= 0; --j) {
@@ -117,9 +119,9 @@ __device__ __forceinline__ void times_state(float (&acc)[CW / 8][4], uint32_t a,
                 if (col >= ow) break;
                 if (!TRANS && col / 64 != sl) continue;
                 if (TRANS)
-                    ldsm_t(bf[nt], lane_at<false>(s + j * 64 * SPITCH, SPITCH, 16 * kt, col, lane));
+                    ldsm_t(bf[nt], TS::template at<false>(s + j * TS::PLANE, kt, col, lane));
                 else
-                    ldsm(bf[nt], lane_at<true>(s + j * 64 * SPITCH, SPITCH, col % 64, 16 * kt, lane));
+                    ldsm(bf[nt], TS::template at<true>(s + j * TS::PLANE, col % 64 / 16, 16 * kt, lane));
             }
 #pragma unroll
             for (int i = NPL - 1; i >= 0; --i)
@@ -137,33 +139,35 @@ __device__ __forceinline__ void times_state(float (&acc)[CW / 8][4], uint32_t a,
 }
 
 // The operands A of the scores: kept in registers where they are one plane of at most 64 columns.
-template <int NPL, int C, int KW>
+template <int NPL, int C, int KW, bool TC>
 struct Rows {
+    using TA = Tile<TC, C, KW>;
     static constexpr bool KEEP = NPL == 1 && KW <= 64;
     uint32_t f[KEEP ? KW / 16 : 1][4];
     uint32_t at;
-    __device__ __forceinline__ Rows(uint32_t a, int block, int kw, int lane) : at(lane_at<false>(a, pitch(KW), 16 * block, 0, lane)) {
+    __device__ __forceinline__ Rows(uint32_t a, int block, int kw, int lane) : at(TA::template at<false>(a, block, 0, lane)) {
         if constexpr (KEEP)
 #pragma unroll
             for (int kt = 0; kt < KW / 16; ++kt)
-                if (16 * kt < kw) ldsm(f[kt], at + 32 * kt);
+                if (16 * kt < kw) ldsm(f[kt], at + TA::STEP * kt);
     }
 };
 // sc = A B^T for the warp's 16 rows and the 16 tokens of block `o` of B.
-template <int NPL, int QP, int C, int KW>
-__device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW>& a, uint32_t b, int o, int kw, int lane) {
-    const uint32_t at = lane_at<true>(b, pitch(KW), 16 * o, 0, lane);
+template <int NPL, int QP, int C, int KW, bool TC>
+__device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW, TC>& a, uint32_t b, int o, int kw, int lane) {
+    using TB = Tile<TC, C, KW>;
+    const uint32_t at = TB::template at<true>(b, o, 0, lane);
 #pragma unroll
     for (int kt = 0; kt < KW / 16; ++kt) {
         if (16 * kt >= kw) break;
         if constexpr (NPL == 1) {
             uint32_t bf[4], af[4];
-            ldsm(bf, at + 32 * kt);
-            if constexpr (Rows<NPL, C, KW>::KEEP) {
+            ldsm(bf, at + TB::STEP * kt);
+            if constexpr (Rows<NPL, C, KW, TC>::KEEP) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) af[e] = a.f[kt][e];
             } else {
-                ldsm(af, a.at + 32 * kt);
+                ldsm(af, a.at + TB::STEP * kt);
             }
             if (kt == 0) {
                 mma_first(sc[0], af, bf[0], bf[1]);
@@ -175,11 +179,11 @@ __device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW>
         } else {
             uint32_t af[NPL][4];
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) ldsm(af[i], a.at + i * C * pitch(KW) + 32 * kt);
+            for (int i = 0; i < NPL; ++i) ldsm(af[i], a.at + i * TB::PLANE + TB::STEP * kt);
 #pragma unroll
             for (int j = NPL - 1; j >= 0; --j) {
                 uint32_t bf[4];
-                ldsm(bf, at + j * C * pitch(KW) + 32 * kt);
+                ldsm(bf, at + j * TB::PLANE + TB::STEP * kt);
 #pragma unroll
                 for (int i = NPL - 1; i >= 0; --i)
                     if (i + j < QP) {
@@ -233,7 +237,7 @@ __device__ __forceinline__ void multiply(float (&sc)[2][4], const float (&m)[2][
 }
 // acc += P Z for columns col0.. of Z's 16 tokens of block `o`; the scores P, split in PP planes, are the operand as
 // they lie.
-template <int NPL, int PP, int C, int OW, int CW>
+template <int NPL, int PP, int C, int OW, int CW, bool TC>
 __device__ __forceinline__ void times_tokens(float (&acc)[CW / 8][4], const float (&sc)[2][4], uint32_t z, int col0, int o, int ow, int lane) {
     uint32_t p[PP][4];
 #pragma unroll
@@ -243,7 +247,8 @@ __device__ __forceinline__ void times_tokens(float (&acc)[CW / 8][4], const floa
 #pragma unroll
         for (int i = 0; i < PP; ++i) p[i][u] = w[i];
     }
-    const uint32_t at = lane_at<false>(z, pitch(OW), 16 * o, col0, lane);
+    using TZ = Tile<TC, C, OW>;
+    const uint32_t at = TZ::template at<false>(z, o, col0, lane);
     constexpr int NG = imin(CW / 16, 4);  // 64 columns at a time
 #pragma unroll
     for (int n0 = 0; n0 < CW / 16; n0 += NG)
@@ -252,7 +257,7 @@ __device__ __forceinline__ void times_tokens(float (&acc)[CW / 8][4], const floa
             uint32_t bf[NG][4];
 #pragma unroll
             for (int nt = 0; nt < NG; ++nt)
-                if (col0 + 16 * (n0 + nt) < ow) ldsm_t(bf[nt], at + j * C * pitch(OW) + 32 * (n0 + nt));
+                if (col0 + 16 * (n0 + nt) < ow) ldsm_t(bf[nt], at + j * TZ::PLANE + TZ::STEP * (n0 + nt));
 #pragma unroll
             for (int i = PP - 1; i >= 0; --i)
                 if (i + j < PP)
@@ -265,16 +270,16 @@ __device__ __forceinline__ void times_tokens(float (&acc)[CW / 8][4], const floa
         }
 }
 // acc = sum over the blocks at or before the warp's of (A B^T, decayed) Z.
-template <int NPL, int QP, int PP, int C, int KW, int OW, int CW>
+template <int NPL, int QP, int PP, int C, int KW, int OW, int CW, bool TC>
 __device__ __forceinline__ void earlier_pairs(float (&acc)[CW / 8][4], uint32_t a, uint32_t b, uint32_t z, int block, int col0, int kw, int ow,
                                               float scale, const Decays<C>& d, int lane) {
-    const Rows<NPL, C, KW> rows(a, block, kw, lane);
+    const Rows<NPL, C, KW, TC> rows(a, block, kw, lane);
     float row[2];
     row_factors<C, true>(row, d, block, scale, lane);
     auto with = [&](int o, auto diag) {
         constexpr bool DIAG = decltype(diag)::value;
         float sc[2][4], m[2][4];
-        scores<NPL, QP, C, KW>(sc, rows, b, o, kw, lane);
+        scores<NPL, QP, C, KW, TC>(sc, rows, b, o, kw, lane);
         pair_factors<C, true, DIAG>(m, d, block, o, row, scale, lane);
         if constexpr (DIAG) {  // (a score that is not wanted may be anything)
 #pragma unroll
@@ -283,7 +288,7 @@ __device__ __forceinline__ void earlier_pairs(float (&acc)[CW / 8][4], uint32_t 
                 for (int e = 0; e < 4; ++e) sc[h][e] = lane / 4 + 8 * (e / 2) >= 8 * h + 2 * (lane % 4) + e % 2 ? sc[h][e] : 0.f;
         }
         multiply(sc, m);
-        times_tokens<NPL, PP, C, OW, CW>(acc, sc, z, col0, o, ow, lane);
+        times_tokens<NPL, PP, C, OW, CW, TC>(acc, sc, z, col0, o, ow, lane);
     };
 #pragma unroll 1
     for (int o = 0; o < block; ++o) with(o, std::false_type());
@@ -327,8 +332,8 @@ __device__ __forceinline__ StateAt state_at(const Scratch& w, const Shape& sh, i
     return r;
 }
 
-// 64 rows of a state from row 64 sl on: fetched into registers, and put as SP planes.
-template <int SP, int PD>
+// 64 rows of a state from row 64 sl on: fetched into registers, and put as SP planes of a tile of 64 rows n.
+template <int SP, int PD, bool TC>
 struct StateTile {
     static constexpr int PER = PD / 4, STEP = NT / PER, K = 64 / STEP;
     float4 v[K];
@@ -339,15 +344,130 @@ struct StateTile {
             v[k] = c < P && r + STEP * k < N ? st.at((r + STEP * k) * P + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __device__ __forceinline__ void put(unsigned char* dst, int tid) const {
-        unsigned char* at = dst + tid / PER * pitch(PD) + 8 * (tid % PER);
+        const int c = 4 * (tid % PER);
+        constexpr int ROW = TC ? 16 : pitch(PD);
+        unsigned char* at = dst + (TC ? c / 8 * group_bytes(64) + c % 8 * 2 : 2 * c) + tid / PER * ROW;
 #pragma unroll
-        for (int k = 0; k < K; ++k, at += STEP * pitch(PD)) {
+        for (int k = 0; k < K; ++k, at += ROW * STEP) {
             uint32_t x[SP], y[SP];
             split<SP>(v[k].x, v[k].y, x);
             split<SP>(v[k].z, v[k].w, y);
 #pragma unroll
-            for (int z = 0; z < SP; ++z) *reinterpret_cast<uint2*>(at + z * 64 * pitch(PD)) = make_uint2(x[z], y[z]);
+            for (int z = 0; z < SP; ++z) *reinterpret_cast<uint2*>(at + z * Tile<TC, 64, PD>::PLANE) = make_uint2(x[z], y[z]);
         }
+    }
+};
+
+// --------------------------------------------------------------- the state's products on tcgen05
+// Chunks of 128 tokens (bfloat16): [128 tokens] x [a state's 64 rows a time] into tensor memory, from the tiles as
+// they lie, beside the warps' work on the scores.  A warp gets its 16 rows in the layout of its own sums.
+constexpr long long kLinattnWait = 4000000000LL;  // ~2 s at 2 GHz
+
+// One thread.  TRANS: D[., p] (+)= A[., n] S[n][p] over the slice's n; else D[., n of the slice] = A[., p] S[n][p].
+template <int KW, int OW, int SP, bool TRANS>
+__device__ __forceinline__ void issue_state(uint32_t tmem, uint32_t a, uint32_t s, int sl, int kw) {
+    constexpr int PLANE = plane_bytes(64, TRANS ? OW : KW), KT = TRANS ? 4 : KW / 16, N = TRANS ? OW : 64;
+    constexpr int GA = group_bytes(128), GS = group_bytes(64);
+    // D fp32, A and B bfloat16, B's columns contiguous (TRANS) or its sum
+    constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (TRANS ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    const int k0 = TRANS ? 64 * sl : 0;
+    if (!TRANS) tmem += 64 * sl;
+#pragma unroll
+    for (int z = SP - 1; z >= 0; --z)
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            if (k0 + 16 * kt >= kw) break;
+            const uint64_t da = tc::make_desc(a + (k0 / 8 + 2 * kt) * GA, GA, 128);
+            const uint64_t db = TRANS ? tc::make_desc(s + z * PLANE + 256 * kt, 128, GS) : tc::make_desc(s + z * PLANE + 2 * GS * kt, GS, 128);
+            tc::mma_f16(tmem, da, db, idesc, z < SP - 1 || kt > 0 || (TRANS && sl > 0));
+        }
+}
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[16]) {  // 16 rows x 32 columns
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// acc += f (rows r0, r0 + 8) times the warp's rows of the product at `tmem`; with DOT, returns the sums of that times the
+// rows of `tile` over the columns, in every lane of the four that share them.
+template <int W, bool DOT>
+__device__ __forceinline__ float2 add_state(float (&acc)[W / 8][4], uint32_t tmem, float f0, float f1, const unsigned char* tile, int block,
+                                            int width, int warp, int lane) {
+    float s[2] = {};
+    tmem += (uint32_t)(32 * (warp % 4) + 16 * (warp / 4)) << 16;
+#pragma unroll
+    for (int g = 0; g < W / 32; ++g) {
+        if (32 * g >= width) break;
+        uint32_t t[16];
+        tmem_ld_rows(tmem + 32 * g, t);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int nt = 4 * g + u;
+            if (8 * nt >= width) break;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f = e ? f1 : f0, x = f * __uint_as_float(t[4 * u + 2 * e]), y = f * __uint_as_float(t[4 * u + 2 * e + 1]);
+                acc[nt][2 * e] += x, acc[nt][2 * e + 1] += y;
+                if (DOT) {
+                    const uint32_t v =
+                        *reinterpret_cast<const uint32_t*>(tile + nt * group_bytes(128) + (16 * place<true>(block) + lane / 4 + 8 * e) * 16 + 4 * (lane % 4));
+                    s[e] = fmaf(x, lo_f(v), fmaf(y, hi_f(v), s[e]));
+                }
+            }
+        }
+    }
+    if (DOT)
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+            s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+            s[1] += __shfl_xor_sync(0xffffffffu, s[1], o);
+        }
+    return make_float2(s[0], s[1]);
+}
+// A CTA's tensor memory and the barrier of its products.
+struct TensorShared {
+    uint64_t done, drain;
+    uint32_t tmem;
+    int gave_up;
+};
+struct Tensor {
+    TensorShared& sh;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void begin(int columns, int tid) {  // (complete after the CTA's next barrier)
+        if (tid / 32 == 0) {
+            tc::tmem_alloc(&sh.tmem, columns);
+            tc::tmem_relinquish();
+        }
+        if (tid == 0) {
+            tc::mbar_init(&sh.done, 1);
+            tc::mbar_init(&sh.drain, 1);
+            tc::mbar_fence_init();
+            sh.gave_up = 0;
+        }
+    }
+    // Every thread, before the barrier behind which one thread issues products from what this one has stored.
+    static __device__ __forceinline__ void publish() {
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+    }
+    // (a wait that gives up: the results are wrong and the status word says so)
+    __device__ __forceinline__ void wait() {
+        if (!tc::mbar_wait_bounded(&sh.done, phase & 1, kLinattnWait)) sh.gave_up = 1;
+        ++phase;
+        tc::fence_after_sync();
+    }
+    __device__ __forceinline__ void end(int columns, int tid, unsigned* status) {
+        tc::fence_before_sync();
+        __syncthreads();
+        if (tid == 0 && sh.gave_up) {
+            tc::drain_mmas(&sh.drain, kLinattnWait);
+            if (status) atomicOr(status, kStatusLinattn);
+        }
+        __syncwarp();
+        if (tid / 32 == 0) tc::tmem_dealloc(sh.tmem, columns);
     }
 };
 
@@ -613,10 +733,11 @@ __device__ __forceinline__ void load_decays(unsigned char* dst, const void* src,
 template <typename E, int ND, int PD, int C>
 struct OutSmem {
     static constexpr int NP = Type<E>::NP, SP = NP == 3 ? 3 : 2;
-    static constexpr int Q = 0, K = Q + NP * C * pitch(ND), V = K + NP * C * pitch(ND), S = V + NP * C * pitch(PD);
-    static constexpr int D = S + imax(SP * 64 * pitch(PD), sizeof(E) == 2 ? C * pitch(PD) : 0);
+    static constexpr int X = NP * Tile<false, C, ND>::PLANE, Y = NP * Tile<false, C, PD>::PLANE;
+    static constexpr int Q = 0, K = X, V = 2 * X, S = 2 * X + Y;
+    static constexpr int D = S + imax(SP * Tile<false, 64, PD>::PLANE, sizeof(E) == 2 ? C * pitch(PD) : 0);
     static constexpr int TABLE = sizeof(Decays<C>) - 4 * C, BYTES = D + TABLE;
-    static constexpr int CTAS = BYTES + 1024 <= 228 * 1024 / 3 ? 3 : BYTES + 1024 <= 114 * 1024 ? 2 : 1;
+    static constexpr int CTAS = BYTES + 1024 <= 76 * 1024 ? 3 : BYTES + 1024 <= 114 * 1024 ? 2 : 1;
 };
 
 template <typename E, int ND, int PD, int C, bool FULL>
@@ -646,7 +767,7 @@ __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
     load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, M::TABLE, tid);
     cp_commit();
     const StateAt st = state_at(w, sh, 0, bh, c, live, start);
-    StateTile<SP, PD> tile;
+    StateTile<SP, PD, false> tile;
     if (st.any()) {
         tile.fetch(st, 0, N, P, tid);
         tile.put(smem + M::S, tid);
@@ -665,14 +786,14 @@ __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
                 tile.fetch(st, sl, N, P, tid);
                 __syncthreads();
                 tile.put(smem + M::S, tid);
-                __syncthreads();
+                            __syncthreads();
             }
             times_state<NP, SP, C, ND, PD, CW, true>(acc, base + M::Q, base + M::S, block, col0, sl, N, P, lane);
         }
         scale_rows(acc, d.in[r0], d.in[r0 + 8]);
     }
     if (16 * block < n)
-        earlier_pairs<NP, NP, SP, C, ND, PD, CW>(acc, base + M::Q, base + M::K, base + M::V, block, col0, N, P, 1.f, d, lane);
+        earlier_pairs<NP, NP, SP, C, ND, PD, CW, false>(acc, base + M::Q, base + M::K, base + M::V, block, col0, N, P, 1.f, d, lane);
     if (sizeof(E) == 2 && st.any()) __syncthreads();  // (the state's planes are read: the stage lies over them)
     put_rows<E, PD, CW>(orow + 16 * block * os, os, acc, sh.scale, smem + M::S + 16 * block * pitch(PD), col0, P, n - 16 * block,
                         rows - 16 * block, lane);
@@ -680,17 +801,21 @@ __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
 
 // --------------------------------------------------------------- gradients
 // 4 x 2048 x 24, 64/64: 137 us at two CTAs an SM, tensor pipe 38 % busy, issue 33 % (dk and dv 50 us, the state's
-// products 45, dq 15, loads and stores the rest).  128/128: one CTA an SM (four tiles of 34 KB), 255 registers; the
-// state's products are half of it (80 of 157 us), whose operands' reads from shared memory (2 MB a chunk) and tensor
-// time (27000 cycles a chunk) are equal.  16 warps a CTA, sharing columns, took 225 us against 212 there and 256
-// against 184 at 64/64 (scores twice).
+// products 45, dq 15, loads and stores the rest).  128/128: one CTA an SM (four tiles of 34 KB), 255 registers; there
+// the state's products by the warps were half of it (80 of 157 us), whose operands' reads from shared memory (2 MB a
+// chunk) and tensor time (27000 cycles a chunk) were equal, so they are tcgen05 ones beside the scores.  16 warps a
+// CTA, sharing columns, took 225 us a call against 212 there (without tcgen05) and 256 against 184 at 64/64 (scores twice).
 // The states have three planes for dq and dk, from which dg (a float32 result) takes its terms, and two for dv.
 template <typename E, int ND, int PD, int C>
 struct GradSmem {
     static constexpr int NP = Type<E>::NP, SP = NP == 3 ? 3 : 2, RB = C / 16;
-    static constexpr int X = NP * C * pitch(ND), Y = NP * C * pitch(PD);
+    // The state's products on tcgen05 for the wide tiles: 195 us against 216 for 4 x 1501 x 16 on 8 key heads, 128/128;
+    // at 64/64, where two CTAs an SM leave 128 registers a thread, 188 against 184 for 4 x 2048 x 24.
+    static constexpr bool TC = C == 128 && (ND > 64 || PD > 64);
+    static constexpr int X = NP * Tile<TC, C, ND>::PLANE, Y = NP * Tile<TC, C, PD>::PLANE;
     static constexpr int Q = 0, K = X, V = 2 * X, DO = 2 * X + Y, S = 2 * X + 2 * Y;
-    static constexpr int D = S + imax(3 * 64 * pitch(PD), sizeof(E) == 2 ? C * pitch(imax(ND, PD)) : 0);
+    static constexpr int D = S + imax(3 * Tile<TC, 64, PD>::PLANE, sizeof(E) == 2 ? C * pitch(imax(ND, PD)) : 0);
+    static constexpr int COLUMNS = ND + PD == 192 ? 256 : ND + PD;  // of tensor memory: dq, then dk; dv
     static constexpr int COL = D + sizeof(Decays<C>);      // [RB][C] sums of W over the tokens j of a block
     static constexpr int ROW = COL + 4 * RB * C;           // [C] sums of W over i
     static constexpr int AQ = ROW + 4 * C, BK = AQ + 8 / RB * C * 4, BYTES = BK + 8 / RB * C * 4;  // [share][C]
@@ -729,11 +854,13 @@ template <typename E, int ND, int PD, int C, bool FULL>
 __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
     grad_kernel(const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const E* __restrict__ dout,
                 const int* __restrict__ lens, bool start, bool end, E* __restrict__ gq, E* __restrict__ gk, E* __restrict__ gv,
-                float* __restrict__ parts, float* __restrict__ gg, float* __restrict__ gg_part, Scratch w, Shape sh) {
+                float* __restrict__ parts, float* __restrict__ gg, float* __restrict__ gg_part, Scratch w, Shape sh, unsigned* status) {
     using M = GradSmem<E, ND, PD, C>;
     constexpr int NP = M::NP, SP = M::SP, QP = NP == 1 ? 1 : 3, CN = ND / Part<C>::CS, CP = PD / Part<C>::CS, SHARES = Part<C>::CS;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_dot[NT / 32];
+    __shared__ __align__(16) TensorShared tensor_sh;
+    Tensor tensor{tensor_sh};
     const Decays<C>& d = *reinterpret_cast<const Decays<C>*>(smem + M::D);
     float(*s_col)[C] = reinterpret_cast<float(*)[C]>(smem + M::COL);
     float* s_row = reinterpret_cast<float*>(smem + M::ROW);
@@ -765,20 +892,29 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
         if (gg_part && tid == 0) gg_part[blockIdx.x] = 0.f;
         return;
     }
-    load_tile<E, PD, C, NT>(smem + M::DO, C * pitch(PD), dout + oo, os, n, P, tid);
-    load_tile<E, PD, C, NT>(smem + M::V, C * pitch(PD), v + oo, os, n, P, tid);
-    load_tile<E, ND, C, NT>(smem + M::K, C * pitch(ND), k + ko, ks, n, N, tid);
-    load_tile<E, ND, C, NT>(smem + M::Q, C * pitch(ND), q + ko, ks, n, N, tid);
+    if (M::TC) tensor.begin(M::COLUMNS, tid);
+    auto load = [&](auto width, unsigned char* to, const E* from, int64_t stride, int tokens, int columns) {
+        constexpr int W = decltype(width)::value;
+        if constexpr (M::TC)
+            load_core<W, NT>(to, from, stride, tokens, columns, tid);
+        else
+            load_tile<E, W, C, NT>(to, C * pitch(W), from, stride, tokens, columns, tid);
+    };
+    load(std::integral_constant<int, PD>(), smem + M::DO, dout + oo, os, n, P);
+    load(std::integral_constant<int, PD>(), smem + M::V, v + oo, os, n, P);
+    load(std::integral_constant<int, ND>(), smem + M::K, k + ko, ks, n, N);
+    load(std::integral_constant<int, ND>(), smem + M::Q, q + ko, ks, n, N);
     delta::wait_for_previous();  // (from here on: what the states' walk left)
     load_decays(smem + M::D, static_cast<const Decays<C>*>(w.decays) + bh * sh.nc + c, sizeof(Decays<C>), tid);
     cp_commit();
     const StateAt sb = state_at(w, sh, 0, bh, c, live, start), sa = state_at(w, sh, 1, bh, c, live, end);
-    StateTile<3, PD> tile;
+    StateTile<3, PD, M::TC> tile;
     if (sb.any()) {
         tile.fetch(sb, 0, N, P, tid);
         tile.put(smem + M::S, tid);
     }
     cp_wait<0>();
+    if (M::TC) Tensor::publish();
     __syncthreads();
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     const Part<C> part(warp);
@@ -795,18 +931,39 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
                 if (64 * sl >= N) break;
                 if (sl) {
                     tile.fetch(sb, sl, N, P, tid);
+                    if (M::TC) tensor.wait();
                     __syncthreads();
                     tile.put(smem + M::S, tid);
+                    if (M::TC) Tensor::publish();
                     __syncthreads();
                 }
-                times_state<NP, 3, C, PD, ND, CN, false>(acc, base + M::DO, base + M::S, block, colN, sl, P, N, lane);
+                if constexpr (M::TC) {
+                    if (tid == 0) {
+                        tc::fence_after_sync();
+                        issue_state<PD, ND, 3, false>(tensor_sh.tmem, base + M::DO, base + M::S, sl, P);
+                        tc::commit(&tensor_sh.done);
+                    }
+                    __syncwarp();
+                } else {
+                    times_state<NP, 3, C, PD, ND, CN, false>(acc, base + M::DO, base + M::S, block, colN, sl, P, N, lane);
+                }
             }
-            scale_rows(acc, scale * d.in[r0], scale * d.in[r0 + 8]);
-            a = dot_rows<NP, C, ND, CN>(acc, smem + M::Q, block, colN, N, lane);
+            if (!M::TC) {
+                scale_rows(acc, scale * d.in[r0], scale * d.in[r0 + 8]);
+                a = dot_rows<NP, C, ND, CN>(acc, smem + M::Q, block, colN, N, lane);
+            }
+        }
+        if (on) earlier_pairs<NP, QP, SP, C, PD, ND, CN, M::TC>(acc, base + M::DO, base + M::V, base + M::K, block, colN, P, N, scale, d, lane);
+        if constexpr (M::TC) {
+            if (sb.any()) {
+                tensor.wait();
+                a = add_state<ND, true>(acc, tensor_sh.tmem, scale * d.in[r0], scale * d.in[r0 + 8], smem + M::Q, block, N, warp, lane);
+                tc::fence_before_sync();  // (dk's product comes over this one behind the next barrier)
+            }
+        } else if (sizeof(E) == 2 && sb.any()) {
+            __syncthreads();  // (the stage lies over the state's planes)
         }
         if (lane % 4 == 0) s_aq[part.share][r0] = a.x, s_aq[part.share][r0 + 8] = a.y;
-        if (on) earlier_pairs<NP, QP, SP, C, PD, ND, CN>(acc, base + M::DO, base + M::V, base + M::K, block, colN, P, N, scale, d, lane);
-        if (sizeof(E) == 2 && sb.any()) __syncthreads();  // (the stage lies over the state's planes)
         if (parts)
             put_rows<float, ND, CN>(parts + po + nq * ps, ps, acc, 1.f, nullptr, colN, N, n - nq, rows - nq, lane);
         else
@@ -821,10 +978,11 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
         for (int sl = 0; sl < ND / 64; ++sl) {
             if (64 * sl >= N) break;
             tile.fetch(sa, sl, N, P, tid);
+            if (M::TC && sl) tensor.wait();
             __syncthreads();
             tile.put(smem + M::S, tid);
             if (both) {
-                using ST = StateTile<3, PD>;
+                using ST = StateTile<3, PD, M::TC>;
                 const int r = 64 * sl + tid / ST::PER, x = 4 * (tid % ST::PER);
 #pragma unroll
                 for (int e = 0; e < ST::K; ++e)
@@ -833,26 +991,38 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
                         dot = fmaf(u.x, y.x, fmaf(u.y, y.y, fmaf(u.z, y.z, fmaf(u.w, y.w, dot))));
                     }
             }
+            if (M::TC) Tensor::publish();
             __syncthreads();
-            times_state<NP, 3, C, PD, ND, CN, false>(dk, base + M::V, base + M::S, block, colN, sl, P, N, lane);
-            times_state<NP, SP, C, ND, PD, CP, true>(dv, base + M::K, base + M::S, block, colP, sl, N, P, lane);
+            if constexpr (M::TC) {
+                if (tid == 0) {
+                    tc::fence_after_sync();
+                    issue_state<PD, ND, 3, false>(tensor_sh.tmem, base + M::V, base + M::S, sl, P);
+                    issue_state<ND, PD, SP, true>(tensor_sh.tmem + ND, base + M::K, base + M::S, sl, N);
+                    tc::commit(&tensor_sh.done);
+                }
+                __syncwarp();
+            } else {
+                times_state<NP, 3, C, PD, ND, CN, false>(dk, base + M::V, base + M::S, block, colN, sl, P, N, lane);
+                times_state<NP, SP, C, ND, PD, CP, true>(dv, base + M::K, base + M::S, block, colP, sl, N, P, lane);
+            }
         }
-        scale_rows(dk, d.out[r0], d.out[r0 + 8]);
-        scale_rows(dv, d.out[r0], d.out[r0 + 8]);
-        own = dot_rows<NP, C, ND, CN>(dk, smem + M::K, block, colN, N, lane);
+        if (!M::TC) {
+            scale_rows(dk, d.out[r0], d.out[r0 + 8]);
+            scale_rows(dv, d.out[r0], d.out[r0 + 8]);
+            own = dot_rows<NP, C, ND, CN>(dk, smem + M::K, block, colN, N, lane);
+        }
     }
-    if (lane % 4 == 0) s_bk[part.share][r0] = own.x, s_bk[part.share][r0 + 8] = own.y;
     float wr[2] = {};  // sums of W over the tokens i
     if (on) {
-        const Rows<NP, C, ND> rk(base + M::K, block, N, lane);
-        const Rows<NP, C, PD> rv(base + M::V, block, P, lane);
+        const Rows<NP, C, ND, M::TC> rk(base + M::K, block, N, lane);
+        const Rows<NP, C, PD, M::TC> rv(base + M::V, block, P, lane);
         float row[2];
         row_factors<C, false>(row, d, block, scale, lane);
 #pragma unroll 1
         for (int o = block; o < last; ++o) {
             float sa_[2][4], sb_[2][4], m[2][4];
-            scores<NP, QP, C, ND>(sa_, rk, base + M::Q, o, N, lane);   // k_j . q_i
-            scores<NP, QP, C, PD>(sb_, rv, base + M::DO, o, P, lane);  // v_j . do_i
+            scores<NP, QP, C, ND, M::TC>(sa_, rk, base + M::Q, o, N, lane);   // k_j . q_i
+            scores<NP, QP, C, PD, M::TC>(sb_, rv, base + M::DO, o, P, lane);  // v_j . do_i
             if (o != block) {
                 pair_factors<C, false, false>(m, d, block, o, row, scale, lane);
             } else {
@@ -882,8 +1052,8 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
                 c0 += __shfl_xor_sync(0xffffffffu, c0, 4);
                 if (!(lane & 4) && part.share == 0) s_col[block][16 * o + (up ? 8 : 0) + 2 * (lane % 4) + (odd ? 1 : 0)] = c0;
             }
-            times_tokens<NP, SP, C, PD, CP>(dv, sa_, base + M::DO, colP, o, P, lane);
-            times_tokens<NP, SP, C, ND, CN>(dk, sb_, base + M::Q, colN, o, N, lane);
+            times_tokens<NP, SP, C, PD, CP, M::TC>(dv, sa_, base + M::DO, colP, o, P, lane);
+            times_tokens<NP, SP, C, ND, CN, M::TC>(dk, sb_, base + M::Q, colN, o, N, lane);
         }
     }
 #pragma unroll
@@ -891,6 +1061,13 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
         wr[0] += __shfl_xor_sync(0xffffffffu, wr[0], o);
         wr[1] += __shfl_xor_sync(0xffffffffu, wr[1], o);
     }
+    if constexpr (M::TC)
+        if (sa.any()) {
+            tensor.wait();
+            own = add_state<ND, true>(dk, tensor_sh.tmem, d.out[r0], d.out[r0 + 8], smem + M::K, block, N, warp, lane);
+            add_state<PD, false>(dv, tensor_sh.tmem + ND, d.out[r0], d.out[r0 + 8], nullptr, block, P, warp, lane);
+        }
+    if (lane % 4 == 0) s_bk[part.share][r0] = own.x, s_bk[part.share][r0 + 8] = own.y;
     if (lane % 4 == 0 && part.share == 0) s_row[r0] = wr[0], s_row[r0 + 8] = wr[1];
 #pragma unroll
     for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
@@ -953,6 +1130,7 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
             if (lane == 0) gg_part[blockIdx.x] = sum;
         }
     }
+    if (M::TC) tensor.end(M::COLUMNS, tid, status);
 }
 
 // Shared key heads: the sum over a key head's value heads, in their order.
@@ -1128,7 +1306,7 @@ cudaError_t backward(const LinattnArgs& a, void* ws, cudaStream_t st) {
     e = launch_behind(grad_kernel<E, ND, PD, C, FULL>, (unsigned)(sh.BH * sh.nc), M::BYTES, st, static_cast<const E*>(a.q),
                       static_cast<const E*>(a.k), static_cast<const E*>(a.v), static_cast<const E*>(a.dout), a.lens, a.h0 != nullptr,
                       a.dh_final != nullptr, static_cast<E*>(a.gq), static_cast<E*>(a.gk), static_cast<E*>(a.gv), parts,
-                      a.g_tokens ? a.gg : nullptr, gg_part, w, sh);
+                      a.g_tokens ? a.gg : nullptr, gg_part, w, sh, status_word());
     if (e != cudaSuccess) return e;
     if (parts) {
         const int64_t vectors = a.Bz * a.T * a.KH * (a.N / 4);

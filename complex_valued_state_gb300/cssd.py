@@ -221,6 +221,7 @@ STATUS_CHUNK_MMA_TIMEOUT = 2
 STATUS_BORN_MMA_TIMEOUT = 4
 STATUS_DELTA_TIMEOUT = 8
 STATUS_NORM_TIMEOUT = 16
+STATUS_LINATTN_TIMEOUT = 32
 
 
 def device_status(clear: bool = False, device=None, stream=None) -> int:

@@ -503,9 +503,10 @@ int cssd_layernorm_backward(int64_t rows, int64_t width, int xtype, int wtype, c
  * g is at most 0 in a model, though any value whose exponentials stay in range
  * works; -inf forgets everything before the token.  A NaN or infinity in a
  * token's inputs may reach any output of its chunk (up to 128 tokens) and what
- * follows; what lies at or past a row's length is never read.  No kernel spins
- * on memory (thread blocks that exchange states are one cluster), and nothing
- * depends on the order of atomics: the same call gives the same bits. */
+ * follows; what lies at or past a row's length is never read.  Every wait inside
+ * the kernels is bounded (see cssd_device_status; thread blocks that exchange
+ * states are one cluster), and nothing depends on the order of atomics: the
+ * same call gives the same bits. */
 
 /* Bytes of device workspace of cssd_linattn_forward and cssd_linattn_backward
  * (0 for invalid sizes): a state (4 N P bytes) and about 26 bytes a token of
@@ -611,7 +612,9 @@ int cssd_gated_norm_backward(int64_t rows, int64_t width, int64_t group, int xty
  *   4  Born attention: a tensor-core completion wait timed out
  *   8  the gated delta rule (16-bit forward or gradients): a wait for a copy,
  *      a tensor-core completion or another group of threads timed out
- *  16  the layer norm's gradients: a wait for a copy timed out
+ *  16  a norm's gradients (layer, add, gated): a wait for a copy timed out
+ *  32  linear attention (bfloat16 gradients with dstate or headdim above 64): a
+ *      tensor-core completion wait timed out
  * The chunked forward's bits also cover cssd_chunked_backward, the precise
  * and host-streamed forwards, which run the same kernel.  This call reads the
  * word of the stream's device (which must be the current device) after the

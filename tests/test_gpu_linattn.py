@@ -424,3 +424,20 @@ def test_states_in_place(cs, NP, dtype):
         o2, _ = cs.linattn_forward(**g, h0=state, h_final=state)
         cs.linattn_backward(**g, do=b["do"], dh_final=dh, h0=h0, grads={"gh0": dh})
         assert torch.equal(o, o2) and torch.equal(h, state) and torch.equal(r["gh0"], dh)
+
+
+@pytest.mark.parametrize("NP", [(128, 128), (128, 64), (64, 128), (112, 80)])
+def test_wide_gradients_side_by_side(cs, NP):
+    """The wide bfloat16 gradients (products on the tensor cores' own memory): many blocks at once and two streams
+    at once give the bits of one call after another, and no wait inside a kernel gives up."""
+    d, opt, back = make(20, 2, 900, 12, 6, *NP, dtype="bf16", state=True, ragged=[900, 517])
+    g, o_, b = on(d), on(opt), on(back)
+    want = cs.linattn_backward(**g, **b, **o_)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [cs.linattn_backward(**g, **b, **o_, stream=streams[i % 2]) for i in range(6)]
+    torch.cuda.synchronize()
+    for r in got:
+        for n in want:
+            assert torch.equal(r[n], want[n]), n
+    assert cs.device_status() == 0
