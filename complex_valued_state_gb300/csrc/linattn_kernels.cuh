@@ -92,6 +92,29 @@ struct Part {
     }
 };
 
+// float32 tensors (three planes): the products other than the leading planes' are summed apart and added at the end.
+// The matrix instruction drops what lies below its sum's last bit, at every one of its steps (outputs of 128/128
+// were off by 1.1e-6 in the 2-norm where plain fp32 arithmetic is off by 2.5e-7).
+template <int NPL, int N>
+struct Rest {
+    float v[NPL == 3 ? N : 1][4];
+    __device__ __forceinline__ Rest() {
+#pragma unroll
+        for (auto& t : v)
+#pragma unroll
+            for (float& x : t) x = 0.f;
+    }
+    // where the product of planes i and j of sum n goes
+    __device__ __forceinline__ float (&of(float (&acc)[N][4], int n, int ij))[4] { return NPL == 3 && ij > 0 ? v[NPL == 3 ? n : 0] : acc[n]; }
+    __device__ __forceinline__ void add_to(float (&acc)[N][4]) const {
+        if constexpr (NPL == 3)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] += v[n][e];
+    }
+};
+
 // acc += A S (or A S^T) of 16 rows and columns col0.. (CW of them): one slice of 64 of the state's rows n, as SP
 // planes at `s`.  A is a tile [token][column] of NPL planes.
 //   TRANS   A's columns are n, the outputs are p:  acc[., p] += sum_n A[., n] S[n][p]
@@ -103,6 +126,7 @@ __device__ __forceinline__ void times_state(float (&acc)[CW / 8][4], uint32_t a,
     using TS = Tile<false, 64, TRANS ? OW : KW>;
     constexpr int KT = TRANS ? imin(4, KW / 16) : KW / 16;
     const int k0 = TRANS ? 64 * sl : 0;
+    Rest<NPL, CW / 8> rest;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
         if (k0 + 16 * kt >= kw) break;
@@ -131,11 +155,12 @@ __device__ __forceinline__ void times_state(float (&acc)[CW / 8][4], uint32_t a,
                         const int col = col0 + 16 * nt;
                         if (col >= ow) break;
                         if (!TRANS && col / 64 != sl) continue;
-                        mma(acc[2 * nt], af[i], bf[nt][0], bf[nt][1]);
-                        mma(acc[2 * nt + 1], af[i], bf[nt][2], bf[nt][3]);
+                        mma(rest.of(acc, 2 * nt, i + j), af[i], bf[nt][0], bf[nt][1]);
+                        mma(rest.of(acc, 2 * nt + 1, i + j), af[i], bf[nt][2], bf[nt][3]);
                     }
         }
     }
+    rest.add_to(acc);
 }
 
 // The operands A of the scores: kept in registers where they are one plane of at most 64 columns.
@@ -157,6 +182,10 @@ template <int NPL, int QP, int C, int KW, bool TC>
 __device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW, TC>& a, uint32_t b, int o, int kw, int lane) {
     using TB = Tile<TC, C, KW>;
     const uint32_t at = TB::template at<true>(b, o, 0, lane);
+    Rest<NPL, 2> rest;
+    if (NPL > 1)
+#pragma unroll
+        for (auto& t : sc) t[0] = t[1] = t[2] = t[3] = 0.f;
 #pragma unroll
     for (int kt = 0; kt < KW / 16; ++kt) {
         if (16 * kt >= kw) break;
@@ -187,17 +216,13 @@ __device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW,
 #pragma unroll
                 for (int i = NPL - 1; i >= 0; --i)
                     if (i + j < QP) {
-                        if (kt == 0 && j == NPL - 1 && i == imin(NPL - 1, QP - NPL)) {
-                            mma_first(sc[0], af[i], bf[0], bf[1]);
-                            mma_first(sc[1], af[i], bf[2], bf[3]);
-                        } else {
-                            mma(sc[0], af[i], bf[0], bf[1]);
-                            mma(sc[1], af[i], bf[2], bf[3]);
-                        }
+                        mma(rest.of(sc, 0, i + j), af[i], bf[0], bf[1]);
+                        mma(rest.of(sc, 1, i + j), af[i], bf[2], bf[3]);
                     }
             }
         }
     }
+    rest.add_to(sc);
 }
 // The factors scale M of a block's pairs: the warp's rows (the later tokens if LOWER, else the earlier ones) with
 // the tokens of block `o`; 0 where the pair is none.  `row`: scale times the rows' own factors.
@@ -250,6 +275,7 @@ __device__ __forceinline__ void times_tokens(float (&acc)[CW / 8][4], const floa
     using TZ = Tile<TC, C, OW>;
     const uint32_t at = TZ::template at<false>(z, o, col0, lane);
     constexpr int NG = imin(CW / 16, 4);  // 64 columns at a time
+    Rest<NPL, CW / 8> rest;
 #pragma unroll
     for (int n0 = 0; n0 < CW / 16; n0 += NG)
 #pragma unroll
@@ -264,10 +290,11 @@ __device__ __forceinline__ void times_tokens(float (&acc)[CW / 8][4], const floa
 #pragma unroll
                     for (int nt = 0; nt < NG; ++nt)
                         if (col0 + 16 * (n0 + nt) < ow) {
-                            mma(acc[2 * (n0 + nt)], p[i], bf[nt][0], bf[nt][1]);
-                            mma(acc[2 * (n0 + nt) + 1], p[i], bf[nt][2], bf[nt][3]);
+                            mma(rest.of(acc, 2 * (n0 + nt), i + j), p[i], bf[nt][0], bf[nt][1]);
+                            mma(rest.of(acc, 2 * (n0 + nt) + 1, i + j), p[i], bf[nt][2], bf[nt][3]);
                         }
         }
+    rest.add_to(acc);
 }
 // acc = sum over the blocks at or before the warp's of (A B^T, decayed) Z.
 template <int NPL, int QP, int PP, int C, int KW, int OW, int CW, bool TC>

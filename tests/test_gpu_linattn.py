@@ -441,3 +441,21 @@ def test_wide_gradients_side_by_side(cs, NP):
         for n in want:
             assert torch.equal(r[n], want[n]), n
     assert cs.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "fp32"])
+@pytest.mark.parametrize("NP", [(64, 64), (128, 128), (128, 64), (16, 32)])
+def test_float32_results_are_float32(cs, NP, dtype):
+    """Every float32 result (all of float32 tensors; states and their gradients, and g's, of float16 ones) is within
+    1e-6 of the 64-bit one in the 2-norm: a sum of up to 128 products (a random walk of 2^-24 each, 7e-7) twice over
+    is 1e-6, and most sums are shorter."""
+    d, opt, back = make(21, 1, 400, 2, 1, *NP, dtype=dtype, state=True)
+    o, h = cs.linattn_forward(**on(d), **on(opt))
+    r = cs.linattn_backward(**on(d), **on(back), **on(opt))
+    n, m, b = np64(d), np64(opt), np64(back)
+    wo, wh, _ = ref.linattn_forward(n["q"], n["k"], n["v"], n["g"], NP[0] ** -0.5, m["h0"])
+    w = ref.linattn_backward(n["q"], n["k"], n["v"], n["g"], NP[0] ** -0.5, b["do"], m["h0"], b["dh_final"])
+    for name, x, y in [("o", o, wo), ("h", h, wh)] + [(k, r[k], w[k]) for k in ("gq", "gk", "gv", "gg", "gh0")]:
+        if x.dtype == torch.float32:
+            off = np.linalg.norm(x.cpu().double().numpy() - y) / np.linalg.norm(y)
+            assert off < 1e-6, (name, off)
