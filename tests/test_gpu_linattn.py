@@ -459,3 +459,15 @@ def test_float32_results_are_float32(cs, NP, dtype):
         if x.dtype == torch.float32:
             off = np.linalg.norm(x.cpu().double().numpy() - y) / np.linalg.norm(y)
             assert off < 1e-6, (name, off)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("NP", [(64, 64), (128, 128), (128, 32), (96, 80)])
+@pytest.mark.parametrize("head", [False, True])
+def test_no_decay_no_gradient(cs, NP, head, dtype):
+    """Rows of at most one token without a state before it: nothing decays, so the gradient of g is zero, to the bit."""
+    for B, T, lens in ((3, 1, None), (4, 2, [0, 1, 1, 0]), (3, 300, [1, 0, 1])):
+        d, opt, back = make(22, B, T, 4, 2, *NP, dtype=dtype, ragged=lens, head=head)
+        r = cs.linattn_backward(**on(d), **on(back), **on(opt))
+        assert r["gg"].shape == d["g"].shape and not r["gg"].any()
+        assert r["gq"].any() and r["gk"].any() and r["gv"].any()
