@@ -11,9 +11,11 @@
 //     dv_j  = e^{G_end - G_j} k_j dS+   + scale sum_i M_ij (q_i.k_j) do_i
 //     dS    = e^{G_end} dS+ + sum_i scale e^{G_i} q_i do_i^T
 //     dg_t  = e^{G_end} <S, dS+> + sum_{j < t} b_j + sum_{u >= t} (a_u + sum_j W_uj - sum_i W_iu)
-// with a_u, b_j the first terms' shares of q_u.dq_u and k_j.dk_j.  (dg_t = <e^{g_t} S_{t-1}, dL/dS_t>, every pair
-// and every state's term that spans t; W is made from the scores in fp32, so that dg does not see the splitting of
-// the operands.)
+// with a_u, b_j the first terms' shares of q_u.dq_u and k_j.dk_j, and W without its diagonal.  (dg_t = <e^{g_t}
+// S_{t-1}, dL/dS_t>, every pair and every state's term that spans t.  The pairs after t cancel in the sum up to its
+// rounding, about 2^-24 of their sizes; with the diagonal, which spans no decay, that would be 2^-24 of the tokens' own
+// writes: a head with g = -10 was off by 0.2 to 0.7 % in the 2-norm.  W is made from the scores in fp32, so that dg
+// does not see the splitting of the operands.)
 //
 // Two kernels:
 //   states   walks the chunks of a row and head and leaves the state before each chunk; for the gradients the same
@@ -1066,6 +1068,13 @@ __global__ void __launch_bounds__(NT, GradSmem<E, ND, PD, C>::CTAS)
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) ws[x][e] = sa_[x][e] * sb_[x][e];
+            if (o == block) {  // (a token's own write spans no decay)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 2 * x; e < 2 * x + 2; ++e)
+                        if (2 * (lane % 4) + e % 2 == lane / 4) ws[x][e] = 0.f;
+            }
             multiply(sb_, m);
             wr[0] += (ws[0][0] + ws[0][1]) + (ws[1][0] + ws[1][1]);
             wr[1] += (ws[0][2] + ws[0][3]) + (ws[1][2] + ws[1][3]);

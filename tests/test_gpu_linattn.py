@@ -471,3 +471,25 @@ def test_no_decay_no_gradient(cs, NP, head, dtype):
         r = cs.linattn_backward(**on(d), **on(back), **on(opt))
         assert r["gg"].shape == d["g"].shape and not r["gg"].any()
         assert r["gq"].any() and r["gk"].any() and r["gv"].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("NP", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("head", [False, True])
+def test_decay_gradients_of_heads_that_forget_fast(cs, NP, head, dtype):
+    """The gradient of g where a token keeps e^-5 or e^-10 of the state: of the size of what is kept, and right to
+    float32 there.  A token's spanning pairs carry the quick exponential's error ((2 + 1.2 |g|) 2^-23 at most, 1.7e-6 at -10),
+    their scores' (a random walk of at most 128 products, 7e-7) and, of the running sums over the chunk's 128 tokens,
+    a random walk of 2^-24 of those pairs' sizes, 7e-7 again: below 4e-6 of the gradient's 2-norm over the tokens, and (one
+    decay a head: the tokens' sum) of the tokens' sizes summed up."""
+    d, opt, back = make(23, 1, 300, 4, 4, *NP, dtype=dtype, state=True, head=head)
+    d["g"][:] = torch.tensor([-3.0, -5.0, -10.0, -14.0])
+    r = cs.linattn_backward(**on(d), **on(back), **on(opt), scale=0.25)
+    n, m, b = np64(d), np64(opt), np64(back)
+    w = ref.linattn_backward(n["q"], n["k"], n["v"], np.broadcast_to(n["g"], (1, 300, 4)), 0.25, b["do"], m["h0"], b["dh_final"])["gg"]
+    got = r["gg"].cpu().double().numpy()
+    for h in range(4):
+        if head:
+            assert abs(got[h] - w[..., h].sum()) < 4e-6 * np.abs(w[..., h]).sum(), h
+        else:
+            assert np.linalg.norm(got[..., h] - w[..., h]) < 4e-6 * np.linalg.norm(w[..., h]), h
