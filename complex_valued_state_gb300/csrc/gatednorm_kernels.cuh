@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) gated_rows(GatedNormArg
             unpack<E>(zr[n][i], z[i]);
 #pragma unroll
             for (int u = 0; u < V; ++u) {
-                z[i][u] *= sigmoid(z[i][u]);
+                z[i][u] *= sigmoid<E>(z[i][u]);
                 if (a.gate_first) f[i][u] *= z[i][u];
             }
         }
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256) gated_stream(GatedNormArgs a) {
             const float xv = to_f(x[c]);
             if (!a.gate_first) return xv;
             const float zv = to_f(z[c]);
-            return xv * (zv * sigmoid(zv));
+            return xv * (zv * sigmoid<E>(zv));
         };
         float t = 0.f;
         if (a.layer)
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) gated_stream(GatedNormArgs a) {
             float v = fmaf((h(c) - m) * r, at_or(w, c0 + c, 1.f), at_or(b, c0 + c, 0.f));
             if (!a.gate_first) {
                 const float zv = to_f(z[c]);
-                v *= zv * sigmoid(zv);
+                v *= zv * sigmoid<E>(zv);
             }
             y[c] = from_f<E>(v);
         }
@@ -129,8 +129,9 @@ __global__ void __launch_bounds__(256) gated_stream(GatedNormArgs a) {
 }
 
 // What a column needs of the gate: silu and its slope.
+template <typename E>
 __device__ __forceinline__ void gate_of(float z, float& gate, float& slope) {
-    const float s = sigmoid(z);
+    const float s = sigmoid<E>(z);
     gate = z * s;
     slope = s * fmaf(z, 1.f - s, 1.f);
 }
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) gated_back_ring(GatedNormAr
                 load<float, V>(sw + v * V, w);
 #pragma unroll
                 for (int u = 0; u < V; ++u) {
-                    sg[i][u] = sigmoid(z[u]);
+                    sg[i][u] = sigmoid<E>(z[u]);
                     const float gate = z[u] * sg[i][u];
                     const float hh = ((FIRST ? x[u] * gate : x[u]) - m[i]) * r[i], du = FIRST ? d[u] : d[u] * gate, g = du * w[u];
                     s1[i] += g;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(256) gated_back_sums(GatedNormArgs a, float2* 
         float s1 = 0.f, s2 = 0.f;
         for (int64_t c = tid; c < a.group; c += TEAM) {
             float gate, slope, xv = to_f(static_cast<const E*>(a.x)[at + c]), d = to_f(static_cast<const E*>(a.dy)[at + c]);
-            gate_of(to_f(static_cast<const E*>(a.z)[at + c]), gate, slope);
+            gate_of<E>(to_f(static_cast<const E*>(a.z)[at + c]), gate, slope);
             (a.gate_first ? xv : d) *= gate;
             const float g = d * at_or(w, c0 + c, 1.f);
             s1 += g;
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(256) gated_back_cols(GatedNormArgs a, const fl
             const int64_t i = row * width + c, u = row * groups + gi;
             const float m = a.layer ? a.mean[u] : 0.f, r = a.rstd[u], xv = to_f(x[i]), d = to_f(dy[i]);
             float gate, slope;
-            gate_of(to_f(z[i]), gate, slope);
+            gate_of<E>(to_f(z[i]), gate, slope);
             const float hh = ((a.gate_first ? xv * gate : xv) - m) * r, du = a.gate_first ? d : d * gate;
             const float2 t = sums[u];
             const float dh = r * (du * wv - t.x - hh * t.y);

@@ -308,3 +308,22 @@ def test_a_layer(cs):
     assert torch.equal(kept, s)
     # (the products in front are a library's, whose sums of 256 terms may go another way: 256 2^-24 of their sizes, before a norm)
     close(got, f64(whole.cpu()), "layer", top=np.abs(f64(whole.cpu())).max(), inner=2e-4)
+
+
+@pytest.mark.parametrize("group", [64, 50, 1500])
+def test_float32_gates_are_float32(cs, group):
+    """Every element of float32 results, with gates from -80 to 20.  With the rstd that came back the norm is one
+    product.  Steps of 2^-24: the gate's exponential 2, the sum 1, the quick quotient 4, its product with z 1, the norm 1
+    and its product with the gate 1: 10 of y.  gz is the norm times the slope s (1 + z (1 - s)): s 7, 1 - s and the bracket
+    (below z = -3 of size |z| - 1 or more) 1 each and 1.5 times more for the 1 beside z, what s moves in it 0.5, the two products
+    and the norm 3: below 14 of gz."""
+    z = torch.linspace(-80, 20, 300 * group).reshape(300, group).flip(0).contiguous()
+    x = torch.rand(z.shape, generator=torch.Generator().manual_seed(8)) + 0.5
+    y, _, rstd = cs.gated_norm(x.cuda(), z.cuda())
+    hh = f64(x) * f64(rstd.cpu())
+    close(y, hh * ref.silu(f64(z)), "y", top=np.abs(hh * ref.silu(f64(z))), inner=10 * 2.0 ** -24)
+    g = cs.gated_norm_backward(torch.ones_like(x).cuda(), x.cuda(), z.cuda(), None, None, None, rstd)
+    s = 1 / (1 + np.exp(-f64(z)))
+    want, low = hh * s * (1 + f64(z) * (1 - s)), f64(z) < -3
+    err = np.abs(f64(g["gz"].cpu()) - want)[low] / np.abs(want)[low]
+    assert (err <= 14 * 2.0 ** -24).all(), err.max() * 2 ** 24
