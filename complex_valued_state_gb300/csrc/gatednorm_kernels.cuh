@@ -373,8 +373,11 @@ cudaError_t gated_bwd(const GatedNormArgs& a, void* ws, cudaStream_t st) {
     if (ring) {
         const cudaError_t e = by_plan(plan, [&](auto g, auto i) {
             constexpr int G = decltype(g)::value, IT = decltype(i)::value;
-            const int64_t slices = lanes ? 1 : groups, want = (a.rows + kRowWarps / G - 1) / (kRowWarps / G), most = kBackGrid / slices;
-            n = (int)(want < most ? want : most);
+            // CTAs a group: what fills the SMs, and with many groups so many that a thread adds up 64 rows in fp32
+            // (as many as the partial sums have room for; 20000 rows of 304 groups, one CTA each: 620 2^-24 off)
+            const int64_t slices = lanes ? 1 : groups, NG = kRowWarps / G, want = (a.rows + NG - 1) / NG;
+            const int64_t fill = kBackGrid / slices, few = grid_of((a.rows + 64 * NG - 1) / (64 * NG), kBackGrid);
+            n = (int)grid_of(want, fill > few ? fill : few);
             auto go = [&](auto first) {
                 constexpr bool FIRST = decltype(first)::value;
                 const cudaError_t e = delta::allow<gated_back_ring<E, IT, G, FIRST>>(220 << 10);

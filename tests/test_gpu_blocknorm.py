@@ -327,3 +327,21 @@ def test_float32_gates_are_float32(cs, group):
     want, low = hh * s * (1 + f64(z) * (1 - s)), f64(z) < -3
     err = np.abs(f64(g["gz"].cpu()) - want)[low] / np.abs(want)[low]
     assert (err <= 14 * 2.0 ** -24).all(), err.max() * 2 ** 24
+
+
+@pytest.mark.parametrize("widths", [(7296, 24), (4800, 24), (960, 80), (7296, 912)])
+def test_sums_over_many_rows_of_many_groups(cs, widths):
+    """Equal rows, whose sums are known: the gradients of the weights over 20000 of them are within (rows / 304 + 64)
+    2^-24 of the sums, as everywhere, however many groups share the blocks, and 10 2^-24 for a row's own products."""
+    (D, group), R = widths, 20000
+    r = np.random.default_rng(9)
+    x, z, dy = (t(np.abs(r.standard_normal(D)) + 0.1, "bf16") for _ in range(3))
+    X, Z, DY = (v.cuda().expand(R, D).contiguous() for v in (x, z, dy))
+    rstd = cs.gated_norm(X, Z, group=group)[2]
+    assert (rstd == rstd[0]).all()
+    g = cs.gated_norm_backward(DY, X, Z, None, None, None, rstd, group=group, wdtype=torch.float32)
+    du = f64(dy) * ref.silu(f64(z))
+    hh = f64(x) * np.repeat(f64(rstd[0].cpu()), group)
+    for n, want in (("gbias", R * du), ("gweight", R * du * hh)):
+        off = np.abs(f64(g[n].cpu()) / want - 1).max() * 2 ** 24
+        assert off <= R / 304 + 64 + 10, (n, off)
