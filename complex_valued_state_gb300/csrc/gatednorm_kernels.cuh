@@ -366,7 +366,9 @@ cudaError_t gated_bwd(const GatedNormArgs& a, void* ws, cudaStream_t st) {
         lanes = (int)gv;
         ring = plan_ring(a.width / V, V, (size_t)3 * a.width * sizeof(E), (size_t)8 * a.width, plan);
     }
-    if (!ring && a.group % V == 0 && groups <= kBackGrid) {
+    // (a warp a group at least: narrow ones are streamed.  8192 x 2040, us, ring and streamed: groups of 3 vectors 393 and
+    // 200, of 5 261 and 185, of 6 234 and 171 but 31 and 49 for 1000 rows, of 10 158 and 143 (29 and 43), of 20 69 and 126)
+    if (!ring && a.group % V == 0 && groups <= kBackGrid && gv >= 6) {
         lanes = 0;
         ring = plan_ring(gv, V, (size_t)3 * a.group * sizeof(E), (size_t)8 * a.group, plan);
     }

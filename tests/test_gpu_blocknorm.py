@@ -329,7 +329,7 @@ def test_float32_gates_are_float32(cs, group):
     assert (err <= 14 * 2.0 ** -24).all(), err.max() * 2 ** 24
 
 
-@pytest.mark.parametrize("widths", [(7296, 24), (4800, 24), (960, 80), (7296, 912)])
+@pytest.mark.parametrize("widths", [(7296, 24), (14592, 48), (960, 80), (7296, 912)])
 def test_sums_over_many_rows_of_many_groups(cs, widths):
     """Equal rows, whose sums are known: the gradients of the weights over 20000 of them are within (rows / 304 + 64)
     2^-24 of the sums, as everywhere, however many groups share the blocks, and 10 2^-24 for a row's own products."""
