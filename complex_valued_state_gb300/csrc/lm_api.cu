@@ -287,6 +287,8 @@ int cssd_layernorm_backward(int64_t rows, int64_t width, int xtype, int wtype, c
 static int check_linattn_dims(const cssd_delta_dims* d, int dtype, bool need_seq) {
     const int s = check_delta_dims(d, dtype, need_seq);
     if (s != CSSD_OK || !need_seq) return s;
+    // tokens, rounded up to chunks of 128, in 32 bits
+    if (d->seqlen > kMaxInt - 127) return CSSD_ERR_DIMS;
     // (row and head, chunk) in 32 bits, for the smallest chunk
     return product_fits(d->batch * d->nheads, (d->seqlen + 31) / 32, kMaxInt) ? CSSD_OK : CSSD_ERR_DIMS;
 }

@@ -494,7 +494,8 @@ int cssd_layernorm_backward(int64_t rows, int64_t width, int xtype, int wtype, c
  * g is a log decay: one a token and head (g_tokens nonzero) or one a head
  * (g_tokens 0: float32 [nheads]).  Sizes, types, layouts, shared key heads,
  * alignment and the meaning of `lens` are those of the gated delta rule above;
- * batch * nheads * (seqlen / 32, rounded up) below 2^31.
+ * batch * nheads * (seqlen / 32, rounded up) below 2^31, and seqlen at most
+ * 2^31 - 128.
  *
  * Sums and states are kept to fp32 accuracy whatever the type.  What 16-bit
  * outputs are made from is held to 16 significant bits (2^-17 relative) before

@@ -249,3 +249,15 @@ def test_binding_rejects_wrong_tensors():
         cssd.add_norm_backward(h, None, None, h, None, None, torch.zeros(4), wdtype=torch.float32)
     with pytest.raises(TypeError):
         cssd.add_norm_backward(h, None, None, h, None, None, torch.zeros(4), wdtype=torch.bfloat16)
+
+
+def test_linattn_longest_sequences(lib):
+    """A length that rounded up to chunks of 128 tokens leaves 32 bits is refused, by both calls and their sizes."""
+    for dtype in (0, 1, 2):
+        for T, ok in (((1 << 31) - 128, True), ((1 << 31) - 127, False), ((1 << 31) - 65, False)):
+            d = dims(1, T, 1, 1, 16, 16)
+            assert (lib.cssd_linattn_workspace_bytes(d, dtype) > 0) == ok and (lib.cssd_linattn_backward_workspace_bytes(d, dtype) > 0) == ok
+            if not ok:
+                p = ptrs(13)
+                assert lib.cssd_linattn_forward(d, dtype, *p[:4], 1, ctypes.c_float(1.0), *p[4:8], None, 0, None) == -2
+                assert lib.cssd_linattn_backward(d, dtype, *p[:4], 1, ctypes.c_float(1.0), *p[4:], None, 0, None) == -2
