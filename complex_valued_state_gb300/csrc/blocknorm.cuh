@@ -15,8 +15,8 @@
 // for the join (227 MB: 5.0 TB/s with it); gated by heads of 64 17 us (76 MB: 4.4 TB/s; issue 76 % busy: the gate's
 // exponential and reciprocal), gradients over whole rows 32 and 4 (126 MB: 3.5 TB/s).  Widths that are no whole
 // 16-byte vectors, rows too wide for the registers or the ring, and the gradients of narrow groups that are no power of
-// two of vectors, take the streaming kernels, which read a row
-// again from the caches for each sum: 47, 93, 102 and 117 us for these cases.
+// two of vectors, take the streaming kernels, which read a row again from the caches for each sum: 47, 93, 102 and
+// 117 us for these cases.
 
 #include <initializer_list>
 #include <type_traits>
