@@ -345,3 +345,104 @@ def test_sums_over_many_rows_of_many_groups(cs, widths):
     for n, want in (("gbias", R * du), ("gweight", R * du * hh)):
         off = np.abs(f64(g[n].cpu()) / want - 1).max() * 2 ** 24
         assert off <= R / 304 + 64 + 10, (n, off)
+
+
+def check_add(cs, R, D, kind, types, bias=True, scale=True, ds=True, wants=True):
+    """One call and its gradients; ds: something else reaches s; wants: the vectors' gradients are asked for (x is not read without)."""
+    (xt, rt, wt), layer = types, kind == "layer"
+    r = np.random.default_rng(R + D)
+    w, b, sc = vectors(r, D, wt, bias)
+    sc = sc if scale else None
+    x, res, dy, ds_ = (t(r.standard_normal((R, D)) * np.exp(r.standard_normal((R, 1))) + r.standard_normal((R, 1)), k) for k in (xt, rt, xt, rt))
+    ds_ = ds_ if ds else None
+    y, s, mean, rstd = cs.add_norm(dev(x), dev(res), dev(w), dev(b), kind=kind, alpha=0.7, scale=dev(sc), eps=EPS)
+    kept = f64(s.cpu())
+    # (alpha in fp32: 2^-25 of the term; the products and the sum 2^-24 each)
+    close(s, f64(res) + 0.7 * f64(x) * (1 if sc is None else f64(sc)), "s", top=np.abs(f64(res)) + np.abs(f64(x)) * (1 if sc is None else np.abs(f64(sc))),
+          inner=2.0 ** -22)
+    wy, _, wm, wr = ref.add_norm(0 * kept, kept, f64(w), f64(b), layer, 0.0, None, EPS)
+    amp = np.abs(kept).max(1, keepdims=True) * wr[:, None]
+    close(y, wy, "y", top=amp * 2 + np.abs(wy).max(1, keepdims=True))
+    close(rstd, wr, "rstd", top=wr, inner=INNER * (1 + (np.abs(wm) * wr) ** 2) if layer else INNER)
+    if layer:
+        close(mean, wm, "mean", top=np.abs(kept).max(1))
+    want = ref.add_norm_backward(f64(dy), f64(ds_), f64(x), kept, f64(w), layer, 0.7, f64(sc), EPS)
+    g = cs.add_norm_backward(dev(dy), dev(ds_), dev(x) if wants else None, s, dev(w), mean, rstd, alpha=0.7, scale=dev(sc), want_weight=wants,
+                             want_bias=bias and wants, want_scale=scale and wants)
+    assert set(g) == {"gx", "gresidual"} | ({"gweight"} if wants else set()) | ({"gbias"} if bias and wants else set()) | ({"gscale"} if scale and wants else set())
+    size = wr[:, None] * np.abs(f64(dy)).max(1, keepdims=True) * np.abs(f64(w)).max() * (1 + amp)
+    size = size + (np.abs(f64(ds_)).max(1, keepdims=True) if ds else 0)
+    close(g["gresidual"], want["gresidual"], "gresidual", top=size)
+    close(g["gx"], want["gx"], "gx", top=size)
+    for n in set(g) - {"gx", "gresidual"}:
+        columns(g[n], want[n], want[n + "_terms"], R, n)
+
+
+def check_gated(cs, R, D, group, kind, first, types, bias=True):
+    (xt, wt), layer = types, kind == "layer"
+    r = np.random.default_rng(R + D + group)
+    w, b = vectors(r, D, wt, bias, 2)
+    x, z, dy = (t(r.standard_normal((R, D)) * np.exp(r.standard_normal((R, 1))) + m * r.standard_normal((R, 1)), xt) for m in (1, 1, 0))
+    y, mean, rstd = cs.gated_norm(dev(x), dev(z), dev(w), dev(b), kind=kind, group=group, gate_first=first, eps=EPS)
+    X, Z, DY, W, B = (f64(v) for v in (x, z, dy, w, b))
+    wy, wm, wr = ref.gated_norm(X, Z, W, B, layer, group, first, EPS)
+    gate = np.abs(ref.silu(Z))
+    peak = np.abs((X * ref.silu(Z) if first else X).reshape(R, -1, group)).max(2)
+    wide = lambda v: np.repeat(v, group, axis=1)  # noqa: E731
+    amp = wide(peak * wr)
+    out = (2 * amp * (1 + np.abs(W)) + (0 if B is None else np.abs(B))) * (1 if first else gate)
+    zed = 1 + np.abs(Z).max() / 64
+    close(y, wy, "y", top=out, inner=INNER * zed)
+    close(rstd, wr, "rstd", top=wr, inner=INNER * zed * (1 + (np.abs(wm) * wr).max() ** 2))
+    if layer:
+        close(mean, wm, "mean", top=peak, inner=INNER * zed)
+    want = ref.gated_norm_backward(DY, X, Z, W, B, layer, group, first, EPS)
+    g = cs.gated_norm_backward(dev(dy), dev(x), dev(z), dev(w), dev(b), mean, rstd, group=group, gate_first=first, want_bias=bias)
+    assert set(g) == {"gx", "gz", "gweight"} | ({"gbias"} if bias else set())
+    du = np.abs(DY) * (1 if first else gate)
+    dh = wide(wr * (du * np.abs(W)).reshape(R, -1, group).max(2)) * (2 + 2 * amp * wide(peak * wr))
+    top = {"gx": dh * (gate if first else 1), "gz": 1.2 * (dh * np.abs(X) if first else np.abs(DY) * out / np.maximum(gate, 1e-30))}
+    for n in ("gx", "gz"):
+        close(g[n], want[n], n, top=top[n], inner=INNER * zed)
+    for n in set(g) - {"gx", "gz"}:
+        columns(g[n], want[n], want[n + "_terms"], R, n)
+
+
+# Rows enough that every group of warps takes five or six one after another: each buffer of the ring is filled again, in
+# both of its barrier's phases, and the last round is ragged.
+@pytest.mark.parametrize("case", [
+    (12163, 64, "rms", ("bf16", "fp32", "bf16")), (12163, 512, "layer", ("bf16", "bf16", "fp32")), (6083, 1000, "rms", ("fp16", "fp16", "fp16")),
+    (3043, 1536, "layer", ("bf16", "fp32", "fp32")), (6083, 1536, "rms", ("bf16", "bf16", "bf16")), (1523, 4096, "rms", ("bf16", "fp32", "bf16")),
+    (3043, 1536, "rms", ("fp32", "fp32", "fp32")), (12163, 128, "layer", ("fp32", "fp32", "fp32")), (6083, 333, "layer", ("bf16", "fp32", "bf16"))])
+@pytest.mark.parametrize("given", [(True, True), (False, True), (True, False), (False, False)])
+def test_add_norm_over_many_rows(cs, case, given):
+    R, D, kind, types = case
+    check_add(cs, R, D, kind, types, ds=given[0], wants=given[1])
+
+
+@pytest.mark.parametrize("case", [
+    (12163, 256, 64, ("bf16", "bf16")), (6083, 1536, 64, ("bf16", "fp32")), (1523, 4096, 128, ("bf16", "bf16")), (3043, 1536, 64, ("fp32", "fp32")),
+    (6083, 1536, 1536, ("bf16", "fp32")), (1523, 4096, 4096, ("fp16", "fp16")), (3043, 2048, 512, ("bf16", "bf16")), (1003, 960, 80, ("bf16", "fp32")),
+    (3043, 960, 96, ("fp32", "fp32")), (12163, 64, 64, ("fp16", "fp32")), (3043, 960, 24, ("bf16", "bf16")), (6083, 333, 111, ("bf16", "bf16"))])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("first", [False, True])
+def test_gated_norm_over_many_rows(cs, case, kind, first):
+    R, D, group, types = case
+    check_gated(cs, R, D, group, kind, first, types)
+
+
+# Each vector there or not, on every path: rows in registers and rings, streamed rows, narrow and wide ones.
+@pytest.mark.parametrize("types", [("bf16", "fp32", "bf16"), ("fp16", "fp16", "fp32"), ("fp32", "fp32", "fp32")])
+@pytest.mark.parametrize("D", [5, 8, 333, 1001, 1536, 2048, 2056, 8200])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("scale", [False, True])
+def test_add_norm_vectors(cs, D, types, bias, scale):
+    check_add(cs, 41, D, "layer" if D % 16 else "rms", types, bias=bias, scale=scale)
+
+
+@pytest.mark.parametrize("types", [("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("widths", [(5, 5), (64, 16), (333, 333), (960, 80), (960, 24), (1001, 143), (1536, 64), (1536, 1536), (2048, 512), (2056, 2056)])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("first", [False, True])
+def test_gated_norm_vectors(cs, widths, types, bias, first):
+    check_gated(cs, 41, *widths, "layer" if widths[1] % 16 else "rms", first, types, bias)
