@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(128) states_kernel(const E* __restrict__ q, co
     constexpr int NP = M::NP, THREADS = M::THREADS, HT = M::HT, HALVES = C / HT, STAGES = M::STAGES, BATCH = M::BATCH;
     extern __shared__ __align__(128) unsigned char smem[];
     float* weights = reinterpret_cast<float*>(smem + M::W);  // [BATCH][C]
-    float* totals = weights + BATCH * C;                     // [BATCH]
+    float2* totals = reinterpret_cast<float2*>(weights + BATCH * C);  // [BATCH] a chunk's decay (exp_pair)
     delta::let_next_start();  // (the kernel behind this one waits for its end before it reads what it leaves)
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int N = sh.N, P = sh.P, s = blockIdx.y, dir = blockIdx.z;
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(128) states_kernel(const E* __restrict__ q, co
             const float2 a = *reinterpret_cast<const float2*>(start + bh * np + i);
             x = a.x, y = a.y;
         });
-    float all = 1.f;  // decay since the segment's start
+    float all = 1.f, all_lo = 0.f;  // decay since the segment's start, as two floats
     for (int i = w0, t = 0; i < w1; ++i) {
         if ((i - w0) % BATCH == 0) {
             if (i > w0) __syncthreads();  // (the weights of the batch before are read)
@@ -581,14 +581,14 @@ __global__ void __launch_bounds__(128) states_kernel(const E* __restrict__ q, co
 #pragma unroll
                 for (int e = 0; e < Sums<C>::K; ++e)
                     weights[j * C + Sums<C>::K * lane + e] = dir ? sh.scale * exp_of(G.G[e]) : exp_between(G.end, G.G[e]);
-                if (lane == 0) totals[j] = exp_of(G.end);
+                if (lane == 0) totals[j] = exp_pair(G.end);
                 if (dir == 0 && slice == 0) put_decays(static_cast<Decays<C>*>(w.decays)[(int64_t)bh * sh.nc + c], G, lane);
             }
             __syncthreads();
         }
         const int c = chunk_of(i);
         const float* wt = weights + (i - w0) % BATCH * C;
-        const float total = totals[(i - w0) % BATCH];
+        const float2 total = totals[(i - w0) % BATCH];
         const bool empty = sh.nseg == 1 ? i == 0 && !start : i == w0;  // (not read by anyone)
         if (mine && !empty) {
             float* to = w.states + (row * sh.nc + c) * np;
@@ -644,8 +644,10 @@ __global__ void __launch_bounds__(128) states_kernel(const E* __restrict__ q, co
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) st[nt][e] = fmaf(total, st[nt][e], big[nt][e] + rest[nt][e]);
-        all *= total;
+            for (int e = 0; e < 4; ++e) st[nt][e] = fmaf(total.x, st[nt][e], fmaf(total.y, st[nt][e], big[nt][e] + rest[nt][e]));
+        const float p = all * total.x, left = fmaf(all, total.x, -p) + fmaf(all, total.y, all_lo * total.x);
+        all = p + left;
+        all_lo = left - (all - p);
     }
     float* last = dir ? gh0 : h_final;
     if (sh.nseg == 1) {

@@ -493,3 +493,52 @@ def test_decay_gradients_of_heads_that_forget_fast(cs, NP, head, dtype):
             assert abs(got[h] - w[..., h].sum()) < 4e-6 * np.abs(w[..., h]).sum(), h
         else:
             assert np.linalg.norm(got[..., h] - w[..., h]) < 4e-6 * np.linalg.norm(w[..., h]), h
+
+
+RATES = [3e-4, 3.7e-4, 4.9e-4, 6.1e-4, 8.3e-4, 1.1e-3]
+
+
+def off(x, y):
+    return float((x.double() - y).norm() / y.norm())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("NP", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("B", [1, 70])
+def test_states_of_slow_heads(cs, NP, dtype, B):
+    """One decay a head, heads that remember thousands of tokens, rows walked whole and cut: the last state and gh0 of each head are
+    within 1e-6 of the 64-bit recurrence in the 2-norm.  Of a state's size, at random: a chunk's rounding (2^-23 / sqrt(12), at
+    most 7 of them as chunks of 32 tokens are forgotten: 2.5e-7), its products' sums in two or more steps that drop up to 2^-23 (2.4e-7),
+    the tokens' decays to the chunk's end 1.2e-7: 4e-7; what is the same in every chunk, its decay's error, is below 2^-24 of what is forgotten."""
+    T, H, (N, P) = 5000, len(RATES), NP
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v, do = (torch.randn(T, H, w, generator=gen, device="cuda").to(TYPES[dtype]) for w in (N, N, P, P))
+    g = -torch.tensor(RATES, device="cuda")
+    h0, dh = (torch.randn(1, H, N, P, generator=gen, device="cuda") for _ in range(2))
+    S, D, a = h0[0].double(), dh[0].double(), torch.exp(g.double())[:, None, None]
+    for t in range(T):
+        S = torch.baddbmm(a * S, k[t].double()[:, :, None], v[t].double()[:, None])
+        u = T - 1 - t
+        D = a * torch.baddbmm(D, q[u].double()[:, :, None], 0.25 * do[u].double()[:, None])
+    many = lambda x: x[None].expand(B, *x.shape).contiguous()  # noqa: E731
+    h0, dh = (x.expand(B, -1, -1, -1).contiguous() for x in (h0, dh))
+    _, h = cs.linattn_forward(many(q), many(k), many(v), g, scale=0.25, h0=h0)
+    r = cs.linattn_backward(many(q), many(k), many(v), g, many(do), scale=0.25, h0=h0, dh_final=dh)
+    for e in range(H):
+        assert off(h[0, e], S[e]) < 1e-6 and off(r["gh0"][0, e], D[e]) < 1e-6, (e, off(h[0, e], S[e]), off(r["gh0"][0, e], D[e]))
+
+
+def test_steps_of_slow_heads(cs):
+    """4000 tokens one by one where a head remembers up to 3300 of them: a token rounds a state twice (2^-23 / sqrt(12) at most, at random),
+    41 times that as it forgets: 1.4e-6, and its decay's error, the same for every token, is below 2^-24 of what is forgotten."""
+    T, H, N, P = 4000, len(RATES), 64, 64
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    k, v = (torch.randn(T, 1, H, w, generator=gen, device="cuda") for w in (N, P))
+    g = -torch.tensor(RATES, device="cuda")
+    h = torch.randn(1, H, N, P, generator=gen, device="cuda")
+    S, a = h[0].double(), torch.exp(g.double())[:, None, None]
+    for t in range(T):
+        cs.linattn_step(h, k[t], k[t], v[t], g)
+        S = torch.baddbmm(a * S, k[t, 0].double()[:, :, None], v[t, 0].double()[:, None])
+    for e in range(H):
+        assert off(h[0, e], S[e]) < 2e-6, (e, off(h[0, e], S[e]))
