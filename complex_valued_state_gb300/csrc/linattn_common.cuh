@@ -268,8 +268,8 @@ __device__ __forceinline__ Sums<C> chunk_sums(const float* g, int64_t stride, in
 // exp(s) as two floats.  A state is multiplied by the decays of as many chunks (of one token's, step by step) as it
 // remembers, and with one decay a head all of them are off the same way: by up to 2^-23 of itself each time for a float
 // (at g = -3e-4 the states of 5000 tokens were off by 2e-6 in the 2-norm, after 4000 single tokens by 4e-5; with both
-// floats by less than 1e-6 and 2e-6, times unchanged within 0.5 %).  Near 1, where states
-// remember, the second float is what expm1, right to its own 2^-23, has beside the first one's distance from 1.
+// floats by less than 1e-6 and 2e-6, times unchanged within 0.5 %).  Near 1, where states remember, the second float is
+// what expm1, right to its own 2^-23, has beside the first one's distance from 1.
 __device__ __forceinline__ float2 exp_pair(Sum2 s) {
     const float e = exp_of(s);
     if (!(fabsf(s.hi) < 0.6f)) return make_float2(e, 0.f);

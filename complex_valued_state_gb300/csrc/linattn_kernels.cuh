@@ -36,10 +36,11 @@
 // and no barrier inside a chunk's products.  The state's products of the wide gradients are tcgen05 ones: there every
 // warp would read all of a state from shared memory for its 16 rows.
 //
-// Measured, bf16 (device time): forward 4 x 2048 x 24, 64/64 65 us (walk 29, outputs 37: half of it the loads'
-// latency at three CTAs an SM; without any products 41 us); 1 x 16384 x 32, 128/64 294 us (walk 118, 1 GB moved with
-// the states); gradients 4 x 2048 x 24, 64/64 184 us (walk 47, grad_kernel 137); 4 x 1501 x 16 on 8 key heads,
-// 128/128 197 us at 82 % of the tokens (walk 51, grad_kernel 130, sum over shared heads 23).
+// Measured, bf16 (a call among others of its kind): forward 4 x 2048 x 24, 64/64 66 us (walk 29, outputs 37: half of
+// it the loads' latency at three CTAs an SM; without any products 41 us); 1 x 16384 x 32, 128/64 298 us (walk 119, 1 GB
+// moved with the states); gradients 4 x 2048 x 24, 64/64 187 us (walk 48, grad_kernel 139, 96 bytes a thread of spilled
+// registers); 4 x 1501 x 16 on 8 key heads, 128/128, rows of random lengths, 165 to 205 us (at 82 % of the tokens 198:
+// walk 52, grad_kernel 130, sum over shared heads 23).
 #pragma once
 
 #include <type_traits>
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
                 tile.fetch(st, sl, N, P, tid);
                 __syncthreads();
                 tile.put(smem + M::S, tid);
-                            __syncthreads();
+                __syncthreads();
             }
             times_state<NP, SP, C, ND, PD, CW, true>(acc, base + M::Q, base + M::S, block, col0, sl, N, P, lane);
         }
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(NT, OutSmem<E, ND, PD, C>::CTAS)
 }
 
 // --------------------------------------------------------------- gradients
-// 4 x 2048 x 24, 64/64: 137 us at two CTAs an SM, tensor pipe 38 % busy, issue 33 % (dk and dv 50 us, the state's
+// 4 x 2048 x 24, 64/64: 139 us at two CTAs an SM, tensor pipe 37 % busy, issue 33 % (dk and dv 50 us, the state's
 // products 45, dq 15, loads and stores the rest).  128/128: one CTA an SM (four tiles of 34 KB), 255 registers; there
 // the state's products by the warps were half of it (80 of 157 us), whose operands' reads from shared memory (2 MB a
 // chunk) and tensor time (27000 cycles a chunk) were equal, so they are tcgen05 ones beside the scores.  16 warps a

@@ -9,8 +9,8 @@
 // still gets P / 32 of them a head.  Eight lanes hold a row's 32 columns as
 // float4 (128 contiguous bytes), 16 row groups of them N / 16 rows each.
 // e^g is two floats (exp_pair): its error is the same for every token that a head with one decay remembers.
-// Measured: 256 rows of a pool of 288, 32 heads, 128/64: 81 us, 6.7 TB/s (99 % of the copy rate); one row of 12
-// heads, 64/64: 2 us (15 a call from Python).
+// Measured: 256 rows of a pool of 288, 32 heads, 128/64: 82 us on the device, 6.7 TB/s (98 % of the copy rate), 83 a call
+// among others; one row of 12 heads, 64/64: 2 us, 15 a call from Python.
 
 #include "cssd_internal.h"
 #include "linattn_common.cuh"

@@ -503,8 +503,10 @@ int cssd_layernorm_backward(int64_t rows, int64_t width, int xtype, int wtype, c
  * float32 and differ from the recurrence by about 1e-6 of their largest value.
  * g is at most 0 in a model, though any value whose exponentials stay in range
  * works; -inf forgets everything before the token.  A NaN or infinity in a
- * token's inputs may reach any output of its chunk (up to 128 tokens) and what
- * follows; what lies at or past a row's length is never read.  Every wait inside
+ * token's inputs may reach any output of its chunk (up to 128 tokens, so up to
+ * 15 tokens before it in the sequence, where the one-token form has none) and
+ * what follows, one in h0 or dh_final any output of its row and head, and an
+ * infinity may become a NaN; what lies at or past a row's length is never read.  Every wait inside
  * the kernels is bounded (see cssd_device_status; thread blocks that exchange
  * states are one cluster), and nothing depends on the order of atomics: the
  * same call gives the same bits. */
