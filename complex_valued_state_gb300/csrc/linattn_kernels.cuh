@@ -95,12 +95,13 @@ struct Part {
     }
 };
 
-// float32 tensors (three planes): the products other than the leading planes' are summed apart and added at the end.
-// The matrix instruction drops what lies below its sum's last bit, at every one of its steps (outputs of 128/128
-// were off by 1.1e-6 in the 2-norm where plain fp32 arithmetic is off by 2.5e-7).
-template <int NPL, int N>
+// What float32 results of tensors in more than one plane come from (APART): the products other than the leading planes'
+// are summed apart and added at the end.  The matrix instruction drops what lies below its sum's last bit, at every one
+// of its steps (in one sum, float32 outputs of 128/128 were off by 1.1e-6 in the 2-norm where plain fp32 arithmetic is off
+// by 2.5e-7, and dg of float16 tensors by 0.7 to 1.0e-6, now 2 to 3e-7; the latter's times are the same within 1 %).
+template <bool APART, int N>
 struct Rest {
-    float v[NPL == 3 ? N : 1][4];
+    float v[APART ? N : 1][4];
     __device__ __forceinline__ Rest() {
 #pragma unroll
         for (auto& t : v)
@@ -108,9 +109,9 @@ struct Rest {
             for (float& x : t) x = 0.f;
     }
     // where the product of planes i and j of sum n goes
-    __device__ __forceinline__ float (&of(float (&acc)[N][4], int n, int ij))[4] { return NPL == 3 && ij > 0 ? v[NPL == 3 ? n : 0] : acc[n]; }
+    __device__ __forceinline__ float (&of(float (&acc)[N][4], int n, int ij))[4] { return APART && ij > 0 ? v[APART ? n : 0] : acc[n]; }
     __device__ __forceinline__ void add_to(float (&acc)[N][4]) const {
-        if constexpr (NPL == 3)
+        if constexpr (APART)
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -129,7 +130,7 @@ __device__ __forceinline__ void times_state(float (&acc)[CW / 8][4], uint32_t a,
     using TS = Tile<false, 64, TRANS ? OW : KW>;
     constexpr int KT = TRANS ? imin(4, KW / 16) : KW / 16;
     const int k0 = TRANS ? 64 * sl : 0;
-    Rest<NPL, CW / 8> rest;
+    Rest<(NPL > 1 && SP == 3), CW / 8> rest;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
         if (k0 + 16 * kt >= kw) break;
@@ -185,7 +186,7 @@ template <int NPL, int QP, int C, int KW, bool TC>
 __device__ __forceinline__ void scores(float (&sc)[2][4], const Rows<NPL, C, KW, TC>& a, uint32_t b, int o, int kw, int lane) {
     using TB = Tile<TC, C, KW>;
     const uint32_t at = TB::template at<true>(b, o, 0, lane);
-    Rest<NPL, 2> rest;
+    Rest<(NPL > 1 && QP == 3), 2> rest;
     if (NPL > 1)
 #pragma unroll
         for (auto& t : sc) t[0] = t[1] = t[2] = t[3] = 0.f;
@@ -278,7 +279,7 @@ __device__ __forceinline__ void times_tokens(float (&acc)[CW / 8][4], const floa
     using TZ = Tile<TC, C, OW>;
     const uint32_t at = TZ::template at<false>(z, o, col0, lane);
     constexpr int NG = imin(CW / 16, 4);  // 64 columns at a time
-    Rest<NPL, CW / 8> rest;
+    Rest<NPL == 3, CW / 8> rest;
 #pragma unroll
     for (int n0 = 0; n0 < CW / 16; n0 += NG)
 #pragma unroll
