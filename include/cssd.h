@@ -565,8 +565,9 @@ typedef enum { CSSD_RMS = 0, CSSD_LAYER = 1 } cssd_norm_kind;
  * normalised for the next.
  *     s = residual + alpha (scale * x)       y = norm(s) weight + bias
  *   x, y       xtype [rows, width]
- *   residual, s  rtype (xtype or CSSD_F32) [rows, width]; the norm is of s as it
- *              is stored (rounded to rtype), which is what the gradients read
+ *   residual, s  rtype (xtype or CSSD_F32) [rows, width]; the products and the
+ *              sum are rounded to fp32 one by one, as written; the norm is of s as
+ *              it is stored (rounded to rtype), which is what the gradients read
  *   mean, rstd [rows]
  * s may be residual, and y may be x.  eps >= 0 (else CSSD_ERR_DIMS). */
 int cssd_add_norm(int64_t rows, int64_t width, int xtype, int rtype, int wtype, int kind, const void* x,

@@ -446,3 +446,21 @@ def test_add_norm_vectors(cs, D, types, bias, scale):
 @pytest.mark.parametrize("first", [False, True])
 def test_gated_norm_vectors(cs, widths, types, bias, first):
     check_gated(cs, 41, *widths, "layer" if widths[1] % 16 else "rms", first, types, bias)
+
+
+@pytest.mark.parametrize("types", [("bf16", "bf16", "bf16"), ("bf16", "fp32", "bf16"), ("fp16", "fp16", "fp16"), ("fp32", "fp32", "fp32")])
+@pytest.mark.parametrize("D", [512, 333, 4096])
+@pytest.mark.parametrize("scale", [False, True])
+def test_residual_sum_to_the_bit(cs, D, types, scale):
+    """s is the formula's operations rounded one by one to fp32, then to its type: ties of a decimal alpha go as they should."""
+    xt, rt, wt = types
+    gen = torch.Generator().manual_seed(12)
+    x, res, sc = torch.randn(600, D, generator=gen).to(TYPES[xt]), (2 * torch.randn(600, D, generator=gen)).to(TYPES[rt]), None
+    want = x.float()
+    if scale:
+        sc = (0.5 + 0.2 * torch.randn(D, generator=gen)).to(TYPES[wt])
+        want = sc.float() * want
+    want = want * torch.tensor(0.7)
+    want = (res.float() + want).to(TYPES[rt])
+    s = cs.add_norm(dev(x), dev(res), None, None, alpha=0.7, scale=dev(sc))[1]
+    assert torch.equal(s.cpu(), want), (s.cpu() != want).sum()
